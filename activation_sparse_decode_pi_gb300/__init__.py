@@ -30,13 +30,15 @@ PI_F32, PI_BF16, PI_F16, PI_INT4_G128 = 0, 1, 2, 3
 DTYPES = {"f32": PI_F32, "bf16": PI_BF16, "f16": PI_F16, "int4g128": PI_INT4_G128}
 KINDS = {"gated": PI_FFN_GATED_RELU, "relu": PI_FFN_RELU}
 
-# every symbol include/pi_ffn.h declares
+# every symbol include/pi_ffn.h and include/pi_kv.h declare
 EXPORTS = (
     "pi_ffn_create", "pi_ffn_destroy", "pi_predict", "pi_sparse_ffn", "pi_decode_stack",
     "pi_hot_first_order", "pi_permute_rows", "pi_get_status", "pi_status_string", "pi_abi_version",
     "pi_profile_begin", "pi_profile_end", "pi_sparse_ffn_noalloc", "pi_selftest_grid_barrier",
     "pi_selftest_umma", "pi_ffn_set_hot_neurons", "pi_ffn_set_hot_prefix", "pi_decode_stack_layers",
     "pi_ffn_set_phase_trace",
+    "pi_kv_create", "pi_kv_destroy", "pi_kv_get_status", "pi_kv_reserve", "pi_kv_append", "pi_kv_attend",
+    "pi_kv_fork", "pi_kv_free", "pi_kv_trim", "pi_kv_copy_pages", "pi_kv_compact",
 )
 PI_STACK_PHASES = 8
 STACK_PHASE_NAMES = ("layer_start", "hidden_done", "logits_start", "list_ready", "first_rows", "ffn_done",
@@ -56,6 +58,21 @@ class PiLayerWeights(ctypes.Structure):
                 ("s_gate", ctypes.c_void_p), ("s_up", ctypes.c_void_p), ("s_down", ctypes.c_void_p),
                 ("b_gate", ctypes.c_void_p), ("p1_t", ctypes.c_void_p), ("p2_t", ctypes.c_void_p),
                 ("b_pred", ctypes.c_void_p)]
+
+
+class PiKvDesc(ctypes.Structure):
+    _fields_ = [("n_layers", ctypes.c_int32), ("n_heads", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("page_tokens", ctypes.c_int32), ("n_pages", ctypes.c_int32),
+                ("max_seqs", ctypes.c_int32), ("max_pages", ctypes.c_int32)]
+
+
+class PiKvLayer(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p)]
+
+
+class PiKvState(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("length", ctypes.c_void_p), ("ref", ctypes.c_void_p)]
 
 
 _P = ctypes.c_void_p
@@ -100,6 +117,24 @@ _lib.pi_profile_begin.restype = ctypes.c_int
 _lib.pi_profile_begin.argtypes = [_P]
 _lib.pi_profile_end.restype = ctypes.c_int
 _lib.pi_profile_end.argtypes = [_P, _P, _P, _I32]
+_F32 = ctypes.c_float
+for _name, _args in {
+    "pi_kv_create": [ctypes.POINTER(_P), ctypes.POINTER(PiKvDesc), ctypes.POINTER(PiKvLayer),
+                     ctypes.POINTER(PiKvState)],
+    "pi_kv_get_status": [_P],
+    "pi_kv_reserve": [_P, _P, _P, _I32, _P],
+    "pi_kv_append": [_P, _I32, _P, _P, _I32, _I32, _P, _P, _I64, _I32, _P],
+    "pi_kv_attend": [_P, _I32, _P, _P, _I32, _I32, _P, _I64, _P, _I64, _P, _I32, _F32, _I32, _I32, _P],
+    "pi_kv_fork": [_P, _P, _P, _I32, _P],
+    "pi_kv_free": [_P, _P, _I32, _P],
+    "pi_kv_trim": [_P, _P, _I32, _I32, _I32, _P],
+    "pi_kv_copy_pages": [_P, _P, _P, _I32, _P],
+    "pi_kv_compact": [_P, _P, _P],
+}.items():
+    getattr(_lib, _name).restype = ctypes.c_int
+    getattr(_lib, _name).argtypes = _args
+_lib.pi_kv_destroy.restype = None
+_lib.pi_kv_destroy.argtypes = [_P]
 
 
 class PiError(RuntimeError):
@@ -223,6 +258,56 @@ def pi_profile_end(h) -> dict:
     return {k: (float(ms[i]), int(cnt[i])) for i, k in enumerate(KERNEL_KINDS)}
 
 
+def pi_kv_create(desc: PiKvDesc, layers, state: PiKvState) -> int:
+    arr = (PiKvLayer * len(layers))(*layers)
+    h = _P()
+    _check(_lib.pi_kv_create(ctypes.byref(h), ctypes.byref(desc), arr, ctypes.byref(state)), "pi_kv_create")
+    return h.value
+
+
+def pi_kv_destroy(h: int) -> None:
+    _lib.pi_kv_destroy(h)
+
+
+def pi_kv_get_status(h) -> int:
+    return _lib.pi_kv_get_status(h)
+
+
+def pi_kv_reserve(h, seqs, tok_start, n, stream=None) -> None:
+    _check(_lib.pi_kv_reserve(h, _ptr(seqs), _ptr(tok_start), n, _stream(stream)), "pi_kv_reserve")
+
+
+def pi_kv_append(h, layer, seqs, tok_start, n, n_tokens, k_new, v_new, ld, dtype, stream=None) -> None:
+    _check(_lib.pi_kv_append(h, layer, _ptr(seqs), _ptr(tok_start), n, n_tokens, _ptr(k_new), _ptr(v_new), ld, dtype,
+                             _stream(stream)), "pi_kv_append")
+
+
+def pi_kv_attend(h, layer, seqs, tok_start, n, n_tokens, q, ld_q, out, ld_out, lse, dtype, scale, window=0, sinks=0,
+                 stream=None) -> None:
+    _check(_lib.pi_kv_attend(h, layer, _ptr(seqs), _ptr(tok_start), n, n_tokens, _ptr(q), ld_q, _ptr(out), ld_out,
+                             _ptr(lse), dtype, scale, window, sinks, _stream(stream)), "pi_kv_attend")
+
+
+def pi_kv_fork(h, src, dst, n, stream=None) -> None:
+    _check(_lib.pi_kv_fork(h, _ptr(src), _ptr(dst), n, _stream(stream)), "pi_kv_fork")
+
+
+def pi_kv_free(h, seqs, n, stream=None) -> None:
+    _check(_lib.pi_kv_free(h, _ptr(seqs), n, _stream(stream)), "pi_kv_free")
+
+
+def pi_kv_trim(h, seqs, n, window, sinks=0, stream=None) -> None:
+    _check(_lib.pi_kv_trim(h, _ptr(seqs), n, window, sinks, _stream(stream)), "pi_kv_trim")
+
+
+def pi_kv_copy_pages(h, src, dst, n, stream=None) -> None:
+    _check(_lib.pi_kv_copy_pages(h, _ptr(src), _ptr(dst), n, _stream(stream)), "pi_kv_copy_pages")
+
+
+def pi_kv_compact(h, n_live=None, stream=None) -> None:
+    _check(_lib.pi_kv_compact(h, _ptr(n_live), _stream(stream)), "pi_kv_compact")
+
+
 # ------------------------------------------------------------------------------------------------
 # torch conveniences (still only marshalling: each call is one C-ABI call)
 # ------------------------------------------------------------------------------------------------
@@ -333,6 +418,187 @@ class SparseFFN:
     def close(self):
         if self.h:
             pi_ffn_destroy(self.h)
+            self.h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+_TORCH_DTYPES = None
+
+
+def _act_dtype(x) -> int:
+    """pi_dtype_t of an activation tensor."""
+    global _TORCH_DTYPES
+    if _TORCH_DTYPES is None:
+        import torch
+
+        _TORCH_DTYPES = {torch.float32: PI_F32, torch.bfloat16: PI_BF16, torch.float16: PI_F16}
+    try:
+        return _TORCH_DTYPES[x.dtype]
+    except KeyError:
+        raise PiError(PI_ERR_UNSUPPORTED, f"dtype {x.dtype}") from None
+
+
+def _i32(x, name, n=None):
+    """A call's index tensor: int32, contiguous, on the GPU (its values are checked by the kernels)."""
+    import torch
+
+    if x.dtype is not torch.int32 or x.dim() != 1 or not x.is_contiguous() or not x.is_cuda:
+        raise ValueError(f"{name}: a contiguous 1-D int32 CUDA tensor")
+    if n is not None and x.shape[0] != n:
+        raise ValueError(f"{name}: {n} entries, got {x.shape[0]}")
+    return x
+
+
+def _token_rows(x, heads, dim, name):
+    """Row stride of a [tokens, heads, dim] tensor whose rows lie [heads, dim] contiguous (a slice of a fused
+    projection is fine)."""
+    if x.dim() != 3 or x.shape[1] != heads or x.shape[2] != dim or not x.is_cuda:
+        raise ValueError(f"{name}: a [tokens, {heads}, {dim}] CUDA tensor, got {tuple(x.shape)}")
+    if x.stride(2) != 1 or (heads > 1 and x.stride(1) != dim):
+        raise ValueError(f"{name}: the heads of a token lie next to each other")
+    return x.stride(0) if x.shape[0] > 1 else heads * dim
+
+
+def _on(stream):
+    """Allocations inside belong to `stream` where it is a torch stream (else to the current one)."""
+    import contextlib
+
+    if stream is None or isinstance(stream, int):
+        return contextlib.nullcontext()
+    import torch
+
+    return torch.cuda.stream(stream)
+
+
+class KVCache:
+    """A pi_kv handle over CUDA tensors (kept referenced for the handle's lifetime): a paged e4m3 key/value cache.
+
+    layers: per layer a dict of ``k``, ``v`` (float8_e4m3fn [pages, kv heads, page tokens, dim]) and ``k_scale``,
+    ``v_scale`` (fp32 [pages, kv heads]); table (int32 [sequences, columns], -1 for no page), length (int32
+    [sequences]), ref (int32 [pages]). ``KVCache.empty`` makes them. A step is one ``reserve``, then per layer
+    ``append`` and ``attend``; ``seqs`` names the call's sequences and ``tok_start`` where each one's new tokens
+    begin in the call's token arrays (one entry more than seqs).
+    """
+
+    def __init__(self, layers, table, length, ref, *, n_heads):
+        import torch
+
+        self.layers, self.table, self.length, self.ref = list(layers), table, length, ref
+        k = self.layers[0]["k"]
+        n_pages, kv_heads, page, dim = k.shape
+        for L in self.layers:
+            for name in ("k", "v"):
+                if L[name].dtype is not torch.float8_e4m3fn or L[name].shape != k.shape or not L[name].is_contiguous():
+                    raise ValueError(f"{name}: contiguous float8_e4m3fn of one shape for all layers")
+            for name in ("k_scale", "v_scale"):
+                x = L[name]
+                if x.dtype is not torch.float32 or tuple(x.shape) != (n_pages, kv_heads) or not x.is_contiguous():
+                    raise ValueError(f"{name}: contiguous fp32 [{n_pages}, {kv_heads}]")
+        for name, x, dims in (("table", table, 2), ("length", length, 1), ("ref", ref, 1)):
+            if x.dtype is not torch.int32 or x.dim() != dims or not x.is_contiguous():
+                raise ValueError(f"{name}: a contiguous int32 tensor of {dims} dimension(s)")
+        if length.shape[0] != table.shape[0] or ref.shape[0] != n_pages:
+            raise ValueError("length has an entry for each table row, ref one for each page")
+        self.n_heads, self.n_kv_heads, self.head_dim, self.page_tokens = n_heads, kv_heads, dim, page
+        self.desc = PiKvDesc(len(self.layers), n_heads, kv_heads, dim, page, n_pages, table.shape[0], table.shape[1])
+        self.h = None
+        self.h = pi_kv_create(self.desc, [PiKvLayer(*(_ptr(L[x]) for x in ("k", "v", "k_scale", "v_scale")))
+                                          for L in self.layers], PiKvState(_ptr(table), _ptr(length), _ptr(ref)))
+
+    @classmethod
+    def empty(cls, n_layers, n_heads, n_kv_heads, head_dim, page_tokens, n_pages, max_seqs, max_tokens, device="cuda"):
+        """A new cache: room for n_pages pages of page_tokens positions, max_seqs sequences of up to max_tokens."""
+        import torch
+
+        def pool():
+            return torch.zeros((n_pages, n_kv_heads, page_tokens, head_dim), dtype=torch.uint8,
+                               device=device).view(torch.float8_e4m3fn)
+
+        def scale():
+            return torch.zeros((n_pages, n_kv_heads), dtype=torch.float32, device=device)
+
+        layers = [dict(k=pool(), v=pool(), k_scale=scale(), v_scale=scale()) for _ in range(n_layers)]
+        columns = -(-max_tokens // page_tokens)
+        i32 = dict(dtype=torch.int32, device=device)
+        return cls(layers, torch.full((max_seqs, columns), -1, **i32), torch.zeros(max_seqs, **i32),
+                   torch.zeros(n_pages, **i32), n_heads=n_heads)
+
+    def reserve(self, seqs, tok_start, stream=None) -> None:
+        """The sequences grow by their new tokens (lengths, pages)."""
+        n = _i32(seqs, "seqs").shape[0]
+        pi_kv_reserve(self.h, seqs, _i32(tok_start, "tok_start", n + 1), n, stream)
+
+    def append(self, layer, seqs, tok_start, k_new, v_new, stream=None) -> None:
+        """Keys and values [tokens, kv heads, dim] (fp32, bf16 or fp16) of the sequences' last positions."""
+        n = _i32(seqs, "seqs").shape[0]
+        ld = _token_rows(k_new, self.n_kv_heads, self.head_dim, "k_new")
+        if _token_rows(v_new, self.n_kv_heads, self.head_dim, "v_new") != ld or v_new.dtype is not k_new.dtype or \
+                v_new.shape[0] != k_new.shape[0]:
+            raise ValueError("k_new and v_new: one shape, type and row stride")
+        pi_kv_append(self.h, layer, seqs, _i32(tok_start, "tok_start", n + 1), n, k_new.shape[0], k_new, v_new, ld,
+                     _act_dtype(k_new), stream)
+
+    def attend(self, layer, seqs, tok_start, q, out=None, lse=None, *, scale=None, window=0, sinks=0, stream=None):
+        """Attention of q [tokens, heads, dim], the sequences' last positions, over their cache; returns out
+        (q's type). window > 0: only the last `window` positions and the first `sinks` are seen. lse: fp32
+        [tokens, heads], filled with the log of each row's sum of exponentials."""
+        import torch
+
+        n, T = _i32(seqs, "seqs").shape[0], q.shape[0]
+        ld = _token_rows(q, self.n_heads, self.head_dim, "q")
+        if out is None:
+            with _on(stream):
+                out = torch.empty((T, self.n_heads, self.head_dim), dtype=q.dtype, device=q.device)
+            ld_out = self.n_heads * self.head_dim
+        else:
+            ld_out = _token_rows(out, self.n_heads, self.head_dim, "out")
+            if out.dtype is not q.dtype or out.shape[0] != T:
+                raise ValueError("out: q's type and number of tokens")
+        if lse is not None and (lse.dtype is not torch.float32 or tuple(lse.shape) != (T, self.n_heads) or
+                                not lse.is_contiguous()):
+            raise ValueError(f"lse: contiguous fp32 [{T}, {self.n_heads}]")
+        pi_kv_attend(self.h, layer, seqs, _i32(tok_start, "tok_start", n + 1), n, T, q, ld, out, ld_out, lse,
+                     _act_dtype(q), self.head_dim ** -0.5 if scale is None else scale, window, sinks, stream)
+        return out
+
+    def fork(self, src, dst, stream=None) -> None:
+        """dst[i] becomes a copy of sequence src[i] that shares its full pages."""
+        n = _i32(src, "src").shape[0]
+        pi_kv_fork(self.h, src, _i32(dst, "dst", n), n, stream)
+
+    def free(self, seqs, stream=None) -> None:
+        """Give back the sequences' pages."""
+        pi_kv_free(self.h, _i32(seqs, "seqs"), seqs.shape[0], stream)
+
+    def trim(self, seqs, window, sinks=0, stream=None) -> None:
+        """Give back the pages that a sliding window with first tokens no longer sees."""
+        pi_kv_trim(self.h, _i32(seqs, "seqs"), seqs.shape[0], window, sinks, stream)
+
+    def copy_pages(self, src, dst, stream=None) -> None:
+        """Copy pages src[i] to dst[i] in every layer (table and counts stay)."""
+        n = _i32(src, "src").shape[0]
+        pi_kv_copy_pages(self.h, src, _i32(dst, "dst", n), n, stream)
+
+    def compact(self, stream=None):
+        """Move the used pages to the lowest ids; returns their number (int32 [1], on the GPU)."""
+        import torch
+
+        with _on(stream):
+            live = torch.empty(1, dtype=torch.int32, device=self.ref.device)
+        pi_kv_compact(self.h, live, stream)
+        return live
+
+    def status(self) -> int:
+        return pi_kv_get_status(self.h)
+
+    def close(self):
+        if self.h:
+            pi_kv_destroy(self.h)
             self.h = None
 
     def __del__(self):

@@ -1,0 +1,80 @@
+// pi_kv_internal.h -- what the paged-cache host side (pi_kv_api.cu) and its kernels share.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "pi_kv.h"
+
+namespace pi {
+
+constexpr int KV_TILE = 64;        // positions per tile of the attention kernels
+constexpr float KV_E4M3_MAX = 448.f;
+constexpr int KV_MIN_EXP = -120;   // smallest exponent of a block scale
+
+// The cache as the kernels see it.
+struct KvView {
+    int n_layers, hq, hkv, dim, page, n_pages, max_seqs, max_pages;
+    int32_t *table, *length, *ref;
+    uint32_t *status;
+};
+
+// One layer's arrays.
+struct KvLayerDev {
+    uint8_t *k, *v;
+    float *ks, *vs;
+};
+
+// The call's ragged batch.
+struct KvBatch {
+    const int32_t *seqs, *start;
+    int n, n_tokens;
+};
+
+struct KvAttendArgs {
+    KvView c;
+    KvBatch b;
+    KvLayerDev l;
+    const void *q;
+    void *out;
+    float *lse;
+    int64_t ldq, ldo;          // elements
+    int dtype;
+    float scale_log2;          // scale * log2(e)
+    int window, sinks;
+    float *part;               // partial numerators [2 * grid][rows][dim]
+    float *part_ml;            // their running maximum and sum [2 * grid][rows][2]
+    uint32_t *tickets;         // [grid], zero on entry, left zero
+};
+
+// The split kernel (pi_kv_split.cuh) of one head dim; TWO: second 16-bit terms, 8 rows to a tile (else 16).
+template <int D, bool TWO>
+cudaError_t split_setup();   // shared-memory opt-in
+template <int D, bool TWO>
+cudaError_t split_launch(const KvAttendArgs &a, const CUtensorMap &mk, const CUtensorMap &mv, int grid, cudaStream_t s);
+#define PI_KV_EXTERN(D, TWO)                         \
+    extern template cudaError_t split_setup<D, TWO>(); \
+    extern template cudaError_t split_launch<D, TWO>(const KvAttendArgs &, const CUtensorMap &, const CUtensorMap &, int, cudaStream_t);
+PI_KV_EXTERN(64, true) PI_KV_EXTERN(64, false) PI_KV_EXTERN(128, true)
+PI_KV_EXTERN(128, false) PI_KV_EXTERN(256, true) PI_KV_EXTERN(256, false)
+#undef PI_KV_EXTERN
+
+cudaError_t launch_kv_append(const KvView &c, const KvBatch &b, const KvLayerDev &l, const void *k_new,
+                             const void *v_new, int64_t ld, int dtype, cudaStream_t s);
+
+struct KvCopyList {
+    int32_t *src, *dst, *count;   // device; count: one int32
+};
+cudaError_t launch_kv_reserve(const KvView &c, const KvBatch &b, int32_t *list, cudaStream_t s);
+cudaError_t launch_kv_fork(const KvView &c, const int32_t *src, const int32_t *dst, int n, const KvCopyList &l,
+                           cudaStream_t s);
+cudaError_t launch_kv_free(const KvView &c, const int32_t *seqs, int n, cudaStream_t s);
+cudaError_t launch_kv_trim(const KvView &c, const int32_t *seqs, int n, int window, int sinks, cudaStream_t s);
+cudaError_t launch_kv_compact(const KvView &c, const KvCopyList &l, int32_t *map, int32_t *n_live, cudaStream_t s);
+// Copies the listed pages in every layer (layers: device array) and, with map, renames every table entry.
+// max_count: an upper bound of *count known to the host.
+cudaError_t launch_kv_copy(const KvView &c, const KvLayerDev *layers, const int32_t *src, const int32_t *dst,
+                           const int32_t *count, int max_count, const int32_t *map, int nsm, cudaStream_t s);
+
+}  // namespace pi

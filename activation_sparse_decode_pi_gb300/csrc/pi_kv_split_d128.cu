@@ -1,0 +1,11 @@
+// pi_kv_split_d128.cu -- split attention kernels for head dim 128 (template in pi_kv_split.cuh).
+#include "pi_kv_split.cuh"
+
+namespace pi {
+template cudaError_t split_setup<128, true>();
+template cudaError_t split_setup<128, false>();
+template cudaError_t split_launch<128, true>(const KvAttendArgs &, const CUtensorMap &, const CUtensorMap &, int,
+                                            cudaStream_t);
+template cudaError_t split_launch<128, false>(const KvAttendArgs &, const CUtensorMap &, const CUtensorMap &, int,
+                                             cudaStream_t);
+}  // namespace pi
