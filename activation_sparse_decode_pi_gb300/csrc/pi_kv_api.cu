@@ -24,7 +24,8 @@ struct pi_kv {
     int dev = 0, nsm = 0;
     void *ws = nullptr;
     float *part = nullptr, *part_ml = nullptr;
-    uint32_t *tickets = nullptr, *status = nullptr;
+    float *rows_part = nullptr, *rows_ml = nullptr;
+    uint32_t *tickets = nullptr, *rows_tickets = nullptr, *status = nullptr;
     KvLayerDev *layers_dev = nullptr;
     int32_t *list_src = nullptr, *list_dst = nullptr, *list_count = nullptr, *page_map = nullptr;
 };
@@ -85,17 +86,38 @@ bool encode_pool(EncodeFn fn, CUtensorMap *m, const pi_kv_desc_t &d, void *base)
 }
 
 template <int D>
-cudaError_t split_setup_both()
+cudaError_t setup_of()
 {
-    const cudaError_t e = split_setup<D, true>();
-    return e != cudaSuccess ? e : split_setup<D, false>();
+    for (cudaError_t e : {split_setup<D, true>(), split_setup<D, false>(), rows_setup<D, 1>(), rows_setup<D, 2>()})
+        if (e != cudaSuccess) return e;
+    return cudaSuccess;
 }
 
+// Sequences with at least this many rows (new tokens x heads of a group) are worth a 128-row tile.
+constexpr int ROWS_FROM = 33;
+
+// The kernels of one call: the split kernel for sequences with few rows, the rows kernel for the others.
 template <int D>
-cudaError_t split_launch_of(bool two, const KvAttendArgs &a, const CUtensorMap &mk, const CUtensorMap &mv, int grid,
-                            cudaStream_t s)
+cudaError_t attend_of(const pi_kv *h, int layer, KvAttendArgs a, cudaStream_t s)
 {
-    return two ? split_launch<D, true>(a, mk, mv, grid, s) : split_launch<D, false>(a, mk, mv, grid, s);
+    const int64_t n = a.b.n, group = a.c.hq / a.c.hkv, rows = (int64_t)a.b.n_tokens * group;
+    // the host knows the rows' total only: one sequence has them all, and a token each is a decode step
+    const bool many = rows >= ROWS_FROM && (n == 1 || a.b.n_tokens > n), few = n > 1 || !many;
+    a.rows_from = many ? (few ? ROWS_FROM : 0) : INT32_MAX;
+    cudaError_t e = cudaSuccess;
+    if (few) {
+        // second 16-bit terms unless the output is bf16 and the rows of a sequence (on average) fill more than 8
+        const bool two = a.dtype != PI_BF16 || many || rows <= 8 * n;
+        e = two ? split_launch<D, true>(a, h->map_k[layer], h->map_v[layer], h->nsm, s)
+                : split_launch<D, false>(a, h->map_k[layer], h->map_v[layer], h->nsm, s);
+    }
+    if (many && e == cudaSuccess) {
+        const int64_t items = (rows / 128 + n) * a.c.hkv;   // at most one partly filled tile per sequence
+        const int64_t splits = items < h->nsm ? std::min<int64_t>(16, 2 * h->nsm / items) : 1;
+        e = a.dtype == PI_F32 ? rows_launch<D, 2>(a, (unsigned)items, (unsigned)splits, s)
+                              : rows_launch<D, 1>(a, (unsigned)items, (unsigned)splits, s);
+    }
+    return e;
 }
 
 size_t up(size_t v) { return (v + 255) / 256 * 256; }
@@ -143,14 +165,15 @@ pi_status_t kv_create(pi_kv_t **out, const pi_kv_desc_t *desc, const pi_kv_layer
         if (!encode_pool(enc, &h->map_k[l], d, layers[l].k) || !encode_pool(enc, &h->map_v[l], d, layers[l].v))
             return PI_ERR_CUDA;
     }
-    if ((s = cuda_status(d.head_dim == 64    ? split_setup_both<64>()
-                         : d.head_dim == 128 ? split_setup_both<128>()
-                                             : split_setup_both<256>())))
+    if ((s = cuda_status(d.head_dim == 64    ? setup_of<64>()
+                         : d.head_dim == 128 ? setup_of<128>()
+                                             : setup_of<256>())))
         return s;
     const size_t list = up(sizeof(int32_t) * (size_t)std::max(d.n_pages, PI_KV_MAX_CALL_SEQS));
     const size_t part = up((size_t)2 * nsm * 16 * d.head_dim * 4), ml = up((size_t)2 * nsm * 16 * 2 * 4);
     const size_t tick = up((size_t)nsm * 4), lay = up(sizeof(KvLayerDev) * (size_t)d.n_layers);
-    const size_t total = 3 * list + part + ml + tick + lay + 2 * 256;
+    const size_t rpart = up((size_t)2 * nsm * 128 * d.head_dim * 4), rml = up((size_t)2 * nsm * 128 * 2 * 4);
+    const size_t total = 3 * list + part + ml + rpart + rml + 3 * tick + lay + 2 * 256;
     if (injected_fault() == FAULT_ALLOC) return PI_ERR_OOM;
     if ((s = cuda_status(cudaMalloc(&h->ws, total)))) return s;
     if (injected_fault() == FAULT_UPLOAD) return PI_ERR_CUDA;
@@ -163,7 +186,10 @@ pi_status_t kv_create(pi_kv_t **out, const pi_kv_desc_t *desc, const pi_kv_layer
     };
     h->part = (float *)take(part);
     h->part_ml = (float *)take(ml);
+    h->rows_part = (float *)take(rpart);
+    h->rows_ml = (float *)take(rml);
     h->tickets = (uint32_t *)take(tick);
+    h->rows_tickets = (uint32_t *)take(2 * tick);
     h->layers_dev = (KvLayerDev *)take(lay);
     h->list_src = (int32_t *)take(list);
     h->list_dst = (int32_t *)take(list);
@@ -242,7 +268,7 @@ pi_status_t pi_kv_get_status(pi_kv_t *h)
     if ((s = cuda_status(cudaMemcpy(&v, h->status, 4, cudaMemcpyDeviceToHost)))) return s;
     if (v && (s = cuda_status(cudaMemset(h->status, 0, 4)))) return s;
     // a kernel that gave up between its tickets leaves them: start the next call clean
-    if (v == PI_ERR_TIMEOUT && (s = cuda_status(cudaMemset(h->tickets, 0, (size_t)h->nsm * 4)))) return s;
+    if (v == PI_ERR_TIMEOUT && (s = cuda_status(cudaMemset(h->tickets, 0, 3 * up((size_t)h->nsm * 4))))) return s;
     return (pi_status_t)v;
 }
 
@@ -303,14 +329,11 @@ pi_status_t pi_kv_attend(pi_kv_t *h, int32_t layer, const int32_t *seqs, const i
     a.part = h->part;
     a.part_ml = h->part_ml;
     a.tickets = h->tickets;
-    // Two 16-bit terms for every query and weight, 8 rows to a tile, unless the output is bf16 and the
-    // rows of a sequence (on average, all that the host knows) fill more than 8.
-    const int64_t group = h->desc.n_heads / h->desc.n_kv_heads;
-    const bool two = dtype != PI_BF16 || (int64_t)n_tokens * group <= (int64_t)8 * n;
-    const auto run = h->desc.head_dim == 64    ? split_launch_of<64>
-                     : h->desc.head_dim == 128 ? split_launch_of<128>
-                                               : split_launch_of<256>;
-    return cuda_status(run(two, a, h->map_k[layer], h->map_v[layer], h->nsm, (cudaStream_t)stream));
+    a.rows_part = h->rows_part;
+    a.rows_ml = h->rows_ml;
+    a.rows_tickets = h->rows_tickets;
+    const auto run = h->desc.head_dim == 64 ? attend_of<64> : h->desc.head_dim == 128 ? attend_of<128> : attend_of<256>;
+    return cuda_status(run(h, layer, a, (cudaStream_t)stream));
 }
 
 pi_status_t pi_kv_fork(pi_kv_t *h, const int32_t *src, const int32_t *dst, int32_t n, void *stream)

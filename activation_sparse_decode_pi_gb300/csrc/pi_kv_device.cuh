@@ -120,6 +120,17 @@ __device__ __forceinline__ void load16(const void *p, int dtype, int64_t at, flo
     }
 }
 
+// 16 codes that are read once: not kept in L1.
+__device__ __forceinline__ uint4 ld_codes(const uint4 *p)
+{
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p)
+                 : "memory");
+    return v;
+}
+
 // ---------------------------------------------------------------- tensor-core product -------
 
 // d += a b: 16 x 8 fp32 += (16 x 16 f16) (16 x 8 f16)
@@ -201,6 +212,13 @@ __device__ __forceinline__ void store_row(const KvAttendArgs &a, const int4 &f, 
         *(uint2 *)((uint16_t *)a.out + at) = v;
     }
     if (a.lse && d == 0) a.lse[tok * a.c.hq + head] = S == 0.f ? -INFINITY : (M + log2f(S)) * 0.6931471805599453f;
+}
+
+__device__ __forceinline__ void store_nan(const KvAttendArgs &a, const int4 &f, int h, int G, int D, int r, int d)
+{
+    const int64_t at = ((int64_t)f.z + r / G) * a.ldo + (int64_t)(h * G + r % G) * D + d;
+    if (a.dtype == DT_F32) ((uint32_t *)a.out)[at] = 0x7fc00000u;
+    else ((uint16_t *)a.out)[at] = a.dtype == DT_BF16 ? 0x7fc0u : 0x7e00u;
 }
 
 }  // namespace pi

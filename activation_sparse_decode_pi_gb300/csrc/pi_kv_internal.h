@@ -46,6 +46,11 @@ struct KvAttendArgs {
     float *part;               // partial numerators [2 * grid][rows][dim]
     float *part_ml;            // their running maximum and sum [2 * grid][rows][2]
     uint32_t *tickets;         // [grid], zero on entry, left zero
+    int rows_from;             // sequences with at least so many rows (new tokens x heads of a group) go to the
+                               // rows kernel, the others to the split kernel
+    float *rows_part;          // rows kernel, split items: numerators [items * splits][128][dim]
+    float *rows_ml;            // their references and sums [items * splits][128][2]
+    uint32_t *rows_tickets;    // [items], zero on entry, left zero
 };
 
 // The split kernel (pi_kv_split.cuh) of one head dim; TWO: second 16-bit terms, 8 rows to a tile (else 16).
@@ -58,6 +63,19 @@ cudaError_t split_launch(const KvAttendArgs &a, const CUtensorMap &mk, const CUt
     extern template cudaError_t split_launch<D, TWO>(const KvAttendArgs &, const CUtensorMap &, const CUtensorMap &, int, cudaStream_t);
 PI_KV_EXTERN(64, true) PI_KV_EXTERN(64, false) PI_KV_EXTERN(128, true)
 PI_KV_EXTERN(128, false) PI_KV_EXTERN(256, true) PI_KV_EXTERN(256, false)
+#undef PI_KV_EXTERN
+
+// The rows kernel (pi_kv_rows.cuh): QT 16-bit terms of queries and weights. items: an upper bound of the
+// call's (sequence, kv head, tile of 128 rows); splits: parts of each item's cache.
+template <int D, int QT>
+cudaError_t rows_setup();
+template <int D, int QT>
+cudaError_t rows_launch(const KvAttendArgs &a, unsigned items, unsigned splits, cudaStream_t s);
+#define PI_KV_EXTERN(D, QT)                        \
+    extern template cudaError_t rows_setup<D, QT>(); \
+    extern template cudaError_t rows_launch<D, QT>(const KvAttendArgs &, unsigned, unsigned, cudaStream_t);
+PI_KV_EXTERN(64, 1) PI_KV_EXTERN(64, 2) PI_KV_EXTERN(128, 1)
+PI_KV_EXTERN(128, 2) PI_KV_EXTERN(256, 1) PI_KV_EXTERN(256, 2)
 #undef PI_KV_EXTERN
 
 cudaError_t launch_kv_append(const KvView &c, const KvBatch &b, const KvLayerDev &l, const void *k_new,

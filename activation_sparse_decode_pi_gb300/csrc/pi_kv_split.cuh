@@ -97,7 +97,8 @@ __global__ void __launch_bounds__(SplitCfg<D, TWO>::NT, 1)
         const int i = base + tid;
         long long w = 0;
         if (i < a.b.n) {
-            const KvSeq q = kv_sequence(c, a.b, i, blockIdx.x == 0);
+            KvSeq q = kv_sequence(c, a.b, i, blockIdx.x == 0);
+            if ((long long)q.n * G >= a.rows_from) q.n = 0;   // the rows kernel's
             info[i] = make_int4(q.row, q.len, q.start, q.n);
             int w0, ns, nt;
             view(q.len, q.n, w0, ns, nt);
