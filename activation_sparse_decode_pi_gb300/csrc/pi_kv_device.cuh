@@ -80,6 +80,16 @@ __device__ __forceinline__ float finite_abs(float x)
     return a <= 3.402823466e38f ? a : 0.f;
 }
 
+// (a.x + b.x, a.y + b.y) in one instruction
+__device__ __forceinline__ float2 fadd2(float2 a, float2 b)
+{
+    unsigned long long r;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(r)
+        : "l"(*reinterpret_cast<unsigned long long *>(&a)), "l"(*reinterpret_cast<unsigned long long *>(&b)));
+    return *reinterpret_cast<float2 *>(&r);
+}
+
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
 {
     const __half2 h = __floats2half2_rn(lo, hi);

@@ -33,7 +33,8 @@ struct RowsCfg {
 constexpr float ROWS_TRAIL = 8.f;   // base-2 growth of the maximum that is taken up without rescaling
 constexpr float ROWS_UNIT = 7.f;    // weights are kept times 2^7: below 2^15 with the trail
 
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32])
+// 32 columns of this thread's lane, asynchronously
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t *r)
 {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
@@ -45,7 +46,15 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32])
           "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(taddr)
         : "memory");
+}
+
+// The loads above have landed; the registers pass through, so that no use of them moves up past the wait.
+template <int N>
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[N])
+{
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
 }
 
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *r)
@@ -70,6 +79,12 @@ __device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, ui
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
         "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"((uint32_t)accum)
         : "memory");
+}
+
+// The lowest n bits (n <= 0: none, n >= 32: all).
+__device__ __forceinline__ uint32_t low_bits(long long n)
+{
+    return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << (int)n) - 1u;
 }
 
 // Pages of one tile for the softmax: scale factors and which are there.
@@ -236,24 +251,37 @@ __global__ void __launch_bounds__(256, (RowsCfg<D, QT>::CTAS))
             }
             return page;
         };
+        // This thread's vectors of a tile: chunk ch of rows tr, tr + TPX, ...
+        constexpr int TPX = 128 / VPR;
+        static_assert(TPX % 8 == 0, "a vector's place in its swizzle atom is the same in every row it takes");
+        const int tr = lt / VPR, ch = lt % VPR, pshift = __ffs(min(P, TOK)) - 1;
         auto fetch = [&](const uint8_t *pool, int i, int pid, uint4 (&r)[NV]) {
             const int j0 = tile_of(i);
             const bool whole = is_whole(j0);
+            const size_t page_bytes = (size_t)P * D;
+            const uint8_t *from = pool + (size_t)((j0 & (P - 1)) * D + ch * 16);
 #pragma unroll
             for (int x = 0; x < NV; ++x) {
-                const int v = x * 128 + lt, tok = v / VPR, j = j0 + tok;
-                const int page = __shfl_sync(0xffffffffu, pid, P >= TOK ? 0 : tok / P);
+                const int tok = x * TPX + tr;
+                const int page = __shfl_sync(0xffffffffu, pid, tok >> pshift);
+                r[x] = make_uint4(0, 0, 0, 0);
                 bool live = page >= 0;
-                if (!whole)
-                    live &= j <= pos_hi && (a.window <= 0 || j < a.sinks || (long long)pos_lo - j < a.window);
-                r[x] = live ? ld_codes((const uint4 *)(pool + (((size_t)page * c.hkv + h) * P + (j & (P - 1))) * D) + v % VPR)
-                            : make_uint4(0, 0, 0, 0);
+                if (!whole) {
+                    const int j = j0 + tok;
+                    live = live && j <= pos_hi && (a.window <= 0 || j < a.sinks || (long long)pos_lo - j < a.window);
+                }
+                if (live)
+                    r[x] = ld_codes((const uint4 *)(from + (unsigned)(page * c.hkv + h) * page_bytes +
+                                                    ((tok & ((1 << pshift) - 1)) * D)));
             }
         };
+        // lanes of odd 128-byte blocks store their second half first: no bank conflict
+        const int first = (ch >> 2) & 1;
+        const uint32_t o_blk = (uint32_t)(ch / 4) * (TOK * 128u);
+        const uint32_t o_lo = o_blk + sw128_off(tr, (ch % 4) * 2 + first), o_hi = o_blk + sw128_off(tr, (ch % 4) * 2 + 1 - first);
         auto convert = [&](uint8_t *dst, const uint4 (&r)[NV]) {
 #pragma unroll
             for (int x = 0; x < NV; ++x) {
-                const int v = x * 128 + lt, tok = v / VPR, ch = v % VPR;
                 const uint32_t w[4] = {r[x].x, r[x].y, r[x].z, r[x].w};
                 uint32_t f[8];
 #pragma unroll
@@ -261,11 +289,9 @@ __global__ void __launch_bounds__(256, (RowsCfg<D, QT>::CTAS))
                     f[2 * e] = e4m3x2_f16x2((uint16_t)w[e]);
                     f[2 * e + 1] = e4m3x2_f16x2((uint16_t)(w[e] >> 16));
                 }
-                uint8_t *blk = dst + (ch / 4) * TOK * 128;
-                const int first = (ch >> 2) & 1;   // lanes of odd blocks store their second half first: no bank conflict
                 const uint4 lo = make_uint4(f[0], f[1], f[2], f[3]), hi = make_uint4(f[4], f[5], f[6], f[7]);
-                *(uint4 *)(blk + sw128_off(tok, (ch % 4) * 2 + first)) = first ? hi : lo;
-                *(uint4 *)(blk + sw128_off(tok, (ch % 4) * 2 + 1 - first)) = first ? lo : hi;
+                *(uint4 *)(dst + o_lo + x * TPX * 128) = first ? hi : lo;
+                *(uint4 *)(dst + o_hi + x * TPX * 128) = first ? lo : hi;
             }
         };
         // A NaN value in a tile that not every row sees in full: 0 here, and the rows that see it learn of it at the end.
@@ -282,11 +308,14 @@ __global__ void __launch_bounds__(256, (RowsCfg<D, QT>::CTAS))
                     }
             }
         };
-        auto describe = [&](int i, int pid) {   // scales of tile i's pages
+        // Scales of the pages of a tile (lanes as in pages()), and what the softmax makes of them.
+        auto scales = [&](int pid, float &ks, float &vs) {
+            ks = pid >= 0 ? a.l.ks[(size_t)pid * c.hkv + h] : 0.f;
+            vs = pid >= 0 ? a.l.vs[(size_t)pid * c.hkv + h] : 0.f;
+        };
+        auto describe = [&](int i, int pid, float ks, float vs) {
             RowsMeta &m = meta[i & 1];
             if (warp != 4) return;
-            const float ks = pid >= 0 ? a.l.ks[(size_t)pid * c.hkv + h] : 0.f;
-            const float vs = pid >= 0 ? a.l.vs[(size_t)pid * c.hkv + h] : 0.f;
             float top = vs;
 #pragma unroll
             for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -335,45 +364,42 @@ __global__ void __launch_bounds__(256, (RowsCfg<D, QT>::CTAS))
             issue_s();
             mbar_arrive(&bar_s);
         };
+        // Everything that a step needs was asked for at least one step before: the page ids of a tile three
+        // steps ahead of its weights' product, its scales and keys two, its values one.
         uint4 kr[NV], vr[NV];
-        int pid = -1;
-        if (nt > 0) {
-            pid = pages(0);
-            fetch(a.l.k, 0, pid, kr);
-            fetch(a.l.v, 0, pid, vr);
-            describe(0, pid);
-            convert(gk, kr);
-            fence_proxy_async_smem();
-            bar_sync(1, 128);
-            if (lt == 0) start_s();
-            if (nt > 1) {
-                pid = pages(1);
-                fetch(a.l.k, 1, pid, kr);
+        int pid1 = -1, pid2 = nt > 0 ? pages(0) : -1;   // pages of tiles i + 1 and i + 2
+        float ks1 = 0.f, vs1 = 0.f;
+#pragma unroll 1
+        for (int i = -2; i < nt; ++i) {
+            const int pid3 = i + 3 < nt ? pages(i + 3) : -1;
+            if (i >= 0) {
+                strip_nan(i, vr);
+                if (i > 0) wait(&bar_v, (i - 1) & 1);      // the product that read the last values is done
+                convert(gv, vr);
             }
-        }
-        for (int i = 0; i < nt; ++i) {
-            strip_nan(i, vr);
-            if (i > 0) wait(&bar_v, (i - 1) & 1);          // the product that read the last values is done
-            convert(gv, vr);
-            if (i + 1 < nt) {
-                fetch(a.l.v, i + 1, pid, vr);
-                wait(&bar_s, i & 1);                       // and the one that read the last keys
-                describe(i + 1, pid);
+            if (i >= -1 && i + 1 < nt) {
+                fetch(a.l.v, i + 1, pid1, vr);
+                if (i >= 0) wait(&bar_s, i & 1);           // and the one that read the last keys
+                describe(i + 1, pid1, ks1, vs1);
                 convert(gk, kr);
-                if (i + 2 < nt) {
-                    pid = pages(i + 2);
-                    fetch(a.l.k, i + 2, pid, kr);
-                }
             }
             fence_proxy_async_smem();
             bar_sync(1, 128);
             if (lt == 0) {
-                wait(&bar_p, i & 1);
-                tc_fence_after();
-                issue_o(i > 0);
-                if (i + 1 < nt) start_s();
+                if (i >= 0) {
+                    wait(&bar_p, i & 1);
+                    tc_fence_after();
+                    issue_o(i > 0);
+                }
+                if (i >= -1 && i + 1 < nt) start_s();
             }
             __syncwarp();
+            if (i + 2 < nt) {
+                scales(pid2, ks1, vs1);
+                fetch(a.l.k, i + 2, pid2, kr);
+            }
+            pid1 = pid2;
+            pid2 = pid3;
         }
     }
 
@@ -382,35 +408,52 @@ __global__ void __launch_bounds__(256, (RowsCfg<D, QT>::CTAS))
     const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
     if (warp < 4) {
         const int pshift = __ffs(P) - 1;
+        // A page's factor from product to base-2 score. Never 0, so that -infinity stays what it is.
+        auto factor = [&](const RowsMeta &mt, int pg) { return fmaxf(qf * mt.ks[pg], 1e-37f); };
         for (int i = 0; i < nt; ++i) {
             wait(&bar_s, i & 1);
             tc_fence_after();
             const RowsMeta &mt = meta[i & 1];
             const int j0 = tile_of(i);
-            const bool whole = mt.whole;
-            const uint32_t valid = mt.valid;
-            auto see = [&](int t) {
-                const int j = j0 + t;
-                return j <= pos && ((valid >> (P >= TOK ? 0 : t >> pshift)) & 1u) &&
-                       (a.window <= 0 || pos - j < a.window || j < a.sinks);
-            };
+            // scores to factors of the row's largest; what a row does not see becomes -infinity in place
             float top = -INFINITY;
+            auto take = [&](const uint32_t *r, int t0) {   // 16 positions: one page
+                float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int e = 0; e < 16; ++e) t[e & 3] = fmaxf(t[e & 3], __uint_as_float(r[e]));
+                const float t4 = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
+                if (t4 > -INFINITY) top = fmaxf(top, t4 * factor(mt, P >= TOK ? 0 : t0 >> pshift));
+            };
+            if (mt.whole) {
 #pragma unroll 1
-            for (int ch = 0; ch < TOK / 32; ++ch) {
-                uint32_t r[32];
-                tmem_ld32(ts + lane_base + ch * 32, r);
+                for (int ch = 0; ch < TOK; ch += 64) {
+                    uint32_t r[64];
+                    tmem_ld32(ts + lane_base + ch, r);
+                    tmem_ld32(ts + lane_base + ch + 32, r + 32);
+                    tmem_wait_ld(r);
 #pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {           // 16 positions: one page
-                    const int pg = P >= TOK ? 0 : (ch * 32 + hf * 16) >> pshift;
-                    float t = -INFINITY;
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        float v = __uint_as_float(r[hf * 16 + e]);
-                        if (!whole) v = see(ch * 32 + hf * 16 + e) ? v : -INFINITY;
-                        t = fmaxf(t, v);
-                    }
-                    if (t > -INFINITY) top = fmaxf(top, t * (qf * mt.ks[pg]));
+                    for (int g16 = 0; g16 < 64; g16 += 16) take(r + g16, ch + g16);
                 }
+            } else {
+#pragma unroll 1
+                for (int ch = 0; ch < TOK; ch += 32) {
+                    uint32_t r[32];
+                    tmem_ld32(ts + lane_base + ch, r);
+                    const int j = j0 + ch;
+                    uint32_t see = low_bits(pos - j + 1);
+                    if (a.window > 0) see &= ~low_bits((long long)pos - a.window + 1 - j) | low_bits((long long)a.sinks - j);
+                    const uint32_t v0 = mt.valid >> (P >= TOK ? 0 : ch >> pshift) & 1u;
+                    const uint32_t v1 = mt.valid >> (P >= TOK ? 0 : (ch + 16) >> pshift) & 1u;
+                    see &= (v0 ? 0xffffu : 0u) | (v1 ? 0xffff0000u : 0u);
+                    tmem_wait_ld(r);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) r[e] = (see >> e) & 1u ? r[e] : 0xff800000u;
+                    take(r, ch);
+                    take(r + 16, ch + 16);
+                    tmem_st16(ts + lane_base + ch, r);
+                    tmem_st16(ts + lane_base + ch + 16, r + 16);
+                }
+                tmem_wait_st();
             }
             // the reference is raised when the maximum has outrun it; O follows it and the unit of the values
             float shrink = 1.f;
@@ -426,6 +469,7 @@ __global__ void __launch_bounds__(256, (RowsCfg<D, QT>::CTAS))
                 for (int ch = 0; ch < D / 32; ++ch) {
                     uint32_t r[32];
                     tmem_ld32(to + lane_base + ch * 32, r);
+                    tmem_wait_ld(r);
 #pragma unroll
                     for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * shrink);
                     tmem_st16(to + lane_base + ch * 32, r);
@@ -433,37 +477,36 @@ __global__ void __launch_bounds__(256, (RowsCfg<D, QT>::CTAS))
                 }
             }
             const float ref = m == -INFINITY ? 0.f : m;
-            uint32_t plo[QT == 2 ? TOK / 2 : 1];
-#pragma unroll(QT == 2 ? TOK / 32 : 1)
-            for (int ch = 0; ch < TOK / 32; ++ch) {
-                uint32_t r[32], ph[16];
-                tmem_ld32(ts + lane_base + ch * 32, r);
+#pragma unroll 1
+            for (int ch = 0; ch < TOK; ch += 64) {
+                uint32_t r[64], plo[QT == 2 ? 32 : 1];
+                tmem_ld32(ts + lane_base + ch, r);
+                tmem_ld32(ts + lane_base + ch + 32, r + 32);
+                tmem_wait_ld(r);
 #pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-                    const int pg = P >= TOK ? 0 : (ch * 32 + hf * 16) >> pshift;
-                    const float f = qf * mt.ks[pg];
-                    const float off = mt.vexp[pg] - ref;
-                    float sum = 0.f;
+                for (int g16 = 0; g16 < 64; g16 += 16) {
+                    const int pg = P >= TOK ? 0 : (ch + g16) >> pshift;
+                    const float f = factor(mt, pg), off = mt.vexp[pg] - ref;
+                    float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-                    for (int e = 0; e < 16; e += 2) {
-                        float x = ex2(fmaf(__uint_as_float(r[hf * 16 + e]), f, off));
-                        float y = ex2(fmaf(__uint_as_float(r[hf * 16 + e + 1]), f, off));
-                        if (!whole) {
-                            x = see(ch * 32 + hf * 16 + e) ? x : 0.f;
-                            y = see(ch * 32 + hf * 16 + e + 1) ? y : 0.f;
-                        }
-                        sum += x + y;
-                        if constexpr (QT == 2) split_pair(x, y, ph[hf * 8 + e / 2], plo[ch * 16 + hf * 8 + e / 2]);
-                        else ph[hf * 8 + e / 2] = pack_f16(x, y);
+                    for (int e = g16; e < g16 + 16; e += 2) {
+                        float2 x = ffma2(make_float2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])),
+                                         make_float2(f, f), make_float2(off, off));
+                        x.x = ex2(x.x);
+                        x.y = ex2(x.y);
+                        sum = fadd2(sum, x);
+                        if constexpr (QT == 2) split_pair(x.x, x.y, r[e / 2], plo[e / 2]);
+                        else r[e / 2] = pack_f16(x.x, x.y);
                     }
-                    l = fmaf(sum, mt.vback[pg], l);
+                    l = fmaf(sum.x + sum.y, mt.vback[pg], l);
                 }
-                // the weights take the place of scores already read (QT 2: their second terms follow below)
-                tmem_st16(ts + lane_base + ch * 16, ph);
-            }
-            if constexpr (QT == 2) {
-#pragma unroll
-                for (int ch = 0; ch < TOK / 32; ++ch) tmem_st16(ts + lane_base + TOK / 2 + ch * 16, plo + ch * 16);
+                // the weights take the place of scores already read, their second terms (TOK 64) that of the rest
+                tmem_st16(ts + lane_base + ch / 2, r);
+                tmem_st16(ts + lane_base + ch / 2 + 16, r + 16);
+                if constexpr (QT == 2) {
+                    tmem_st16(ts + lane_base + 32, plo);
+                    tmem_st16(ts + lane_base + 48, plo + 16);
+                }
             }
             tmem_wait_st();
             tc_fence_before();
@@ -480,7 +523,10 @@ __global__ void __launch_bounds__(256, (RowsCfg<D, QT>::CTAS))
 #pragma unroll 1
         for (int ch = 0; ch < D / 32; ++ch) {
             uint32_t r[32];
-            if (nt > 0) tmem_ld32(to + lane_base + ch * 32, r);
+            if (nt > 0) {
+                tmem_ld32(to + lane_base + ch * 32, r);
+                tmem_wait_ld(r);
+            }
             if (!on) continue;
 #pragma unroll
             for (int e = 0; e < 32; e += 4) {
