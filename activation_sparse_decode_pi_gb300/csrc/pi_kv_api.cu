@@ -112,7 +112,7 @@ cudaError_t attend_of(const pi_kv *h, int layer, KvAttendArgs a, cudaStream_t s)
                 : split_launch<D, false>(a, h->map_k[layer], h->map_v[layer], h->nsm, s);
     }
     if (many && e == cudaSuccess) {
-        const int64_t items = (rows / 128 + n) * a.c.hkv;   // at most one partly filled tile per sequence
+        const int64_t items = (rows / rows_per_item(D) + n) * a.c.hkv;   // at most one partly filled per sequence
         const int64_t splits = items < h->nsm ? std::min<int64_t>(16, 2 * h->nsm / items) : 1;
         e = a.dtype == PI_F32 ? rows_launch<D, 2>(a, (unsigned)items, (unsigned)splits, s)
                               : rows_launch<D, 1>(a, (unsigned)items, (unsigned)splits, s);
@@ -172,7 +172,8 @@ pi_status_t kv_create(pi_kv_t **out, const pi_kv_desc_t *desc, const pi_kv_layer
     const size_t list = up(sizeof(int32_t) * (size_t)std::max(d.n_pages, PI_KV_MAX_CALL_SEQS));
     const size_t part = up((size_t)2 * nsm * 16 * d.head_dim * 4), ml = up((size_t)2 * nsm * 16 * 2 * 4);
     const size_t tick = up((size_t)nsm * 4), lay = up(sizeof(KvLayerDev) * (size_t)d.n_layers);
-    const size_t rpart = up((size_t)2 * nsm * 128 * d.head_dim * 4), rml = up((size_t)2 * nsm * 128 * 2 * 4);
+    const size_t rpart = up((size_t)2 * nsm * rows_per_item(d.head_dim) * d.head_dim * 4),
+                 rml = up((size_t)2 * nsm * rows_per_item(d.head_dim) * 2 * 4);
     const size_t total = 3 * list + part + ml + rpart + rml + 3 * tick + lay + 2 * 256;
     if (injected_fault() == FAULT_ALLOC) return PI_ERR_OOM;
     if ((s = cuda_status(cudaMalloc(&h->ws, total)))) return s;

@@ -48,6 +48,15 @@ __device__ __forceinline__ uint32_t e4m3x2_f16x2(uint16_t v)
     return r;
 }
 
+// The four codes of a word, low bytes first.
+__device__ __forceinline__ void e4m3x4_f16x4(uint32_t w, uint32_t &lo, uint32_t &hi)
+{
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+}
+
 // Codes of (lo, hi): nearest, saturated to +-448, NaN kept.
 __device__ __forceinline__ uint16_t f32x2_e4m3x2(float lo, float hi)
 {

@@ -48,8 +48,8 @@ struct KvAttendArgs {
     uint32_t *tickets;         // [grid], zero on entry, left zero
     int rows_from;             // sequences with at least so many rows (new tokens x heads of a group) go to the
                                // rows kernel, the others to the split kernel
-    float *rows_part;          // rows kernel, split items: numerators [items * splits][128][dim]
-    float *rows_ml;            // their references and sums [items * splits][128][2]
+    float *rows_part;          // rows kernel, split items: numerators [items * splits][rows][dim]
+    float *rows_ml;            // their references and sums [items * splits][rows][2]
     uint32_t *rows_tickets;    // [items], zero on entry, left zero
 };
 
@@ -66,7 +66,8 @@ PI_KV_EXTERN(128, false) PI_KV_EXTERN(256, true) PI_KV_EXTERN(256, false)
 #undef PI_KV_EXTERN
 
 // The rows kernel (pi_kv_rows.cuh): QT 16-bit terms of queries and weights. items: an upper bound of the
-// call's (sequence, kv head, tile of 128 rows); splits: parts of each item's cache.
+// call's (sequence, kv head, run of rows_per_item rows); splits: parts of each item's cache.
+constexpr int rows_per_item(int dim) { return dim == 256 ? 128 : 256; }
 template <int D, int QT>
 cudaError_t rows_setup();
 template <int D, int QT>

@@ -5,15 +5,16 @@
 // tensor memory; the weights P = 2^(S - m) go back to tensor memory as f16 and are the A operand of
 // the second product. Nothing of S or P leaves the SM.
 //
-// What bounds it: per tile the two products take 2 * 128 * TOK * D / 8192 cycles, the softmax about as
-// many issue slots (one exponential and a handful of operations per score), and e4m3 has to become f16
-// in shared memory first, since a tcgen05 product takes operands of one width and 8 bits are too few
-// for queries and weights. Two CTAs share an SM, so that one's products run under the other's
-// softmax. In a CTA: 4 warps with a row per thread, and 4 warps that load codes (16-byte loads, a tile
-// ahead in registers), convert them and issue the products.
+// What bounds it: per 128 rows and tile the two products take 2 * 128 * TOK * D / 8192 cycles, the softmax
+// about as many issue slots (one exponential and a handful of operations per score), and e4m3 has to
+// become f16 in shared memory first, since a tcgen05 product takes operands of one width and 8 bits are
+// too few for queries and weights. So a CTA works on NG = 2 tiles of 128 rows at once (head dim 256: one):
+// a converted tile serves both, and one's products run under the other's softmax. Each has 4 warps
+// with a row per thread, whose first thread issues its products; 4 more warps load codes (16-byte
+// loads, a tile ahead in registers) and convert them into a ring of NB tiles.
 // Rounding: as in pi_kv_split.cuh: q as f16 scaled per row by a power of two, weights as f16 in
 // units of 2^-7 of a reference that trails the running maximum by at most 2^8 (floor 2^-31 of the
-// row's largest weight). QT = PT = 2 (fp32 output): a second f16 term of both.
+// row's largest weight). QT = 2 (fp32 output): a second f16 term of both.
 #pragma once
 
 #include "pi_kv_device.cuh"
@@ -23,11 +24,13 @@ namespace pi {
 
 template <int D, int QT>
 struct RowsCfg {
-    static constexpr int TOK = D == 256 || QT == 2 ? 64 : 128;
+    static constexpr int NG = D == 256 ? 1 : 2;                 // groups of 128 rows
+    static constexpr int ROWS = 128 * NG, NT = ROWS + 128;      // threads: a row each, and the loaders
+    static constexpr int TOK = D == 256 || QT == 2 ? 64 : 128;  // positions per tile
+    static constexpr int NB = D == 256 && QT == 2 ? 1 : 2;      // tiles of K and of V in shared memory
     static constexpr int Q_BYTES = 128 * D * 2, KV_BYTES = TOK * D * 2;
-    static constexpr int SMEM = 1024 + QT * Q_BYTES + 2 * KV_BYTES;
-    static constexpr int TCOLS = D == 256 ? 512 : 256;   // S (TOK columns) and O (D columns)
-    static constexpr int CTAS = D == 256 ? 1 : 2;        // per SM
+    static constexpr int SMEM = 1024 + NG * QT * Q_BYTES + 2 * NB * KV_BYTES;
+    static constexpr int TCOLS = 512;                           // per group: S (TOK columns) and O (D columns)
 };
 
 constexpr float ROWS_TRAIL = 8.f;   // base-2 growth of the maximum that is taken up without rescaling
@@ -99,27 +102,24 @@ struct RowsMeta {
 };
 
 template <int D, int QT>
-__global__ void __launch_bounds__(256, (RowsCfg<D, QT>::CTAS))
-    k_kv_rows(const __grid_constant__ KvAttendArgs a)
+__global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_constant__ KvAttendArgs a)
 {
     using C = RowsCfg<D, QT>;
-    constexpr int TOK = C::TOK, NV = TOK * D / 16 / 128, VPR = D / 16;   // 16-byte vectors per loader thread, per row
+    constexpr int TOK = C::TOK, NB = C::NB, NW = C::NT / 32;
+    constexpr int NBLK = D / 64, NV = TOK * D / 16 / 128;   // 64-column blocks; 16-byte vectors per loader thread
     extern __shared__ uint8_t dsm[];
-    __shared__ uint64_t bar_s, bar_p, bar_v;
+    __shared__ uint64_t bar_s[2], bar_o[2], kfull[2], kempty[2], vfull[2], vempty[2];
     __shared__ uint32_t taddr_s;
-    __shared__ RowsMeta meta[2];
-    __shared__ int s_item[4], wsum[8], s_nan, s_last;
+    __shared__ RowsMeta meta[4];
+    __shared__ int s_item[4], wsum[NW], s_nan, s_last;
     const uint32_t base = (smem_u32(dsm) + 1023u) & ~1023u;
-    uint8_t *const gq = dsm + (base - smem_u32(dsm)), *const gk = gq + QT * C::Q_BYTES, *const gv = gk + C::KV_BYTES;
+    uint8_t *const gq = dsm + (base - smem_u32(dsm));
+    const uint32_t off_k = C::NG * QT * C::Q_BYTES, off_v = off_k + NB * C::KV_BYTES;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const KvView &c = a.c;
     const int G = c.hq / c.hkv, P = c.page;
 
     if (tid == 0) {
-        mbar_init(&bar_s, 2);   // the product's completion, and the loaders' description of its tile
-        mbar_init(&bar_p, 4);
-        mbar_init(&bar_v, 1);
-        fence_mbar_init();
         s_item[0] = -1;
         s_nan = 0;
     }
@@ -127,16 +127,16 @@ __global__ void __launch_bounds__(256, (RowsCfg<D, QT>::CTAS))
     pdl_wait();
     pdl_launch_dependents();
 
-    // the blockIdx.x-th item of the call: sequence, kv head, tile of 128 rows (the last rows, which see most, first)
+    // the blockIdx.x-th item of the call: sequence, kv head, run of ROWS rows (the last rows, which see most, first)
     {
         int before = 0;
-        for (int b0 = 0; b0 < a.b.n && before <= (int)blockIdx.x; b0 += 256) {
+        for (int b0 = 0; b0 < a.b.n && before <= (int)blockIdx.x; b0 += C::NT) {
             const int i = b0 + tid;
             int cnt = 0, rts = 0;
             if (i < a.b.n) {
                 const KvSeq q = kv_sequence(c, a.b, i, blockIdx.x == 0 && blockIdx.y == 0);
                 const long long rows = (long long)q.n * G;
-                rts = rows >= a.rows_from ? (int)((rows + 127) / 128) : 0;
+                rts = rows >= a.rows_from ? (int)((rows + C::ROWS - 1) / C::ROWS) : 0;
                 cnt = rts * c.hkv;
             }
             int inc = cnt;
@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(256, (RowsCfg<D, QT>::CTAS))
             if (lane == 31) wsum[warp] = inc;
             __syncthreads();
             int at = before + inc - cnt;
-            for (int w = 0; w < 8; ++w) {
+            for (int w = 0; w < NW; ++w) {
                 at += w < warp ? wsum[w] : 0;
                 before += wsum[w];
             }
@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(256, (RowsCfg<D, QT>::CTAS))
     }
     if (s_item[0] < 0) return;
     const KvSeq sq = kv_sequence(c, a.b, s_item[0], false);
-    const int h = s_item[2], row0 = s_item[1] * 128, rows = min(128, sq.n * G - row0), p0 = sq.len - sq.n;
+    const int h = s_item[2], row0 = s_item[1] * C::ROWS, rows = min(C::ROWS, sq.n * G - row0), p0 = sq.len - sq.n;
     const int pos_lo = p0 + row0 / G, pos_hi = p0 + (row0 + rows - 1) / G;
     // tiles [0, ns) and [w0, w1) hold what the rows see; this CTA takes its split's share of them
     const long long low = a.window > 0 ? max(0ll, (long long)pos_lo - a.window + 1) : 0ll;
@@ -177,6 +177,18 @@ __global__ void __launch_bounds__(256, (RowsCfg<D, QT>::CTAS))
         return j0 + TOK - 1 <= pos_lo && (a.window <= 0 || (long long)pos_hi - j0 < a.window || j0 + TOK <= a.sinks);
     };
 
+    const int groups = rows > 128 ? 2 : 1;   // that have rows
+    if (tid == 0) {
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(&bar_s[x], 2);   // the product, and what its issuer has seen of the loaders' (the tile's description)
+            mbar_init(&bar_o[x], 1);
+            mbar_init(&kfull[x], 4);
+            mbar_init(&vfull[x], 4);
+            mbar_init(&kempty[x], groups);
+            mbar_init(&vempty[x], groups);
+        }
+        fence_mbar_init();
+    }
     if (warp == 0) tmem_alloc(&taddr_s, C::TCOLS);
     bool dead = false;
     auto wait = [&](uint64_t *bar, uint32_t parity) {
@@ -188,9 +200,10 @@ __global__ void __launch_bounds__(256, (RowsCfg<D, QT>::CTAS))
 
     // ---------------------------------------------------------------- queries: a row per thread
     float qf = 0.f;
-    const bool on = tid < rows;   // rows <= 128: the softmax threads
+    const bool on = tid < rows;
+    const int grp = warp >> 2;   // of a row's thread
     const int pos = on ? p0 + (row0 + tid) / G : -1;
-    if (tid < 128) {
+    if (tid < C::ROWS) {
         const int64_t at = on ? ((int64_t)sq.start + (row0 + tid) / G) * a.ldq + (int64_t)(h * G + (row0 + tid) % G) * D : 0;
         float top = 0.f;
         if (on) {
@@ -217,7 +230,7 @@ __global__ void __launch_bounds__(256, (RowsCfg<D, QT>::CTAS))
             for (int e = 0; e < 8; ++e) split_pair(f[2 * e] * mul, f[2 * e + 1] * mul, hi[e], lo[e]);
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
-                const uint32_t off = (uint32_t)(x / 4) * 16384u + sw128_off(tid, (x % 4) * 2 + hf);
+                const uint32_t off = (uint32_t)(grp * QT) * C::Q_BYTES + (uint32_t)(x / 4) * 16384u + sw128_off(tid & 127, (x % 4) * 2 + hf);
                 *(uint4 *)(gq + off) = make_uint4(hi[4 * hf], hi[4 * hf + 1], hi[4 * hf + 2], hi[4 * hf + 3]);
                 if constexpr (QT == 2)
                     *(uint4 *)(gq + C::Q_BYTES + off) = make_uint4(lo[4 * hf], lo[4 * hf + 1], lo[4 * hf + 2], lo[4 * hf + 3]);
@@ -228,11 +241,11 @@ __global__ void __launch_bounds__(256, (RowsCfg<D, QT>::CTAS))
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t ts = taddr_s, to = ts + TOK;
+    const uint32_t tmem = taddr_s;
 
-    if (warp >= 4) {
+    if (tid >= C::ROWS) {
         // ------------------------------------------------------------ loaders
-        const int lt = tid - 128;
+        const int lt = tid - C::ROWS;
         const int ppt = P >= TOK ? 1 : TOK / P;   // pages per tile
         float unit = 0.f;
         // page ids of tile i: lane x < ppt holds that of its x-th page (-1: no row sees it, or it is absent)
@@ -251,47 +264,40 @@ __global__ void __launch_bounds__(256, (RowsCfg<D, QT>::CTAS))
             }
             return page;
         };
-        // This thread's vectors of a tile: chunk ch of rows tr, tr + TPX, ...
-        constexpr int TPX = 128 / VPR;
-        static_assert(TPX % 8 == 0, "a vector's place in its swizzle atom is the same in every row it takes");
-        const int tr = lt / VPR, ch = lt % VPR, pshift = __ffs(min(P, TOK)) - 1;
+        // This thread's vectors of a tile: x = 0, 1, ...: 64-column block x % NBLK of row 32 (x / NBLK) + tr. Eight
+        // lanes hold four chunks of two rows, whose places in the swizzled atoms fall into different banks.
+        const int tr = lt / 4, ch = lt % 4, pshift = __ffs(min(P, TOK)) - 1;
         auto fetch = [&](const uint8_t *pool, int i, int pid, uint4 (&r)[NV]) {
             const int j0 = tile_of(i);
             const bool whole = is_whole(j0);
-            const size_t page_bytes = (size_t)P * D;
             const uint8_t *from = pool + (size_t)((j0 & (P - 1)) * D + ch * 16);
 #pragma unroll
-            for (int x = 0; x < NV; ++x) {
-                const int tok = x * TPX + tr;
+            for (int y = 0; y < TOK / 32; ++y) {
+                const int tok = y * 32 + tr;
                 const int page = __shfl_sync(0xffffffffu, pid, tok >> pshift);
-                r[x] = make_uint4(0, 0, 0, 0);
                 bool live = page >= 0;
                 if (!whole) {
                     const int j = j0 + tok;
                     live = live && j <= pos_hi && (a.window <= 0 || j < a.sinks || (long long)pos_lo - j < a.window);
                 }
-                if (live)
-                    r[x] = ld_codes((const uint4 *)(from + (unsigned)(page * c.hkv + h) * page_bytes +
-                                                    ((tok & ((1 << pshift) - 1)) * D)));
+                const uint8_t *row = from + (size_t)(unsigned)(page * c.hkv + h) * (unsigned)(P * D) +
+                                     (tok & ((1 << pshift) - 1)) * D;
+#pragma unroll
+                for (int b = 0; b < NBLK; ++b)
+                    r[y * NBLK + b] = live ? ld_codes((const uint4 *)(row + b * 64)) : make_uint4(0, 0, 0, 0);
             }
         };
-        // lanes of odd 128-byte blocks store their second half first: no bank conflict
-        const int first = (ch >> 2) & 1;
-        const uint32_t o_blk = (uint32_t)(ch / 4) * (TOK * 128u);
-        const uint32_t o_lo = o_blk + sw128_off(tr, (ch % 4) * 2 + first), o_hi = o_blk + sw128_off(tr, (ch % 4) * 2 + 1 - first);
-        auto convert = [&](uint8_t *dst, const uint4 (&r)[NV]) {
+        const uint32_t o_lo = sw128_off(tr, ch * 2), o_hi = sw128_off(tr, ch * 2 + 1);
+        auto convert = [&](uint32_t at, const uint4 (&r)[NV]) {
 #pragma unroll
             for (int x = 0; x < NV; ++x) {
                 const uint32_t w[4] = {r[x].x, r[x].y, r[x].z, r[x].w};
                 uint32_t f[8];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    f[2 * e] = e4m3x2_f16x2((uint16_t)w[e]);
-                    f[2 * e + 1] = e4m3x2_f16x2((uint16_t)(w[e] >> 16));
-                }
-                const uint4 lo = make_uint4(f[0], f[1], f[2], f[3]), hi = make_uint4(f[4], f[5], f[6], f[7]);
-                *(uint4 *)(dst + o_lo + x * TPX * 128) = first ? hi : lo;
-                *(uint4 *)(dst + o_hi + x * TPX * 128) = first ? lo : hi;
+                for (int e = 0; e < 4; ++e) e4m3x4_f16x4(w[e], f[2 * e], f[2 * e + 1]);
+                uint8_t *dst = gq + at + (x % NBLK) * (TOK * 128) + (x / NBLK) * 32 * 128;
+                *(uint4 *)(dst + o_lo) = make_uint4(f[0], f[1], f[2], f[3]);
+                *(uint4 *)(dst + o_hi) = make_uint4(f[4], f[5], f[6], f[7]);
             }
         };
         // A NaN value in a tile that not every row sees in full: 0 here, and the rows that see it learn of it at the end.
@@ -314,8 +320,8 @@ __global__ void __launch_bounds__(256, (RowsCfg<D, QT>::CTAS))
             vs = pid >= 0 ? a.l.vs[(size_t)pid * c.hkv + h] : 0.f;
         };
         auto describe = [&](int i, int pid, float ks, float vs) {
-            RowsMeta &m = meta[i & 1];
-            if (warp != 4) return;
+            RowsMeta &m = meta[i & 3];
+            if (warp != C::ROWS / 32) return;
             float top = vs;
 #pragma unroll
             for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -336,84 +342,84 @@ __global__ void __launch_bounds__(256, (RowsCfg<D, QT>::CTAS))
             }
             unit = top;
         };
-        constexpr uint32_t ID_S = f16_idesc(0, 0, 0, 128, TOK), ID_O = f16_idesc(0, 0, 1, 128, D);
-        auto issue_s = [&]() {
-#pragma unroll
-            for (int term = 0; term < QT; ++term)
-#pragma unroll
-                for (int b = 0; b < D / 64; ++b)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const uint64_t ad = sw128_desc(base + term * C::Q_BYTES + b * 16384u + j * 32u, 16u, 1024u);
-                        const uint64_t bd = sw128_desc(smem_u32(gk) + b * (TOK * 128u) + j * 32u, 16u, 1024u);
-                        umma_f16(ts, ad, bd, ID_S, term + b + j > 0);
-                    }
-            umma_commit(&bar_s);
+        auto ready = [&](uint64_t *bar) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar);
         };
-        auto issue_o = [&](bool accum) {
-#pragma unroll
-            for (int term = 0; term < QT; ++term)
-#pragma unroll
-                for (int j = 0; j < TOK / 16; ++j) {
-                    const uint64_t bd = sw128_desc(smem_u32(gv) + j * 2048u, TOK * 128u, 1024u);
-                    umma_f16_ts(to, ts + term * (TOK / 2) + j * 8, bd, ID_O, accum || term + j > 0);
-                }
-            umma_commit(&bar_v);
-        };
-        auto start_s = [&]() {
-            issue_s();
-            mbar_arrive(&bar_s);
-        };
-        // Everything that a step needs was asked for at least one step before: the page ids of a tile three
-        // steps ahead of its weights' product, its scales and keys two, its values one.
+        // Codes and scales are asked for a tile ahead, page ids two.
         uint4 kr[NV], vr[NV];
-        int pid1 = -1, pid2 = nt > 0 ? pages(0) : -1;   // pages of tiles i + 1 and i + 2
-        float ks1 = 0.f, vs1 = 0.f;
+        int pid0 = -1, pid1 = nt > 0 ? pages(0) : -1;
+        float ks0 = 0.f, vs0 = 0.f;
 #pragma unroll 1
-        for (int i = -2; i < nt; ++i) {
-            const int pid3 = i + 3 < nt ? pages(i + 3) : -1;
+        for (int i = -1; i < nt; ++i) {
+            const int pid2 = i + 2 < nt ? pages(i + 2) : -1, b = i & (NB - 1);
+            if (i >= 0) {
+                if (i >= NB) wait(&kempty[b], (i / NB - 1) & 1);
+                describe(i, pid0, ks0, vs0);
+                convert(off_k + b * C::KV_BYTES, kr);
+                ready(&kfull[b]);
+            }
+            if (i + 1 < nt) {
+                scales(pid1, ks0, vs0);
+                fetch(a.l.k, i + 1, pid1, kr);
+            }
             if (i >= 0) {
                 strip_nan(i, vr);
-                if (i > 0) wait(&bar_v, (i - 1) & 1);      // the product that read the last values is done
-                convert(gv, vr);
+                if (i >= NB) wait(&vempty[b], (i / NB - 1) & 1);
+                convert(off_v + b * C::KV_BYTES, vr);
+                ready(&vfull[b]);
             }
-            if (i >= -1 && i + 1 < nt) {
-                fetch(a.l.v, i + 1, pid1, vr);
-                if (i >= 0) wait(&bar_s, i & 1);           // and the one that read the last keys
-                describe(i + 1, pid1, ks1, vs1);
-                convert(gk, kr);
-            }
-            fence_proxy_async_smem();
-            bar_sync(1, 128);
-            if (lt == 0) {
-                if (i >= 0) {
-                    wait(&bar_p, i & 1);
-                    tc_fence_after();
-                    issue_o(i > 0);
-                }
-                if (i >= -1 && i + 1 < nt) start_s();
-            }
-            __syncwarp();
-            if (i + 2 < nt) {
-                scales(pid2, ks1, vs1);
-                fetch(a.l.k, i + 2, pid2, kr);
-            }
+            if (i + 1 < nt) fetch(a.l.v, i + 1, pid1, vr);
+            pid0 = pid1;
             pid1 = pid2;
-            pid2 = pid3;
         }
     }
 
     // ---------------------------------------------------------------- softmax
     float m = -INFINITY, l = 0.f, unit = 0.f;
     const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
-    if (warp < 4) {
+    const uint32_t ts = tmem + grp * (TOK + D), to = ts + TOK;
+    if (grp < groups && tid < C::ROWS) {
+        constexpr uint32_t ID_S = f16_idesc(0, 0, 0, 128, TOK), ID_O = f16_idesc(0, 0, 1, 128, D);
+        auto issue_s = [&](int i) {   // S = Q K^T of tile i
+            const int b = i & (NB - 1);
+            wait(&kfull[b], (i / NB) & 1);
+            const uint32_t q0 = base + (uint32_t)(grp * QT) * C::Q_BYTES, k0s = base + off_k + b * C::KV_BYTES;
+#pragma unroll
+            for (int term = 0; term < QT; ++term)
+#pragma unroll
+                for (int x = 0; x < D / 64; ++x)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        umma_f16(ts, sw128_desc(q0 + term * C::Q_BYTES + x * 16384u + j * 32u, 16u, 1024u),
+                                 sw128_desc(k0s + x * (TOK * 128u) + j * 32u, 16u, 1024u), ID_S, term + x + j > 0);
+            umma_commit(&bar_s[grp]);
+            umma_commit(&kempty[b]);
+            mbar_arrive(&bar_s[grp]);
+        };
+        auto issue_o = [&](int i) {   // O += P V
+            const int b = i & (NB - 1);
+            wait(&vfull[b], (i / NB) & 1);
+            const uint32_t v0s = base + off_v + b * C::KV_BYTES;
+#pragma unroll
+            for (int term = 0; term < QT; ++term)
+#pragma unroll
+                for (int j = 0; j < TOK / 16; ++j)
+                    umma_f16_ts(to, ts + term * (TOK / 2) + j * 8, sw128_desc(v0s + j * 2048u, TOK * 128u, 1024u), ID_O,
+                                i > 0 || term + j > 0);
+            umma_commit(&vempty[b]);
+            if (i + 1 == nt) umma_commit(&bar_o[grp]);
+        };
+        if (nt > 0 && (tid & 127) == 0) issue_s(0);
+        __syncwarp();
         const int pshift = __ffs(P) - 1;
         // A page's factor from product to base-2 score. Never 0, so that -infinity stays what it is.
         auto factor = [&](const RowsMeta &mt, int pg) { return fmaxf(qf * mt.ks[pg], 1e-37f); };
         for (int i = 0; i < nt; ++i) {
-            wait(&bar_s, i & 1);
+            wait(&bar_s[grp], i & 1);
             tc_fence_after();
-            const RowsMeta &mt = meta[i & 1];
+            const RowsMeta &mt = meta[i & 3];
             const int j0 = tile_of(i);
             // scores to factors of the row's largest; what a row does not see becomes -infinity in place
             float top = -INFINITY;
@@ -510,10 +516,15 @@ __global__ void __launch_bounds__(256, (RowsCfg<D, QT>::CTAS))
             }
             tmem_wait_st();
             tc_fence_before();
+            bar_sync(2 + grp, 128);
+            if ((tid & 127) == 0) {
+                tc_fence_after();
+                issue_o(i);
+                if (i + 1 < nt) issue_s(i + 1);
+            }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bar_p);
         }
-        if (nt > 0) wait(&bar_v, (nt - 1) & 1);
+        if (nt > 0) wait(&bar_o[grp], 0);
         tc_fence_after();
 
         // ------------------------------------------------------------ output
@@ -534,20 +545,20 @@ __global__ void __launch_bounds__(256, (RowsCfg<D, QT>::CTAS))
                 if (nt > 0)
                     o = make_float4(__uint_as_float(r[e]) * back, __uint_as_float(r[e + 1]) * back,
                                     __uint_as_float(r[e + 2]) * back, __uint_as_float(r[e + 3]) * back);
-                if (splits > 1) *(float4 *)&a.rows_part[(unit_id * 128 + tid) * D + ch * 32 + e] = o;
+                if (splits > 1) *(float4 *)&a.rows_part[(unit_id * C::ROWS + tid) * D + ch * 32 + e] = o;
                 else store_row(a, f4, h, G, D, row0 + tid, ch * 32 + e, o, m, l);
             }
         }
         if (splits > 1 && on) {
-            a.rows_ml[(unit_id * 128 + tid) * 2] = m;
-            a.rows_ml[(unit_id * 128 + tid) * 2 + 1] = l;
+            a.rows_ml[(unit_id * C::ROWS + tid) * 2] = m;
+            a.rows_ml[(unit_id * C::ROWS + tid) * 2 + 1] = l;
         }
     }
     tc_fence_before();
     __syncthreads();
     if (warp == 0) {
         tc_fence_after();
-        tmem_dealloc(ts, C::TCOLS);
+        tmem_dealloc(tmem, C::TCOLS);
     }
     const int4 f4 = make_int4(sq.row, sq.len, sq.start, sq.n);
     if (splits > 1) {
@@ -559,16 +570,16 @@ __global__ void __launch_bounds__(256, (RowsCfg<D, QT>::CTAS))
         __syncthreads();
         if (!s_last) return;
         const int64_t u0 = (int64_t)blockIdx.x * splits;
-        for (int x = tid; x < rows * (D / 4); x += 256) {
+        for (int x = tid; x < rows * (D / 4); x += C::NT) {
             const int r = x / (D / 4), d = (x % (D / 4)) * 4;
             float M = -INFINITY, S = 0.f;
-            for (int y = 0; y < splits; ++y) M = fmaxf(M, __ldcg(&a.rows_ml[((u0 + y) * 128 + r) * 2]));
+            for (int y = 0; y < splits; ++y) M = fmaxf(M, __ldcg(&a.rows_ml[((u0 + y) * C::ROWS + r) * 2]));
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
             for (int y = 0; y < splits; ++y) {
-                const float my = __ldcg(&a.rows_ml[((u0 + y) * 128 + r) * 2]);
-                const float ly = __ldcg(&a.rows_ml[((u0 + y) * 128 + r) * 2 + 1]);
+                const float my = __ldcg(&a.rows_ml[((u0 + y) * C::ROWS + r) * 2]);
+                const float ly = __ldcg(&a.rows_ml[((u0 + y) * C::ROWS + r) * 2 + 1]);
                 const float w = my == -INFINITY ? (ly != 0.f ? 1.f : 0.f) : ex2(my - M);
-                const float4 v = __ldcg((const float4 *)&a.rows_part[((u0 + y) * 128 + r) * D + d]);
+                const float4 v = __ldcg((const float4 *)&a.rows_part[((u0 + y) * C::ROWS + r) * D + d]);
                 S += w * ly;
                 o.x += v.x * w, o.y += v.y * w, o.z += v.z * w, o.w += v.w * w;
             }
@@ -608,7 +619,7 @@ cudaError_t rows_launch(const KvAttendArgs &a, unsigned items, unsigned splits, 
 {
     Launch L;
     L.grid = dim3(items, splits);
-    L.block = dim3(256);
+    L.block = dim3(RowsCfg<D, QT>::NT);
     L.smem = RowsCfg<D, QT>::SMEM;
     L.stream = s;
     L.pdl = true;
