@@ -66,7 +66,7 @@ pi_status_t validate(const pi_kv_desc_t *d)
     if (d->n_heads > (1 << 16)) return PI_ERR_UNSUPPORTED;
     const int64_t lim = (int64_t)1 << 31;
     // tensor-map rows and positions are 32-bit
-    if ((int64_t)d->n_pages * d->n_kv_heads >= lim / d->page_tokens || (int64_t)d->max_pages * d->page_tokens >= lim)
+    if ((int64_t)d->n_pages * d->n_kv_heads >= lim / d->page_tokens || (int64_t)d->max_pages * d->page_tokens > KV_MAX_LEN)
         return PI_ERR_UNSUPPORTED;
     return PI_OK;
 }
@@ -114,8 +114,9 @@ cudaError_t attend_of(const pi_kv *h, int layer, KvAttendArgs a, cudaStream_t s)
     if (many && e == cudaSuccess) {
         const int64_t items = (rows / rows_per_item(D) + n) * a.c.hkv;   // at most one partly filled per sequence
         const int64_t splits = items < h->nsm ? std::min<int64_t>(16, 2 * h->nsm / items) : 1;
-        e = a.dtype == PI_F32 ? rows_launch<D, 2>(a, (unsigned)items, (unsigned)splits, s)
-                              : rows_launch<D, 1>(a, (unsigned)items, (unsigned)splits, s);
+        const CUtensorMap &mk = h->map_k[layer], &mv = h->map_v[layer];
+        e = a.dtype == PI_F32 ? rows_launch<D, 2>(a, mk, mv, (unsigned)items, (unsigned)splits, s)
+                              : rows_launch<D, 1>(a, mk, mv, (unsigned)items, (unsigned)splits, s);
     }
     return e;
 }
@@ -289,7 +290,7 @@ pi_status_t pi_kv_append(pi_kv_t *h, int32_t layer, const int32_t *seqs, const i
     pi_status_t s;
     if ((s = check_call(h, n))) return s;
     const int es = elt_size(dtype);
-    if (layer < 0 || layer >= h->desc.n_layers || n_tokens < 0 || !es) return PI_ERR_INVALID_ARG;
+    if (layer < 0 || layer >= h->desc.n_layers || n_tokens < 0 || n_tokens > KV_MAX_LEN || !es) return PI_ERR_INVALID_ARG;
     if (n == 0 || n_tokens == 0) return PI_OK;
     if ((s = check_batch(h, seqs, tok_start, n))) return s;
     const int64_t width = (int64_t)h->desc.n_kv_heads * h->desc.head_dim;
@@ -306,7 +307,7 @@ pi_status_t pi_kv_attend(pi_kv_t *h, int32_t layer, const int32_t *seqs, const i
     pi_status_t s;
     if ((s = check_call(h, n))) return s;
     const int es = elt_size(dtype);
-    if (layer < 0 || layer >= h->desc.n_layers || n_tokens < 0 || !es || !std::isfinite(scale) || sinks < 0)
+    if (layer < 0 || layer >= h->desc.n_layers || n_tokens < 0 || n_tokens > KV_MAX_LEN || !es || !std::isfinite(scale) || sinks < 0)
         return PI_ERR_INVALID_ARG;
     if (n == 0 || n_tokens == 0) return PI_OK;
     if ((s = check_batch(h, seqs, tok_start, n))) return s;
@@ -325,8 +326,9 @@ pi_status_t pi_kv_attend(pi_kv_t *h, int32_t layer, const int32_t *seqs, const i
     a.ldo = ld_out;
     a.dtype = dtype;
     a.scale_log2 = (float)((double)scale * 1.4426950408889634);
-    a.window = window;
-    a.sinks = sinks;
+    // no window: one that is never shorter than the distance of two positions (all below 2^30)
+    a.window = window > 0 ? std::min(window, KV_MAX_LEN) : KV_MAX_LEN;
+    a.sinks = std::min(sinks, KV_MAX_LEN);
     a.part = h->part;
     a.part_ml = h->part_ml;
     a.tickets = h->tickets;

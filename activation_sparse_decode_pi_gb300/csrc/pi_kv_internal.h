@@ -10,7 +10,7 @@
 namespace pi {
 
 constexpr int KV_TILE = 64;        // positions per tile of the attention kernels
-constexpr float KV_E4M3_MAX = 448.f;
+constexpr int KV_MAX_LEN = 1 << 30;   // positions of a sequence and tokens of a call: differences stay 32-bit
 constexpr int KV_MIN_EXP = -120;   // smallest exponent of a block scale
 
 // The cache as the kernels see it.
@@ -42,7 +42,7 @@ struct KvAttendArgs {
     int64_t ldq, ldo;          // elements
     int dtype;
     float scale_log2;          // scale * log2(e)
-    int window, sinks;
+    int window, sinks;         // window KV_MAX_LEN: none
     float *part;               // partial numerators [2 * grid][rows][dim]
     float *part_ml;            // their running maximum and sum [2 * grid][rows][2]
     uint32_t *tickets;         // [grid], zero on entry, left zero
@@ -71,10 +71,11 @@ constexpr int rows_per_item(int dim) { return dim == 256 ? 128 : 256; }
 template <int D, int QT>
 cudaError_t rows_setup();
 template <int D, int QT>
-cudaError_t rows_launch(const KvAttendArgs &a, unsigned items, unsigned splits, cudaStream_t s);
+cudaError_t rows_launch(const KvAttendArgs &a, const CUtensorMap &mk, const CUtensorMap &mv, unsigned items,
+                        unsigned splits, cudaStream_t s);
 #define PI_KV_EXTERN(D, QT)                        \
     extern template cudaError_t rows_setup<D, QT>(); \
-    extern template cudaError_t rows_launch<D, QT>(const KvAttendArgs &, unsigned, unsigned, cudaStream_t);
+    extern template cudaError_t rows_launch<D, QT>(const KvAttendArgs &, const CUtensorMap &, const CUtensorMap &, unsigned, unsigned, cudaStream_t);
 PI_KV_EXTERN(64, 1) PI_KV_EXTERN(64, 2) PI_KV_EXTERN(128, 1)
 PI_KV_EXTERN(128, 2) PI_KV_EXTERN(256, 1) PI_KV_EXTERN(256, 2)
 #undef PI_KV_EXTERN

@@ -10,8 +10,8 @@
 // become f16 in shared memory first, since a tcgen05 product takes operands of one width and 8 bits are
 // too few for queries and weights. So a CTA works on NG = 2 tiles of 128 rows at once (head dim 256: one):
 // a converted tile serves both, and one's products run under the other's softmax. Each has 4 warps
-// with a row per thread, whose first thread issues its products; 4 more warps load codes (16-byte
-// loads, a tile ahead in registers) and convert them into a ring of NB tiles.
+// with a row per thread, whose first thread issues its products; 8 more warps convert codes, which TMA
+// brings a tile ahead, into a ring of NB tiles.
 // Rounding: as in pi_kv_split.cuh: q as f16 scaled per row by a power of two, weights as f16 in
 // units of 2^-7 of a reference that trails the running maximum by at most 2^8 (floor 2^-31 of the
 // row's largest weight). QT = 2 (fp32 output): a second f16 term of both.
@@ -25,16 +25,25 @@ namespace pi {
 template <int D, int QT>
 struct RowsCfg {
     static constexpr int NG = D == 256 ? 1 : 2;                 // groups of 128 rows
-    static constexpr int ROWS = 128 * NG, NT = ROWS + 128;      // threads: a row each, and the loaders
+    static constexpr int ROWS = 128 * NG, LOADERS = 256, NT = ROWS + LOADERS;   // threads: a row each, and the loaders
     static constexpr int TOK = D == 256 || QT == 2 ? 64 : 128;  // positions per tile
     static constexpr int NB = D == 256 && QT == 2 ? 1 : 2;      // tiles of K and of V in shared memory
     static constexpr int Q_BYTES = 128 * D * 2, KV_BYTES = TOK * D * 2;
-    static constexpr int SMEM = 1024 + NG * QT * Q_BYTES + 2 * NB * KV_BYTES;
+    static constexpr int STAGE = TOK * D;                       // bytes of the codes of one tile
+    static constexpr int SMEM = 1024 + NG * QT * Q_BYTES + 2 * NB * KV_BYTES + 2 * STAGE;
     static constexpr int TCOLS = 512;                           // per group: S (TOK columns) and O (D columns)
 };
 
 constexpr float ROWS_TRAIL = 8.f;   // base-2 growth of the maximum that is taken up without rescaling
 constexpr float ROWS_UNIT = 7.f;    // weights are kept times 2^7: below 2^15 with the trail
+
+// True in one thread of a converged warp.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
 
 // 32 columns of this thread's lane, asynchronously
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t *r)
@@ -85,37 +94,47 @@ __device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, ui
 }
 
 // The lowest n bits (n <= 0: none, n >= 32: all).
-__device__ __forceinline__ uint32_t low_bits(long long n)
+__device__ __forceinline__ uint32_t low_bits(int n)
 {
-    return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << (int)n) - 1u;
+    return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
 }
 
-// Pages of one tile for the softmax: scale factors and which are there.
+// One tile for the softmax, by runs of 16 positions (each in one page).
 struct RowsMeta {
     float ks[8];      // key scale
     float vexp[8];    // ROWS_UNIT + log2(value scale / unit): the value scale rides in the weight's exponent
     float vback[8];   // 2^-vexp
     float unit;       // largest value scale of the tiles so far
     float shrink;     // the last tile's unit over this one's
-    uint32_t valid;   // bit per page: present
+    uint32_t valid;   // bit per run: its page is present
     int whole;        // every row sees every position of the tile
 };
 
+__device__ __forceinline__ float lg2(float x)
+{
+    float r;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
 template <int D, int QT>
-__global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_constant__ KvAttendArgs a)
+__global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_constant__ KvAttendArgs a,
+                                                                    const __grid_constant__ CUtensorMap mk,
+                                                                    const __grid_constant__ CUtensorMap mv)
 {
     using C = RowsCfg<D, QT>;
     constexpr int TOK = C::TOK, NB = C::NB, NW = C::NT / 32;
-    constexpr int NBLK = D / 64, NV = TOK * D / 16 / 128;   // 64-column blocks; 16-byte vectors per loader thread
+    constexpr int NBLK = D / 64, NV = TOK * D / 16 / C::LOADERS;   // 64-column blocks; 16-byte vectors per loader thread
+    constexpr int RPY = C::LOADERS / 4;   // rows of a tile that the loaders take at a time
     extern __shared__ uint8_t dsm[];
-    __shared__ uint64_t bar_s[2], bar_o[2], kfull[2], kempty[2], vfull[2], vempty[2];
+    __shared__ uint64_t bar_s[2], bar_o[2], kfull[2], kempty[2], vfull[2], vempty[2], sfull[2], sempty[2];
     __shared__ uint32_t taddr_s;
     __shared__ RowsMeta meta[4];
     __shared__ int s_item[4], wsum[NW], s_nan, s_last;
     const uint32_t base = (smem_u32(dsm) + 1023u) & ~1023u;
     uint8_t *const gq = dsm + (base - smem_u32(dsm));
-    const uint32_t off_k = C::NG * QT * C::Q_BYTES, off_v = off_k + NB * C::KV_BYTES;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t off_k = C::NG * QT * C::Q_BYTES, off_v = off_k + NB * C::KV_BYTES, off_st = off_v + NB * C::KV_BYTES;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;   // warp: uniform
     const KvView &c = a.c;
     const int G = c.hq / c.hkv, P = c.page;
 
@@ -166,15 +185,14 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
     const int h = s_item[2], row0 = s_item[1] * C::ROWS, rows = min(C::ROWS, sq.n * G - row0), p0 = sq.len - sq.n;
     const int pos_lo = p0 + row0 / G, pos_hi = p0 + (row0 + rows - 1) / G;
     // tiles [0, ns) and [w0, w1) hold what the rows see; this CTA takes its split's share of them
-    const long long low = a.window > 0 ? max(0ll, (long long)pos_lo - a.window + 1) : 0ll;
-    const int w0 = (int)(low / TOK), w1 = pos_hi < 0 ? w0 : pos_hi / TOK + 1;
-    const int ns = a.window > 0 && pos_hi >= 0 ? (int)min(((long long)a.sinks + TOK - 1) / TOK, (long long)w0) : 0;
+    const int w0 = max(0, pos_lo - a.window + 1) / TOK, w1 = pos_hi < 0 ? w0 : pos_hi / TOK + 1;
+    const int ns = pos_hi >= 0 ? min((a.sinks + TOK - 1) / TOK, w0) : 0;
     const int nt_all = ns + max(w1 - w0, 0), splits = gridDim.y;
     const int k0 = (int)((long long)nt_all * blockIdx.y / splits), k1 = (int)((long long)nt_all * (blockIdx.y + 1) / splits);
     const int nt = k1 - k0;
     auto tile_of = [&](int i) { return (k0 + i < ns ? k0 + i : w0 + k0 + i - ns) * TOK; };   // its first position
     auto is_whole = [&](int j0) {
-        return j0 + TOK - 1 <= pos_lo && (a.window <= 0 || (long long)pos_hi - j0 < a.window || j0 + TOK <= a.sinks);
+        return j0 + TOK - 1 <= pos_lo && (pos_hi - j0 < a.window || j0 + TOK <= a.sinks);
     };
 
     const int groups = rows > 128 ? 2 : 1;   // that have rows
@@ -182,8 +200,10 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
         for (int x = 0; x < 2; ++x) {
             mbar_init(&bar_s[x], 2);   // the product, and what its issuer has seen of the loaders' (the tile's description)
             mbar_init(&bar_o[x], 1);
-            mbar_init(&kfull[x], 4);
-            mbar_init(&vfull[x], 4);
+            mbar_init(&kfull[x], C::LOADERS / 32);
+            mbar_init(&vfull[x], C::LOADERS / 32);
+            mbar_init(&sfull[x], 1);
+            mbar_init(&sempty[x], C::LOADERS / 32);
             mbar_init(&kempty[x], groups);
             mbar_init(&vempty[x], groups);
         }
@@ -246,59 +266,82 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
     if (tid >= C::ROWS) {
         // ------------------------------------------------------------ loaders
         const int lt = tid - C::ROWS;
-        const int ppt = P >= TOK ? 1 : TOK / P;   // pages per tile
+        const int page_shift = __ffs(P) - 1, ppt = max(1, TOK >> page_shift);   // pages per tile
         float unit = 0.f;
-        // page ids of tile i: lane x < ppt holds that of its x-th page (-1: no row sees it, or it is absent)
+        // Page ids of tile i: lane x < ppt holds that of its x-th page, as the table has it; UNSEEN where no row sees the
+        // page. Looked at (clean) a tile later, so that nothing waits for the load.
+        constexpr int UNSEEN = -2;
         auto pages = [&](int i) {
-            int page = -1;
-            const int j0 = tile_of(i) + lane * P;
-            if (lane < ppt && j0 <= pos_hi) {
-                const int end = j0 + min(P, TOK);
-                if (a.window <= 0 || j0 < a.sinks || (long long)pos_lo - (end - 1) < a.window) {
-                    page = c.table[(size_t)sq.row * c.max_pages + j0 / P];
-                    if (page < 0 || page >= c.n_pages) {
-                        set_status(c.status, ST_DEVICE_CHECK);
-                        page = -1;
-                    }
-                }
-            }
-            return page;
+            const int j0 = tile_of(i) + (lane << page_shift), end = j0 + min(P, TOK);
+            const bool seen = lane < ppt && j0 <= pos_hi &&
+                              (j0 < a.sinks || pos_lo - (end - 1) < a.window);
+            return seen ? c.table[(size_t)sq.row * c.max_pages + (j0 >> page_shift)] : UNSEEN;
         };
-        // This thread's vectors of a tile: x = 0, 1, ...: 64-column block x % NBLK of row 32 (x / NBLK) + tr. Eight
-        // lanes hold four chunks of two rows, whose places in the swizzled atoms fall into different banks.
-        const int tr = lt / 4, ch = lt % 4, pshift = __ffs(min(P, TOK)) - 1;
-        auto fetch = [&](const uint8_t *pool, int i, int pid, uint4 (&r)[NV]) {
+        auto clean = [&](int pid) { return (unsigned)pid < (unsigned)c.n_pages ? pid : -1; };
+        // Codes of tile i (kv 0: keys, 1: values) into their stage, by the first loader warp. Absent pages are left out.
+        const int box_rows = min(P, KV_TILE), box_shift = __ffs(box_rows) - 1, boxes = TOK >> box_shift;
+        const int pshift = __ffs(min(P, TOK)) - 1;   // of a page's positions inside a tile
+        auto request = [&](int kv, int i, int pid) {
+            const int page = __shfl_sync(0xffffffffu, pid, lane < boxes ? (lane << box_shift) >> pshift : 0);
+            const bool go = lane < boxes && page >= 0;
+            const uint32_t n = __popc(__ballot_sync(0xffffffffu, go));
+            if (i > 0) wait(&sempty[kv], (i - 1) & 1);   // the loaders have read the last tile's
+            if (lane == 0) mbar_arrive_expect_tx(&sfull[kv], n * box_rows * D);
+            __syncwarp();
+            if (go) {
+                const int row = (page * c.hkv + h) * P + ((tile_of(i) + lane * box_rows) & (P - 1));
+                uint8_t *dst = gq + off_st + kv * C::STAGE + lane * box_rows * (D < 128 ? D : 128);
+#pragma unroll
+                for (int x0 = 0; x0 < D; x0 += 128) tma_load_2d(dst + x0 * TOK, kv ? &mv : &mk, x0, row, &sfull[kv]);
+            }
+            __syncwarp();
+        };
+        // This thread's vectors of a tile: rows RPY y + tr, 64-column blocks b. Eight lanes hold four chunks of two
+        // rows, odd rows a block off, so that reads of the stage and writes of the operand hit every bank once.
+        const int tr = lt / 4, ch = lt % 4, odd = NBLK > 1 ? tr & 1 : 0;
+        auto fetch = [&](int kv, int i, int pid, uint4 (&r)[NV]) {
+            wait(&sfull[kv], i & 1);
+            const uint8_t *st = gq + off_st + kv * C::STAGE;
+#pragma unroll
+            for (int y = 0; y < TOK / RPY; ++y)
+#pragma unroll
+                for (int b = 0; b < NBLK; ++b) {
+                    const int tok = y * RPY + tr, bb = b ^ odd;
+                    const int off = D == 64 ? tok * 64 + ((ch ^ ((tr >> 1) & 3)) << 4)
+                                            : (bb >> 1) * TOK * 128 + tok * 128 + ((((bb & 1) * 4 + ch) ^ (tr & 7)) << 4);
+                    r[y * NBLK + b] = *(const uint4 *)(st + off);
+                }
             const int j0 = tile_of(i);
-            const bool whole = is_whole(j0);
-            const uint8_t *from = pool + (size_t)((j0 & (P - 1)) * D + ch * 16);
+            const uint32_t there = __ballot_sync(0xffffffffu, pid >= 0);
+            if (!is_whole(j0) || there != (1u << ppt) - 1u) {   // positions that no row sees, absent pages: zeros
 #pragma unroll
-            for (int y = 0; y < TOK / 32; ++y) {
-                const int tok = y * 32 + tr;
-                const int page = __shfl_sync(0xffffffffu, pid, tok >> pshift);
-                bool live = page >= 0;
-                if (!whole) {
-                    const int j = j0 + tok;
-                    live = live && j <= pos_hi && (a.window <= 0 || j < a.sinks || (long long)pos_lo - j < a.window);
+                for (int y = 0; y < TOK / RPY; ++y) {
+                    const int tok = y * RPY + tr, j = j0 + tok;
+                    const bool live = ((there >> (tok >> pshift)) & 1u) && j <= pos_hi &&
+                                      (j < a.sinks || pos_lo - j < a.window);
+#pragma unroll
+                    for (int b = 0; b < NBLK; ++b)
+                        if (!live) r[y * NBLK + b] = make_uint4(0, 0, 0, 0);
                 }
-                const uint8_t *row = from + (size_t)(unsigned)(page * c.hkv + h) * (unsigned)(P * D) +
-                                     (tok & ((1 << pshift) - 1)) * D;
-#pragma unroll
-                for (int b = 0; b < NBLK; ++b)
-                    r[y * NBLK + b] = live ? ld_codes((const uint4 *)(row + b * 64)) : make_uint4(0, 0, 0, 0);
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sempty[kv]);
         };
-        const uint32_t o_lo = sw128_off(tr, ch * 2), o_hi = sw128_off(tr, ch * 2 + 1);
         auto convert = [&](uint32_t at, const uint4 (&r)[NV]) {
+            const uint32_t o_lo = sw128_off(tr, ch * 2), o_hi = sw128_off(tr, ch * 2 + 1);
 #pragma unroll
-            for (int x = 0; x < NV; ++x) {
-                const uint32_t w[4] = {r[x].x, r[x].y, r[x].z, r[x].w};
-                uint32_t f[8];
+            for (int y = 0; y < TOK / RPY; ++y)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) e4m3x4_f16x4(w[e], f[2 * e], f[2 * e + 1]);
-                uint8_t *dst = gq + at + (x % NBLK) * (TOK * 128) + (x / NBLK) * 32 * 128;
-                *(uint4 *)(dst + o_lo) = make_uint4(f[0], f[1], f[2], f[3]);
-                *(uint4 *)(dst + o_hi) = make_uint4(f[4], f[5], f[6], f[7]);
-            }
+                for (int b = 0; b < NBLK; ++b) {
+                    const uint4 v = r[y * NBLK + b];
+                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                    uint32_t f[8];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) e4m3x4_f16x4(w[e], f[2 * e], f[2 * e + 1]);
+                    uint8_t *dst = gq + at + (b ^ odd) * (TOK * 128) + y * RPY * 128;
+                    *(uint4 *)(dst + o_lo) = make_uint4(f[0], f[1], f[2], f[3]);
+                    *(uint4 *)(dst + o_hi) = make_uint4(f[4], f[5], f[6], f[7]);
+                }
         };
         // A NaN value in a tile that not every row sees in full: 0 here, and the rows that see it learn of it at the end.
         auto strip_nan = [&](int i, uint4 (&r)[NV]) {
@@ -314,31 +357,32 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
                     }
             }
         };
-        // Scales of the pages of a tile (lanes as in pages()), and what the softmax makes of them.
+        // Scales of a tile's pages, one run of 16 positions to a lane, and what the softmax makes of them.
         auto scales = [&](int pid, float &ks, float &vs) {
-            ks = pid >= 0 ? a.l.ks[(size_t)pid * c.hkv + h] : 0.f;
-            vs = pid >= 0 ? a.l.vs[(size_t)pid * c.hkv + h] : 0.f;
+            const int page = __shfl_sync(0xffffffffu, pid, lane < TOK / 16 ? (lane * 16) >> pshift : 0);
+            ks = page >= 0 ? a.l.ks[(size_t)page * c.hkv + h] : 0.f;
+            vs = page >= 0 ? a.l.vs[(size_t)page * c.hkv + h] : 0.f;
         };
         auto describe = [&](int i, int pid, float ks, float vs) {
             RowsMeta &m = meta[i & 3];
-            if (warp != C::ROWS / 32) return;
             float top = vs;
 #pragma unroll
             for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
             top = fmaxf(unit, __shfl_sync(0xffffffffu, top, 0));
-            const uint32_t there = __ballot_sync(0xffffffffu, pid >= 0);
-            if (lane < ppt) {
+            const uint32_t there = __ballot_sync(0xffffffffu, __shfl_sync(0xffffffffu, pid, (lane * 16) >> pshift) >= 0);
+            if (lane < TOK / 16) {
                 // below 2^-60 of the largest scale a page adds nothing either way; its weights still count in the sum
-                const float b = (vs > 0.f ? fmaxf(log2f(vs / top), -60.f) : -60.f) + ROWS_UNIT;
+                const float b = (vs > 0.f ? fmaxf(lg2(vs) - lg2(top), -60.f) : -60.f) + ROWS_UNIT;
                 m.ks[lane] = ks;
                 m.vexp[lane] = b;
                 m.vback[lane] = ex2(-b);
             }
             if (lane == 0) {
+                constexpr uint32_t all = (1u << (TOK / 16)) - 1u;
                 m.unit = top;
                 m.shrink = top > unit ? unit / top : 1.f;
                 m.valid = there;
-                m.whole = is_whole(tile_of(i)) && there == (1u << ppt) - 1u;
+                m.whole = is_whole(tile_of(i)) && (there & all) == all;
             }
             unit = top;
         };
@@ -347,32 +391,40 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
             __syncwarp();
             if (lane == 0) mbar_arrive(bar);
         };
-        // Codes and scales are asked for a tile ahead, page ids two.
-        uint4 kr[NV], vr[NV];
-        int pid0 = -1, pid1 = nt > 0 ? pages(0) : -1;
-        float ks0 = 0.f, vs0 = 0.f;
+        // Codes and scales are asked for a tile ahead, page ids two. The first warp asks for keys, the third for
+        // values, the second describes the tile.
+        const int role = warp - C::ROWS / 32;
+        uint4 r[NV];
+        int pid0 = -1, raw1 = nt > 0 ? pages(0) : UNSEEN;
+        float ks0 = 0.f, vs0 = 0.f, ks1 = 0.f, vs1 = 0.f;
 #pragma unroll 1
         for (int i = -1; i < nt; ++i) {
-            const int pid2 = i + 2 < nt ? pages(i + 2) : -1, b = i & (NB - 1);
+            const int raw2 = i + 2 < nt ? pages(i + 2) : UNSEEN, pid1 = clean(raw1), b = i & (NB - 1);
+            const bool more = i + 1 < nt;
+            if (role == 1) {
+                if (pid1 < 0 && raw1 != UNSEEN) set_status(c.status, ST_DEVICE_CHECK);   // seen, but absent
+                if (more) scales(pid1, ks1, vs1);
+            }
+            if (i >= 0) fetch(0, i, pid0, r);
+            if (role == 0 && more) request(0, i + 1, pid1);
             if (i >= 0) {
                 if (i >= NB) wait(&kempty[b], (i / NB - 1) & 1);
-                describe(i, pid0, ks0, vs0);
-                convert(off_k + b * C::KV_BYTES, kr);
+                if (role == 1) describe(i, pid0, ks0, vs0);
+                convert(off_k + b * C::KV_BYTES, r);
                 ready(&kfull[b]);
+                fetch(1, i, pid0, r);
             }
-            if (i + 1 < nt) {
-                scales(pid1, ks0, vs0);
-                fetch(a.l.k, i + 1, pid1, kr);
-            }
+            if (role == 2 && more) request(1, i + 1, pid1);
             if (i >= 0) {
-                strip_nan(i, vr);
+                strip_nan(i, r);
                 if (i >= NB) wait(&vempty[b], (i / NB - 1) & 1);
-                convert(off_v + b * C::KV_BYTES, vr);
+                convert(off_v + b * C::KV_BYTES, r);
                 ready(&vfull[b]);
             }
-            if (i + 1 < nt) fetch(a.l.v, i + 1, pid1, vr);
             pid0 = pid1;
-            pid1 = pid2;
+            raw1 = raw2;
+            ks0 = ks1;
+            vs0 = vs1;
         }
     }
 
@@ -382,18 +434,22 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
     const uint32_t ts = tmem + grp * (TOK + D), to = ts + TOK;
     if (grp < groups && tid < C::ROWS) {
         constexpr uint32_t ID_S = f16_idesc(0, 0, 0, 128, TOK), ID_O = f16_idesc(0, 0, 1, 128, D);
+        // One thread of the group's first warp issues its products. Descriptors differ in their address only (bits 0-13,
+        // in 16 bytes), and everything here is uniform over the warp, so that each product is one instruction and an add.
+        const uint64_t dq = sw128_desc(base + (uint32_t)(grp * QT) * C::Q_BYTES, 16u, 1024u);
+        const uint64_t dk = sw128_desc(base + off_k, 16u, 1024u), dv = sw128_desc(base + off_v, TOK * 128u, 1024u);
         auto issue_s = [&](int i) {   // S = Q K^T of tile i
             const int b = i & (NB - 1);
             wait(&kfull[b], (i / NB) & 1);
-            const uint32_t q0 = base + (uint32_t)(grp * QT) * C::Q_BYTES, k0s = base + off_k + b * C::KV_BYTES;
+            const uint64_t k1 = dk + (uint32_t)(b * C::KV_BYTES / 16);
 #pragma unroll
             for (int term = 0; term < QT; ++term)
 #pragma unroll
                 for (int x = 0; x < D / 64; ++x)
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        umma_f16(ts, sw128_desc(q0 + term * C::Q_BYTES + x * 16384u + j * 32u, 16u, 1024u),
-                                 sw128_desc(k0s + x * (TOK * 128u) + j * 32u, 16u, 1024u), ID_S, term + x + j > 0);
+                        umma_f16(ts, dq + (uint32_t)((term * C::Q_BYTES + x * 16384 + j * 32) / 16),
+                                 k1 + (uint32_t)((x * TOK * 128 + j * 32) / 16), ID_S, term + x + j > 0);
             umma_commit(&bar_s[grp]);
             umma_commit(&kempty[b]);
             mbar_arrive(&bar_s[grp]);
@@ -401,44 +457,46 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
         auto issue_o = [&](int i) {   // O += P V
             const int b = i & (NB - 1);
             wait(&vfull[b], (i / NB) & 1);
-            const uint32_t v0s = base + off_v + b * C::KV_BYTES;
+            const uint64_t v1 = dv + (uint32_t)(b * C::KV_BYTES / 16);
 #pragma unroll
             for (int term = 0; term < QT; ++term)
 #pragma unroll
                 for (int j = 0; j < TOK / 16; ++j)
-                    umma_f16_ts(to, ts + term * (TOK / 2) + j * 8, sw128_desc(v0s + j * 2048u, TOK * 128u, 1024u), ID_O,
+                    umma_f16_ts(to, ts + term * (TOK / 2) + j * 8, v1 + (uint32_t)(j * 2048 / 16), ID_O,
                                 i > 0 || term + j > 0);
             umma_commit(&vempty[b]);
             if (i + 1 == nt) umma_commit(&bar_o[grp]);
         };
-        if (nt > 0 && (tid & 127) == 0) issue_s(0);
+        const bool issues = (warp & 3) == 0;
+        if (nt > 0 && issues && elect_one()) issue_s(0);
         __syncwarp();
-        const int pshift = __ffs(P) - 1;
-        // A page's factor from product to base-2 score. Never 0, so that -infinity stays what it is.
-        auto factor = [&](const RowsMeta &mt, int pg) { return fmaxf(qf * mt.ks[pg], 1e-37f); };
         for (int i = 0; i < nt; ++i) {
             wait(&bar_s[grp], i & 1);
             tc_fence_after();
             const RowsMeta &mt = meta[i & 3];
             const int j0 = tile_of(i);
+            // From product to base-2 score, by runs of 16. Never 0, so that -infinity stays what it is.
+            float factor[TOK / 16];
+#pragma unroll
+            for (int x = 0; x < TOK / 16; ++x) factor[x] = fmaxf(qf * mt.ks[x], 1e-37f);
             // scores to factors of the row's largest; what a row does not see becomes -infinity in place
             float top = -INFINITY;
-            auto take = [&](const uint32_t *r, int t0) {   // 16 positions: one page
+            auto take = [&](const uint32_t *r, float f) {   // 16 positions
                 float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                 for (int e = 0; e < 16; ++e) t[e & 3] = fmaxf(t[e & 3], __uint_as_float(r[e]));
                 const float t4 = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
-                if (t4 > -INFINITY) top = fmaxf(top, t4 * factor(mt, P >= TOK ? 0 : t0 >> pshift));
+                top = fmaxf(top, t4 * f);
             };
             if (mt.whole) {
-#pragma unroll 1
+#pragma unroll
                 for (int ch = 0; ch < TOK; ch += 64) {
                     uint32_t r[64];
                     tmem_ld32(ts + lane_base + ch, r);
                     tmem_ld32(ts + lane_base + ch + 32, r + 32);
                     tmem_wait_ld(r);
 #pragma unroll
-                    for (int g16 = 0; g16 < 64; g16 += 16) take(r + g16, ch + g16);
+                    for (int g16 = 0; g16 < 64; g16 += 16) take(r + g16, factor[(ch + g16) / 16]);
                 }
             } else {
 #pragma unroll 1
@@ -447,15 +505,14 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
                     tmem_ld32(ts + lane_base + ch, r);
                     const int j = j0 + ch;
                     uint32_t see = low_bits(pos - j + 1);
-                    if (a.window > 0) see &= ~low_bits((long long)pos - a.window + 1 - j) | low_bits((long long)a.sinks - j);
-                    const uint32_t v0 = mt.valid >> (P >= TOK ? 0 : ch >> pshift) & 1u;
-                    const uint32_t v1 = mt.valid >> (P >= TOK ? 0 : (ch + 16) >> pshift) & 1u;
-                    see &= (v0 ? 0xffffu : 0u) | (v1 ? 0xffff0000u : 0u);
+                    see &= ~low_bits(pos - a.window + 1 - j) | low_bits(a.sinks - j);
+                    const uint32_t there = mt.valid >> (ch / 16);
+                    see &= (there & 1u ? 0xffffu : 0u) | (there & 2u ? 0xffff0000u : 0u);
                     tmem_wait_ld(r);
 #pragma unroll
                     for (int e = 0; e < 32; ++e) r[e] = (see >> e) & 1u ? r[e] : 0xff800000u;
-                    take(r, ch);
-                    take(r + 16, ch + 16);
+                    take(r, fmaxf(qf * mt.ks[ch / 16], 1e-37f));
+                    take(r + 16, fmaxf(qf * mt.ks[ch / 16 + 1], 1e-37f));
                     tmem_st16(ts + lane_base + ch, r);
                     tmem_st16(ts + lane_base + ch + 16, r + 16);
                 }
@@ -483,7 +540,7 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
                 }
             }
             const float ref = m == -INFINITY ? 0.f : m;
-#pragma unroll 1
+#pragma unroll
             for (int ch = 0; ch < TOK; ch += 64) {
                 uint32_t r[64], plo[QT == 2 ? 32 : 1];
                 tmem_ld32(ts + lane_base + ch, r);
@@ -491,8 +548,7 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
                 tmem_wait_ld(r);
 #pragma unroll
                 for (int g16 = 0; g16 < 64; g16 += 16) {
-                    const int pg = P >= TOK ? 0 : (ch + g16) >> pshift;
-                    const float f = factor(mt, pg), off = mt.vexp[pg] - ref;
+                    const float f = factor[(ch + g16) / 16], off = mt.vexp[(ch + g16) / 16] - ref;
                     float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
                     for (int e = g16; e < g16 + 16; e += 2) {
@@ -504,7 +560,7 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
                         if constexpr (QT == 2) split_pair(x.x, x.y, r[e / 2], plo[e / 2]);
                         else r[e / 2] = pack_f16(x.x, x.y);
                     }
-                    l = fmaf(sum.x + sum.y, mt.vback[pg], l);
+                    l = fmaf(sum.x + sum.y, mt.vback[(ch + g16) / 16], l);
                 }
                 // the weights take the place of scores already read, their second terms (TOK 64) that of the rest
                 tmem_st16(ts + lane_base + ch / 2, r);
@@ -517,7 +573,7 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
             tmem_wait_st();
             tc_fence_before();
             bar_sync(2 + grp, 128);
-            if ((tid & 127) == 0) {
+            if (issues && elect_one()) {
                 tc_fence_after();
                 issue_o(i);
                 if (i + 1 < nt) issue_s(i + 1);
@@ -596,7 +652,7 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
         const int j0 = (x < ns ? x : w0 + x - ns) * TOK;
         if (is_whole(j0)) continue;
         for (int j = j0; j < j0 + TOK && j <= pos; ++j) {
-            if (a.window > 0 && pos - j >= a.window && j >= a.sinks) continue;
+            if (pos - j >= a.window && j >= a.sinks) continue;
             const int page = c.table[(size_t)sq.row * c.max_pages + j / P];
             if (page < 0 || page >= c.n_pages) continue;
             const uint32_t *v = (const uint32_t *)(a.l.v + (((size_t)page * c.hkv + h) * P + (j & (P - 1))) * D);
@@ -615,7 +671,8 @@ cudaError_t rows_setup()
 }
 
 template <int D, int QT>
-cudaError_t rows_launch(const KvAttendArgs &a, unsigned items, unsigned splits, cudaStream_t s)
+cudaError_t rows_launch(const KvAttendArgs &a, const CUtensorMap &mk, const CUtensorMap &mv, unsigned items,
+                        unsigned splits, cudaStream_t s)
 {
     Launch L;
     L.grid = dim3(items, splits);
@@ -624,7 +681,7 @@ cudaError_t rows_launch(const KvAttendArgs &a, unsigned items, unsigned splits, 
     L.stream = s;
     L.pdl = true;
     L.nsm = 0;
-    return launch_ex(L, k_kv_rows<D, QT>, a);
+    return launch_ex(L, k_kv_rows<D, QT>, a, mk, mv);
 }
 
 }  // namespace pi

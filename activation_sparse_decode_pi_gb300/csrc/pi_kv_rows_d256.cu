@@ -4,6 +4,6 @@
 namespace pi {
 template cudaError_t rows_setup<256, 1>();
 template cudaError_t rows_setup<256, 2>();
-template cudaError_t rows_launch<256, 1>(const KvAttendArgs &, unsigned, unsigned, cudaStream_t);
-template cudaError_t rows_launch<256, 2>(const KvAttendArgs &, unsigned, unsigned, cudaStream_t);
+template cudaError_t rows_launch<256, 1>(const KvAttendArgs &, const CUtensorMap &, const CUtensorMap &, unsigned, unsigned, cudaStream_t);
+template cudaError_t rows_launch<256, 2>(const KvAttendArgs &, const CUtensorMap &, const CUtensorMap &, unsigned, unsigned, cudaStream_t);
 }  // namespace pi

@@ -86,10 +86,9 @@ __global__ void __launch_bounds__(SplitCfg<D, TWO>::NT, 1)
 
     // tiles of every sequence, and their running sum
     auto view = [&](int L, int nq, int &w0, int &ns, int &nt) {   // tiles [0, ns) and [w0, ...) are read
-        const long long low = a.window > 0 ? max(0ll, (long long)L - nq - a.window + 1) : 0ll;
-        w0 = (int)(low / KV_TILE);
+        w0 = max(0, L - nq - a.window + 1) / KV_TILE;
         const int w1 = max((L + KV_TILE - 1) / KV_TILE, w0 + 1);
-        ns = a.window > 0 ? (int)min(((long long)a.sinks + KV_TILE - 1) / KV_TILE, (long long)w0) : 0;
+        ns = min((a.sinks + KV_TILE - 1) / KV_TILE, w0);
         nt = ns + w1 - w0;
     };
     long long run = 0;
@@ -167,8 +166,8 @@ __global__ void __launch_bounds__(SplitCfg<D, TWO>::NT, 1)
                 const int pos = tile * KV_TILE + sub * box_rows;
                 int page = -1;
                 float ks = 0.f, vs = 0.f;
-                const long long low = (long long)f.y - f.w - a.window + 1;   // first position in the windows
-                const bool seen = pos < f.y && (a.window <= 0 || pos < a.sinks || pos + box_rows > low);
+                const int low = f.y - f.w - a.window + 1;   // first position in the windows
+                const bool seen = pos < f.y && (pos < a.sinks || pos + box_rows > low);
                 if (k < g.k1 && lane < per * np && seen) {
                     page = c.table[(size_t)f.x * c.max_pages + pos / P];
                     if (page < 0 || page >= c.n_pages) {
@@ -332,7 +331,7 @@ __global__ void __launch_bounds__(SplitCfg<D, TWO>::NT, 1)
             const uint8_t *kt = ring + (size_t)ks_slot * C::SLOT;
             const uint32_t valid = meta[ks_slot].valid;
             const bool whole = valid == (1u << np) - 1u && j0 + KV_TILE - 1 <= pos_lo &&
-                               (a.window <= 0 || pos_hi - j0 < a.window || j0 + KV_TILE <= a.sinks);
+                               (pos_hi - j0 < a.window || j0 + KV_TILE <= a.sinks);
             float s[8][4];
 #pragma unroll
             for (int nt = 0; nt < 8; ++nt)
@@ -392,7 +391,7 @@ __global__ void __launch_bounds__(SplitCfg<D, TWO>::NT, 1)
                         if (!whole) {
                             const int j = j0 + nt * 8 + 2 * q + e;
                             const bool see = j <= pos[rr] && ((valid >> ((nt * 8) >> page_shift)) & 1u) &&
-                                             (a.window <= 0 || pos[rr] - j < a.window || j < a.sinks);
+                                             (pos[rr] - j < a.window || j < a.sinks);
                             v = see ? v : -INFINITY;
                         }
                         s[nt][2 * rr + e] = v;
@@ -445,7 +444,7 @@ __global__ void __launch_bounds__(SplitCfg<D, TWO>::NT, 1)
                 // meet a zero weight: 0 * NaN. Others that are NaN poison only the rows that see them.
                 auto dead_token = [&](int j) {
                     if (!((valid >> ((j - j0) >> page_shift)) & 1u) || j > pos_hi) return true;
-                    return a.window > 0 && j >= a.sinks && pos_lo - j >= a.window;
+                    return j >= a.sinks && pos_lo - j >= a.window;
                 };
                 bool nan = false;
                 for (int x = lane; x < C::SLOT / 16; x += 32) {
@@ -463,7 +462,7 @@ __global__ void __launch_bounds__(SplitCfg<D, TWO>::NT, 1)
                                 if ((vt[tile_byte<D>(tok, d)] & 0x7f) != 0x7f) continue;
                                 for (int rr = 0; rr < (TWO ? 1 : 2); ++rr) {
                                     const int j = j0 + tok;
-                                    if (j <= pos[rr] && (a.window <= 0 || pos[rr] - j < a.window || j < a.sinks))
+                                    if (j <= pos[rr] && (pos[rr] - j < a.window || j < a.sinks))
                                         poison(acc, jj, 2 * rr + e);
                                 }
                             }

@@ -22,7 +22,7 @@
  *    workspace, so they are ordered on one stream (or by events).
  *  - seqs: int32 [n] device, table rows, 0 <= n <= PI_KV_MAX_CALL_SEQS; tok_start: int32 [n + 1]
  *    device, ascending from 0: sequence i's new tokens are rows tok_start[i] .. tok_start[i + 1] of
- *    the call's token arrays (n_tokens rows; what lies past them is not touched, and flagged).
+ *    the call's token arrays (n_tokens <= 2^30 rows; what lies past them is not touched, and flagged).
  *    Except for pi_kv_attend, a sequence appears at most once in a call.
  *  - A step: pi_kv_reserve once (lengths grow, pages are found), then per layer pi_kv_append and
  *    pi_kv_attend. No call allocates, synchronises or reads back: a step can be captured in a graph.
@@ -46,7 +46,7 @@ typedef struct {
     int32_t page_tokens;   /* 16, 32, 64 or 128 */
     int32_t n_pages;       /* pages of the pool, >= 1; n_pages * n_kv_heads * page_tokens < 2^31 */
     int32_t max_seqs;      /* rows of the table, >= 1 */
-    int32_t max_pages;     /* columns of the table, >= 1; max_pages * page_tokens < 2^31 */
+    int32_t max_pages;     /* columns of the table, >= 1; max_pages * page_tokens <= 2^30 */
 } pi_kv_desc_t;
 
 typedef struct {
