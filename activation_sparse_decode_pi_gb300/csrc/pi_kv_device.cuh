@@ -71,6 +71,13 @@ __device__ __forceinline__ bool e4m3_any_nan(uint32_t w)
     return (((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0;
 }
 
+// The word with 0 for every NaN code.
+__device__ __forceinline__ uint32_t e4m3_no_nan(uint32_t w)
+{
+    const uint32_t n = ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;   // top bit of every NaN code
+    return w & ~((n - (n >> 7)) | n);
+}
+
 // ---------------------------------------------------------------- numbers -------------------
 
 __device__ __forceinline__ float ex2(float x)

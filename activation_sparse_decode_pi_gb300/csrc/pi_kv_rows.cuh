@@ -9,9 +9,10 @@
 // about as many issue slots (one exponential and a handful of operations per score), and e4m3 has to
 // become f16 in shared memory first, since a tcgen05 product takes operands of one width and 8 bits are
 // too few for queries and weights. So a CTA works on NG = 2 tiles of 128 rows at once (head dim 256: one):
-// a converted tile serves both, and one's products run under the other's softmax. Each has 4 warps
-// with a row per thread, whose first thread issues its products; 8 more warps convert codes, which TMA
-// brings a tile ahead, into a ring of NB tiles.
+// a converted tile serves both, and one's products run under the other's softmax. Each has 8 warps with
+// two threads to a row (a half of the tile's positions each: the softmax is latency-bound with fewer),
+// whose first warp issues its products; 4 more warps convert codes, which TMA brings a tile ahead,
+// into a ring of NB tiles.
 // Rounding: as in pi_kv_split.cuh: q as f16 scaled per row by a power of two, weights as f16 in
 // units of 2^-7 of a reference that trails the running maximum by at most 2^8 (floor 2^-31 of the
 // row's largest weight). QT = 2 (fp32 output): a second f16 term of both.
@@ -25,12 +26,13 @@ namespace pi {
 template <int D, int QT>
 struct RowsCfg {
     static constexpr int NG = D == 256 ? 1 : 2;                 // groups of 128 rows
-    static constexpr int ROWS = 128 * NG, LOADERS = 256, NT = ROWS + LOADERS;   // threads: a row each, and the loaders
+    static constexpr int ROWS = 128 * NG, RT = 2 * ROWS;        // rows, and their threads
+    static constexpr int LOADERS = 128, NT = RT + LOADERS;
     static constexpr int TOK = D == 256 || QT == 2 ? 64 : 128;  // positions per tile
     static constexpr int NB = D == 256 && QT == 2 ? 1 : 2;      // tiles of K and of V in shared memory
     static constexpr int Q_BYTES = 128 * D * 2, KV_BYTES = TOK * D * 2;
     static constexpr int STAGE = TOK * D;                       // bytes of the codes of one tile
-    static constexpr int SMEM = 1024 + NG * QT * Q_BYTES + 2 * NB * KV_BYTES + 2 * STAGE;
+    static constexpr int DATA = NG * QT * Q_BYTES + 2 * NB * KV_BYTES + 2 * STAGE;
     static constexpr int TCOLS = 512;                           // per group: S (TOK columns) and O (D columns)
 };
 
@@ -56,6 +58,17 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t *r)
           "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
           "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
           "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+}
+
+// 16 columns
+__device__ __forceinline__ void tmem_ld16u(uint32_t taddr, uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(taddr)
         : "memory");
 }
@@ -117,6 +130,24 @@ __device__ __forceinline__ float lg2(float x)
     return r;
 }
 
+template <int ROWS, int NW>
+struct RowsShared {
+    uint64_t bar_s[2], bar_o[2], kfull[2], kempty[2], vfull[2], vempty[2], sfull[2], sempty[2];
+    RowsMeta meta[4];
+    float half[2][ROWS];   // what the two threads of a row tell each other
+    int item[4], wsum[NW], nan, last;
+    uint32_t taddr;
+};
+
+template <int D, int QT>
+constexpr int rows_smem()
+{
+    using C = RowsCfg<D, QT>;
+    constexpr int n = C::DATA + (int)sizeof(RowsShared<C::ROWS, C::NT / 32>);
+    static_assert(n <= 227 * 1024, "shared memory");
+    return n;
+}
+
 template <int D, int QT>
 __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_constant__ KvAttendArgs a,
                                                                     const __grid_constant__ CUtensorMap mk,
@@ -126,13 +157,22 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
     constexpr int TOK = C::TOK, NB = C::NB, NW = C::NT / 32;
     constexpr int NBLK = D / 64, NV = TOK * D / 16 / C::LOADERS;   // 64-column blocks; 16-byte vectors per loader thread
     constexpr int RPY = C::LOADERS / 4;   // rows of a tile that the loaders take at a time
-    extern __shared__ uint8_t dsm[];
-    __shared__ uint64_t bar_s[2], bar_o[2], kfull[2], kempty[2], vfull[2], vempty[2], sfull[2], sempty[2];
-    __shared__ uint32_t taddr_s;
-    __shared__ RowsMeta meta[4];
-    __shared__ int s_item[4], wsum[NW], s_nan, s_last;
-    const uint32_t base = (smem_u32(dsm) + 1023u) & ~1023u;
-    uint8_t *const gq = dsm + (base - smem_u32(dsm));
+    extern __shared__ __align__(1024) uint8_t dsm[];   // no static shared memory beside it: it starts on its alignment
+    uint8_t *const gq = dsm;
+    const uint32_t base = smem_u32(dsm);
+    if (base & 1023u) {
+        if (threadIdx.x == 0) set_status(a.c.status, ST_DEVICE_CHECK);
+        return;
+    }
+    RowsShared<C::ROWS, NW> &sh = *(RowsShared<C::ROWS, NW> *)(dsm + C::DATA);
+    auto &bar_s = sh.bar_s, &bar_o = sh.bar_o, &kfull = sh.kfull, &kempty = sh.kempty, &vfull = sh.vfull,
+         &vempty = sh.vempty, &sfull = sh.sfull, &sempty = sh.sempty;
+    auto &meta = sh.meta;
+    auto &s_half = sh.half;
+    auto &s_item = sh.item;
+    auto &wsum = sh.wsum;
+    int &s_nan = sh.nan, &s_last = sh.last;
+    uint32_t &taddr_s = sh.taddr;
     const uint32_t off_k = C::NG * QT * C::Q_BYTES, off_v = off_k + NB * C::KV_BYTES, off_st = off_v + NB * C::KV_BYTES;
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;   // warp: uniform
     const KvView &c = a.c;
@@ -202,7 +242,7 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
             mbar_init(&bar_o[x], 1);
             mbar_init(&kfull[x], C::LOADERS / 32);
             mbar_init(&vfull[x], C::LOADERS / 32);
-            mbar_init(&sfull[x], 1);
+            mbar_init(&sfull[x], x == 0 ? 2 : 1);   // keys: their bytes, and the tile's description
             mbar_init(&sempty[x], C::LOADERS / 32);
             mbar_init(&kempty[x], groups);
             mbar_init(&vempty[x], groups);
@@ -218,16 +258,17 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
         }
     };
 
-    // ---------------------------------------------------------------- queries: a row per thread
+    // ---------------------------------------------------------------- queries: two threads to a row
     float qf = 0.f;
-    const bool on = tid < rows;
-    const int grp = warp >> 2;   // of a row's thread
-    const int pos = on ? p0 + (row0 + tid) / G : -1;
-    if (tid < C::ROWS) {
-        const int64_t at = on ? ((int64_t)sq.start + (row0 + tid) / G) * a.ldq + (int64_t)(h * G + (row0 + tid) % G) * D : 0;
+    const int grp = warp >> 3, half = (warp >> 2) & 1, row = grp * 128 + (warp & 3) * 32 + lane;   // of a row's thread
+    const bool mine = tid < C::RT, on = mine && row < rows;
+    const int pos = on ? p0 + (row0 + row) / G : -1;
+    if (mine) {
+        const int64_t at =
+            on ? ((int64_t)sq.start + (row0 + row) / G) * a.ldq + (int64_t)(h * G + (row0 + row) % G) * D : 0;
         float top = 0.f;
         if (on) {
-#pragma unroll 4
+#pragma unroll 2
             for (int x = 0; x < D / 16; ++x) {
                 float f[16];
                 load16(a.q, a.dtype, at + x * 16, f);
@@ -239,8 +280,9 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
         // the sign of the scale goes into q, so that a larger product is a larger score
         const float mul = a.scale_log2 < 0.f ? -exp2i(7 - ex) : exp2i(7 - ex);
         qf = fabsf(a.scale_log2) * exp2i(ex - 7);
-#pragma unroll 2
-        for (int x = 0; x < D / 16; ++x) {
+        uint8_t *const dst = gq + (uint32_t)(grp * QT) * C::Q_BYTES;
+#pragma unroll 1
+        for (int x = half * (D / 32); x < (half + 1) * (D / 32); ++x) {
             float f[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) f[e] = 0.f;
@@ -250,10 +292,11 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
             for (int e = 0; e < 8; ++e) split_pair(f[2 * e] * mul, f[2 * e + 1] * mul, hi[e], lo[e]);
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
-                const uint32_t off = (uint32_t)(grp * QT) * C::Q_BYTES + (uint32_t)(x / 4) * 16384u + sw128_off(tid & 127, (x % 4) * 2 + hf);
-                *(uint4 *)(gq + off) = make_uint4(hi[4 * hf], hi[4 * hf + 1], hi[4 * hf + 2], hi[4 * hf + 3]);
+                const uint32_t off = (uint32_t)(x / 4) * 16384u + sw128_off(row & 127, (x % 4) * 2 + hf);
+                *(uint4 *)(dst + off) = make_uint4(hi[4 * hf], hi[4 * hf + 1], hi[4 * hf + 2], hi[4 * hf + 3]);
                 if constexpr (QT == 2)
-                    *(uint4 *)(gq + C::Q_BYTES + off) = make_uint4(lo[4 * hf], lo[4 * hf + 1], lo[4 * hf + 2], lo[4 * hf + 3]);
+                    *(uint4 *)(dst + C::Q_BYTES + off) =
+                        make_uint4(lo[4 * hf], lo[4 * hf + 1], lo[4 * hf + 2], lo[4 * hf + 3]);
             }
         }
         fence_proxy_async_smem();
@@ -263,24 +306,23 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
     tc_fence_after();
     const uint32_t tmem = taddr_s;
 
-    if (tid >= C::ROWS) {
+    if (!mine) {
         // ------------------------------------------------------------ loaders
-        const int lt = tid - C::ROWS;
+        // All four warps convert. The first also asks for codes, the second describes the tiles: page ids are
+        // loaded a step before they are looked at, scales another step before they are used.
+        const int lt = tid - C::RT, role = warp - C::RT / 32;
         const int page_shift = __ffs(P) - 1, ppt = max(1, TOK >> page_shift);   // pages per tile
-        float unit = 0.f;
-        // Page ids of tile i: lane x < ppt holds that of its x-th page, as the table has it; UNSEEN where no row sees the
-        // page. Looked at (clean) a tile later, so that nothing waits for the load.
+        const int box_rows = min(P, KV_TILE), box_shift = __ffs(box_rows) - 1, boxes = TOK >> box_shift;
+        const int pshift = __ffs(min(P, TOK)) - 1;   // of a page's positions inside a tile
         constexpr int UNSEEN = -2;
+        // Page ids of tile i: lane x < ppt gets that of its x-th page as the table has it, UNSEEN where no row sees it.
         auto pages = [&](int i) {
-            const int j0 = tile_of(i) + (lane << page_shift), end = j0 + min(P, TOK);
-            const bool seen = lane < ppt && j0 <= pos_hi &&
-                              (j0 < a.sinks || pos_lo - (end - 1) < a.window);
+            const int j0 = tile_of(i) + (lane << page_shift), last = j0 + min(P, TOK) - 1;
+            const bool seen = i < nt && lane < ppt && j0 <= pos_hi && (j0 < a.sinks || pos_lo - last < a.window);
             return seen ? c.table[(size_t)sq.row * c.max_pages + (j0 >> page_shift)] : UNSEEN;
         };
         auto clean = [&](int pid) { return (unsigned)pid < (unsigned)c.n_pages ? pid : -1; };
-        // Codes of tile i (kv 0: keys, 1: values) into their stage, by the first loader warp. Absent pages are left out.
-        const int box_rows = min(P, KV_TILE), box_shift = __ffs(box_rows) - 1, boxes = TOK >> box_shift;
-        const int pshift = __ffs(min(P, TOK)) - 1;   // of a page's positions inside a tile
+        // Codes of tile i (kv 0: keys, 1: values) into their stage. Absent pages are left out.
         auto request = [&](int kv, int i, int pid) {
             const int page = __shfl_sync(0xffffffffu, pid, lane < boxes ? (lane << box_shift) >> pshift : 0);
             const bool go = lane < boxes && page >= 0;
@@ -289,80 +331,21 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
             if (lane == 0) mbar_arrive_expect_tx(&sfull[kv], n * box_rows * D);
             __syncwarp();
             if (go) {
-                const int row = (page * c.hkv + h) * P + ((tile_of(i) + lane * box_rows) & (P - 1));
-                uint8_t *dst = gq + off_st + kv * C::STAGE + lane * box_rows * (D < 128 ? D : 128);
+                const int at = (page * c.hkv + h) * P + ((tile_of(i) + (lane << box_shift)) & (P - 1));
+                uint8_t *dst = gq + off_st + kv * C::STAGE + (lane << box_shift) * (D < 128 ? D : 128);
 #pragma unroll
-                for (int x0 = 0; x0 < D; x0 += 128) tma_load_2d(dst + x0 * TOK, kv ? &mv : &mk, x0, row, &sfull[kv]);
+                for (int x0 = 0; x0 < D; x0 += 128) tma_load_2d(dst + x0 * TOK, kv ? &mv : &mk, x0, at, &sfull[kv]);
             }
             __syncwarp();
-        };
-        // This thread's vectors of a tile: rows RPY y + tr, 64-column blocks b. Eight lanes hold four chunks of two
-        // rows, odd rows a block off, so that reads of the stage and writes of the operand hit every bank once.
-        const int tr = lt / 4, ch = lt % 4, odd = NBLK > 1 ? tr & 1 : 0;
-        auto fetch = [&](int kv, int i, int pid, uint4 (&r)[NV]) {
-            wait(&sfull[kv], i & 1);
-            const uint8_t *st = gq + off_st + kv * C::STAGE;
-#pragma unroll
-            for (int y = 0; y < TOK / RPY; ++y)
-#pragma unroll
-                for (int b = 0; b < NBLK; ++b) {
-                    const int tok = y * RPY + tr, bb = b ^ odd;
-                    const int off = D == 64 ? tok * 64 + ((ch ^ ((tr >> 1) & 3)) << 4)
-                                            : (bb >> 1) * TOK * 128 + tok * 128 + ((((bb & 1) * 4 + ch) ^ (tr & 7)) << 4);
-                    r[y * NBLK + b] = *(const uint4 *)(st + off);
-                }
-            const int j0 = tile_of(i);
-            const uint32_t there = __ballot_sync(0xffffffffu, pid >= 0);
-            if (!is_whole(j0) || there != (1u << ppt) - 1u) {   // positions that no row sees, absent pages: zeros
-#pragma unroll
-                for (int y = 0; y < TOK / RPY; ++y) {
-                    const int tok = y * RPY + tr, j = j0 + tok;
-                    const bool live = ((there >> (tok >> pshift)) & 1u) && j <= pos_hi &&
-                                      (j < a.sinks || pos_lo - j < a.window);
-#pragma unroll
-                    for (int b = 0; b < NBLK; ++b)
-                        if (!live) r[y * NBLK + b] = make_uint4(0, 0, 0, 0);
-                }
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sempty[kv]);
-        };
-        auto convert = [&](uint32_t at, const uint4 (&r)[NV]) {
-            const uint32_t o_lo = sw128_off(tr, ch * 2), o_hi = sw128_off(tr, ch * 2 + 1);
-#pragma unroll
-            for (int y = 0; y < TOK / RPY; ++y)
-#pragma unroll
-                for (int b = 0; b < NBLK; ++b) {
-                    const uint4 v = r[y * NBLK + b];
-                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-                    uint32_t f[8];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) e4m3x4_f16x4(w[e], f[2 * e], f[2 * e + 1]);
-                    uint8_t *dst = gq + at + (b ^ odd) * (TOK * 128) + y * RPY * 128;
-                    *(uint4 *)(dst + o_lo) = make_uint4(f[0], f[1], f[2], f[3]);
-                    *(uint4 *)(dst + o_hi) = make_uint4(f[4], f[5], f[6], f[7]);
-                }
-        };
-        // A NaN value in a tile that not every row sees in full: 0 here, and the rows that see it learn of it at the end.
-        auto strip_nan = [&](int i, uint4 (&r)[NV]) {
-            if (is_whole(tile_of(i))) return;
-#pragma unroll
-            for (int x = 0; x < NV; ++x) {
-                uint32_t *w = &r[x].x;
-                for (int e = 0; e < 4; ++e)
-                    if (e4m3_any_nan(w[e])) {
-                        for (int b = 0; b < 32; b += 8)
-                            if (((w[e] >> b) & 0x7fu) == 0x7fu) w[e] &= ~(0xffu << b);
-                        s_nan = 1;
-                    }
-            }
         };
         // Scales of a tile's pages, one run of 16 positions to a lane, and what the softmax makes of them.
         auto scales = [&](int pid, float &ks, float &vs) {
             const int page = __shfl_sync(0xffffffffu, pid, lane < TOK / 16 ? (lane * 16) >> pshift : 0);
-            ks = page >= 0 ? a.l.ks[(size_t)page * c.hkv + h] : 0.f;
-            vs = page >= 0 ? a.l.vs[(size_t)page * c.hkv + h] : 0.f;
+            const bool run = lane < TOK / 16 && page >= 0;
+            ks = run ? a.l.ks[(size_t)page * c.hkv + h] : 0.f;
+            vs = run ? a.l.vs[(size_t)page * c.hkv + h] : 0.f;
         };
+        float unit = 0.f;
         auto describe = [&](int i, int pid, float ks, float vs) {
             RowsMeta &m = meta[i & 3];
             float top = vs;
@@ -381,50 +364,107 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
                 constexpr uint32_t all = (1u << (TOK / 16)) - 1u;
                 m.unit = top;
                 m.shrink = top > unit ? unit / top : 1.f;
-                m.valid = there;
+                m.valid = there & all;
                 m.whole = is_whole(tile_of(i)) && (there & all) == all;
             }
             unit = top;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sfull[0]);
         };
-        auto ready = [&](uint64_t *bar) {
+        // This thread's vectors of a tile: rows RPY y + tr, 64-column blocks b. Eight lanes hold four chunks of two
+        // rows, odd rows a block off, so that reads of the stage and writes of the operand hit every bank once.
+        const int tr = lt / 4, ch = lt % 4, odd = NBLK > 1 ? tr & 1 : 0;
+        auto fetch = [&](int kv, int i, uint4 (&r)[NV]) {
+            wait(&sfull[kv], i & 1);
+            const uint8_t *st = gq + off_st + kv * C::STAGE;
+#pragma unroll
+            for (int y = 0; y < TOK / RPY; ++y)
+#pragma unroll
+                for (int b = 0; b < NBLK; ++b) {
+                    const int bb = b ^ odd;
+                    const int off = D == 64 ? tr * 64 + ((ch ^ ((tr >> 1) & 3)) << 4)
+                                            : (bb >> 1) * TOK * 128 + tr * 128 + ((((bb & 1) * 4 + ch) ^ (tr & 7)) << 4);
+                    r[y * NBLK + b] = *(const uint4 *)(st + off + y * RPY * (D < 128 ? D : 128));
+                }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sempty[kv]);
+            if (meta[i & 3].whole) return;
+            // positions that no row sees and absent pages: zeros. A NaN among values that not every row sees: 0 too,
+            // and the rows that see it learn of it at the end.
+            const uint32_t there = meta[i & 3].valid;
+            const int j0 = tile_of(i);
+            const bool part = !is_whole(j0);
+#pragma unroll
+            for (int y = 0; y < TOK / RPY; ++y) {
+                const int tok = y * RPY + tr, j = j0 + tok;
+                const bool live =
+                    ((there >> (tok >> 4)) & 1u) && j <= pos_hi && (j < a.sinks || pos_lo - j < a.window);
+#pragma unroll
+                for (int b = 0; b < NBLK; ++b) {
+                    uint4 &v = r[y * NBLK + b];
+                    if (!live) v = make_uint4(0, 0, 0, 0);
+                    else if (kv && part && (e4m3_any_nan(v.x) | e4m3_any_nan(v.y) | e4m3_any_nan(v.z) | e4m3_any_nan(v.w))) {
+                        v = make_uint4(e4m3_no_nan(v.x), e4m3_no_nan(v.y), e4m3_no_nan(v.z), e4m3_no_nan(v.w));
+                        s_nan = 1;
+                    }
+                }
+            }
+        };
+        const uint32_t o_lo = sw128_off(tr, ch * 2), o_hi = sw128_off(tr, ch * 2 + 1);
+        auto convert = [&](uint32_t at, const uint4 (&r)[NV], uint64_t *full) {
+#pragma unroll
+            for (int b = 0; b < NBLK; ++b) {
+                uint8_t *const lo = gq + at + (b ^ odd) * (TOK * 128) + o_lo, *const hi = lo + (int)(o_hi - o_lo);
+#pragma unroll
+                for (int y = 0; y < TOK / RPY; ++y) {
+                    const uint4 v = r[y * NBLK + b];
+                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                    uint32_t f[8];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) e4m3x4_f16x4(w[e], f[2 * e], f[2 * e + 1]);
+                    *(uint4 *)(lo + y * RPY * 128) = make_uint4(f[0], f[1], f[2], f[3]);
+                    *(uint4 *)(hi + y * RPY * 128) = make_uint4(f[4], f[5], f[6], f[7]);
+                }
+            }
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar);
+            if (lane == 0) mbar_arrive(full);
         };
-        // Codes and scales are asked for a tile ahead, page ids two. The first warp asks for keys, the third for
-        // values, the second describes the tile.
-        const int role = warp - C::ROWS / 32;
         uint4 r[NV];
-        int pid0 = -1, raw1 = nt > 0 ? pages(0) : UNSEEN;
-        float ks0 = 0.f, vs0 = 0.f, ks1 = 0.f, vs1 = 0.f;
+        int pid1 = -1, raw2 = UNSEEN;   // pages of tiles i + 1 (clean) and i + 2
+        float ks1 = 0.f, vs1 = 0.f;
 #pragma unroll 1
-        for (int i = -1; i < nt; ++i) {
-            const int raw2 = i + 2 < nt ? pages(i + 2) : UNSEEN, pid1 = clean(raw1), b = i & (NB - 1);
-            const bool more = i + 1 < nt;
-            if (role == 1) {
-                if (pid1 < 0 && raw1 != UNSEEN) set_status(c.status, ST_DEVICE_CHECK);   // seen, but absent
-                if (more) scales(pid1, ks1, vs1);
+        for (int i = -3; i < nt; ++i) {
+            int pid2 = -1, raw3 = UNSEEN;
+            float ks2 = 0.f, vs2 = 0.f;
+            if (role < 2) {
+                pid2 = clean(raw2);
+                if (role == 1) {
+                    if (pid2 < 0 && raw2 != UNSEEN) set_status(c.status, ST_DEVICE_CHECK);   // seen, but absent
+                    scales(pid2, ks2, vs2);
+                }
+                raw3 = pages(i + 3);
             }
-            if (i >= 0) fetch(0, i, pid0, r);
-            if (role == 0 && more) request(0, i + 1, pid1);
+            const bool next = i >= -1 && i + 1 < nt;
+            const int b = i & (NB - 1);
+            if (i >= 0) fetch(0, i, r);
+            // (arrivals for the next tile's keys: only after this tile's phase, which fetch has waited for)
+            if (role == 0 && next) request(0, i + 1, pid1);
+            if (role == 1 && next) describe(i + 1, pid1, ks1, vs1);
             if (i >= 0) {
-                if (i >= NB) wait(&kempty[b], (i / NB - 1) & 1);
-                if (role == 1) describe(i, pid0, ks0, vs0);
-                convert(off_k + b * C::KV_BYTES, r);
-                ready(&kfull[b]);
-                fetch(1, i, pid0, r);
+                if (i >= NB) wait(&kempty[b], (i / NB - 1) & 1);   // the product that read the tile's place before
+                convert(off_k + b * C::KV_BYTES, r, &kfull[b]);
+                fetch(1, i, r);
             }
-            if (role == 2 && more) request(1, i + 1, pid1);
+            if (role == 0 && next) request(1, i + 1, pid1);
             if (i >= 0) {
-                strip_nan(i, r);
                 if (i >= NB) wait(&vempty[b], (i / NB - 1) & 1);
-                convert(off_v + b * C::KV_BYTES, r);
-                ready(&vfull[b]);
+                convert(off_v + b * C::KV_BYTES, r, &vfull[b]);
             }
-            pid0 = pid1;
-            raw1 = raw2;
-            ks0 = ks1;
-            vs0 = vs1;
+            pid1 = pid2;
+            raw2 = raw3;
+            ks1 = ks2;
+            vs1 = vs2;
         }
     }
 
@@ -432,7 +472,7 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
     float m = -INFINITY, l = 0.f, unit = 0.f;
     const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t ts = tmem + grp * (TOK + D), to = ts + TOK;
-    if (grp < groups && tid < C::ROWS) {
+    if (mine && grp < groups) {
         constexpr uint32_t ID_S = f16_idesc(0, 0, 0, 128, TOK), ID_O = f16_idesc(0, 0, 1, 128, D);
         // One thread of the group's first warp issues its products. Descriptors differ in their address only (bits 0-13,
         // in 16 bytes), and everything here is uniform over the warp, so that each product is one instruction and an add.
@@ -467,112 +507,91 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
             umma_commit(&vempty[b]);
             if (i + 1 == nt) umma_commit(&bar_o[grp]);
         };
-        const bool issues = (warp & 3) == 0;
+        const bool issues = (warp & 7) == 0;
         if (nt > 0 && issues && elect_one()) issue_s(0);
         __syncwarp();
+        constexpr int HC = TOK / 2;   // positions of the tile that this thread takes
+        const uint32_t my_s = ts + lane_base + half * HC, my_p = ts + lane_base + half * (HC / 2);
         for (int i = 0; i < nt; ++i) {
             wait(&bar_s[grp], i & 1);
             tc_fence_after();
             const RowsMeta &mt = meta[i & 3];
-            const int j0 = tile_of(i);
-            // From product to base-2 score, by runs of 16. Never 0, so that -infinity stays what it is.
-            float factor[TOK / 16];
+            uint32_t r[HC];
 #pragma unroll
-            for (int x = 0; x < TOK / 16; ++x) factor[x] = fmaxf(qf * mt.ks[x], 1e-37f);
-            // scores to factors of the row's largest; what a row does not see becomes -infinity in place
-            float top = -INFINITY;
-            auto take = [&](const uint32_t *r, float f) {   // 16 positions
-                float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            for (int x = 0; x < HC; x += 32) tmem_ld32(my_s + x, r + x);
+            tmem_wait_ld(r);
+            if (!mt.whole) {   // what the row does not see: -infinity
+                const int j0 = tile_of(i) + half * HC;
 #pragma unroll
-                for (int e = 0; e < 16; ++e) t[e & 3] = fmaxf(t[e & 3], __uint_as_float(r[e]));
-                const float t4 = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
-                top = fmaxf(top, t4 * f);
-            };
-            if (mt.whole) {
-#pragma unroll
-                for (int ch = 0; ch < TOK; ch += 64) {
-                    uint32_t r[64];
-                    tmem_ld32(ts + lane_base + ch, r);
-                    tmem_ld32(ts + lane_base + ch + 32, r + 32);
-                    tmem_wait_ld(r);
-#pragma unroll
-                    for (int g16 = 0; g16 < 64; g16 += 16) take(r + g16, factor[(ch + g16) / 16]);
-                }
-            } else {
-#pragma unroll 1
-                for (int ch = 0; ch < TOK; ch += 32) {
-                    uint32_t r[32];
-                    tmem_ld32(ts + lane_base + ch, r);
-                    const int j = j0 + ch;
+                for (int x = 0; x < HC; x += 32) {
+                    const int j = j0 + x;
                     uint32_t see = low_bits(pos - j + 1);
                     see &= ~low_bits(pos - a.window + 1 - j) | low_bits(a.sinks - j);
-                    const uint32_t there = mt.valid >> (ch / 16);
+                    const uint32_t there = mt.valid >> ((half * HC + x) / 16);
                     see &= (there & 1u ? 0xffffu : 0u) | (there & 2u ? 0xffff0000u : 0u);
-                    tmem_wait_ld(r);
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) r[e] = (see >> e) & 1u ? r[e] : 0xff800000u;
-                    take(r, fmaxf(qf * mt.ks[ch / 16], 1e-37f));
-                    take(r + 16, fmaxf(qf * mt.ks[ch / 16 + 1], 1e-37f));
-                    tmem_st16(ts + lane_base + ch, r);
-                    tmem_st16(ts + lane_base + ch + 16, r + 16);
+                    for (int e = 0; e < 32; ++e) r[x + e] = (see >> e) & 1u ? r[x + e] : 0xff800000u;
                 }
-                tmem_wait_st();
             }
+            // From product to base-2 score, by runs of 16. Never 0, so that -infinity stays what it is.
+            float factor[HC / 16], top = -INFINITY;
+#pragma unroll
+            for (int x = 0; x < HC / 16; ++x) {
+                factor[x] = fmaxf(qf * mt.ks[half * (HC / 16) + x], 1e-37f);
+                float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int e = 0; e < 16; ++e) t[e & 3] = fmaxf(t[e & 3], __uint_as_float(r[x * 16 + e]));
+                top = fmaxf(top, fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * factor[x]);
+            }
+            s_half[half][row] = top;
+            bar_sync(2 + grp, 256);   // also: every score of the group's tile has been read
+            top = fmaxf(top, s_half[half ^ 1][row]);
             // the reference is raised when the maximum has outrun it; O follows it and the unit of the values
-            float shrink = 1.f;
+            float shrink = mt.shrink;
             if (top > m + ROWS_TRAIL || (m == -INFINITY && top > m)) {
-                shrink = ex2(m - top);
+                const float down = ex2(m - top);
+                shrink *= down;
+                l *= down;
                 m = top;
-                l *= shrink;
             }
-            shrink *= mt.shrink;
             unit = mt.unit;
             if (i > 0 && __any_sync(0xffffffffu, shrink != 1.f)) {
 #pragma unroll 1
-                for (int ch = 0; ch < D / 32; ++ch) {
-                    uint32_t r[32];
-                    tmem_ld32(to + lane_base + ch * 32, r);
-                    tmem_wait_ld(r);
+                for (int x = half * (D / 2); x < (half + 1) * (D / 2); x += 16) {
+                    uint32_t o[16];
+                    tmem_ld16u(to + lane_base + x, o);
+                    tmem_wait_ld(o);
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * shrink);
-                    tmem_st16(to + lane_base + ch * 32, r);
-                    tmem_st16(to + lane_base + ch * 32 + 16, r + 16);
+                    for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * shrink);
+                    tmem_st16(to + lane_base + x, o);
                 }
             }
             const float ref = m == -INFINITY ? 0.f : m;
+            uint32_t plo[QT == 2 ? HC / 2 : 1];
 #pragma unroll
-            for (int ch = 0; ch < TOK; ch += 64) {
-                uint32_t r[64], plo[QT == 2 ? 32 : 1];
-                tmem_ld32(ts + lane_base + ch, r);
-                tmem_ld32(ts + lane_base + ch + 32, r + 32);
-                tmem_wait_ld(r);
+            for (int x = 0; x < HC / 16; ++x) {
+                const float f = factor[x], off = mt.vexp[half * (HC / 16) + x] - ref;
+                float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-                for (int g16 = 0; g16 < 64; g16 += 16) {
-                    const float f = factor[(ch + g16) / 16], off = mt.vexp[(ch + g16) / 16] - ref;
-                    float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
-                    for (int e = g16; e < g16 + 16; e += 2) {
-                        float2 x = ffma2(make_float2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])),
-                                         make_float2(f, f), make_float2(off, off));
-                        x.x = ex2(x.x);
-                        x.y = ex2(x.y);
-                        sum = fadd2(sum, x);
-                        if constexpr (QT == 2) split_pair(x.x, x.y, r[e / 2], plo[e / 2]);
-                        else r[e / 2] = pack_f16(x.x, x.y);
-                    }
-                    l = fmaf(sum.x + sum.y, mt.vback[(ch + g16) / 16], l);
+                for (int e = x * 16; e < x * 16 + 16; e += 2) {
+                    float2 w = ffma2(make_float2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), make_float2(f, f),
+                                     make_float2(off, off));
+                    w.x = ex2(w.x);
+                    w.y = ex2(w.y);
+                    sum = fadd2(sum, w);
+                    if constexpr (QT == 2) split_pair(w.x, w.y, r[e / 2], plo[e / 2]);
+                    else r[e / 2] = pack_f16(w.x, w.y);
                 }
-                // the weights take the place of scores already read, their second terms (TOK 64) that of the rest
-                tmem_st16(ts + lane_base + ch / 2, r);
-                tmem_st16(ts + lane_base + ch / 2 + 16, r + 16);
-                if constexpr (QT == 2) {
-                    tmem_st16(ts + lane_base + 32, plo);
-                    tmem_st16(ts + lane_base + 48, plo + 16);
+                l = fmaf(sum.x + sum.y, mt.vback[half * (HC / 16) + x], l);
+                // The weights take the place of the scores: first terms in columns [0, TOK / 2), second ones behind.
+                if (x & 1) {
+                    tmem_st16(my_p + (x / 2) * 16, r + (x / 2) * 16);
+                    if constexpr (QT == 2) tmem_st16(my_p + TOK / 2 + (x / 2) * 16, plo + (x / 2) * 16);
                 }
             }
             tmem_wait_st();
             tc_fence_before();
-            bar_sync(2 + grp, 128);
+            bar_sync(2 + grp, 256);
             if (issues && elect_one()) {
                 tc_fence_after();
                 issue_o(i);
@@ -584,30 +603,33 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
         tc_fence_after();
 
         // ------------------------------------------------------------ output
+        s_half[half][row] = l;
+        bar_sync(2 + grp, 256);
+        l += s_half[half ^ 1][row];
         const float back = unit * exp2i(-(int)ROWS_UNIT);
-        const int64_t unit_id = (int64_t)blockIdx.x * splits + blockIdx.y;
+        const int64_t at = ((int64_t)blockIdx.x * splits + blockIdx.y) * C::ROWS + row;
         const int4 f4 = make_int4(sq.row, sq.len, sq.start, sq.n);
 #pragma unroll 1
-        for (int ch = 0; ch < D / 32; ++ch) {
-            uint32_t r[32];
+        for (int x = half * (D / 2); x < (half + 1) * (D / 2); x += 16) {
+            uint32_t o[16];
             if (nt > 0) {
-                tmem_ld32(to + lane_base + ch * 32, r);
-                tmem_wait_ld(r);
+                tmem_ld16u(to + lane_base + x, o);
+                tmem_wait_ld(o);
             }
             if (!on) continue;
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-                float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int e = 0; e < 16; e += 4) {
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (nt > 0)
-                    o = make_float4(__uint_as_float(r[e]) * back, __uint_as_float(r[e + 1]) * back,
-                                    __uint_as_float(r[e + 2]) * back, __uint_as_float(r[e + 3]) * back);
-                if (splits > 1) *(float4 *)&a.rows_part[(unit_id * C::ROWS + tid) * D + ch * 32 + e] = o;
-                else store_row(a, f4, h, G, D, row0 + tid, ch * 32 + e, o, m, l);
+                    v = make_float4(__uint_as_float(o[e]) * back, __uint_as_float(o[e + 1]) * back,
+                                    __uint_as_float(o[e + 2]) * back, __uint_as_float(o[e + 3]) * back);
+                if (splits > 1) *(float4 *)&a.rows_part[at * D + x + e] = v;
+                else store_row(a, f4, h, G, D, row0 + row, x + e, v, m, l);
             }
         }
-        if (splits > 1 && on) {
-            a.rows_ml[(unit_id * C::ROWS + tid) * 2] = m;
-            a.rows_ml[(unit_id * C::ROWS + tid) * 2 + 1] = l;
+        if (splits > 1 && on && half == 0) {
+            a.rows_ml[at * 2] = m;
+            a.rows_ml[at * 2 + 1] = l;
         }
     }
     tc_fence_before();
@@ -647,7 +669,7 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
     // NaN values among positions that not every row sees: they were left out above; here each row that
     // sees one gets it (rare, so straight from the pool).
     __syncthreads();
-    if (!on) return;
+    if (!on || half) return;
     for (int x = 0; x < nt_all; ++x) {
         const int j0 = (x < ns ? x : w0 + x - ns) * TOK;
         if (is_whole(j0)) continue;
@@ -659,7 +681,7 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
             for (int w = 0; w < D / 4; ++w)
                 if (e4m3_any_nan(v[w]))
                     for (int b = 0; b < 4; ++b)
-                        if (((v[w] >> (8 * b)) & 0x7fu) == 0x7fu) store_nan(a, f4, h, G, D, row0 + tid, 4 * w + b);
+                        if (((v[w] >> (8 * b)) & 0x7fu) == 0x7fu) store_nan(a, f4, h, G, D, row0 + row, 4 * w + b);
         }
     }
 }
@@ -667,7 +689,7 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
 template <int D, int QT>
 cudaError_t rows_setup()
 {
-    return cudaFuncSetAttribute(k_kv_rows<D, QT>, cudaFuncAttributeMaxDynamicSharedMemorySize, RowsCfg<D, QT>::SMEM);
+    return cudaFuncSetAttribute(k_kv_rows<D, QT>, cudaFuncAttributeMaxDynamicSharedMemorySize, rows_smem<D, QT>());
 }
 
 template <int D, int QT>
@@ -677,7 +699,7 @@ cudaError_t rows_launch(const KvAttendArgs &a, const CUtensorMap &mk, const CUte
     Launch L;
     L.grid = dim3(items, splits);
     L.block = dim3(RowsCfg<D, QT>::NT);
-    L.smem = RowsCfg<D, QT>::SMEM;
+    L.smem = rows_smem<D, QT>();
     L.stream = s;
     L.pdl = true;
     L.nsm = 0;
