@@ -213,6 +213,47 @@ __device__ __forceinline__ void poison(float (&acc)[N][4], int j, int e)
 
 // ---------------------------------------------------------------- output --------------------
 
+template <int N>
+__device__ __forceinline__ void store_f32(float *p, const float (&f)[N])
+{
+#pragma unroll
+    for (int e = 0; e < N; e += 4) *(float4 *)(p + e) = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
+}
+
+// N consecutive outputs (a multiple of 4; 8-byte aligned for 16-bit types) at element `at`.
+template <int N>
+__device__ __forceinline__ void store_out(const KvAttendArgs &a, int64_t at, const float (&f)[N])
+{
+    if (a.dtype == DT_F32) {
+        store_f32((float *)a.out + at, f);
+        return;
+    }
+    uint32_t w[N / 2];
+#pragma unroll
+    for (int e = 0; e < N / 2; ++e) {
+        if (a.dtype == DT_BF16) {
+            const __nv_bfloat162 x = __floats2bfloat162_rn(f[2 * e], f[2 * e + 1]);
+            w[e] = *(const uint32_t *)&x;
+        } else {
+            w[e] = pack_f16(f[2 * e], f[2 * e + 1]);
+        }
+    }
+    uint16_t *p = (uint16_t *)a.out + at;
+    if constexpr (N % 8 == 0) {
+#pragma unroll
+        for (int e = 0; e < N / 2; e += 4) *(uint4 *)(p + 2 * e) = make_uint4(w[e], w[e + 1], w[e + 2], w[e + 3]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < N / 2; e += 2) *(uint2 *)(p + 2 * e) = make_uint2(w[e], w[e + 1]);
+    }
+}
+
+// log of a row's sum of exponentials: maximum (or reference) M in base 2, sum S relative to it
+__device__ __forceinline__ float row_lse(float M, float S)
+{
+    return S == 0.f ? -INFINITY : (M + log2f(S)) * 0.6931471805599453f;
+}
+
 // Four columns (from d) of row `r` (query token r / G, head r % G of kv head h) of the sequence f (table row,
 // length, start, new tokens): numerators o over the sum S, and with d = 0 the row's log of the sum.
 __device__ __forceinline__ void store_row(const KvAttendArgs &a, const int4 &f, int h, int G, int D, int r, int d,
@@ -220,24 +261,12 @@ __device__ __forceinline__ void store_row(const KvAttendArgs &a, const int4 &f, 
 {
     const int64_t tok = (int64_t)f.z + r / G;
     const int head = h * G + r % G;
+    const float inv = 1.f / S;
     // S = 0: nothing seen. (A NaN sum stays: it is not equal to 0.)
-    const float inv = S == 0.f ? 0.f : 1.f / S;
-    o.x *= inv, o.y *= inv, o.z *= inv, o.w *= inv;
-    if (S == 0.f) o = make_float4(0.f, 0.f, 0.f, 0.f);
-    const int64_t at = tok * a.ldo + (int64_t)head * D + d;
-    if (a.dtype == DT_F32) {
-        *(float4 *)((float *)a.out + at) = o;
-    } else {
-        uint2 v;
-        if (a.dtype == DT_BF16) {
-            const __nv_bfloat162 x = __floats2bfloat162_rn(o.x, o.y), y = __floats2bfloat162_rn(o.z, o.w);
-            v = make_uint2(*(const uint32_t *)&x, *(const uint32_t *)&y);
-        } else {
-            v = make_uint2(pack_f16(o.x, o.y), pack_f16(o.z, o.w));
-        }
-        *(uint2 *)((uint16_t *)a.out + at) = v;
-    }
-    if (a.lse && d == 0) a.lse[tok * a.c.hq + head] = S == 0.f ? -INFINITY : (M + log2f(S)) * 0.6931471805599453f;
+    const float v[4] = {S == 0.f ? 0.f : o.x * inv, S == 0.f ? 0.f : o.y * inv, S == 0.f ? 0.f : o.z * inv,
+                        S == 0.f ? 0.f : o.w * inv};
+    store_out<4>(a, tok * a.ldo + (int64_t)head * D + d, v);
+    if (a.lse && d == 0) a.lse[tok * a.c.hq + head] = row_lse(M, S);
 }
 
 __device__ __forceinline__ void store_nan(const KvAttendArgs &a, const int4 &f, int h, int G, int D, int r, int d)

@@ -136,6 +136,7 @@ struct RowsShared {
     RowsMeta meta[4];
     float half[2][ROWS];   // what the two threads of a row tell each other
     int item[4], wsum[NW], nan, last;
+    KvSeq seq;
     uint32_t taddr;
 };
 
@@ -216,12 +217,13 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
                 s_item[0] = i;
                 s_item[1] = rts - 1 - local / c.hkv;
                 s_item[2] = local % c.hkv;
+                sh.seq = kv_sequence(c, a.b, i, false);
             }
             __syncthreads();
         }
     }
     if (s_item[0] < 0) return;
-    const KvSeq sq = kv_sequence(c, a.b, s_item[0], false);
+    const KvSeq sq = sh.seq;
     const int h = s_item[2], row0 = s_item[1] * C::ROWS, rows = min(C::ROWS, sq.n * G - row0), p0 = sq.len - sq.n;
     const int pos_lo = p0 + row0 / G, pos_hi = p0 + (row0 + rows - 1) / G;
     // tiles [0, ns) and [w0, w1) hold what the rows see; this CTA takes its split's share of them
@@ -258,49 +260,9 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
         }
     };
 
-    // ---------------------------------------------------------------- queries: two threads to a row
-    float qf = 0.f;
     const int grp = warp >> 3, half = (warp >> 2) & 1, row = grp * 128 + (warp & 3) * 32 + lane;   // of a row's thread
     const bool mine = tid < C::RT, on = mine && row < rows;
     const int pos = on ? p0 + (row0 + row) / G : -1;
-    if (mine) {
-        const int64_t at =
-            on ? ((int64_t)sq.start + (row0 + row) / G) * a.ldq + (int64_t)(h * G + (row0 + row) % G) * D : 0;
-        float top = 0.f;
-        if (on) {
-#pragma unroll 2
-            for (int x = 0; x < D / 16; ++x) {
-                float f[16];
-                load16(a.q, a.dtype, at + x * 16, f);
-#pragma unroll
-                for (int e = 0; e < 16; ++e) top = fmaxf(top, finite_abs(f[e]));
-            }
-        }
-        const int ex = top > 0.f ? min(max(ilogbf(top), -118), 127) : 0;
-        // the sign of the scale goes into q, so that a larger product is a larger score
-        const float mul = a.scale_log2 < 0.f ? -exp2i(7 - ex) : exp2i(7 - ex);
-        qf = fabsf(a.scale_log2) * exp2i(ex - 7);
-        uint8_t *const dst = gq + (uint32_t)(grp * QT) * C::Q_BYTES;
-#pragma unroll 1
-        for (int x = half * (D / 32); x < (half + 1) * (D / 32); ++x) {
-            float f[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) f[e] = 0.f;
-            if (on) load16(a.q, a.dtype, at + x * 16, f);
-            uint32_t hi[8], lo[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) split_pair(f[2 * e] * mul, f[2 * e + 1] * mul, hi[e], lo[e]);
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                const uint32_t off = (uint32_t)(x / 4) * 16384u + sw128_off(row & 127, (x % 4) * 2 + hf);
-                *(uint4 *)(dst + off) = make_uint4(hi[4 * hf], hi[4 * hf + 1], hi[4 * hf + 2], hi[4 * hf + 3]);
-                if constexpr (QT == 2)
-                    *(uint4 *)(dst + C::Q_BYTES + off) =
-                        make_uint4(lo[4 * hf], lo[4 * hf + 1], lo[4 * hf + 2], lo[4 * hf + 3]);
-            }
-        }
-        fence_proxy_async_smem();
-    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -473,6 +435,60 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
     const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t ts = tmem + grp * (TOK + D), to = ts + TOK;
     if (mine && grp < groups) {
+        // ------------------------------------------------------------ queries: half a row to a thread
+        float qf;
+        {
+            constexpr int QV = QT == 2 ? D / 8 : D / 16;   // 16-byte vectors (QT 2: fp32)
+            uint4 raw[QV];
+            const int64_t at = ((int64_t)sq.start + (row0 + row) / G) * a.ldq + (int64_t)(h * G + (row0 + row) % G) * D +
+                               half * (D / 2);
+            const uint4 *from = (const uint4 *)((const uint8_t *)a.q + at * (QT == 2 ? 4 : 2));
+#pragma unroll
+            for (int x = 0; x < QV; ++x) raw[x] = on ? from[x] : make_uint4(0, 0, 0, 0);
+            auto eight = [&](int x, float (&f)[8]) {   // elements 8 x ... of the half
+                if constexpr (QT == 2) {
+                    float u[4], v[4];
+                    unpack<DT_F32>(raw[2 * x], u);
+                    unpack<DT_F32>(raw[2 * x + 1], v);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) f[e] = u[e], f[4 + e] = v[e];
+                } else if (a.dtype == DT_BF16) {
+                    unpack<DT_BF16>(raw[x], f);
+                } else {
+                    unpack<DT_F16>(raw[x], f);
+                }
+            };
+            float top = 0.f;
+#pragma unroll
+            for (int x = 0; x < D / 16; ++x) {
+                float f[8];
+                eight(x, f);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) top = fmaxf(top, finite_abs(f[e]));
+            }
+            s_half[half][row] = top;
+            bar_sync(2 + grp, 256);
+            top = fmaxf(top, s_half[half ^ 1][row]);
+            const int ex = top > 0.f ? min(max(ilogbf(top), -118), 127) : 0;
+            // the sign of the scale goes into q, so that a larger product is a larger score
+            const float mul = a.scale_log2 < 0.f ? -exp2i(7 - ex) : exp2i(7 - ex);
+            qf = fabsf(a.scale_log2) * exp2i(ex - 7);
+            uint8_t *const dst = gq + (uint32_t)(grp * QT) * C::Q_BYTES;
+#pragma unroll
+            for (int x = 0; x < D / 16; ++x) {
+                float f[8];
+                uint32_t hi[4], lo[4];
+                eight(x, f);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) split_pair(f[2 * e] * mul, f[2 * e + 1] * mul, hi[e], lo[e]);
+                const int ch = half * (D / 16) + x;
+                const uint32_t off = (uint32_t)(ch / 8) * 16384u + sw128_off(row & 127, ch % 8);
+                *(uint4 *)(dst + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                if constexpr (QT == 2) *(uint4 *)(dst + C::Q_BYTES + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            }
+            fence_proxy_async_smem();
+            bar_sync(2 + grp, 256);
+        }
         constexpr uint32_t ID_S = f16_idesc(0, 0, 0, 128, TOK), ID_O = f16_idesc(0, 0, 1, 128, D);
         // One thread of the group's first warp issues its products. Descriptors differ in their address only (bits 0-13,
         // in 16 bytes), and everything here is uniform over the warp, so that each product is one instruction and an add.
@@ -606,27 +622,25 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
         s_half[half][row] = l;
         bar_sync(2 + grp, 256);
         l += s_half[half ^ 1][row];
-        const float back = unit * exp2i(-(int)ROWS_UNIT);
+        const float back = unit * exp2i(-(int)ROWS_UNIT), norm = splits > 1 ? back : l == 0.f ? 0.f : back / l;
         const int64_t at = ((int64_t)blockIdx.x * splits + blockIdx.y) * C::ROWS + row;
-        const int4 f4 = make_int4(sq.row, sq.len, sq.start, sq.n);
+        const int64_t at_out = ((int64_t)sq.start + (row0 + row) / G) * a.ldo + (int64_t)(h * G + (row0 + row) % G) * D;
 #pragma unroll 1
-        for (int x = half * (D / 2); x < (half + 1) * (D / 2); x += 16) {
-            uint32_t o[16];
+        for (int x = half * (D / 2); x < (half + 1) * (D / 2); x += 32) {
+            uint32_t o[32];
             if (nt > 0) {
-                tmem_ld16u(to + lane_base + x, o);
+                tmem_ld32(to + lane_base + x, o);
                 tmem_wait_ld(o);
             }
             if (!on) continue;
+            float f[32];   // l = 0: nothing seen (a NaN sum stays: it is not equal to 0)
 #pragma unroll
-            for (int e = 0; e < 16; e += 4) {
-                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (nt > 0)
-                    v = make_float4(__uint_as_float(o[e]) * back, __uint_as_float(o[e + 1]) * back,
-                                    __uint_as_float(o[e + 2]) * back, __uint_as_float(o[e + 3]) * back);
-                if (splits > 1) *(float4 *)&a.rows_part[at * D + x + e] = v;
-                else store_row(a, f4, h, G, D, row0 + row, x + e, v, m, l);
-            }
+            for (int e = 0; e < 32; ++e) f[e] = nt == 0 || l == 0.f ? 0.f : __uint_as_float(o[e]) * norm;
+            if (splits > 1) store_f32<32>(a.rows_part + at * D + x, f);
+            else store_out<32>(a, at_out + x, f);
         }
+        if (splits == 1 && on && half == 0 && a.lse)
+            a.lse[((int64_t)sq.start + (row0 + row) / G) * c.hq + h * G + (row0 + row) % G] = row_lse(m, l);
         if (splits > 1 && on && half == 0) {
             a.rows_ml[at * 2] = m;
             a.rows_ml[at * 2 + 1] = l;
