@@ -88,7 +88,8 @@ bool encode_pool(EncodeFn fn, CUtensorMap *m, const pi_kv_desc_t &d, void *base)
 template <int D>
 cudaError_t setup_of()
 {
-    for (cudaError_t e : {split_setup<D, true>(), split_setup<D, false>(), rows_setup<D, 1>(), rows_setup<D, 2>()})
+    for (cudaError_t e : {split_setup<D, 1, 1>(), split_setup<D, 1, 2>(), split_setup<D, 2, 1>(), split_setup<D, 2, 2>(),
+                          rows_setup<D, 1>(), rows_setup<D, 2>()})
         if (e != cudaSuccess) return e;
     return cudaSuccess;
 }
@@ -106,10 +107,11 @@ cudaError_t attend_of(const pi_kv *h, int layer, KvAttendArgs a, cudaStream_t s)
     a.rows_from = many ? (few ? ROWS_FROM : 0) : INT32_MAX;
     cudaError_t e = cudaSuccess;
     if (few) {
-        // second 16-bit terms unless the output is bf16 and the rows of a sequence (on average) fill more than 8
-        const bool two = a.dtype != PI_BF16 || many || rows <= 8 * n;
-        e = two ? split_launch<D, true>(a, h->map_k[layer], h->map_v[layer], h->nsm, s)
-                : split_launch<D, false>(a, h->map_k[layer], h->map_v[layer], h->nsm, s);
+        // 16 rows to a tile where the rows of a sequence (on average: all that the host knows) fill more than 8
+        const bool wide = many || rows > 8 * n, one = a.dtype == PI_BF16;
+        const auto run = wide ? (one ? split_launch<D, 2, 1> : split_launch<D, 2, 2>)
+                              : (one ? split_launch<D, 1, 1> : split_launch<D, 1, 2>);
+        e = run(a, h->map_k[layer], h->map_v[layer], h->nsm, s);
     }
     if (many && e == cudaSuccess) {
         const int64_t items = (rows / rows_per_item(D) + n) * a.c.hkv;   // at most one partly filled per sequence

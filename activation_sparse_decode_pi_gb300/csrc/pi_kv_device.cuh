@@ -167,6 +167,16 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// The 8 x 8 matrix of 16-bit elements that the warp holds (row lane / 4, columns 2 (lane % 4) and on), transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x)
+{
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t word4(const uint4 &v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+
 // ---------------------------------------------------------------- TMA -----------------------
 
 __device__ __forceinline__ void prefetch_tensormap(const CUtensorMap *m)
@@ -186,11 +196,11 @@ __device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *m, int
 
 // ---------------------------------------------------------------- tile geometry -------------
 
-// Column of dim that n-index n of value product j holds (16 consecutive columns per n, 8 for dim 64).
+// Column of dim that row n + 8 h of value product j stands for (a lane's bytes of a value row, two to a product).
 template <int D>
-__device__ __forceinline__ int out_col(int j, int n)
+__device__ __forceinline__ int out_col(int j, int n, int h)
 {
-    return D == 64 ? 8 * n + j : (j >> 4) * 128 + 16 * n + (j & 15);
+    return D == 64 ? 8 * n + 2 * j + h : (j >> 3) * 128 + 16 * n + 2 * (j & 7) + h;
 }
 
 // Byte of (token, column) inside a swizzled 64-position tile.

@@ -53,16 +53,17 @@ struct KvAttendArgs {
     uint32_t *rows_tickets;    // [items], zero on entry, left zero
 };
 
-// The split kernel (pi_kv_split.cuh) of one head dim; TWO: second 16-bit terms, 8 rows to a tile (else 16).
-template <int D, bool TWO>
+// The split kernel (pi_kv_split.cuh) of one head dim; QN: runs of 8 rows per tile, T: 16-bit terms.
+template <int D, int QN, int T>
 cudaError_t split_setup();   // shared-memory opt-in
-template <int D, bool TWO>
+template <int D, int QN, int T>
 cudaError_t split_launch(const KvAttendArgs &a, const CUtensorMap &mk, const CUtensorMap &mv, int grid, cudaStream_t s);
-#define PI_KV_EXTERN(D, TWO)                         \
-    extern template cudaError_t split_setup<D, TWO>(); \
-    extern template cudaError_t split_launch<D, TWO>(const KvAttendArgs &, const CUtensorMap &, const CUtensorMap &, int, cudaStream_t);
-PI_KV_EXTERN(64, true) PI_KV_EXTERN(64, false) PI_KV_EXTERN(128, true)
-PI_KV_EXTERN(128, false) PI_KV_EXTERN(256, true) PI_KV_EXTERN(256, false)
+#define PI_KV_EXTERN(D, QN, T)                       \
+    extern template cudaError_t split_setup<D, QN, T>(); \
+    extern template cudaError_t split_launch<D, QN, T>(const KvAttendArgs &, const CUtensorMap &, const CUtensorMap &, int, cudaStream_t);
+#define PI_KV_EXTERN4(D) PI_KV_EXTERN(D, 1, 1) PI_KV_EXTERN(D, 1, 2) PI_KV_EXTERN(D, 2, 1) PI_KV_EXTERN(D, 2, 2)
+PI_KV_EXTERN4(64) PI_KV_EXTERN4(128) PI_KV_EXTERN4(256)
+#undef PI_KV_EXTERN4
 #undef PI_KV_EXTERN
 
 // The rows kernel (pi_kv_rows.cuh): QT 16-bit terms of queries and weights. items: an upper bound of the

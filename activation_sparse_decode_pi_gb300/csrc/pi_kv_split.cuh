@@ -10,17 +10,17 @@
 // query head), so everything else has to hide under the loads:
 //  - one producer warp keeps a ring of K and V tiles in flight with TMA (swizzled, so that the
 //    fragment reads are free of bank conflicts); consumer warps take the tiles in turn;
-//  - the products run on mma.sync m16n8k16 (f16 in, fp32 out): an e4m3 code is exact in f16, two codes
-//    convert in one instruction, and the fragments are read straight from the tile's rows because the
-//    contraction may run over dim in any order that q and k share. A tcgen05 product would need
-//    128 rows; a decode step has 1 to 16;
+//  - the products run on mma.sync m16n8k16 (f16 in, fp32 out) with the cache as the 16-row operand (16
+//    positions of K, 16 columns of V) and the queries as the 8 columns, so that a decode step's few rows
+//    waste little of it. An e4m3 code is exact in f16, two codes convert in one instruction, and the
+//    fragments are read straight from the tile's rows because the contraction may run over dim in any
+//    order that q and k share, and the output's rows may stand for its columns in any order;
 //  - all (sequence, kv head, row tile) items are laid end to end and cut into equal runs of tiles, one
 //    per CTA, so ragged lengths and one long sequence fill the GPU alike. An item cut over CTAs is
 //    joined by the last of them to finish, in the order of its parts (the same bits every time).
 // Rounding: q is scaled by a power of two per row so that its largest value lies in [128, 256) and cut
-// to f16, weights are held as f16 in units of 2^-14 (floor 2^-38). TWO: both keep a second f16 term
-// (22 bits, fp32 accuracy; rows 8-15 of the mma hold the second terms of rows 0-7, at no extra cost).
-// Without it (bf16 output, more than 8 rows) 11 bits of the weight meet the output's 8.
+// to f16, weights are held as f16 in units of 2^-14 (floor 2^-38). T = 2: both keep a second f16 term
+// (22 bits, fp32 accuracy). T = 1 (bf16 output): 11 bits of the weight meet the output's 8.
 #pragma once
 
 #include "pi_kv_device.cuh"
@@ -28,44 +28,52 @@
 
 namespace pi {
 
-template <int D, bool TWO>
+// QN: runs of 8 rows per tile; T: 16-bit terms.
+template <int D, int QN, int T>
 struct SplitCfg {
-    static constexpr int NW = D == 256 ? 4 : 7;          // consumer warps (8 warps in all: 255 registers each)
-    static constexpr int R = TWO ? 8 : 16;               // rows per tile
+    static constexpr bool WIDE = QN == 2 || D == 256;    // accumulators that leave no more than 8 warps on an SM
+    static constexpr int NW = !WIDE ? 11 : QN == 2 && D == 256 ? 4 : 7;   // consumer warps (and one producer)
+    static constexpr int R = 8 * QN;                     // rows per tile
     static constexpr int SLOT = KV_TILE * D;             // bytes of one K or V tile
     static constexpr int NT = (NW + 1) * 32;
     static constexpr int MERGE = NW * R * (D + 4) * 4;   // bytes: numerators of every warp
-    static constexpr int QB = D == 256 ? 16 * 512 : 0;   // bytes: query fragments (D 256 has no registers left)
+    static constexpr int STEPS = D / 16;                 // 16-wide steps of the score's contraction
+    // query fragments in shared memory where they and the accumulators are too many for the registers
+    static constexpr bool QS = STEPS * 2 * T * QN + D / 16 * QN * 4 > 160;
+    static constexpr int QB = QS ? STEPS * QN * T * 32 * 8 : 0;
     static constexpr int MAX_SLOTS = 24;
 };
 
 struct SplitMeta {   // of one ring slot
     float sc[4];     // block scales of the tile's pages
     uint32_t valid;  // bit per page: present
-    uint32_t pad[3];
+    uint32_t round;  // times the slot was filled before
+    uint32_t pad[2];
 };
 
 struct Seg {
     int i, h, rt, k0, k1, nt;
 };
 
-template <int D, bool TWO>
-__global__ void __launch_bounds__(SplitCfg<D, TWO>::NT, 1)
+template <int D, int QN, int T>
+__global__ void __launch_bounds__(SplitCfg<D, QN, T>::NT, 1)
     k_kv_split(const __grid_constant__ KvAttendArgs a, const __grid_constant__ CUtensorMap mk,
                const __grid_constant__ CUtensorMap mv, int slots)
 {
-    using C = SplitCfg<D, TWO>;
-    constexpr int NW = C::NW, R = C::R, NJ = D / 8, NCH = D / 64;   // output n-tiles, 16-byte key chunks per lane
+    using C = SplitCfg<D, QN, T>;
+    constexpr int NW = C::NW, R = C::R, NJ = D / 16, NCH = D / 64;   // output row tiles, 16-byte key chunks per lane
+    constexpr int QC = 2 * QN;                                       // rows (columns of the products) a lane holds
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     float *merge = (float *)(ring + (size_t)slots * C::SLOT);
-    uint4 *qfrag = (uint4 *)((uint8_t *)merge + C::MERGE);
+    uint2 *qfrag = (uint2 *)((uint8_t *)merge + C::MERGE);   // [step][run of rows][term][lane]
     float *ml = (float *)((uint8_t *)qfrag + C::QB);                       // [NW][R][2]
     SplitMeta *meta = (SplitMeta *)(ml + NW * R * 2);
     uint64_t *full = (uint64_t *)(meta + slots), *empty = full + slots;
     long long *prefix = (long long *)(empty + slots);                      // [n + 1] tiles before sequence i
     int4 *info = (int4 *)((uintptr_t)(prefix + a.b.n + 2) & ~(uintptr_t)15);   // [n] row, length, start, new tokens
     __shared__ long long wtot[NW + 1];
+    __shared__ float qscale[R];
     __shared__ int s_last, s_dead;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -73,6 +81,7 @@ __global__ void __launch_bounds__(SplitCfg<D, TWO>::NT, 1)
     const int G = c.hq / c.hkv;
     if (tid == 0) {
         for (int s = 0; s < slots; ++s) {
+            meta[s].round = 0xffffffffu;
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
         }
@@ -178,35 +187,49 @@ __global__ void __launch_bounds__(SplitCfg<D, TWO>::NT, 1)
                         vs = a.l.vs[(size_t)page * c.hkv + g.h];
                     }
                 }
+                // Four ring slots at a time, a lane to each: keys and values of two tiles.
                 const uint32_t there = __ballot_sync(0xffffffffu, page >= 0);
-                for (int x = 0; x < per && kb + x < g.k1; ++x, ++n) {
-                    const uint32_t valid = (there >> (x * np)) & ((1u << np) - 1u);
-                    const uint32_t bytes = __popc(valid) * box_rows * D;
-                    const bool mine = lane / np == x && lane < per * np;
-#pragma unroll
-                    for (int kv = 0; kv < 2; ++kv) {
-                        const uint32_t u = 2 * n + kv, slot = u % slots, round = u / slots;
-                        if (round > 0 && !dead && !mbar_wait(&empty[slot], (round - 1) & 1)) dead = true;
-                        if (*(volatile int *)&s_dead) dead = true;
-                        dead = __any_sync(0xffffffffu, dead);
-                        if (dead) break;
-                        if (mine) {
-                            meta[slot].sc[sub] = kv ? vs : ks;
-                            if (sub == 0) meta[slot].valid = valid;
-                        }
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive_expect_tx(&full[slot], bytes);
-                        __syncwarp();
-                        if (mine && page >= 0) {
-                            const int row = (page * c.hkv + g.h) * P + (P > KV_TILE ? (pos & (P - 1)) : 0);
-                            uint8_t *dst = ring + (size_t)slot * C::SLOT + sub * box_rows * (D < 128 ? D : 128);
-#pragma unroll
-                            for (int x0 = 0; x0 < D; x0 += 128)
-                                tma_load_2d(dst + x0 * KV_TILE, kv ? &mv : &mk, x0, row, &full[slot]);
-                        }
+                const int count = min(per, g.k1 - kb);
+                for (int x = 0; x < count && !dead; x += 2) {
+                    const int y = x + ((lane >> 1) & 1), kv = lane & 1;
+                    const bool act = lane < 4 && y < count;
+                    const uint32_t u = 2 * (n + y) + kv, slot = u % slots, round = u / slots;
+                    if (act && round > 0 && !mbar_wait(&empty[slot], (round - 1) & 1)) dead = true;
+                    if (*(volatile int *)&s_dead) dead = true;
+                    dead = __any_sync(0xffffffffu, dead);
+                    if (dead) {
+                        n += x;
+                        break;
                     }
-                    if (dead) break;
+                    const uint32_t valid = (there >> (y * np)) & ((1u << np) - 1u);
+                    if (act) {
+                        meta[slot].valid = valid;
+                        *(volatile uint32_t *)&meta[slot].round = round;
+                    }
+                    int pg[4];
+#pragma unroll
+                    for (int p = 0; p < 4; ++p) {
+                        const int from = (y * np + p) & 31;
+                        pg[p] = __shfl_sync(0xffffffffu, page, from);
+                        const float k1 = __shfl_sync(0xffffffffu, ks, from), v1 = __shfl_sync(0xffffffffu, vs, from);
+                        if (act && p < np) meta[slot].sc[p] = kv ? v1 : k1;
+                    }
+                    if (act) {
+                        mbar_arrive_expect_tx(&full[slot], __popc(valid) * box_rows * D);
+#pragma unroll
+                        for (int p = 0; p < 4; ++p)
+                            if (p < np && ((valid >> p) & 1u)) {
+                                const int tl = kb + y < ns ? kb + y : w0 + kb + y - ns;
+                                const int row = (pg[p] * c.hkv + g.h) * P + ((tl * KV_TILE + p * box_rows) & (P - 1));
+                                uint8_t *dst = ring + (size_t)slot * C::SLOT + p * box_rows * (D < 128 ? D : 128);
+#pragma unroll
+                                for (int x0 = 0; x0 < D; x0 += 128)
+                                    tma_load_2d(dst + x0 * KV_TILE, kv ? &mv : &mk, x0, row, &full[slot]);
+                            }
+                    }
+                    __syncwarp();
                 }
+                if (!dead) n += count;
             }
             t += g.k1 - g.k0;
         }
@@ -239,12 +262,22 @@ __global__ void __launch_bounds__(SplitCfg<D, TWO>::NT, 1)
     const int page_shift = __ffs(box_rows) - 1;
     uint32_t n0 = 0;
     bool dead = false;
+    float inv = 0.f;   // 2^14 / unit of the item
+    // A warp may come to a slot two fillings early (there are about as many warps as slots for two tiles each), and
+    // parity tells a phase from its neighbours only: the filling is right when the producer's count says so too.
+    auto filled = [&](uint32_t slot, uint32_t round) {
+        return mbar_try_wait(&full[slot], round & 1) && *(volatile uint32_t *)&meta[slot].round == round;
+    };
     auto wait_full = [&](uint32_t slot, uint32_t round) {
-        if (!dead && !mbar_wait(&full[slot], round & 1)) {
-            dead = true;
-            *(volatile int *)&s_dead = 1;
-            set_status(c.status, ST_TIMEOUT);
-        }
+        if (dead || filled(slot, round)) return;
+        const unsigned long long since = globaltimer_ns();
+        while (!filled(slot, round))
+            if (globaltimer_ns() - since > WAIT_LIMIT_NS) {
+                dead = true;
+                *(volatile int *)&s_dead = 1;
+                set_status(c.status, ST_TIMEOUT);
+                break;
+            }
     };
 
     for (long long t = t0; t < t1;) {
@@ -255,15 +288,12 @@ __global__ void __launch_bounds__(SplitCfg<D, TWO>::NT, 1)
         view(L, nq, w0, ns, nt_all);
         const int row0 = sg.rt * R, rows = min(R, nq * G - row0);   // rows of this tile
         const int pos_lo = p0 + row0 / G, pos_hi = p0 + (row0 + rows - 1) / G;
-        int pos[TWO ? 1 : 2];
-        float qf[TWO ? 1 : 2];
-        uint32_t qa[D == 256 ? 1 : NCH * 4][4];
-        // query fragments: this lane's row(s), elements koff-ordered like the keys
+        // query fragments: this lane's row(s) of each run, elements in the order of the keys' bytes
+        uint32_t qa[C::QS ? 1 : C::STEPS][QN][T][2];
 #pragma unroll
-        for (int rr = 0; rr < (TWO ? 1 : 2); ++rr) {
+        for (int rr = 0; rr < QN; ++rr) {
             const int r = g + 8 * rr;
             const bool on = r < rows;
-            pos[rr] = on ? p0 + (row0 + r) / G : -1;
             const int64_t at = on ? ((int64_t)f.z + (row0 + r) / G) * a.ldq +
                                         (int64_t)(sg.h * G + (row0 + r) % G) * D
                                   : 0;
@@ -283,7 +313,7 @@ __global__ void __launch_bounds__(SplitCfg<D, TWO>::NT, 1)
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
             const int ex = top > 0.f ? min(max(ilogbf(top), -118), 127) : 0;   // 2^ex <= top < 2^(ex + 1)
             const float mul = exp2i(7 - ex);
-            qf[rr] = a.scale_log2 * exp2i(ex - 7);
+            if (warp == 0 && q == 0) qscale[r] = a.scale_log2 * exp2i(ex - 7);
 #pragma unroll
             for (int ch = 0; ch < NCH; ++ch)
 #pragma unroll
@@ -292,153 +322,171 @@ __global__ void __launch_bounds__(SplitCfg<D, TWO>::NT, 1)
 #pragma unroll
                     for (int e = 0; e < 2; ++e)
                         split_pair(x[ch][st * 4 + 2 * e] * mul, x[ch][st * 4 + 2 * e + 1] * mul, hi[e], lo[e]);
-                    uint32_t *dst;
-                    if constexpr (D == 256) dst = (uint32_t *)&qfrag[(ch * 4 + st) * 32 + lane];
-                    else dst = qa[ch * 4 + st];
-                    if constexpr (D == 256) {
-                        if ((ch * 4 + st) % NW != warp) continue;   // the warps share one copy
-                    }
-                    if constexpr (TWO) {
-                        dst[0] = hi[0];
-                        dst[1] = lo[0];
-                        dst[2] = hi[1];
-                        dst[3] = lo[1];
+                    const int k = ch * 4 + st;
+                    if constexpr (C::QS) {
+                        if (k % NW != warp) continue;   // the warps share one copy
+                        qfrag[((k * QN + rr) * T) * 32 + lane] = make_uint2(hi[0], hi[1]);
+                        if constexpr (T == 2) qfrag[((k * QN + rr) * T + 1) * 32 + lane] = make_uint2(lo[0], lo[1]);
                     } else {
-                        dst[rr] = hi[0];
-                        dst[2 + rr] = hi[1];
+                        qa[k][rr][0][0] = hi[0], qa[k][rr][0][1] = hi[1];
+                        if constexpr (T == 2) qa[k][rr][T - 1][0] = lo[0], qa[k][rr][T - 1][1] = lo[1];
                     }
                 }
         }
-        if constexpr (D == 256) bar_sync(1, NW * 32);
-
-        float m[TWO ? 1 : 2], l[TWO ? 1 : 2], acc[NJ][4], unit = 0.f;
+        bar_sync(1, NW * 32);
+        // of this lane's rows 8 rr + 2 q + e: position, and factor from product to base-2 score
+        int pos[QC];
+        float qf[QC], m[QC], l[QC], acc[QN][NJ][4], unit = 0.f;
+        inv = 0.f;
 #pragma unroll
-        for (int rr = 0; rr < (TWO ? 1 : 2); ++rr) {
-            m[rr] = -INFINITY;
-            l[rr] = 0.f;
+        for (int x = 0; x < QC; ++x) {
+            const int r = 8 * (x >> 1) + 2 * q + (x & 1);
+            pos[x] = r < rows ? p0 + (row0 + r) / G : -1;
+            qf[x] = qscale[r];
+            m[x] = -INFINITY;
+            l[x] = 0.f;
         }
 #pragma unroll
-        for (int j = 0; j < NJ; ++j)
+        for (int rr = 0; rr < QN; ++rr)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
+            for (int j = 0; j < NJ; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[rr][j][e] = 0.f;
 
         for (int k = sg.k0 + warp; k < sg.k1; k += NW) {
             const uint32_t u = 2 * (n0 + (k - sg.k0));
             const int tile = k < ns ? k : w0 + k - ns, j0 = tile * KV_TILE;
-            // ---- scores
+            // ---- scores: s[rr][t][2 h + e] of position 16 t + 8 h + g and row 8 rr + 2 q + e
             const uint32_t ks_slot = u % slots;
             wait_full(ks_slot, u / slots);
             const uint8_t *kt = ring + (size_t)ks_slot * C::SLOT;
             const uint32_t valid = meta[ks_slot].valid;
             const bool whole = valid == (1u << np) - 1u && j0 + KV_TILE - 1 <= pos_lo &&
                                (pos_hi - j0 < a.window || j0 + KV_TILE <= a.sinks);
-            float s[8][4];
+            float s[QN][4][4];
 #pragma unroll
-            for (int nt = 0; nt < 8; ++nt)
+            for (int rr = 0; rr < QN; ++rr)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
+                for (int t = 0; t < 4; ++t)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[rr][t][e] = 0.f;
 #pragma unroll
             for (int ch = 0; ch < NCH; ++ch) {
 #pragma unroll
-                for (int h4 = 0; h4 < 2; ++h4) {
-                    uint4 kw[4];
+                for (int t2 = 0; t2 < 4; t2 += 2) {   // two runs of 16 positions at a time
+                    uint4 kw[2][2];
 #pragma unroll
-                    for (int nt = 0; nt < 4; ++nt)
-                        kw[nt] = *(const uint4 *)(kt + (ch >> 1) * KV_TILE * 128 + (h4 * 4 + nt) * 8 * ROWB +
-                                                  koff[ch & 1]);
+                    for (int t = 0; t < 2; ++t)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            kw[t][h] = *(const uint4 *)(kt + (ch >> 1) * KV_TILE * 128 +
+                                                        ((t2 + t) * 16 + h * 8) * ROWB + koff[ch & 1]);
 #pragma unroll
                     for (int st = 0; st < 4; ++st) {
-                        uint32_t af[4];
-                        if constexpr (D == 256) {
-                            const uint4 v = qfrag[(ch * 4 + st) * 32 + lane];
-                            af[0] = v.x, af[1] = v.y, af[2] = v.z, af[3] = v.w;
-                        } else {
+                        uint32_t qb[QN][T][2];
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) af[e] = qa[ch * 4 + st][e];
-                        }
+                        for (int rr = 0; rr < QN; ++rr)
 #pragma unroll
-                        for (int nt = 0; nt < 4; ++nt) {
-                            const uint32_t w = st == 0 ? kw[nt].x : st == 1 ? kw[nt].y : st == 2 ? kw[nt].z : kw[nt].w;
-                            mma_f16(s[h4 * 4 + nt], af, e4m3x2_f16x2((uint16_t)w), e4m3x2_f16x2((uint16_t)(w >> 16)));
+                            for (int x = 0; x < T; ++x) {
+                                if constexpr (C::QS) {
+                                    const uint2 v = qfrag[(((ch * 4 + st) * QN + rr) * T + x) * 32 + lane];
+                                    qb[rr][x][0] = v.x, qb[rr][x][1] = v.y;
+                                } else {
+                                    qb[rr][x][0] = qa[ch * 4 + st][rr][x][0], qb[rr][x][1] = qa[ch * 4 + st][rr][x][1];
+                                }
+                            }
+#pragma unroll
+                        for (int t = 0; t < 2; ++t) {
+                            uint32_t ka[4];   // rows g and g + 8, columns 0-1 and 2-3 of this lane's four
+                            e4m3x4_f16x4(word4(kw[t][0], st), ka[0], ka[2]);
+                            e4m3x4_f16x4(word4(kw[t][1], st), ka[1], ka[3]);
+#pragma unroll
+                            for (int rr = 0; rr < QN; ++rr)
+#pragma unroll
+                                for (int x = 0; x < T; ++x) mma_f16(s[rr][t2 + t], ka, qb[rr][x][0], qb[rr][x][1]);
                         }
                     }
                 }
             }
-            float sc[4];
-            if (np == 1) {
-                sc[0] = meta[ks_slot].sc[0];
-            } else {
-                const float4 v = *(const float4 *)meta[ks_slot].sc;
-                sc[0] = v.x, sc[1] = v.y, sc[2] = v.z, sc[3] = v.w;
-            }
-            auto pick = [&](const float (&v)[4], int nt) {   // of the page that n-tile nt lies in
-                const int p = (nt * 8) >> page_shift;
-                return np == 1 ? v[0] : p == 0 ? v[0] : p == 1 ? v[1] : p == 2 ? v[2] : v[3];
+            float sc[4];   // of the four runs of 16 positions
+            auto run_scales = [&](uint32_t slot) {
+                if (np == 1) {
+                    sc[0] = sc[1] = sc[2] = sc[3] = meta[slot].sc[0];
+                } else {
+                    const float4 v = *(const float4 *)meta[slot].sc;
+                    sc[0] = v.x, sc[1] = np == 2 ? v.x : v.y, sc[2] = np == 2 ? v.y : v.z, sc[3] = np == 2 ? v.y : v.w;
+                }
             };
-            // ---- to base-2 logits; what a row does not see is -infinity
-            float top[TWO ? 1 : 2];
-#pragma unroll
-            for (int rr = 0; rr < (TWO ? 1 : 2); ++rr) top[rr] = -INFINITY;
-#pragma unroll
-            for (int nt = 0; nt < 8; ++nt) {
-                const float ks = pick(sc, nt);
-#pragma unroll
-                for (int rr = 0; rr < (TWO ? 1 : 2); ++rr)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float v = TWO ? s[nt][e] + s[nt][2 + e] : s[nt][2 * rr + e];
-                        v *= qf[rr] * ks;
-                        if (!whole) {
-                            const int j = j0 + nt * 8 + 2 * q + e;
-                            const bool see = j <= pos[rr] && ((valid >> ((nt * 8) >> page_shift)) & 1u) &&
-                                             (pos[rr] - j < a.window || j < a.sinks);
-                            v = see ? v : -INFINITY;
-                        }
-                        s[nt][2 * rr + e] = v;
-                        top[rr] = fmaxf(top[rr], v);
-                    }
-            }
+            run_scales(ks_slot);
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[ks_slot]);   // every lane has read its keys and their scales
+            // ---- to base-2 logits; what a row does not see is -infinity
+            float top[QC];
+#pragma unroll
+            for (int x = 0; x < QC; ++x) top[x] = -INFINITY;
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int rr = 0; rr < QN; ++rr)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float v = s[rr][t][e] * (qf[2 * rr + (e & 1)] * sc[t]);
+                        s[rr][t][e] = v;
+                    }
+            if (!whole) {
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+#pragma unroll
+                    for (int rr = 0; rr < QN; ++rr)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int j = j0 + t * 16 + (e >> 1) * 8 + g, p = pos[2 * rr + (e & 1)];
+                            const bool see = j <= p && ((valid >> ((t * 16) >> page_shift)) & 1u) &&
+                                             (p - j < a.window || j < a.sinks);
+                            if (!see) s[rr][t][e] = -INFINITY;
+                        }
+            }
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int rr = 0; rr < QN; ++rr)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) top[2 * rr + (e & 1)] = fmaxf(top[2 * rr + (e & 1)], s[rr][t][e]);
             // ---- running maximum
-            float corr[TWO ? 1 : 2];
+            float corr[QC];
             bool grew = false;
 #pragma unroll
-            for (int rr = 0; rr < (TWO ? 1 : 2); ++rr) {
-                top[rr] = fmaxf(top[rr], __shfl_xor_sync(0xffffffffu, top[rr], 1));
-                top[rr] = fmaxf(top[rr], __shfl_xor_sync(0xffffffffu, top[rr], 2));
-                const float mn = fmaxf(m[rr], top[rr]);
-                corr[rr] = mn > m[rr] ? ex2(m[rr] - mn) : 1.f;   // m = -infinity: 0
-                grew |= mn > m[rr];
-                m[rr] = mn;
+            for (int x = 0; x < QC; ++x) {
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], o));
+                const float mn = fmaxf(m[x], top[x]);
+                corr[x] = mn > m[x] ? ex2(m[x] - mn) : 1.f;   // m = -infinity: 0
+                grew |= mn > m[x];
+                m[x] = mn;
             }
             // ---- values
             const uint32_t vs_slot = (u + 1) % slots;
             wait_full(vs_slot, (u + 1) / slots);
             uint8_t *vt = ring + (size_t)vs_slot * C::SLOT;
-            if (np == 1) {
-                sc[0] = meta[vs_slot].sc[0];
-            } else {
-                const float4 v = *(const float4 *)meta[vs_slot].sc;
-                sc[0] = v.x, sc[1] = v.y, sc[2] = v.z, sc[3] = v.w;
-            }
-            float vmax = sc[0];
-            for (int p = 1; p < np; ++p) vmax = fmaxf(vmax, p == 1 ? sc[1] : p == 2 ? sc[2] : sc[3]);
+            run_scales(vs_slot);
+            const float vmax = fmaxf(fmaxf(sc[0], sc[1]), fmaxf(sc[2], sc[3]));
             // numerators are kept in units of the largest value scale so far
             float shrink = 1.f;
             if (vmax > unit) {
                 shrink = unit / vmax;
                 unit = vmax;
+                inv = 16384.f / unit;
             }
-            const float inv = unit > 0.f ? 16384.f / unit : 0.f;
             if (__any_sync(0xffffffffu, grew) || shrink != 1.f) {
 #pragma unroll
-                for (int j = 0; j < NJ; ++j)
+                for (int rr = 0; rr < QN; ++rr)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[j][e] *= corr[TWO ? 0 : e >> 1] * shrink;
+                    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[rr][j][e] *= corr[2 * rr + (e & 1)] * shrink;
             }
 #pragma unroll
-            for (int rr = 0; rr < (TWO ? 1 : 2); ++rr) l[rr] *= corr[rr];
+            for (int x = 0; x < QC; ++x) l[x] *= corr[x];
             if (!whole) {
                 // values of positions that no row of the tile sees (stale, absent, past the end) must not
                 // meet a zero weight: 0 * NaN. Others that are NaN poison only the rows that see them.
@@ -456,15 +504,14 @@ __global__ void __launch_bounds__(SplitCfg<D, TWO>::NT, 1)
                 __syncwarp();
                 if (__any_sync(0xffffffffu, nan)) {
                     for (int tok = 0; tok < KV_TILE; ++tok)
-                        for (int jj = 0; jj < NJ; ++jj)
-                            for (int e = 0; e < 2; ++e) {
-                                const int d = out_col<D>(jj, 2 * q + e);
-                                if ((vt[tile_byte<D>(tok, d)] & 0x7f) != 0x7f) continue;
-                                for (int rr = 0; rr < (TWO ? 1 : 2); ++rr) {
-                                    const int j = j0 + tok;
-                                    if (j <= pos[rr] && (pos[rr] - j < a.window || j < a.sinks))
-                                        poison(acc, jj, 2 * rr + e);
-                                }
+                        for (int j = 0; j < NJ; ++j)
+                            for (int h = 0; h < 2; ++h) {
+                                if ((vt[tile_byte<D>(tok, out_col<D>(j, g, h))] & 0x7f) != 0x7f) continue;
+                                const int at = j0 + tok;
+#pragma unroll
+                                for (int x = 0; x < QC; ++x)
+                                    if (at <= pos[x] && (pos[x] - at < a.window || at < a.sinks))
+                                        poison(acc[x >> 1], j, 2 * h + (x & 1));
                             }
                     __syncwarp();
                     for (int x = lane; x < C::SLOT; x += 32)
@@ -473,31 +520,38 @@ __global__ void __launch_bounds__(SplitCfg<D, TWO>::NT, 1)
                 fence_proxy_async_smem();   // the slot's next copy comes after these stores
                 __syncwarp();
             }
-            // ---- weights and their products with the values, 16 positions at a time
+            // ---- weights, and their products with the values, 16 positions at a time
+            float ref[QC];
 #pragma unroll
-            for (int st = 0; st < 4; ++st) {
-                uint32_t pf[4];
+            for (int x = 0; x < QC; ++x) ref[x] = m[x] == -INFINITY ? 0.f : m[x];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int nt = 2 * st + h;
-                    const float vs = pick(sc, nt) * inv;
+            for (int t = 0; t < 4; ++t) {
+                uint32_t pb[QN][T][2];   // positions 2 q, 2 q + 1 (and 8 on) of row g: the scores' fragment transposed
+                const float vs = sc[t] * inv;
 #pragma unroll
-                    for (int rr = 0; rr < (TWO ? 1 : 2); ++rr) {
-                        const float ref = m[rr] == -INFINITY ? 0.f : m[rr];
-                        const float e0 = ex2(s[nt][2 * rr] - ref), e1 = ex2(s[nt][2 * rr + 1] - ref);
-                        l[rr] += e0 + e1;
-                        if constexpr (TWO) split_pair(e0 * vs, e1 * vs, pf[2 * h], pf[2 * h + 1]);
-                        else pf[2 * h + rr] = pack_f16(e0 * vs, e1 * vs);
+                for (int rr = 0; rr < QN; ++rr)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float e0 = ex2(s[rr][t][2 * h] - ref[2 * rr]), e1 = ex2(s[rr][t][2 * h + 1] - ref[2 * rr + 1]);
+                        l[2 * rr] += e0;
+                        l[2 * rr + 1] += e1;
+                        if constexpr (T == 2) {
+                            uint32_t hi, lo;
+                            split_pair(e0 * vs, e1 * vs, hi, lo);
+                            pb[rr][0][h] = transpose8(hi);
+                            pb[rr][T - 1][h] = transpose8(lo);
+                        } else {
+                            pb[rr][0][h] = transpose8(pack_f16(e0 * vs, e1 * vs));
+                        }
                     }
-                }
 #pragma unroll
                 for (int hf = 0; hf < (D + 127) / 128; ++hf) {
-                    uint32_t vw[2][2][4];   // [token half][even / odd token][words]
+                    uint32_t vw[2][2][4];   // [position half][even / odd position][words]
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            const uint8_t *p = vt + hf * KV_TILE * 128 + (st * 16 + h * 8) * ROWB + voff[e];
+                            const uint8_t *p = vt + hf * KV_TILE * 128 + (t * 16 + h * 8) * ROWB + voff[e];
                             if constexpr (D == 64) {
                                 const uint2 v = *(const uint2 *)p;
                                 vw[h][e][0] = v.x, vw[h][e][1] = v.y;
@@ -509,13 +563,15 @@ __global__ void __launch_bounds__(SplitCfg<D, TWO>::NT, 1)
 #pragma unroll
                     for (int w = 0; w < (D == 64 ? 2 : 4); ++w)
 #pragma unroll
-                        for (int b2 = 0; b2 < 2; ++b2) {   // bytes 2 b2 and 2 b2 + 1 of the word
-                            const uint32_t p0w = __byte_perm(vw[0][0][w], vw[0][1][w], b2 ? 0x7362 : 0x5140);
-                            const uint32_t p1w = __byte_perm(vw[1][0][w], vw[1][1][w], b2 ? 0x7362 : 0x5140);
-                            const int j = hf * 16 + w * 4 + b2 * 2;
-                            mma_f16(acc[j], pf, e4m3x2_f16x2((uint16_t)p0w), e4m3x2_f16x2((uint16_t)p1w));
-                            mma_f16(acc[j + 1], pf, e4m3x2_f16x2((uint16_t)(p0w >> 16)),
-                                    e4m3x2_f16x2((uint16_t)(p1w >> 16)));
+                        for (int b2 = 0; b2 < 2; ++b2) {   // columns 2 b2 and 2 b2 + 1 of the word
+                            uint32_t va[4];
+                            e4m3x4_f16x4(__byte_perm(vw[0][0][w], vw[0][1][w], b2 ? 0x7362 : 0x5140), va[0], va[1]);
+                            e4m3x4_f16x4(__byte_perm(vw[1][0][w], vw[1][1][w], b2 ? 0x7362 : 0x5140), va[2], va[3]);
+                            const int j = hf * 8 + w * 2 + b2;
+#pragma unroll
+                            for (int rr = 0; rr < QN; ++rr)
+#pragma unroll
+                                for (int x = 0; x < T; ++x) mma_f16(acc[rr][j], va, pb[rr][x][0], pb[rr][x][1]);
                         }
                 }
             }
@@ -527,20 +583,18 @@ __global__ void __launch_bounds__(SplitCfg<D, TWO>::NT, 1)
         // ---- join the warps
         const float back = unit * (1.f / 16384.f);
 #pragma unroll
-        for (int rr = 0; rr < (TWO ? 1 : 2); ++rr) {
-            const int r = g + 8 * rr;
-            l[rr] += __shfl_xor_sync(0xffffffffu, l[rr], 1);
-            l[rr] += __shfl_xor_sync(0xffffffffu, l[rr], 2);
-            if (q == 0) {
-                ml[(warp * R + r) * 2] = m[rr];
-                ml[(warp * R + r) * 2 + 1] = l[rr];
+        for (int x = 0; x < QC; ++x) {
+            const int r = 8 * (x >> 1) + 2 * q + (x & 1);
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) l[x] += __shfl_xor_sync(0xffffffffu, l[x], o);
+            if (g == 0) {
+                ml[(warp * R + r) * 2] = m[x];
+                ml[(warp * R + r) * 2 + 1] = l[x];
             }
 #pragma unroll
             for (int j = 0; j < NJ; ++j)
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    merge[(warp * R + r) * (D + 4) + out_col<D>(j, 2 * q + e)] =
-                        (TWO ? acc[j][e] + acc[j][2 + e] : acc[j][2 * rr + e]) * back;
+                *(float2 *)&merge[(warp * R + r) * (D + 4) + out_col<D>(j, g, 0)] =
+                    make_float2(acc[x >> 1][j][x & 1] * back, acc[x >> 1][j][2 + (x & 1)] * back);
         }
         bar_sync(1, NW * 32);
         const bool cut = sg.k0 > 0 || sg.k1 < sg.nt;
@@ -630,10 +684,10 @@ struct SplitPlan {
     int slots;
     size_t smem;
 };
-template <int D, bool TWO>
+template <int D, int QN, int T>
 SplitPlan split_plan(int n)
 {
-    using C = SplitCfg<D, TWO>;
+    using C = SplitCfg<D, QN, T>;
     SplitPlan p;
     const size_t fixed = 1024 + C::MERGE + C::QB + C::NW * C::R * 8 + (size_t)(n + 2) * 8 + 32 + (size_t)n * 16;
     const size_t avail = 227 * 1024 - 256 - fixed;   // 256: static shared memory
@@ -643,24 +697,24 @@ SplitPlan split_plan(int n)
     return p;
 }
 
-template <int D, bool TWO>
+template <int D, int QN, int T>
 cudaError_t split_setup()
 {
-    return cudaFuncSetAttribute(k_kv_split<D, TWO>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024 - 256);
+    return cudaFuncSetAttribute(k_kv_split<D, QN, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024 - 256);
 }
 
-template <int D, bool TWO>
+template <int D, int QN, int T>
 cudaError_t split_launch(const KvAttendArgs &a, const CUtensorMap &mk, const CUtensorMap &mv, int grid, cudaStream_t s)
 {
-    const SplitPlan p = split_plan<D, TWO>(a.b.n);
+    const SplitPlan p = split_plan<D, QN, T>(a.b.n);
     Launch L;
     L.grid = dim3(grid);
-    L.block = dim3(SplitCfg<D, TWO>::NT);
+    L.block = dim3(SplitCfg<D, QN, T>::NT);
     L.smem = p.smem;
     L.stream = s;
     L.pdl = true;
     L.nsm = grid;
-    return launch_ex(L, k_kv_split<D, TWO>, a, mk, mv, p.slots);
+    return launch_ex(L, k_kv_split<D, QN, T>, a, mk, mv, p.slots);
 }
 
 }  // namespace pi

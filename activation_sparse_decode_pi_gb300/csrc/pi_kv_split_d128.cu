@@ -2,10 +2,16 @@
 #include "pi_kv_split.cuh"
 
 namespace pi {
-template cudaError_t split_setup<128, true>();
-template cudaError_t split_setup<128, false>();
-template cudaError_t split_launch<128, true>(const KvAttendArgs &, const CUtensorMap &, const CUtensorMap &, int,
+template cudaError_t split_setup<128, 1, 1>();
+template cudaError_t split_launch<128, 1, 1>(const KvAttendArgs &, const CUtensorMap &, const CUtensorMap &, int,
                                             cudaStream_t);
-template cudaError_t split_launch<128, false>(const KvAttendArgs &, const CUtensorMap &, const CUtensorMap &, int,
-                                             cudaStream_t);
+template cudaError_t split_setup<128, 1, 2>();
+template cudaError_t split_launch<128, 1, 2>(const KvAttendArgs &, const CUtensorMap &, const CUtensorMap &, int,
+                                            cudaStream_t);
+template cudaError_t split_setup<128, 2, 1>();
+template cudaError_t split_launch<128, 2, 1>(const KvAttendArgs &, const CUtensorMap &, const CUtensorMap &, int,
+                                            cudaStream_t);
+template cudaError_t split_setup<128, 2, 2>();
+template cudaError_t split_launch<128, 2, 2>(const KvAttendArgs &, const CUtensorMap &, const CUtensorMap &, int,
+                                            cudaStream_t);
 }  // namespace pi
