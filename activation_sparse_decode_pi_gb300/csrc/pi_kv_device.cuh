@@ -38,6 +38,11 @@ __device__ __forceinline__ KvSeq kv_sequence(const KvView &c, const KvBatch &b, 
     return s;
 }
 
+template <bool B>
+struct Const {
+    static constexpr bool value = B;
+};
+
 // ---------------------------------------------------------------- e4m3 ----------------------
 
 // Two codes (low byte first) as two f16 values, exactly.

@@ -32,11 +32,15 @@ namespace pi {
 template <int D, int QN, int T>
 struct SplitCfg {
     static constexpr bool WIDE = QN == 2 || D == 256;    // accumulators that leave no more than 8 warps on an SM
-    static constexpr int NW = !WIDE ? 11 : QN == 2 && D == 256 ? 4 : 7;   // consumer warps (and one producer)
+    static constexpr int NW = QN == 2 && D == 256 ? 4 : 7;   // consumer warps (and one producer)
+    // Where there is room, 4 more warps join the consumers' results of an item while these go on to the next one.
+    static constexpr bool FLOW = !WIDE;
     static constexpr int R = 8 * QN;                     // rows per tile
     static constexpr int SLOT = KV_TILE * D;             // bytes of one K or V tile
-    static constexpr int NT = (NW + 1) * 32;
-    static constexpr int MERGE = NW * R * (D + 4) * 4;   // bytes: numerators of every warp
+    static constexpr int JT = FLOW ? 128 : NW * 32;      // threads that join
+    static constexpr int NT = (NW + 1) * 32 + (FLOW ? JT : 0);
+    static constexpr int NM = FLOW ? 2 : 1;              // buffers of the warps' results
+    static constexpr int MERGE = NW * R * (D + 4) * 4;   // bytes of one: numerators of every warp
     static constexpr int STEPS = D / 16;                 // 16-wide steps of the score's contraction
     // query fragments in shared memory where they and the accumulators are too many for the registers
     static constexpr bool QS = STEPS * 2 * T * QN + D / 16 * QN * 4 > 160;
@@ -66,14 +70,14 @@ __global__ void __launch_bounds__(SplitCfg<D, QN, T>::NT, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     float *merge = (float *)(ring + (size_t)slots * C::SLOT);
-    uint2 *qfrag = (uint2 *)((uint8_t *)merge + C::MERGE);   // [step][run of rows][term][lane]
-    float *ml = (float *)((uint8_t *)qfrag + C::QB);                       // [NW][R][2]
-    SplitMeta *meta = (SplitMeta *)(ml + NW * R * 2);
+    uint2 *qfrag = (uint2 *)((uint8_t *)merge + C::NM * C::MERGE);   // [step][run of rows][term][lane]
+    float *ml = (float *)((uint8_t *)qfrag + C::QB);   // per buffer: [NW][R][2] of the warps, [R][2] joined
+    SplitMeta *meta = (SplitMeta *)(ml + C::NM * (NW + 1) * R * 2);
     uint64_t *full = (uint64_t *)(meta + slots), *empty = full + slots;
     long long *prefix = (long long *)(empty + slots);                      // [n + 1] tiles before sequence i
     int4 *info = (int4 *)((uintptr_t)(prefix + a.b.n + 2) & ~(uintptr_t)15);   // [n] row, length, start, new tokens
-    __shared__ long long wtot[NW + 1];
-    __shared__ float qscale[R];
+    __shared__ long long wtot[C::NT / 32];
+    __shared__ uint64_t jfull[2], jempty[2];   // results of a segment: written, joined
     __shared__ int s_last, s_dead;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -84,6 +88,10 @@ __global__ void __launch_bounds__(SplitCfg<D, QN, T>::NT, 1)
             meta[s].round = 0xffffffffu;
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
+        }
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(&jfull[x], NW);
+            mbar_init(&jempty[x], 1);
         }
         fence_mbar_init();
         s_dead = 0;
@@ -121,7 +129,7 @@ __global__ void __launch_bounds__(SplitCfg<D, QN, T>::NT, 1)
         if (lane == 31) wtot[warp] = inc;
         __syncthreads();
         long long before = run, all = 0;
-        for (int k = 0; k <= NW; ++k) {
+        for (int k = 0; k < C::NT / 32; ++k) {
             before += k < warp ? wtot[k] : 0;
             all += wtot[k];
         }
@@ -245,6 +253,124 @@ __global__ void __launch_bounds__(SplitCfg<D, QN, T>::NT, 1)
         return;
     }
 
+    // Joins a segment (its first tile t, the CTA's n-th tile): the results of the warps that had tiles of it, in the
+    // order of their tiles, by the JT threads `me`.
+    auto join = [&](const Seg &sg, long long t, uint32_t n, int buf, int me) {
+        auto sync = [&]() { bar_sync(2, C::JT); };
+        float *const mg = merge + buf * (C::MERGE / 4), *const mm = ml + buf * ((NW + 1) * R * 2);
+        float *const sums = mm + NW * R * 2;
+        const int4 f = info[sg.i];
+        const int row0 = sg.rt * R, rows = min(R, f.w * G - row0), count = sg.k1 - sg.k0, turn = n % NW;
+        const bool cut = sg.k0 > 0 || sg.k1 < sg.nt;
+        const long long item0 = t - sg.k0;                                 // first tile of the item
+        const int ca = (int)(item0 / quota), cb = (int)((item0 + sg.nt - 1) / quota);
+        const int part = (int)blockIdx.x == ca ? 2 * ca + 1 : 2 * (int)blockIdx.x;
+        // per row: the warps' weights against the common maximum (in place of their own), the maximum and the sum
+        const int np_w = min(count, NW);
+        if (me < rows) {
+            float M = -INFINITY, S = 0.f;
+            for (int y = 0, w = turn; y < np_w; ++y, w = w + 1 == NW ? 0 : w + 1) M = fmaxf(M, mm[(w * R + me) * 2]);
+            for (int y = 0, w = turn; y < np_w; ++y, w = w + 1 == NW ? 0 : w + 1) {
+                const float mw = mm[(w * R + me) * 2], lw = mm[(w * R + me) * 2 + 1];
+                const float f2 = mw == -INFINITY ? (lw != 0.f ? 1.f : 0.f) : ex2(mw - M);
+                S += lw * f2;
+                mm[(w * R + me) * 2] = f2;
+            }
+            sums[me * 2] = M;
+            sums[me * 2 + 1] = S;
+        }
+        sync();
+        for (int x = me; x < rows * (D / 4); x += C::JT) {
+            const int r = x / (D / 4), d = (x % (D / 4)) * 4;
+            const float M = sums[r * 2], S = sums[r * 2 + 1];
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            int w = turn;
+#pragma unroll
+            for (int y = 0; y < NW; ++y) {
+                if (y < np_w) {
+                    const float f2 = mm[(w * R + r) * 2];
+                    const float4 v = *(const float4 *)&mg[(w * R + r) * (D + 4) + d];
+                    o.x += v.x * f2, o.y += v.y * f2, o.z += v.z * f2, o.w += v.w * f2;
+                }
+                w = w + 1 == NW ? 0 : w + 1;
+            }
+            if (cut) {
+                *(float4 *)&a.part[((size_t)part * R + r) * D + d] = o;
+                if (d == 0) {
+                    a.part_ml[((size_t)part * R + r) * 2] = M;
+                    a.part_ml[((size_t)part * R + r) * 2 + 1] = S;
+                }
+            } else {
+                store_row(a, f, sg.h, G, D, row0 + r, d, o, M, S);
+            }
+        }
+        sync();
+        if (!cut) return;
+        if (me == 0) s_last = ticket_acq_rel(&a.tickets[ca], 1u) == (uint32_t)(cb - ca);
+        sync();
+        if (!s_last) return;
+        float *wt = mg;   // [parts][R] weights
+        const int parts = cb - ca + 1;
+        for (int r = me / 32; r < rows; r += C::JT / 32) {
+            float M = -INFINITY;
+            for (int x = lane; x < parts; x += 32) {
+                const int sl = x == 0 ? 2 * ca + 1 : 2 * (ca + x);
+                M = fmaxf(M, __ldcg(&a.part_ml[((size_t)sl * R + r) * 2]));
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+            float S = 0.f;
+            for (int x = lane; x < parts; x += 32) {
+                const int sl = x == 0 ? 2 * ca + 1 : 2 * (ca + x);
+                const float mx = __ldcg(&a.part_ml[((size_t)sl * R + r) * 2]);
+                const float sx = __ldcg(&a.part_ml[((size_t)sl * R + r) * 2 + 1]);
+                const float w = mx == -INFINITY ? (sx != 0.f ? 1.f : 0.f) : ex2(mx - M);
+                wt[x * R + r] = w;
+                S += w * sx;
+            }
+            S = warp_sum(S);
+            if (lane == 0) {
+                sums[r * 2] = M;
+                sums[r * 2 + 1] = S;
+            }
+        }
+        sync();
+        for (int x = me; x < rows * (D / 4); x += C::JT) {
+            const int r = x / (D / 4), d = (x % (D / 4)) * 4;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+            for (int y = 0; y < parts; ++y) {
+                const int sl = y == 0 ? 2 * ca + 1 : 2 * (ca + y);
+                const float4 v = __ldcg((const float4 *)&a.part[((size_t)sl * R + r) * D + d]);
+                const float w = wt[y * R + r];
+                o.x += v.x * w, o.y += v.y * w, o.z += v.z * w, o.w += v.w * w;
+            }
+            store_row(a, f, sg.h, G, D, row0 + r, d, o, sums[r * 2], sums[r * 2 + 1]);
+        }
+        if (me == 0) a.tickets[ca] = 0;
+        sync();
+    };
+
+    if (C::FLOW && warp > NW) {
+        // ------------------------------------------------------------ joiners
+        uint32_t n = 0;
+        int number = 0;
+        bool dead = false;
+        for (long long t = t0; t < t1; ++number) {
+            const Seg sg = segment(t);
+            if (!dead && !mbar_wait(&jfull[number & 1], (number >> 1) & 1)) {
+                dead = true;
+                set_status(c.status, ST_TIMEOUT);
+            }
+            join(sg, t, n, number & 1, tid - (NW + 1) * 32);
+            bar_sync(2, C::JT);
+            if (tid == (NW + 1) * 32) mbar_arrive(&jempty[number & 1]);
+            n += sg.k1 - sg.k0;
+            t += sg.k1 - sg.k0;
+        }
+        return;
+    }
+
     // ---------------------------------------------------------------- consumers
     const int g = lane >> 2, q = lane & 3;
     // byte offsets of this lane's key chunk 0/1 and value chunks of even/odd tokens inside a tile
@@ -280,8 +406,28 @@ __global__ void __launch_bounds__(SplitCfg<D, QN, T>::NT, 1)
             }
     };
 
+    int number = -1;   // of the segment
     for (long long t = t0; t < t1;) {
         const Seg sg = segment(t);
+        const int count = sg.k1 - sg.k0;
+        // this warp's first tile of the segment: the warps take the CTA's tiles in turn
+        const int kw0 = sg.k0 + (int)((warp + NW - n0 % NW) % NW);
+        ++number;
+        const int buf = C::FLOW ? number & 1 : 0;
+        auto buffer_free = [&]() {   // the results of the segment before the last have left it
+            if (C::FLOW && number > 1 && !dead && !mbar_wait(&jempty[buf], ((number >> 1) - 1) & 1)) {
+                dead = true;
+                *(volatile int *)&s_dead = 1;
+                set_status(c.status, ST_TIMEOUT);
+            }
+        };
+        if (C::FLOW && kw0 >= sg.k1) {   // no tile of it is this warp's
+            buffer_free();
+            if (lane == 0) mbar_arrive(&jfull[buf]);
+            n0 += count;
+            t += count;
+            continue;
+        }
         const int4 f = info[sg.i];
         const int L = f.y, nq = f.w, p0 = L - nq;
         int w0, ns, nt_all;
@@ -290,6 +436,7 @@ __global__ void __launch_bounds__(SplitCfg<D, QN, T>::NT, 1)
         const int pos_lo = p0 + row0 / G, pos_hi = p0 + (row0 + rows - 1) / G;
         // query fragments: this lane's row(s) of each run, elements in the order of the keys' bytes
         uint32_t qa[C::QS ? 1 : C::STEPS][QN][T][2];
+        float qs[QN];   // factor from product to base-2 score of row g of each run
 #pragma unroll
         for (int rr = 0; rr < QN; ++rr) {
             const int r = g + 8 * rr;
@@ -313,7 +460,7 @@ __global__ void __launch_bounds__(SplitCfg<D, QN, T>::NT, 1)
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
             const int ex = top > 0.f ? min(max(ilogbf(top), -118), 127) : 0;   // 2^ex <= top < 2^(ex + 1)
             const float mul = exp2i(7 - ex);
-            if (warp == 0 && q == 0) qscale[r] = a.scale_log2 * exp2i(ex - 7);
+            qs[rr] = a.scale_log2 * exp2i(ex - 7);
 #pragma unroll
             for (int ch = 0; ch < NCH; ++ch)
 #pragma unroll
@@ -333,7 +480,7 @@ __global__ void __launch_bounds__(SplitCfg<D, QN, T>::NT, 1)
                     }
                 }
         }
-        bar_sync(1, NW * 32);
+        if constexpr (C::QS) bar_sync(1, NW * 32);
         // of this lane's rows 8 rr + 2 q + e: position, and factor from product to base-2 score
         int pos[QC];
         float qf[QC], m[QC], l[QC], acc[QN][NJ][4], unit = 0.f;
@@ -342,7 +489,7 @@ __global__ void __launch_bounds__(SplitCfg<D, QN, T>::NT, 1)
         for (int x = 0; x < QC; ++x) {
             const int r = 8 * (x >> 1) + 2 * q + (x & 1);
             pos[x] = r < rows ? p0 + (row0 + r) / G : -1;
-            qf[x] = qscale[r];
+            qf[x] = __shfl_sync(0xffffffffu, qs[x >> 1], (2 * q + (x & 1)) * 4);
             m[x] = -INFINITY;
             l[x] = 0.f;
         }
@@ -353,7 +500,7 @@ __global__ void __launch_bounds__(SplitCfg<D, QN, T>::NT, 1)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) acc[rr][j][e] = 0.f;
 
-        for (int k = sg.k0 + warp; k < sg.k1; k += NW) {
+        for (int k = kw0; k < sg.k1; k += NW) {
             const uint32_t u = 2 * (n0 + (k - sg.k0));
             const int tile = k < ns ? k : w0 + k - ns, j0 = tile * KV_TILE;
             // ---- scores: s[rr][t][2 h + e] of position 16 t + 8 h + g and row 8 rr + 2 q + e
@@ -532,7 +679,8 @@ __global__ void __launch_bounds__(SplitCfg<D, QN, T>::NT, 1)
                 for (int rr = 0; rr < QN; ++rr)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const float e0 = ex2(s[rr][t][2 * h] - ref[2 * rr]), e1 = ex2(s[rr][t][2 * h + 1] - ref[2 * rr + 1]);
+                        const float e0 = ex2(s[rr][t][2 * h] - ref[2 * rr]);
+                        const float e1 = ex2(s[rr][t][2 * h + 1] - ref[2 * rr + 1]);
                         l[2 * rr] += e0;
                         l[2 * rr + 1] += e1;
                         if constexpr (T == 2) {
@@ -578,104 +726,35 @@ __global__ void __launch_bounds__(SplitCfg<D, QN, T>::NT, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[vs_slot]);
         }
-        n0 += sg.k1 - sg.k0;
-
-        // ---- join the warps
+        // ---- the warp's results, for the join
+        buffer_free();
+        float *const mg = merge + buf * (C::MERGE / 4), *const mm = ml + buf * ((NW + 1) * R * 2);
         const float back = unit * (1.f / 16384.f);
 #pragma unroll
         for (int x = 0; x < QC; ++x) {
             const int r = 8 * (x >> 1) + 2 * q + (x & 1);
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) l[x] += __shfl_xor_sync(0xffffffffu, l[x], o);
+            if (r >= rows) continue;
             if (g == 0) {
-                ml[(warp * R + r) * 2] = m[x];
-                ml[(warp * R + r) * 2 + 1] = l[x];
+                mm[(warp * R + r) * 2] = m[x];
+                mm[(warp * R + r) * 2 + 1] = l[x];
             }
 #pragma unroll
             for (int j = 0; j < NJ; ++j)
-                *(float2 *)&merge[(warp * R + r) * (D + 4) + out_col<D>(j, g, 0)] =
+                *(float2 *)&mg[(warp * R + r) * (D + 4) + out_col<D>(j, g, 0)] =
                     make_float2(acc[x >> 1][j][x & 1] * back, acc[x >> 1][j][2 + (x & 1)] * back);
         }
-        bar_sync(1, NW * 32);
-        const bool cut = sg.k0 > 0 || sg.k1 < sg.nt;
-        const long long item0 = t - sg.k0;                                 // first tile of the item
-        const int ca = (int)(item0 / quota), cb = (int)((item0 + sg.nt - 1) / quota);
-        const int part = (int)blockIdx.x == ca ? 2 * ca + 1 : 2 * (int)blockIdx.x;
-        for (int x = tid; x < R * D / 4; x += NW * 32) {
-            const int r = x / (D / 4), d = (x % (D / 4)) * 4;
-            float M = -INFINITY, S = 0.f;
-#pragma unroll
-            for (int w = 0; w < NW; ++w) M = fmaxf(M, ml[(w * R + r) * 2]);
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int w = 0; w < NW; ++w) {
-                const float mw = ml[(w * R + r) * 2], f2 = mw == -INFINITY ? (ml[(w * R + r) * 2 + 1] != 0.f ? 1.f : 0.f) : ex2(mw - M);
-                const float4 v = *(const float4 *)&merge[(w * R + r) * (D + 4) + d];
-                S += ml[(w * R + r) * 2 + 1] * f2;
-                o.x += v.x * f2, o.y += v.y * f2, o.z += v.z * f2, o.w += v.w * f2;
-            }
-            if (r >= rows) continue;
-            if (cut) {
-                *(float4 *)&a.part[((size_t)part * R + r) * D + d] = o;
-                if (d == 0) {
-                    a.part_ml[((size_t)part * R + r) * 2] = M;
-                    a.part_ml[((size_t)part * R + r) * 2 + 1] = S;
-                }
-            } else {
-                store_row(a, f, sg.h, G, D, row0 + r, d, o, M, S);
-            }
-        }
-        bar_sync(1, NW * 32);
-        if (cut) {
-            if (tid == 0) {
-                const uint32_t before = ticket_acq_rel(&a.tickets[ca], 1u);
-                s_last = before == (uint32_t)(cb - ca);
-            }
+        if constexpr (C::FLOW) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&jfull[buf]);
+        } else {
             bar_sync(1, NW * 32);
-            if (s_last) {
-                float *wt = merge;   // [parts][R] weights, then [R][2] maximum and sum
-                const int parts = cb - ca + 1;
-                for (int r = warp; r < rows; r += NW) {
-                    float M = -INFINITY;
-                    for (int x = lane; x < parts; x += 32) {
-                        const int sl = x == 0 ? 2 * ca + 1 : 2 * (ca + x);
-                        M = fmaxf(M, __ldcg(&a.part_ml[((size_t)sl * R + r) * 2]));
-                    }
-#pragma unroll
-                    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-                    float S = 0.f;
-                    for (int x = lane; x < parts; x += 32) {
-                        const int sl = x == 0 ? 2 * ca + 1 : 2 * (ca + x);
-                        const float mx = __ldcg(&a.part_ml[((size_t)sl * R + r) * 2]);
-                        const float sx = __ldcg(&a.part_ml[((size_t)sl * R + r) * 2 + 1]);
-                        const float w = mx == -INFINITY ? (sx != 0.f ? 1.f : 0.f) : ex2(mx - M);
-                        wt[x * R + r] = w;
-                        S += w * sx;
-                    }
-                    S = warp_sum(S);
-                    if (lane == 0) {
-                        ml[r * 2] = M;
-                        ml[r * 2 + 1] = S;
-                    }
-                }
-                bar_sync(1, NW * 32);
-                for (int x = tid; x < rows * (D / 4); x += NW * 32) {
-                    const int r = x / (D / 4), d = (x % (D / 4)) * 4;
-                    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-                    for (int y = 0; y < parts; ++y) {
-                        const int sl = y == 0 ? 2 * ca + 1 : 2 * (ca + y);
-                        const float4 v = __ldcg((const float4 *)&a.part[((size_t)sl * R + r) * D + d]);
-                        const float w = wt[y * R + r];
-                        o.x += v.x * w, o.y += v.y * w, o.z += v.z * w, o.w += v.w * w;
-                    }
-                    store_row(a, f, sg.h, G, D, row0 + r, d, o, ml[r * 2], ml[r * 2 + 1]);
-                }
-                if (tid == 0) a.tickets[ca] = 0;
-                bar_sync(1, NW * 32);
-            }
+            join(sg, t, n0, 0, tid);
+            bar_sync(1, NW * 32);
         }
-        t += sg.k1 - sg.k0;
+        n0 += count;
+        t += count;
     }
 }
 
@@ -689,7 +768,8 @@ SplitPlan split_plan(int n)
 {
     using C = SplitCfg<D, QN, T>;
     SplitPlan p;
-    const size_t fixed = 1024 + C::MERGE + C::QB + C::NW * C::R * 8 + (size_t)(n + 2) * 8 + 32 + (size_t)n * 16;
+    const size_t fixed = 1024 + C::NM * (C::MERGE + (C::NW + 1) * C::R * 8) + C::QB + (size_t)(n + 2) * 8 + 32 +
+                         (size_t)n * 16;
     const size_t avail = 227 * 1024 - 256 - fixed;   // 256: static shared memory
     p.slots = (int)(avail / (C::SLOT + sizeof(SplitMeta) + 16));
     if (p.slots > C::MAX_SLOTS) p.slots = C::MAX_SLOTS;
