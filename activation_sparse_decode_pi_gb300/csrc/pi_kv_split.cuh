@@ -169,77 +169,92 @@ __global__ void __launch_bounds__(SplitCfg<D, QN, T>::NT, 1)
 
     if (warp == NW) {
         // ------------------------------------------------------------ producer
+        // Runs of up to `per` tiles of a segment, whose pages the lanes look up at once (lane: tile lane / np, its page
+        // lane % np). Page ids are loaded two runs before the copies are issued, scales one.
+        struct Run {
+            int h, k, k1, w0, ns, row, len, low, page;   // low: first position in the windows
+            float ks, vs;
+        };
+        const int per = 32 / np;
+        long long at = t0;   // next segment
+        Run seg{0, 0, 0, 0, 0, 0, 0, 0, -1, 0.f, 0.f};
+        auto next = [&]() {   // the next run and its page ids; k >= k1 when there is none
+            if (seg.k >= seg.k1 && at < t1) {
+                const Seg g = segment(at);
+                const int4 f = info[g.i];
+                int nt;
+                view(f.y, f.w, seg.w0, seg.ns, nt);
+                seg.h = g.h, seg.k = g.k0, seg.k1 = g.k1, seg.row = f.x, seg.len = f.y;
+                seg.low = f.y - f.w - a.window + 1;
+                at += g.k1 - g.k0;
+            }
+            Run r = seg;
+            r.k1 = min(seg.k1, seg.k + per);
+            seg.k = r.k1;
+            const int k = r.k + lane / np, pos = (k < r.ns ? k : r.w0 + k - r.ns) * KV_TILE + (lane % np) * box_rows;
+            const bool seen = k < r.k1 && lane < per * np && pos < r.len && (pos < a.sinks || pos + box_rows > r.low);
+            r.page = seen ? c.table[(size_t)r.row * c.max_pages + pos / P] : -2;
+            return r;
+        };
+        auto scales = [&](Run &r) {
+            if (r.page != -2 && (unsigned)r.page >= (unsigned)c.n_pages) set_status(c.status, ST_DEVICE_CHECK);
+            if ((unsigned)r.page >= (unsigned)c.n_pages) r.page = -1;
+            r.ks = r.page >= 0 ? a.l.ks[(size_t)r.page * c.hkv + r.h] : 0.f;
+            r.vs = r.page >= 0 ? a.l.vs[(size_t)r.page * c.hkv + r.h] : 0.f;
+        };
         uint32_t n = 0;   // tiles issued
         bool dead = false;
-        for (long long t = t0; t < t1 && !dead;) {
-            const Seg g = segment(t);
-            const int4 f = info[g.i];
-            int w0, ns, nt;
-            view(f.y, f.w, w0, ns, nt);
-            const int per = 32 / np;   // tiles whose pages the lanes look up at once
-            for (int kb = g.k0; kb < g.k1 && !dead; kb += per) {
-                const int k = kb + lane / np, sub = lane % np;
-                const int tile = k < ns ? k : w0 + k - ns;
-                const int pos = tile * KV_TILE + sub * box_rows;
-                int page = -1;
-                float ks = 0.f, vs = 0.f;
-                const int low = f.y - f.w - a.window + 1;   // first position in the windows
-                const bool seen = pos < f.y && (pos < a.sinks || pos + box_rows > low);
-                if (k < g.k1 && lane < per * np && seen) {
-                    page = c.table[(size_t)f.x * c.max_pages + pos / P];
-                    if (page < 0 || page >= c.n_pages) {
-                        set_status(c.status, ST_DEVICE_CHECK);
-                        page = -1;
-                    } else {
-                        ks = a.l.ks[(size_t)page * c.hkv + g.h];
-                        vs = a.l.vs[(size_t)page * c.hkv + g.h];
-                    }
+        Run r0 = next();
+        scales(r0);
+        Run r1 = next();
+        while (r0.k < r0.k1 && !dead) {
+            const Run r2 = next();
+            scales(r1);
+            // Four ring slots at a time, a lane to each: keys and values of two tiles.
+            const uint32_t there = __ballot_sync(0xffffffffu, r0.page >= 0);
+            const int count = r0.k1 - r0.k;
+            for (int x = 0; x < count; x += 2) {
+                const int y = x + ((lane >> 1) & 1), kv = lane & 1;
+                const bool act = lane < 4 && y < count;
+                const uint32_t u = 2 * (n + y) + kv, slot = u % slots, round = u / slots;
+                if (act && round > 0 && !mbar_wait(&empty[slot], (round - 1) & 1)) dead = true;
+                if (*(volatile int *)&s_dead) dead = true;
+                dead = __any_sync(0xffffffffu, dead);
+                if (dead) {
+                    n += x;
+                    break;
                 }
-                // Four ring slots at a time, a lane to each: keys and values of two tiles.
-                const uint32_t there = __ballot_sync(0xffffffffu, page >= 0);
-                const int count = min(per, g.k1 - kb);
-                for (int x = 0; x < count && !dead; x += 2) {
-                    const int y = x + ((lane >> 1) & 1), kv = lane & 1;
-                    const bool act = lane < 4 && y < count;
-                    const uint32_t u = 2 * (n + y) + kv, slot = u % slots, round = u / slots;
-                    if (act && round > 0 && !mbar_wait(&empty[slot], (round - 1) & 1)) dead = true;
-                    if (*(volatile int *)&s_dead) dead = true;
-                    dead = __any_sync(0xffffffffu, dead);
-                    if (dead) {
-                        n += x;
-                        break;
-                    }
-                    const uint32_t valid = (there >> (y * np)) & ((1u << np) - 1u);
-                    if (act) {
-                        meta[slot].valid = valid;
-                        *(volatile uint32_t *)&meta[slot].round = round;
-                    }
-                    int pg[4];
-#pragma unroll
-                    for (int p = 0; p < 4; ++p) {
-                        const int from = (y * np + p) & 31;
-                        pg[p] = __shfl_sync(0xffffffffu, page, from);
-                        const float k1 = __shfl_sync(0xffffffffu, ks, from), v1 = __shfl_sync(0xffffffffu, vs, from);
-                        if (act && p < np) meta[slot].sc[p] = kv ? v1 : k1;
-                    }
-                    if (act) {
-                        mbar_arrive_expect_tx(&full[slot], __popc(valid) * box_rows * D);
-#pragma unroll
-                        for (int p = 0; p < 4; ++p)
-                            if (p < np && ((valid >> p) & 1u)) {
-                                const int tl = kb + y < ns ? kb + y : w0 + kb + y - ns;
-                                const int row = (pg[p] * c.hkv + g.h) * P + ((tl * KV_TILE + p * box_rows) & (P - 1));
-                                uint8_t *dst = ring + (size_t)slot * C::SLOT + p * box_rows * (D < 128 ? D : 128);
-#pragma unroll
-                                for (int x0 = 0; x0 < D; x0 += 128)
-                                    tma_load_2d(dst + x0 * KV_TILE, kv ? &mv : &mk, x0, row, &full[slot]);
-                            }
-                    }
-                    __syncwarp();
+                const uint32_t valid = (there >> ((y * np) & 31)) & ((1u << np) - 1u);
+                if (act) {
+                    meta[slot].valid = valid;
+                    *(volatile uint32_t *)&meta[slot].round = round;
                 }
-                if (!dead) n += count;
+                int pg[4];
+#pragma unroll
+                for (int p = 0; p < 4; ++p) {
+                    const int from = (y * np + p) & 31;
+                    pg[p] = __shfl_sync(0xffffffffu, r0.page, from);
+                    const float k1 = __shfl_sync(0xffffffffu, r0.ks, from), v1 = __shfl_sync(0xffffffffu, r0.vs, from);
+                    if (act && p < np) meta[slot].sc[p] = kv ? v1 : k1;
+                }
+                if (act) {
+                    mbar_arrive_expect_tx(&full[slot], __popc(valid) * box_rows * D);
+                    const int k = r0.k + y, tile = k < r0.ns ? k : r0.w0 + k - r0.ns;
+#pragma unroll
+                    for (int p = 0; p < 4; ++p)
+                        if (p < np && ((valid >> p) & 1u)) {
+                            const int row = (pg[p] * c.hkv + r0.h) * P + ((tile * KV_TILE + p * box_rows) & (P - 1));
+                            uint8_t *dst = ring + (size_t)slot * C::SLOT + p * box_rows * (D < 128 ? D : 128);
+#pragma unroll
+                            for (int x0 = 0; x0 < D; x0 += 128)
+                                tma_load_2d(dst + x0 * KV_TILE, kv ? &mv : &mk, x0, row, &full[slot]);
+                        }
+                }
+                __syncwarp();
             }
-            t += g.k1 - g.k0;
+            if (!dead) n += count;
+            r0 = r1;
+            r1 = r2;
         }
         if (dead && lane == 0) {   // nothing may land after the CTA is gone: the last copies of every slot (bounded)
             *(volatile int *)&s_dead = 1;
