@@ -28,6 +28,9 @@
 
 namespace pi {
 
+// What an item costs besides its tiles, in tiles (measured: ragged 16 x 8k d5120 139 us at 4, 136 at 8, 185 without).
+constexpr int SPLIT_ITEM = 8;
+
 // QN: runs of 8 rows per tile; T: 16-bit terms.
 template <int D, int QN, int T>
 struct SplitCfg {
@@ -37,7 +40,7 @@ struct SplitCfg {
     static constexpr bool FLOW = !WIDE;
     static constexpr int R = 8 * QN;                     // rows per tile
     static constexpr int SLOT = KV_TILE * D;             // bytes of one K or V tile
-    static constexpr int JT = FLOW ? 128 : NW * 32;      // threads that join
+    static constexpr int JT = FLOW ? (11 - NW) * 32 : NW * 32;   // threads that join
     static constexpr int NT = (NW + 1) * 32 + (FLOW ? JT : 0);
     static constexpr int NM = FLOW ? 2 : 1;              // buffers of the warps' results
     static constexpr int MERGE = NW * R * (D + 4) * 4;   // bytes of one: numerators of every warp
@@ -57,6 +60,9 @@ struct SplitMeta {   // of one ring slot
 
 struct Seg {
     int i, h, rt, k0, k1, nt;
+    long long first;   // step of the item's first tile
+    // the step after the last of its tiles that the CTA takes (or would)
+    __device__ __forceinline__ long long after() const { return first + k1; }
 };
 
 template <int D, int QN, int T>
@@ -118,7 +124,7 @@ __global__ void __launch_bounds__(SplitCfg<D, QN, T>::NT, 1)
             info[i] = make_int4(q.row, q.len, q.start, q.n);
             int w0, ns, nt;
             view(q.len, q.n, w0, ns, nt);
-            w = (((long long)q.n * G + R - 1) / R) * nt * c.hkv;
+            w = (((long long)q.n * G + R - 1) / R) * (nt + SPLIT_ITEM) * c.hkv;
         }
         long long inc = w;
 #pragma unroll
@@ -140,12 +146,13 @@ __global__ void __launch_bounds__(SplitCfg<D, QN, T>::NT, 1)
     if (tid == 0) prefix[a.b.n] = run;
     __syncthreads();
     const long long total = run;
-    // A CTA's share: equal shares over the grid, but a tile at least for every consumer warp.
-    const long long quota = max((total + gridDim.x - 1) / gridDim.x, (long long)NW);
+    // A CTA's share: equal shares over the grid, but a tile at least for every consumer warp. Shares are counted in
+    // steps: an item is SPLIT_ITEM steps of its own, and then a step for each tile.
+    const long long quota = max((total + gridDim.x - 1) / gridDim.x, (long long)(NW + SPLIT_ITEM));
     const long long t0 = quota * blockIdx.x, t1 = min(total, t0 + quota);
     if (t0 >= t1) return;
 
-    auto segment = [&](long long t) {   // the item that tile t belongs to, and its tiles up to t1
+    auto segment = [&](long long t) {   // the item that step t belongs to, and its tiles up to step t1
         int lo = 0, hi = a.b.n;
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
@@ -157,12 +164,13 @@ __global__ void __launch_bounds__(SplitCfg<D, QN, T>::NT, 1)
         const int4 f = info[lo];
         int w0, ns;
         view(f.y, f.w, w0, ns, s.nt);
-        const long long local = t - prefix[lo], item = local / s.nt;
+        const long long local = t - prefix[lo], item = local / (s.nt + SPLIT_ITEM);
         const int rts = (int)(((long long)f.w * G + R - 1) / R);
         s.h = (int)(item / rts);
         s.rt = (int)(item % rts);
-        s.k0 = (int)(local % s.nt);
-        s.k1 = (int)min((long long)s.nt, s.k0 + (t1 - t));
+        s.first = prefix[lo] + item * (s.nt + SPLIT_ITEM) + SPLIT_ITEM;
+        s.k0 = (int)max(t - s.first, 0ll);
+        s.k1 = (int)min((long long)s.nt, max(t1 - s.first, 0ll));   // (none: the share ends before the first tile)
         return s;
     };
     const int P = c.page, box_rows = min(P, KV_TILE), np = KV_TILE / box_rows;   // pages (boxes) per tile
@@ -186,7 +194,7 @@ __global__ void __launch_bounds__(SplitCfg<D, QN, T>::NT, 1)
                 view(f.y, f.w, seg.w0, seg.ns, nt);
                 seg.h = g.h, seg.k = g.k0, seg.k1 = g.k1, seg.row = f.x, seg.len = f.y;
                 seg.low = f.y - f.w - a.window + 1;
-                at += g.k1 - g.k0;
+                at = g.k0 < g.k1 ? g.after() : t1;
             }
             Run r = seg;
             r.k1 = min(seg.k1, seg.k + per);
@@ -268,17 +276,16 @@ __global__ void __launch_bounds__(SplitCfg<D, QN, T>::NT, 1)
         return;
     }
 
-    // Joins a segment (its first tile t, the CTA's n-th tile): the results of the warps that had tiles of it, in the
+    // Joins a segment (whose first tile is the CTA's n-th): the results of the warps that had tiles of it, in the
     // order of their tiles, by the JT threads `me`.
-    auto join = [&](const Seg &sg, long long t, uint32_t n, int buf, int me) {
+    auto join = [&](const Seg &sg, uint32_t n, int buf, int me) {
         auto sync = [&]() { bar_sync(2, C::JT); };
         float *const mg = merge + buf * (C::MERGE / 4), *const mm = ml + buf * ((NW + 1) * R * 2);
         float *const sums = mm + NW * R * 2;
         const int4 f = info[sg.i];
         const int row0 = sg.rt * R, rows = min(R, f.w * G - row0), count = sg.k1 - sg.k0, turn = n % NW;
         const bool cut = sg.k0 > 0 || sg.k1 < sg.nt;
-        const long long item0 = t - sg.k0;                                 // first tile of the item
-        const int ca = (int)(item0 / quota), cb = (int)((item0 + sg.nt - 1) / quota);
+        const int ca = (int)(sg.first / quota), cb = (int)((sg.first + sg.nt - 1) / quota);   // the item's CTAs
         const int part = (int)blockIdx.x == ca ? 2 * ca + 1 : 2 * (int)blockIdx.x;
         // per row: the warps' weights against the common maximum (in place of their own), the maximum and the sum
         const int np_w = min(count, NW);
@@ -373,15 +380,16 @@ __global__ void __launch_bounds__(SplitCfg<D, QN, T>::NT, 1)
         bool dead = false;
         for (long long t = t0; t < t1; ++number) {
             const Seg sg = segment(t);
+            if (sg.k0 >= sg.k1) break;
             if (!dead && !mbar_wait(&jfull[number & 1], (number >> 1) & 1)) {
                 dead = true;
                 set_status(c.status, ST_TIMEOUT);
             }
-            join(sg, t, n, number & 1, tid - (NW + 1) * 32);
+            join(sg, n, number & 1, tid - (NW + 1) * 32);
             bar_sync(2, C::JT);
             if (tid == (NW + 1) * 32) mbar_arrive(&jempty[number & 1]);
             n += sg.k1 - sg.k0;
-            t += sg.k1 - sg.k0;
+            t = sg.after();
         }
         return;
     }
@@ -425,6 +433,7 @@ __global__ void __launch_bounds__(SplitCfg<D, QN, T>::NT, 1)
     for (long long t = t0; t < t1;) {
         const Seg sg = segment(t);
         const int count = sg.k1 - sg.k0;
+        if (count <= 0) break;
         // this warp's first tile of the segment: the warps take the CTA's tiles in turn
         const int kw0 = sg.k0 + (int)((warp + NW - n0 % NW) % NW);
         ++number;
@@ -440,7 +449,7 @@ __global__ void __launch_bounds__(SplitCfg<D, QN, T>::NT, 1)
             buffer_free();
             if (lane == 0) mbar_arrive(&jfull[buf]);
             n0 += count;
-            t += count;
+            t = sg.after();
             continue;
         }
         const int4 f = info[sg.i];
@@ -765,11 +774,11 @@ __global__ void __launch_bounds__(SplitCfg<D, QN, T>::NT, 1)
             if (lane == 0) mbar_arrive(&jfull[buf]);
         } else {
             bar_sync(1, NW * 32);
-            join(sg, t, n0, 0, tid);
+            join(sg, n0, 0, tid);
             bar_sync(1, NW * 32);
         }
         n0 += count;
-        t += count;
+        t = sg.after();
     }
 }
 
