@@ -160,11 +160,19 @@ def _ptr(x):
     return x.data_ptr()
 
 
+_current_stream = None   # the current CUDA stream's handle, without building a torch.cuda.Stream
+
+
 def _stream(s):
     if s is None:
-        import torch
+        global _current_stream
+        if _current_stream is None:
+            import torch
 
-        return torch.cuda.current_stream().cuda_stream
+            torch.cuda.current_stream()   # initialises CUDA
+            raw, device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+            _current_stream = lambda: raw(device())
+        return _current_stream()
     if isinstance(s, int):
         return s
     return s.cuda_stream
@@ -443,36 +451,44 @@ def _act_dtype(x) -> int:
         raise PiError(PI_ERR_UNSUPPORTED, f"dtype {x.dtype}") from None
 
 
-def _i32(x, name, n=None):
-    """A call's index tensor: int32, contiguous, on the GPU (its values are checked by the kernels)."""
-    import torch
+_INT32 = None
 
-    if x.dtype is not torch.int32 or x.dim() != 1 or not x.is_contiguous() or not x.is_cuda:
+
+def _i32(x, name, n=None):
+    """A call's index tensor: int32, contiguous, on the GPU (its values are checked by the kernels). Its address."""
+    global _INT32
+    if _INT32 is None:
+        import torch
+
+        _INT32 = torch.int32
+    shape = x.shape
+    if x.dtype is not _INT32 or len(shape) != 1 or not x.is_cuda or (shape[0] > 1 and x.stride(0) != 1):
         raise ValueError(f"{name}: a contiguous 1-D int32 CUDA tensor")
-    if n is not None and x.shape[0] != n:
-        raise ValueError(f"{name}: {n} entries, got {x.shape[0]}")
-    return x
+    if n is not None and shape[0] != n:
+        raise ValueError(f"{name}: {n} entries, got {shape[0]}")
+    return x.data_ptr()
 
 
 def _token_rows(x, heads, dim, name):
     """Row stride of a [tokens, heads, dim] tensor whose rows lie [heads, dim] contiguous (a slice of a fused
     projection is fine)."""
-    if x.dim() != 3 or x.shape[1] != heads or x.shape[2] != dim or not x.is_cuda:
-        raise ValueError(f"{name}: a [tokens, {heads}, {dim}] CUDA tensor, got {tuple(x.shape)}")
-    if x.stride(2) != 1 or (heads > 1 and x.stride(1) != dim):
+    shape = x.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != dim or not x.is_cuda:
+        raise ValueError(f"{name}: a [tokens, {heads}, {dim}] CUDA tensor, got {tuple(shape)}")
+    row, head, one = x.stride()
+    if one != 1 or (heads > 1 and head != dim):
         raise ValueError(f"{name}: the heads of a token lie next to each other")
-    return x.stride(0) if x.shape[0] > 1 else heads * dim
+    return row if shape[0] > 1 else heads * dim
 
 
-def _on(stream):
-    """Allocations inside belong to `stream` where it is a torch stream (else to the current one)."""
-    import contextlib
-
-    if stream is None or isinstance(stream, int):
-        return contextlib.nullcontext()
+def _empty(shape, dtype, device, stream):
+    """A new tensor that belongs to `stream` where that is a torch stream (else to the current one)."""
     import torch
 
-    return torch.cuda.stream(stream)
+    if stream is None or isinstance(stream, int):
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 class KVCache:
@@ -530,46 +546,43 @@ class KVCache:
 
     def reserve(self, seqs, tok_start, stream=None) -> None:
         """The sequences grow by their new tokens (lengths, pages)."""
-        n = _i32(seqs, "seqs").shape[0]
-        pi_kv_reserve(self.h, seqs, _i32(tok_start, "tok_start", n + 1), n, stream)
+        n = seqs.shape[0]
+        pi_kv_reserve(self.h, _i32(seqs, "seqs"), _i32(tok_start, "tok_start", n + 1), n, stream)
 
     def append(self, layer, seqs, tok_start, k_new, v_new, stream=None) -> None:
         """Keys and values [tokens, kv heads, dim] (fp32, bf16 or fp16) of the sequences' last positions."""
-        n = _i32(seqs, "seqs").shape[0]
+        n, T = seqs.shape[0], k_new.shape[0]
         ld = _token_rows(k_new, self.n_kv_heads, self.head_dim, "k_new")
         if _token_rows(v_new, self.n_kv_heads, self.head_dim, "v_new") != ld or v_new.dtype is not k_new.dtype or \
-                v_new.shape[0] != k_new.shape[0]:
+                v_new.shape[0] != T:
             raise ValueError("k_new and v_new: one shape, type and row stride")
-        pi_kv_append(self.h, layer, seqs, _i32(tok_start, "tok_start", n + 1), n, k_new.shape[0], k_new, v_new, ld,
-                     _act_dtype(k_new), stream)
+        pi_kv_append(self.h, layer, _i32(seqs, "seqs"), _i32(tok_start, "tok_start", n + 1), n, T, k_new.data_ptr(),
+                     v_new.data_ptr(), ld, _act_dtype(k_new), stream)
 
     def attend(self, layer, seqs, tok_start, q, out=None, lse=None, *, scale=None, window=0, sinks=0, stream=None):
         """Attention of q [tokens, heads, dim], the sequences' last positions, over their cache; returns out
         (q's type). window > 0: only the last `window` positions and the first `sinks` are seen. lse: fp32
         [tokens, heads], filled with the log of each row's sum of exponentials."""
-        import torch
-
-        n, T = _i32(seqs, "seqs").shape[0], q.shape[0]
-        ld = _token_rows(q, self.n_heads, self.head_dim, "q")
+        n, T, heads, dim = seqs.shape[0], q.shape[0], self.n_heads, self.head_dim
+        ld, dtype = _token_rows(q, heads, dim, "q"), _act_dtype(q)
         if out is None:
-            with _on(stream):
-                out = torch.empty((T, self.n_heads, self.head_dim), dtype=q.dtype, device=q.device)
-            ld_out = self.n_heads * self.head_dim
+            out, ld_out = _empty((T, heads, dim), q.dtype, q.device, stream), heads * dim
         else:
-            ld_out = _token_rows(out, self.n_heads, self.head_dim, "out")
+            ld_out = _token_rows(out, heads, dim, "out")
             if out.dtype is not q.dtype or out.shape[0] != T:
                 raise ValueError("out: q's type and number of tokens")
-        if lse is not None and (lse.dtype is not torch.float32 or tuple(lse.shape) != (T, self.n_heads) or
-                                not lse.is_contiguous()):
-            raise ValueError(f"lse: contiguous fp32 [{T}, {self.n_heads}]")
-        pi_kv_attend(self.h, layer, seqs, _i32(tok_start, "tok_start", n + 1), n, T, q, ld, out, ld_out, lse,
-                     _act_dtype(q), self.head_dim ** -0.5 if scale is None else scale, window, sinks, stream)
+        if lse is not None:
+            if _act_dtype(lse) != PI_F32 or tuple(lse.shape) != (T, heads) or not lse.is_contiguous():
+                raise ValueError(f"lse: contiguous fp32 [{T}, {heads}]")
+            lse = lse.data_ptr()
+        pi_kv_attend(self.h, layer, _i32(seqs, "seqs"), _i32(tok_start, "tok_start", n + 1), n, T, q.data_ptr(), ld,
+                     out.data_ptr(), ld_out, lse, dtype, dim ** -0.5 if scale is None else scale, window, sinks, stream)
         return out
 
     def fork(self, src, dst, stream=None) -> None:
         """dst[i] becomes a copy of sequence src[i] that shares its full pages."""
-        n = _i32(src, "src").shape[0]
-        pi_kv_fork(self.h, src, _i32(dst, "dst", n), n, stream)
+        n = src.shape[0]
+        pi_kv_fork(self.h, _i32(src, "src"), _i32(dst, "dst", n), n, stream)
 
     def free(self, seqs, stream=None) -> None:
         """Give back the sequences' pages."""
@@ -581,16 +594,13 @@ class KVCache:
 
     def copy_pages(self, src, dst, stream=None) -> None:
         """Copy pages src[i] to dst[i] in every layer (table and counts stay)."""
-        n = _i32(src, "src").shape[0]
-        pi_kv_copy_pages(self.h, src, _i32(dst, "dst", n), n, stream)
+        n = src.shape[0]
+        pi_kv_copy_pages(self.h, _i32(src, "src"), _i32(dst, "dst", n), n, stream)
 
     def compact(self, stream=None):
         """Move the used pages to the lowest ids; returns their number (int32 [1], on the GPU)."""
-        import torch
-
-        with _on(stream):
-            live = torch.empty(1, dtype=torch.int32, device=self.ref.device)
-        pi_kv_compact(self.h, live, stream)
+        live = _empty(1, self.ref.dtype, self.ref.device, stream)
+        pi_kv_compact(self.h, live.data_ptr(), stream)
         return live
 
     def status(self) -> int:
