@@ -299,7 +299,7 @@ pi_status_t pi_kv_append(pi_kv_t *h, int32_t layer, const int32_t *seqs, const i
     if ((s = check_rows(h, k_new, n_tokens, width, ld, es))) return s;
     if ((s = check_rows(h, v_new, n_tokens, width, ld, es))) return s;
     return cuda_status(launch_kv_append(h->view, {seqs, tok_start, n, n_tokens}, h->layers[layer], k_new, v_new, ld,
-                                        dtype, (cudaStream_t)stream));
+                                        dtype, h->nsm, (cudaStream_t)stream));
 }
 
 pi_status_t pi_kv_attend(pi_kv_t *h, int32_t layer, const int32_t *seqs, const int32_t *tok_start, int32_t n,

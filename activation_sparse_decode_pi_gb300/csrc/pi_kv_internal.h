@@ -82,7 +82,7 @@ PI_KV_EXTERN(128, 2) PI_KV_EXTERN(256, 1) PI_KV_EXTERN(256, 2)
 #undef PI_KV_EXTERN
 
 cudaError_t launch_kv_append(const KvView &c, const KvBatch &b, const KvLayerDev &l, const void *k_new,
-                             const void *v_new, int64_t ld, int dtype, cudaStream_t s);
+                             const void *v_new, int64_t ld, int dtype, int nsm, cudaStream_t s);
 
 struct KvCopyList {
     int32_t *src, *dst, *count;   // device; count: one int32
