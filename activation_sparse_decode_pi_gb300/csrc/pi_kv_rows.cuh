@@ -270,8 +270,8 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
 
     if (!mine) {
         // ------------------------------------------------------------ loaders
-        // All four warps convert. The first also asks for codes, the second describes the tiles: page ids are
-        // loaded a step before they are looked at, scales another step before they are used.
+        // All four warps convert. The first also asks for keys, the second describes the tiles, the third asks for
+        // values: page ids are loaded a step before they are looked at, scales another step before they are used.
         const int lt = tid - C::RT, role = warp - C::RT / 32;
         const int page_shift = __ffs(P) - 1, ppt = max(1, TOK >> page_shift);   // pages per tile
         const int box_rows = min(P, KV_TILE), box_shift = __ffs(box_rows) - 1, boxes = TOK >> box_shift;
@@ -399,7 +399,7 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
         for (int i = -3; i < nt; ++i) {
             int pid2 = -1, raw3 = UNSEEN;
             float ks2 = 0.f, vs2 = 0.f;
-            if (role < 2) {
+            if (role < 3) {
                 pid2 = clean(raw2);
                 if (role == 1) {
                     if (pid2 < 0 && raw2 != UNSEEN) set_status(c.status, ST_DEVICE_CHECK);   // seen, but absent
@@ -418,7 +418,7 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
                 convert(off_k + b * C::KV_BYTES, r, &kfull[b]);
                 fetch(1, i, r);
             }
-            if (role == 0 && next) request(1, i + 1, pid1);
+            if (role == 2 && next) request(1, i + 1, pid1);
             if (i >= 0) {
                 if (i >= NB) wait(&vempty[b], (i / NB - 1) & 1);
                 convert(off_v + b * C::KV_BYTES, r, &vfull[b]);
