@@ -499,13 +499,13 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
             wait(&kfull[b], (i / NB) & 1);
             const uint64_t k1 = dk + (uint32_t)(b * C::KV_BYTES / 16);
 #pragma unroll
-            for (int term = 0; term < QT; ++term)
+            for (int term = QT - 1; term >= 0; --term)   // (second terms first: sums are cut off, small ones lose less)
 #pragma unroll
                 for (int x = 0; x < D / 64; ++x)
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
                         umma_f16(ts, dq + (uint32_t)((term * C::Q_BYTES + x * 16384 + j * 32) / 16),
-                                 k1 + (uint32_t)((x * TOK * 128 + j * 32) / 16), ID_S, term + x + j > 0);
+                                 k1 + (uint32_t)((x * TOK * 128 + j * 32) / 16), ID_S, QT - 1 - term + x + j > 0);
             umma_commit(&bar_s[grp]);
             umma_commit(&kempty[b]);
             mbar_arrive(&bar_s[grp]);

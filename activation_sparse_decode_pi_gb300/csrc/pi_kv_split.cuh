@@ -48,6 +48,7 @@ struct SplitCfg {
     // query fragments in shared memory where they and the accumulators are too many for the registers
     static constexpr bool QS = STEPS * 2 * T * QN + D / 16 * QN * 4 > 160;
     static constexpr int QB = QS ? STEPS * QN * T * 32 * 8 : 0;
+    static constexpr bool FRESH = T == 2 && D / 16 * QN <= 8;   // fp32 accuracy, where registers allow
     static constexpr int MAX_SLOTS = 24;
 };
 
@@ -447,6 +448,7 @@ __global__ void __launch_bounds__(SplitCfg<D, QN, T>::NT, 1)
         };
         if (C::FLOW && kw0 >= sg.k1) {   // no tile of it is this warp's
             buffer_free();
+            __syncwarp();   // every lane has seen that phase: one that is left behind would take a later one for it
             if (lane == 0) mbar_arrive(&jfull[buf]);
             n0 += count;
             t = sg.after();
@@ -534,13 +536,18 @@ __global__ void __launch_bounds__(SplitCfg<D, QN, T>::NT, 1)
             const uint32_t valid = meta[ks_slot].valid;
             const bool whole = valid == (1u << np) - 1u && j0 + KV_TILE - 1 <= pos_lo &&
                                (pos_hi - j0 < a.window || j0 + KV_TILE <= a.sinks);
-            float s[QN][4][4];
+            // (T 2: second terms in sums of their own. The tensor cores cut sums off, each time by up to a unit of the
+            // sum's last place, so every product added to a large sum costs.)
+            float s[QN][4][4], s2[T == 2 ? QN : 1][4][4];
 #pragma unroll
             for (int rr = 0; rr < QN; ++rr)
 #pragma unroll
                 for (int t = 0; t < 4; ++t)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) s[rr][t][e] = 0.f;
+                    for (int e = 0; e < 4; ++e) {
+                        s[rr][t][e] = 0.f;
+                        if constexpr (T == 2) s2[rr][t][e] = 0.f;
+                    }
 #pragma unroll
             for (int ch = 0; ch < NCH; ++ch) {
 #pragma unroll
@@ -572,9 +579,10 @@ __global__ void __launch_bounds__(SplitCfg<D, QN, T>::NT, 1)
                             e4m3x4_f16x4(word4(kw[t][0], st), ka[0], ka[2]);
                             e4m3x4_f16x4(word4(kw[t][1], st), ka[1], ka[3]);
 #pragma unroll
-                            for (int rr = 0; rr < QN; ++rr)
-#pragma unroll
-                                for (int x = 0; x < T; ++x) mma_f16(s[rr][t2 + t], ka, qb[rr][x][0], qb[rr][x][1]);
+                            for (int rr = 0; rr < QN; ++rr) {
+                                mma_f16(s[rr][t2 + t], ka, qb[rr][0][0], qb[rr][0][1]);
+                                if constexpr (T == 2) mma_f16(s2[rr][t2 + t], ka, qb[rr][T - 1][0], qb[rr][T - 1][1]);
+                            }
                         }
                     }
                 }
@@ -601,8 +609,9 @@ __global__ void __launch_bounds__(SplitCfg<D, QN, T>::NT, 1)
                 for (int rr = 0; rr < QN; ++rr)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const float v = s[rr][t][e] * (qf[2 * rr + (e & 1)] * sc[t]);
-                        s[rr][t][e] = v;
+                        float v = s[rr][t][e];
+                        if constexpr (T == 2) v += s2[rr][t][e];
+                        s[rr][t][e] = v * (qf[2 * rr + (e & 1)] * sc[t]);
                     }
             if (!whole) {
 #pragma unroll
@@ -655,6 +664,16 @@ __global__ void __launch_bounds__(SplitCfg<D, QN, T>::NT, 1)
                     for (int j = 0; j < NJ; ++j)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) acc[rr][j][e] *= corr[2 * rr + (e & 1)] * shrink;
+            }
+            // FRESH: a tile's products in sums of their own, which are then added with rounding (see above)
+            float sum[C::FRESH ? QN : 1][NJ][4];
+            if constexpr (C::FRESH) {
+#pragma unroll
+                for (int rr = 0; rr < QN; ++rr)
+#pragma unroll
+                    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) sum[rr][j][e] = 0.f;
             }
 #pragma unroll
             for (int x = 0; x < QC; ++x) l[x] *= corr[x];
@@ -743,9 +762,20 @@ __global__ void __launch_bounds__(SplitCfg<D, QN, T>::NT, 1)
 #pragma unroll
                             for (int rr = 0; rr < QN; ++rr)
 #pragma unroll
-                                for (int x = 0; x < T; ++x) mma_f16(acc[rr][j], va, pb[rr][x][0], pb[rr][x][1]);
+                                for (int x = 0; x < T; ++x) {
+                                    if constexpr (C::FRESH) mma_f16(sum[rr][j], va, pb[rr][x][0], pb[rr][x][1]);
+                                    else mma_f16(acc[rr][j], va, pb[rr][x][0], pb[rr][x][1]);
+                                }
                         }
                 }
+            }
+            if constexpr (C::FRESH) {
+#pragma unroll
+                for (int rr = 0; rr < QN; ++rr)
+#pragma unroll
+                    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[rr][j][e] += sum[rr][j][e];
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[vs_slot]);

@@ -200,6 +200,24 @@ def test_attend_same_bits_every_time(P):
         assert torch.equal(b.cache.attend(0, *a, q), first)
 
 
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_attend_many_short_sequences(P, kind):
+    """Thousands of items of one to five tiles, call after call without a pause: every share is a chain of short
+    segments that some warps have no tile of. No wait may run out, and the bits stay the same."""
+    heads, seqs = 40, 85
+    lens = [3 + 7 * i % 299 for i in range(seqs)]
+    b = Both(P, hq=heads, hkv=heads, dim=128, page=32, n_pages=600, max_seqs=seqs, max_pages=10)
+    b.cache.reserve(*b.args(range(seqs), lens))
+    k = torch.randn(sum(lens), heads, 128, device="cuda", dtype=TYPES[kind])
+    b.cache.append(0, *b.args(range(seqs), lens), k, k.flip(0))
+    q = torch.randn(seqs, heads, 128, device="cuda", dtype=TYPES[kind])
+    a = b.args(range(seqs), [1] * seqs)
+    first = b.cache.attend(0, *a, q)
+    outs = [b.cache.attend(0, *a, q) for _ in range(300)]
+    assert b.cache.status() == 0
+    assert all(torch.equal(o, first) for o in outs)
+
+
 def test_attend_block_scales_far_apart(P):
     """Pages whose scales differ by many powers of two, and a page of zeros, in one sequence."""
     b = Both(P, hq=2, hkv=1, dim=128, page=16, n_pages=32, max_pages=16)
