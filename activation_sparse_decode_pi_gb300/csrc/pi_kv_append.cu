@@ -4,7 +4,9 @@
 // at most 448; x / s is then exact and the rounding to e4m3 the only one. W warps own one (page, head)
 // of K or V: they read the new rows once for their maximum and keep what fits in registers for the
 // codes, so the bytes of the new values bound it. One warp is enough for a decode step's single rows;
-// a prompt's whole pages take four, so that a page is one round of loads.
+// a prompt's whole pages take four, so that a page is one round of loads. Measured: 7 prompts of 1015..3351
+// tokens, 8 heads of 128, bf16 31 us = 3.0 TB/s (four warps; 52 us with one), bound by the latency of a page's
+// loads, maximum and stores; 64 single tokens of 40 heads, fp32 7.7 us, which is the host's time.
 #include <algorithm>
 
 #include "pi_async.cuh"

@@ -13,6 +13,9 @@
 // two threads to a row (a half of the tile's positions each: the softmax is latency-bound with fewer),
 // whose first warp issues its products; 4 more warps convert codes, which TMA brings a tile ahead,
 // into a ring of NB tiles.
+// Measured: four chunks of 707..1724 tokens over 2290..6425 positions, 32 heads on 8 of 128, bf16 341 us =
+// 954 TFLOP/s of the visible pairs (tensor pipe 42% active: the hand-offs between conversion, products and
+// softmax bound it); one prompt of 8191 in a window of 1000 + 70, 32 heads, fp16 276 us.
 // Rounding: as in pi_kv_split.cuh: q as f16 scaled per row by a power of two, weights as f16 in
 // units of 2^-7 of a reference that trails the running maximum by at most 2^8 (floor 2^-31 of the
 // row's largest weight). QT = 2 (fp32 output): a second f16 term of both.
