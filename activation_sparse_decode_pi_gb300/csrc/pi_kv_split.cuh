@@ -182,6 +182,25 @@ __global__ void __launch_bounds__(SplitCfg<D, QN, T>::NT, 1)
         s.k1 = (int)min((long long)s.nt, max(t1 - s.first, 0ll));   // (none: the share ends before the first tile)
         return s;
     };
+    auto following = [&](const Seg &p) {   // the next item, where p goes to the end of its own and ends before t1
+        Seg s = p;
+        const long long t = p.after();
+        s.first = t + SPLIT_ITEM;
+        if ((long long)++s.rt * R >= (long long)info[s.i].w * G) {
+            s.rt = 0;
+            if (++s.h == c.hkv) {
+                s.h = 0;
+                do ++s.i;
+                while (prefix[s.i + 1] <= t);   // (sequences without rows; prefix[n] >= t1 > t)
+                const int4 f = info[s.i];
+                int w0, ns;
+                view(f.y, f.w, w0, ns, s.nt);
+            }
+        }
+        s.k0 = 0;
+        s.k1 = (int)min((long long)s.nt, max(t1 - s.first, 0ll));
+        return s;
+    };
     const int P = c.page, box_rows = min(P, KV_TILE), np = KV_TILE / box_rows;   // pages (boxes) per tile
 
     if (warp == NW) {
@@ -194,10 +213,11 @@ __global__ void __launch_bounds__(SplitCfg<D, QN, T>::NT, 1)
         };
         const int per = 32 / np;
         long long at = t0;   // next segment
+        Seg g;
         Run seg{0, 0, 0, 0, 0, 0, 0, 0, -1, 0.f, 0.f};
         auto next = [&]() {   // the next run and its page ids; k >= k1 when there is none
             if (seg.k >= seg.k1 && at < t1) {
-                const Seg g = segment(at);
+                g = at == t0 ? segment(at) : following(g);
                 const int4 f = info[g.i];
                 int nt;
                 view(f.y, f.w, seg.w0, seg.ns, nt);
@@ -294,7 +314,8 @@ __global__ void __launch_bounds__(SplitCfg<D, QN, T>::NT, 1)
         const int4 f = info[sg.i];
         const int row0 = sg.rt * R, rows = min(R, f.w * G - row0), count = sg.k1 - sg.k0, turn = n % NW;
         const bool cut = sg.k0 > 0 || sg.k1 < sg.nt;
-        const int ca = (int)(sg.first / quota), cb = (int)((sg.first + sg.nt - 1) / quota);   // the item's CTAs
+        int ca = 0, cb = 0;   // the item's CTAs
+        if (cut) ca = (int)(sg.first / quota), cb = (int)((sg.first + sg.nt - 1) / quota);
         const int part = (int)blockIdx.x == ca ? 2 * ca + 1 : 2 * (int)blockIdx.x;
         // per row: the warps' weights against the common maximum (in place of their own), the maximum and the sum
         const int np_w = min(count, NW);
@@ -387,8 +408,9 @@ __global__ void __launch_bounds__(SplitCfg<D, QN, T>::NT, 1)
         uint32_t n = 0;
         int number = 0;
         bool dead = false;
+        Seg sg;
         for (long long t = t0; t < t1; ++number) {
-            const Seg sg = segment(t);
+            sg = t == t0 ? segment(t) : following(sg);
             if (sg.k0 >= sg.k1) break;
             if (!dead && !mbar_wait(&jfull[number & 1], (number >> 1) & 1)) {
                 dead = true;
@@ -439,8 +461,9 @@ __global__ void __launch_bounds__(SplitCfg<D, QN, T>::NT, 1)
     };
 
     int number = -1;   // of the segment
+    Seg sg;
     for (long long t = t0; t < t1;) {
-        const Seg sg = segment(t);
+        sg = t == t0 ? segment(t) : following(sg);
         const int count = sg.k1 - sg.k0;
         if (count <= 0) break;
         // this warp's first tile of the segment: the warps take the CTA's tiles in turn
