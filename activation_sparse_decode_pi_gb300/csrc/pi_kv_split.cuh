@@ -20,9 +20,10 @@
 //    joined by the last of them to finish, in the order of its parts (the same bits every time).
 // Measured (one token a sequence, 8 kv heads of 128 for 64 or 32 heads, bf16): 128 sequences of 129..16383
 // positions 327 us = 6.7 TB/s, 64 windows of 4096 + 4 positions 93 us, one sequence of 131067 56 us (start and
-// join ~15 us). fp32, 16 sequences of 1..8191, 40 heads: 162 us = 4.2 TB/s, bound by the consumer warps, whose
-// second terms double the products. Many items of 1 to 5 tiles (85 sequences, 40 heads): 176 us at a floor of
-// 22 us, since two items of a CTA at most are between their first product and their join.
+// join ~15 us). fp32, 16 sequences of 1..8191, 40 heads: 154 us = 4.5 TB/s, bound by the consumer warps, whose
+// second terms double the products. Many items of 1 to 5 tiles (85 sequences, 40 heads, fp32): 146 us at a floor of
+// 22 us, of which the joins are some 35 (left out to time the rest); two result slots to every warp, up to 8 items
+// between their first product and their join, gained nothing there and cost 5% on 128 x 300..1000.
 // Rounding: q is scaled by a power of two per row so that its largest value lies in [128, 256) and cut
 // to f16, weights are held as f16 in units of 2^-14 (floor 2^-38). T = 2: both keep a second f16 term
 // (22 bits, fp32 accuracy). T = 1 (bf16 output): 11 bits of the weight meet the output's 8.
@@ -42,12 +43,14 @@ template <int D, int QN, int T>
 struct SplitCfg {
     static constexpr bool WIDE = QN == 2 || D == 256;    // accumulators that leave no more than 8 warps on an SM
     static constexpr int NW = QN == 2 && D == 256 ? 4 : 7;   // consumer warps (and one producer)
-    // Where there is room, 4 more warps join the consumers' results of an item while these go on to the next one.
+    // Where there is room, 4 more warps join the consumers' results of an item while these go on to the next one: two
+    // to each of the two buffers, so that short items do not queue for one join, and all four to a cut item (85
+    // sequences of 1..300, 40 heads, fp32: 146 us, 153 with four to each; one of 131067: 56 us, 62 with two).
     static constexpr bool FLOW = !WIDE;
     static constexpr int R = 8 * QN;                     // rows per tile
     static constexpr int SLOT = KV_TILE * D;             // bytes of one K or V tile
-    static constexpr int JT = FLOW ? (11 - NW) * 32 : NW * 32;   // threads that join
-    static constexpr int NT = (NW + 1) * 32 + (FLOW ? JT : 0);
+    static constexpr int JT = FLOW ? 64 : NW * 32;       // threads that join an item
+    static constexpr int NT = (NW + 1) * 32 + (FLOW ? 2 * JT : 0);
     static constexpr int NM = FLOW ? 2 : 1;              // buffers of the warps' results
     static constexpr int MERGE = NW * R * (D + 4) * 4;   // bytes of one: numerators of every warp
     static constexpr int STEPS = D / 16;                 // 16-wide steps of the score's contraction
@@ -56,7 +59,8 @@ struct SplitCfg {
     static constexpr int QB = QS ? STEPS * QN * T * 32 * 8 : 0;
     static constexpr bool FRESH = T == 2 && D / 16 * QN <= 8;
     // ^ a tile's products in sums of their own, where registers allow: adding to a large sum inside the
-    // product loses low bits. 16 x 8k, 40 heads, fp32: error 5.6e-7 in 162 us, without 1.4e-6 in 136 us.
+    // product loses low bits. 16 x 8k, 40 heads, fp32: error 5.6e-7 in 162 us, without 1.4e-6 in 136 us
+    // (both before items were stepped through without searching: 154 us now).
     static constexpr int MAX_SLOTS = 24;
 };
 
@@ -93,7 +97,7 @@ __global__ void __launch_bounds__(SplitCfg<D, QN, T>::NT, 1)
     int4 *info = (int4 *)((uintptr_t)(prefix + a.b.n + 2) & ~(uintptr_t)15);   // [n] row, length, start, new tokens
     __shared__ long long wtot[C::NT / 32];
     __shared__ uint64_t jfull[2], jempty[2];   // results of a segment: written, joined
-    __shared__ int s_last, s_dead;
+    __shared__ int s_last[2], s_dead;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const KvView &c = a.c;
@@ -306,9 +310,9 @@ __global__ void __launch_bounds__(SplitCfg<D, QN, T>::NT, 1)
     }
 
     // Joins a segment (whose first tile is the CTA's n-th): the results of the warps that had tiles of it, in the
-    // order of their tiles, by the JT threads `me`.
-    auto join = [&](const Seg &sg, uint32_t n, int buf, int me) {
-        auto sync = [&]() { bar_sync(2, C::JT); };
+    // order of their tiles, by the `threads` threads `me`, which meet at barrier `bar`.
+    auto join = [&](const Seg &sg, uint32_t n, int buf, int me, int threads, int bar) {
+        auto sync = [&]() { bar_sync(bar, threads); };
         float *const mg = merge + buf * (C::MERGE / 4), *const mm = ml + buf * ((NW + 1) * R * 2);
         float *const sums = mm + NW * R * 2;
         const int4 f = info[sg.i];
@@ -332,7 +336,7 @@ __global__ void __launch_bounds__(SplitCfg<D, QN, T>::NT, 1)
             sums[me * 2 + 1] = S;
         }
         sync();
-        for (int x = me; x < rows * (D / 4); x += C::JT) {
+        for (int x = me; x < rows * (D / 4); x += threads) {
             const int r = x / (D / 4), d = (x % (D / 4)) * 4;
             const float M = sums[r * 2], S = sums[r * 2 + 1];
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -356,14 +360,14 @@ __global__ void __launch_bounds__(SplitCfg<D, QN, T>::NT, 1)
                 store_row(a, f, sg.h, G, D, row0 + r, d, o, M, S);
             }
         }
-        sync();
         if (!cut) return;
-        if (me == 0) s_last = ticket_acq_rel(&a.tickets[ca], 1u) == (uint32_t)(cb - ca);
         sync();
-        if (!s_last) return;
+        if (me == 0) s_last[buf] = ticket_acq_rel(&a.tickets[ca], 1u) == (uint32_t)(cb - ca);
+        sync();
+        if (!s_last[buf]) return;
         float *wt = mg;   // [parts][R] weights
         const int parts = cb - ca + 1;
-        for (int r = me / 32; r < rows; r += C::JT / 32) {
+        for (int r = me / 32; r < rows; r += threads / 32) {
             float M = -INFINITY;
             for (int x = lane; x < parts; x += 32) {
                 const int sl = x == 0 ? 2 * ca + 1 : 2 * (ca + x);
@@ -387,7 +391,7 @@ __global__ void __launch_bounds__(SplitCfg<D, QN, T>::NT, 1)
             }
         }
         sync();
-        for (int x = me; x < rows * (D / 4); x += C::JT) {
+        for (int x = me; x < rows * (D / 4); x += threads) {
             const int r = x / (D / 4), d = (x % (D / 4)) * 4;
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
@@ -405,6 +409,7 @@ __global__ void __launch_bounds__(SplitCfg<D, QN, T>::NT, 1)
 
     if (C::FLOW && warp > NW) {
         // ------------------------------------------------------------ joiners
+        const int own = (warp - NW - 1) / 2;   // buffer of this pair of warps
         uint32_t n = 0;
         int number = 0;
         bool dead = false;
@@ -412,13 +417,21 @@ __global__ void __launch_bounds__(SplitCfg<D, QN, T>::NT, 1)
         for (long long t = t0; t < t1; ++number) {
             sg = t == t0 ? segment(t) : following(sg);
             if (sg.k0 >= sg.k1) break;
-            if (!dead && !mbar_wait(&jfull[number & 1], (number >> 1) & 1)) {
-                dead = true;
-                set_status(c.status, ST_TIMEOUT);
+            // A cut item is the first or the last of the share, and on the way to the call's end: every joiner's. (The
+            // pair of the other buffer has seen the segment before, so it cannot take an older phase for this one's.)
+            const bool all = sg.k0 > 0 || sg.k1 < sg.nt;
+            const int b = number & 1;
+            if (all || b == own) {
+                if (!dead && !mbar_wait(&jfull[b], (number >> 1) & 1)) {
+                    dead = true;
+                    set_status(c.status, ST_TIMEOUT);
+                }
+                const int me = tid - (NW + 1) * 32 - (all ? 0 : own * C::JT);
+                const int threads = all ? 2 * C::JT : C::JT, bar = all ? 4 : 2 + own;
+                join(sg, n, b, me, threads, bar);
+                bar_sync(bar, threads);
+                if (me == 0) mbar_arrive(&jempty[b]);
             }
-            join(sg, n, number & 1, tid - (NW + 1) * 32);
-            bar_sync(2, C::JT);
-            if (tid == (NW + 1) * 32) mbar_arrive(&jempty[number & 1]);
             n += sg.k1 - sg.k0;
             t = sg.after();
         }
@@ -835,7 +848,7 @@ __global__ void __launch_bounds__(SplitCfg<D, QN, T>::NT, 1)
             if (lane == 0) mbar_arrive(&jfull[buf]);
         } else {
             bar_sync(1, NW * 32);
-            join(sg, n0, 0, tid);
+            join(sg, n0, 0, tid, C::JT, 2);
             bar_sync(1, NW * 32);
         }
         n0 += count;
