@@ -456,10 +456,12 @@ __global__ void __launch_bounds__(SplitCfg<D, QN, T>::NT, 1)
     uint32_t n0 = 0;
     bool dead = false;
     float inv = 0.f;   // 2^14 / unit of the item
-    // A warp may come to a slot two fillings early (there are about as many warps as slots for two tiles each), and
-    // parity tells a phase from its neighbours only: the filling is right when the producer's count says so too.
+    // A warp may come to a slot while an earlier filling is on its way (most do where the ring has fewer slots than
+    // the warps' tiles), and parity tells a phase from its neighbours only. So the producer's count is read first: it
+    // reaches `round` after phase round - 1 has completed, and phase round + 1 cannot complete before this warp has
+    // released the slot, so a parity read after it is that of `round` or of the phase under way.
     auto filled = [&](uint32_t slot, uint32_t round) {
-        return mbar_try_wait(&full[slot], round & 1) && *(volatile uint32_t *)&meta[slot].round == round;
+        return *(volatile uint32_t *)&meta[slot].round == round && mbar_try_wait(&full[slot], round & 1);
     };
     auto wait_full = [&](uint32_t slot, uint32_t round) {
         if (dead || filled(slot, round)) return;

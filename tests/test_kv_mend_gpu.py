@@ -1,0 +1,118 @@
+"""Attention over the paged 8-bit cache where hand-offs between warps, tiles and kernels count: against a plain form in
+64 bits on the same codes, every (token, head) row by its own error.
+
+Tolerances (relative L2 error of a row). Output: bf16 rounds by at most 2^-8 of a value, fp16 by 2^-11. Weights of 16-bit
+types are f16: 2^-11 / sqrt(3) of each on average, and over the 64 or more columns of a row that is 2.8e-4 of it; four
+times that for rows that fall badly. fp32: terms of 22 bits, but the tensor cores cut sums off by up to 2^-23 of them at
+every addition: 32 additions into a score of up to 10 and some 200 into an output, 6.4e-5 together.
+"""
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+ROW_TOL = {"f32": 1e-4, "bf16": 2.0 ** -8 + 1.2e-3, "f16": 2.0 ** -11 + 1.2e-3}
+TYPES = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+
+
+@pytest.fixture(scope="module")
+def P():
+    import activation_sparse_decode_pi_gb300 as P
+
+    return P
+
+
+def dev(a, dtype=torch.int32):
+    return torch.tensor(np.asarray(a), device="cuda").to(dtype)
+
+
+def starts(new):
+    return dev(np.concatenate([[0], np.cumsum(new)]))
+
+
+class Filled:
+    """A cache whose pages were filled with random codes and scales, in shuffled order."""
+
+    def __init__(self, P, lens, *, hq, hkv, dim, page, seed=0, spread=2):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        cols = [-(-n // page) for n in lens]
+        n_pages = sum(cols) + 3
+        self.lens, self.hq, self.hkv, self.dim, self.page = lens, hq, hkv, dim, page
+
+        def pool():
+            x = torch.randn((n_pages, hkv, page, dim), generator=g, device="cuda").mul_(64).clamp_(-448, 448)
+            s = torch.exp2(torch.randint(-7, -6 + spread, (n_pages, hkv), generator=g, device="cuda").float())
+            return x.to(torch.float8_e4m3fn), s
+        self.k, self.ks = pool()
+        self.v, self.vs = pool()
+        order = torch.randperm(n_pages, generator=g, device="cuda").to(torch.int32)
+        self.table = torch.full((len(lens), max(cols)), -1, dtype=torch.int32, device="cuda")
+        at = 0
+        for i, c in enumerate(cols):
+            self.table[i, :c] = order[at:at + c]
+            at += c
+        ref = torch.zeros(n_pages, dtype=torch.int32, device="cuda")
+        ref[order[:at].long()] = 1
+        self.g = g
+        self.cache = P.KVCache([dict(k=self.k, v=self.v, k_scale=self.ks, v_scale=self.vs)], self.table, dev(lens), ref,
+                               n_heads=hq)
+
+    def queries(self, new, kind):
+        return torch.randn((int(sum(new)), self.hq, self.dim), generator=self.g, device="cuda").to(TYPES[kind])
+
+    def attend(self, new, q, **kw):
+        return self.cache.attend(0, dev(range(len(self.lens))), starts(new), q, **kw)
+
+    def exact(self, new, q, window=0, sinks=0):
+        """(out, lse) in fp64 from the definition, a sequence and kv head at a time."""
+        out = torch.zeros(q.shape, dtype=torch.float64, device="cuda")
+        lse = torch.full(q.shape[:2], -torch.inf, dtype=torch.float64, device="cuda")
+        G, row = self.hq // self.hkv, 0
+        for i, (total, m) in enumerate(zip(self.lens, new)):
+            if m == 0:
+                continue
+            j = torch.arange(total, device="cuda")
+            page = self.table[i].long()[j // self.page]
+            pos = torch.arange(total - m, total, device="cuda")[:, None]
+            see = j[None] <= pos
+            if window > 0:
+                see &= (pos - j[None] < window) | (j[None] < sinks)
+            for h in range(self.hkv):
+                k, v = ((x.view(torch.uint8)[page, h, j % self.page].view(torch.float8_e4m3fn).double()
+                         * s[page, h].double()[:, None]) for x, s in ((self.k, self.ks), (self.v, self.vs)))
+                x = q[row:row + m, h * G:(h + 1) * G].double()
+                x = torch.einsum("tgd,kd->tgk", x, k) * self.dim ** -0.5
+                x = x.masked_fill(~see[:, None], -torch.inf)
+                lse[row:row + m, h * G:(h + 1) * G] = torch.logsumexp(x, -1)
+                p = torch.exp(x - x.amax(-1, keepdim=True).clamp(min=-1e300)).nan_to_num(0.0)
+                z = p.sum(-1, keepdim=True)
+                out[row:row + m, h * G:(h + 1) * G] = torch.einsum("tgk,kd->tgd", p, v) / torch.where(z > 0, z, 1.0)
+            row += m
+        return out, lse
+
+    def check(self, new, kind, window=0, sinks=0, repeat=0):
+        q = self.queries(new, kind)
+        lse = torch.empty(q.shape[:2], device="cuda")
+        got = self.attend(new, q, lse=lse, window=window, sinks=sinks)
+        want, want_lse = self.exact(new, q, window, sinks)
+        err = (got.double() - want).norm(dim=-1) / want.norm(dim=-1).clamp(min=1e-300)
+        assert self.cache.status() == 0
+        bad = torch.nonzero(~(err <= ROW_TOL[kind]))
+        assert bad.numel() == 0, (len(bad), err.max().item(), bad[:8].tolist())
+        assert torch.allclose(lse.double(), want_lse, rtol=1e-5, atol=5e-5)
+        outs = [self.attend(new, q, window=window, sinks=sinks) for _ in range(repeat)]
+        assert self.cache.status() == 0
+        assert all(torch.equal(o, got) for o in outs)
+
+
+# ------------------------------------------------------------------------------------------------ few rows
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("group", [1, 16])
+def test_few_rows_ring_shorter_than_the_warps_tiles(P, kind, group):
+    """Head dim 256: the ring has 8 to 10 slots, fewer than two for each consumer warp, so that warps wait for a slot's
+    next filling while an earlier one is on its way. Many short items and some long ones, call after call."""
+    lens = [3 + 37 * i % 700 for i in range(70)] + [9001]
+    f = Filled(P, lens, hq=4 * group, hkv=4, dim=256, page=32)
+    f.check([1] * len(lens), kind, repeat=100)
