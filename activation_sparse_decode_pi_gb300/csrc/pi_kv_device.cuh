@@ -3,7 +3,7 @@
 
 #include <cuda_bf16.h>
 
-#include "pi_common.cuh"
+#include "pi_async.cuh"
 #include "pi_kv_internal.h"
 
 namespace pi {
@@ -42,6 +42,15 @@ template <bool B>
 struct Const {
     static constexpr bool value = B;
 };
+
+// ---------------------------------------------------------------- waiting -------------------
+
+// mbar_wait by a whole warp, whose lanes leave it together and with one answer: a lane leaves its own polling loop when it
+// has seen the phase, and what follows a wait (tcgen05, mma.sync, movmatrix, bar.sync) takes the warp as one.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity)
+{
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity));
+}
 
 // ---------------------------------------------------------------- e4m3 ----------------------
 

@@ -255,8 +255,14 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
         fence_mbar_init();
     }
     if (warp == 0) tmem_alloc(&taddr_s, C::TCOLS);
-    bool dead = false;
-    auto wait = [&](uint64_t *bar, uint32_t parity) {
+    bool dead = false;   // the same in all lanes of a warp
+    auto wait = [&](uint64_t *bar, uint32_t parity) {   // by the whole warp
+        if (!dead && !warp_wait(bar, parity)) {
+            dead = true;
+            set_status(c.status, ST_TIMEOUT);
+        }
+    };
+    auto wait_alone = [&](uint64_t *bar, uint32_t parity) {   // by one thread, which shares `dead` with its warp afterwards
         if (!dead && !mbar_wait(bar, parity)) {
             dead = true;
             set_status(c.status, ST_TIMEOUT);
@@ -499,7 +505,7 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
         const uint64_t dk = sw128_desc(base + off_k, 16u, 1024u), dv = sw128_desc(base + off_v, TOK * 128u, 1024u);
         auto issue_s = [&](int i) {   // S = Q K^T of tile i
             const int b = i & (NB - 1);
-            wait(&kfull[b], (i / NB) & 1);
+            wait_alone(&kfull[b], (i / NB) & 1);
             const uint64_t k1 = dk + (uint32_t)(b * C::KV_BYTES / 16);
 #pragma unroll
             for (int term = QT - 1; term >= 0; --term)   // (second terms first: sums are cut off, small ones lose less)
@@ -515,7 +521,7 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
         };
         auto issue_o = [&](int i) {   // O += P V
             const int b = i & (NB - 1);
-            wait(&vfull[b], (i / NB) & 1);
+            wait_alone(&vfull[b], (i / NB) & 1);
             const uint64_t v1 = dv + (uint32_t)(b * C::KV_BYTES / 16);
 #pragma unroll
             for (int term = 0; term < QT; ++term)
@@ -528,7 +534,7 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
         };
         const bool issues = (warp & 7) == 0;
         if (nt > 0 && issues && elect_one()) issue_s(0);
-        __syncwarp();
+        dead = __any_sync(0xffffffffu, dead);
         constexpr int HC = TOK / 2;   // positions of the tile that this thread takes
         const uint32_t my_s = ts + lane_base + half * HC, my_p = ts + lane_base + half * (HC / 2);
         for (int i = 0; i < nt; ++i) {
@@ -616,7 +622,7 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
                 issue_o(i);
                 if (i + 1 < nt) issue_s(i + 1);
             }
-            __syncwarp();
+            dead = __any_sync(0xffffffffu, dead);
         }
         if (nt > 0) wait(&bar_o[grp], 0);
         tc_fence_after();

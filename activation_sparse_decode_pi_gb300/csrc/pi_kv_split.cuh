@@ -312,7 +312,10 @@ __global__ void __launch_bounds__(SplitCfg<D, QN, T>::NT, 1)
     // Joins a segment (whose first tile is the CTA's n-th): the results of the warps that had tiles of it, in the
     // order of their tiles, by the `threads` threads `me`, which meet at barrier `bar`.
     auto join = [&](const Seg &sg, uint32_t n, int buf, int me, int threads, int bar) {
-        auto sync = [&]() { bar_sync(bar, threads); };
+        auto sync = [&]() {
+            __syncwarp();   // (a warp's lanes come from loops of different lengths)
+            bar_sync(bar, threads);
+        };
         float *const mg = merge + buf * (C::MERGE / 4), *const mm = ml + buf * ((NW + 1) * R * 2);
         float *const sums = mm + NW * R * 2;
         const int4 f = info[sg.i];
@@ -422,7 +425,7 @@ __global__ void __launch_bounds__(SplitCfg<D, QN, T>::NT, 1)
             const bool all = sg.k0 > 0 || sg.k1 < sg.nt;
             const int b = number & 1;
             if (all || b == own) {
-                if (!dead && !mbar_wait(&jfull[b], (number >> 1) & 1)) {
+                if (!dead && !warp_wait(&jfull[b], (number >> 1) & 1)) {
                     dead = true;
                     set_status(c.status, ST_TIMEOUT);
                 }
@@ -464,15 +467,18 @@ __global__ void __launch_bounds__(SplitCfg<D, QN, T>::NT, 1)
         return *(volatile uint32_t *)&meta[slot].round == round && mbar_try_wait(&full[slot], round & 1);
     };
     auto wait_full = [&](uint32_t slot, uint32_t round) {
-        if (dead || filled(slot, round)) return;
-        const unsigned long long since = globaltimer_ns();
-        while (!filled(slot, round))
-            if (globaltimer_ns() - since > WAIT_LIMIT_NS) {
-                dead = true;
-                *(volatile int *)&s_dead = 1;
-                set_status(c.status, ST_TIMEOUT);
-                break;
-            }
+        if (dead) return;
+        bool ok = filled(slot, round);
+        if (!ok) {
+            const unsigned long long since = globaltimer_ns();
+            while (!(ok = filled(slot, round)))
+                if (globaltimer_ns() - since > WAIT_LIMIT_NS) break;
+        }
+        if (!__all_sync(0xffffffffu, ok)) {   // (the warp leaves as one, as from warp_wait)
+            dead = true;
+            *(volatile int *)&s_dead = 1;
+            set_status(c.status, ST_TIMEOUT);
+        }
     };
 
     int number = -1;   // of the segment
@@ -486,15 +492,14 @@ __global__ void __launch_bounds__(SplitCfg<D, QN, T>::NT, 1)
         ++number;
         const int buf = C::FLOW ? number & 1 : 0;
         auto buffer_free = [&]() {   // the results of the segment before the last have left it
-            if (C::FLOW && number > 1 && !dead && !mbar_wait(&jempty[buf], ((number >> 1) - 1) & 1)) {
+            if (C::FLOW && number > 1 && !dead && !warp_wait(&jempty[buf], ((number >> 1) - 1) & 1)) {
                 dead = true;
                 *(volatile int *)&s_dead = 1;
                 set_status(c.status, ST_TIMEOUT);
             }
         };
         if (C::FLOW && kw0 >= sg.k1) {   // no tile of it is this warp's
-            buffer_free();
-            __syncwarp();   // every lane has seen that phase: one that is left behind would take a later one for it
+            buffer_free();   // (every lane has seen that phase: one left behind could take a later one for it)
             if (lane == 0) mbar_arrive(&jfull[buf]);
             n0 += count;
             t = sg.after();

@@ -116,3 +116,32 @@ def test_few_rows_ring_shorter_than_the_warps_tiles(P, kind, group):
     lens = [3 + 37 * i % 700 for i in range(70)] + [9001]
     f = Filled(P, lens, hq=4 * group, hkv=4, dim=256, page=32)
     f.check([1] * len(lens), kind, repeat=100)
+
+
+# ------------------------------------------------------------------------------------------------ prompts
+
+LONG = [1750, 903, 37, 1290]
+CHUNKS = [1700, 903, 30, 260]
+PROMPTS = [   # group, kv heads, dim, page
+    (1, 24, 64, 16), (5, 4, 64, 64), (2, 8, 64, 128), (1, 24, 128, 32), (4, 8, 128, 16), (8, 3, 128, 128),
+    (1, 16, 256, 32), (3, 5, 256, 128), (16, 2, 128, 64), (16, 1, 256, 64),
+]
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("group,hkv,dim,page", PROMPTS)
+def test_prompt_rows_one_by_one(P, group, hkv, dim, page, kind):
+    """Ragged prompts of many tiles and several waves of CTAs, whole and under windows: every row, and 50 calls bit for
+    bit."""
+    f = Filled(P, LONG, hq=group * hkv, hkv=hkv, dim=dim, page=page)
+    f.check(CHUNKS, kind, repeat=50)
+    f.check([700, 1, 37, 1290], kind, window=333, sinks=70, repeat=10)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("dim,page", [(64, 32), (128, 64), (256, 16)])
+def test_short_prompt_over_a_long_cache(P, dim, page, kind):
+    """Few items: each one's cache is split over CTAs, and the last of them joins the parts."""
+    f = Filled(P, [6007, 129], hq=6, hkv=2, dim=dim, page=page)
+    f.check([61, 129], kind, repeat=50)
+    f.check([150, 0], kind, window=3000, sinks=200, repeat=10)
