@@ -641,12 +641,14 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
                 tmem_ld32(to + lane_base + x, o);
                 tmem_wait_ld(o);
             }
-            if (!on) continue;
-            float f[32];   // l = 0: nothing seen (a NaN sum stays: it is not equal to 0)
+            if (on) {
+                float f[32];   // l = 0: nothing seen (a NaN sum stays: it is not equal to 0)
 #pragma unroll
-            for (int e = 0; e < 32; ++e) f[e] = nt == 0 || l == 0.f ? 0.f : __uint_as_float(o[e]) * norm;
-            if (splits > 1) store_f32<32>(a.rows_part + at * D + x, f);
-            else store_out<32>(a, at_out + x, f);
+                for (int e = 0; e < 32; ++e) f[e] = nt == 0 || l == 0.f ? 0.f : __uint_as_float(o[e]) * norm;
+                if (splits > 1) store_f32<32>(a.rows_part + at * D + x, f);
+                else store_out<32>(a, at_out + x, f);
+            }
+            __syncwarp();   // the next load of tensor memory takes the whole warp, lanes past the last row too
         }
         if (splits == 1 && on && half == 0 && a.lse)
             a.lse[((int64_t)sq.start + (row0 + row) / G) * c.hq + h * G + (row0 + row) % G] = row_lse(m, l);

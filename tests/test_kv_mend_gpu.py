@@ -145,3 +145,12 @@ def test_short_prompt_over_a_long_cache(P, dim, page, kind):
     f = Filled(P, [6007, 129], hq=6, hkv=2, dim=dim, page=page)
     f.check([61, 129], kind, repeat=50)
     f.check([150, 0], kind, window=3000, sinks=200, repeat=10)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_prompts_that_end_inside_a_warp(P, dim, kind):
+    """Every count of rows in the last warp: its lanes past the end take part in the loads of the results."""
+    new = [34 + i for i in range(33)] + [129, 257, 287]
+    f = Filled(P, [n + 7 * i % 50 for i, n in enumerate(new)], hq=2, hkv=2, dim=dim, page=16)
+    f.check(new, kind, repeat=10)
