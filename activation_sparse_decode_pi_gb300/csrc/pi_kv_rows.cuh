@@ -36,7 +36,13 @@ struct RowsCfg {
     static constexpr int Q_BYTES = 128 * D * 2, KV_BYTES = TOK * D * 2;
     static constexpr int STAGE = TOK * D;                       // bytes of the codes of one tile
     static constexpr int DATA = NG * QT * Q_BYTES + 2 * NB * KV_BYTES + 2 * STAGE;
-    static constexpr int TCOLS = 512;                           // per group: S (TOK columns) and O (D columns)
+    // Tensor memory, per group: S (TOK columns), O (D) and, where there is room, P (two 16-bit weights to a column).
+    // The tensor cores keep products in their order only where these go to one accumulator in one shape. So the next
+    // tile's S is not written over weights that P V may still read: P has columns of its own (APART), or S waits until
+    // P V is done (head dim 128, 16-bit types).
+    static constexpr int TCOLS = 512, PCOLS = QT * TOK / 2;
+    static constexpr bool APART = NG * (TOK + D + PCOLS) <= TCOLS;
+    static constexpr int GCOLS = TOK + D + (APART ? PCOLS : 0);
 };
 
 constexpr float ROWS_TRAIL = 8.f;   // base-2 growth of the maximum that is taken up without rescaling
@@ -135,7 +141,7 @@ __device__ __forceinline__ float lg2(float x)
 
 template <int ROWS, int NW>
 struct RowsShared {
-    uint64_t bar_s[2], bar_o[2], kfull[2], kempty[2], vfull[2], vempty[2], sfull[2], sempty[2];
+    uint64_t bar_s[2], bar_p[2], bar_o[2], kfull[2], kempty[2], vfull[2], vempty[2], sfull[2], sempty[2];
     RowsMeta meta[4];
     float half[2][ROWS];   // what the two threads of a row tell each other
     int item[4], wsum[NW], nan, last;
@@ -169,7 +175,7 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
         return;
     }
     RowsShared<C::ROWS, NW> &sh = *(RowsShared<C::ROWS, NW> *)(dsm + C::DATA);
-    auto &bar_s = sh.bar_s, &bar_o = sh.bar_o, &kfull = sh.kfull, &kempty = sh.kempty, &vfull = sh.vfull,
+    auto &bar_s = sh.bar_s, &bar_p = sh.bar_p, &bar_o = sh.bar_o, &kfull = sh.kfull, &kempty = sh.kempty, &vfull = sh.vfull,
          &vempty = sh.vempty, &sfull = sh.sfull, &sempty = sh.sempty;
     auto &meta = sh.meta;
     auto &s_half = sh.half;
@@ -244,6 +250,7 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
     if (tid == 0) {
         for (int x = 0; x < 2; ++x) {
             mbar_init(&bar_s[x], 2);   // the product, and what its issuer has seen of the loaders' (the tile's description)
+            mbar_init(&bar_p[x], 1);
             mbar_init(&bar_o[x], 1);
             mbar_init(&kfull[x], C::LOADERS / 32);
             mbar_init(&vfull[x], C::LOADERS / 32);
@@ -442,7 +449,7 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
     // ---------------------------------------------------------------- softmax
     float m = -INFINITY, l = 0.f, unit = 0.f;
     const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
-    const uint32_t ts = tmem + grp * (TOK + D), to = ts + TOK;
+    const uint32_t ts = tmem + grp * C::GCOLS, to = ts + TOK, tp = C::APART ? to + D : ts;
     if (mine && grp < groups) {
         // ------------------------------------------------------------ queries: half a row to a thread
         float qf;
@@ -506,6 +513,10 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
         auto issue_s = [&](int i) {   // S = Q K^T of tile i
             const int b = i & (NB - 1);
             wait_alone(&kfull[b], (i / NB) & 1);
+            if constexpr (!C::APART) {   // the last tile's P V has read the weights
+                if (i > 0) wait_alone(&bar_p[grp], (i - 1) & 1);
+                tc_fence_after();
+            }
             const uint64_t k1 = dk + (uint32_t)(b * C::KV_BYTES / 16);
 #pragma unroll
             for (int term = QT - 1; term >= 0; --term)   // (second terms first: sums are cut off, small ones lose less)
@@ -527,8 +538,9 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
             for (int term = 0; term < QT; ++term)
 #pragma unroll
                 for (int j = 0; j < TOK / 16; ++j)
-                    umma_f16_ts(to, ts + term * (TOK / 2) + j * 8, v1 + (uint32_t)(j * 2048 / 16), ID_O,
+                    umma_f16_ts(to, tp + term * (TOK / 2) + j * 8, v1 + (uint32_t)(j * 2048 / 16), ID_O,
                                 i > 0 || term + j > 0);
+            if constexpr (!C::APART) umma_commit(&bar_p[grp]);
             umma_commit(&vempty[b]);
             if (i + 1 == nt) umma_commit(&bar_o[grp]);
         };
@@ -536,7 +548,7 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
         if (nt > 0 && issues && elect_one()) issue_s(0);
         dead = __any_sync(0xffffffffu, dead);
         constexpr int HC = TOK / 2;   // positions of the tile that this thread takes
-        const uint32_t my_s = ts + lane_base + half * HC, my_p = ts + lane_base + half * (HC / 2);
+        const uint32_t my_s = ts + lane_base + half * HC, my_p = tp + lane_base + half * (HC / 2);
         for (int i = 0; i < nt; ++i) {
             wait(&bar_s[grp], i & 1);
             tc_fence_after();
@@ -569,7 +581,9 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
                 top = fmaxf(top, fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * factor[x]);
             }
             s_half[half][row] = top;
+            tc_fence_before();
             bar_sync(2 + grp, 256);   // also: every score of the group's tile has been read
+            tc_fence_after();
             top = fmaxf(top, s_half[half ^ 1][row]);
             // the reference is raised when the maximum has outrun it; O follows it and the unit of the values
             float shrink = mt.shrink;
@@ -608,7 +622,7 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
                     else r[e / 2] = pack_f16(w.x, w.y);
                 }
                 l = fmaf(sum.x + sum.y, mt.vback[half * (HC / 16) + x], l);
-                // The weights take the place of the scores: first terms in columns [0, TOK / 2), second ones behind.
+                // Weights: first terms in columns [0, TOK / 2) of P, second ones behind.
                 if (x & 1) {
                     tmem_st16(my_p + (x / 2) * 16, r + (x / 2) * 16);
                     if constexpr (QT == 2) tmem_st16(my_p + TOK / 2 + (x / 2) * 16, plo + (x / 2) * 16);

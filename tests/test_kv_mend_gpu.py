@@ -154,3 +154,11 @@ def test_prompts_that_end_inside_a_warp(P, dim, kind):
     new = [34 + i for i in range(33)] + [129, 257, 287]
     f = Filled(P, [n + 7 * i % 50 for i, n in enumerate(new)], hq=2, hkv=2, dim=dim, page=16)
     f.check(new, kind, repeat=10)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_prompt_weights_are_not_written_over(P, dim, kind):
+    """Hundreds of tiles in a row for each CTA: the next tile's scores never reach weights that are still being read."""
+    f = Filled(P, [12000, 11000], hq=32, hkv=32, dim=dim, page=64)
+    f.check([256, 513], kind, repeat=100)
