@@ -4,7 +4,7 @@
 Tolerances (relative L2 error of a row). Output: bf16 rounds by at most 2^-8 of a value, fp16 by 2^-11. Weights of 16-bit
 types are f16: 2^-11 / sqrt(3) of each on average, and over the 64 or more columns of a row that is 2.8e-4 of it; four
 times that for rows that fall badly. fp32: terms of 22 bits, but the tensor cores cut sums off by up to 2^-23 of them at
-every addition: 32 additions into a score of up to 10 and some 200 into an output, 6.4e-5 together.
+every addition: 32 additions into a score of up to 10 (3.8e-5), and one for each 8 positions into an output.
 """
 import numpy as np
 import pytest
@@ -12,7 +12,7 @@ import torch
 
 pytestmark = pytest.mark.gpu
 
-ROW_TOL = {"f32": 1e-4, "bf16": 2.0 ** -8 + 1.2e-3, "f16": 2.0 ** -11 + 1.2e-3}
+ROW_TOL = {"f32": 3.8e-5, "bf16": 2.0 ** -8 + 1.2e-3, "f16": 2.0 ** -11 + 1.2e-3}
 TYPES = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
 
 
@@ -98,7 +98,7 @@ class Filled:
         want, want_lse = self.exact(new, q, window, sinks)
         err = (got.double() - want).norm(dim=-1) / want.norm(dim=-1).clamp(min=1e-300)
         assert self.cache.status() == 0
-        bad = torch.nonzero(~(err <= ROW_TOL[kind]))
+        bad = torch.nonzero(~(err <= ROW_TOL[kind] + max(self.lens) / 8 * 2.0 ** -23))
         assert bad.numel() == 0, (len(bad), err.max().item(), bad[:8].tolist())
         assert torch.allclose(lse.double(), want_lse, rtol=1e-5, atol=5e-5)
         outs = [self.attend(new, q, window=window, sinks=sinks) for _ in range(repeat)]
