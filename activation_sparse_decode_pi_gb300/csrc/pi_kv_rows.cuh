@@ -141,7 +141,7 @@ __device__ __forceinline__ float lg2(float x)
 
 template <int ROWS, int NW>
 struct RowsShared {
-    uint64_t bar_s[2], bar_p[2], bar_o[2], kfull[2], kempty[2], vfull[2], vempty[2], sfull[2], sempty[2];
+    uint64_t bar_s[2], bar_p[2], bar_o[2], drain[2], kfull[2], kempty[2], vfull[2], vempty[2], sfull[2], sempty[2];
     RowsMeta meta[4];
     float half[2][ROWS];   // what the two threads of a row tell each other
     int item[4], wsum[NW], nan, last;
@@ -252,6 +252,7 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
             mbar_init(&bar_s[x], 2);   // the product, and what its issuer has seen of the loaders' (the tile's description)
             mbar_init(&bar_p[x], 1);
             mbar_init(&bar_o[x], 1);
+            mbar_init(&sh.drain[x], 1);
             mbar_init(&kfull[x], C::LOADERS / 32);
             mbar_init(&vfull[x], C::LOADERS / 32);
             mbar_init(&sfull[x], x == 0 ? 2 : 1);   // keys: their bytes, and the tile's description
@@ -262,6 +263,8 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
         fence_mbar_init();
     }
     if (warp == 0) tmem_alloc(&taddr_s, C::TCOLS);
+    // A warp whose wait has run out asks for no more copies and issues no more products, waits (again bounded) for those
+    // that it has under way, and goes through the CTA's barriers to the end, where the tensor memory is freed.
     bool dead = false;   // the same in all lanes of a warp
     auto wait = [&](uint64_t *bar, uint32_t parity) {   // by the whole warp
         if (!dead && !warp_wait(bar, parity)) {
@@ -301,11 +304,14 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
         };
         auto clean = [&](int pid) { return (unsigned)pid < (unsigned)c.n_pages ? pid : -1; };
         // Codes of tile i (kv 0: keys, 1: values) into their stage. Absent pages are left out.
+        int asked = -1;   // last tile whose codes this warp has asked for
         auto request = [&](int kv, int i, int pid) {
             const int page = __shfl_sync(0xffffffffu, pid, lane < boxes ? (lane << box_shift) >> pshift : 0);
             const bool go = lane < boxes && page >= 0;
             const uint32_t n = __popc(__ballot_sync(0xffffffffu, go));
             if (i > 0) wait(&sempty[kv], (i - 1) & 1);   // the loaders have read the last tile's
+            if (dead) return;
+            asked = i;
             if (lane == 0) mbar_arrive_expect_tx(&sfull[kv], n * box_rows * D);
             __syncwarp();
             if (go) {
@@ -354,6 +360,7 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
         const int tr = lt / 4, ch = lt % 4, odd = NBLK > 1 ? tr & 1 : 0;
         auto fetch = [&](int kv, int i, uint4 (&r)[NV]) {
             wait(&sfull[kv], i & 1);
+            if (dead) return;
             const uint8_t *st = gq + off_st + kv * C::STAGE;
 #pragma unroll
             for (int y = 0; y < TOK / RPY; ++y)
@@ -426,17 +433,21 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
             const bool next = i >= -1 && i + 1 < nt;
             const int b = i & (NB - 1);
             if (i >= 0) fetch(0, i, r);
+            if (dead) break;
             // (arrivals for the next tile's keys: only after this tile's phase, which fetch has waited for)
             if (role == 0 && next) request(0, i + 1, pid1);
             if (role == 1 && next) describe(i + 1, pid1, ks1, vs1);
             if (i >= 0) {
                 if (i >= NB) wait(&kempty[b], (i / NB - 1) & 1);   // the product that read the tile's place before
+                if (dead) break;
                 convert(off_k + b * C::KV_BYTES, r, &kfull[b]);
                 fetch(1, i, r);
+                if (dead) break;
             }
             if (role == 2 && next) request(1, i + 1, pid1);
             if (i >= 0) {
                 if (i >= NB) wait(&vempty[b], (i / NB - 1) & 1);
+                if (dead) break;
                 convert(off_v + b * C::KV_BYTES, r, &vfull[b]);
             }
             pid1 = pid2;
@@ -444,6 +455,7 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
             ks1 = ks2;
             vs1 = vs2;
         }
+        if (dead && asked >= 0) warp_wait(&sfull[role >> 1], asked & 1);
     }
 
     // ---------------------------------------------------------------- softmax
@@ -517,6 +529,7 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
                 if (i > 0) wait_alone(&bar_p[grp], (i - 1) & 1);
                 tc_fence_after();
             }
+            if (dead) return;
             const uint64_t k1 = dk + (uint32_t)(b * C::KV_BYTES / 16);
 #pragma unroll
             for (int term = QT - 1; term >= 0; --term)   // (second terms first: sums are cut off, small ones lose less)
@@ -533,6 +546,7 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
         auto issue_o = [&](int i) {   // O += P V
             const int b = i & (NB - 1);
             wait_alone(&vfull[b], (i / NB) & 1);
+            if (dead) return;
             const uint64_t v1 = dv + (uint32_t)(b * C::KV_BYTES / 16);
 #pragma unroll
             for (int term = 0; term < QT; ++term)
@@ -639,6 +653,13 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
             dead = __any_sync(0xffffffffu, dead);
         }
         if (nt > 0) wait(&bar_o[grp], 0);
+        if (dead && issues) {
+            if (elect_one()) {
+                umma_commit(&sh.drain[grp]);
+                mbar_wait(&sh.drain[grp], 0);
+            }
+            __syncwarp();
+        }
         tc_fence_after();
 
         // ------------------------------------------------------------ output
