@@ -194,7 +194,6 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
     }
     __syncthreads();
     pdl_wait();
-    pdl_launch_dependents();
 
     // the blockIdx.x-th item of the call: sequence, kv head, run of ROWS rows (the last rows, which see most, first)
     {
@@ -286,6 +285,9 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = taddr_s;
+    // Only now: a CTA of the next kernel that shares the SM may take tensor memory before it waits for this one
+    // (k_tc does), and the allocation above would then wait for it in turn.
+    pdl_launch_dependents();
 
     if (!mine) {
         // ------------------------------------------------------------ loaders

@@ -162,3 +162,25 @@ def test_prompt_weights_are_not_written_over(P, dim, kind):
     """Hundreds of tiles in a row for each CTA: the next tile's scores never reach weights that are still being read."""
     f = Filled(P, [12000, 11000], hq=32, hkv=32, dim=dim, page=64)
     f.check([256, 513], kind, repeat=100)
+
+
+def test_prompt_attention_right_before_the_tensor_core_ffn(P):
+    """The predictor's kernel starts while the attention's last CTAs run, and takes tensor memory before it waits."""
+    from workload import WORKLOADS, make_layer, scaled
+
+    w = scaled(WORKLOADS["relullama7b_d4096_f11008_bf16_L32"], d=1024, f=2752, r=128, n_layers=1)
+    ffn = P.SparseFFN.from_workload(w, [P.apply_hot_first(make_layer(w, 0, 0, device="cuda"))[0]], max_batch=64)
+    u = torch.randn(64, 1024, device="cuda")
+    idx, count = ffn.predict(0, u)
+    for dim in (64, 128, 256):
+        f = Filled(P, [900, 700], hq=8, hkv=8, dim=dim, page=64)
+        q = f.queries([800, 700], "f16")
+        want = f.attend([800, 700], q)
+        for _ in range(30):
+            got = f.attend([800, 700], q)
+            idx2, count2 = ffn.predict(0, u)
+            n = int(count)
+            assert torch.equal(got, want) and int(count2) == n and torch.equal(idx2[:n], idx[:n])
+        assert f.cache.status() == 0
+    assert ffn.status() == 0
+    ffn.close()
