@@ -234,7 +234,8 @@ pi_status_t check_batch(const pi_kv_t *h, const int32_t *seqs, const int32_t *st
 // [n_tokens x width] elements of es bytes, rows ld elements apart, all on 16-byte boundaries.
 pi_status_t check_rows(const pi_kv_t *h, const void *p, int64_t n_tokens, int64_t width, int64_t ld, int es)
 {
-    if (ld < width || ld > ((int64_t)1 << 40) || (ld * es) % 16) return PI_ERR_INVALID_ARG;
+    // (rows beyond any memory first: (n_tokens - 1) * ld * es has to stay a 64-bit number)
+    if (ld < width || ld > ((int64_t)1 << 60) / n_tokens || (ld * es) % 16) return PI_ERR_INVALID_ARG;
     return check_ptr(p, (size_t)(((n_tokens - 1) * ld + width) * es), 16, h->dev);
 }
 

@@ -184,3 +184,23 @@ def test_prompt_attention_right_before_the_tensor_core_ffn(P):
         assert f.cache.status() == 0
     assert ffn.status() == 0
     ffn.close()
+
+
+# ------------------------------------------------------------------------------------------------ refusals
+
+def test_row_strides_whose_extent_passes_64_bits(P):
+    """2^30 rows of 2^34 (or 2^40) fp32 elements: their extent is 0 modulo 2^64. (The one sequence has no new token, so
+    that nothing is read even if the call is taken.)"""
+    f = Filled(P, [40], hq=2, hkv=2, dim=64, page=16)
+    seqs, start = dev([0]), dev([0, 0])
+    q = torch.zeros((1, 2, 64), device="cuda")
+    for ld in (1 << 34, 1 << 40):
+        for n in ((1 << 30) - 1, 1 << 30):
+            for a, b in ((ld, 128), (128, ld), (ld, ld)):
+                with pytest.raises(P.PiError) as e:
+                    P.pi_kv_attend(f.cache.h, 0, seqs, start, 1, n, q, a, q, b, None, P.PI_F32, 0.1)
+                assert e.value.code == P.PI_ERR_INVALID_ARG
+            with pytest.raises(P.PiError) as e:
+                P.pi_kv_append(f.cache.h, 0, seqs, start, 1, n, q, q, ld, P.PI_F32)
+            assert e.value.code == P.PI_ERR_INVALID_ARG
+    assert f.cache.status() == 0
