@@ -482,11 +482,14 @@ def _token_rows(x, heads, dim, name):
 
 
 def _empty(shape, dtype, device, stream):
-    """A new tensor that belongs to `stream` where that is a torch stream (else to the current one)."""
+    """A new tensor that belongs to `stream` (a torch stream or a handle; None: the current one), so that memory which
+    work on another stream may still use is not taken for it."""
     import torch
 
-    if stream is None or isinstance(stream, int):
+    if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=device)
 

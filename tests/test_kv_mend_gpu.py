@@ -204,3 +204,33 @@ def test_row_strides_whose_extent_passes_64_bits(P):
                 P.pi_kv_append(f.cache.h, 0, seqs, start, 1, n, q, q, ld, P.PI_F32)
             assert e.value.code == P.PI_ERR_INVALID_ARG
     assert f.cache.status() == 0
+
+
+# ------------------------------------------------------------------------------------------------ streams
+
+def test_results_belong_to_the_stream_of_the_call(P):
+    """Memory freed on one stream (whose work may still use it) is not handed to a call on another, given as a torch
+    stream or as a handle."""
+    f = Filled(P, [300], hq=8, hkv=8, dim=64, page=16)
+    q = f.queries([300], "f32")
+    want = f.attend([300], q)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for stream in (side, side.cuda_stream):
+        freed = torch.empty_like(q)
+        at = freed.data_ptr()
+        del freed                                                # the current stream's next block of this size
+        out = f.attend([300], q, stream=stream)
+        assert out.data_ptr() != at
+        side.synchronize()
+        assert torch.equal(out, want)
+        del out
+        assert f.cache.compact(stream=stream).data_ptr() != torch.empty(1, dtype=torch.int32, device="cuda").data_ptr()
+    with torch.cuda.stream(side):                                # the default stream's handle is 0
+        freed = torch.empty_like(q)
+        at = freed.data_ptr()
+        del freed
+        out = f.attend([300], q, stream=0)
+        assert out.data_ptr() != at
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and f.cache.status() == 0
