@@ -373,6 +373,7 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
                                             : (bb >> 1) * TOK * 128 + tr * 128 + ((((bb & 1) * 4 + ch) ^ (tr & 7)) << 4);
                     r[y * NBLK + b] = *(const uint4 *)(st + off + y * RPY * (D < 128 ? D : 128));
                 }
+            fence_proxy_async_smem();   // the next copy into the stage comes after these loads
             __syncwarp();
             if (lane == 0) mbar_arrive(&sempty[kv]);
             if (meta[i & 3].whole) return;

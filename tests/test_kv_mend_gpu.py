@@ -234,3 +234,12 @@ def test_results_belong_to_the_stream_of_the_call(P):
         assert out.data_ptr() != at
     torch.cuda.synchronize()
     assert torch.equal(out, want) and f.cache.status() == 0
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_prompt_codes_are_read_before_the_next_copy_lands(P, dim, page, kind):
+    """Short parts of a split cache, where the next tile's copy follows at once on the loads of the last."""
+    f = Filled(P, [6007], hq=6, hkv=2, dim=dim, page=page)
+    f.check([61], kind, repeat=200)
