@@ -648,8 +648,11 @@ __global__ void __launch_bounds__(SplitCfg<D, QN, T>::NT, 1)
                 }
             };
             run_scales(ks_slot);
+            // Every lane has read its keys and their scales, and the slot's next copy (by TMA, past the order of ordinary
+            // loads) comes after that.
+            fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&empty[ks_slot]);   // every lane has read its keys and their scales
+            if (lane == 0) mbar_arrive(&empty[ks_slot]);
             // ---- to base-2 logits; what a row does not see is -infinity
             float top[QC];
 #pragma unroll
@@ -758,7 +761,6 @@ __global__ void __launch_bounds__(SplitCfg<D, QN, T>::NT, 1)
                     for (int x = lane; x < C::SLOT; x += 32)
                         if ((vt[x] & 0x7f) == 0x7f) vt[x] = 0;
                 }
-                fence_proxy_async_smem();   // the slot's next copy comes after these stores
                 __syncwarp();
             }
             // ---- weights, and their products with the values, 16 positions at a time
@@ -828,6 +830,7 @@ __global__ void __launch_bounds__(SplitCfg<D, QN, T>::NT, 1)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) acc[rr][j][e] += sum[rr][j][e];
             }
+            fence_proxy_async_smem();   // the slot's next copy comes after the loads (and what was cleared)
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[vs_slot]);
         }

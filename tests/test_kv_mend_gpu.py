@@ -243,3 +243,11 @@ def test_prompt_codes_are_read_before_the_next_copy_lands(P, dim, page, kind):
     """Short parts of a split cache, where the next tile's copy follows at once on the loads of the last."""
     f = Filled(P, [6007], hq=6, hkv=2, dim=dim, page=page)
     f.check([61], kind, repeat=200)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("dim,group", [(64, 1), (64, 16), (128, 1), (128, 16), (256, 1), (256, 16)])
+def test_few_rows_codes_are_read_before_the_next_copy_lands(P, dim, group, kind):
+    """Single tokens over caches of many rounds of the ring, call after call bit for bit."""
+    f = Filled(P, [9000 + 501 * i for i in range(12)], hq=4 * group, hkv=4, dim=dim, page=64)
+    f.check([1] * 12, kind, repeat=200)
