@@ -458,7 +458,7 @@ __global__ void __launch_bounds__(SplitCfg<D, QN, T>::NT, 1)
     const int page_shift = __ffs(box_rows) - 1;
     uint32_t n0 = 0;
     bool dead = false;
-    float inv = 0.f;   // 2^14 / unit of the item
+    float inv = 0.f;   // 1 / unit of the item
     // A warp may come to a slot while an earlier filling is on its way (most do where the ring has fewer slots than
     // the warps' tiles), and parity tells a phase from its neighbours only. So the producer's count is read first: it
     // reaches `round` after phase round - 1 has completed, and phase round + 1 cannot complete before this warp has
@@ -707,9 +707,11 @@ __global__ void __launch_bounds__(SplitCfg<D, QN, T>::NT, 1)
             // numerators are kept in units of the largest value scale so far
             float shrink = 1.f;
             if (vmax > unit) {
-                shrink = unit / vmax;
-                unit = vmax;
-                inv = 16384.f / unit;
+                // (an append gives zeros the scale 2^-120: the unit's reciprocal has to be finite, and 2^14 stays out of it)
+                const float up = fmaxf(vmax, 0x1p-126f);
+                shrink = unit / up;
+                unit = up;
+                inv = 1.f / unit;
             }
             if (__any_sync(0xffffffffu, grew) || shrink != 1.f) {
 #pragma unroll
@@ -770,7 +772,7 @@ __global__ void __launch_bounds__(SplitCfg<D, QN, T>::NT, 1)
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
                 uint32_t pb[QN][T][2];   // positions 2 q, 2 q + 1 (and 8 on) of row g: the scores' fragment transposed
-                const float vs = sc[t] * inv;
+                const float vs = sc[t] * inv * 16384.f;
 #pragma unroll
                 for (int rr = 0; rr < QN; ++rr)
 #pragma unroll
@@ -837,7 +839,6 @@ __global__ void __launch_bounds__(SplitCfg<D, QN, T>::NT, 1)
         // ---- the warp's results, for the join
         buffer_free();
         float *const mg = merge + buf * (C::MERGE / 4), *const mm = ml + buf * ((NW + 1) * R * 2);
-        const float back = unit * (1.f / 16384.f);
 #pragma unroll
         for (int x = 0; x < QC; ++x) {
             const int r = 8 * (x >> 1) + 2 * q + (x & 1);
@@ -851,7 +852,7 @@ __global__ void __launch_bounds__(SplitCfg<D, QN, T>::NT, 1)
 #pragma unroll
             for (int j = 0; j < NJ; ++j)
                 *(float2 *)&mg[(warp * R + r) * (D + 4) + out_col<D>(j, g, 0)] =
-                    make_float2(acc[x >> 1][j][x & 1] * back, acc[x >> 1][j][2 + (x & 1)] * back);
+                    make_float2(acc[x >> 1][j][x & 1] * 0x1p-14f * unit, acc[x >> 1][j][2 + (x & 1)] * 0x1p-14f * unit);
         }
         if constexpr (C::FLOW) {
             __syncwarp();

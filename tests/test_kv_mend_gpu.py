@@ -78,6 +78,7 @@ class Filled:
             see = j[None] <= pos
             if window > 0:
                 see &= (pos - j[None] < window) | (j[None] < sinks)
+            see &= page[None] >= 0
             for h in range(self.hkv):
                 k, v = ((x.view(torch.uint8)[page, h, j % self.page].view(torch.float8_e4m3fn).double()
                          * s[page, h].double()[:, None]) for x, s in ((self.k, self.ks), (self.v, self.vs)))
@@ -251,3 +252,42 @@ def test_few_rows_codes_are_read_before_the_next_copy_lands(P, dim, group, kind)
     """Single tokens over caches of many rounds of the ring, call after call bit for bit."""
     f = Filled(P, [9000 + 501 * i for i in range(12)], hq=4 * group, hkv=4, dim=dim, page=64)
     f.check([1] * 12, kind, repeat=200)
+
+
+# ------------------------------------------------------------------------------------------------ values of any size
+
+SIZES = [(64, 16, 1), (64, 64, 12), (128, 32, 3), (128, 64, 16), (256, 16, 1), (256, 128, 9)]   # dim, page, group
+
+
+def zero_positions(f, seq, p0, p1):
+    """Values of zero at positions [p0, p1) of a sequence, whole pages of them as an append leaves them."""
+    for c in range(p0 // f.page, p1 // f.page):
+        f.v.view(torch.uint8)[f.table[seq, c].long()] = 0
+        f.vs[f.table[seq, c].long()] = 2.0 ** -120
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("dim,page,group", SIZES)
+def test_a_cache_of_zero_values(P, dim, page, group, kind):
+    """Every value zero, appended as such: outputs of zero, and the logs of the sums as ever."""
+    lens = [300, 64, 1100]
+    f = Filled(P, lens, hq=2 * group, hkv=2, dim=dim, page=page)
+    x = torch.randn((sum(lens), 2, dim), device="cuda")
+    f.cache.append(0, dev(range(3)), starts(lens), x, torch.zeros_like(x))
+    assert (f.vs[f.table[0, 0].long()] == 2.0 ** -120).all()
+    for new in ([1, 1, 1], [2, 1, 1], [300, 64, 1100]):
+        f.check(new, kind)
+        f.check(new, kind, window=100, sinks=3)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("dim,page,group", SIZES)
+def test_tiles_of_zero_values_among_others(P, dim, page, group, kind):
+    """64, 128 and 512 zero positions before, between and behind others."""
+    lens = [3000, 704, 1024, 1536]
+    f = Filled(P, lens, hq=2 * group, hkv=2, dim=dim, page=page)
+    for seq, p0, p1 in ((0, 0, 128), (0, 1024, 1536), (1, 0, 640), (2, 512, 1024), (3, 256, 384), (3, 1024, 1152)):
+        zero_positions(f, seq, p0, p1)
+    for new in ([1, 1, 1, 1], [3, 0, 2, 1], [700, 600, 1024, 90]):
+        f.check(new, kind)
+        f.check(new, kind, window=900, sinks=130)
