@@ -669,7 +669,8 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
         s_half[half][row] = l;
         bar_sync(2 + grp, 256);
         l += s_half[half ^ 1][row];
-        const float back = unit * exp2i(-(int)ROWS_UNIT), norm = splits > 1 ? back : l == 0.f ? 0.f : back / l;
+        // (the unit, which may be as small as an append's 2^-120, is multiplied in by itself: its quotient would lose bits)
+        const float back = exp2i(-(int)ROWS_UNIT), norm = splits > 1 ? back : l == 0.f ? 0.f : back / l;
         const int64_t at = ((int64_t)blockIdx.x * splits + blockIdx.y) * C::ROWS + row;
         const int64_t at_out = ((int64_t)sq.start + (row0 + row) / G) * a.ldo + (int64_t)(h * G + (row0 + row) % G) * D;
 #pragma unroll 1
@@ -682,7 +683,7 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
             if (on) {
                 float f[32];   // l = 0: nothing seen (a NaN sum stays: it is not equal to 0)
 #pragma unroll
-                for (int e = 0; e < 32; ++e) f[e] = nt == 0 || l == 0.f ? 0.f : __uint_as_float(o[e]) * norm;
+                for (int e = 0; e < 32; ++e) f[e] = nt == 0 || l == 0.f ? 0.f : __uint_as_float(o[e]) * norm * unit;
                 if (splits > 1) store_f32<32>(a.rows_part + at * D + x, f);
                 else store_out<32>(a, at_out + x, f);
             }

@@ -291,3 +291,14 @@ def test_tiles_of_zero_values_among_others(P, dim, page, group, kind):
     for new in ([1, 1, 1, 1], [3, 0, 2, 1], [700, 600, 1024, 90]):
         f.check(new, kind)
         f.check(new, kind, window=900, sinks=130)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("dim,page,group", SIZES)
+@pytest.mark.parametrize("low", [-120, -115, -113])
+def test_values_of_the_smallest_scales(P, dim, page, group, kind, low):
+    f = Filled(P, [900, 517], hq=2 * group, hkv=2, dim=dim, page=page)
+    f.vs.fill_(2.0 ** low)
+    f.vs[f.table[0, 3:5].long()] = 2.0 ** -120
+    for new in ([1, 1], [2, 1], [850, 517]):
+        f.check(new, kind)
