@@ -43,6 +43,9 @@ struct Const {
     static constexpr bool value = B;
 };
 
+// Whether a block scale is one: a number >= 0. A page in view without one is left out, as an absent page is.
+__device__ __forceinline__ bool is_scale(float s) { return s >= 0.f && s <= 3.402823466e38f; }
+
 // ---------------------------------------------------------------- waiting -------------------
 
 // mbar_wait by a whole warp, whose lanes leave it together and with one answer: a lane leaves its own polling loop when it

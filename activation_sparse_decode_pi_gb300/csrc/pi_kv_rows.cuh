@@ -334,11 +334,17 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
         float unit = 0.f;
         auto describe = [&](int i, int pid, float ks, float vs) {
             RowsMeta &m = meta[i & 3];
+            const bool ok = is_scale(ks) && is_scale(vs);
+            if (!ok) {
+                set_status(c.status, ST_DEVICE_CHECK);
+                ks = vs = 0.f;
+            }
             float top = vs;
 #pragma unroll
             for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
             top = fmaxf(unit, __shfl_sync(0xffffffffu, top, 0));
-            const uint32_t there = __ballot_sync(0xffffffffu, __shfl_sync(0xffffffffu, pid, (lane * 16) >> pshift) >= 0);
+            const int page = __shfl_sync(0xffffffffu, pid, (lane * 16) >> pshift);   // of the lane's run
+            const uint32_t there = __ballot_sync(0xffffffffu, ok && page >= 0);
             if (lane < TOK / 16) {
                 // below 2^-60 of the largest scale a page adds nothing either way; its weights still count in the sum
                 const float b = (vs > 0.f ? fmaxf(lg2(vs) - lg2(top), -60.f) : -60.f) + ROWS_UNIT;
@@ -741,7 +747,9 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
             if (pos - j >= a.window && j >= a.sinks) continue;
             const int page = c.table[(size_t)sq.row * c.max_pages + j / P];
             if (page < 0 || page >= c.n_pages) continue;
-            const uint32_t *v = (const uint32_t *)(a.l.v + (((size_t)page * c.hkv + h) * P + (j & (P - 1))) * D);
+            const size_t block = (size_t)page * c.hkv + h;
+            if (!is_scale(a.l.ks[block]) || !is_scale(a.l.vs[block])) continue;
+            const uint32_t *v = (const uint32_t *)(a.l.v + (block * P + (j & (P - 1))) * D);
             for (int w = 0; w < D / 4; ++w)
                 if (e4m3_any_nan(v[w]))
                     for (int b = 0; b < 4; ++b)

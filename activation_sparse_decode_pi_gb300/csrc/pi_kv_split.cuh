@@ -251,6 +251,11 @@ __global__ void __launch_bounds__(SplitCfg<D, QN, T>::NT, 1)
         while (r0.k < r0.k1 && !dead) {
             const Run r2 = next();
             scales(r1);
+            if (!is_scale(r0.ks) || !is_scale(r0.vs)) {   // (looked at no earlier: they were loaded a run ahead)
+                set_status(c.status, ST_DEVICE_CHECK);
+                r0.page = -1;
+                r0.ks = r0.vs = 0.f;
+            }
             // Four ring slots at a time, a lane to each: keys and values of two tiles.
             const uint32_t there = __ballot_sync(0xffffffffu, r0.page >= 0);
             const int count = r0.k1 - r0.k;

@@ -7,7 +7,7 @@
  *  - A page holds page_tokens consecutive positions of one sequence, for every layer. Per layer the
  *    caller lends four arrays: k and v, e4m3 (1 sign, 4 exponent, 3 mantissa bits, largest value
  *    448) [n_pages x n_kv_heads x page_tokens x head_dim], and k_scale and v_scale, fp32
- *    [n_pages x n_kv_heads]: the value is code * scale of its page and head.
+ *    [n_pages x n_kv_heads]: the value is code * scale of its page and head, the scale a number >= 0.
  *  - Shared by all layers: table int32 [max_seqs x max_pages] (row s, column c: the page of
  *    positions [c * page_tokens, (c + 1) * page_tokens) of sequence s, -1 for none), length int32
  *    [max_seqs] (tokens held), ref int32 [n_pages] (how many table entries name the page; 0 = free).
@@ -111,7 +111,8 @@ pi_status_t pi_kv_append(pi_kv_t *h, int32_t layer, const int32_t *seqs, const i
  *   out = sum_j softmax_j(scale * q . k_j) v_j   over what it sees,  lse = log sum_j exp(scale * q . k_j).
  * A query that sees nothing (its position is negative) gives 0 and -infinity. What no query of the
  * call sees is not read, so it may be absent, stale or NaN; a page that is seen but absent (-1, or
- * no page of the pool) is left out and flagged. q, out: [n_tokens x n_heads x head_dim] of `dtype`
+ * no page of the pool), or has for the head a scale that is not a number >= 0, is left out and
+ * flagged. q, out: [n_tokens x n_heads x head_dim] of `dtype`
  * (PI_F32, PI_BF16 or PI_F16), row t at element t * ld_q (ld_out); bases and row strides multiples
  * of 16 bytes. lse: fp32 [n_tokens x n_heads] or NULL. scale is finite. Scores, the softmax's
  * statistics and the output sums are fp32; the output is rounded to `dtype` once.

@@ -80,6 +80,8 @@ class Filled:
             if window > 0:
                 see &= (pos - j[None] < window) | (j[None] < sinks)
             see &= page[None] >= 0
+            keep = see.any(0)                                    # (0 * NaN: what nothing sees is not summed)
+            j, page, see = j[keep], page[keep], see[:, keep]
             for h in range(self.hkv):
                 k, v = ((x.view(torch.uint8)[page, h, j % self.page].view(torch.float8_e4m3fn).double()
                          * s[page, h].double()[:, None]) for x, s in ((self.k, self.ks), (self.v, self.vs)))
@@ -304,3 +306,29 @@ def test_values_of_the_smallest_scales(P, dim, page, group, kind, low):
     f.vs[f.table[0, 3:5].long()] = 2.0 ** -120
     for new in ([1, 1], [2, 1], [850, 517]):
         f.check(new, kind)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("dim,page,group", SIZES)
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -1.0])
+def test_pages_whose_scale_is_no_scale(P, dim, page, group, kind, bad):
+    """A page in view with a scale that is not a number >= 0: left out and flagged like an absent one, by every kernel."""
+    f = Filled(P, [900, 517], hq=2 * group, hkv=2, dim=dim, page=page)
+    whole = f.table.clone()
+    f.ks[f.table[0, 2].long(), 0] = bad
+    f.vs[f.table[0, 4].long(), 1] = bad
+    f.vs[f.table[1, 1].long(), 0] = bad
+    left = {0: [(0, 2), (1, 1)], 1: [(0, 4)]}                    # kv head: (sequence, column) left out
+    for new in ([1, 1], [2, 1], [700, 517]):
+        q = f.queries(new, kind)
+        got = f.attend(new, q).double()
+        assert f.cache.status() == P.PI_ERR_DEVICE_CHECK
+        for h, gone in left.items():
+            for i, c in gone:
+                f.table[i, c] = -1
+            want, _ = f.exact(new, q)
+            f.table.copy_(whole)
+            a, b = got[:, h * group:(h + 1) * group], want[:, h * group:(h + 1) * group]
+            err = (a - b).norm(dim=-1) / b.norm(dim=-1).clamp(min=1e-300)
+            assert (err <= ROW_TOL[kind] + 900 / 8 * 2.0 ** -23).all(), (h, new, err.max().item())
+    f.check([1, 0], kind, window=1)                              # out of view: not looked at
