@@ -30,7 +30,7 @@ __device__ __forceinline__ KvSeq kv_sequence(const KvView &c, const KvBatch &b, 
     } else {
         s.len = c.length[s.row];
         if (s.len < 0 || s.len > c.max_pages * c.page) {
-            s.len = 0;
+            s.len = s.n = 0;
             bad = true;
         }
     }

@@ -332,3 +332,25 @@ def test_pages_whose_scale_is_no_scale(P, dim, page, group, kind, bad):
             err = (a - b).norm(dim=-1) / b.norm(dim=-1).clamp(min=1e-300)
             assert (err <= ROW_TOL[kind] + 900 / 8 * 2.0 ** -23).all(), (h, new, err.max().item())
     f.check([1, 0], kind, window=1)                              # out of view: not looked at
+
+
+def test_lengths_out_of_range_are_left_alone(P):
+    """A sequence whose length its row cannot have: skipped and flagged by every call, its pages and length untouched."""
+    f = Filled(P, [100, 200], hq=4, hkv=2, dim=64, page=16)
+    c = f.cache
+    q = f.queries([1, 1], "f32")
+    want = f.attend([1, 1], q)
+    assert c.status() == 0
+    x = torch.randn((2, 2, 64), device="cuda")
+    for bad in (-1, f.table.shape[1] * 16 + 1, -2 ** 31, 2 ** 31 - 1):
+        c.length[0] = bad
+        table, ref, k = f.table.clone(), c.ref.clone(), f.k.view(torch.uint8).clone()
+        c.reserve(dev([0]), dev([0, 1]))
+        assert c.status() == P.PI_ERR_DEVICE_CHECK
+        assert int(c.length[0]) == bad and torch.equal(f.table, table) and torch.equal(c.ref, ref)
+        out = torch.full_like(q, 7.0)
+        f.attend([1, 1], q, out=out)
+        assert c.status() == P.PI_ERR_DEVICE_CHECK
+        assert (out[0] == 7).all() and torch.equal(out[1], want[1])
+        c.append(0, dev([0]), dev([0, 2]), x, x)
+        assert c.status() == P.PI_ERR_DEVICE_CHECK and torch.equal(f.k.view(torch.uint8), k)
