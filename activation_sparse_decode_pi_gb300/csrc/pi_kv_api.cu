@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 #include <cstdint>
 #include <new>
@@ -314,7 +315,9 @@ pi_status_t pi_kv_attend(pi_kv_t *h, int32_t layer, const int32_t *seqs, const i
     pi_status_t s;
     if ((s = check_call(h, n))) return s;
     const int es = elt_size(dtype);
-    if (layer < 0 || layer >= h->desc.n_layers || n_tokens < 0 || n_tokens > KV_MAX_LEN || !es || !std::isfinite(scale) || sinks < 0)
+    const double scale_log2 = (double)scale * 1.4426950408889634;
+    if (layer < 0 || layer >= h->desc.n_layers || n_tokens < 0 || n_tokens > KV_MAX_LEN || !es || sinks < 0 ||
+        !(std::fabs(scale_log2) <= (double)FLT_MAX))   // (a NaN scale fails too)
         return PI_ERR_INVALID_ARG;
     if (n == 0 || n_tokens == 0) return PI_OK;
     if ((s = check_batch(h, seqs, tok_start, n))) return s;
@@ -332,7 +335,7 @@ pi_status_t pi_kv_attend(pi_kv_t *h, int32_t layer, const int32_t *seqs, const i
     a.ldq = ld_q;
     a.ldo = ld_out;
     a.dtype = dtype;
-    a.scale_log2 = (float)((double)scale * 1.4426950408889634);
+    a.scale_log2 = (float)scale_log2;
     // no window: one that is never shorter than the distance of two positions (all below 2^30)
     a.window = window > 0 ? std::min(window, KV_MAX_LEN) : KV_MAX_LEN;
     a.sinks = std::min(sinks, KV_MAX_LEN);

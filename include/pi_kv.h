@@ -114,7 +114,7 @@ pi_status_t pi_kv_append(pi_kv_t *h, int32_t layer, const int32_t *seqs, const i
  * no page of the pool), or has for the head a scale that is not a number >= 0, is left out and
  * flagged. q, out: [n_tokens x n_heads x head_dim] of `dtype`
  * (PI_F32, PI_BF16 or PI_F16), row t at element t * ld_q (ld_out); bases and row strides multiples
- * of 16 bytes. lse: fp32 [n_tokens x n_heads] or NULL. scale is finite. Scores, the softmax's
+ * of 16 bytes. lse: fp32 [n_tokens x n_heads] or NULL. scale * log2(e) is finite in fp32. Scores, the softmax's
  * statistics and the output sums are fp32; the output is rounded to `dtype` once.
  * The same inputs give the same bits, whatever the GPU does besides.
  */

@@ -354,3 +354,39 @@ def test_lengths_out_of_range_are_left_alone(P):
         assert (out[0] == 7).all() and torch.equal(out[1], want[0])
         c.append(0, dev([0]), dev([0, 2]), x, x)
         assert c.status() == P.PI_ERR_DEVICE_CHECK and torch.equal(f.k.view(torch.uint8), k)
+
+
+def test_scales_of_the_scores_at_the_ends_of_fp32(P):
+    """The scale is multiplied by log2(e): one that leaves fp32 with it is refused, the largest others and 0 are right."""
+    f = Filled(P, [150], hq=2, hkv=2, dim=64, page=16)
+    for new in ([1], [150]):
+        q = f.queries(new, "f32")
+        for scale in (3e38, -3e38):
+            with pytest.raises(P.PiError) as e:
+                f.attend(new, q, scale=scale)
+            assert e.value.code == P.PI_ERR_INVALID_ARG
+        small = torch.full_like(q, 2.0 ** -126)
+        big = f.attend(new, small, scale=2.0 ** 126)             # scores of q * scale = 1 in every column
+        one = f.attend(new, torch.ones_like(q), scale=1.0)
+        assert (big - one).norm() <= 1e-5 * one.norm()
+        flat = f.attend(new, q, scale=0.0)
+        mean = f.attend(new, torch.zeros_like(q))
+        assert (flat - mean).norm() <= 1e-6 * mean.norm() and f.cache.status() == 0
+
+
+def test_scales_of_the_scores_at_the_ends_of_fp32(P):
+    """The scale is multiplied by log2(e): one that leaves fp32 with it is refused, the largest others and 0 are right."""
+    f = Filled(P, [150], hq=2, hkv=2, dim=64, page=16)
+    for new in ([1], [150]):
+        q = f.queries(new, "f32")
+        for scale in (3e38, -3e38):
+            with pytest.raises(P.PiError) as e:
+                f.attend(new, q, scale=scale)
+            assert e.value.code == P.PI_ERR_INVALID_ARG
+        small = torch.full_like(q, 2.0 ** -126)
+        big = f.attend(new, small, scale=2.0 ** 126)             # scores of q * scale = 1 in every column
+        one = f.attend(new, torch.ones_like(q), scale=1.0)
+        assert (big - one).norm() <= 1e-5 * one.norm()
+        flat = f.attend(new, q, scale=0.0)
+        mean = f.attend(new, torch.zeros_like(q))
+        assert (flat - mean).norm() <= 1e-6 * mean.norm() and f.cache.status() == 0
