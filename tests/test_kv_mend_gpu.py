@@ -65,8 +65,9 @@ class Filled:
     def attend(self, new, q, **kw):
         return self.cache.attend(0, dev(range(len(self.lens))), starts(new), q, **kw)
 
-    def exact(self, new, q, window=0, sinks=0):
-        """(out, lse) in fp64 from the definition, a sequence and kv head at a time."""
+    def exact(self, new, q, window=0, sinks=0, by_column=False):
+        """(out, lse) in fp64 from the definition, a sequence and kv head at a time. by_column: a NaN value is in the sums
+        of the rows that see it only (in products it meets weights of zero, too)."""
         out = torch.zeros(q.shape, dtype=torch.float64, device="cuda")
         lse = torch.full(q.shape[:2], -torch.inf, dtype=torch.float64, device="cuda")
         G, row = self.hq // self.hkv, 0
@@ -89,9 +90,12 @@ class Filled:
                 x = torch.einsum("tgd,kd->tgk", x, k) * self.dim ** -0.5
                 x = x.masked_fill(~see[:, None], -torch.inf)
                 lse[row:row + m, h * G:(h + 1) * G] = torch.logsumexp(x, -1)
-                p = torch.exp(x - x.amax(-1, keepdim=True).clamp(min=-1e300)).nan_to_num(0.0)
+                p = torch.exp(x - x.amax(-1, keepdim=True).clamp(min=-1e300))
                 z = p.sum(-1, keepdim=True)
-                out[row:row + m, h * G:(h + 1) * G] = torch.einsum("tgk,kd->tgd", p, v) / torch.where(z > 0, z, 1.0)
+                o = torch.einsum("tgk,kd->tgd", p, v.nan_to_num() if by_column else v) / torch.where(z == 0, 1.0, z)
+                if by_column:
+                    o[((see.double() @ v.isnan().double()) > 0)[:, None].expand_as(o)] = torch.nan
+                out[row:row + m, h * G:(h + 1) * G] = o
             row += m
         return out, lse
 
@@ -374,19 +378,36 @@ def test_scales_of_the_scores_at_the_ends_of_fp32(P):
         assert (flat - mean).norm() <= 1e-6 * mean.norm() and f.cache.status() == 0
 
 
-def test_scales_of_the_scores_at_the_ends_of_fp32(P):
-    """The scale is multiplied by log2(e): one that leaves fp32 with it is refused, the largest others and 0 are right."""
-    f = Filled(P, [150], hq=2, hkv=2, dim=64, page=16)
-    for new in ([1], [150]):
-        q = f.queries(new, "f32")
-        for scale in (3e38, -3e38):
-            with pytest.raises(P.PiError) as e:
-                f.attend(new, q, scale=scale)
-            assert e.value.code == P.PI_ERR_INVALID_ARG
-        small = torch.full_like(q, 2.0 ** -126)
-        big = f.attend(new, small, scale=2.0 ** 126)             # scores of q * scale = 1 in every column
-        one = f.attend(new, torch.ones_like(q), scale=1.0)
-        assert (big - one).norm() <= 1e-5 * one.norm()
-        flat = f.attend(new, q, scale=0.0)
-        mean = f.attend(new, torch.zeros_like(q))
-        assert (flat - mean).norm() <= 1e-6 * mean.norm() and f.cache.status() == 0
+# ------------------------------------------------------------------------------------------------ NaN codes
+
+def spoil(f, seq, pos, h, col, which="v"):
+    x = (f.v if which == "v" else f.k).view(torch.uint8)
+    x[f.table[seq, pos // f.page].long(), h, pos % f.page, col] = 0x7f
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("dim,page,group", SIZES)
+@pytest.mark.parametrize("seqs", [1, 40])
+def test_nan_codes_reach_the_rows_that_see_them(P, dim, page, group, kind, seqs):
+    """NaN values in the last, partial tile, at a window's edge and among the first tokens, for few rows and for prompts
+    (of one sequence, whose cache is split, and of many), and NaN keys, which reach every column."""
+    lens = [700 + i for i in range(seqs)]
+    f = Filled(P, lens, hq=2 * group, hkv=2, dim=dim, page=page)
+    last = seqs - 1
+    for pos, h, col in ((lens[last] - 1, 0, 5), (lens[last] - 3, 1, dim - 1), (lens[last] - 40, 0, 0), (600, 1, 17), (2, 0, 9)):
+        spoil(f, last, pos, h, col)
+    spoil(f, 0, 650, 1, 3, "k")
+    for m in (1, 2, 8, 160):
+        if m * group * seqs > 20000:
+            continue
+        new = [m] * seqs
+        q = f.queries(new, kind)
+        for kw in (dict(), dict(window=101, sinks=0), dict(window=40, sinks=3), dict(window=650, sinks=1)):
+            got = f.attend(new, q, **kw).double()
+            want, _ = f.exact(new, q, by_column=True, **kw)
+            assert f.cache.status() == 0
+            assert torch.equal(got.isnan(), want.isnan()), (m, kw, torch.nonzero(got.isnan() != want.isnan())[:6].tolist())
+            ok = ~want.isnan()
+            a, b = torch.where(ok, got, 0.0), torch.where(ok, want, 0.0)
+            err = (a - b).norm(dim=-1) / b.norm(dim=-1).clamp(min=1e-300)
+            assert (err <= ROW_TOL[kind] + 740 / 8 * 2.0 ** -23).all(), (m, kw, err.max().item())
