@@ -38,11 +38,6 @@ __device__ __forceinline__ KvSeq kv_sequence(const KvView &c, const KvBatch &b, 
     return s;
 }
 
-template <bool B>
-struct Const {
-    static constexpr bool value = B;
-};
-
 // Whether a block scale is one: a number >= 0. A page in view without one is left out, as an absent page is.
 __device__ __forceinline__ bool is_scale(float s) { return s >= 0.f && s <= 3.402823466e38f; }
 
@@ -161,17 +156,6 @@ __device__ __forceinline__ void load16(const void *p, int dtype, int64_t at, flo
             for (int e = 0; e < 8; ++e) x[8 * i + e] = v[e];
         }
     }
-}
-
-// 16 codes that are read once: not kept in L1.
-__device__ __forceinline__ uint4 ld_codes(const uint4 *p)
-{
-    uint4 v;
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p)
-                 : "memory");
-    return v;
 }
 
 // ---------------------------------------------------------------- tensor-core product -------
