@@ -96,8 +96,8 @@ cudaError_t setup_of()
 }
 
 // Sequences with at least this many rows (new tokens x heads of a group) are worth a 128-row tile. Measured, 16 sequences
-// of 4096, 64 query heads on 8, split / rows kernel: 16 rows 45 / 79 us, 32 rows 72 / 81 us, 48 rows 95 / 71 us, 64 rows
-// 121 / 71 us; fp32: 32 rows 94 / 112 us, 64 rows 164 / 104 us.
+// of 4096, 64 query heads on 8, split / rows kernel: 16 rows 45 / 79 us, 32 rows 71 / 83 us, 48 rows 95 / 72 us, 64 rows
+// 120 / 73 us; fp32: 32 rows 99 / 118 us, 64 rows 173 / 109 us.
 constexpr int ROWS_FROM = 33;
 
 // The kernels of one call: the split kernel for sequences with few rows, the rows kernel for the others.
@@ -111,8 +111,8 @@ cudaError_t attend_of(const pi_kv *h, int layer, KvAttendArgs a, cudaStream_t s)
     cudaError_t e = cudaSuccess;
     if (few) {
         // 16 rows to a tile where the rows of a sequence (on average: all that the host knows) fill more than 8: the cache
-        // is then read once instead of twice (64 sequences, 16 heads to a group: 234 / 324 us with 16 / 8; 8 heads, 128
-        // sequences: 392 / 328 us, since 16 leave room for fewer warps)
+        // is then read once instead of twice (64 sequences, 16 heads to a group: 229 / 323 us with 16 / 8; 8 heads, 128
+        // sequences: 381 / 330 us, since 16 leave room for fewer warps)
         const bool wide = many || rows > 8 * n, one = a.dtype == PI_BF16;
         const auto run = wide ? (one ? split_launch<D, 2, 1> : split_launch<D, 2, 2>)
                               : (one ? split_launch<D, 1, 1> : split_launch<D, 1, 2>);

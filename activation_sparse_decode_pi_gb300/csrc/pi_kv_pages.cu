@@ -4,7 +4,7 @@
 // free list to keep, the pool stays dense at its bottom, and every result is a function of the state.
 // The bookkeeping of reserve, fork and compact needs the counts in order (a prefix sum), so one CTA
 // does it; the copies of the listed pages run on the whole GPU right behind it. Measured: 8 to 64 sequences
-// forked over 8 layers 48 us (7 us of it bookkeeping), 16 of 32 sequences' pages moved down 197 us = 5.9 TB/s.
+// forked over 8 layers 48 us (7 us of it bookkeeping), 16 of 32 sequences' pages moved down 205 us = 5.6 TB/s.
 #include <algorithm>
 
 #include "pi_kv_device.cuh"

@@ -3,7 +3,8 @@
 // For prompt chunks: 128 rows (query token and head of the group) of one sequence and kv head against
 // tiles of TOK positions. S = Q K^T and O += P V run on the tensor cores with fp32 accumulators in
 // tensor memory; the weights P = 2^(S - m) go back to tensor memory as f16 and are the A operand of
-// the second product. Nothing of S or P leaves the SM.
+// the second product. Nothing of S or P leaves the SM. The next tile's S is written over no P that a product may
+// still read, and a tile's codes are read from their stage before the next copy into it is asked for.
 //
 // What bounds it: per 128 rows and tile the two products take 2 * 128 * TOK * D / 8192 cycles, the softmax
 // about as many issue slots (one exponential and a handful of operations per score), and e4m3 has to
@@ -13,12 +14,14 @@
 // two threads to a row (a half of the tile's positions each: the softmax is latency-bound with fewer),
 // whose first warp issues its products; 4 more warps convert codes, which TMA brings a tile ahead,
 // into a ring of NB tiles.
-// Measured: four chunks of 707..1724 tokens over 2290..6425 positions, 32 heads on 8 of 128, bf16 341 us =
-// 954 TFLOP/s of the visible pairs (tensor pipe 42% active: the hand-offs between conversion, products and
-// softmax bound it); one prompt of 8191 in a window of 1000 + 70, 32 heads, fp16 276 us.
+// Measured: four chunks of 707..1724 tokens over 2290..6425 positions, 32 heads on 8 of 128, bf16 354 us =
+// 918 TFLOP/s of the visible pairs (tensor pipe 41% active: the hand-offs between conversion, products and
+// softmax bound it); one prompt of 8191 in a window of 1000 + 70, 32 heads, fp16 282 us.
 // Rounding: as in pi_kv_split.cuh: q as f16 scaled per row by a power of two, weights as f16 in
 // units of 2^-7 of a reference that trails the running maximum by at most 2^8 (floor 2^-31 of the
-// row's largest weight). QT = 2 (fp32 output): a second f16 term of both.
+// row's largest weight). QT = 2 (fp32 output): a second f16 term of both. QT = 1: 11 bits of the weight, for fp16
+// outputs as for bf16: on the windowed prompt the error against 64 bits is 2.7e-4, 2.1e-4 of it the output's rounding;
+// a second term would double the second product and halve the tile.
 #pragma once
 
 #include "pi_kv_device.cuh"

@@ -19,11 +19,12 @@
 //    per CTA, so ragged lengths and one long sequence fill the GPU alike. An item cut over CTAs is
 //    joined by the last of them to finish, in the order of its parts (the same bits every time).
 // Measured (one token a sequence, 8 kv heads of 128 for 64 or 32 heads, bf16): 128 sequences of 129..16383
-// positions 327 us = 6.7 TB/s, 64 windows of 4096 + 4 positions 93 us, one sequence of 131067 56 us (start and
-// join ~15 us). fp32, 16 sequences of 1..8191, 40 heads: 154 us = 4.5 TB/s, bound by the consumer warps, whose
-// second terms double the products. Many items of 1 to 5 tiles (85 sequences, 40 heads, fp32): 146 us at a floor of
-// 22 us, of which the joins are some 35 (left out to time the rest); two result slots to every warp, up to 8 items
-// between their first product and their join, gained nothing there and cost 5% on 128 x 300..1000.
+// positions 332 us = 6.6 TB/s, 64 windows of 4096 + 4 positions 96 us, one sequence of 131067 56 us (start and
+// join ~15 us). fp32, 16 sequences of 1..8191, 40 heads: 151 us = 4.6 TB/s, bound by the consumer warps, whose
+// second terms double the products. Many items of 1 to 5 tiles (85 sequences, 40 heads, fp32): 158 us at a floor of
+// 22 us. (146 us before a slot's loads were fenced off from its next copy; of that the joins were some 35, left out
+// to time the rest; two result slots to every warp, up to 8 items between their first product and their join, gained
+// nothing there and cost 5% on 128 x 300..1000.)
 // Rounding: q is scaled by a power of two per row so that its largest value lies in [128, 256) and cut
 // to f16, weights are held as f16 in units of 2^-14 (floor 2^-38). T = 2: both keep a second f16 term
 // (22 bits, fp32 accuracy). T = 1 (bf16 output): 11 bits of the weight meet the output's 8.
@@ -45,7 +46,8 @@ struct SplitCfg {
     static constexpr int NW = QN == 2 && D == 256 ? 4 : 7;   // consumer warps (and one producer)
     // Where there is room, 4 more warps join the consumers' results of an item while these go on to the next one: two
     // to each of the two buffers, so that short items do not queue for one join, and all four to a cut item (85
-    // sequences of 1..300, 40 heads, fp32: 146 us, 153 with four to each; one of 131067: 56 us, 62 with two).
+    // sequences of 1..300, 40 heads, fp32, before loads were fenced: 146 us, 153 with four to each; one of 131067:
+    // 56 us, 62 with two).
     static constexpr bool FLOW = !WIDE;
     static constexpr int R = 8 * QN;                     // rows per tile
     static constexpr int SLOT = KV_TILE * D;             // bytes of one K or V tile
@@ -60,7 +62,7 @@ struct SplitCfg {
     static constexpr bool FRESH = T == 2 && D / 16 * QN <= 8;
     // ^ a tile's products in sums of their own, where registers allow: adding to a large sum inside the
     // product loses low bits. 16 x 8k, 40 heads, fp32: error 5.6e-7 in 162 us, without 1.4e-6 in 136 us
-    // (both before items were stepped through without searching: 154 us now).
+    // (both before items were stepped through without searching: 151 us now).
     static constexpr int MAX_SLOTS = 24;
 };
 

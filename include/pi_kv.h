@@ -114,9 +114,15 @@ pi_status_t pi_kv_append(pi_kv_t *h, int32_t layer, const int32_t *seqs, const i
  * no page of the pool), or has for the head a scale that is not a number >= 0, is left out and
  * flagged. q, out: [n_tokens x n_heads x head_dim] of `dtype`
  * (PI_F32, PI_BF16 or PI_F16), row t at element t * ld_q (ld_out); bases and row strides multiples
- * of 16 bytes. lse: fp32 [n_tokens x n_heads] or NULL. scale * log2(e) is finite in fp32. Scores, the softmax's
- * statistics and the output sums are fp32; the output is rounded to `dtype` once.
- * The same inputs give the same bits, whatever the GPU does besides.
+ * of 16 bytes. lse: fp32 [n_tokens x n_heads] or NULL. scale * log2(e) is
+ * finite in fp32. Scores, the softmax's statistics and the output sums are fp32; the output is
+ * rounded to `dtype` once. Queries and weights enter the products as f16 terms, the weights in units
+ * that follow the largest value scale: two terms (22 bits) for PI_F32, and for PI_F16 where a
+ * sequence has few rows (new tokens x heads of a group); else one (11 bits of a weight, while a
+ * PI_BF16 or PI_F16 query is exact in one). The sums are divided last: values whose weighted sum over
+ * the cache leaves fp32 give infinities.
+ * The same call gives the same bits, whatever the GPU does besides (another set of sequences may cut
+ * the caches elsewhere).
  */
 pi_status_t pi_kv_attend(pi_kv_t *h, int32_t layer, const int32_t *seqs, const int32_t *tok_start, int32_t n,
                          int32_t n_tokens, const void *q, int64_t ld_q, void *out, int64_t ld_out, float *lse,
