@@ -411,3 +411,49 @@ def test_nan_codes_reach_the_rows_that_see_them(P, dim, page, group, kind, seqs)
             a, b = torch.where(ok, got, 0.0), torch.where(ok, want, 0.0)
             err = (a - b).norm(dim=-1) / b.norm(dim=-1).clamp(min=1e-300)
             assert (err <= ROW_TOL[kind] + 740 / 8 * 2.0 ** -23).all(), (m, kw, err.max().item())
+
+
+# ------------------------------------------------------------------------------------------------ ends of the ranges
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("dim,group", [(64, 1), (64, 16), (128, 3), (128, 16), (256, 2), (256, 16)])
+def test_as_many_sequences_as_a_call_takes(P, dim, group, kind):
+    """1024 sequences: the call's tables leave the ring the fewest slots. Single tokens, and short prompts among them."""
+    lens = [1 + 29 * i % 190 for i in range(1024)]
+    f = Filled(P, lens, hq=group, hkv=1, dim=dim, page=16)
+    f.check([1] * 1024, kind, repeat=5)
+    f.check([min(n, 3 if i % 3 else 50) for i, n in enumerate(lens)], kind, repeat=5)
+    f.check([min(n, i % 2) for i, n in enumerate(lens)], kind, window=20, sinks=2, repeat=5)
+
+
+def test_offsets_past_32_bits(P):
+    """Pools of more than 2^32 bytes with the sequences' pages at their ends: append, attention and page copies."""
+    dim, page, hkv, n_pages = 256, 64, 2, 140000
+    k, v = (torch.empty((n_pages, hkv, page, dim), dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+            for _ in range(2))
+    ks, vs = (torch.ones((n_pages, hkv), device="cuda") for _ in range(2))
+    assert k.numel() > 2 ** 32
+    cols = 14
+    table = torch.arange(n_pages - 1, n_pages - 1 - cols, -1, dtype=torch.int32, device="cuda")[None].contiguous()
+    ref = torch.zeros(n_pages, dtype=torch.int32, device="cuda")
+    ref[table[0].long()] = 1
+    f = Filled(P, [cols * page - 5], hq=8, hkv=hkv, dim=dim, page=page)      # the same sequence in a small pool
+    small = f.table[0, :cols].long()
+    f.cache.append(0, dev([0]), starts(f.lens), *[torch.randn((f.lens[0], hkv, dim), device="cuda") for _ in range(2)])
+    cache = P.KVCache([dict(k=k, v=v, k_scale=ks, v_scale=vs)], table, dev(f.lens), ref, n_heads=8)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    new = [torch.randn((f.lens[0], hkv, dim), generator=g, device="cuda") for _ in range(2)]
+    f.cache.append(0, dev([0]), starts(f.lens), *new)
+    cache.append(0, dev([0]), starts(f.lens), *new)
+    for a, b in ((k, f.k), (v, f.v)):
+        at = a.view(torch.uint8)[table[0].long()].transpose(1, 2).reshape(-1, hkv, dim)[:f.lens[0]]
+        assert torch.equal(at, b.view(torch.uint8)[small].transpose(1, 2).reshape(-1, hkv, dim)[:f.lens[0]])
+    for m in (1, 3, 300):
+        q = f.queries([m], "bf16")
+        assert torch.equal(cache.attend(0, dev([0]), starts([m]), q), f.attend([m], q))
+    cache.compact()                                              # from the pool's end to its start
+    assert table[0].sort().values.tolist() == list(range(cols))
+    q = f.queries([70], "f32")
+    assert torch.equal(cache.attend(0, dev([0]), starts([70]), q), f.attend([70], q)) and cache.status() == 0
+    cache.copy_pages(table[0, :1].contiguous(), dev([n_pages - 1]))
+    assert torch.equal(k.view(torch.uint8)[n_pages - 1], k.view(torch.uint8)[table[0, 0].long()]) and cache.status() == 0
