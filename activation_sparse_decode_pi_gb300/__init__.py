@@ -30,7 +30,7 @@ PI_F32, PI_BF16, PI_F16, PI_INT4_G128 = 0, 1, 2, 3
 DTYPES = {"f32": PI_F32, "bf16": PI_BF16, "f16": PI_F16, "int4g128": PI_INT4_G128}
 KINDS = {"gated": PI_FFN_GATED_RELU, "relu": PI_FFN_RELU}
 
-# every symbol include/pi_ffn.h and include/pi_kv.h declare
+# every symbol that the headers in include/ declare
 EXPORTS = (
     "pi_ffn_create", "pi_ffn_destroy", "pi_predict", "pi_sparse_ffn", "pi_decode_stack",
     "pi_hot_first_order", "pi_permute_rows", "pi_get_status", "pi_status_string", "pi_abi_version",
@@ -39,6 +39,7 @@ EXPORTS = (
     "pi_ffn_set_phase_trace",
     "pi_kv_create", "pi_kv_destroy", "pi_kv_get_status", "pi_kv_reserve", "pi_kv_append", "pi_kv_attend",
     "pi_kv_fork", "pi_kv_free", "pi_kv_trim", "pi_kv_copy_pages", "pi_kv_compact",
+    "pi_kv_append_rotated", "pi_rotate", "pi_int4_linear",
 )
 PI_STACK_PHASES = 8
 STACK_PHASE_NAMES = ("layer_start", "hidden_done", "logits_start", "list_ready", "first_rows", "ffn_done",
@@ -73,6 +74,12 @@ class PiKvLayer(ctypes.Structure):
 
 class PiKvState(ctypes.Structure):
     _fields_ = [("table", ctypes.c_void_p), ("length", ctypes.c_void_p), ("ref", ctypes.c_void_p)]
+
+
+class PiRotary(ctypes.Structure):
+    _fields_ = [("turns", ctypes.c_void_p), ("q_norm", ctypes.c_void_p), ("k_norm", ctypes.c_void_p),
+                ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("norm", ctypes.c_int32),
+                ("amp", ctypes.c_float), ("eps", ctypes.c_float)]
 
 
 _P = ctypes.c_void_p
@@ -130,6 +137,10 @@ for _name, _args in {
     "pi_kv_trim": [_P, _P, _I32, _I32, _I32, _P],
     "pi_kv_copy_pages": [_P, _P, _P, _I32, _P],
     "pi_kv_compact": [_P, _P, _P],
+    "pi_kv_append_rotated": [_P, _I32, _P, _P, _I32, _I32, ctypes.POINTER(PiRotary), _P, _I64, _P, _I64, _P, _P, _I64,
+                             _I32, _P],
+    "pi_rotate": [ctypes.POINTER(PiRotary), _P, _I32, _I32, _I32, _I32, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _I32, _P],
+    "pi_int4_linear": [_P, _P, _P, _I32, _I32, _P, _I64, _I32, _P, _I64, _P, _I64, _I32, _P],
 }.items():
     getattr(_lib, _name).restype = ctypes.c_int
     getattr(_lib, _name).argtypes = _args
@@ -316,6 +327,25 @@ def pi_kv_compact(h, n_live=None, stream=None) -> None:
     _check(_lib.pi_kv_compact(h, _ptr(n_live), _stream(stream)), "pi_kv_compact")
 
 
+def pi_kv_append_rotated(h, layer, seqs, tok_start, n, n_tokens, rotary, q, ld_q, q_out, ld_q_out, k_new, v_new, ld, dtype,
+                         stream=None) -> None:
+    _check(_lib.pi_kv_append_rotated(h, layer, _ptr(seqs), _ptr(tok_start), n, n_tokens, ctypes.byref(rotary), _ptr(q),
+                                     ld_q, _ptr(q_out), ld_q_out, _ptr(k_new), _ptr(v_new), ld, dtype, _stream(stream)),
+           "pi_kv_append_rotated")
+
+
+def pi_rotate(rotary, pos, n_tokens, n_heads, n_kv_heads, head_dim, q, ld_q, q_out, ld_q_out, k, ld_k, k_out, ld_k_out,
+              dtype, stream=None) -> None:
+    _check(_lib.pi_rotate(ctypes.byref(rotary), _ptr(pos), n_tokens, n_heads, n_kv_heads, head_dim, _ptr(q), ld_q,
+                          _ptr(q_out), ld_q_out, _ptr(k), ld_k, _ptr(k_out), ld_k_out, dtype, _stream(stream)),
+           "pi_rotate")
+
+
+def pi_int4_linear(w, s, bias, n, k, x, ld_x, rows, add, ld_add, y, ld_y, dtype, stream=None) -> None:
+    _check(_lib.pi_int4_linear(_ptr(w), _ptr(s), _ptr(bias), n, k, _ptr(x), ld_x, rows, _ptr(add), ld_add, _ptr(y), ld_y,
+                               dtype, _stream(stream)), "pi_int4_linear")
+
+
 # ------------------------------------------------------------------------------------------------
 # torch conveniences (still only marshalling: each call is one C-ABI call)
 # ------------------------------------------------------------------------------------------------
@@ -494,6 +524,149 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _rows(x, width, name):
+    """Row stride of a [rows, width] tensor with contiguous rows."""
+    shape = x.shape
+    if len(shape) != 2 or shape[1] != width or not x.is_cuda or (width > 1 and x.stride(1) != 1):
+        raise ValueError(f"{name}: a [rows, {width}] CUDA tensor with contiguous rows, got {tuple(shape)}")
+    return x.stride(0) if shape[0] > 1 else width
+
+
+class Int4Linear:
+    """y = x W^T (+ bias) (+ add) with 4-bit weights in the format of SparseFFN's (group 128), for 1 to 256 rows.
+
+    w: uint8 [n, k / 2] (two's-complement nibbles, the even element low), s: fp16 [n, k / 128], bias: fp32 [n] or None
+    (kept referenced).
+    """
+
+    def __init__(self, w, s, bias=None):
+        import torch
+
+        if w.dtype is not torch.uint8 or w.dim() != 2 or not w.is_contiguous():
+            raise ValueError("w: contiguous uint8 [n, k / 2]")
+        self.n, self.k = w.shape[0], 2 * w.shape[1]
+        if s.dtype is not torch.float16 or tuple(s.shape) != (self.n, self.k // 128) or not s.is_contiguous():
+            raise ValueError(f"s: contiguous fp16 [{self.n}, {self.k // 128}]")
+        if bias is not None and (bias.dtype is not torch.float32 or tuple(bias.shape) != (self.n,) or not bias.is_contiguous()):
+            raise ValueError(f"bias: contiguous fp32 [{self.n}]")
+        self.w, self.s, self.bias = w, s, bias
+
+    def __call__(self, x, out=None, add=None, stream=None):
+        """x [rows, k] (fp32, bf16 or fp16); add: x's type, [rows, n]; out: likewise, and may be add itself."""
+        rows, n = x.shape[0], self.n
+        ld_x, dtype, ld_add = _rows(x, self.k, "x"), _act_dtype(x), 0
+        if add is not None:
+            ld_add = _rows(add, n, "add")
+            if add.dtype is not x.dtype or add.shape[0] != rows:
+                raise ValueError("add: x's type and number of rows")
+            add = add.data_ptr()
+        if out is None:
+            out, ld_out = _empty((rows, n), x.dtype, x.device, stream), n
+        else:
+            ld_out = _rows(out, n, "out")
+            if out.dtype is not x.dtype or out.shape[0] != rows:
+                raise ValueError("out: x's type and number of rows")
+        pi_int4_linear(self.w.data_ptr(), self.s.data_ptr(), _ptr(self.bias), n, self.k, x.data_ptr(), ld_x, rows, add,
+                       ld_add, out.data_ptr(), ld_out, dtype, stream)
+        return out
+
+
+def rotary_frequencies(rot_dim, base=10000.0, *, stretch=1.0, trained=None, slow=1.0, fast=32.0):
+    """Radians per position of the rot_dim / 2 pairs: base^(-2 i / rot_dim), for contexts `stretch` times the trained
+    length. trained None: every frequency over stretch. Else pairs that turn at least `fast` times within `trained`
+    positions keep theirs, those that turn at most `slow` times get it over stretch, and in between the two are mixed
+    in proportion."""
+    import math
+
+    out = []
+    for i in range(rot_dim // 2):
+        f = base ** (-2.0 * i / rot_dim)
+        keep = 0.0
+        if trained is not None:
+            keep = min(1.0, max(0.0, (trained * f / (2 * math.pi) - slow) / (fast - slow)))
+        out.append(f * (keep + (1.0 - keep) / stretch))
+    return out
+
+
+def _pi_bits(n):
+    """pi * 2^n to the nearest integer but one: 16 atan(1/5) - 4 atan(1/239)."""
+    one = 1 << (n + 32)
+
+    def atan_of_inverse(q):
+        total, term, k = 0, one // q, 1
+        while term:
+            total += term // k if k % 4 == 1 else -(term // k)
+            term //= q * q
+            k += 2
+        return total
+
+    return (16 * atan_of_inverse(5) - 4 * atan_of_inverse(239)) >> 32
+
+
+def rotary_turns(freq):
+    """Each frequency (radians per position) as a fraction of a turn per position in units of 2^-64, exactly rounded
+    from the given double: what pi_rotary_t's `turns` holds. Ints in [0, 2^64)."""
+    bits = 256
+    turn = 2 * _pi_bits(bits)
+    out = []
+    for f in freq:
+        num, den = float(f).as_integer_ratio()
+        num, den = num << (64 + bits), den * turn
+        out.append((2 * num + den) // (2 * den) % (1 << 64))
+    return out
+
+
+class Rotary:
+    """Norm (optional) and position rotation of query and key heads, for ``rotate`` and ``KVCache.append_rotated``.
+
+    freq: radians per position of each pair (any doubles; ``rotary_frequencies`` has the usual ones); the first
+    2 len(freq) elements of a head are turned, in pairs (i, i + len(freq)) or, interleaved, (2 i, 2 i + 1), and multiplied by
+    amp. norm: each head is divided by its root mean square first; q_norm, k_norm: fp32 [head_dim] weights, None: ones.
+    """
+
+    def __init__(self, freq, head_dim, *, interleaved=False, amp=1.0, norm=False, q_norm=None, k_norm=None, eps=1e-6,
+                 device="cuda"):
+        import torch
+
+        turns = [t - (1 << 64) if t >= 1 << 63 else t for t in rotary_turns(freq)]
+        self.head_dim, self.q_norm, self.k_norm = head_dim, q_norm, k_norm
+        for name, w in (("q_norm", q_norm), ("k_norm", k_norm)):
+            if w is None:
+                continue
+            if w.dtype is not torch.float32 or tuple(w.shape) != (head_dim,) or not w.is_contiguous():
+                raise ValueError(f"{name}: contiguous fp32 [{head_dim}]")
+            if not norm:
+                raise ValueError(f"{name}: weights of a norm that is off")
+        self.turns = torch.tensor(turns, dtype=torch.int64).to(device)
+        self.desc = PiRotary(_ptr(self.turns) if turns else None, _ptr(q_norm), _ptr(k_norm), 2 * len(turns), int(interleaved),
+                             int(norm), amp, eps)
+
+    def rotate(self, pos, q, k=None, q_out=None, k_out=None, stream=None):
+        """(q_out, k_out): q [tokens, heads, dim] and k [tokens, kv heads, dim] (fp32, bf16 or fp16) at positions pos
+        (int32 [tokens]). q_out and k_out may be q and k themselves."""
+        T, heads, dim, dtype = q.shape[0], q.shape[1], self.head_dim, _act_dtype(q)
+        args, outs = [], []
+        for name, x, out in (("q", q, q_out), ("k", k, k_out)):
+            if x is None:
+                args += [None, 0, None, 0]
+                outs.append(None)
+                continue
+            if x.dim() != 3 or x.dtype is not q.dtype or x.shape[0] != T:
+                raise ValueError(f"{name}: [tokens, heads, dim] of one type and number of tokens")
+            n = x.shape[1]
+            ld = _token_rows(x, n, dim, name)
+            if out is None:
+                out, ld_out = _empty((T, n, dim), x.dtype, x.device, stream), n * dim
+            else:
+                ld_out = _token_rows(out, n, dim, name + "_out")
+                if out.dtype is not x.dtype or out.shape[0] != T:
+                    raise ValueError(f"{name}_out: {name}'s type and number of tokens")
+            args += [x.data_ptr(), ld, out.data_ptr(), ld_out]
+            outs.append(out)
+        pi_rotate(self.desc, _i32(pos, "pos", T), T, heads, 0 if k is None else k.shape[1], dim, *args, dtype, stream)
+        return tuple(outs)
+
+
 class KVCache:
     """A pi_kv handle over CUDA tensors (kept referenced for the handle's lifetime): a paged e4m3 key/value cache.
 
@@ -561,6 +734,27 @@ class KVCache:
             raise ValueError("k_new and v_new: one shape, type and row stride")
         pi_kv_append(self.h, layer, _i32(seqs, "seqs"), _i32(tok_start, "tok_start", n + 1), n, T, k_new.data_ptr(),
                      v_new.data_ptr(), ld, _act_dtype(k_new), stream)
+
+    def append_rotated(self, layer, seqs, tok_start, rotary, q, k_new, v_new, q_out=None, stream=None):
+        """append with rotary's norm and rotation in the same pass: keys are turned by their positions before they are
+        coded; returns q_out, q [tokens, heads, dim] turned likewise (q_out may be q itself)."""
+        n, T, heads, dim = seqs.shape[0], q.shape[0], self.n_heads, self.head_dim
+        if rotary.head_dim != dim:
+            raise ValueError(f"rotary: made for heads of {rotary.head_dim}, not {dim}")
+        ld_q, ld, dtype = _token_rows(q, heads, dim, "q"), _token_rows(k_new, self.n_kv_heads, dim, "k_new"), _act_dtype(q)
+        if _token_rows(v_new, self.n_kv_heads, dim, "v_new") != ld or v_new.dtype is not k_new.dtype or \
+                k_new.dtype is not q.dtype or v_new.shape[0] != T or k_new.shape[0] != T:
+            raise ValueError("q, k_new and v_new: one type and number of tokens, the latter two one row stride")
+        if q_out is None:
+            q_out, ld_out = _empty((T, heads, dim), q.dtype, q.device, stream), heads * dim
+        else:
+            ld_out = _token_rows(q_out, heads, dim, "q_out")
+            if q_out.dtype is not q.dtype or q_out.shape[0] != T:
+                raise ValueError("q_out: q's type and number of tokens")
+        pi_kv_append_rotated(self.h, layer, _i32(seqs, "seqs"), _i32(tok_start, "tok_start", n + 1), n, T, rotary.desc,
+                             q.data_ptr(), ld_q, q_out.data_ptr(), ld_out, k_new.data_ptr(), v_new.data_ptr(), ld, dtype,
+                             stream)
+        return q_out
 
     def attend(self, layer, seqs, tok_start, q, out=None, lse=None, *, scale=None, window=0, sinks=0, stream=None):
         """Attention of q [tokens, heads, dim], the sequences' last positions, over their cache; returns out

@@ -308,6 +308,40 @@ pi_status_t pi_kv_append(pi_kv_t *h, int32_t layer, const int32_t *seqs, const i
                                         dtype, h->nsm, (cudaStream_t)stream));
 }
 
+pi_status_t pi_kv_append_rotated(pi_kv_t *h, int32_t layer, const int32_t *seqs, const int32_t *tok_start, int32_t n,
+                                 int32_t n_tokens, const pi_rotary_t *rotary, const void *q, int64_t ld_q, void *q_out,
+                                 int64_t ld_q_out, const void *k_new, const void *v_new, int64_t ld, int32_t dtype,
+                                 void *stream)
+{
+    pi_status_t s;
+    if ((s = check_call(h, n))) return s;
+    const int es = elt_size(dtype);
+    if (layer < 0 || layer >= h->desc.n_layers || n_tokens < 0 || n_tokens > KV_MAX_LEN || !es) return PI_ERR_INVALID_ARG;
+    KvAppendRotArgs a = {};
+    if ((s = check_rotary(rotary, h->desc.head_dim, h->dev, &a.r))) return s;
+    if (n == 0 || n_tokens == 0) return PI_OK;
+    if ((s = check_batch(h, seqs, tok_start, n))) return s;
+    const int64_t width = (int64_t)h->desc.n_kv_heads * h->desc.head_dim, wide = (int64_t)h->desc.n_heads * h->desc.head_dim;
+    if ((s = check_rows(h, k_new, n_tokens, width, ld, es))) return s;
+    if ((s = check_rows(h, v_new, n_tokens, width, ld, es))) return s;
+    if ((s = check_rows(h, q, n_tokens, wide, ld_q, es))) return s;
+    if ((s = check_rows(h, q_out, n_tokens, wide, ld_q_out, es))) return s;
+    const Strided sq{q, n_tokens, wide, ld_q, es}, so{q_out, n_tokens, wide, ld_q_out, es};
+    const Strided sk{k_new, n_tokens, width, ld, es}, sv{v_new, n_tokens, width, ld, es};
+    if ((!same_place(sq, so) && may_overlap(sq, so)) || may_overlap(so, sk) || may_overlap(so, sv)) return PI_ERR_INVALID_ARG;
+    a.c = h->view;
+    a.b = {seqs, tok_start, n, n_tokens};
+    a.l = h->layers[layer];
+    a.q = q;
+    a.k = k_new;
+    a.v = v_new;
+    a.qo = q_out;
+    a.ldq = ld_q;
+    a.ldqo = ld_q_out;
+    a.ld = ld;
+    return cuda_status(launch_kv_append_rot(a, dtype, h->nsm, (cudaStream_t)stream));
+}
+
 pi_status_t pi_kv_attend(pi_kv_t *h, int32_t layer, const int32_t *seqs, const int32_t *tok_start, int32_t n,
                          int32_t n_tokens, const void *q, int64_t ld_q, void *out, int64_t ld_out, float *lse,
                          int32_t dtype, float scale, int32_t window, int32_t sinks, void *stream)

@@ -22,14 +22,6 @@ struct AppendCfg {
     static constexpr int BUF = W == 1 ? 2 : 8, CTAS = W == 1 ? 6 : 3;
 };
 
-// Smallest e >= KV_MIN_EXP with a <= 448 * 2^e = 1.75 * 2^(8 + e), a finite and >= 0.
-__device__ __forceinline__ int block_exponent(float a)
-{
-    const uint32_t b = __float_as_uint(a);
-    const int k = (int)(b >> 23) - 127;   // a = 1.m * 2^k (subnormals land far below KV_MIN_EXP)
-    return max(k - 8 + ((b & 0x7fffffu) > 0x600000u), KV_MIN_EXP);
-}
-
 template <int DT, int W>
 __global__ void __launch_bounds__(AP_NT, AppendCfg<W>::CTAS) k_kv_append(const KvView c, const KvBatch b, const KvLayerDev l,
                                                      const void *k_new, const void *v_new, int64_t ld)
@@ -105,16 +97,7 @@ __global__ void __launch_bounds__(AP_NT, AppendCfg<W>::CTAS) k_kv_append(const K
             float s = exp2i(block_exponent(top));
             if (p0 > 0) {
                 s = fmaxf(was, s);
-                if (s > was) {   // the page's earlier codes in the new unit
-                    const float f = was / s;
-                    for (int x = th; x < p0 * D / 4; x += NTH) {
-                        const uint32_t w = ((const uint32_t *)codes)[x];
-                        const uint32_t a0 = e4m3x2_f16x2((uint16_t)w), a1 = e4m3x2_f16x2((uint16_t)(w >> 16));
-                        const float2 x0 = __half22float2(u32_h2(a0)), x1 = __half22float2(u32_h2(a1));
-                        ((uint32_t *)codes)[x] =
-                            f32x2_e4m3x2(x0.x * f, x0.y * f) | (uint32_t)f32x2_e4m3x2(x1.x * f, x1.y * f) << 16;
-                    }
-                }
+                if (s > was) recode(codes, p0 * D / 4, was / s, th, NTH);   // the page's earlier codes in the new unit
             }
             if (th == 0 && (p0 == 0 || s > was)) *scale = s;
 

@@ -158,6 +158,27 @@ __device__ __forceinline__ void load16(const void *p, int dtype, int64_t at, flo
     }
 }
 
+// ---------------------------------------------------------------- block scales --------------
+
+// Smallest e >= KV_MIN_EXP with a <= 448 * 2^e = 1.75 * 2^(8 + e), a finite and >= 0.
+__device__ __forceinline__ int block_exponent(float a)
+{
+    const uint32_t b = __float_as_uint(a);
+    const int k = (int)(b >> 23) - 127;   // a = 1.m * 2^k (subnormals land far below KV_MIN_EXP)
+    return max(k - 8 + ((b & 0x7fffffu) > 0x600000u), KV_MIN_EXP);
+}
+
+// The codes of n words in a unit 1 / f times as large, by `threads` threads th.
+__device__ __forceinline__ void recode(uint8_t *codes, int n, float f, int th, int threads)
+{
+    for (int x = th; x < n; x += threads) {
+        const uint32_t w = ((const uint32_t *)codes)[x];
+        const uint32_t a0 = e4m3x2_f16x2((uint16_t)w), a1 = e4m3x2_f16x2((uint16_t)(w >> 16));
+        const float2 x0 = __half22float2(u32_h2(a0)), x1 = __half22float2(u32_h2(a1));
+        ((uint32_t *)codes)[x] = f32x2_e4m3x2(x0.x * f, x0.y * f) | (uint32_t)f32x2_e4m3x2(x1.x * f, x1.y * f) << 16;
+    }
+}
+
 // ---------------------------------------------------------------- tensor-core product -------
 
 // d += a b: 16 x 8 fp32 += (16 x 16 f16) (16 x 8 f16)

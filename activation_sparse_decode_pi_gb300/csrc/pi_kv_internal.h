@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include "pi_kv.h"
+#include "pi_proj_internal.h"
 
 namespace pi {
 
@@ -83,6 +84,18 @@ PI_KV_EXTERN(128, 2) PI_KV_EXTERN(256, 1) PI_KV_EXTERN(256, 2)
 
 cudaError_t launch_kv_append(const KvView &c, const KvBatch &b, const KvLayerDev &l, const void *k_new,
                              const void *v_new, int64_t ld, int dtype, int nsm, cudaStream_t s);
+
+struct KvAppendRotArgs {
+    KvView c;
+    KvBatch b;
+    KvLayerDev l;
+    RotaryDev r;
+    const void *q, *k, *v;
+    void *qo;
+    int64_t ldq, ldqo, ld;   // elements
+    int cap;                 // the launch's: tokens of a page with a place in the table of cosines and sines
+};
+cudaError_t launch_kv_append_rot(const KvAppendRotArgs &a, int dtype, int nsm, cudaStream_t s);
 
 struct KvCopyList {
     int32_t *src, *dst, *count;   // device; count: one int32

@@ -1,0 +1,56 @@
+// pi_proj_internal.h -- what the host side of pi_proj.h (pi_proj_api.cu) and its kernels share.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <cuda_fp16.h>
+#include <stdint.h>
+
+#include "pi_internal.h"
+#include "pi_proj.h"
+
+namespace pi {
+
+struct Int4Args {
+    const uint8_t *w;      // [n x k/2]
+    const __half *s;       // [n x k/128]
+    const float *bias;     // [n] or NULL
+    const void *x, *add;   // add: or NULL
+    void *y;
+    int64_t ldx, ldadd, ldy;   // elements
+    int n, k, rows;
+    int kw, cluster, chunk;    // the launch's: warps along k, CTAs along k, groups of x in shared memory
+};
+cudaError_t launch_int4_linear(const Int4Args &a, int dtype, int nsm, cudaStream_t s);
+
+struct RotaryDev {
+    const uint64_t *turns;
+    const float *qn, *kn;
+    int rot, interleaved, norm;
+    float amp, eps;
+};
+
+struct RotateArgs {
+    RotaryDev r;
+    const int32_t *pos;
+    const void *q, *k;
+    void *qo, *ko;
+    int64_t ldq, ldqo, ldk, ldko;   // elements
+    int n_tokens, hq, hk;
+    int parts_q, parts_k;           // the launch's: warps that share a token's heads
+};
+cudaError_t launch_rotate(const RotateArgs &a, int dim, int dtype, int nsm, cudaStream_t s);
+
+// The arguments that pi_rotate and pi_kv_append_rotated share (pi_proj_api.cu).
+pi_status_t check_rotary(const pi_rotary_t *r, int head_dim, int dev, RotaryDev *out);
+
+// Two strided arrays on the device: es bytes an element, `rows` rows of `width` elements ld apart.
+struct Strided {
+    const void *p;
+    int64_t rows, width, ld;
+    int es;
+};
+bool same_place(const Strided &a, const Strided &b);
+// Whether an element of one may be one of the other (parts of one row layout, side by side, are not).
+bool may_overlap(const Strided &a, const Strided &b);
+
+}  // namespace pi

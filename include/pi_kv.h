@@ -31,6 +31,7 @@
 #define PI_KV_H
 
 #include "pi_ffn.h"
+#include "pi_proj.h"
 
 #ifdef __cplusplus
 extern "C" {
@@ -102,6 +103,18 @@ pi_status_t pi_kv_reserve(pi_kv_t *h, const int32_t *seqs, const int32_t *tok_st
 pi_status_t pi_kv_append(pi_kv_t *h, int32_t layer, const int32_t *seqs, const int32_t *tok_start, int32_t n,
                          int32_t n_tokens, const void *k_new, const void *v_new, int64_t ld, int32_t dtype,
                          void *stream);
+
+/*
+ * pi_kv_append with the norms and the rotation of pi_rotate in the same pass: the keys' heads are normed and turned by
+ * their tokens' positions in the sequences (the last n_i) and then coded, from fp32; values are coded as they are; q_out
+ * = the queries' heads, normed and turned. q, q_out: [n_tokens x n_heads x head_dim] of `dtype`, row t at element t *
+ * ld_q (ld_q_out), bases and row strides multiples of 16 bytes; q_out is q (same address and stride) or touches no other
+ * array of the call. A sequence that pi_kv_append would skip keeps its rows of q_out as they were.
+ */
+pi_status_t pi_kv_append_rotated(pi_kv_t *h, int32_t layer, const int32_t *seqs, const int32_t *tok_start, int32_t n,
+                                 int32_t n_tokens, const pi_rotary_t *rotary, const void *q, int64_t ld_q, void *q_out,
+                                 int64_t ld_q_out, const void *k_new, const void *v_new, int64_t ld, int32_t dtype,
+                                 void *stream);
 
 /*
  * Attention of each sequence's last n_i tokens over the sequence's cache in layer `layer`. The
