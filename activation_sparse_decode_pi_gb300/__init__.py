@@ -39,7 +39,7 @@ EXPORTS = (
     "pi_ffn_set_phase_trace",
     "pi_kv_create", "pi_kv_destroy", "pi_kv_get_status", "pi_kv_reserve", "pi_kv_append", "pi_kv_attend",
     "pi_kv_fork", "pi_kv_free", "pi_kv_trim", "pi_kv_copy_pages", "pi_kv_compact",
-    "pi_kv_append_rotated", "pi_rotate", "pi_int4_linear",
+    "pi_kv_append_rotated", "pi_kv_share", "pi_kv_attend_shared", "pi_rotate", "pi_int4_linear",
 )
 PI_STACK_PHASES = 8
 STACK_PHASE_NAMES = ("layer_start", "hidden_done", "logits_start", "list_ready", "first_rows", "ffn_done",
@@ -139,6 +139,8 @@ for _name, _args in {
     "pi_kv_compact": [_P, _P, _P],
     "pi_kv_append_rotated": [_P, _I32, _P, _P, _I32, _I32, ctypes.POINTER(PiRotary), _P, _I64, _P, _I64, _P, _P, _I64,
                              _I32, _P],
+    "pi_kv_share": [_P, _P, _P, _I32, _P, _I32, _P, _P],
+    "pi_kv_attend_shared": [_P, _I32, _P, _P, _I32, _I32, _P, _I32, _P, _I64, _P, _I64, _P, _I32, _F32, _P, _P],
     "pi_rotate": [ctypes.POINTER(PiRotary), _P, _I32, _I32, _I32, _I32, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _I32, _P],
     "pi_int4_linear": [_P, _P, _P, _I32, _I32, _P, _I64, _I32, _P, _I64, _P, _I64, _I32, _P],
 }.items():
@@ -332,6 +334,18 @@ def pi_kv_append_rotated(h, layer, seqs, tok_start, n, n_tokens, rotary, q, ld_q
     _check(_lib.pi_kv_append_rotated(h, layer, _ptr(seqs), _ptr(tok_start), n, n_tokens, ctypes.byref(rotary), _ptr(q),
                                      ld_q, _ptr(q_out), ld_q_out, _ptr(k_new), _ptr(v_new), ld, dtype, _stream(stream)),
            "pi_kv_append_rotated")
+
+
+def pi_kv_share(h, seqs, tok_start, n, group_start, n_groups, plan, stream=None) -> None:
+    _check(_lib.pi_kv_share(h, _ptr(seqs), _ptr(tok_start), n, _ptr(group_start), n_groups, _ptr(plan), _stream(stream)),
+           "pi_kv_share")
+
+
+def pi_kv_attend_shared(h, layer, seqs, tok_start, n, n_tokens, plan, n_groups, q, ld_q, out, ld_out, lse, dtype, scale,
+                        work, stream=None) -> None:
+    _check(_lib.pi_kv_attend_shared(h, layer, _ptr(seqs), _ptr(tok_start), n, n_tokens, _ptr(plan), n_groups, _ptr(q), ld_q,
+                                    _ptr(out), ld_out, _ptr(lse), dtype, scale, _ptr(work), _stream(stream)),
+           "pi_kv_attend_shared")
 
 
 def pi_rotate(rotary, pos, n_tokens, n_heads, n_kv_heads, head_dim, q, ld_q, q_out, ld_q_out, k, ld_k, k_out, ld_k_out,
@@ -760,7 +774,15 @@ class KVCache:
         """Attention of q [tokens, heads, dim], the sequences' last positions, over their cache; returns out
         (q's type). window > 0: only the last `window` positions and the first `sinks` are seen. lse: fp32
         [tokens, heads], filled with the log of each row's sum of exponentials."""
-        n, T, heads, dim = seqs.shape[0], q.shape[0], self.n_heads, self.head_dim
+        n, T = seqs.shape[0], q.shape[0]
+        out, args = self._attend_args(q, out, lse, stream)
+        pi_kv_attend(self.h, layer, _i32(seqs, "seqs"), _i32(tok_start, "tok_start", n + 1), n, T, *args,
+                     self.head_dim ** -0.5 if scale is None else scale, window, sinks, stream)
+        return out
+
+    def _attend_args(self, q, out, lse, stream):
+        """out (made where it is None), and the addresses and strides of q, out and lse with q's type."""
+        T, heads, dim = q.shape[0], self.n_heads, self.head_dim
         ld, dtype = _token_rows(q, heads, dim, "q"), _act_dtype(q)
         if out is None:
             out, ld_out = _empty((T, heads, dim), q.dtype, q.device, stream), heads * dim
@@ -772,8 +794,34 @@ class KVCache:
             if _act_dtype(lse) != PI_F32 or tuple(lse.shape) != (T, heads) or not lse.is_contiguous():
                 raise ValueError(f"lse: contiguous fp32 [{T}, {heads}]")
             lse = lse.data_ptr()
-        pi_kv_attend(self.h, layer, _i32(seqs, "seqs"), _i32(tok_start, "tok_start", n + 1), n, T, q.data_ptr(), ld,
-                     out.data_ptr(), ld_out, lse, dtype, dim ** -0.5 if scale is None else scale, window, sinks, stream)
+        return out, (q.data_ptr(), ld, out.data_ptr(), ld_out, lse, dtype)
+
+    def share(self, seqs, tok_start, group_start, stream=None):
+        """What groups of the call's sequences share (group g: group_start[g] .. group_start[g + 1] of seqs), for
+        attend_shared: an int32 tensor. It serves every layer and later steps of the same seqs and tok_start while the
+        sequences only grow."""
+        n, groups = seqs.shape[0], group_start.shape[0] - 1
+        plan = _empty(3 * (n + groups) + 2, group_start.dtype, group_start.device, stream)
+        pi_kv_share(self.h, _i32(seqs, "seqs"), _i32(tok_start, "tok_start", n + 1), n, _i32(group_start, "group_start"),
+                    groups, plan.data_ptr(), stream)
+        return plan
+
+    def attend_shared(self, layer, seqs, tok_start, plan, q, out=None, lse=None, *, scale=None, work=None, stream=None):
+        """attend (without a window) with the plan's shared prefixes read once for all sequences of a group. work: fp32, at
+        least tokens * heads * (dim + 2) elements to use in between."""
+        n, T = seqs.shape[0], q.shape[0]
+        groups = (plan.shape[0] - 2) // 3 - n if plan.dim() == 1 else -1
+        if groups < 0 or groups > n:
+            raise ValueError(f"plan: what share returned for these {n} sequences")
+        out, args = self._attend_args(q, out, lse, stream)
+        room = T * self.n_heads * (self.head_dim + 2)
+        if work is None:
+            work = _empty(room, self.layers[0]["k_scale"].dtype, q.device, stream)
+        elif _act_dtype(work) != PI_F32 or work.numel() < room or not work.is_contiguous():
+            raise ValueError(f"work: contiguous fp32 of {room} elements")
+        pi_kv_attend_shared(self.h, layer, _i32(seqs, "seqs"), _i32(tok_start, "tok_start", n + 1), n, T,
+                            _i32(plan, "plan", 3 * (n + groups) + 2), groups, *args,
+                            self.head_dim ** -0.5 if scale is None else scale, work.data_ptr(), stream)
         return out
 
     def fork(self, src, dst, stream=None) -> None:

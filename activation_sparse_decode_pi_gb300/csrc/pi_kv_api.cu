@@ -216,6 +216,8 @@ pi_status_t kv_create(pi_kv_t **out, const pi_kv_desc_t *desc, const pi_kv_layer
     return PI_OK;
 }
 
+int elt_size(int32_t dtype) { return dtype == PI_F32 ? 4 : dtype == PI_BF16 || dtype == PI_F16 ? 2 : 0; }
+
 // The handle is used on the device it was made on, with a list of at most PI_KV_MAX_CALL_SEQS sequences.
 pi_status_t check_call(const pi_kv_t *h, int32_t n)
 {
@@ -240,7 +242,52 @@ pi_status_t check_rows(const pi_kv_t *h, const void *p, int64_t n_tokens, int64_
     return check_ptr(p, (size_t)(((n_tokens - 1) * ld + width) * es), 16, h->dev);
 }
 
-int elt_size(int32_t dtype) { return dtype == PI_F32 ? 4 : dtype == PI_BF16 || dtype == PI_F16 ? 2 : 0; }
+// The arguments of an attention, checked; a is filled where there is something to do.
+pi_status_t attend_args(const pi_kv_t *h, int32_t layer, const int32_t *seqs, const int32_t *tok_start, int32_t n,
+                        int32_t n_tokens, const void *q, int64_t ld_q, void *out, int64_t ld_out, float *lse, int32_t dtype,
+                        float scale, int32_t window, int32_t sinks, KvAttendArgs *to)
+{
+    pi_status_t s;
+    if ((s = check_call(h, n))) return s;
+    const int es = elt_size(dtype);
+    const double scale_log2 = (double)scale * 1.4426950408889634;
+    if (layer < 0 || layer >= h->desc.n_layers || n_tokens < 0 || n_tokens > KV_MAX_LEN || !es || sinks < 0 ||
+        !(std::fabs(scale_log2) <= (double)FLT_MAX))   // (a NaN scale fails too)
+        return PI_ERR_INVALID_ARG;
+    if (n == 0 || n_tokens == 0) return PI_OK;
+    if ((s = check_batch(h, seqs, tok_start, n))) return s;
+    const int64_t width = (int64_t)h->desc.n_heads * h->desc.head_dim;
+    if ((s = check_rows(h, q, n_tokens, width, ld_q, es))) return s;
+    if ((s = check_rows(h, out, n_tokens, width, ld_out, es))) return s;
+    if (lse && (s = check_ptr(lse, (size_t)n_tokens * h->desc.n_heads * 4, 4, h->dev))) return s;
+    KvAttendArgs &a = *to;
+    a.c = h->view;
+    a.b = {seqs, tok_start, n, n_tokens, nullptr, nullptr, nullptr};
+    a.l = h->layers[layer];
+    a.q = q;
+    a.out = out;
+    a.lse = lse;
+    a.ldq = ld_q;
+    a.ldo = ld_out;
+    a.dtype = dtype;
+    a.scale_log2 = (float)scale_log2;
+    // no window: one that is never shorter than the distance of two positions (all below 2^30)
+    a.window = window > 0 ? std::min(window, KV_MAX_LEN) : KV_MAX_LEN;
+    a.sinks = std::min(sinks, KV_MAX_LEN);
+    a.part = h->part;
+    a.part_ml = h->part_ml;
+    a.tickets = h->tickets;
+    a.rows_part = h->rows_part;
+    a.rows_ml = h->rows_ml;
+    a.rows_tickets = h->rows_tickets;
+    return PI_OK;
+}
+
+cudaError_t attend(const pi_kv_t *h, int32_t layer, const KvAttendArgs &a, cudaStream_t s)
+{
+    const auto run = h->desc.head_dim == 64 ? attend_of<64> : h->desc.head_dim == 128 ? attend_of<128> : attend_of<256>;
+    return run(h, layer, a, s);
+}
 
 }  // namespace
 
@@ -288,7 +335,7 @@ pi_status_t pi_kv_reserve(pi_kv_t *h, const int32_t *seqs, const int32_t *tok_st
     if ((s = check_call(h, n))) return s;
     if (n == 0) return PI_OK;
     if ((s = check_batch(h, seqs, tok_start, n))) return s;
-    return cuda_status(launch_kv_reserve(h->view, {seqs, tok_start, n, INT32_MAX}, h->list_dst, (cudaStream_t)stream));
+    return cuda_status(launch_kv_reserve(h->view, {seqs, tok_start, n, INT32_MAX, nullptr, nullptr, nullptr}, h->list_dst, (cudaStream_t)stream));
 }
 
 pi_status_t pi_kv_append(pi_kv_t *h, int32_t layer, const int32_t *seqs, const int32_t *tok_start, int32_t n,
@@ -304,7 +351,7 @@ pi_status_t pi_kv_append(pi_kv_t *h, int32_t layer, const int32_t *seqs, const i
     const int64_t width = (int64_t)h->desc.n_kv_heads * h->desc.head_dim;
     if ((s = check_rows(h, k_new, n_tokens, width, ld, es))) return s;
     if ((s = check_rows(h, v_new, n_tokens, width, ld, es))) return s;
-    return cuda_status(launch_kv_append(h->view, {seqs, tok_start, n, n_tokens}, h->layers[layer], k_new, v_new, ld,
+    return cuda_status(launch_kv_append(h->view, {seqs, tok_start, n, n_tokens, nullptr, nullptr, nullptr}, h->layers[layer], k_new, v_new, ld,
                                         dtype, h->nsm, (cudaStream_t)stream));
 }
 
@@ -330,7 +377,7 @@ pi_status_t pi_kv_append_rotated(pi_kv_t *h, int32_t layer, const int32_t *seqs,
     const Strided sk{k_new, n_tokens, width, ld, es}, sv{v_new, n_tokens, width, ld, es};
     if ((!same_place(sq, so) && may_overlap(sq, so)) || may_overlap(so, sk) || may_overlap(so, sv)) return PI_ERR_INVALID_ARG;
     a.c = h->view;
-    a.b = {seqs, tok_start, n, n_tokens};
+    a.b = {seqs, tok_start, n, n_tokens, nullptr, nullptr, nullptr};
     a.l = h->layers[layer];
     a.q = q;
     a.k = k_new;
@@ -347,40 +394,52 @@ pi_status_t pi_kv_attend(pi_kv_t *h, int32_t layer, const int32_t *seqs, const i
                          int32_t dtype, float scale, int32_t window, int32_t sinks, void *stream)
 {
     pi_status_t s;
-    if ((s = check_call(h, n))) return s;
-    const int es = elt_size(dtype);
-    const double scale_log2 = (double)scale * 1.4426950408889634;
-    if (layer < 0 || layer >= h->desc.n_layers || n_tokens < 0 || n_tokens > KV_MAX_LEN || !es || sinks < 0 ||
-        !(std::fabs(scale_log2) <= (double)FLT_MAX))   // (a NaN scale fails too)
-        return PI_ERR_INVALID_ARG;
+    KvAttendArgs a = {};
+    if ((s = attend_args(h, layer, seqs, tok_start, n, n_tokens, q, ld_q, out, ld_out, lse, dtype, scale, window, sinks, &a)))
+        return s;
     if (n == 0 || n_tokens == 0) return PI_OK;
+    return cuda_status(attend(h, layer, a, (cudaStream_t)stream));
+}
+
+pi_status_t pi_kv_share(pi_kv_t *h, const int32_t *seqs, const int32_t *tok_start, int32_t n, const int32_t *group_start,
+                        int32_t n_groups, int32_t *plan, void *stream)
+{
+    pi_status_t s;
+    if ((s = check_call(h, n))) return s;
+    if (n_groups < 0 || n_groups > n) return PI_ERR_INVALID_ARG;
+    if (n == 0) return PI_OK;
     if ((s = check_batch(h, seqs, tok_start, n))) return s;
-    const int64_t width = (int64_t)h->desc.n_heads * h->desc.head_dim;
-    if ((s = check_rows(h, q, n_tokens, width, ld_q, es))) return s;
-    if ((s = check_rows(h, out, n_tokens, width, ld_out, es))) return s;
-    if (lse && (s = check_ptr(lse, (size_t)n_tokens * h->desc.n_heads * 4, 4, h->dev))) return s;
-    KvAttendArgs a;
-    a.c = h->view;
-    a.b = {seqs, tok_start, n, n_tokens};
-    a.l = h->layers[layer];
-    a.q = q;
-    a.out = out;
-    a.lse = lse;
-    a.ldq = ld_q;
-    a.ldo = ld_out;
-    a.dtype = dtype;
-    a.scale_log2 = (float)scale_log2;
-    // no window: one that is never shorter than the distance of two positions (all below 2^30)
-    a.window = window > 0 ? std::min(window, KV_MAX_LEN) : KV_MAX_LEN;
-    a.sinks = std::min(sinks, KV_MAX_LEN);
-    a.part = h->part;
-    a.part_ml = h->part_ml;
-    a.tickets = h->tickets;
-    a.rows_part = h->rows_part;
-    a.rows_ml = h->rows_ml;
-    a.rows_tickets = h->rows_tickets;
-    const auto run = h->desc.head_dim == 64 ? attend_of<64> : h->desc.head_dim == 128 ? attend_of<128> : attend_of<256>;
-    return cuda_status(run(h, layer, a, (cudaStream_t)stream));
+    if ((s = check_ptr(group_start, ((size_t)n_groups + 1) * 4, 4, h->dev))) return s;
+    if ((s = check_ptr(plan, (size_t)PI_KV_SHARE_INTS(n, n_groups) * 4, 4, h->dev))) return s;
+    return cuda_status(launch_kv_share(h->view, {seqs, tok_start, n, KV_MAX_LEN, nullptr, nullptr, nullptr}, group_start,
+                                       n_groups, plan, (cudaStream_t)stream));
+}
+
+pi_status_t pi_kv_attend_shared(pi_kv_t *h, int32_t layer, const int32_t *seqs, const int32_t *tok_start, int32_t n,
+                                int32_t n_tokens, const int32_t *plan, int32_t n_groups, const void *q, int64_t ld_q,
+                                void *out, int64_t ld_out, float *lse, int32_t dtype, float scale, void *work, void *stream)
+{
+    pi_status_t s;
+    KvAttendArgs a = {};
+    if (n_groups < 0 || n_groups > n) return PI_ERR_INVALID_ARG;
+    if ((s = attend_args(h, layer, seqs, tok_start, n, n_tokens, q, ld_q, out, ld_out, lse, dtype, scale, 0, 0, &a))) return s;
+    if (n == 0 || n_tokens == 0) return PI_OK;
+    if ((s = check_ptr(plan, (size_t)PI_KV_SHARE_INTS(n, n_groups) * 4, 4, h->dev))) return s;
+    const int64_t rows = (int64_t)n_tokens * h->desc.n_heads;
+    if ((s = check_ptr(work, (size_t)rows * (h->desc.head_dim + 2) * 4, 16, h->dev))) return s;
+    a.prior = (float *)work;
+    a.prior_ml = a.prior + rows * h->desc.head_dim;
+    const int32_t *lead = plan, *start = lead + n_groups, *len = start + n_groups + 1, *skip = len + n_groups, *was = skip + n;
+    if (n_groups > 0) {
+        KvAttendArgs first = a;
+        first.pass = 1;
+        first.b = {lead, start, n_groups, n_tokens, len, nullptr, nullptr};
+        if ((s = cuda_status(attend(h, layer, first, (cudaStream_t)stream)))) return s;
+    }
+    a.pass = 2;
+    a.b.skip = skip;
+    a.b.was = was;
+    return cuda_status(attend(h, layer, a, (cudaStream_t)stream));
 }
 
 pi_status_t pi_kv_fork(pi_kv_t *h, const int32_t *src, const int32_t *dst, int32_t n, void *stream)

@@ -12,6 +12,7 @@ namespace pi {
 
 struct KvSeq {
     int row, len, start, n;   // table row, tokens held, first row of the call's arrays, new tokens
+    int skip;                 // positions below this are another pass's
 };
 
 // Sequence i of the call, its fields brought into range; what was out of range is flagged and reads
@@ -24,14 +25,23 @@ __device__ __forceinline__ KvSeq kv_sequence(const KvView &c, const KvBatch &b, 
     bool bad = s.row < 0 || s.row >= c.max_seqs || s0 < 0 || s1 < s0 || s1 > b.n_tokens;
     s.start = s0;
     s.n = s1 - s0;
-    s.len = 0;
+    s.len = s.skip = 0;
+    if (b.skip && (b.was[i] != s.row || b.was[b.n + i] != s0 || b.was[b.n + i + 1] != s1)) bad = true;
     if (bad) {
         s.row = s.start = s.n = 0;
     } else {
-        s.len = c.length[s.row];
+        s.len = b.len ? b.len[i] : c.length[s.row];
         if (s.len < 0 || s.len > c.max_pages * c.page) {
             s.len = s.n = 0;
             bad = true;
+        }
+        if (b.len && s.len == 0) s.n = 0;   // nothing shared
+        if (b.skip) {
+            s.skip = b.skip[i];
+            if (s.skip < 0 || s.skip % KV_SHARE || s.skip > s.len - s.n) {
+                s.skip = s.len = s.n = 0;
+                bad = true;
+            }
         }
     }
     if (bad && flag) set_status(c.status, ST_DEVICE_CHECK);
@@ -286,13 +296,42 @@ __device__ __forceinline__ float row_lse(float M, float S)
     return S == 0.f ? -INFINITY : (M + log2f(S)) * 0.6931471805599453f;
 }
 
+// Weights of two partial sums with maxima (or references) ma, mb and sums sa, sb against their common maximum M; S: the
+// joined sum. A sum whose maximum is -infinity counts only where it is not 0 (it is NaN then).
+struct JoinedRow {
+    float wa, wb, M, S;
+    __device__ __forceinline__ JoinedRow(float ma, float sa, float mb, float sb)
+    {
+        M = fmaxf(ma, mb);
+        wa = ma == -INFINITY ? (sa != 0.f ? 1.f : 0.f) : ex2(ma - M);
+        wb = mb == -INFINITY ? (sb != 0.f ? 1.f : 0.f) : ex2(mb - M);
+        S = wa * sa + wb * sb;
+    }
+};
+
 // Four columns (from d) of row `r` (query token r / G, head r % G of kv head h) of the sequence f (table row,
 // length, start, new tokens): numerators o over the sum S, and with d = 0 the row's log of the sum.
 __device__ __forceinline__ void store_row(const KvAttendArgs &a, const int4 &f, int h, int G, int D, int r, int d,
-                                          float4 o, float M, float S)
+                                          float4 o, float M, float S, bool join = false)
 {
     const int64_t tok = (int64_t)f.z + r / G;
     const int head = h * G + r % G;
+    if (a.pass) {
+        float *const po = a.prior + (tok * a.c.hq + head) * D + d, *const pml = a.prior_ml + (tok * a.c.hq + head) * 2;
+        if (a.pass == 1) {
+            *(float4 *)po = o;
+            if (d == 0) *(float2 *)pml = make_float2(M, S);
+            return;
+        }
+        if (join) {
+            const float2 ml = __ldcg((const float2 *)pml);
+            const float4 v = __ldcg((const float4 *)po);
+            const JoinedRow j(M, S, ml.x, ml.y);
+            o = make_float4(o.x * j.wa + v.x * j.wb, o.y * j.wa + v.y * j.wb, o.z * j.wa + v.z * j.wb, o.w * j.wa + v.w * j.wb);
+            M = j.M;
+            S = j.S;
+        }
+    }
     const float inv = 1.f / S;
     // S = 0: nothing seen. (A NaN sum stays: it is not equal to 0.)
     const float v[4] = {S == 0.f ? 0.f : o.x * inv, S == 0.f ? 0.f : o.y * inv, S == 0.f ? 0.f : o.z * inv,

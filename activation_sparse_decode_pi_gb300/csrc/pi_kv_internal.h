@@ -31,6 +31,9 @@ struct KvLayerDev {
 struct KvBatch {
     const int32_t *seqs, *start;
     int n, n_tokens;
+    const int32_t *len;    // lengths to take in place of the sequences' own, or NULL
+    const int32_t *skip;   // positions of each sequence that another pass attends to, or NULL
+    const int32_t *was;    // with skip: [n] table rows and [n + 1] starts that the plan was made for
 };
 
 struct KvAttendArgs {
@@ -52,7 +55,12 @@ struct KvAttendArgs {
     float *rows_part;          // rows kernel, split items: numerators [items * splits][rows][dim]
     float *rows_ml;            // their references and sums [items * splits][rows][2]
     uint32_t *rows_tickets;    // [items], zero on entry, left zero
+    // Attention in two passes (pi_kv_attend_shared): the first leaves every row's numerators, maximum and sum, the second
+    // adds them to its own.
+    int pass;                  // 0: one pass alone; 1: the first, whose rows all see positions [0, length); 2: the second
+    float *prior, *prior_ml;   // [n_tokens x hq][dim], [n_tokens x hq][2]
 };
+constexpr int KV_SHARE = 128;   // a shared prefix is a multiple of this: whole tiles of both kernels, whole pages
 
 // The split kernel (pi_kv_split.cuh) of one head dim; QN: runs of 8 rows per tile, T: 16-bit terms.
 template <int D, int QN, int T>
@@ -108,6 +116,8 @@ cudaError_t launch_kv_trim(const KvView &c, const int32_t *seqs, int n, int wind
 cudaError_t launch_kv_compact(const KvView &c, const KvCopyList &l, int32_t *map, int32_t *n_live, cudaStream_t s);
 // Copies the listed pages in every layer (layers: device array) and, with map, renames every table entry.
 // max_count: an upper bound of *count known to the host.
+// plan: see pi_kv_share in pi_kv.h
+cudaError_t launch_kv_share(const KvView &c, const KvBatch &b, const int32_t *groups, int n_groups, int32_t *plan, cudaStream_t s);
 cudaError_t launch_kv_copy(const KvView &c, const KvLayerDev *layers, const int32_t *src, const int32_t *dst,
                            const int32_t *count, int max_count, const int32_t *map, int nsm, cudaStream_t s);
 

@@ -236,9 +236,11 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
     if (s_item[0] < 0) return;
     const KvSeq sq = sh.seq;
     const int h = s_item[2], row0 = s_item[1] * C::ROWS, rows = min(C::ROWS, sq.n * G - row0), p0 = sq.len - sq.n;
-    const int pos_lo = p0 + row0 / G, pos_hi = p0 + (row0 + rows - 1) / G;
+    const bool flat = a.pass == 1;   // every row sees the whole length
+    const int pos_lo = flat ? sq.len - 1 : p0 + row0 / G, pos_hi = flat ? sq.len - 1 : p0 + (row0 + rows - 1) / G;
+    const bool join = a.pass == 2 && sq.skip > 0;
     // tiles [0, ns) and [w0, w1) hold what the rows see; this CTA takes its split's share of them
-    const int w0 = max(0, pos_lo - a.window + 1) / TOK, w1 = pos_hi < 0 ? w0 : pos_hi / TOK + 1;
+    const int w0 = max(sq.skip, pos_lo - a.window + 1) / TOK, w1 = pos_hi < 0 ? w0 : pos_hi / TOK + 1;
     const int ns = pos_hi >= 0 ? min((a.sinks + TOK - 1) / TOK, w0) : 0;
     const int nt_all = ns + max(w1 - w0, 0), splits = gridDim.y;
     const int k0 = (int)((long long)nt_all * blockIdx.y / splits), k1 = (int)((long long)nt_all * (blockIdx.y + 1) / splits);
@@ -283,7 +285,7 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
 
     const int grp = warp >> 3, half = (warp >> 2) & 1, row = grp * 128 + (warp & 3) * 32 + lane;   // of a row's thread
     const bool mine = tid < C::RT, on = mine && row < rows;
-    const int pos = on ? p0 + (row0 + row) / G : -1;
+    const int pos = !on ? -1 : flat ? sq.len - 1 : p0 + (row0 + row) / G;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -679,7 +681,20 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
         bar_sync(2 + grp, 256);
         l += s_half[half ^ 1][row];
         // (the unit, which may be as small as an append's 2^-120, is multiplied in by itself: its quotient would lose bits)
-        const float back = exp2i(-(int)ROWS_UNIT), norm = splits > 1 ? back : l == 0.f ? 0.f : back / l;
+        const float back = exp2i(-(int)ROWS_UNIT), norm = splits > 1 || a.pass == 1 ? back : l == 0.f ? 0.f : back / l;
+        // of a row that another pass has begun: its sums join this one's here (a split item's where its parts are added)
+        const int64_t prow = ((int64_t)sq.start + (row0 + row) / G) * c.hq + h * G + (row0 + row) % G;
+        const bool joins = join && splits == 1 && on;
+        float mine_w = norm, prior_w = 0.f, M = m, S = l;
+        if (joins) {
+            const float2 ml = __ldcg((const float2 *)(a.prior_ml + prow * 2));
+            const JoinedRow j(m, l, ml.x, ml.y);
+            const float inv = j.S == 0.f ? 0.f : 1.f / j.S;
+            mine_w = j.wa * inv * back;
+            prior_w = j.wb * inv;
+            M = j.M;
+            S = j.S;
+        }
         const int64_t at = ((int64_t)blockIdx.x * splits + blockIdx.y) * C::ROWS + row;
         const int64_t at_out = ((int64_t)sq.start + (row0 + row) / G) * a.ldo + (int64_t)(h * G + (row0 + row) % G) * D;
 #pragma unroll 1
@@ -692,14 +707,24 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
             if (on) {
                 float f[32];   // l = 0: nothing seen (a NaN sum stays: it is not equal to 0)
 #pragma unroll
-                for (int e = 0; e < 32; ++e) f[e] = nt == 0 || l == 0.f ? 0.f : __uint_as_float(o[e]) * norm * unit;
+                for (int e = 0; e < 32; ++e) f[e] = nt == 0 || l == 0.f ? 0.f : __uint_as_float(o[e]) * mine_w * unit;
+                if (joins) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4) {
+                        const float4 v = __ldcg((const float4 *)(a.prior + prow * D + x + e));
+                        f[e] += v.x * prior_w, f[e + 1] += v.y * prior_w, f[e + 2] += v.z * prior_w, f[e + 3] += v.w * prior_w;
+                    }
+                }
                 if (splits > 1) store_f32<32>(a.rows_part + at * D + x, f);
+                else if (a.pass == 1) store_f32<32>(a.prior + prow * D + x, f);
                 else store_out<32>(a, at_out + x, f);
             }
             __syncwarp();   // the next load of tensor memory takes the whole warp, lanes past the last row too
         }
-        if (splits == 1 && on && half == 0 && a.lse)
-            a.lse[((int64_t)sq.start + (row0 + row) / G) * c.hq + h * G + (row0 + row) % G] = row_lse(m, l);
+        if (splits == 1 && on && half == 0) {
+            if (a.pass == 1) *(float2 *)(a.prior_ml + prow * 2) = make_float2(m, l);
+            else if (a.lse) a.lse[prow] = row_lse(M, S);
+        }
         if (splits > 1 && on && half == 0) {
             a.rows_ml[at * 2] = m;
             a.rows_ml[at * 2 + 1] = l;
@@ -734,7 +759,7 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
                 S += w * ly;
                 o.x += v.x * w, o.y += v.y * w, o.z += v.z * w, o.w += v.w * w;
             }
-            store_row(a, f4, h, G, D, row0 + r, d, o, M, S);
+            store_row(a, f4, h, G, D, row0 + r, d, o, M, S, join);
         }
         if (tid == 0) a.rows_tickets[blockIdx.x] = 0;
     }

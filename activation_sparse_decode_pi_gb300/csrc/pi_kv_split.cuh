@@ -97,6 +97,7 @@ __global__ void __launch_bounds__(SplitCfg<D, QN, T>::NT, 1)
     uint64_t *full = (uint64_t *)(meta + slots), *empty = full + slots;
     long long *prefix = (long long *)(empty + slots);                      // [n + 1] tiles before sequence i
     int4 *info = (int4 *)((uintptr_t)(prefix + a.b.n + 2) & ~(uintptr_t)15);   // [n] row, length, start, new tokens
+    int *skips = (int *)(info + a.b.n);                                        // [n] in a second pass (a.pass == 2)
     __shared__ long long wtot[C::NT / 32];
     __shared__ uint64_t jfull[2], jempty[2];   // results of a segment: written, joined
     __shared__ int s_last[2], s_dead;
@@ -123,8 +124,10 @@ __global__ void __launch_bounds__(SplitCfg<D, QN, T>::NT, 1)
     pdl_launch_dependents();
 
     // tiles of every sequence, and their running sum
-    auto view = [&](int L, int nq, int &w0, int &ns, int &nt) {   // tiles [0, ns) and [w0, ...) are read
-        w0 = max(0, L - nq - a.window + 1) / KV_TILE;
+    const bool flat = a.pass == 1, second = a.pass == 2;   // flat: every row sees the whole length
+    // of sequence i with L positions, nq of them new: tiles [0, ns) and [w0, ...) are read
+    auto view = [&](int i, int L, int nq, int &w0, int &ns, int &nt) {
+        w0 = max(second ? skips[i] : 0, L - nq - a.window + 1) / KV_TILE;
         const int w1 = max((L + KV_TILE - 1) / KV_TILE, w0 + 1);
         ns = min((a.sinks + KV_TILE - 1) / KV_TILE, w0);
         nt = ns + w1 - w0;
@@ -137,8 +140,9 @@ __global__ void __launch_bounds__(SplitCfg<D, QN, T>::NT, 1)
             KvSeq q = kv_sequence(c, a.b, i, blockIdx.x == 0);
             if ((long long)q.n * G >= a.rows_from) q.n = 0;   // the rows kernel's
             info[i] = make_int4(q.row, q.len, q.start, q.n);
+            if (second) skips[i] = q.skip;
             int w0, ns, nt;
-            view(q.len, q.n, w0, ns, nt);
+            view(i, q.len, q.n, w0, ns, nt);
             w = (((long long)q.n * G + R - 1) / R) * (nt + SPLIT_ITEM) * c.hkv;
         }
         long long inc = w;
@@ -178,7 +182,7 @@ __global__ void __launch_bounds__(SplitCfg<D, QN, T>::NT, 1)
         s.i = lo;
         const int4 f = info[lo];
         int w0, ns;
-        view(f.y, f.w, w0, ns, s.nt);
+        view(lo, f.y, f.w, w0, ns, s.nt);
         const long long local = t - prefix[lo], item = local / (s.nt + SPLIT_ITEM);
         const int rts = (int)(((long long)f.w * G + R - 1) / R);
         s.h = (int)(item / rts);
@@ -200,7 +204,7 @@ __global__ void __launch_bounds__(SplitCfg<D, QN, T>::NT, 1)
                 while (prefix[s.i + 1] <= t);   // (sequences without rows; prefix[n] >= t1 > t)
                 const int4 f = info[s.i];
                 int w0, ns;
-                view(f.y, f.w, w0, ns, s.nt);
+                view(s.i, f.y, f.w, w0, ns, s.nt);
             }
         }
         s.k0 = 0;
@@ -226,7 +230,7 @@ __global__ void __launch_bounds__(SplitCfg<D, QN, T>::NT, 1)
                 g = at == t0 ? segment(at) : following(g);
                 const int4 f = info[g.i];
                 int nt;
-                view(f.y, f.w, seg.w0, seg.ns, nt);
+                view(g.i, f.y, f.w, seg.w0, seg.ns, nt);
                 seg.h = g.h, seg.k = g.k0, seg.k1 = g.k1, seg.row = f.x, seg.len = f.y;
                 seg.low = f.y - f.w - a.window + 1;
                 at = g.k0 < g.k1 ? g.after() : t1;
@@ -327,7 +331,7 @@ __global__ void __launch_bounds__(SplitCfg<D, QN, T>::NT, 1)
         float *const sums = mm + NW * R * 2;
         const int4 f = info[sg.i];
         const int row0 = sg.rt * R, rows = min(R, f.w * G - row0), count = sg.k1 - sg.k0, turn = n % NW;
-        const bool cut = sg.k0 > 0 || sg.k1 < sg.nt;
+        const bool cut = sg.k0 > 0 || sg.k1 < sg.nt, prior = second && skips[sg.i] > 0;
         int ca = 0, cb = 0;   // the item's CTAs
         if (cut) ca = (int)(sg.first / quota), cb = (int)((sg.first + sg.nt - 1) / quota);
         const int part = (int)blockIdx.x == ca ? 2 * ca + 1 : 2 * (int)blockIdx.x;
@@ -367,7 +371,7 @@ __global__ void __launch_bounds__(SplitCfg<D, QN, T>::NT, 1)
                     a.part_ml[((size_t)part * R + r) * 2 + 1] = S;
                 }
             } else {
-                store_row(a, f, sg.h, G, D, row0 + r, d, o, M, S);
+                store_row(a, f, sg.h, G, D, row0 + r, d, o, M, S, prior);
             }
         }
         if (!cut) return;
@@ -411,7 +415,7 @@ __global__ void __launch_bounds__(SplitCfg<D, QN, T>::NT, 1)
                 const float w = wt[y * R + r];
                 o.x += v.x * w, o.y += v.y * w, o.z += v.z * w, o.w += v.w * w;
             }
-            store_row(a, f, sg.h, G, D, row0 + r, d, o, sums[r * 2], sums[r * 2 + 1]);
+            store_row(a, f, sg.h, G, D, row0 + r, d, o, sums[r * 2], sums[r * 2 + 1], prior);
         }
         if (me == 0) a.tickets[ca] = 0;
         sync();
@@ -515,9 +519,9 @@ __global__ void __launch_bounds__(SplitCfg<D, QN, T>::NT, 1)
         const int4 f = info[sg.i];
         const int L = f.y, nq = f.w, p0 = L - nq;
         int w0, ns, nt_all;
-        view(L, nq, w0, ns, nt_all);
+        view(sg.i, L, nq, w0, ns, nt_all);
         const int row0 = sg.rt * R, rows = min(R, nq * G - row0);   // rows of this tile
-        const int pos_lo = p0 + row0 / G, pos_hi = p0 + (row0 + rows - 1) / G;
+        const int pos_lo = flat ? L - 1 : p0 + row0 / G, pos_hi = flat ? L - 1 : p0 + (row0 + rows - 1) / G;
         // query fragments: this lane's row(s) of each run, elements in the order of the keys' bytes
         uint32_t qa[C::QS ? 1 : C::STEPS][QN][T][2];
         float qs[QN];   // factor from product to base-2 score of row g of each run
@@ -572,7 +576,7 @@ __global__ void __launch_bounds__(SplitCfg<D, QN, T>::NT, 1)
 #pragma unroll
         for (int x = 0; x < QC; ++x) {
             const int r = 8 * (x >> 1) + 2 * q + (x & 1);
-            pos[x] = r < rows ? p0 + (row0 + r) / G : -1;
+            pos[x] = r >= rows ? -1 : flat ? L - 1 : p0 + (row0 + r) / G;
             qf[x] = __shfl_sync(0xffffffffu, qs[x >> 1], (2 * q + (x & 1)) * 4);
             m[x] = -INFINITY;
             l[x] = 0.f;
@@ -880,12 +884,12 @@ struct SplitPlan {
     size_t smem;
 };
 template <int D, int QN, int T>
-SplitPlan split_plan(int n)
+SplitPlan split_plan(int n, bool second)
 {
     using C = SplitCfg<D, QN, T>;
     SplitPlan p;
     const size_t fixed = 1024 + C::NM * (C::MERGE + (C::NW + 1) * C::R * 8) + C::QB + (size_t)(n + 2) * 8 + 32 +
-                         (size_t)n * 16;
+                         (size_t)n * (second ? 20 : 16);
     const size_t avail = 227 * 1024 - 256 - fixed;   // 256: static shared memory
     p.slots = (int)(avail / (C::SLOT + sizeof(SplitMeta) + 16));
     if (p.slots > C::MAX_SLOTS) p.slots = C::MAX_SLOTS;
@@ -902,7 +906,7 @@ cudaError_t split_setup()
 template <int D, int QN, int T>
 cudaError_t split_launch(const KvAttendArgs &a, const CUtensorMap &mk, const CUtensorMap &mv, int grid, cudaStream_t s)
 {
-    const SplitPlan p = split_plan<D, QN, T>(a.b.n);
+    const SplitPlan p = split_plan<D, QN, T>(a.b.n, a.pass == 2);
     Launch L;
     L.grid = dim3(grid);
     L.block = dim3(SplitCfg<D, QN, T>::NT);

@@ -142,6 +142,32 @@ pi_status_t pi_kv_attend(pi_kv_t *h, int32_t layer, const int32_t *seqs, const i
                          int32_t dtype, float scale, int32_t window, int32_t sinks, void *stream);
 
 /*
+ * What sequences of a call share, for pi_kv_attend_shared. Group g is the call's sequences group_start[g] ..
+ * group_start[g + 1] (int32 [n_groups + 1] device, ascending, within 0 .. n; 0 <= n_groups <= n; sequences of no group share
+ * nothing). The shared prefix of a group is the longest run of leading columns in which the table rows of all its
+ * sequences with new tokens name the same pages, as far as it lies before every sequence's new tokens, cut to a
+ * multiple of 128 positions; it is 0 for a group with one such sequence. plan: int32 [PI_KV_SHARE_INTS(n, n_groups)]
+ * device, written. It serves all layers and later steps as long as the sequences only grow (pi_kv_reserve,
+ * pi_kv_append) or their pages move with their table rows (pi_kv_compact), and the calls name the same seqs,
+ * tok_start and n_groups. groups out of order are flagged and share nothing.
+ */
+#define PI_KV_SHARE_INTS(n, n_groups) (3 * ((n) + (n_groups)) + 2)
+pi_status_t pi_kv_share(pi_kv_t *h, const int32_t *seqs, const int32_t *tok_start, int32_t n, const int32_t *group_start,
+                        int32_t n_groups, int32_t *plan, void *stream);
+
+/*
+ * pi_kv_attend without a window, for sequences that share prefixes: a group's prefix is read once for all its rows,
+ * through the table row of its first sequence with new tokens, what lies behind it for each sequence, and the two are joined
+ * by their maxima and sums in fp32 (the output is rounded once). Same results as pi_kv_attend up to fp32 rounding and the
+ * terms that many and few rows keep. plan: from pi_kv_share for the same seqs, tok_start and n_groups (a sequence
+ * whose entry differs is skipped and flagged). work: fp32 device [n_tokens * n_heads * (head_dim + 2)], 16-byte
+ * aligned, overwritten.
+ */
+pi_status_t pi_kv_attend_shared(pi_kv_t *h, int32_t layer, const int32_t *seqs, const int32_t *tok_start, int32_t n,
+                                int32_t n_tokens, const int32_t *plan, int32_t n_groups, const void *q, int64_t ld_q,
+                                void *out, int64_t ld_out, float *lse, int32_t dtype, float scale, void *work, void *stream);
+
+/*
  * dst[i] becomes a copy of sequence src[i]: what dst[i] held is given back (as by pi_kv_free), src's
  * full pages are shared (ref + 1), a partly filled last page is copied, whole and in every layer,
  * into the lowest free page (in the order of i). src, dst: int32 [n] device; the dst are distinct

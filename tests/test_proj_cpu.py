@@ -53,6 +53,11 @@ def test_null_handle(P):
     assert P._lib.pi_kv_append_rotated(None, 0, None, None, 1, 1, ctypes.byref(r), None, 64, None, 64, None, None, 64, 0, None) == 1
 
 
+def test_null_handle_of_shared_attention(P):
+    assert P._lib.pi_kv_share(None, None, None, 1, None, 1, None, None) == 1
+    assert P._lib.pi_kv_attend_shared(None, 0, None, None, 1, 1, None, 1, None, 64, None, 64, None, 0, 1.0, None, None) == 1
+
+
 def test_turns(P):
     freq = [1.0, 0.5, 1e4 ** -0.7, 5e-324, 3e-6, 2 * math.pi, 1e300, 0.0, -0.25]
     for f, got in zip(freq, P.rotary_turns(freq)):
