@@ -18,9 +18,11 @@ struct Int4Args {
     void *y;
     int64_t ldx, ldadd, ldy;   // elements
     int n, k, rows;
-    int kw, cluster, chunk;    // the launch's: warps along k, CTAs along k, groups of x in shared memory
+    // the launch's: warps and CTAs along k, rows of x to a CTA, groups of its share of k at most
+    int kw, cluster, rows_per, groups;
 };
-cudaError_t launch_int4_linear(const Int4Args &a, int dtype, int nsm, cudaStream_t s);
+cudaError_t launch_int4_linear(const Int4Args &a, int dtype, int nsm, cudaStream_t s);   // k <= INT4_MAX_K
+constexpr int INT4_MAX_K = 1 << 18;   // a row of x in the shared memory of a cluster
 
 struct RotaryDev {
     const uint64_t *turns;
