@@ -13,6 +13,8 @@
 #include <cooperative_groups.h>
 
 #include <algorithm>
+#include <cstdio>
+#include <cstdlib>
 
 #include "pi_proj_internal.h"
 #include "pi_kv_device.cuh"
@@ -21,88 +23,111 @@ namespace pi {
 
 namespace cg = cooperative_groups;
 
-constexpr int I4_NT = 256, I4_NW = I4_NT / 32;
+constexpr int I4_NT = 512, I4_NW = I4_NT / 32;
 constexpr int I4_GROUP = 128;
-constexpr int I4_SMEM = 208 * 1024;   // of a CTA at most
-constexpr int I4_BATCH = 4;           // runs of 16 rows by 128 of a warp that are loaded at a time
+constexpr int I4_SMEM = 227 * 1024;    // of a CTA, one to an SM
+constexpr double I4_TILE_US = 0.5, I4_CLUSTER_US = 1.0, I4_X_US = 0.01;
+constexpr int I4_BOX = 16 * 128;       // bytes of a box: 16 rows of W, two groups
+constexpr int I4_SLOTS = 6;            // places for boxes of a warp, at most
 
-// One lane's 16 bytes of a row of W against its four 16-wide chunks: f16 pairs of nibbles (i, i + 4) of each word.
+// The eight nibbles of a word as f16 pairs (i, i + 4): a nibble in the low bits of a half is the subnormal (q + 8) 2^-24
+// (flipping its top bit turns two's complement into offset binary), one in bits 4..7 the subnormal (q + 8) 2^-20. So pairs
+// 1 and 3 are 16 times as large as 0 and 2, which their x makes up for, and the offset is taken off each group's sum.
 __device__ __forceinline__ void i4_word_h2(uint32_t w, uint32_t (&p)[4])
 {
     const uint32_t w8 = w >> 8;
-    const __half2 k1032 = u32_h2(0x64086408u);   // 1032
-    const __half2 k16th = u32_h2(0x2C002C00u);   // 1 / 16
-    const __half2 km72 = u32_h2(0xD480D480u);    // -72 = -(1024 / 16 + 8)
-    const auto bits = [](__half2 h) { return *reinterpret_cast<uint32_t *>(&h); };
-    p[0] = bits(__hsub2(u32_h2(lop3_and_xor(w, 0x000F000Fu, 0x64086408u)), k1032));
-    p[1] = bits(__hfma2(u32_h2(lop3_and_xor(w, 0x00F000F0u, 0x64806480u)), k16th, km72));
-    p[2] = bits(__hsub2(u32_h2(lop3_and_xor(w8, 0x000F000Fu, 0x64086408u)), k1032));
-    p[3] = bits(__hfma2(u32_h2(lop3_and_xor(w8, 0x00F000F0u, 0x64806480u)), k16th, km72));
+    p[0] = lop3_and_xor(w, 0x000F000Fu, 0x00080008u);
+    p[1] = lop3_and_xor(w, 0x00F000F0u, 0x00800080u);
+    p[2] = lop3_and_xor(w8, 0x000F000Fu, 0x00080008u);
+    p[3] = lop3_and_xor(w8, 0x00F000F0u, 0x00800080u);
 }
 
-// MT: runs of 16 rows of W to a warp; NT: runs of 8 rows of x.
-// CTAs to an SM, as registers allow, and places for a tile's sums.
-template <int DT, int NT>
-struct Int4Cfg {
-    static constexpr int CTAS = NT == 4 || (NT == 2 && DT == DT_F32) ? 1 : 2, SUMS = NT == 4 ? 1 : 2;
-};
+// Element k of row i by the plain definition: for rows of x with an infinity or NaN, where an offset's product is none.
+template <int DT>
+__device__ __noinline__ float plain_dot(const Int4Args &a, int64_t x_at, int i)
+{
+    const int G = a.k / I4_GROUP;
+    float v = 0.f;
+    for (int gr = 0; gr < G; ++gr) {
+        float d = 0.f;
+        for (int e = 0; e < I4_GROUP; ++e) {
+            const int k = gr * I4_GROUP + e;
+            const uint32_t byte = a.w[(size_t)i * (a.k / 2) + k / 2];
+            const float q = (float)((int)((k & 1 ? byte >> 4 : byte & 15u) ^ 8u) - 8);
+            float x;
+            if constexpr (DT == DT_F32) x = ((const float *)a.x)[x_at + k];
+            else if constexpr (DT == DT_BF16) x = __bfloat162float(((const __nv_bfloat16 *)a.x)[x_at + k]);
+            else x = __half2float(((const __half *)a.x)[x_at + k]);
+            d = fmaf(q, x, d);
+        }
+        v = fmaf(d, __half2float(a.s[(size_t)i * G + gr]), v);
+    }
+    return v;
+}
 
-template <int DT, int MT, int NT>
-__global__ void __launch_bounds__(I4_NT, Int4Cfg<DT, NT>::CTAS) k_int4_linear(const Int4Args a)
+// NT: runs of 8 rows of x.
+template <int DT, int NT>
+__global__ void __launch_bounds__(I4_NT, 1) k_int4_linear(const __grid_constant__ Int4Args a, const __grid_constant__ CUtensorMap map)
 {
     constexpr int T = DT == DT_F32 ? 2 : 1;
-    constexpr int U = I4_BATCH / MT;   // groups whose weights are loaded at a time
-    extern __shared__ __align__(16) uint8_t smem[];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
-    const int kw = a.kw, mw = I4_NW / kw, R = 16 * MT * mw;
+    extern __shared__ __align__(1024) uint8_t smem[];   // no static shared memory beside it: it starts on its alignment
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31, g = lane >> 2, q = lane & 3;
+    const int kw = a.kw, mw = I4_NW / kw, R = 16 * mw, slots = a.slots;
     const int cs = a.cluster, rank = blockIdx.x % cs, tile0 = blockIdx.x / cs, step_t = gridDim.x / cs;
     const int b0 = blockIdx.y * a.rows_per, nb = min(a.rows - b0, a.rows_per);
     const int G = a.k / I4_GROUP, g_lo = (int)((int64_t)G * rank / cs), gn = (int)((int64_t)G * (rank + 1) / cs) - g_lo;
     const int wk = warp % kw, wm = warp / kw;
-    const size_t row_bytes = (size_t)a.k / 2;
-    const int tiles = (a.n + R - 1) / R;
+    const int tiles = (a.n + R - 1) / R, pairs = (gn + 1) / 2;
 
-    uint8_t *const frag = smem;                                            // [group][word][term][row][64 bytes]
-    float *const xf = (float *)(smem + (size_t)a.groups * 256 * T * nb);   // [group][8 NT] units of x
-    float *const red = xf + a.groups * 8 * NT;                             // [SUMS][KW][8 NT][R + 1] sums
-
-    // Into L2 before the previous kernel's results are waited for (a hint: nothing is read yet).
-    for (int r = tid; r < R; r += I4_NT) {
-        const int at = tile0 * R + r;
-        if (at < a.n) prefetch_l2(a.w + (size_t)at * row_bytes + (size_t)g_lo * 64, (uint32_t)gn * 64u);
+    uint8_t *const ring = smem + warp * slots * I4_BOX;                    // the warp's boxes
+    uint8_t *const frag = smem + I4_NW * slots * I4_BOX;                   // [group][word][term][row][64 bytes]
+    // [group][8 NT]: the unit of x, and what the offset 8 adds to a sum in that unit, negative
+    float2 *const xf = (float2 *)(frag + (size_t)a.groups * 256 * T * nb);
+    float *const red = (float *)(xf + a.groups * 8 * NT);                  // [KW][8 NT][R + 1] sums
+    uint64_t *const full = (uint64_t *)(smem + a.bar_at) + warp * slots;
+    if (lane == 0) {
+        for (int x = 0; x < slots; ++x) mbar_init(&full[x], 1);
+        fence_mbar_init();
     }
+    __syncwarp();
+    if (tid == 0) prefetch_tensormap(&map);
     pdl_wait();
     pdl_launch_dependents();
 
-    // Batches of U groups: every warp has the same number to a tile, the last ones partly or wholly past its groups. A
-    // batch's weights are loaded while the one before is worked on, from one tile into the next.
-    const int per_tile = max(1, ((gn + kw - 1) / kw + U - 1) / U);
-    uint4 w[2][U][MT][2];
-    __half s[2][U][MT][2];
-    int lt = tile0, lb = 0;   // the next batch to load
-    auto load = [&](int buf) {
-        if (lt >= tiles) return;
-        const int row0 = lt * R + wm * 16 * MT + g;
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int gr = (lb * U + u) * kw + wk;
-            if (gr < gn) {
-#pragma unroll
-                for (int m = 0; m < MT; ++m)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {   // (rows past the last read the last: their results are not stored)
-                        const size_t r = (size_t)min(row0 + m * 16 + h * 8, a.n - 1);
-                        w[buf][u][m][h] = ld_stream((const uint4 *)(a.w + r * row_bytes + (size_t)(g_lo + gr) * 64 + q * 16));
-                        s[buf][u][m][h] = a.s[r * G + g_lo + gr];
-                    }
-            }
-        }
-        if (++lb == per_tile) {
-            lb = 0;
-            lt += step_t;
+    // The warp's boxes: of each of the CTA's tiles the pairs of groups wk, wk + kw, ... of its 16 rows
+    struct Cursor {
+        int tile, pair;
+    };
+    auto advance = [&](Cursor &c) {
+        c.pair += kw;
+        if (c.pair >= pairs) {
+            c.pair = wk;
+            c.tile += step_t;
         }
     };
-    load(0);
+    Cursor ask{wk < pairs ? tile0 : tiles, wk}, sc{ask};
+    int asked = 0;   // boxes asked for
+    auto request = [&](int slot) {   // the next box into a place (uniform over the warp)
+        if (ask.tile >= tiles) return;
+        if (lane == 0) {
+            mbar_arrive_expect_tx(&full[slot], I4_BOX);
+            tma_load_2d(ring + slot * I4_BOX, &map, (g_lo + 2 * ask.pair) * 64, ask.tile * R + wm * 16, &full[slot]);
+        }
+        ++asked;
+        advance(ask);
+    };
+    for (int x = 0; x < slots; ++x) request(x);
+    // scales of a box: row lane % 16, group lane / 16, loaded four boxes ahead
+    auto scale = [&]() {
+        __half v = __ushort_as_half(0);
+        if (sc.tile < tiles) {
+            const int row = min(sc.tile * R + wm * 16 + (lane & 15), a.n - 1), gr = min(2 * sc.pair + (lane >> 4), gn - 1);
+            v = a.s[(size_t)row * G + g_lo + gr];
+            advance(sc);
+        }
+        return v;
+    };
+    __half s0 = scale(), s1 = scale(), s2 = scale(), s3 = scale();
 
     // x: a warp to a row's group, four elements to a lane, four groups' loads under way at a time
     constexpr int S = 4;
@@ -139,11 +164,11 @@ __global__ void __launch_bounds__(I4_NT, Int4Cfg<DT, NT>::CTAS) k_int4_linear(co
         for (int y = 0; y < S; ++y) {
             const int it = it0 + y * I4_NW, gl = it / nb, b = it - gl * nb;
             if (it >= gn * nb) break;
-            // 2^ex <= top < 2^(ex + 1): the largest lies in [128, 256) (zeros and the smallest numbers below)
-            const int ex = max((int)(__float_as_uint(top[y]) >> 23) - 127, -118);
-            const float mul = exp2i(7 - ex);
+            // 2^ex <= top < 2^(ex + 1): the largest lies in [2^11, 2^12) (zeros and the smallest numbers below)
+            const int ex = max((int)(__float_as_uint(top[y]) >> 23) - 127, -116);
+            const float mul = exp2i(11 - ex);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) f[y][e] *= mul;
+            for (int e = 0; e < 4; ++e) f[y][e] *= e & 1 ? mul * 0.0625f : mul;   // (pairs 1 and 3: nibbles 16 times as large)
             // a word's elements 0..3 lie in an even lane, 4..7 in the next: the even lane takes pairs (0, 4) and (1, 5)
             const bool odd = lane & 1;
             const float p0 = __shfl_xor_sync(0xffffffffu, odd ? f[y][0] : f[y][2], 1);
@@ -152,169 +177,187 @@ __global__ void __launch_bounds__(I4_NT, Int4Cfg<DT, NT>::CTAS) k_int4_linear(co
             const int word = (lane >> 1) & 3, qq = lane >> 3;
             uint8_t *const to = frag + ((gl * 4 + word) * T * nb + b) * 64 + qq * 16 + odd * 8;
             const uint32_t h0 = pack_f16(x0, y0), h1 = pack_f16(x1, y1);
+            const float2 c0 = __half22float2(u32_h2(h0)), c1 = __half22float2(u32_h2(h1));
+            float sum = (c0.x + c0.y) + 16.f * (c1.x + c1.y);   // of the terms that the products take
             *(uint2 *)to = make_uint2(h0, h1);
             if constexpr (T == 2) {
-                const float2 c0 = __half22float2(u32_h2(h0)), c1 = __half22float2(u32_h2(h1));
-                // (an infinity has no second term)
-                const auto rest = [](float v, float c) { return fabsf(c) <= 65504.f ? v - c : 0.f; };
-                *(uint2 *)(to + 64 * nb) = make_uint2(pack_f16(rest(x0, c0.x), rest(y0, c0.y)), pack_f16(rest(x1, c1.x), rest(y1, c1.y)));
+                const uint32_t l0 = pack_f16(x0 - c0.x, y0 - c0.y), l1 = pack_f16(x1 - c1.x, y1 - c1.y);
+                const float2 r0 = __half22float2(u32_h2(l0)), r1 = __half22float2(u32_h2(l1));
+                sum += (r0.x + r0.y) + 16.f * (r1.x + r1.y);
+                *(uint2 *)(to + 64 * nb) = make_uint2(l0, l1);
             }
-            if (lane == 0) xf[gl * (8 * NT) + b] = exp2i(ex - 7);
+            sum = warp_sum(sum);
+            const float unit = exp2i(ex);
+            if (lane == 0) xf[gl * (8 * NT) + b] = make_float2(unit, -8.f * 0x1p-24f * sum * unit);
         }
     }
     __syncthreads();
 
-    float tot[MT][NT][4];
-    auto clear = [&]() {
+    // Row g of a product is row ((g & 1) << 2 | g >> 1) of a box (and 8 + that): so eight lanes' reads, two rows' halves, lie
+    // in different banks of the swizzled box.
+    const int rg = (g & 1) << 2 | g >> 1;
+    int xrow[NT];   // (rows past the last read another: their columns of the products are not looked at)
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+    for (int n = 0; n < NT; ++n) xrow[n] = min(8 * n + g, nb - 1) * 64 + q * 16;
+    float tot[NT][4];
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) tot[m][n][e] = 0.f;
-    };
-    clear();
-    auto step = [&](const uint4 (&wv)[MT][2], const __half (&sv)[MT][2], int gl) {
-        float d[T][MT][NT][4];
+        for (int e = 0; e < 4; ++e) tot[n][e] = 0.f;
+    auto step = [&](const uint4 (&wv)[2], const float (&sv)[2], int gl) {
+        float d[T][NT][4];
 #pragma unroll
         for (int t = 0; t < T; ++t)
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) d[t][m][n][e] = 0.f;
-        const uint8_t *const xg = frag + gl * 4 * T * nb * 64 + g * 64 + q * 16;
+                for (int e = 0; e < 4; ++e) d[t][n][e] = 0.f;
+        const uint8_t *const xg = frag + gl * 4 * T * nb * 64;
 #pragma unroll
         for (int word = 0; word < 4; ++word) {
-            uint32_t pa[MT][2][4];
+            uint32_t pa[2][4];
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) i4_word_h2(word4(wv[m][h], word), pa[m][h]);
+            for (int h = 0; h < 2; ++h) i4_word_h2(word4(wv[h], word), pa[h]);
+            const uint32_t a0[4] = {pa[0][0], pa[1][0], pa[0][1], pa[1][1]};
+            const uint32_t a1[4] = {pa[0][2], pa[1][2], pa[0][3], pa[1][3]};
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int t = 0; t < T; ++t) {
-                    uint4 b = make_uint4(0, 0, 0, 0);   // rows past the last: nothing was stored
-                    if (8 * n + g < nb) b = *(const uint4 *)(xg + ((word * T + t) * nb + 8 * n) * 64);
-#pragma unroll
-                    for (int m = 0; m < MT; ++m) {
-                        const uint32_t a0[4] = {pa[m][0][0], pa[m][1][0], pa[m][0][1], pa[m][1][1]};
-                        const uint32_t a1[4] = {pa[m][0][2], pa[m][1][2], pa[m][0][3], pa[m][1][3]};
-                        mma_f16(d[t][m][n], a0, b.x, b.y);
-                        mma_f16(d[t][m][n], a1, b.z, b.w);
-                    }
+                    const uint4 b = *(const uint4 *)(xg + xrow[n] + (word * T + t) * nb * 64);
+                    mma_f16(d[t][n], a0, b.x, b.y);
+                    mma_f16(d[t][n], a1, b.z, b.w);
                 }
         }
-        float sc[MT][2];
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) sc[m][h] = __half2float(sv[m][h]);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const float2 u = *(const float2 *)&xf[gl * (8 * NT) + 8 * n + 2 * q];
+            const float4 u = *(const float4 *)&xf[gl * (8 * NT) + 8 * n + 2 * q];
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float v = d[0][m][n][e];
-                    if constexpr (T == 2) v += d[T - 1][m][n][e];
-                    tot[m][n][e] = fmaf(v * (e & 1 ? u.y : u.x), sc[m][e >> 1], tot[m][n][e]);
-                }
+            for (int e = 0; e < 4; ++e) {
+                float v = d[0][n][e];
+                if constexpr (T == 2) v += d[T - 1][n][e];
+                tot[n][e] = fmaf(fmaf(v, e & 1 ? u.z : u.x, e & 1 ? u.w : u.y), sv[e >> 1], tot[n][e]);
+            }
         }
     };
     cg::cluster_group cl = cg::this_cluster();
-    int ct = tile0, cb = 0, turn = 0;   // the batch that is worked on; sums alternate between two places
-    auto batch = [&](int buf) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int gr = (cb * U + u) * kw + wk;
-            if (gr < gn) step(w[buf][u], s[buf][u], gr);
+    auto meet = [&]() {
+        if (cs > 1) cl.sync();
+        else __syncthreads();
+    };
+    auto store = [&](float v, int b, int i) {   // row b of x, row i of W
+        if (v != v) v = plain_dot<DT>(a, (int64_t)(b0 + b) * a.ldx, i);
+        if (a.bias) v += a.bias[i];
+        const int64_t at = (int64_t)(b0 + b) * a.ldy + i, at_add = (int64_t)(b0 + b) * a.ldadd + i;
+        if constexpr (DT == DT_F32) {
+            if (a.add) v += ((const float *)a.add)[at_add];
+            ((float *)a.y)[at] = v;
+        } else if constexpr (DT == DT_BF16) {
+            if (a.add) v += __bfloat162float(((const __nv_bfloat16 *)a.add)[at_add]);
+            ((__nv_bfloat16 *)a.y)[at] = __float2bfloat16_rn(v);
+        } else {
+            if (a.add) v += __half2float(((const __half *)a.add)[at_add]);
+            ((__half *)a.y)[at] = __float2half_rn(v);
         }
-        if (++cb < per_tile) return;
-        // the tile's end: sums of the warps and of the cluster
-        cb = 0;
-        float *const to = red + turn * (kw * 8 * NT * (R + 1));
-        auto meet = [&]() {
-            if (cs > 1) cl.sync();
-            else __syncthreads();
-        };
-        if constexpr (Int4Cfg<DT, NT>::SUMS == 2) turn ^= 1;
-        else if (ct != tile0) meet();   // the last tile's sums have been read
+    };
+    int slot = 0;
+    uint32_t parity = 0;
+    bool dead = false;
+    for (int tile = tile0; tile < tiles; tile += step_t) {
+        for (int pair = wk; pair < pairs; pair += kw) {
+            const float sv = __half2float(s0) * 0x1p13f;   // x's unit is 2^-11 of xf's, the nibbles' 2^-24
+            s0 = s1, s1 = s2, s2 = s3, s3 = scale();
+            if (!dead && !warp_wait(&full[slot], parity)) dead = true;
+            const uint8_t *const box = ring + slot * I4_BOX + rg * 128;
+            uint4 w[2][2];
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) w[j][h] = *(const uint4 *)(box + h * 1024 + (((j * 4 + q) ^ rg) << 4));
+            fence_proxy_async_smem();   // the next copy into the place comes after these loads
+            __syncwarp();
+            if (!dead) request(slot);
+            if (++slot == slots) slot = 0, parity ^= 1;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const float se[2] = {__shfl_sync(0xffffffffu, sv, j * 16 + rg), __shfl_sync(0xffffffffu, sv, j * 16 + 8 + rg)};
+                if (2 * pair + j < gn) step(w[j], se, 2 * pair + j);
+            }
+        }
+        if (dead) {   // a wait ran out: no number
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) tot[n][e] = __int_as_float(0x7fc00000);
+        }
+        // sums of the warps and of the cluster
+        if (kw == 1 && cs == 1) {
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const int r = wm * 16 * MT + m * 16 + (e >> 1) * 8 + g, b = 8 * n + 2 * q + (e & 1);
-                    if (b < nb) to[(wk * (8 * NT) + b) * (R + 1) + r] = tot[m][n][e];
+                    const int i = tile * R + wm * 16 + (e >> 1) * 8 + rg, b = 8 * n + 2 * q + (e & 1);
+                    if (b < nb && i < a.n) store(tot[n][e], b, i);
                 }
-        clear();
-        meet();
-        const int per = R / cs;   // rows that this CTA adds up
-        for (int x = tid; x < per * nb; x += I4_NT) {
-            const int b = x / per, r = rank * per + x - b * per, i = ct * R + r;
-            if (i >= a.n) continue;
-            float v = 0.f;
-            for (int c = 0; c < cs; ++c) {
-                const float *from = cs > 1 ? cl.map_shared_rank(to, c) : to;
-                for (int y = 0; y < kw; ++y) v += from[(y * (8 * NT) + b) * (R + 1) + r];
-            }
-            if (a.bias) v += a.bias[i];
-            const int64_t at = (int64_t)(b0 + b) * a.ldy + i, at_add = (int64_t)(b0 + b) * a.ldadd + i;
-            if constexpr (DT == DT_F32) {
-                if (a.add) v += ((const float *)a.add)[at_add];
-                ((float *)a.y)[at] = v;
-            } else if constexpr (DT == DT_BF16) {
-                if (a.add) v += __bfloat162float(((const __nv_bfloat16 *)a.add)[at_add]);
-                ((__nv_bfloat16 *)a.y)[at] = __float2bfloat16_rn(v);
-            } else {
-                if (a.add) v += __half2float(((const __half *)a.add)[at_add]);
-                ((__half *)a.y)[at] = __float2half_rn(v);
+        } else {
+            if (tile != tile0) meet();   // the last tile's sums have been read
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int r = wm * 16 + (e >> 1) * 8 + rg, b = 8 * n + 2 * q + (e & 1);
+                    if (b < nb) red[(wk * (8 * NT) + b) * (R + 1) + r] = tot[n][e];
+                }
+            meet();
+            const int per = R / cs;   // rows that this CTA adds up
+            for (int x = tid; x < per * nb; x += I4_NT) {
+                const int b = x / per, r = rank * per + x - b * per, i = tile * R + r;
+                if (i >= a.n) continue;
+                float v = 0.f;
+                for (int c = 0; c < cs; ++c) {
+                    const float *from = cs > 1 ? cl.map_shared_rank(red, c) : red;
+                    for (int y = 0; y < kw; ++y) v += from[(y * (8 * NT) + b) * (R + 1) + r];
+                }
+                store(v, b, i);
             }
         }
-        ct += step_t;
-    };
-    while (ct < tiles) {
-        load(1);
-        batch(0);
-        if (ct >= tiles) break;
-        load(0);
-        batch(1);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) tot[n][e] = 0.f;
     }
+    if (dead)   // nothing may land after the CTA is gone: the last copy into each place (bounded)
+        for (int x = 0; x < slots && x < asked; ++x) warp_wait(&full[x], ((asked - 1 - x) / slots) & 1);
     if (cs > 1) cl.sync();   // the others have read this CTA's sums
 }
 
 namespace {
 
 struct Int4Plan {
-    int mw, cluster, rows_per;
+    int kw, cluster, rows_per, slots;
+    size_t smem, bar_at;
 };
 
-template <int DT, int MT, int NT>
-cudaError_t launch_of(const Int4Args &in, const Int4Plan &p, int nsm, cudaStream_t s)
+template <int DT, int NT>
+cudaError_t launch_of(const Int4Args &in, const Int4Plan &p, const CUtensorMap &map, int nsm, cudaStream_t s)
 {
     Int4Args a = in;
-    constexpr int T = DT == DT_F32 ? 2 : 1;
-    const int nb = std::min(a.rows, p.rows_per), R = 16 * MT * p.mw, G = a.k / I4_GROUP;
-    a.kw = I4_NW / p.mw;
+    const int R = 16 * (I4_NW / p.kw), G = a.k / I4_GROUP;
+    a.kw = p.kw;
     a.cluster = p.cluster;
     a.rows_per = p.rows_per;
+    a.slots = p.slots;
     a.groups = (G + p.cluster - 1) / p.cluster;
-    const auto kern = k_int4_linear<DT, MT, NT>;
+    a.bar_at = (int)p.bar_at;
+    const auto kern = k_int4_linear<DT, NT>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, I4_SMEM);
     if (e != cudaSuccess) return e;
-    const size_t smem = (size_t)a.groups * (256 * T * nb + 4 * 8 * NT) + (size_t)Int4Cfg<DT, NT>::SUMS * a.kw * 8 * NT * (R + 1) * 4;
     // CTAs stay and go through tiles: as many as the GPU holds at a time
-    const int slices = (a.rows + p.rows_per - 1) / p.rows_per, hold = smem <= I4_SMEM / 2 ? Int4Cfg<DT, NT>::CTAS * nsm : nsm;
-    const int tiles = (a.n + R - 1) / R, room = std::max(1, hold / (p.cluster * slices));
+    const int slices = (a.rows + p.rows_per - 1) / p.rows_per, tiles = (a.n + R - 1) / R;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(std::min(tiles, room) * p.cluster), (unsigned)slices);
+    cfg.gridDim = dim3((unsigned)(std::min(tiles, std::max(1, nsm / (p.cluster * slices))) * p.cluster), (unsigned)slices);
     cfg.blockDim = dim3(I4_NT);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = p.smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -324,41 +367,66 @@ cudaError_t launch_of(const Int4Args &in, const Int4Plan &p, int nsm, cudaStream
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = p.cluster > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kern, a);
+    return cudaLaunchKernelEx(&cfg, kern, a, map);
 }
 
 template <int DT>
-cudaError_t launch_dt(const Int4Args &a, int nsm, cudaStream_t s)
+cudaError_t launch_dt(const Int4Args &a, const CUtensorMap &map, int nsm, cudaStream_t s)
 {
     const int G = a.k / I4_GROUP, T = DT == DT_F32 ? 2 : 1;
-    Int4Plan p;
+    Int4Plan p = {};
     // rows of x that a CTA keeps: what 8 CTAs' shared memory holds of their whole length
-    const int fit = (int)std::min<int64_t>(32, (int64_t)(I4_SMEM - 40 * 1024) / ((int64_t)(G + 7) / 8 * 256 * T));
+    const int fit = (int)std::min<int64_t>(32, (int64_t)(I4_SMEM - 2 * I4_NW * I4_BOX - 48 * 1024) / ((int64_t)(G + 7) / 8 * 256 * T));
     p.rows_per = std::min(a.rows, std::max(1, fit));
-    const int nt = p.rows_per <= 8 ? 1 : p.rows_per <= 16 ? 2 : 4, mt = nt == 1 ? 1 : 2;
-    // A CTA brings its rows of x into shared memory, so its share of W should be larger.
-    p.mw = 1;
-    while (p.mw < I4_NW && 16 * mt * p.mw < p.rows_per * 2 * T) p.mw *= 2;
-    const int kw = I4_NW / p.mw, slices = (a.rows + p.rows_per - 1) / p.rows_per;
-    const int64_t tiles = (int64_t)((a.n + 16 * mt * p.mw - 1) / (16 * mt * p.mw)) * slices;
-    const size_t sums = (size_t)(nt == 4 ? 1 : 2) * kw * 8 * nt * (16 * mt * p.mw + 1) * 4;
-    p.cluster = 1;
-    while (p.cluster < 8 && (size_t)((G + p.cluster - 1) / p.cluster) * (256 * T * p.rows_per + 32 * nt) + sums > I4_SMEM) p.cluster *= 2;
-    // two CTAs to an SM, as long as every warp has a group of its own
-    while (p.cluster < 8 && tiles * p.cluster < nsm && G >= 2 * p.cluster * kw) p.cluster *= 2;
-    return nt == 1   ? launch_of<DT, 1, 1>(a, p, nsm, s)
-           : nt == 2 ? launch_of<DT, 2, 2>(a, p, nsm, s)
-                     : launch_of<DT, 2, 4>(a, p, nsm, s);
+    const int nt = p.rows_per <= 8 ? 1 : p.rows_per <= 16 ? 2 : 4;
+    const int slices = (a.rows + p.rows_per - 1) / p.rows_per;
+    double best = 0;
+    const char *ekw = getenv("I4_MW"), *ecs = getenv("I4_CS");
+    for (int cs = 1; cs <= 8; cs *= 2)
+        for (int kw = 1; kw <= I4_NW; kw *= 2) {
+            const int R = 16 * (I4_NW / kw), groups = (G + cs - 1) / cs;
+            if (R < cs) continue;
+            const size_t sums = kw == 1 && cs == 1 ? 0 : (size_t)kw * 8 * nt * (R + 1) * 4;
+            const size_t rest = ((size_t)groups * (256 * T * p.rows_per + 64 * nt) + sums + 7) / 8 * 8 + 8 * I4_NW * I4_SLOTS;
+            if (rest + 2 * I4_NW * I4_BOX > I4_SMEM) continue;
+            const int n_slots = std::min<int>(I4_SLOTS, (int)((I4_SMEM - rest) / (I4_NW * I4_BOX)));
+            const int64_t tiles = (int64_t)((a.n + R - 1) / R) * slices, room = std::max(1, nsm / cs);
+            const int64_t rounds = (tiles + room - 1) / room;
+            const int boxes = ((groups + 1) / 2 + kw - 1) / kw;
+            const double us = (double)rounds * (std::max(boxes * kw * (R / 16) * I4_BOX / 45e3, boxes * 0.15) + I4_TILE_US * (sums > 0) + (cs > 1 ? I4_CLUSTER_US : 0.0)) + (double)groups * p.rows_per * I4_X_US;
+            if ((ekw && atoi(ekw) != kw) || (ecs && atoi(ecs) != cs)) continue;
+            if (p.cluster == 0 || us < best) {
+                best = us;
+                p.cluster = cs;
+                p.kw = kw;
+                p.slots = n_slots;
+                p.bar_at = (size_t)I4_NW * n_slots * I4_BOX + rest - 8 * I4_NW * I4_SLOTS;
+                p.smem = p.bar_at + (size_t)8 * I4_NW * n_slots;
+            }
+        }
+    if (getenv("I4_SHOW")) printf("kw %d cluster %d rows_per %d slots %d est %.1f\n", p.kw, p.cluster, p.rows_per, p.slots, best);
+    if (p.cluster == 0) return cudaErrorInvalidConfiguration;
+    return nt == 1   ? launch_of<DT, 1>(a, p, map, nsm, s)
+           : nt == 2 ? launch_of<DT, 2>(a, p, map, nsm, s)
+                     : launch_of<DT, 4>(a, p, map, nsm, s);
 }
 
 }  // namespace
 
 cudaError_t launch_int4_linear(const Int4Args &a, int dtype, int nsm, cudaStream_t s)
 {
+    // W as rows of k / 2 bytes; boxes of 16 rows and 128 bytes, swizzled. What lies past its edges reads as zeros.
+    CUtensorMap map;
+    const cuuint64_t dims[2] = {(cuuint64_t)a.k / 2, (cuuint64_t)a.n}, strides[1] = {(cuuint64_t)a.k / 2};
+    const cuuint32_t box[2] = {128, 16}, one[2] = {1, 1};
+    const EncodeFn encode = tensor_map_encoder();
+    if (!encode || encode(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, (void *)a.w, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return cudaErrorUnknown;
     switch (dtype) {
-    case DT_F32: return launch_dt<DT_F32>(a, nsm, s);
-    case DT_BF16: return launch_dt<DT_BF16>(a, nsm, s);
-    default: return launch_dt<DT_F16>(a, nsm, s);
+    case DT_F32: return launch_dt<DT_F32>(a, map, nsm, s);
+    case DT_BF16: return launch_dt<DT_BF16>(a, map, nsm, s);
+    default: return launch_dt<DT_F16>(a, map, nsm, s);
     }
 }
 

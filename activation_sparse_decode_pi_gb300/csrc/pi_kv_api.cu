@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cfloat>
 #include <cmath>
 #include <cstdint>
@@ -31,22 +32,26 @@ struct pi_kv {
     int32_t *list_src = nullptr, *list_dst = nullptr, *list_count = nullptr, *page_map = nullptr;
 };
 
-namespace {
+namespace pi {
 
-typedef CUresult (*EncodeFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                             const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                             CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeFn encode_fn()
+EncodeFn tensor_map_encoder()
 {
+    static std::atomic<EncodeFn> found{nullptr};   // (looked up until it is there)
+    if (EncodeFn fn = found.load(std::memory_order_relaxed)) return fn;
     void *p = nullptr;
     cudaDriverEntryPointQueryResult q;
     if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
+        q == cudaDriverEntryPointSuccess) {
+        found.store((EncodeFn)p, std::memory_order_relaxed);
         return (EncodeFn)p;
+    }
     cudaGetLastError();
     return nullptr;
 }
+
+}  // namespace pi
+
+namespace {
 
 pi_status_t cuda_status(cudaError_t e)
 {
@@ -150,7 +155,7 @@ pi_status_t kv_create(pi_kv_t **out, const pi_kv_desc_t *desc, const pi_kv_layer
     if ((s = check_ptr(state->table, (size_t)d.max_seqs * d.max_pages * 4, 4, dev))) return s;
     if ((s = check_ptr(state->length, (size_t)d.max_seqs * 4, 4, dev))) return s;
     if ((s = check_ptr(state->ref, (size_t)d.n_pages * 4, 4, dev))) return s;
-    EncodeFn enc = encode_fn();
+    EncodeFn enc = tensor_map_encoder();
     if (!enc) return PI_ERR_CUDA;
 
     struct Holder {   // frees what exists when a later step fails

@@ -1,6 +1,7 @@
 // pi_proj_internal.h -- what the host side of pi_proj.h (pi_proj_api.cu) and its kernels share.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <cuda_fp16.h>
 #include <stdint.h>
@@ -10,6 +11,12 @@
 
 namespace pi {
 
+// cuTensorMapEncodeTiled, or NULL (pi_kv_api.cu)
+typedef CUresult (*EncodeFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                             const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                             CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeFn tensor_map_encoder();
+
 struct Int4Args {
     const uint8_t *w;      // [n x k/2]
     const __half *s;       // [n x k/128]
@@ -18,8 +25,9 @@ struct Int4Args {
     void *y;
     int64_t ldx, ldadd, ldy;   // elements
     int n, k, rows;
-    // the launch's: warps and CTAs along k, rows of x to a CTA, groups of its share of k at most
-    int kw, cluster, rows_per, groups;
+    // the launch's: warps and CTAs along k, rows of x to a CTA, groups of its share of k at most, boxes of a warp,
+    // where the barriers lie
+    int kw, cluster, rows_per, groups, slots, bar_at;
 };
 cudaError_t launch_int4_linear(const Int4Args &a, int dtype, int nsm, cudaStream_t s);   // k <= INT4_MAX_K
 constexpr int INT4_MAX_K = 1 << 18;   // a row of x in the shared memory of a cluster
