@@ -13,8 +13,6 @@
 #include <cooperative_groups.h>
 
 #include <algorithm>
-#include <cstdio>
-#include <cstdlib>
 
 #include "pi_proj_internal.h"
 #include "pi_kv_device.cuh"
@@ -27,8 +25,8 @@ constexpr int I4_NT = 512, I4_NW = I4_NT / 32;
 constexpr int I4_GROUP = 128;
 constexpr int I4_SMEM = 227 * 1024;    // of a CTA, one to an SM
 constexpr double I4_TILE_US = 0.5, I4_CLUSTER_US = 1.0, I4_X_US = 0.01;
-constexpr int I4_BOX = 16 * 128;       // bytes of a box: 16 rows of W, two groups
-constexpr int I4_SLOTS = 6;            // places for boxes of a warp, at most
+constexpr int I4_BOX = 32 * 128;       // bytes of a box: 32 rows of W, two groups
+constexpr int I4_SLOTS = 3;            // places for boxes of a warp, at most
 
 // The eight nibbles of a word as f16 pairs (i, i + 4): a nibble in the low bits of a half is the subnormal (q + 8) 2^-24
 // (flipping its top bit turns two's complement into offset binary), one in bits 4..7 the subnormal (q + 8) 2^-20. So pairs
@@ -72,7 +70,7 @@ __global__ void __launch_bounds__(I4_NT, 1) k_int4_linear(const __grid_constant_
     constexpr int T = DT == DT_F32 ? 2 : 1;
     extern __shared__ __align__(1024) uint8_t smem[];   // no static shared memory beside it: it starts on its alignment
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31, g = lane >> 2, q = lane & 3;
-    const int kw = a.kw, mw = I4_NW / kw, R = 16 * mw, slots = a.slots;
+    const int kw = a.kw, mw = I4_NW / kw, R = 32 * mw, slots = a.slots;
     const int cs = a.cluster, rank = blockIdx.x % cs, tile0 = blockIdx.x / cs, step_t = gridDim.x / cs;
     const int b0 = blockIdx.y * a.rows_per, nb = min(a.rows - b0, a.rows_per);
     const int G = a.k / I4_GROUP, g_lo = (int)((int64_t)G * rank / cs), gn = (int)((int64_t)G * (rank + 1) / cs) - g_lo;
@@ -94,7 +92,7 @@ __global__ void __launch_bounds__(I4_NT, 1) k_int4_linear(const __grid_constant_
     pdl_wait();
     pdl_launch_dependents();
 
-    // The warp's boxes: of each of the CTA's tiles the pairs of groups wk, wk + kw, ... of its 16 rows
+    // The warp's boxes: of each of the CTA's tiles the pairs of groups wk, wk + kw, ... of its 32 rows
     struct Cursor {
         int tile, pair;
     };
@@ -111,23 +109,30 @@ __global__ void __launch_bounds__(I4_NT, 1) k_int4_linear(const __grid_constant_
         if (ask.tile >= tiles) return;
         if (lane == 0) {
             mbar_arrive_expect_tx(&full[slot], I4_BOX);
-            tma_load_2d(ring + slot * I4_BOX, &map, (g_lo + 2 * ask.pair) * 64, ask.tile * R + wm * 16, &full[slot]);
+            tma_load_2d(ring + slot * I4_BOX, &map, (g_lo + 2 * ask.pair) * 64, ask.tile * R + wm * 32, &full[slot]);
         }
         ++asked;
         advance(ask);
     };
     for (int x = 0; x < slots; ++x) request(x);
-    // scales of a box: row lane % 16, group lane / 16, loaded four boxes ahead
+    // Scales of a box, both groups of row `lane`, loaded two boxes ahead. (An odd share's last box has one group; what lies
+    // behind it may be another CTA's or none.)
+    const __half *sp = a.s;
+    auto scale_row = [&]() { sp = a.s + (size_t)min(sc.tile * R + wm * 32 + lane, a.n - 1) * G + g_lo + 2 * wk; };
+    scale_row();
     auto scale = [&]() {
-        __half v = __ushort_as_half(0);
+        uint32_t v = 0;
         if (sc.tile < tiles) {
-            const int row = min(sc.tile * R + wm * 16 + (lane & 15), a.n - 1), gr = min(2 * sc.pair + (lane >> 4), gn - 1);
-            v = a.s[(size_t)row * G + g_lo + gr];
+            v = __half_as_ushort(sp[0]);
+            if (2 * sc.pair + 1 < gn) v |= (uint32_t)__half_as_ushort(sp[1]) << 16;
+            sp += 2 * kw;
+            const int was = sc.tile;
             advance(sc);
+            if (sc.tile != was) scale_row();
         }
         return v;
     };
-    __half s0 = scale(), s1 = scale(), s2 = scale(), s3 = scale();
+    uint32_t s0 = scale(), s1 = scale();
 
     // x: a warp to a row's group, four elements to a lane, four groups' loads under way at a time
     constexpr int S = 4;
@@ -196,48 +201,73 @@ __global__ void __launch_bounds__(I4_NT, 1) k_int4_linear(const __grid_constant_
     // Row g of a product is row ((g & 1) << 2 | g >> 1) of a box (and 8 + that): so eight lanes' reads, two rows' halves, lie
     // in different banks of the swizzled box.
     const int rg = (g & 1) << 2 | g >> 1;
+    const int wj0 = rg * 128 + ((q ^ rg) << 4), wj1 = rg * 128 + (((4 + q) ^ rg) << 4);   // the lane's chunks of a row's groups
     int xrow[NT];   // (rows past the last read another: their columns of the products are not looked at)
 #pragma unroll
     for (int n = 0; n < NT; ++n) xrow[n] = min(8 * n + g, nb - 1) * 64 + q * 16;
-    float tot[NT][4];
+    float tot[2][NT][4];   // of rows 16 m + ...
+    auto clear = [&]() {
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) tot[n][e] = 0.f;
-    auto step = [&](const uint4 (&wv)[2], const float (&sv)[2], int gl) {
-        float d[T][NT][4];
-#pragma unroll
-        for (int t = 0; t < T; ++t)
+        for (int m = 0; m < 2; ++m)
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) d[t][n][e] = 0.f;
+                for (int e = 0; e < 4; ++e) tot[m][n][e] = 0.f;
+    };
+    clear();
+    auto step = [&](const uint8_t *box, int j, float sv, int gl) {   // group j of the box, gl of the CTA's share
+        float d[T][2][NT][4];
+#pragma unroll
+        for (int t = 0; t < T; ++t)
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) d[t][m][n][e] = 0.f;
+        uint4 wv[2][2];
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) wv[m][h] = *(const uint4 *)(box + m * 2048 + h * 1024 + (j ? wj1 : wj0));
         const uint8_t *const xg = frag + gl * 4 * T * nb * 64;
 #pragma unroll
         for (int word = 0; word < 4; ++word) {
-            uint32_t pa[2][4];
+            uint32_t pa[2][2][4];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) i4_word_h2(word4(wv[h], word), pa[h]);
-            const uint32_t a0[4] = {pa[0][0], pa[1][0], pa[0][1], pa[1][1]};
-            const uint32_t a1[4] = {pa[0][2], pa[1][2], pa[0][3], pa[1][3]};
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) i4_word_h2(word4(wv[m][h], word), pa[m][h]);
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int t = 0; t < T; ++t) {
                     const uint4 b = *(const uint4 *)(xg + xrow[n] + (word * T + t) * nb * 64);
-                    mma_f16(d[t][n], a0, b.x, b.y);
-                    mma_f16(d[t][n], a1, b.z, b.w);
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) {
+                        const uint32_t a0[4] = {pa[m][0][0], pa[m][1][0], pa[m][0][1], pa[m][1][1]};
+                        const uint32_t a1[4] = {pa[m][0][2], pa[m][1][2], pa[m][0][3], pa[m][1][3]};
+                        mma_f16(d[t][m][n], a0, b.x, b.y);
+                        mma_f16(d[t][m][n], a1, b.z, b.w);
+                    }
                 }
         }
+        float se[2][2];
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) se[m][h] = __shfl_sync(0xffffffffu, sv, m * 16 + h * 8 + rg);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const float4 u = *(const float4 *)&xf[gl * (8 * NT) + 8 * n + 2 * q];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                float v = d[0][n][e];
-                if constexpr (T == 2) v += d[T - 1][n][e];
-                tot[n][e] = fmaf(fmaf(v, e & 1 ? u.z : u.x, e & 1 ? u.w : u.y), sv[e >> 1], tot[n][e]);
-            }
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float v = d[0][m][n][e];
+                    if constexpr (T == 2) v += d[T - 1][m][n][e];
+                    tot[m][n][e] = fmaf(fmaf(v, e & 1 ? u.z : u.x, e & 1 ? u.w : u.y), se[m][e >> 1], tot[m][n][e]);
+                }
         }
     };
     cg::cluster_group cl = cg::this_cluster();
@@ -265,49 +295,46 @@ __global__ void __launch_bounds__(I4_NT, 1) k_int4_linear(const __grid_constant_
     bool dead = false;
     for (int tile = tile0; tile < tiles; tile += step_t) {
         for (int pair = wk; pair < pairs; pair += kw) {
-            const float sv = __half2float(s0) * 0x1p13f;   // x's unit is 2^-11 of xf's, the nibbles' 2^-24
-            s0 = s1, s1 = s2, s2 = s3, s3 = scale();
+            const float2 sv = __half22float2(u32_h2(s0));
+            s0 = s1, s1 = scale();
             if (!dead && !warp_wait(&full[slot], parity)) dead = true;
-            const uint8_t *const box = ring + slot * I4_BOX + rg * 128;
-            uint4 w[2][2];
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) w[j][h] = *(const uint4 *)(box + h * 1024 + (((j * 4 + q) ^ rg) << 4));
-            fence_proxy_async_smem();   // the next copy into the place comes after these loads
+            const uint8_t *const box = ring + slot * I4_BOX;
+            // (x's unit is 2^-11 of xf's, the nibbles' 2^-24)
+            step(box, 0, sv.x * 0x1p13f, 2 * pair);
+            if (2 * pair + 1 < gn) step(box, 1, sv.y * 0x1p13f, 2 * pair + 1);
+            fence_proxy_async_smem();   // the next copy into the place comes after the loads
             __syncwarp();
             if (!dead) request(slot);
             if (++slot == slots) slot = 0, parity ^= 1;
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const float se[2] = {__shfl_sync(0xffffffffu, sv, j * 16 + rg), __shfl_sync(0xffffffffu, sv, j * 16 + 8 + rg)};
-                if (2 * pair + j < gn) step(w[j], se, 2 * pair + j);
-            }
         }
         if (dead) {   // a wait ran out: no number
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) tot[n][e] = __int_as_float(0x7fc00000);
+                for (int e = 0; e < 4; ++e) tot[0][n][e] = tot[1][n][e] = __int_as_float(0x7fc00000);
         }
         // sums of the warps and of the cluster
         if (kw == 1 && cs == 1) {
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+            for (int m = 0; m < 2; ++m)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int i = tile * R + wm * 16 + (e >> 1) * 8 + rg, b = 8 * n + 2 * q + (e & 1);
-                    if (b < nb && i < a.n) store(tot[n][e], b, i);
-                }
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int i = tile * R + wm * 32 + m * 16 + (e >> 1) * 8 + rg, b = 8 * n + 2 * q + (e & 1);
+                        if (b < nb && i < a.n) store(tot[m][n][e], b, i);
+                    }
         } else {
             if (tile != tile0) meet();   // the last tile's sums have been read
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+            for (int m = 0; m < 2; ++m)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int r = wm * 16 + (e >> 1) * 8 + rg, b = 8 * n + 2 * q + (e & 1);
-                    if (b < nb) red[(wk * (8 * NT) + b) * (R + 1) + r] = tot[n][e];
-                }
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int r = wm * 32 + m * 16 + (e >> 1) * 8 + rg, b = 8 * n + 2 * q + (e & 1);
+                        if (b < nb) red[(wk * (8 * NT) + b) * (R + 1) + r] = tot[m][n][e];
+                    }
             meet();
             const int per = R / cs;   // rows that this CTA adds up
             for (int x = tid; x < per * nb; x += I4_NT) {
@@ -321,10 +348,7 @@ __global__ void __launch_bounds__(I4_NT, 1) k_int4_linear(const __grid_constant_
                 store(v, b, i);
             }
         }
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) tot[n][e] = 0.f;
+        clear();
     }
     if (dead)   // nothing may land after the CTA is gone: the last copy into each place (bounded)
         for (int x = 0; x < slots && x < asked; ++x) warp_wait(&full[x], ((asked - 1 - x) / slots) & 1);
@@ -342,7 +366,7 @@ template <int DT, int NT>
 cudaError_t launch_of(const Int4Args &in, const Int4Plan &p, const CUtensorMap &map, int nsm, cudaStream_t s)
 {
     Int4Args a = in;
-    const int R = 16 * (I4_NW / p.kw), G = a.k / I4_GROUP;
+    const int R = 32 * (I4_NW / p.kw), G = a.k / I4_GROUP;
     a.kw = p.kw;
     a.cluster = p.cluster;
     a.rows_per = p.rows_per;
@@ -376,25 +400,23 @@ cudaError_t launch_dt(const Int4Args &a, const CUtensorMap &map, int nsm, cudaSt
     const int G = a.k / I4_GROUP, T = DT == DT_F32 ? 2 : 1;
     Int4Plan p = {};
     // rows of x that a CTA keeps: what 8 CTAs' shared memory holds of their whole length
-    const int fit = (int)std::min<int64_t>(32, (int64_t)(I4_SMEM - 2 * I4_NW * I4_BOX - 48 * 1024) / ((int64_t)(G + 7) / 8 * 256 * T));
+    const int fit = (int)std::min<int64_t>(32, (int64_t)(I4_SMEM - I4_NW * I4_BOX - 72 * 1024) / ((int64_t)(G + 7) / 8 * 256 * T));
     p.rows_per = std::min(a.rows, std::max(1, fit));
     const int nt = p.rows_per <= 8 ? 1 : p.rows_per <= 16 ? 2 : 4;
     const int slices = (a.rows + p.rows_per - 1) / p.rows_per;
     double best = 0;
-    const char *ekw = getenv("I4_MW"), *ecs = getenv("I4_CS");
     for (int cs = 1; cs <= 8; cs *= 2)
         for (int kw = 1; kw <= I4_NW; kw *= 2) {
-            const int R = 16 * (I4_NW / kw), groups = (G + cs - 1) / cs;
+            const int R = 32 * (I4_NW / kw), groups = (G + cs - 1) / cs;
             if (R < cs) continue;
             const size_t sums = kw == 1 && cs == 1 ? 0 : (size_t)kw * 8 * nt * (R + 1) * 4;
             const size_t rest = ((size_t)groups * (256 * T * p.rows_per + 64 * nt) + sums + 7) / 8 * 8 + 8 * I4_NW * I4_SLOTS;
-            if (rest + 2 * I4_NW * I4_BOX > I4_SMEM) continue;
+            if (rest + I4_NW * I4_BOX > I4_SMEM) continue;
             const int n_slots = std::min<int>(I4_SLOTS, (int)((I4_SMEM - rest) / (I4_NW * I4_BOX)));
             const int64_t tiles = (int64_t)((a.n + R - 1) / R) * slices, room = std::max(1, nsm / cs);
             const int64_t rounds = (tiles + room - 1) / room;
             const int boxes = ((groups + 1) / 2 + kw - 1) / kw;
-            const double us = (double)rounds * (std::max(boxes * kw * (R / 16) * I4_BOX / 45e3, boxes * 0.15) + I4_TILE_US * (sums > 0) + (cs > 1 ? I4_CLUSTER_US : 0.0)) + (double)groups * p.rows_per * I4_X_US;
-            if ((ekw && atoi(ekw) != kw) || (ecs && atoi(ecs) != cs)) continue;
+            const double us = (double)rounds * (std::max(boxes * kw * (R / 32) * I4_BOX / 45e3, boxes * 0.15) + I4_TILE_US * (sums > 0) + (cs > 1 ? I4_CLUSTER_US : 0.0)) + (double)groups * p.rows_per * I4_X_US;
             if (p.cluster == 0 || us < best) {
                 best = us;
                 p.cluster = cs;
@@ -404,7 +426,6 @@ cudaError_t launch_dt(const Int4Args &a, const CUtensorMap &map, int nsm, cudaSt
                 p.smem = p.bar_at + (size_t)8 * I4_NW * n_slots;
             }
         }
-    if (getenv("I4_SHOW")) printf("kw %d cluster %d rows_per %d slots %d est %.1f\n", p.kw, p.cluster, p.rows_per, p.slots, best);
     if (p.cluster == 0) return cudaErrorInvalidConfiguration;
     return nt == 1   ? launch_of<DT, 1>(a, p, map, nsm, s)
            : nt == 2 ? launch_of<DT, 2>(a, p, map, nsm, s)
@@ -415,10 +436,10 @@ cudaError_t launch_dt(const Int4Args &a, const CUtensorMap &map, int nsm, cudaSt
 
 cudaError_t launch_int4_linear(const Int4Args &a, int dtype, int nsm, cudaStream_t s)
 {
-    // W as rows of k / 2 bytes; boxes of 16 rows and 128 bytes, swizzled. What lies past its edges reads as zeros.
+    // W as rows of k / 2 bytes; boxes of 32 rows and 128 bytes, swizzled. What lies past its edges reads as zeros.
     CUtensorMap map;
     const cuuint64_t dims[2] = {(cuuint64_t)a.k / 2, (cuuint64_t)a.n}, strides[1] = {(cuuint64_t)a.k / 2};
-    const cuuint32_t box[2] = {128, 16}, one[2] = {1, 1};
+    const cuuint32_t box[2] = {128, 32}, one[2] = {1, 1};
     const EncodeFn encode = tensor_map_encoder();
     if (!encode || encode(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, (void *)a.w, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
