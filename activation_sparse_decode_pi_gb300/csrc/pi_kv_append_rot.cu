@@ -16,7 +16,7 @@ constexpr int AR_NT = 256, AR_NW = AR_NT / 32;
 // sines (tokens past it work theirs out for every head).
 template <int W>
 struct AppendRotCfg {
-    static constexpr int BUF = W == 1 ? 1 : 8, CTAS = W == 1 ? 3 : 2, TABLE = W == 1 ? 16 * 1024 : 64 * 1024;
+    static constexpr int BUF = W == 1 ? 1 : 4, CTAS = 2, TABLE = W == 1 ? 16 * 1024 : 64 * 1024;
 };
 
 // turn_cos_sin out of line, for tokens without a place in the table
@@ -25,11 +25,11 @@ __device__ __noinline__ float2 turn_cos_sin_call(uint64_t turns, int p, float am
 template <int DT, int D, int W>
 __global__ void __launch_bounds__(AR_NT, AppendRotCfg<W>::CTAS) k_kv_append_rot(const KvAppendRotArgs a)
 {
-    constexpr int LPR = D / 8, RPW = 32 / LPR, BUF = AppendRotCfg<W>::BUF, NTH = W * 32;
+    constexpr int LPR = D / 8, BUF = AppendRotCfg<W>::BUF, NTH = W * 32, ES = DT == DT_F32 ? 4 : 2;
     extern __shared__ __align__(16) float table[];   // [a.cap][rot / 2] cosines, then sines
     __shared__ float s_top[AR_NW];
     const KvView &c = a.c;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, P = c.page, sub = lane / LPR;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, P = c.page;
     pdl_wait();
     pdl_launch_dependents();
     const bool flag = blockIdx.y == 0 && blockIdx.z == 0;
@@ -44,39 +44,15 @@ __global__ void __launch_bounds__(AR_NT, AppendRotCfg<W>::CTAS) k_kv_append_rot(
     const int hq0 = (int)((int64_t)c.hq * slice / slices), hq1 = (int)((int64_t)c.hq * (slice + 1) / slices);
     const RotaryLane l = rotary_lane<D>(a.r, lane);
     float *const cosv = table, *const sinv = table + a.cap * half;
-    // coefficients of a token for the lane's eight elements and their partners: a pair's (c, -s) and (c, s)
-    auto coefs = [&](int row, int pos, const float (&w)[8], const float (&wp)[8], float (&wc)[8], float (&ws)[8]) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) wc[e] = w[e], ws[e] = wp[e];
+    auto pair_cos_sin = [&](int row, int pos, float2 (&cs)[4]) {   // of the lane's four pairs, at the page's row-th new token
         if (!l.turned) return;
-        if (a.r.interleaved) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int i = l.pair0 + e;
-                const float2 cs = row < a.cap ? make_float2(cosv[row * half + i], sinv[row * half + i])
-                                              : turn_cos_sin_call(a.r.turns[i], pos, a.r.amp);
-                wc[2 * e] *= cs.x;
-                wc[2 * e + 1] *= cs.x;
-                ws[2 * e] *= -cs.y;
-                ws[2 * e + 1] *= cs.y;
-            }
-        } else if (row < a.cap) {
-            const float4 *cp = (const float4 *)(cosv + row * half + l.pair0), *sp = (const float4 *)(sinv + row * half + l.pair0);
-            const float4 c0 = cp[0], c1 = cp[1], s0 = sp[0], s1 = sp[1];
-            const float cc[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
-            const float ss[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                wc[e] *= cc[e];
-                ws[e] *= l.second ? ss[e] : -ss[e];
-            }
+        if (row < a.cap) {
+            const float4 c4 = *(const float4 *)(cosv + row * half + l.pair0), s4 = *(const float4 *)(sinv + row * half + l.pair0);
+            cs[0] = make_float2(c4.x, s4.x), cs[1] = make_float2(c4.y, s4.y);
+            cs[2] = make_float2(c4.z, s4.z), cs[3] = make_float2(c4.w, s4.w);
         } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float2 cs = turn_cos_sin_call(a.r.turns[l.pair0 + e], pos, a.r.amp);
-                wc[e] *= cs.x;
-                ws[e] *= l.second ? cs.y : -cs.y;
-            }
+            for (int i = 0; i < 4; ++i) cs[i] = turn_cos_sin_call(a.r.turns[l.pair0 + i], pos, a.r.amp);
         }
     };
 
@@ -101,33 +77,37 @@ __global__ void __launch_bounds__(AR_NT, AppendRotCfg<W>::CTAS) k_kv_append_rot(
         for (int u = slice * (AR_NW / W) + warp / W; page >= 0 && u < 2 * c.hkv; u += slices * (AR_NW / W)) {
             const bool val = u >= c.hkv;
             const int h = val ? u - c.hkv : u;
-            const void *src = val ? a.v : a.k;
+            const uint8_t *src = (const uint8_t *)(val ? a.v : a.k) + (row0 * a.ld + h * D + l.off_a) * ES;
             uint8_t *codes = (val ? a.l.v : a.l.k) + ((size_t)page * c.hkv + h) * P * D;
             float *scale = (val ? a.l.vs : a.l.ks) + (size_t)page * c.hkv + h;
             const int nv = rows * LPR;   // groups of eight of the block
-            float w[8], wp[8];
-            norm_weights<D>(a.r, l, val ? nullptr : a.r.kn, lane, w, wp);
             auto fetch = [&](int v) {
                 Eight<DT> raw;
-                if (v < nv) raw.load(src, (row0 + v / LPR) * a.ld + h * D + lane % LPR * 8);
+                const uint8_t *const at = src + ((v / LPR) * a.ld) * ES;
+                if (v < nv) raw.load(at, at + (l.off_b - l.off_a) * ES);
                 else raw.clear();
                 return raw;
             };
-            auto finish = [&](const Eight<DT> &raw, int v, float (&f)[8]) {   // by the whole warp
+            auto finish = [&](const Eight<DT> &raw, int v, float2 (&f)[4]) {   // by the whole warp
                 if (val) {
                     raw.widen(f);
                     return;
                 }
-                float wc[8], ws[8];
+                float2 cs[4];
                 const int row = min(v / LPR, rows - 1);
-                coefs(row, pos0 + row, w, wp, wc, ws);
-                rotate_eight<DT, D>(a.r, l, raw, wc, ws, f);
+                pair_cos_sin(row, pos0 + row, cs);
+                rotate_eight<DT, D>(a.r, l, raw, rotary_coef(a.r, l, a.r.kn, cs), f);
             };
-            float buf[BUF][8];
+            auto largest = [](float top, const float2 (&f)[4]) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) top = fmaxf(top, fmaxf(finite_abs(f[e].x), finite_abs(f[e].y)));
+                return top;
+            };
+            float2 buf[BUF][4];
             float top = 0.f;
             const float was = p0 > 0 ? *scale : 0.f;
             const int v0 = th & ~31;   // the warp's first
-            constexpr int LD = BUF < 4 ? BUF : 4;   // loads under way at a time
+            constexpr int LD = BUF < 2 ? BUF : 2;   // loads under way at a time
 #pragma unroll
             for (int x0 = 0; x0 < BUF; x0 += LD) {
                 Eight<DT> raw[LD];
@@ -137,19 +117,13 @@ __global__ void __launch_bounds__(AR_NT, AppendRotCfg<W>::CTAS) k_kv_append_rot(
                 for (int x = 0; x < LD; ++x)
                     if ((x0 + x) * NTH + v0 < nv) {
                         finish(raw[x], (x0 + x) * NTH + th, buf[x0 + x]);
-                        if ((x0 + x) * NTH + th < nv) {
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) top = fmaxf(top, finite_abs(buf[x0 + x][e]));
-                        }
+                        if ((x0 + x) * NTH + th < nv) top = largest(top, buf[x0 + x]);
                     }
             }
             for (int v = BUF * NTH; v + v0 < nv; v += NTH) {
-                float f[8];
+                float2 f[4];
                 finish(fetch(v + th), v + th, f);
-                if (v + th < nv) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) top = fmaxf(top, finite_abs(f[e]));
-                }
+                if (v + th < nv) top = largest(top, f);
             }
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -168,50 +142,35 @@ __global__ void __launch_bounds__(AR_NT, AppendRotCfg<W>::CTAS) k_kv_append_rot(
             // x / s: the reciprocal of a power of two is exact (a scale the caller put there may be another number)
             const bool pow2 = (__float_as_uint(s) & 0x7fffffu) == 0;
             const float rcp = 1.f / s;
-            auto put = [&](int v, float (&f)[8]) {
+            auto put = [&](int v, float2 (&f)[4]) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) f[e] = pow2 ? f[e] * rcp : f[e] / s;
+                for (int e = 0; e < 4; ++e) f[e] = pow2 ? fmul2(f[e], make_float2(rcp, rcp)) : make_float2(f[e].x / s, f[e].y / s);
                 uint32_t o[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
-                    o[e] = f32x2_e4m3x2(f[4 * e], f[4 * e + 1]) | (uint32_t)f32x2_e4m3x2(f[4 * e + 2], f[4 * e + 3]) << 16;
-                if (v < nv) *(uint2 *)(codes + (size_t)(p0 + v / LPR) * D + lane % LPR * 8) = make_uint2(o[0], o[1]);
+                    o[e] = f32x2_e4m3x2(f[2 * e].x, f[2 * e].y) | (uint32_t)f32x2_e4m3x2(f[2 * e + 1].x, f[2 * e + 1].y) << 16;
+                if (v < nv) {
+                    uint8_t *const to = codes + (size_t)(p0 + v / LPR) * D;
+                    *(uint32_t *)(to + l.off_a) = o[0];
+                    *(uint32_t *)(to + l.off_b) = o[1];
+                }
             };
 #pragma unroll
             for (int x = 0; x < BUF; ++x)
                 if (x * NTH + v0 < nv) put(x * NTH + th, buf[x]);
             for (int v = BUF * NTH; v + v0 < nv; v += NTH) {
-                float f[8];
+                float2 f[4];
                 finish(fetch(v + th), v + th, f);
                 put(v + th, f);
             }
             if constexpr (W > 1) bar_sync(1 + warp / W, NTH);
         }
         // ---------------------------------------------------------------- queries: a token to a warp
-        float w[8], wp[8];
-        norm_weights<D>(a.r, l, a.r.qn, lane, w, wp);
-        constexpr int U = 4;
         for (int t = warp; t < rows; t += AR_NW) {
-            float wc[8], ws[8];
-            coefs(t, pos0 + t, w, wp, wc, ws);
-            const int64_t at = (row0 + t) * a.ldq + lane % LPR * 8, to = (row0 + t) * a.ldqo + lane % LPR * 8;
-            for (int h = hq0; h < hq1; h += U * RPW) {
-                Eight<DT> raw[U];
-#pragma unroll
-                for (int x = 0; x < U; ++x) {
-                    const int r = h + x * RPW + sub;
-                    if (r < hq1) raw[x].load(a.q, at + (int64_t)r * D);
-                    else raw[x].clear();
-                }
-#pragma unroll
-                for (int x = 0; x < U; ++x) {
-                    if (h + x * RPW >= hq1) break;
-                    const int r = h + x * RPW + sub;
-                    float out[8];
-                    rotate_eight<DT, D>(a.r, l, raw[x], wc, ws, out);
-                    if (r < hq1) Eight<DT>::store(a.qo, to + (int64_t)r * D, out);
-                }
-            }
+            float2 cs[4];
+            pair_cos_sin(t, pos0 + t, cs);
+            rotate_heads<DT, D, W == 1 ? 2 : 4>(a.r, l, rotary_coef(a.r, l, a.r.qn, cs), (const uint8_t *)a.q + (row0 + t) * a.ldq * ES,
+                                                (uint8_t *)a.qo + (row0 + t) * a.ldqo * ES, hq0, hq1, lane);
         }
     }
 }
@@ -250,7 +209,7 @@ template <int DT, int D>
 cudaError_t launch_w(const KvAppendRotArgs &a, int nsm, cudaStream_t s)
 {
     // Four warps to a unit where sequences bring 4 tokens or more on average, as in pi_kv_append.cu.
-    return a.b.n_tokens >= 4 * (int64_t)a.b.n ? launch_of<DT, D, 4>(a, nsm, s) : launch_of<DT, D, 1>(a, nsm, s);
+    return a.b.n_tokens >= 4 * (int64_t)a.b.n ? launch_of<DT, D, 8>(a, nsm, s) : launch_of<DT, D, 1>(a, nsm, s);
 }
 
 template <int DT>

@@ -46,7 +46,7 @@ struct RotateArgs {
     void *qo, *ko;
     int64_t ldq, ldqo, ldk, ldko;   // elements
     int n_tokens, hq, hk;
-    int parts_q, parts_k;           // the launch's: warps that share a token's heads
+    int parts;                      // the launch's: warps that share a token's heads
 };
 cudaError_t launch_rotate(const RotateArgs &a, int dim, int dtype, int nsm, cudaStream_t s);
 

@@ -1,8 +1,9 @@
 // pi_rotary.cuh -- norm and position rotation of a head, eight elements to a lane (sm_103a).
 //
-// A head of D elements lies in D / 8 neighbouring lanes of a warp. Pairs are eight elements or a multiple apart (rot_dim is
-// a multiple of 16) or neighbours, so an element's partner is in another lane at the same place or in its own lane.
-// With w the norm's weights, c and s the angle's cosine and sine times amp (s negative for a pair's first),
+// A head of D elements lies in D / 8 neighbouring lanes of a warp, each with two runs of four elements, A and B. In the half
+// layout the first rot / 8 lanes take A from the first half of what is turned and B from the same place of the second, so
+// an element's partner is in the same lane; neighbouring pairs are anyway. With w the norm's weights, c and s the
+// angle's cosine and sine times amp (s negative for a pair's first),
 //   out = inv (x w c + x' w' s),   inv = 1 / sqrt(mean x^2 + eps):
 // the two coefficients of an element depend on the token only, and serve all its heads.
 #pragma once
@@ -12,60 +13,64 @@
 
 namespace pi {
 
-// Eight consecutive elements, as they lie in memory.
+// A lane's eight elements, as they lie in memory.
 template <int DT>
 struct Eight {
-    static constexpr int W = DT == DT_F32 ? 8 : 4;   // 32-bit words
-    uint32_t w[W];
+    static constexpr int W = DT == DT_F32 ? 4 : 2;   // 32-bit words of a run
+    uint32_t w[2][W];
 
-    __device__ __forceinline__ void load(const void *p, int64_t at)
+    __device__ __forceinline__ void load(const uint8_t *a, const uint8_t *b)   // where its runs lie
     {
-        const uint4 *s = (const uint4 *)((const uint8_t *)p + at * (DT == DT_F32 ? 4 : 2));
 #pragma unroll
-        for (int i = 0; i < W / 4; ++i) {
-            const uint4 v = s[i];
-            w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+        for (int r = 0; r < 2; ++r) {
+            if constexpr (DT == DT_F32) {
+                const uint4 v = *(const uint4 *)(r ? b : a);
+                w[r][0] = v.x, w[r][1] = v.y, w[r][2] = v.z, w[r][3] = v.w;
+            } else {
+                const uint2 v = *(const uint2 *)(r ? b : a);
+                w[r][0] = v.x, w[r][1] = v.y;
+            }
         }
     }
     __device__ __forceinline__ void clear()
     {
 #pragma unroll
-        for (int i = 0; i < W; ++i) w[i] = 0;
-    }
-    __device__ __forceinline__ void widen(float (&f)[8]) const
-    {
-        if constexpr (DT == DT_F32) {
+        for (int r = 0; r < 2; ++r)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(w[i]);
-        } else {
-            unpack<DT>(make_uint4(w[0], w[1], w[2], w[3]), f);
+            for (int i = 0; i < W; ++i) w[r][i] = 0;
+    }
+    // elements 2 i, 2 i + 1 of A (i < 2) and of B (i >= 2)
+    __device__ __forceinline__ void widen(float2 (&f)[4]) const
+    {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t *const v = w[i >> 1];
+            if constexpr (DT == DT_F32) {
+                f[i] = make_float2(__uint_as_float(v[2 * (i & 1)]), __uint_as_float(v[2 * (i & 1) + 1]));
+            } else if constexpr (DT == DT_BF16) {
+                f[i] = make_float2(__uint_as_float(v[i & 1] << 16), __uint_as_float(v[i & 1] & 0xffff0000u));
+            } else {
+                f[i] = __half22float2(u32_h2(v[i & 1]));
+            }
         }
     }
-    __device__ __forceinline__ Eight from_lane(int lane) const
+    static __device__ __forceinline__ void store(uint8_t *a, uint8_t *b, const float2 (&f)[4])
     {
-        Eight r;
 #pragma unroll
-        for (int i = 0; i < W; ++i) r.w[i] = __shfl_sync(0xffffffffu, w[i], lane);
-        return r;
-    }
-    static __device__ __forceinline__ void store(void *p, int64_t at, const float (&f)[8])
-    {
-        uint4 *d = (uint4 *)((uint8_t *)p + at * (DT == DT_F32 ? 4 : 2));
-        if constexpr (DT == DT_F32) {
-            d[0] = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
-            d[1] = make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]), __float_as_uint(f[7]));
-        } else {
-            uint32_t o[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
+        for (int r = 0; r < 2; ++r) {
+            const float2 x = f[2 * r], y = f[2 * r + 1];
+            if constexpr (DT == DT_F32) {
+                *(float4 *)(r ? b : a) = make_float4(x.x, x.y, y.x, y.y);
+            } else {
+                uint2 o;
                 if constexpr (DT == DT_BF16) {
-                    const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-                    o[i] = *reinterpret_cast<const uint32_t *>(&h);
+                    const __nv_bfloat162 h = __floats2bfloat162_rn(x.x, x.y), k = __floats2bfloat162_rn(y.x, y.y);
+                    o = make_uint2(*reinterpret_cast<const uint32_t *>(&h), *reinterpret_cast<const uint32_t *>(&k));
                 } else {
-                    o[i] = pack_f16(f[2 * i], f[2 * i + 1]);
+                    o = make_uint2(pack_f16(x.x, x.y), pack_f16(y.x, y.y));
                 }
+                *(uint2 *)(r ? b : a) = o;
             }
-            d[0] = make_uint4(o[0], o[1], o[2], o[3]);
         }
     }
 };
@@ -83,74 +88,136 @@ __device__ __forceinline__ float2 turn_cos_sin(uint64_t turns, int p, float amp)
     return quarter & 2 ? make_float2(-a * amp, -b * amp) : make_float2(a * amp, b * amp);
 }
 
-// What a lane knows of its eight elements' columns.
+// (a.x b.x, a.y b.y) in one instruction
+__device__ __forceinline__ float2 fmul2(float2 a, float2 b)
+{
+    unsigned long long r;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(r)
+        : "l"(*reinterpret_cast<unsigned long long *>(&a)), "l"(*reinterpret_cast<unsigned long long *>(&b)));
+    return *reinterpret_cast<float2 *>(&r);
+}
+
+// Which elements of a head a lane has.
 struct RotaryLane {
-    int pair0;        // pair of its first element (interleaved: of its first two)
-    int partner;      // lane with the partners (itself: interleaved, or not turned)
-    bool turned, second;
+    int off_a, off_b;   // first elements of its runs
+    int pair0;          // first of its four pairs
+    bool turned;
 };
 
 template <int D>
 __device__ __forceinline__ RotaryLane rotary_lane(const RotaryDev &r, int lane)
 {
-    constexpr int LPR = D / 8;
-    const int l = lane % LPR, col = l * 8, half = r.rot / 2;
+    const int l = lane % (D / 8);
     RotaryLane o;
-    o.turned = col < r.rot;
-    o.second = o.turned && !r.interleaved && col >= half;
-    o.pair0 = !o.turned ? 0 : r.interleaved ? col / 2 : o.second ? col - half : col;
-    o.partner = !o.turned || r.interleaved ? lane : o.second ? lane - half / 8 : lane + half / 8;
+    o.turned = 8 * l < r.rot;
+    o.pair0 = o.turned ? 4 * l : 0;
+    const bool halves = o.turned && !r.interleaved;
+    o.off_a = halves ? 4 * l : 8 * l;
+    o.off_b = halves ? r.rot / 2 + 4 * l : 8 * l + 4;
     return o;
 }
 
-// 1 / sqrt(mean x^2 + eps) of the head that the lane's D / 8 lanes hold
-template <int D>
-__device__ __forceinline__ float head_inv(const float (&x)[8], float eps)
-{
-    float q = 0.f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) q = fmaf(x[e], x[e], q);
-#pragma unroll
-    for (int o = D / 16; o > 0; o >>= 1) q += __shfl_xor_sync(0xffffffffu, q, o);
-    return rsqrtf(q * (1.f / D) + eps);
-}
+// Coefficients of a lane's elements, as its runs lie: x's own, and its partner's.
+struct RotaryCoef {
+    float2 own[4], other[4];
+};
 
-// The lane's eight outputs: own coefficients wc, partners' ws. The whole warp takes part.
-template <int DT, int D>
-__device__ __forceinline__ void rotate_eight(const RotaryDev &r, const RotaryLane &l, const Eight<DT> &raw,
-                                             const float (&wc)[8], const float (&ws)[8], float (&out)[8])
+// From a norm's weights (NULL: ones) and the cosines and sines, times amp, of the lane's four pairs.
+__device__ __forceinline__ RotaryCoef rotary_coef(const RotaryDev &r, const RotaryLane &l, const float *weight, const float2 (&cs)[4])
 {
-    float x[8], y[8];
-    raw.widen(x);
-    const float inv = r.norm ? head_inv<D>(x, r.eps) : 1.f;
+    float w[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e] = 1.f;
+    if (r.norm && weight) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = weight[e < 4 ? l.off_a + e : l.off_b + e - 4];
+    }
+    RotaryCoef o;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        o.own[i] = make_float2(w[2 * i], w[2 * i + 1]);
+        o.other[i] = make_float2(0.f, 0.f);
+    }
+    if (!l.turned) return o;
     if (r.interleaved) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = x[e ^ 1];
+        for (int i = 0; i < 4; ++i) {   // pair i: elements 2 i and 2 i + 1
+            o.own[i] = make_float2(w[2 * i] * cs[i].x, w[2 * i + 1] * cs[i].x);
+            o.other[i] = make_float2(-w[2 * i + 1] * cs[i].y, w[2 * i] * cs[i].y);
+        }
     } else {
-        raw.from_lane(l.partner).widen(y);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {   // pairs 2 i and 2 i + 1: their firsts in A, their seconds in B
+            const float2 u = cs[2 * i], v = cs[2 * i + 1];
+            o.own[i] = make_float2(w[2 * i] * u.x, w[2 * i + 1] * v.x);
+            o.own[2 + i] = make_float2(w[4 + 2 * i] * u.x, w[5 + 2 * i] * v.x);
+            o.other[i] = make_float2(-w[4 + 2 * i] * u.y, -w[5 + 2 * i] * v.y);
+            o.other[2 + i] = make_float2(w[2 * i] * u.y, w[2 * i + 1] * v.y);
+        }
+    }
+    return o;
+}
+
+// The lane's eight outputs. The whole warp takes part.
+template <int DT, int D>
+__device__ __forceinline__ void rotate_eight(const RotaryDev &r, const RotaryLane &l, const Eight<DT> &raw, const RotaryCoef &k,
+                                             float2 (&out)[4])
+{
+    float2 x[4];
+    raw.widen(x);
+    float inv = 1.f;
+    if (r.norm) {   // 1 / sqrt(mean x^2 + eps) of the head, over its D / 8 lanes
+        float2 q = fmul2(x[0], x[0]);
+#pragma unroll
+        for (int i = 1; i < 4; ++i) q = ffma2(x[i], x[i], q);
+        float s = q.x + q.y;
+#pragma unroll
+        for (int o = D / 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        inv = rsqrtf(s * (1.f / D) + r.eps);
     }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        float v = x[e] * wc[e];
-        if (l.turned) v = fmaf(y[e], ws[e], v);   // (not turned: its partner's infinity must not meet a zero)
-        out[e] = v * inv;
+    for (int i = 0; i < 4; ++i) out[i] = fmul2(x[i], k.own[i]);
+    if (l.turned) {   // (not turned: nothing that lies beside it may meet a zero, for 0 * infinity)
+        if (r.interleaved) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) out[i] = ffma2(make_float2(x[i].y, x[i].x), k.other[i], out[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) out[i] = ffma2(x[i ^ 2], k.other[i], out[i]);
+        }
+    }
+    if (r.norm) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) out[i] = fmul2(out[i], make_float2(inv, inv));
     }
 }
 
-// Weights of the lane's eight elements and of their partners (ones without a norm).
-template <int D>
-__device__ __forceinline__ void norm_weights(const RotaryDev &r, const RotaryLane &l, const float *weight, int lane,
-                                             float (&w)[8], float (&wp)[8])
+// Heads [h0, h1) of one token: src and dst are where the token's heads of the array begin, k its coefficients. A warp has
+// 256 / D heads to a round, and U rounds of loads under way.
+template <int DT, int D, int U>
+__device__ __forceinline__ void rotate_heads(const RotaryDev &r, const RotaryLane &l, const RotaryCoef &k, const void *src,
+                                             void *dst, int h0, int h1, int lane)
 {
-    constexpr int LPR = D / 8;
+    constexpr int RPW = 256 / D, ES = DT == DT_F32 ? 4 : 2, ROUND = RPW * D * ES;
+    const int sub = lane / (D / 8), mine = h0 * D + sub * D;
+    const uint8_t *sa = (const uint8_t *)src + (int64_t)(mine + l.off_a) * ES, *sb = sa + (l.off_b - l.off_a) * ES;
+    uint8_t *da = (uint8_t *)dst + (int64_t)(mine + l.off_a) * ES, *db = da + (l.off_b - l.off_a) * ES;
+    for (int left = h1 - h0; left > 0; left -= U * RPW) {
+        Eight<DT> raw[U];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) w[e] = wp[e] = 1.f;
-    if (!r.norm || !weight) return;
-    const float *a = weight + lane % LPR * 8, *b = weight + l.partner % LPR * 8;
+        for (int u = 0; u < U; ++u) {
+            if (u * RPW + sub < left) raw[u].load(sa + u * ROUND, sb + u * ROUND);
+            else raw[u].clear();
+        }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        w[e] = a[e];
-        wp[e] = r.interleaved ? a[e ^ 1] : b[e];
+        for (int u = 0; u < U; ++u) {
+            if (u * RPW >= left) break;
+            float2 out[4];
+            rotate_eight<DT, D>(r, l, raw[u], k, out);
+            if (u * RPW + sub < left) Eight<DT>::store(da + u * ROUND, db + u * ROUND, out);
+        }
+        sa += U * ROUND, sb += U * ROUND, da += U * ROUND, db += U * ROUND;
     }
 }
 

@@ -1,7 +1,7 @@
 // pi_rotate.cu -- norms of query and key heads with the position rotation (sm_103a).
 //
-// Each element is read and written once, and the bytes bound it. A warp takes a token and some of its heads (all of one
-// array): it works out the token's coefficients once, then streams heads, four rounds of loads at a time.
+// Each element is read and written once, and the bytes bound it. A warp takes a token and some of its heads: it works out
+// the cosines and sines of its columns once, then streams queries and keys, four rounds of loads at a time.
 #include <algorithm>
 
 #include "pi_rotary.cuh"
@@ -11,80 +11,39 @@ namespace pi {
 constexpr int RO_NT = 256, RO_NW = RO_NT / 32;
 
 template <int DT, int D>
-__global__ void __launch_bounds__(RO_NT) k_rotate(const RotateArgs a)
+__global__ void __launch_bounds__(RO_NT, DT == DT_F32 ? 3 : 4) k_rotate(const RotateArgs a)
 {
-    constexpr int LPR = D / 8, RPW = 32 / LPR, U = 4;
-    const int lane = threadIdx.x & 31, sub = lane / LPR;
+    constexpr int ES = DT == DT_F32 ? 4 : 2;
+    const int lane = threadIdx.x & 31;
     pdl_wait();
     pdl_launch_dependents();
     const int64_t item = (int64_t)blockIdx.x * RO_NW + (threadIdx.x >> 5);
-    const int parts = a.parts_q + a.parts_k;
-    if (item >= (int64_t)a.n_tokens * parts) return;
-    const int64_t tok = item / parts;
-    const int part = (int)(item % parts);
-    const bool key = part >= a.parts_q;
-    const int heads = key ? a.hk : a.hq, n = key ? a.parts_k : a.parts_q, x = key ? part - a.parts_q : part;
-    const int h0 = (int)((int64_t)heads * x / n), h1 = (int)((int64_t)heads * (x + 1) / n);
-    const uint8_t *src = (const uint8_t *)(key ? a.k : a.q);
-    uint8_t *dst = (uint8_t *)(key ? a.ko : a.qo);
-    const int64_t at = tok * (key ? a.ldk : a.ldq) + lane % LPR * 8, to = tok * (key ? a.ldko : a.ldqo) + lane % LPR * 8;
-
-    Eight<DT> raw[U];
-    auto load = [&](int h) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int r = h + u * RPW + sub;
-            if (r < h1) raw[u].load(src, at + (int64_t)r * D);
-            else raw[u].clear();
-        }
-    };
-    load(h0);
+    if (item >= (int64_t)a.n_tokens * a.parts) return;
+    const int64_t tok = item / a.parts;
+    const int part = (int)(item - tok * a.parts), heads = a.hq + a.hk;
+    const int h_lo = (int)((int64_t)heads * part / a.parts), h_hi = (int)((int64_t)heads * (part + 1) / a.parts);
     const RotaryLane l = rotary_lane<D>(a.r, lane);
-    float wc[8], ws[8];
-    norm_weights<D>(a.r, l, key ? a.r.kn : a.r.qn, lane, wc, ws);
+    float2 cs[4];
     if (l.turned) {
         const int p = a.pos[tok];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            if (a.r.interleaved && (e & 1)) continue;
-            const float2 cs = turn_cos_sin(a.r.turns[l.pair0 + (a.r.interleaved ? e / 2 : e)], p, a.r.amp);
-            wc[e] *= cs.x;
-            ws[e] *= l.second ? cs.y : -cs.y;
-            if (a.r.interleaved) {
-                wc[e + 1 & 7] *= cs.x;
-                ws[e + 1 & 7] *= cs.y;
-            }
-        }
+        for (int i = 0; i < 4; ++i) cs[i] = turn_cos_sin(a.r.turns[l.pair0 + i], p, a.r.amp);
     }
-    for (int h = h0; h < h1; h += U * RPW) {
-        Eight<DT> now[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) now[u] = raw[u];
-        if (h + U * RPW < h1) load(h + U * RPW);
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int r = h + u * RPW + sub;
-            if (h + u * RPW >= h1) break;
-            float out[8];
-            rotate_eight<DT, D>(a.r, l, now[u], wc, ws, out);
-            if (r < h1) Eight<DT>::store(dst, to + (int64_t)r * D, out);
-        }
-    }
+    if (h_lo < a.hq)
+        rotate_heads<DT, D, 4>(a.r, l, rotary_coef(a.r, l, a.r.qn, cs), (const uint8_t *)a.q + tok * a.ldq * ES,
+                               (uint8_t *)a.qo + tok * a.ldqo * ES, h_lo, min(h_hi, a.hq), lane);
+    if (h_hi > a.hq)
+        rotate_heads<DT, D, 4>(a.r, l, rotary_coef(a.r, l, a.r.kn, cs), (const uint8_t *)a.k + tok * a.ldk * ES,
+                               (uint8_t *)a.ko + tok * a.ldko * ES, max(h_lo, a.hq) - a.hq, h_hi - a.hq, lane);
 }
 
 cudaError_t launch_rotate(const RotateArgs &in, int dim, int dtype, int nsm, cudaStream_t s)
 {
     RotateArgs a = in;
-    // Warps: about 32 to an SM where the tokens are few (a warp takes one round of heads at least), else one to a token
-    // and array.
-    const int64_t want = std::max<int64_t>(1, (int64_t)32 * nsm / a.n_tokens);
-    const int heads = a.hq + a.hk, round = 256 / dim;
-    const auto parts = [&](int h) {
-        return h == 0 ? 0 : (int)std::max<int64_t>(1, std::min<int64_t>((h + round - 1) / round, want * h / heads));
-    };
-    a.parts_q = parts(a.hq);
-    a.parts_k = parts(a.hk);
-    const int64_t items = (int64_t)a.n_tokens * (a.parts_q + a.parts_k);
+    // Warps to a token: 32 to an SM in all where the tokens are few (and a round of heads to each at least).
+    const int64_t rounds = (a.hq + a.hk + 256 / dim - 1) / (256 / dim);
+    a.parts = (int)std::max<int64_t>(1, std::min(rounds, (int64_t)32 * nsm / a.n_tokens));
+    const int64_t items = (int64_t)a.n_tokens * a.parts;
     Launch L;
     L.grid = dim3((unsigned)((items + RO_NW - 1) / RO_NW));
     L.block = dim3(RO_NT);
