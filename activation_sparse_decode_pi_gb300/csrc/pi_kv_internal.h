@@ -101,7 +101,8 @@ struct KvAppendRotArgs {
     const void *q, *k, *v;
     void *qo;
     int64_t ldq, ldqo, ld;   // elements
-    int cap;                 // the launch's: tokens of a page with a place in the table of cosines and sines
+    int cap, slices_q, warps;   // the launch's: new tokens of a page at most; CTAs that share a page's queries; warps to one
+                                // of its heads
 };
 cudaError_t launch_kv_append_rot(const KvAppendRotArgs &a, int dtype, int nsm, cudaStream_t s);
 

@@ -76,16 +76,16 @@ struct Eight {
 };
 
 // Cosine and sine of position p's angle, times amp. The angle in 2^-32 of a turn is a whole number; what is left of it
-// next to a multiple of a quarter turn goes to the functions, so its rounding to fp32 is at most 2^-26 of a turn.
+// next to a multiple of a quarter turn, u eighths of a turn with |u| <= 1, goes into polynomials in u^2 (fitted to
+// sin(pi u / 4) / u and cos(pi u / 4) for the smallest largest error: 2.5e-9 and 5e-11, in fp32 6e-8 of a value).
 __device__ __forceinline__ float2 turn_cos_sin(uint64_t turns, int p, float amp)
 {
-    const int x = (int)(uint32_t)((turns * (uint64_t)(int64_t)p) >> 32);
-    const int quarter = (int)(((uint32_t)x + 0x20000000u) >> 30);
-    const int left = (int)((uint32_t)x - ((uint32_t)quarter << 30));
-    float s, c;
-    sincospif((float)left * 0x1p-31f, &s, &c);
+    const uint32_t x = (uint32_t)((turns * (uint64_t)(int64_t)p) >> 32), quarter = (x + 0x20000000u) >> 30;
+    const float u = (float)(int)(x - (quarter << 30)) * 0x1p-29f, v = u * u;
+    const float s = amp * (u * fmaf(v, fmaf(v, fmaf(v, -0x1.2d9bb8p-15f, 0x1.465ec6p-9f), -0x1.4abbbap-4f), 0x1.921fb6p-1f));
+    const float c = amp * fmaf(v, fmaf(v, fmaf(v, fmaf(v, 0x1.d9c364p-19f, -0x1.55c57cp-12f), 0x1.03c1dcp-6f), -0x1.3bd3ccp-2f), 1.f);
     const float a = quarter & 1 ? -s : c, b = quarter & 1 ? c : s;   // a quarter turn: (c, s) -> (-s, c)
-    return quarter & 2 ? make_float2(-a * amp, -b * amp) : make_float2(a * amp, b * amp);
+    return quarter & 2 ? make_float2(-a, -b) : make_float2(a, b);
 }
 
 // (a.x b.x, a.y b.y) in one instruction
@@ -123,16 +123,22 @@ struct RotaryCoef {
     float2 own[4], other[4];
 };
 
-// From a norm's weights (NULL: ones) and the cosines and sines, times amp, of the lane's four pairs.
-__device__ __forceinline__ RotaryCoef rotary_coef(const RotaryDev &r, const RotaryLane &l, const float *weight, const float2 (&cs)[4])
+// A norm's weights of the lane's elements (NULL: ones).
+__device__ __forceinline__ void rotary_weights(const RotaryDev &r, const RotaryLane &l, const float *weight, float (&w)[8])
 {
-    float w[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) w[e] = 1.f;
     if (r.norm && weight) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) w[e] = weight[e < 4 ? l.off_a + e : l.off_b + e - 4];
     }
+}
+
+// From a norm's weights (NULL: ones) and the cosines and sines, times amp, of the lane's four pairs.
+__device__ __forceinline__ RotaryCoef rotary_coef(const RotaryDev &r, const RotaryLane &l, const float *weight, const float2 (&cs)[4])
+{
+    float w[8];
+    rotary_weights(r, l, weight, w);
     RotaryCoef o;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -159,6 +165,47 @@ __device__ __forceinline__ RotaryCoef rotary_coef(const RotaryDev &r, const Rota
     return o;
 }
 
+// 1 / sqrt(mean x^2 + eps) of the head that the lane's D / 8 lanes hold
+template <int D>
+__device__ __forceinline__ float head_inv(const RotaryDev &r, const float2 (&x)[4])
+{
+    float2 q = fmul2(x[0], x[0]);
+#pragma unroll
+    for (int i = 1; i < 4; ++i) q = ffma2(x[i], x[i], q);
+    float s = q.x + q.y;
+#pragma unroll
+    for (int o = D / 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    return rsqrtf(s * (1.f / D) + r.eps);
+}
+
+// The lane's eight elements of one head, from its weights and the cosines and sines of its pairs (first two, last two): for
+// tokens that differ from lane to lane, where there are no coefficients to keep. The whole warp takes part.
+template <int D>
+__device__ __forceinline__ void rotate_once(const RotaryDev &r, const RotaryLane &l, const float (&w)[8], const float2 (&c)[2],
+                                            const float2 (&s)[2], float2 (&x)[4])
+{
+    if (r.norm) {
+        const float inv = head_inv<D>(r, x);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = fmul2(x[i], make_float2(w[2 * i] * inv, w[2 * i + 1] * inv));
+    }
+    if (!l.turned) return;
+    if (r.interleaved) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float cc = i & 1 ? c[i >> 1].y : c[i >> 1].x, ss = i & 1 ? s[i >> 1].y : s[i >> 1].x;
+            x[i] = ffma2(make_float2(x[i].y, x[i].x), make_float2(-ss, ss), fmul2(x[i], make_float2(cc, cc)));
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float2 a = x[i], b = x[2 + i];
+            x[i] = ffma2(b, make_float2(-s[i].x, -s[i].y), fmul2(a, c[i]));
+            x[2 + i] = ffma2(a, s[i], fmul2(b, c[i]));
+        }
+    }
+}
+
 // The lane's eight outputs. The whole warp takes part.
 template <int DT, int D>
 __device__ __forceinline__ void rotate_eight(const RotaryDev &r, const RotaryLane &l, const Eight<DT> &raw, const RotaryCoef &k,
@@ -167,15 +214,7 @@ __device__ __forceinline__ void rotate_eight(const RotaryDev &r, const RotaryLan
     float2 x[4];
     raw.widen(x);
     float inv = 1.f;
-    if (r.norm) {   // 1 / sqrt(mean x^2 + eps) of the head, over its D / 8 lanes
-        float2 q = fmul2(x[0], x[0]);
-#pragma unroll
-        for (int i = 1; i < 4; ++i) q = ffma2(x[i], x[i], q);
-        float s = q.x + q.y;
-#pragma unroll
-        for (int o = D / 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        inv = rsqrtf(s * (1.f / D) + r.eps);
-    }
+    if (r.norm) inv = head_inv<D>(r, x);
 #pragma unroll
     for (int i = 0; i < 4; ++i) out[i] = fmul2(x[i], k.own[i]);
     if (l.turned) {   // (not turned: nothing that lies beside it may meet a zero, for 0 * infinity)
