@@ -26,8 +26,8 @@ struct pi_kv {
     int dev = 0, nsm = 0;
     void *ws = nullptr;
     float *part = nullptr, *part_ml = nullptr;
-    float *rows_part = nullptr, *rows_ml = nullptr;
-    uint32_t *tickets = nullptr, *rows_tickets = nullptr, *status = nullptr;
+    float *rows_part = nullptr, *rows_ml = nullptr, *prior = nullptr, *short_part = nullptr, *short_ml = nullptr;
+    uint32_t *tickets = nullptr, *rows_tickets = nullptr, *short_tickets = nullptr, *status = nullptr;
     KvLayerDev *layers_dev = nullptr;
     int32_t *list_src = nullptr, *list_dst = nullptr, *list_count = nullptr, *page_map = nullptr;
 };
@@ -94,9 +94,14 @@ bool encode_pool(EncodeFn fn, CUtensorMap *m, const pi_kv_desc_t &d, void *base)
 template <int D>
 cudaError_t setup_of()
 {
-    for (cudaError_t e : {split_setup<D, 1, 1>(), split_setup<D, 1, 2>(), split_setup<D, 2, 1>(), split_setup<D, 2, 2>(),
-                          rows_setup<D, 1>(), rows_setup<D, 2>()})
+    for (cudaError_t e : {split_setup<D, 1, 1, false>(), split_setup<D, 1, 2, false>(), split_setup<D, 2, 1, false>(),
+                          split_setup<D, 2, 2, false>(), rows_setup<D, 1, false>(), rows_setup<D, 2, false>(),
+                          split_setup<D, 1, 1, true>(), split_setup<D, 1, 2, true>(), split_setup<D, 2, 1, true>(),
+                          split_setup<D, 2, 2, true>(), rows_setup<D, 1, true>(), rows_setup<D, 2, true>()})
         if (e != cudaSuccess) return e;
+    if constexpr (D <= 128)
+        for (cudaError_t e : {short_setup<D, 1>(), short_setup<D, 2>()})
+            if (e != cudaSuccess) return e;
     return cudaSuccess;
 }
 
@@ -106,7 +111,7 @@ cudaError_t setup_of()
 constexpr int ROWS_FROM = 33;
 
 // The kernels of one call: the split kernel for sequences with few rows, the rows kernel for the others.
-template <int D>
+template <int D, bool SHARED>
 cudaError_t attend_of(const pi_kv *h, int layer, KvAttendArgs a, cudaStream_t s)
 {
     const int64_t n = a.b.n, group = a.c.hq / a.c.hkv, rows = (int64_t)a.b.n_tokens * group;
@@ -114,21 +119,34 @@ cudaError_t attend_of(const pi_kv *h, int layer, KvAttendArgs a, cudaStream_t s)
     const bool many = rows >= ROWS_FROM && (n == 1 || a.b.n_tokens > n), few = n > 1 || !many;
     a.rows_from = many ? (few ? ROWS_FROM : 0) : INT32_MAX;
     cudaError_t e = cudaSuccess;
-    if (few) {
+    bool done = false;   // the few rows
+    if constexpr (SHARED && D <= 128)
+        if (few && a.pass == 2) {
+            KvAttendArgs b = a;
+            b.part = h->short_part;
+            b.part_ml = h->short_ml;
+            b.tickets = h->short_tickets;
+            e = a.dtype == PI_BF16 ? short_launch<D, 1>(b, h->nsm, s) : short_launch<D, 2>(b, h->nsm, s);
+            done = true;
+        }
+    if (few && !done) {
         // 16 rows to a tile where the rows of a sequence (on average: all that the host knows) fill more than 8: the cache
         // is then read once instead of twice (64 sequences, 16 heads to a group: 229 / 323 us with 16 / 8; 8 heads, 128
         // sequences: 381 / 330 us, since 16 leave room for fewer warps)
-        const bool wide = many || rows > 8 * n, one = a.dtype == PI_BF16;
-        const auto run = wide ? (one ? split_launch<D, 2, 1> : split_launch<D, 2, 2>)
-                              : (one ? split_launch<D, 1, 1> : split_launch<D, 1, 2>);
+        const bool wide = (many && !SHARED) || rows > 8 * n, one = a.dtype == PI_BF16;
+        const auto run = wide ? (one ? split_launch<D, 2, 1, SHARED> : split_launch<D, 2, 2, SHARED>)
+                              : (one ? split_launch<D, 1, 1, SHARED> : split_launch<D, 1, 2, SHARED>);
         e = run(a, h->map_k[layer], h->map_v[layer], h->nsm, s);
     }
     if (many && e == cudaSuccess) {
-        const int64_t items = (rows / rows_per_item(D) + n) * a.c.hkv;   // at most one partly filled per sequence
-        const int64_t splits = items < h->nsm ? std::min<int64_t>(16, 2 * h->nsm / items) : 1;
+        // (sequence, kv head, run of rows): at most one partly filled run to each sequence that has ROWS_FROM rows
+        const int64_t runs = rows / rows_per_item(D), items = (runs + n) * a.c.hkv;
+        const int64_t grid = a.rows_from ? std::min(runs + n, rows / a.rows_from) * a.c.hkv : items;
+        int64_t splits = items < h->nsm ? std::min<int64_t>(16, 2 * h->nsm / items) : 1;
+        if (a.pass == 1) splits = a.parts;
         const CUtensorMap &mk = h->map_k[layer], &mv = h->map_v[layer];
-        e = a.dtype == PI_F32 ? rows_launch<D, 2>(a, mk, mv, (unsigned)items, (unsigned)splits, s)
-                              : rows_launch<D, 1>(a, mk, mv, (unsigned)items, (unsigned)splits, s);
+        e = a.dtype == PI_F32 ? rows_launch<D, 2, SHARED>(a, mk, mv, (unsigned)grid, (unsigned)splits, s)
+                              : rows_launch<D, 1, SHARED>(a, mk, mv, (unsigned)grid, (unsigned)splits, s);
     }
     return e;
 }
@@ -187,7 +205,9 @@ pi_status_t kv_create(pi_kv_t **out, const pi_kv_desc_t *desc, const pi_kv_layer
     const size_t tick = up((size_t)nsm * 4), lay = up(sizeof(KvLayerDev) * (size_t)d.n_layers);
     const size_t rpart = up((size_t)2 * nsm * rows_per_item(d.head_dim) * d.head_dim * 4),
                  rml = up((size_t)2 * nsm * rows_per_item(d.head_dim) * 2 * 4);
-    const size_t total = 3 * list + part + ml + rpart + rml + 3 * tick + lay + 2 * 256;
+    const size_t prior = up((size_t)nsm * rows_per_item(d.head_dim) * (d.head_dim + 2) * 4);
+    const size_t spart = up((size_t)2 * SHORT_CTAS * nsm * 8 * d.head_dim * 4), sml = up((size_t)2 * SHORT_CTAS * nsm * 8 * 2 * 4);
+    const size_t total = 3 * list + part + ml + rpart + rml + prior + spart + sml + (3 + SHORT_CTAS) * tick + lay + 2 * 256;
     if (injected_fault() == FAULT_ALLOC) return PI_ERR_OOM;
     if ((s = cuda_status(cudaMalloc(&h->ws, total)))) return s;
     if (injected_fault() == FAULT_UPLOAD) return PI_ERR_CUDA;
@@ -202,8 +222,12 @@ pi_status_t kv_create(pi_kv_t **out, const pi_kv_desc_t *desc, const pi_kv_layer
     h->part_ml = (float *)take(ml);
     h->rows_part = (float *)take(rpart);
     h->rows_ml = (float *)take(rml);
+    h->prior = (float *)take(prior);
+    h->short_part = (float *)take(spart);
+    h->short_ml = (float *)take(sml);
     h->tickets = (uint32_t *)take(tick);
     h->rows_tickets = (uint32_t *)take(2 * tick);
+    h->short_tickets = (uint32_t *)take(SHORT_CTAS * tick);
     h->layers_dev = (KvLayerDev *)take(lay);
     h->list_src = (int32_t *)take(list);
     h->list_dst = (int32_t *)take(list);
@@ -290,7 +314,9 @@ pi_status_t attend_args(const pi_kv_t *h, int32_t layer, const int32_t *seqs, co
 
 cudaError_t attend(const pi_kv_t *h, int32_t layer, const KvAttendArgs &a, cudaStream_t s)
 {
-    const auto run = h->desc.head_dim == 64 ? attend_of<64> : h->desc.head_dim == 128 ? attend_of<128> : attend_of<256>;
+    const int d = h->desc.head_dim;
+    const auto run = a.pass ? (d == 64 ? attend_of<64, true> : d == 128 ? attend_of<128, true> : attend_of<256, true>)
+                            : (d == 64 ? attend_of<64, false> : d == 128 ? attend_of<128, false> : attend_of<256, false>);
     return run(h, layer, a, s);
 }
 
@@ -432,8 +458,13 @@ pi_status_t pi_kv_attend_shared(pi_kv_t *h, int32_t layer, const int32_t *seqs, 
     if ((s = check_ptr(plan, (size_t)PI_KV_SHARE_INTS(n, n_groups) * 4, 4, h->dev))) return s;
     const int64_t rows = (int64_t)n_tokens * h->desc.n_heads;
     if ((s = check_ptr(work, (size_t)rows * (h->desc.head_dim + 2) * 4, 16, h->dev))) return s;
-    a.prior = (float *)work;
-    a.prior_ml = a.prior + rows * h->desc.head_dim;
+    // Prefixes of many rows are split along their positions over what the GPU holds (at most one partly filled run of rows
+    // to each group but one); their parts lie in the workspace then, which has room for them: parts * most <= nsm.
+    const int64_t group_rows = (int64_t)n_tokens * (h->desc.n_heads / h->desc.n_kv_heads);
+    const int64_t run = rows_per_item(h->desc.head_dim), most = ((group_rows + run - 1) / run + n_groups - 1) * h->desc.n_kv_heads;
+    a.parts = n_groups > 0 && group_rows >= ROWS_FROM ? (int)std::max<int64_t>(1, std::min<int64_t>(16, h->nsm / most)) : 1;
+    a.prior = a.parts > 1 ? h->prior : (float *)work;
+    a.prior_ml = a.prior + a.parts * rows * h->desc.head_dim;
     const int32_t *lead = plan, *start = lead + n_groups, *len = start + n_groups + 1, *skip = len + n_groups, *was = skip + n;
     if (n_groups > 0) {
         KvAttendArgs first = a;

@@ -17,6 +17,8 @@ struct KvSeq {
 
 // Sequence i of the call, its fields brought into range; what was out of range is flagged and reads
 // as a sequence without new tokens.
+// SHARED: in a pass of pi_kv_attend_shared, whose batches may have lengths of their own and positions to skip.
+template <bool SHARED = false>
 __device__ __forceinline__ KvSeq kv_sequence(const KvView &c, const KvBatch &b, int i, bool flag)
 {
     KvSeq s;
@@ -26,19 +28,19 @@ __device__ __forceinline__ KvSeq kv_sequence(const KvView &c, const KvBatch &b, 
     s.start = s0;
     s.n = s1 - s0;
     s.len = s.skip = 0;
-    if (b.skip && (b.was[i] != s.row || b.was[b.n + i] != s0 || b.was[b.n + i + 1] != s1)) bad = true;
+    if (SHARED && b.skip && (b.was[i] != s.row || b.was[b.n + i] != s0 || b.was[b.n + i + 1] != s1)) bad = true;
     if (bad) {
         s.row = s.start = s.n = 0;
     } else {
-        s.len = b.len ? b.len[i] : c.length[s.row];
+        s.len = SHARED && b.len ? b.len[i] : c.length[s.row];
         if (s.len < 0 || s.len > c.max_pages * c.page) {
             s.len = s.n = 0;
             bad = true;
         }
-        if (b.len && s.len == 0) s.n = 0;   // nothing shared
-        if (b.skip) {
+        if (SHARED && b.len && s.len == 0) s.n = 0;   // nothing shared
+        if (SHARED && b.skip) {
             s.skip = b.skip[i];
-            if (s.skip < 0 || s.skip % KV_SHARE || s.skip > s.len - s.n) {
+            if (s.skip < 0 || s.skip % KV_SHARE || (s.skip > 0 && s.skip > s.len - s.n)) {
                 s.skip = s.len = s.n = 0;
                 bad = true;
             }
@@ -296,42 +298,51 @@ __device__ __forceinline__ float row_lse(float M, float S)
     return S == 0.f ? -INFINITY : (M + log2f(S)) * 0.6931471805599453f;
 }
 
-// Weights of two partial sums with maxima (or references) ma, mb and sums sa, sb against their common maximum M; S: the
-// joined sum. A sum whose maximum is -infinity counts only where it is not 0 (it is NaN then).
-struct JoinedRow {
-    float wa, wb, M, S;
-    __device__ __forceinline__ JoinedRow(float ma, float sa, float mb, float sb)
-    {
-        M = fmaxf(ma, mb);
-        wa = ma == -INFINITY ? (sa != 0.f ? 1.f : 0.f) : ex2(ma - M);
-        wb = mb == -INFINITY ? (sb != 0.f ? 1.f : 0.f) : ex2(mb - M);
-        S = wa * sa + wb * sb;
+// Weight of a partial sum s with maximum (or reference) m against the maximum M of all. One whose maximum is -infinity
+// counts only where its sum is not 0 (it is NaN then).
+__device__ __forceinline__ float part_weight(float m, float s, float M) { return m == -INFINITY ? (s != 0.f ? 1.f : 0.f) : ex2(m - M); }
+
+// Joins a row's numerators o (four columns), maximum M and sum S with the parts that the first pass left of it.
+__device__ __forceinline__ void join_prior(const KvAttendArgs &a, int64_t row, int D, int d, float4 &o, float &M, float &S)
+{
+    const int64_t rows = (int64_t)a.b.n_tokens * a.c.hq;
+    const float2 *const ml = (const float2 *)a.prior_ml + row;
+    const float *const num = a.prior + row * D + d;
+    float top = M;
+#pragma unroll 4
+    for (int x = 0; x < a.parts; ++x) top = fmaxf(top, __ldcg(ml + x * rows).x);
+    const float w0 = part_weight(M, S, top);
+    o = make_float4(o.x * w0, o.y * w0, o.z * w0, o.w * w0);
+    S *= w0;
+    M = top;
+#pragma unroll 4
+    for (int x = 0; x < a.parts; ++x) {
+        const float2 p = __ldcg(ml + x * rows);
+        const float w = part_weight(p.x, p.y, top);
+        const float4 v = __ldcg((const float4 *)(num + x * rows * D));
+        S += w * p.y;
+        if (w != 0.f) o.x += v.x * w, o.y += v.y * w, o.z += v.z * w, o.w += v.w * w;   // (an empty part has no numerators)
     }
-};
+}
 
 // Four columns (from d) of row `r` (query token r / G, head r % G of kv head h) of the sequence f (table row,
 // length, start, new tokens): numerators o over the sum S, and with d = 0 the row's log of the sum.
+template <bool SHARED>
 __device__ __forceinline__ void store_row(const KvAttendArgs &a, const int4 &f, int h, int G, int D, int r, int d,
                                           float4 o, float M, float S, bool join = false)
 {
     const int64_t tok = (int64_t)f.z + r / G;
     const int head = h * G + r % G;
-    if (a.pass) {
-        float *const po = a.prior + (tok * a.c.hq + head) * D + d, *const pml = a.prior_ml + (tok * a.c.hq + head) * 2;
-        if (a.pass == 1) {
-            *(float4 *)po = o;
-            if (d == 0) *(float2 *)pml = make_float2(M, S);
-            return;
+    if (SHARED && a.pass == 1) {   // the row's one part
+        const int64_t row = tok * a.c.hq + head, rows = (int64_t)a.b.n_tokens * a.c.hq;
+        *(float4 *)(a.prior + row * D + d) = o;
+        if (d == 0) {
+            *((float2 *)a.prior_ml + row) = make_float2(M, S);
+            for (int x = 1; x < a.parts; ++x) *((float2 *)a.prior_ml + row + x * rows) = make_float2(-INFINITY, 0.f);
         }
-        if (join) {
-            const float2 ml = __ldcg((const float2 *)pml);
-            const float4 v = __ldcg((const float4 *)po);
-            const JoinedRow j(M, S, ml.x, ml.y);
-            o = make_float4(o.x * j.wa + v.x * j.wb, o.y * j.wa + v.y * j.wb, o.z * j.wa + v.z * j.wb, o.w * j.wa + v.w * j.wb);
-            M = j.M;
-            S = j.S;
-        }
+        return;
     }
+    if (SHARED && join) join_prior(a, tok * a.c.hq + head, D, d, o, M, S);
     const float inv = 1.f / S;
     // S = 0: nothing seen. (A NaN sum stays: it is not equal to 0.)
     const float v[4] = {S == 0.f ? 0.f : o.x * inv, S == 0.f ? 0.f : o.y * inv, S == 0.f ? 0.f : o.z * inv,

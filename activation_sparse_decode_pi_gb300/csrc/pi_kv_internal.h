@@ -58,36 +58,51 @@ struct KvAttendArgs {
     // Attention in two passes (pi_kv_attend_shared): the first leaves every row's numerators, maximum and sum, the second
     // adds them to its own.
     int pass;                  // 0: one pass alone; 1: the first, whose rows all see positions [0, length); 2: the second
-    float *prior, *prior_ml;   // [n_tokens x hq][dim], [n_tokens x hq][2]
+    float *prior, *prior_ml;   // [parts][n_tokens x hq][dim], [parts][n_tokens x hq][2]
+    int parts;                 // of a row that the first pass has split along its prefix
 };
 constexpr int KV_SHARE = 128;   // a shared prefix is a multiple of this: whole tiles of both kernels, whole pages
 
-// The split kernel (pi_kv_split.cuh) of one head dim; QN: runs of 8 rows per tile, T: 16-bit terms.
-template <int D, int QN, int T>
+// The split kernel (pi_kv_split.cuh) of one head dim; QN: runs of 8 rows per tile, T: 16-bit terms, SHARED: for a pass of
+// pi_kv_attend_shared.
+template <int D, int QN, int T, bool SHARED>
 cudaError_t split_setup();   // shared-memory opt-in
-template <int D, int QN, int T>
+template <int D, int QN, int T, bool SHARED>
 cudaError_t split_launch(const KvAttendArgs &a, const CUtensorMap &mk, const CUtensorMap &mv, int grid, cudaStream_t s);
-#define PI_KV_EXTERN(D, QN, T)                       \
-    extern template cudaError_t split_setup<D, QN, T>(); \
-    extern template cudaError_t split_launch<D, QN, T>(const KvAttendArgs &, const CUtensorMap &, const CUtensorMap &, int, cudaStream_t);
-#define PI_KV_EXTERN4(D) PI_KV_EXTERN(D, 1, 1) PI_KV_EXTERN(D, 1, 2) PI_KV_EXTERN(D, 2, 1) PI_KV_EXTERN(D, 2, 2)
-PI_KV_EXTERN4(64) PI_KV_EXTERN4(128) PI_KV_EXTERN4(256)
-#undef PI_KV_EXTERN4
-#undef PI_KV_EXTERN
+#define PI_KV_SPLIT1(WORD, D, QN, T, S)                  \
+    WORD template cudaError_t split_setup<D, QN, T, S>(); \
+    WORD template cudaError_t split_launch<D, QN, T, S>(const KvAttendArgs &, const CUtensorMap &, const CUtensorMap &, int, cudaStream_t);
+#define PI_KV_SPLIT(WORD, D, S) \
+    PI_KV_SPLIT1(WORD, D, 1, 1, S) PI_KV_SPLIT1(WORD, D, 1, 2, S) PI_KV_SPLIT1(WORD, D, 2, 1, S) PI_KV_SPLIT1(WORD, D, 2, 2, S)
+PI_KV_SPLIT(extern, 64, false) PI_KV_SPLIT(extern, 128, false) PI_KV_SPLIT(extern, 256, false)
+PI_KV_SPLIT(extern, 64, true) PI_KV_SPLIT(extern, 128, true) PI_KV_SPLIT(extern, 256, true)
 
 // The rows kernel (pi_kv_rows.cuh): QT 16-bit terms of queries and weights. items: an upper bound of the
 // call's (sequence, kv head, run of rows_per_item rows); splits: parts of each item's cache.
 constexpr int rows_per_item(int dim) { return dim == 256 ? 128 : 256; }
-template <int D, int QT>
+template <int D, int QT, bool SHARED>
 cudaError_t rows_setup();
-template <int D, int QT>
+template <int D, int QT, bool SHARED>
 cudaError_t rows_launch(const KvAttendArgs &a, const CUtensorMap &mk, const CUtensorMap &mv, unsigned items,
                         unsigned splits, cudaStream_t s);
-#define PI_KV_EXTERN(D, QT)                        \
-    extern template cudaError_t rows_setup<D, QT>(); \
-    extern template cudaError_t rows_launch<D, QT>(const KvAttendArgs &, const CUtensorMap &, const CUtensorMap &, unsigned, unsigned, cudaStream_t);
-PI_KV_EXTERN(64, 1) PI_KV_EXTERN(64, 2) PI_KV_EXTERN(128, 1)
-PI_KV_EXTERN(128, 2) PI_KV_EXTERN(256, 1) PI_KV_EXTERN(256, 2)
+#define PI_KV_ROWS1(WORD, D, QT, S)                  \
+    WORD template cudaError_t rows_setup<D, QT, S>(); \
+    WORD template cudaError_t rows_launch<D, QT, S>(const KvAttendArgs &, const CUtensorMap &, const CUtensorMap &, unsigned, unsigned, cudaStream_t);
+#define PI_KV_ROWS(WORD, D, S) PI_KV_ROWS1(WORD, D, 1, S) PI_KV_ROWS1(WORD, D, 2, S)
+PI_KV_ROWS(extern, 64, false) PI_KV_ROWS(extern, 128, false) PI_KV_ROWS(extern, 256, false)
+PI_KV_ROWS(extern, 64, true) PI_KV_ROWS(extern, 128, true) PI_KV_ROWS(extern, 256, true)
+
+// The kernel of few rows behind a shared prefix (pi_kv_short.cuh): head dims 64 and 128, T 16-bit terms. part, part_ml and
+// tickets: [2 * grid][8][dim], [2 * grid][8][2] and [grid] for a grid of SHORT_CTAS * nsm at most.
+constexpr int SHORT_CTAS = 3;
+template <int D, int T>
+cudaError_t short_setup();
+template <int D, int T>
+cudaError_t short_launch(const KvAttendArgs &a, int nsm, cudaStream_t s);
+#define PI_KV_EXTERN(D, T)                           \
+    extern template cudaError_t short_setup<D, T>(); \
+    extern template cudaError_t short_launch<D, T>(const KvAttendArgs &, int, cudaStream_t);
+PI_KV_EXTERN(64, 1) PI_KV_EXTERN(64, 2) PI_KV_EXTERN(128, 1) PI_KV_EXTERN(128, 2)
 #undef PI_KV_EXTERN
 
 cudaError_t launch_kv_append(const KvView &c, const KvBatch &b, const KvLayerDev &l, const void *k_new,

@@ -161,7 +161,8 @@ constexpr int rows_smem()
     return n;
 }
 
-template <int D, int QT>
+// SHARED: a pass of pi_kv_attend_shared (a.pass), else one pass alone
+template <int D, int QT, bool SHARED>
 __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_constant__ KvAttendArgs a,
                                                                     const __grid_constant__ CUtensorMap mk,
                                                                     const __grid_constant__ CUtensorMap mv)
@@ -205,7 +206,7 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
             const int i = b0 + tid;
             int cnt = 0, rts = 0;
             if (i < a.b.n) {
-                const KvSeq q = kv_sequence(c, a.b, i, blockIdx.x == 0 && blockIdx.y == 0);
+                const KvSeq q = kv_sequence<SHARED>(c, a.b, i, blockIdx.x == 0 && blockIdx.y == 0);
                 const long long rows = (long long)q.n * G;
                 rts = rows >= a.rows_from ? (int)((rows + C::ROWS - 1) / C::ROWS) : 0;
                 cnt = rts * c.hkv;
@@ -228,7 +229,7 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
                 s_item[0] = i;
                 s_item[1] = rts - 1 - local / c.hkv;
                 s_item[2] = local % c.hkv;
-                sh.seq = kv_sequence(c, a.b, i, false);
+                sh.seq = kv_sequence<SHARED>(c, a.b, i, false);
             }
             __syncthreads();
         }
@@ -236,11 +237,12 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
     if (s_item[0] < 0) return;
     const KvSeq sq = sh.seq;
     const int h = s_item[2], row0 = s_item[1] * C::ROWS, rows = min(C::ROWS, sq.n * G - row0), p0 = sq.len - sq.n;
-    const bool flat = a.pass == 1;   // every row sees the whole length
+    const bool flat = SHARED && a.pass == 1;   // every row sees the whole length
     const int pos_lo = flat ? sq.len - 1 : p0 + row0 / G, pos_hi = flat ? sq.len - 1 : p0 + (row0 + rows - 1) / G;
-    const bool join = a.pass == 2 && sq.skip > 0;
+    const bool join = SHARED && a.pass == 2 && sq.skip > 0;
+    const int64_t all_rows = (int64_t)a.b.n_tokens * c.hq;
     // tiles [0, ns) and [w0, w1) hold what the rows see; this CTA takes its split's share of them
-    const int w0 = max(sq.skip, pos_lo - a.window + 1) / TOK, w1 = pos_hi < 0 ? w0 : pos_hi / TOK + 1;
+    const int w0 = max(SHARED ? sq.skip : 0, pos_lo - a.window + 1) / TOK, w1 = pos_hi < 0 ? w0 : pos_hi / TOK + 1;
     const int ns = pos_hi >= 0 ? min((a.sinks + TOK - 1) / TOK, w0) : 0;
     const int nt_all = ns + max(w1 - w0, 0), splits = gridDim.y;
     const int k0 = (int)((long long)nt_all * blockIdx.y / splits), k1 = (int)((long long)nt_all * (blockIdx.y + 1) / splits);
@@ -681,20 +683,9 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
         bar_sync(2 + grp, 256);
         l += s_half[half ^ 1][row];
         // (the unit, which may be as small as an append's 2^-120, is multiplied in by itself: its quotient would lose bits)
-        const float back = exp2i(-(int)ROWS_UNIT), norm = splits > 1 || a.pass == 1 ? back : l == 0.f ? 0.f : back / l;
-        // of a row that another pass has begun: its sums join this one's here (a split item's where its parts are added)
+        const float back = exp2i(-(int)ROWS_UNIT), norm = splits > 1 || flat || join ? back : l == 0.f ? 0.f : back / l;
         const int64_t prow = ((int64_t)sq.start + (row0 + row) / G) * c.hq + h * G + (row0 + row) % G;
-        const bool joins = join && splits == 1 && on;
-        float mine_w = norm, prior_w = 0.f, M = m, S = l;
-        if (joins) {
-            const float2 ml = __ldcg((const float2 *)(a.prior_ml + prow * 2));
-            const JoinedRow j(m, l, ml.x, ml.y);
-            const float inv = j.S == 0.f ? 0.f : 1.f / j.S;
-            mine_w = j.wa * inv * back;
-            prior_w = j.wb * inv;
-            M = j.M;
-            S = j.S;
-        }
+        float M = m, S = l;
         const int64_t at = ((int64_t)blockIdx.x * splits + blockIdx.y) * C::ROWS + row;
         const int64_t at_out = ((int64_t)sq.start + (row0 + row) / G) * a.ldo + (int64_t)(h * G + (row0 + row) % G) * D;
 #pragma unroll 1
@@ -707,25 +698,26 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
             if (on) {
                 float f[32];   // l = 0: nothing seen (a NaN sum stays: it is not equal to 0)
 #pragma unroll
-                for (int e = 0; e < 32; ++e) f[e] = nt == 0 || l == 0.f ? 0.f : __uint_as_float(o[e]) * mine_w * unit;
-                if (joins) {
+                for (int e = 0; e < 32; ++e) f[e] = nt == 0 || l == 0.f ? 0.f : __uint_as_float(o[e]) * norm * unit;
+                if (join && splits == 1) {   // (a split item's where its parts are added)
 #pragma unroll
                     for (int e = 0; e < 32; e += 4) {
-                        const float4 v = __ldcg((const float4 *)(a.prior + prow * D + x + e));
-                        f[e] += v.x * prior_w, f[e + 1] += v.y * prior_w, f[e + 2] += v.z * prior_w, f[e + 3] += v.w * prior_w;
+                        float4 v = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
+                        M = m, S = l;
+                        join_prior(a, prow, D, x + e, v, M, S);
+                        const float inv = S == 0.f ? 0.f : 1.f / S;
+                        f[e] = v.x * inv, f[e + 1] = v.y * inv, f[e + 2] = v.z * inv, f[e + 3] = v.w * inv;
                     }
                 }
-                if (splits > 1) store_f32<32>(a.rows_part + at * D + x, f);
-                else if (a.pass == 1) store_f32<32>(a.prior + prow * D + x, f);
+                if (flat) store_f32<32>(a.prior + (prow + blockIdx.y * all_rows) * D + x, f);
+                else if (splits > 1) store_f32<32>(a.rows_part + at * D + x, f);
                 else store_out<32>(a, at_out + x, f);
             }
             __syncwarp();   // the next load of tensor memory takes the whole warp, lanes past the last row too
         }
-        if (splits == 1 && on && half == 0) {
-            if (a.pass == 1) *(float2 *)(a.prior_ml + prow * 2) = make_float2(m, l);
-            else if (a.lse) a.lse[prow] = row_lse(M, S);
-        }
-        if (splits > 1 && on && half == 0) {
+        if (flat && on && half == 0) *((float2 *)a.prior_ml + prow + blockIdx.y * all_rows) = make_float2(m, l);
+        else if (splits == 1 && on && half == 0 && a.lse) a.lse[prow] = row_lse(M, S);
+        if (splits > 1 && !flat && on && half == 0) {
             a.rows_ml[at * 2] = m;
             a.rows_ml[at * 2 + 1] = l;
         }
@@ -737,6 +729,7 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
         tmem_dealloc(tmem, C::TCOLS);
     }
     const int4 f4 = make_int4(sq.row, sq.len, sq.start, sq.n);
+    if (flat) return;   // every part is the second pass's (and every row sees all of its positions, NaN too)
     if (splits > 1) {
         if (tid == 0) {   // bit 16 of the ticket: a part met a NaN value
             const uint32_t before = ticket_acq_rel(&a.rows_tickets[blockIdx.x], s_nan ? 0x10001u : 1u);
@@ -759,7 +752,7 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
                 S += w * ly;
                 o.x += v.x * w, o.y += v.y * w, o.z += v.z * w, o.w += v.w * w;
             }
-            store_row(a, f4, h, G, D, row0 + r, d, o, M, S, join);
+            store_row<SHARED>(a, f4, h, G, D, row0 + r, d, o, M, S, join);
         }
         if (tid == 0) a.rows_tickets[blockIdx.x] = 0;
     }
@@ -786,13 +779,13 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
     }
 }
 
-template <int D, int QT>
+template <int D, int QT, bool SHARED>
 cudaError_t rows_setup()
 {
-    return cudaFuncSetAttribute(k_kv_rows<D, QT>, cudaFuncAttributeMaxDynamicSharedMemorySize, rows_smem<D, QT>());
+    return cudaFuncSetAttribute(k_kv_rows<D, QT, SHARED>, cudaFuncAttributeMaxDynamicSharedMemorySize, rows_smem<D, QT>());
 }
 
-template <int D, int QT>
+template <int D, int QT, bool SHARED>
 cudaError_t rows_launch(const KvAttendArgs &a, const CUtensorMap &mk, const CUtensorMap &mv, unsigned items,
                         unsigned splits, cudaStream_t s)
 {
@@ -803,7 +796,7 @@ cudaError_t rows_launch(const KvAttendArgs &a, const CUtensorMap &mk, const CUte
     L.stream = s;
     L.pdl = true;
     L.nsm = 0;
-    return launch_ex(L, k_kv_rows<D, QT>, a, mk, mv);
+    return launch_ex(L, k_kv_rows<D, QT, SHARED>, a, mk, mv);
 }
 
 }  // namespace pi

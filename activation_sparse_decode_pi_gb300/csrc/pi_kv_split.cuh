@@ -80,7 +80,8 @@ struct Seg {
     __device__ __forceinline__ long long after() const { return first + k1; }
 };
 
-template <int D, int QN, int T>
+// SHARED: a pass of pi_kv_attend_shared (a.pass), else one pass alone
+template <int D, int QN, int T, bool SHARED>
 __global__ void __launch_bounds__(SplitCfg<D, QN, T>::NT, 1)
     k_kv_split(const __grid_constant__ KvAttendArgs a, const __grid_constant__ CUtensorMap mk,
                const __grid_constant__ CUtensorMap mv, int slots)
@@ -124,7 +125,7 @@ __global__ void __launch_bounds__(SplitCfg<D, QN, T>::NT, 1)
     pdl_launch_dependents();
 
     // tiles of every sequence, and their running sum
-    const bool flat = a.pass == 1, second = a.pass == 2;   // flat: every row sees the whole length
+    const bool flat = SHARED && a.pass == 1, second = SHARED && a.pass == 2;   // flat: every row sees the whole length
     // of sequence i with L positions, nq of them new: tiles [0, ns) and [w0, ...) are read
     auto view = [&](int i, int L, int nq, int &w0, int &ns, int &nt) {
         w0 = max(second ? skips[i] : 0, L - nq - a.window + 1) / KV_TILE;
@@ -137,7 +138,7 @@ __global__ void __launch_bounds__(SplitCfg<D, QN, T>::NT, 1)
         const int i = base + tid;
         long long w = 0;
         if (i < a.b.n) {
-            KvSeq q = kv_sequence(c, a.b, i, blockIdx.x == 0);
+            KvSeq q = kv_sequence<SHARED>(c, a.b, i, blockIdx.x == 0);
             if ((long long)q.n * G >= a.rows_from) q.n = 0;   // the rows kernel's
             info[i] = make_int4(q.row, q.len, q.start, q.n);
             if (second) skips[i] = q.skip;
@@ -371,7 +372,7 @@ __global__ void __launch_bounds__(SplitCfg<D, QN, T>::NT, 1)
                     a.part_ml[((size_t)part * R + r) * 2 + 1] = S;
                 }
             } else {
-                store_row(a, f, sg.h, G, D, row0 + r, d, o, M, S, prior);
+                store_row<SHARED>(a, f, sg.h, G, D, row0 + r, d, o, M, S, prior);
             }
         }
         if (!cut) return;
@@ -415,7 +416,7 @@ __global__ void __launch_bounds__(SplitCfg<D, QN, T>::NT, 1)
                 const float w = wt[y * R + r];
                 o.x += v.x * w, o.y += v.y * w, o.z += v.z * w, o.w += v.w * w;
             }
-            store_row(a, f, sg.h, G, D, row0 + r, d, o, sums[r * 2], sums[r * 2 + 1], prior);
+            store_row<SHARED>(a, f, sg.h, G, D, row0 + r, d, o, sums[r * 2], sums[r * 2 + 1], prior);
         }
         if (me == 0) a.tickets[ca] = 0;
         sync();
@@ -897,13 +898,13 @@ SplitPlan split_plan(int n, bool second)
     return p;
 }
 
-template <int D, int QN, int T>
+template <int D, int QN, int T, bool SHARED>
 cudaError_t split_setup()
 {
-    return cudaFuncSetAttribute(k_kv_split<D, QN, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024 - 256);
+    return cudaFuncSetAttribute(k_kv_split<D, QN, T, SHARED>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024 - 256);
 }
 
-template <int D, int QN, int T>
+template <int D, int QN, int T, bool SHARED>
 cudaError_t split_launch(const KvAttendArgs &a, const CUtensorMap &mk, const CUtensorMap &mv, int grid, cudaStream_t s)
 {
     const SplitPlan p = split_plan<D, QN, T>(a.b.n, a.pass == 2);
@@ -914,7 +915,7 @@ cudaError_t split_launch(const KvAttendArgs &a, const CUtensorMap &mk, const CUt
     L.stream = s;
     L.pdl = true;
     L.nsm = grid;
-    return launch_ex(L, k_kv_split<D, QN, T>, a, mk, mv, p.slots);
+    return launch_ex(L, k_kv_split<D, QN, T, SHARED>, a, mk, mv, p.slots);
 }
 
 }  // namespace pi

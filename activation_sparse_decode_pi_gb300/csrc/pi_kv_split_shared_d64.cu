@@ -1,0 +1,7 @@
+// pi_kv_split_shared_d64.cu -- split attention kernels, for a pass over or behind shared prefixes, head dim 64 (template in
+// pi_kv_split.cuh).
+#include "pi_kv_split.cuh"
+
+namespace pi {
+PI_KV_SPLIT(, 64, true)
+}  // namespace pi

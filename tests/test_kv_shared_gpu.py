@@ -215,6 +215,35 @@ def test_rows_past_the_last_sequence_and_strided_outputs(P):
     assert torch.allclose(wide[:5, :512].unflatten(1, (4, 128)), want, rtol=0, atol=2.2e-5 * 24)
 
 
+@pytest.mark.parametrize("dim,page", [(64, 16), (128, 64)])
+def test_queries_before_the_first_position(P, dim, page):
+    """More new tokens than positions, beside a group that shares: what sees nothing gives 0 and -infinity."""
+    b = Shared(P, hq=4, hkv=2, dim=dim, page=page, n_pages=60, max_pages=20)
+    b.grow([0, 3], [300, 2])
+    b.fork([0], [1])
+    b.grow([0, 1], [3, 2])
+    seqs, new = [0, 1, 3, 5], [1, 2, 5, 3]                                      # 3 of sequence 3's, all of 5's see nothing
+    args = b.args(seqs, new)
+    q, qn = b.tokens(new, "f32", 4, spread=0)
+    lse = torch.full(q.shape[:2], 9.0, device="cuda")
+    out = b.cache.attend_shared(0, *args, b.cache.share(*args, dev([0, 2])), q, lse=lse, scale=0.1)
+    want, want_lse = b.plain.attend(0, seqs, new, qn, 0.1)
+    nothing = np.isneginf(want_lse)
+    assert nothing.sum() == 6 * 4 and np.array_equal(np.isneginf(lse.cpu().numpy()), nothing)
+    assert not out.cpu().numpy()[nothing].any() and b.cache.status() == 0
+    assert np.allclose(out.double().cpu().numpy(), want, rtol=0, atol=1.1e-5 * 24)     # (A is below 24 here)
+
+
+def test_one_long_sequence_among_short_ones(P):
+    """Shares that cut an item over many CTAs, with and without a prefix."""
+    b = Shared(P, hq=8, hkv=2, dim=128, page=32, n_pages=500, max_seqs=12, max_pages=400)
+    b.grow([0], [260])
+    b.fork([0] * 5, [1, 2, 3, 4, 5])
+    b.grow([0, 1, 2, 3, 4, 5, 7], [3, 9000, 70, 1, 200, 64, 2500])
+    for kind in ("f32", "bf16"):
+        b.check([0, 1, 2, 3, 4, 5, 7], [1, 1, 1, 1, 3, 1, 2], [0, 6], kind, [256])
+
+
 @pytest.mark.parametrize("rows", [1, 40])
 def test_nan_in_the_prefix_reaches_all_and_behind_it_one(P, rows):
     b = Shared(P, hq=2, hkv=1, dim=64, page=16, n_pages=80, max_pages=40)
@@ -273,7 +302,8 @@ def test_groups_out_of_order_share_nothing(P, groups):
     n = len(groups) - 1
     assert (plan[2 * n + 1:3 * n + 5] == 0).all()
     q = torch.randn(4, 2, 64, device="cuda")
-    assert torch.equal(b.cache.attend_shared(0, *args, plan, q), b.cache.attend(0, *args, q)) and b.cache.status() == 0
+    got, want = b.cache.attend_shared(0, *args, plan, q), b.cache.attend(0, *args, q)
+    assert torch.allclose(got, want, rtol=0, atol=2.2e-5 * 24) and b.cache.status() == 0     # (as above)
 
 
 def test_refusals(P):
