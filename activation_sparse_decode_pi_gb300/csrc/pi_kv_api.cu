@@ -21,7 +21,7 @@ using namespace pi;
 struct pi_kv {
     pi_kv_desc_t desc;
     std::vector<KvLayerDev> layers;
-    std::vector<CUtensorMap> map_k, map_v;
+    std::vector<CUtensorMap> map_k, map_v, box_k, box_v;   // of 64-position tiles; of 16 rows
     KvView view;
     int dev = 0, nsm = 0;
     void *ws = nullptr;
@@ -77,14 +77,14 @@ pi_status_t validate(const pi_kv_desc_t *d)
     return PI_OK;
 }
 
-// Pool of one layer as rows of head_dim bytes; boxes of one 64-position tile's share of a page and
+// Pool of one layer as rows of head_dim bytes; boxes of one 64-position tile's share of a page (or of `rows` of it) and
 // 128 bytes (64 for head_dim 64), swizzled so that the kernels' reads spread over the banks.
-bool encode_pool(EncodeFn fn, CUtensorMap *m, const pi_kv_desc_t &d, void *base)
+bool encode_pool(EncodeFn fn, CUtensorMap *m, const pi_kv_desc_t &d, void *base, int rows = KV_TILE)
 {
     const cuuint64_t dims[2] = {(cuuint64_t)d.head_dim, (cuuint64_t)d.n_pages * d.n_kv_heads * d.page_tokens};
     const cuuint64_t strides[1] = {(cuuint64_t)d.head_dim};
     const cuuint32_t box[2] = {(cuuint32_t)(d.head_dim < 128 ? d.head_dim : 128),
-                               (cuuint32_t)(d.page_tokens < KV_TILE ? d.page_tokens : KV_TILE)};
+                               (cuuint32_t)std::min(d.page_tokens, rows)};
     const cuuint32_t one[2] = {1, 1};
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
               d.head_dim < 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
@@ -126,7 +126,8 @@ cudaError_t attend_of(const pi_kv *h, int layer, KvAttendArgs a, cudaStream_t s)
             b.part = h->short_part;
             b.part_ml = h->short_ml;
             b.tickets = h->short_tickets;
-            e = a.dtype == PI_BF16 ? short_launch<D, 1>(b, h->nsm, s) : short_launch<D, 2>(b, h->nsm, s);
+            const CUtensorMap &bk = h->box_k[layer], &bv = h->box_v[layer];
+            e = a.dtype == PI_BF16 ? short_launch<D, 1>(b, bk, bv, h->nsm, s) : short_launch<D, 2>(b, bk, bv, h->nsm, s);
             done = true;
         }
     if (few && !done) {
@@ -191,9 +192,12 @@ pi_status_t kv_create(pi_kv_t **out, const pi_kv_desc_t *desc, const pi_kv_layer
     h->nsm = nsm;
     h->map_k.resize(d.n_layers);
     h->map_v.resize(d.n_layers);
+    h->box_k.resize(d.n_layers);
+    h->box_v.resize(d.n_layers);
     for (int l = 0; l < d.n_layers; ++l) {
         h->layers.push_back({(uint8_t *)layers[l].k, (uint8_t *)layers[l].v, layers[l].k_scale, layers[l].v_scale});
-        if (!encode_pool(enc, &h->map_k[l], d, layers[l].k) || !encode_pool(enc, &h->map_v[l], d, layers[l].v))
+        if (!encode_pool(enc, &h->map_k[l], d, layers[l].k) || !encode_pool(enc, &h->map_v[l], d, layers[l].v) ||
+            !encode_pool(enc, &h->box_k[l], d, layers[l].k, 16) || !encode_pool(enc, &h->box_v[l], d, layers[l].v, 16))
             return PI_ERR_CUDA;
     }
     if ((s = cuda_status(d.head_dim == 64    ? setup_of<64>()

@@ -92,16 +92,17 @@ cudaError_t rows_launch(const KvAttendArgs &a, const CUtensorMap &mk, const CUte
 PI_KV_ROWS(extern, 64, false) PI_KV_ROWS(extern, 128, false) PI_KV_ROWS(extern, 256, false)
 PI_KV_ROWS(extern, 64, true) PI_KV_ROWS(extern, 128, true) PI_KV_ROWS(extern, 256, true)
 
-// The kernel of few rows behind a shared prefix (pi_kv_short.cuh): head dims 64 and 128, T 16-bit terms. part, part_ml and
+// The kernel of few rows behind a shared prefix (pi_kv_short.cuh): head dims 64 and 128, T 16-bit terms, maps of 16-row
+// boxes. part, part_ml and
 // tickets: [2 * grid][8][dim], [2 * grid][8][2] and [grid] for a grid of SHORT_CTAS * nsm at most.
 constexpr int SHORT_CTAS = 3;
 template <int D, int T>
 cudaError_t short_setup();
 template <int D, int T>
-cudaError_t short_launch(const KvAttendArgs &a, int nsm, cudaStream_t s);
+cudaError_t short_launch(const KvAttendArgs &a, const CUtensorMap &mk, const CUtensorMap &mv, int nsm, cudaStream_t s);
 #define PI_KV_EXTERN(D, T)                           \
     extern template cudaError_t short_setup<D, T>(); \
-    extern template cudaError_t short_launch<D, T>(const KvAttendArgs &, int, cudaStream_t);
+    extern template cudaError_t short_launch<D, T>(const KvAttendArgs &, const CUtensorMap &, const CUtensorMap &, int, cudaStream_t);
 PI_KV_EXTERN(64, 1) PI_KV_EXTERN(64, 2) PI_KV_EXTERN(128, 1) PI_KV_EXTERN(128, 2)
 #undef PI_KV_EXTERN
 

@@ -3,11 +3,12 @@
 // The second pass of pi_kv_attend_shared: for each sequence and kv head a tile of up to 8 rows (query token and head of the
 // group) and the positions behind the prefix, often some hundred, then the join with what the first pass left of the rows.
 // There are many such items and little in each, so what counts is how many are under way and what one costs from end to
-// end: a CTA has four warps and no shared tiles, three (fp32, fp16: two) of them to an SM. A warp takes 16 of a tile's 64
-// positions, loads their codes from memory straight into the fragments' registers, the next tile's under this one's work,
-// and keeps its own maximum, sum and numerators; the products are pi_kv_split.cuh's (the cache as the 16-row operand on
-// mma.sync m16n8k16, codes to f16 two at a time, queries in terms), and so are their units and rounding. The items are laid
-// end to end and cut into equal shares; an item cut over CTAs is joined by the last of them, in the order of its parts.
+// end: a CTA has four warps that share nothing until an item's end, three CTAs to an SM. A warp takes 16 of a tile's 64
+// positions: it asks for their codes by TMA, four tiles ahead, into boxes of its own, and keeps its own maximum, sum and
+// numerators; the products are pi_kv_split.cuh's (the cache as the 16-row operand on mma.sync m16n8k16, codes to f16 two
+// at a time, queries in terms), and so are their units and rounding. The items are laid end to end and cut into equal
+// shares. An item of up to two shares belongs to the CTA with its first step; a longer one is cut over CTAs and joined by
+// the last of them, in the order of its parts.
 #pragma once
 
 #include "pi_kv_device.cuh"
@@ -19,27 +20,47 @@ constexpr int SHORT_ITEM = 4;   // what an item costs besides its tiles, in tile
 
 template <int D, int T>
 struct ShortCfg {
-    static constexpr int NW = 4, NT = NW * 32, R = 8, CTAS = T == 1 ? 3 : 2;
-    static constexpr int SMEM = NW * R * (D + 4) * 4 + (NW + 1) * R * 8;   // the warps' results; and 28 bytes a sequence
+    static constexpr int NW = 4, NT = NW * 32, R = 8, CTAS = SHORT_CTAS;
+    static constexpr int SLOTS = 4, BOX = 16 * D;   // places of a warp for 16 positions' keys and values; bytes of either
+    static constexpr int RING = NW * SLOTS * 2 * BOX;
+    static_assert(RING >= NW * R * (D + 4) * 4, "the warps' results take the boxes' place");
+    static constexpr int SMEM = RING + (NW + 1) * R * 8 + NW * SLOTS * 8;   // and 28 bytes a sequence
 };
 
 template <int D, int T>
-__global__ void __launch_bounds__(ShortCfg<D, T>::NT, ShortCfg<D, T>::CTAS) k_kv_short(const __grid_constant__ KvAttendArgs a)
+__global__ void __launch_bounds__(ShortCfg<D, T>::NT, ShortCfg<D, T>::CTAS)
+    k_kv_short(const __grid_constant__ KvAttendArgs a, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv)
 {
     using C = ShortCfg<D, T>;
     constexpr int NW = C::NW, NT = C::NT, R = C::R, NJ = D / 16, NCH = D / 64;
-    extern __shared__ __align__(16) uint8_t smem[];
-    float *const merge = (float *)smem, *const ml = merge + NW * R * (D + 4), *const sums = ml + NW * R * 2;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *const smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+    float *const merge = (float *)smem, *const ml = (float *)(smem + C::RING), *const sums = ml + NW * R * 2;
     int4 *const info = (int4 *)(smem + C::SMEM);                                  // [n] row, length, start, new tokens
     long long *const prefix = (long long *)(info + a.b.n);                        // [n + 1] steps before sequence i
     int *const skips = (int *)(prefix + a.b.n + 1);                               // [n]
     __shared__ long long wtot[NW];
     __shared__ int s_last;
+    __shared__ float s_pw[R][16], s_pm[R], s_ps[R];   // weights of what the first pass left of a row; its maximum and sum
+    static_assert(NT == R * 16, "a thread to a row's part");
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
     const KvView &c = a.c;
     const int G = c.hq / c.hkv, P = c.page;
+    uint8_t *const ring = smem + warp * C::SLOTS * 2 * C::BOX;
+    uint64_t *const full = (uint64_t *)(sums + R * 2) + warp * C::SLOTS;
+    if (lane == 0) {
+        for (int x = 0; x < C::SLOTS; ++x) mbar_init(&full[x], 1);
+        fence_mbar_init();
+    }
+    __syncwarp();
+    if (tid == 0) {
+        prefetch_tensormap(&mk);
+        prefetch_tensormap(&mv);
+    }
     pdl_wait();
     pdl_launch_dependents();
+    uint32_t asked = 0, taken = 0;   // boxes of the warp
+    bool dead = false;
     long long run = 0;
     for (int base = 0; base < a.b.n; base += NT) {
         const int i = base + tid;
@@ -87,9 +108,17 @@ __global__ void __launch_bounds__(ShortCfg<D, T>::NT, ShortCfg<D, T>::CTAS) k_kv
         const long long local = t - prefix[i], item = local / (nt + SHORT_ITEM);
         const int rts = (int)(((long long)nq * G + R - 1) / R), h = (int)(item / rts), row0 = (int)(item % rts) * R;
         const long long first = prefix[i] + item * (nt + SHORT_ITEM) + SHORT_ITEM;   // step of the item's first tile
-        const int k0 = (int)max(t - first, 0ll), k1 = (int)min((long long)nt, max(t1 - first, 0ll));
-        t = first + nt < t1 ? first + nt : t1;
-        if (k0 >= k1 && !(nt == 0 && k0 == 0)) continue;   // (the share ends before the item's first tile)
+        const bool whole_item = nt + SHORT_ITEM <= 2 * quota;
+        int k0 = 0, k1 = nt;
+        if (whole_item) {
+            t = first + nt;
+            if (first - SHORT_ITEM < t0) continue;   // the CTA's before
+        } else {
+            k0 = (int)max(t - first, 0ll);
+            k1 = (int)min((long long)nt, max(t1 - first, 0ll));
+            t = first + nt < t1 ? first + nt : t1;
+            if (k0 >= k1) continue;   // (the share ends before the item's first tile)
+        }
         const int p0 = L - nq, rows = min(R, nq * G - row0);
         const int pos_lo = p0 + row0 / G, pos_hi = p0 + (row0 + rows - 1) / G;
 
@@ -161,54 +190,113 @@ __global__ void __launch_bounds__(ShortCfg<D, T>::NT, ShortCfg<D, T>::CTAS) k_kv
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
 
-        uint4 kn[NCH][2], vn[2][2];   // the next tile's codes: keys of rows g and g + 8, values of tokens 2 q + e (+ 8)
-        int n_pid;
-        float n_ks, n_vs;
-        auto fetch = [&](int k, int kb) {   // tile k; kb: the first of the 32 looked up
-            n_pid = __shfl_sync(0xffffffffu, pid, k - kb);
-            n_ks = __shfl_sync(0xffffffffu, ks, k - kb);
-            n_vs = __shfl_sync(0xffffffffu, vs, k - kb);
-            if (n_pid < 0) return;   // (absent, or no row sees any of it)
-            const int at = (tile0 + k) * KV_TILE + warp * 16;
-            const size_t row = ((size_t)n_pid * c.hkv + h) * P + (at & (P - 1));
-            const uint8_t *kp = a.l.k + row * D, *vp = a.l.v + row * D;
+        // What the first pass has left of this thread's outputs, under the first tiles' way.
+        constexpr int PER = R * (D / 4) / NT;   // float4 of outputs to a thread
+        const bool cut = k0 > 0 || k1 < nt, join = skips[i] > 0;
+        float4 prior[PER];
+        // A box's codes into a place: the next tile that is there, in order. kb: the first of the 32 looked up.
+        int kb = k0, ka_next = k0;
+        auto ask = [&]() {   // by the whole warp
+            while (ka_next < k1) {
+                if (ka_next - kb >= 32) return;   // (after the tiles that are looked up now)
+                const int page = __shfl_sync(0xffffffffu, pid, ka_next - kb), at = (tile0 + ka_next) * KV_TILE + warp * 16;
+                ++ka_next;
+                if (page < 0) continue;   // absent, or no row sees any of it
+                const int slot = asked % C::SLOTS;
+                if (lane == 0) {
+                    const int row = (page * c.hkv + h) * P + (at & (P - 1));
+                    mbar_arrive_expect_tx(&full[slot], 2 * C::BOX);
+                    tma_load_2d(ring + slot * 2 * C::BOX, &mk, 0, row, &full[slot]);
+                    tma_load_2d(ring + slot * 2 * C::BOX + C::BOX, &mv, 0, row, &full[slot]);
+                }
+                ++asked;
+                return;
+            }
+        };
+        if (!dead)
+            for (int x = 0; x < C::SLOTS; ++x) ask();
+        // The first pass's parts of the item's rows, joined: their weights, a part to a thread, then the numerators of this
+        // thread's outputs.
+        auto prior_rows = [&]() {
+            const int64_t all = (int64_t)a.b.n_tokens * c.hq;
+            auto row_of = [&](int r) { return ((int64_t)f.z + (row0 + r) / G) * c.hq + h * G + (row0 + r) % G; };
+            {
+                const int r = tid / 16, x = tid % 16;
+                float2 p = make_float2(-INFINITY, 0.f);
+                if (r < rows && x < a.parts) p = __ldcg((const float2 *)a.prior_ml + row_of(r) + x * all);
+                float M = p.x;
+#pragma unroll
+                for (int o = 8; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+                const float w = part_weight(p.x, p.y, M);
+                float S = w * p.y;
+#pragma unroll
+                for (int o = 8; o > 0; o >>= 1) S += __shfl_xor_sync(0xffffffffu, S, o);
+                s_pw[r][x] = w;
+                if (x == 0) s_pm[r] = M, s_ps[r] = S;
+            }
+            __syncthreads();
+#pragma unroll
+            for (int y = 0; y < PER; ++y) {
+                const int x = tid + y * NT, r = min(x / (D / 4), rows - 1), d = (x % (D / 4)) * 4;
+                const float *const num = a.prior + row_of(r) * D + d;
+                float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+                for (int z = 0; z < a.parts; ++z) {
+                    const float4 v = __ldcg((const float4 *)(num + z * all * D));
+                    const float w = s_pw[r][z];
+                    if (w != 0.f) o.x += v.x * w, o.y += v.y * w, o.z += v.z * w, o.w += v.w * w;   // (an empty part has none)
+                }
+                prior[y] = o;
+            }
+        };
+        auto add_prior = [&](int y, int r, float4 &o, float &M, float &S) {
+            const float top = fmaxf(M, s_pm[r]), w0 = part_weight(M, S, top), w1 = part_weight(s_pm[r], s_ps[r], top);
+            o = make_float4(o.x * w0 + prior[y].x * w1, o.y * w0 + prior[y].y * w1, o.z * w0 + prior[y].z * w1,
+                            o.w * w0 + prior[y].w * w1);
+            S = S * w0 + s_ps[r] * w1;
+            M = top;
+        };
+        if (join && !cut) prior_rows();
+        for (int k = k0; k < k1; ++k) {
+            if (k - kb == 32) {
+                kb = k;
+                look_up(kb);
+                look_up_scales();
+                if (!dead)
+                    while (asked - taken < (uint32_t)C::SLOTS && ka_next < k1 && ka_next - kb < 32) ask();
+            }
+            const int page = __shfl_sync(0xffffffffu, pid, k - kb), j0 = (tile0 + k) * KV_TILE + warp * 16;
+            const float sk = __shfl_sync(0xffffffffu, ks, k - kb), sv = __shfl_sync(0xffffffffu, vs, k - kb);
+            if (page < 0 || dead) continue;
+            const int slot = taken % C::SLOTS;
+            if (!warp_wait(&full[slot], taken / C::SLOTS & 1)) {
+                dead = true;
+                set_status(c.status, ST_TIMEOUT);
+                continue;
+            }
+            ++taken;
+            const uint8_t *const kt = ring + slot * 2 * C::BOX, *const vt = kt + C::BOX;
+            uint4 kc[NCH][2], vc[2][2];   // keys of rows g and g + 8, values of tokens 2 q + e (+ 8)
 #pragma unroll
             for (int ch = 0; ch < NCH; ++ch)
 #pragma unroll
                 for (int x = 0; x < 2; ++x)
-                    kn[ch][x] = ld_stream((const uint4 *)(kp + (x * 8 + g) * D + (D == 64 ? q * 16 : (2 * q + ch) * 16)));
+                    kc[ch][x] = *(const uint4 *)(kt + (D == 64 ? (x * 8 + g) * 64 + ((q ^ ((g >> 1) & 3)) << 4)
+                                                               : (x * 8 + g) * 128 + (((2 * q + ch) ^ g) << 4)));
 #pragma unroll
             for (int x = 0; x < 2; ++x)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const uint8_t *p = vp + (x * 8 + 2 * q + e) * D;
                     if constexpr (D == 64) {
-                        const uint2 v = *(const uint2 *)(p + g * 8);
-                        vn[x][e] = make_uint4(v.x, v.y, 0, 0);
+                        const uint2 v = *(const uint2 *)(vt + (x * 8 + 2 * q + e) * 64 + (((g >> 1) ^ q) << 4) + (g & 1) * 8);
+                        vc[x][e] = make_uint4(v.x, v.y, 0, 0);
                     } else {
-                        vn[x][e] = ld_stream((const uint4 *)(p + g * 16));
+                        vc[x][e] = *(const uint4 *)(vt + (x * 8 + 2 * q + e) * 128 + ((g ^ (2 * q + e)) << 4));
                     }
                 }
-        };
-        int kb = k0;
-        if (k0 < k1) fetch(k0, kb);
-        for (int k = k0; k < k1; ++k) {
-            const int page = n_pid, j0 = (tile0 + k) * KV_TILE + warp * 16;
-            const float sk = n_ks, sv = n_vs;
-            uint4 kc[NCH][2], vc[2][2];
-#pragma unroll
-            for (int ch = 0; ch < NCH; ++ch) kc[ch][0] = kn[ch][0], kc[ch][1] = kn[ch][1];
-#pragma unroll
-            for (int x = 0; x < 2; ++x) vc[x][0] = vn[x][0], vc[x][1] = vn[x][1];
-            if (k + 1 < k1) {
-                if (k + 1 - kb == 32) {
-                    kb = k + 1;
-                    look_up(kb);
-                    look_up_scales();
-                }
-                fetch(k + 1, kb);
-            }
-            if (page < 0) continue;
+            fence_proxy_async_smem();   // the next copy into the place comes after these loads
+            __syncwarp();
+            ask();
             // ---- scores: s[2 x + e] of position 8 x + g and row 2 q + e
             float s[4] = {0.f, 0.f, 0.f, 0.f}, s2[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -331,6 +419,7 @@ __global__ void __launch_bounds__(ShortCfg<D, T>::NT, ShortCfg<D, T>::CTAS) k_kv
                 }
         }
         // ---------------------------------------------------------------- the warps' results, joined
+        __syncthreads();   // all boxes have been read: the results take their place
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int r = 2 * q + e;
@@ -346,7 +435,6 @@ __global__ void __launch_bounds__(ShortCfg<D, T>::NT, ShortCfg<D, T>::CTAS) k_kv
                     make_float2(acc[j][e] * 0x1p-14f * unit, acc[j][2 + e] * 0x1p-14f * unit);
         }
         __syncthreads();
-        const bool cut = k0 > 0 || k1 < nt, join = skips[i] > 0;
         const int ca = cut ? (int)(first / quota) : 0, cb = cut ? (int)((first + nt - 1) / quota) : 0;   // the item's CTAs
         const int part = (int)blockIdx.x == ca ? 2 * ca + 1 : 2 * (int)blockIdx.x;
         if (tid < rows) {
@@ -363,9 +451,11 @@ __global__ void __launch_bounds__(ShortCfg<D, T>::NT, ShortCfg<D, T>::CTAS) k_kv
             sums[tid * 2 + 1] = S;
         }
         __syncthreads();
-        for (int x = tid; x < rows * (D / 4); x += NT) {
-            const int r = x / (D / 4), d = (x % (D / 4)) * 4;
-            const float M = sums[r * 2], S = sums[r * 2 + 1];
+#pragma unroll
+        for (int y = 0; y < PER; ++y) {
+            const int x = tid + y * NT, r = x / (D / 4), d = (x % (D / 4)) * 4;
+            if (r >= rows) break;
+            float M = sums[r * 2], S = sums[r * 2 + 1];
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int w = 0; w < NW; ++w) {
@@ -376,54 +466,62 @@ __global__ void __launch_bounds__(ShortCfg<D, T>::NT, ShortCfg<D, T>::CTAS) k_kv
             if (cut) {
                 *(float4 *)&a.part[((size_t)part * R + r) * D + d] = o;
                 if (d == 0) *(float2 *)&a.part_ml[((size_t)part * R + r) * 2] = make_float2(M, S);
-            } else {
-                store_row<true>(a, f, h, G, D, row0 + r, d, o, M, S, join);
+                continue;
             }
+            if (join) add_prior(y, r, o, M, S);
+            store_row<true>(a, f, h, G, D, row0 + r, d, o, M, S);
         }
+        fence_proxy_async_smem();   // (the next item's boxes come after these loads)
         __syncthreads();
         if (!cut) continue;
         if (tid == 0) s_last = ticket_acq_rel(&a.tickets[ca], 1u) == (uint32_t)(cb - ca);
         __syncthreads();
         if (!s_last) continue;
         auto slot = [&](int y) { return y == ca ? 2 * ca + 1 : 2 * y; };
-        for (int x = tid; x < rows * (D / 4); x += NT) {
-            const int r = x / (D / 4), d = (x % (D / 4)) * 4;
+        if (join) prior_rows();
+#pragma unroll
+        for (int y = 0; y < PER; ++y) {
+            const int x = tid + y * NT, r = x / (D / 4), d = (x % (D / 4)) * 4;
+            if (r >= rows) break;
             float M = -INFINITY, S = 0.f;
-            for (int y = ca; y <= cb; ++y) M = fmaxf(M, __ldcg(&a.part_ml[((size_t)slot(y) * R + r) * 2]));
+            for (int z = ca; z <= cb; ++z) M = fmaxf(M, __ldcg(&a.part_ml[((size_t)slot(z) * R + r) * 2]));
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-            for (int y = ca; y <= cb; ++y) {
-                const float2 p = __ldcg((const float2 *)&a.part_ml[((size_t)slot(y) * R + r) * 2]);
-                const float4 v = __ldcg((const float4 *)&a.part[((size_t)slot(y) * R + r) * D + d]);
+            for (int z = ca; z <= cb; ++z) {
+                const float2 p = __ldcg((const float2 *)&a.part_ml[((size_t)slot(z) * R + r) * 2]);
+                const float4 v = __ldcg((const float4 *)&a.part[((size_t)slot(z) * R + r) * D + d]);
                 const float w = part_weight(p.x, p.y, M);
                 S += w * p.y;
                 o.x += v.x * w, o.y += v.y * w, o.z += v.z * w, o.w += v.w * w;
             }
-            store_row<true>(a, f, h, G, D, row0 + r, d, o, M, S, join);
+            if (join) add_prior(y, r, o, M, S);
+            store_row<true>(a, f, h, G, D, row0 + r, d, o, M, S);
         }
         if (tid == 0) a.tickets[ca] = 0;
         __syncthreads();
     }
+    if (dead)   // nothing may land after the CTA is gone: the last copies into each place (bounded)
+        for (uint32_t x = 0; x < (uint32_t)C::SLOTS && x < asked; ++x) warp_wait(&full[x], (asked - 1 - x) / C::SLOTS & 1);
 }
 
 template <int D, int T>
 cudaError_t short_setup()
 {
     return cudaFuncSetAttribute(k_kv_short<D, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                ShortCfg<D, T>::SMEM + 28 * PI_KV_MAX_CALL_SEQS + 8);
+                                ShortCfg<D, T>::SMEM + 28 * PI_KV_MAX_CALL_SEQS + 8 + 1024);
 }
 
 template <int D, int T>
-cudaError_t short_launch(const KvAttendArgs &a, int nsm, cudaStream_t s)
+cudaError_t short_launch(const KvAttendArgs &a, const CUtensorMap &mk, const CUtensorMap &mv, int nsm, cudaStream_t s)
 {
     Launch L;
     L.grid = dim3((unsigned)(ShortCfg<D, T>::CTAS * nsm));
     L.block = dim3(ShortCfg<D, T>::NT);
-    L.smem = ShortCfg<D, T>::SMEM + 28 * (size_t)a.b.n + 8;
+    L.smem = ShortCfg<D, T>::SMEM + 28 * (size_t)a.b.n + 8 + 1024;
     L.stream = s;
     L.pdl = true;
     L.nsm = nsm;
-    return launch_ex(L, k_kv_short<D, T>, a);
+    return launch_ex(L, k_kv_short<D, T>, a, mk, mv);
 }
 
 }  // namespace pi
