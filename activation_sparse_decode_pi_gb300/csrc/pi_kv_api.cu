@@ -121,7 +121,7 @@ cudaError_t attend_of(const pi_kv *h, int layer, KvAttendArgs a, cudaStream_t s)
     cudaError_t e = cudaSuccess;
     bool done = false;   // the few rows
     if constexpr (SHARED && D <= 128)
-        if (few && a.pass == 2) {
+        if (few) {
             KvAttendArgs b = a;
             b.part = h->short_part;
             b.part_ml = h->short_ml;

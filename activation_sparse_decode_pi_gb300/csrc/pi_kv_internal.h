@@ -95,7 +95,7 @@ PI_KV_ROWS(extern, 64, true) PI_KV_ROWS(extern, 128, true) PI_KV_ROWS(extern, 25
 // The kernel of few rows behind a shared prefix (pi_kv_short.cuh): head dims 64 and 128, T 16-bit terms, maps of 16-row
 // boxes. part, part_ml and
 // tickets: [2 * grid][8][dim], [2 * grid][8][2] and [grid] for a grid of SHORT_CTAS * nsm at most.
-constexpr int SHORT_CTAS = 3;
+constexpr int SHORT_CTAS = 4;
 template <int D, int T>
 cudaError_t short_setup();
 template <int D, int T>

@@ -2,9 +2,10 @@
 //
 // The second pass of pi_kv_attend_shared: for each sequence and kv head a tile of up to 8 rows (query token and head of the
 // group) and the positions behind the prefix, often some hundred, then the join with what the first pass left of the rows.
+// And the first pass where a prefix has few rows, which all see all of it.
 // There are many such items and little in each, so what counts is how many are under way and what one costs from end to
-// end: a CTA has four warps that share nothing until an item's end, three CTAs to an SM. A warp takes 16 of a tile's 64
-// positions: it asks for their codes by TMA, four tiles ahead, into boxes of its own, and keeps its own maximum, sum and
+// end: a CTA has four warps that share nothing until an item's end, four CTAs to an SM. A warp takes 16 of a tile's 64
+// positions: it asks for their codes by TMA, three tiles ahead, into boxes of its own, and keeps its own maximum, sum and
 // numerators; the products are pi_kv_split.cuh's (the cache as the 16-row operand on mma.sync m16n8k16, codes to f16 two
 // at a time, queries in terms), and so are their units and rounding. The items are laid end to end and cut into equal
 // shares. An item of up to two shares belongs to the CTA with its first step; a longer one is cut over CTAs and joined by
@@ -21,7 +22,7 @@ constexpr int SHORT_ITEM = 4;   // what an item costs besides its tiles, in tile
 template <int D, int T>
 struct ShortCfg {
     static constexpr int NW = 4, NT = NW * 32, R = 8, CTAS = SHORT_CTAS;
-    static constexpr int SLOTS = 4, BOX = 16 * D;   // places of a warp for 16 positions' keys and values; bytes of either
+    static constexpr int SLOTS = 3, BOX = 16 * D;   // places of a warp for 16 positions' keys and values; bytes of either
     static constexpr int RING = NW * SLOTS * 2 * BOX;
     static_assert(RING >= NW * R * (D + 4) * 4, "the warps' results take the boxes' place");
     static constexpr int SMEM = RING + (NW + 1) * R * 8 + NW * SLOTS * 8;   // and 28 bytes a sequence
@@ -46,6 +47,7 @@ __global__ void __launch_bounds__(ShortCfg<D, T>::NT, ShortCfg<D, T>::CTAS)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
     const KvView &c = a.c;
     const int G = c.hq / c.hkv, P = c.page;
+    const bool flat = a.pass == 1;   // every row sees the whole length
     uint8_t *const ring = smem + warp * C::SLOTS * 2 * C::BOX;
     uint64_t *const full = (uint64_t *)(sums + R * 2) + warp * C::SLOTS;
     if (lane == 0) {
@@ -93,6 +95,7 @@ __global__ void __launch_bounds__(ShortCfg<D, T>::NT, ShortCfg<D, T>::CTAS)
     if (tid == 0) prefix[a.b.n] = run;
     __syncthreads();
     const long long quota = max((run + gridDim.x - 1) / gridDim.x, (long long)(SHORT_ITEM + 1));
+    const bool small = run < (1ll << 31);   // steps are 32-bit numbers: the divisions cost less
     const long long t0 = quota * blockIdx.x, t1 = min(run, t0 + quota);
 
     for (long long t = t0; t < t1;) {
@@ -105,8 +108,9 @@ __global__ void __launch_bounds__(ShortCfg<D, T>::NT, ShortCfg<D, T>::CTAS)
         }
         const int4 f = info[i];
         const int L = f.y, nq = f.w, tile0 = skips[i] / KV_TILE, nt = max(0, (L + KV_TILE - 1) / KV_TILE - tile0);
-        const long long local = t - prefix[i], item = local / (nt + SHORT_ITEM);
-        const int rts = (int)(((long long)nq * G + R - 1) / R), h = (int)(item / rts), row0 = (int)(item % rts) * R;
+        const long long local = t - prefix[i], item = small ? (long long)((uint32_t)local / (uint32_t)(nt + SHORT_ITEM)) : local / (nt + SHORT_ITEM);
+        const int rts = (int)(((long long)nq * G + R - 1) / R), h = small ? (int)((uint32_t)item / (uint32_t)rts) : (int)(item / rts);
+        const int row0 = (int)(item - (long long)h * rts) * R;
         const long long first = prefix[i] + item * (nt + SHORT_ITEM) + SHORT_ITEM;   // step of the item's first tile
         const bool whole_item = nt + SHORT_ITEM <= 2 * quota;
         int k0 = 0, k1 = nt;
@@ -120,7 +124,7 @@ __global__ void __launch_bounds__(ShortCfg<D, T>::NT, ShortCfg<D, T>::CTAS)
             if (k0 >= k1) continue;   // (the share ends before the item's first tile)
         }
         const int p0 = L - nq, rows = min(R, nq * G - row0);
-        const int pos_lo = p0 + row0 / G, pos_hi = p0 + (row0 + rows - 1) / G;
+        const int pos_lo = flat ? L - 1 : p0 + row0 / G, pos_hi = flat ? L - 1 : p0 + (row0 + rows - 1) / G;
 
         // ---------------------------------------------------------------- pages of up to 32 tiles, one to a lane
         int pid = -2;
@@ -182,7 +186,7 @@ __global__ void __launch_bounds__(ShortCfg<D, T>::NT, ShortCfg<D, T>::CTAS)
         float qf[2], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, acc[NJ][4], unit = 0.f, inv = 0.f;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            pos[e] = 2 * q + e < rows ? p0 + (row0 + 2 * q + e) / G : -1;
+            pos[e] = 2 * q + e >= rows ? -1 : flat ? L - 1 : p0 + (row0 + 2 * q + e) / G;
             qf[e] = __shfl_sync(0xffffffffu, qs, (2 * q + e) * 4);
         }
 #pragma unroll
@@ -435,7 +439,8 @@ __global__ void __launch_bounds__(ShortCfg<D, T>::NT, ShortCfg<D, T>::CTAS)
                     make_float2(acc[j][e] * 0x1p-14f * unit, acc[j][2 + e] * 0x1p-14f * unit);
         }
         __syncthreads();
-        const int ca = cut ? (int)(first / quota) : 0, cb = cut ? (int)((first + nt - 1) / quota) : 0;   // the item's CTAs
+        int ca = 0, cb = 0;   // the item's CTAs
+        if (cut) ca = (int)(first / quota), cb = (int)((first + nt - 1) / quota);
         const int part = (int)blockIdx.x == ca ? 2 * ca + 1 : 2 * (int)blockIdx.x;
         if (tid < rows) {
             float M = -INFINITY, S = 0.f;
