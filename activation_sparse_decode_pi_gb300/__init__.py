@@ -525,6 +525,11 @@ def _token_rows(x, heads, dim, name):
     return row if shape[0] > 1 else heads * dim
 
 
+def _empty_like(x, shape, stream):
+    """A new tensor of x's type on x's device that belongs to `stream` (see _empty)."""
+    return x.new_empty(shape) if stream is None else _empty(shape, x.dtype, x.device, stream)
+
+
 def _empty(shape, dtype, device, stream):
     """A new tensor that belongs to `stream` (a torch stream or a handle; None: the current one), so that memory which
     work on another stream may still use is not taken for it."""
@@ -564,6 +569,7 @@ class Int4Linear:
         if bias is not None and (bias.dtype is not torch.float32 or tuple(bias.shape) != (self.n,) or not bias.is_contiguous()):
             raise ValueError(f"bias: contiguous fp32 [{self.n}]")
         self.w, self.s, self.bias = w, s, bias
+        self._weights = w.data_ptr(), s.data_ptr(), _ptr(bias), self.n, self.k
 
     def __call__(self, x, out=None, add=None, stream=None):
         """x [rows, k] (fp32, bf16 or fp16); add: x's type, [rows, n]; out: likewise, and may be add itself."""
@@ -575,13 +581,15 @@ class Int4Linear:
                 raise ValueError("add: x's type and number of rows")
             add = add.data_ptr()
         if out is None:
-            out, ld_out = _empty((rows, n), x.dtype, x.device, stream), n
+            out, ld_out = _empty_like(x, (rows, n), stream), n
         else:
             ld_out = _rows(out, n, "out")
             if out.dtype is not x.dtype or out.shape[0] != rows:
                 raise ValueError("out: x's type and number of rows")
-        pi_int4_linear(self.w.data_ptr(), self.s.data_ptr(), _ptr(self.bias), n, self.k, x.data_ptr(), ld_x, rows, add,
-                       ld_add, out.data_ptr(), ld_out, dtype, stream)
+        code = _lib.pi_int4_linear(*self._weights, x.data_ptr(), ld_x, rows, add, ld_add, out.data_ptr(), ld_out, dtype,
+                                   _stream(stream))
+        if code:
+            _check(code, "pi_int4_linear")
         return out
 
 
@@ -654,31 +662,46 @@ class Rotary:
         self.turns = torch.tensor(turns, dtype=torch.int64).to(device)
         self.desc = PiRotary(_ptr(self.turns) if turns else None, _ptr(q_norm), _ptr(k_norm), 2 * len(turns), int(interleaved),
                              int(norm), amp, eps)
+        self._desc = ctypes.byref(self.desc)
 
     def rotate(self, pos, q, k=None, q_out=None, k_out=None, stream=None):
         """(q_out, k_out): q [tokens, heads, dim] and k [tokens, kv heads, dim] (fp32, bf16 or fp16) at positions pos
         (int32 [tokens]). q_out and k_out may be q and k themselves."""
-        T, heads, dim, dtype = q.shape[0], q.shape[1], self.head_dim, _act_dtype(q)
-        args, outs = [], []
-        for name, x, out in (("q", q, q_out), ("k", k, k_out)):
-            if x is None:
-                args += [None, 0, None, 0]
-                outs.append(None)
-                continue
-            if x.dim() != 3 or x.dtype is not q.dtype or x.shape[0] != T:
-                raise ValueError(f"{name}: [tokens, heads, dim] of one type and number of tokens")
-            n = x.shape[1]
-            ld = _token_rows(x, n, dim, name)
-            if out is None:
-                out, ld_out = _empty((T, n, dim), x.dtype, x.device, stream), n * dim
+        shape, dtype = q.shape, _act_dtype(q)
+        if len(shape) != 3:
+            raise ValueError("q: [tokens, heads, dim]")
+        T, heads, dim = shape[0], shape[1], self.head_dim
+        ld_q = _token_rows(q, heads, dim, "q")
+        if q_out is None:
+            q_out, ld_q_out = _empty_like(q, (T, heads, dim), stream), heads * dim
+        else:
+            ld_q_out = self._out(q_out, q, heads, "q_out")
+        kv_heads = ld_k = ld_k_out = 0
+        k_at = k_out_at = None
+        if k is None:
+            k_out = None
+        else:
+            shape = k.shape
+            if len(shape) != 3 or shape[0] != T or k.dtype is not q.dtype:
+                raise ValueError("k: [tokens, kv heads, dim] of q's type and number of tokens")
+            kv_heads = shape[1]
+            ld_k = _token_rows(k, kv_heads, dim, "k")
+            if k_out is None:
+                k_out, ld_k_out = _empty_like(k, (T, kv_heads, dim), stream), kv_heads * dim
             else:
-                ld_out = _token_rows(out, n, dim, name + "_out")
-                if out.dtype is not x.dtype or out.shape[0] != T:
-                    raise ValueError(f"{name}_out: {name}'s type and number of tokens")
-            args += [x.data_ptr(), ld, out.data_ptr(), ld_out]
-            outs.append(out)
-        pi_rotate(self.desc, _i32(pos, "pos", T), T, heads, 0 if k is None else k.shape[1], dim, *args, dtype, stream)
-        return tuple(outs)
+                ld_k_out = self._out(k_out, k, kv_heads, "k_out")
+            k_at, k_out_at = k.data_ptr(), k_out.data_ptr()
+        code = _lib.pi_rotate(self._desc, _i32(pos, "pos", T), T, heads, kv_heads, dim, q.data_ptr(), ld_q, q_out.data_ptr(),
+                              ld_q_out, k_at, ld_k, k_out_at, ld_k_out, dtype, _stream(stream))
+        if code:
+            _check(code, "pi_rotate")
+        return q_out, k_out
+
+    def _out(self, out, x, heads, name):
+        """Row stride of an output given for x."""
+        if out.dtype is not x.dtype or out.shape[0] != x.shape[0]:
+            raise ValueError(f"{name}: its input's type and number of tokens")
+        return _token_rows(out, heads, self.head_dim, name)
 
 
 class KVCache:
@@ -712,6 +735,7 @@ class KVCache:
             raise ValueError("length has an entry for each table row, ref one for each page")
         self.n_heads, self.n_kv_heads, self.head_dim, self.page_tokens = n_heads, kv_heads, dim, page
         self.desc = PiKvDesc(len(self.layers), n_heads, kv_heads, dim, page, n_pages, table.shape[0], table.shape[1])
+        self._f32 = self.layers[0]["k_scale"]
         self.h = None
         self.h = pi_kv_create(self.desc, [PiKvLayer(*(_ptr(L[x]) for x in ("k", "v", "k_scale", "v_scale")))
                                           for L in self.layers], PiKvState(_ptr(table), _ptr(length), _ptr(ref)))
@@ -760,14 +784,14 @@ class KVCache:
                 k_new.dtype is not q.dtype or v_new.shape[0] != T or k_new.shape[0] != T:
             raise ValueError("q, k_new and v_new: one type and number of tokens, the latter two one row stride")
         if q_out is None:
-            q_out, ld_out = _empty((T, heads, dim), q.dtype, q.device, stream), heads * dim
+            q_out, ld_out = _empty_like(q, (T, heads, dim), stream), heads * dim
         else:
-            ld_out = _token_rows(q_out, heads, dim, "q_out")
-            if q_out.dtype is not q.dtype or q_out.shape[0] != T:
-                raise ValueError("q_out: q's type and number of tokens")
-        pi_kv_append_rotated(self.h, layer, _i32(seqs, "seqs"), _i32(tok_start, "tok_start", n + 1), n, T, rotary.desc,
-                             q.data_ptr(), ld_q, q_out.data_ptr(), ld_out, k_new.data_ptr(), v_new.data_ptr(), ld, dtype,
-                             stream)
+            ld_out = rotary._out(q_out, q, heads, "q_out")
+        code = _lib.pi_kv_append_rotated(self.h, layer, _i32(seqs, "seqs"), _i32(tok_start, "tok_start", n + 1), n, T,
+                                         rotary._desc, q.data_ptr(), ld_q, q_out.data_ptr(), ld_out, k_new.data_ptr(),
+                                         v_new.data_ptr(), ld, dtype, _stream(stream))
+        if code:
+            _check(code, "pi_kv_append_rotated")
         return q_out
 
     def attend(self, layer, seqs, tok_start, q, out=None, lse=None, *, scale=None, window=0, sinks=0, stream=None):
@@ -785,7 +809,7 @@ class KVCache:
         T, heads, dim = q.shape[0], self.n_heads, self.head_dim
         ld, dtype = _token_rows(q, heads, dim, "q"), _act_dtype(q)
         if out is None:
-            out, ld_out = _empty((T, heads, dim), q.dtype, q.device, stream), heads * dim
+            out, ld_out = _empty_like(q, (T, heads, dim), stream), heads * dim
         else:
             ld_out = _token_rows(out, heads, dim, "out")
             if out.dtype is not q.dtype or out.shape[0] != T:
@@ -816,12 +840,14 @@ class KVCache:
         out, args = self._attend_args(q, out, lse, stream)
         room = T * self.n_heads * (self.head_dim + 2)
         if work is None:
-            work = _empty(room, self.layers[0]["k_scale"].dtype, q.device, stream)
+            work = _empty_like(self._f32, (room,), stream)
         elif _act_dtype(work) != PI_F32 or work.numel() < room or not work.is_contiguous():
             raise ValueError(f"work: contiguous fp32 of {room} elements")
-        pi_kv_attend_shared(self.h, layer, _i32(seqs, "seqs"), _i32(tok_start, "tok_start", n + 1), n, T,
-                            _i32(plan, "plan", 3 * (n + groups) + 2), groups, *args,
-                            self.head_dim ** -0.5 if scale is None else scale, work.data_ptr(), stream)
+        code = _lib.pi_kv_attend_shared(self.h, layer, _i32(seqs, "seqs"), _i32(tok_start, "tok_start", n + 1), n, T,
+                                        _i32(plan, "plan", 3 * (n + groups) + 2), groups, *args,
+                                        self.head_dim ** -0.5 if scale is None else scale, work.data_ptr(), _stream(stream))
+        if code:
+            _check(code, "pi_kv_attend_shared")
         return out
 
     def fork(self, src, dst, stream=None) -> None:

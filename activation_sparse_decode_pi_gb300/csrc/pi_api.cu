@@ -26,23 +26,17 @@ namespace {
 
 constexpr float RMS_EPS = 1e-6f;
 
-typedef CUresult (*GetRangeFn)(CUdeviceptr *, size_t *, CUdeviceptr);
+typedef CUresult (*GetAttributesFn)(unsigned int, CUpointer_attribute *, void **, CUdeviceptr);
 
-GetRangeFn get_range_fn()
+GetAttributesFn find_attributes_fn()
 {
-    static GetRangeFn fn = nullptr;
-    static bool tried = false;
-    if (!tried) {
-        tried = true;
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuMemGetAddressRange", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = (GetRangeFn)p;
-        else
-            cudaGetLastError();
-    }
-    return fn;
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuPointerGetAttributes", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+        return (GetAttributesFn)p;
+    cudaGetLastError();
+    return nullptr;
 }
 
 }  // namespace
@@ -52,6 +46,21 @@ namespace pi {
 pi_status_t check_ptr(const void *p, size_t bytes, size_t align, int dev)
 {
     if (!p || ((uintptr_t)p % align) != 0) return PI_ERR_INVALID_ARG;
+    static const GetAttributesFn fn = find_attributes_fn();
+    // one call to the driver: what memory it is, on which device, and its allocation (0 where the driver cannot say)
+    unsigned int type = 0, managed = 0;
+    int device = -1;
+    CUdeviceptr base = 0;
+    size_t size = 0;
+    CUpointer_attribute what[5] = {CU_POINTER_ATTRIBUTE_MEMORY_TYPE, CU_POINTER_ATTRIBUTE_IS_MANAGED,
+                                   CU_POINTER_ATTRIBUTE_DEVICE_ORDINAL, CU_POINTER_ATTRIBUTE_RANGE_START_ADDR,
+                                   CU_POINTER_ATTRIBUTE_RANGE_SIZE};
+    void *to[5] = {&type, &managed, &device, &base, &size};
+    if (fn && fn(5, what, to, (CUdeviceptr)(uintptr_t)p) == CUDA_SUCCESS) {
+        if (!managed && (type != CU_MEMORYTYPE_DEVICE || device != dev)) return PI_ERR_INVALID_ARG;
+        if (size && (uintptr_t)p + bytes > (uintptr_t)base + size) return PI_ERR_INVALID_ARG;
+        return PI_OK;
+    }
     cudaPointerAttributes a;
     if (cudaPointerGetAttributes(&a, p) != cudaSuccess) {
         cudaGetLastError();
@@ -59,13 +68,6 @@ pi_status_t check_ptr(const void *p, size_t bytes, size_t align, int dev)
     }
     if (a.type != cudaMemoryTypeDevice && a.type != cudaMemoryTypeManaged) return PI_ERR_INVALID_ARG;
     if (a.type == cudaMemoryTypeDevice && a.device != dev) return PI_ERR_INVALID_ARG;
-    if (GetRangeFn fn = get_range_fn()) {
-        CUdeviceptr base = 0;
-        size_t size = 0;
-        if (fn(&base, &size, (CUdeviceptr)(uintptr_t)p) == CUDA_SUCCESS) {
-            if ((uintptr_t)p + bytes > (uintptr_t)base + size) return PI_ERR_INVALID_ARG;
-        }
-    }
     return PI_OK;
 }
 

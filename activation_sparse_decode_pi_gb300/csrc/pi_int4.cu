@@ -374,8 +374,8 @@ cudaError_t launch_of(const Int4Args &in, const Int4Plan &p, const CUtensorMap &
     a.groups = (G + p.cluster - 1) / p.cluster;
     a.bar_at = (int)p.bar_at;
     const auto kern = k_int4_linear<DT, NT>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, I4_SMEM);
-    if (e != cudaSuccess) return e;
+    cudaError_t e;
+    if ((e = allow_smem<k_int4_linear<DT, NT>>(I4_SMEM)) != cudaSuccess) return e;
     // CTAs stay and go through tiles: as many as the GPU holds at a time
     const int slices = (a.rows + p.rows_per - 1) / p.rows_per, tiles = (a.n + R - 1) / R;
     cudaLaunchConfig_t cfg = {};

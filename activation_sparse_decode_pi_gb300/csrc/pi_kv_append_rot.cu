@@ -230,7 +230,7 @@ cudaError_t launch_of(const KvAppendRotArgs &in, int nsm, cudaStream_t s)
     a.cap = (int)std::min<int64_t>(a.c.page, T);
     const size_t smem = (size_t)a.cap * a.r.rot * 4;   // at most 128 x 256 x 4
     if (smem > 40 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(k_kv_append_rot<DT, D, U>, cudaFuncAttributeMaxDynamicSharedMemorySize, 128 * D * 4);
+        const cudaError_t e = allow_smem<k_kv_append_rot<DT, D, U>>(128 * D * 4);
         if (e != cudaSuccess) return e;
     }
     Launch L;

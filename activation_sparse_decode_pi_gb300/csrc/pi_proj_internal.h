@@ -6,6 +6,8 @@
 #include <cuda_fp16.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "pi_internal.h"
 #include "pi_proj.h"
 
@@ -16,6 +18,20 @@ typedef CUresult (*EncodeFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, voi
                              const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 EncodeFn tensor_map_encoder();
+
+// Lets a kernel have `bytes` of dynamic shared memory on the current device, once for each device (safe from any thread).
+template <auto kernel>
+cudaError_t allow_smem(int bytes)
+{
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || dev >= 64) return e != cudaSuccess ? e : cudaErrorInvalidDevice;
+    if (done.load(std::memory_order_acquire) >> dev & 1) return cudaSuccess;
+    const cudaError_t f = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (f == cudaSuccess) done.fetch_or((uint64_t)1 << dev, std::memory_order_release);
+    return f;
+}
 
 struct Int4Args {
     const uint8_t *w;      // [n x k/2]
