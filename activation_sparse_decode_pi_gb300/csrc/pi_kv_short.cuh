@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(ShortCfg<D, T>::NT, ShortCfg<D, T>::CTAS)
         const int rts = (int)(((long long)nq * G + R - 1) / R), h = small ? (int)((uint32_t)item / (uint32_t)rts) : (int)(item / rts);
         const int row0 = (int)(item - (long long)h * rts) * R;
         const long long first = prefix[i] + item * (nt + SHORT_ITEM) + SHORT_ITEM;   // step of the item's first tile
-        const bool whole_item = nt + SHORT_ITEM <= 2 * quota;
+        const bool whole_item = nt == 0 || nt + SHORT_ITEM <= 2 * quota;   // (without positions there is nothing to cut)
         int k0 = 0, k1 = nt;
         if (whole_item) {
             t = first + nt;

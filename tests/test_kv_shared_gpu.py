@@ -132,6 +132,24 @@ def test_groups_of_different_prompts(P, kind):
     b.check([5, 5, 4, 5], [1, 4, 1, 1], [0, 4], kind, [896])                    # one sequence thrice
 
 
+@pytest.mark.parametrize("kind", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("dim,page", [(64, 16), (128, 64), (256, 32)])
+def test_groups_of_some_dozen_rows(P, dim, page, kind):
+    """Prefixes that fill a part of a 128-row tile, all of one, and more than one beside a smaller group."""
+    b = Shared(P, hq=8, hkv=2, dim=dim, page=page, n_pages=-(-3000 // page) + 150, max_seqs=60, max_pages=-(-1300 // page))
+    b.grow([0, 1], [1100, 530])
+    first, second = list(range(2, 40)), list(range(40, 48))
+    b.fork([0] * len(first), first)
+    b.fork([1] * len(second), second)
+    one, two = [0] + first, [1] + second
+    b.grow(one + two, [1 + i % 4 for i in range(len(one) + len(two))])
+    b.check(one[:9], [1] * 9, [0, 9], kind, [1024])                             # 36 rows, split along the prefix
+    b.check(one[:32], [1] * 32, [0, 32], kind, [1024])                          # 128
+    b.check(one + two, [1] * 48, [0, 39, 48], kind, [1024, 512])                # 156 and 36
+    b.check(two + one[:12], [1] * 21, [0, 9, 21], kind, [512, 1024])
+    b.check(one[:3] + two, [1] * 12, [0, 3, 12], kind, [1024, 512])             # 12 rows beside 36
+
+
 def test_long_prefix_is_split(P):
     b = Shared(P, hq=16, hkv=2, dim=128, page=64, n_pages=500, max_seqs=70, max_pages=360)
     b.grow([0], [20000])
