@@ -60,6 +60,7 @@ struct KvAttendArgs {
     int pass;                  // 0: one pass alone; 1: the first, whose rows all see positions [0, length); 2: the second
     float *prior, *prior_ml;   // [parts][n_tokens x hq][dim], [parts][n_tokens x hq][2]
     int parts;                 // of a row that the first pass has split along its prefix
+    bool few;                  // first pass: the rows kernel's items have up to 128 rows
 };
 constexpr int KV_SHARE = 128;   // a shared prefix is a multiple of this: whole tiles of both kernels, whole pages
 
@@ -79,16 +80,18 @@ PI_KV_SPLIT(extern, 64, true) PI_KV_SPLIT(extern, 128, true) PI_KV_SPLIT(extern,
 
 // The rows kernel (pi_kv_rows.cuh): QT 16-bit terms of queries and weights. items: an upper bound of the
 // call's (sequence, kv head, run of rows_per_item rows); splits: parts of each item's cache.
-constexpr int rows_per_item(int dim) { return dim == 256 ? 128 : 256; }
-template <int D, int QT, bool SHARED>
+constexpr int rows_per_item(int dim, bool few = false) { return dim == 256 || few ? 128 : 256; }
+template <int D, int QT, bool SHARED, bool FEW>
 cudaError_t rows_setup();
-template <int D, int QT, bool SHARED>
+template <int D, int QT, bool SHARED, bool FEW>
 cudaError_t rows_launch(const KvAttendArgs &a, const CUtensorMap &mk, const CUtensorMap &mv, unsigned items,
                         unsigned splits, cudaStream_t s);
-#define PI_KV_ROWS1(WORD, D, QT, S)                  \
-    WORD template cudaError_t rows_setup<D, QT, S>(); \
-    WORD template cudaError_t rows_launch<D, QT, S>(const KvAttendArgs &, const CUtensorMap &, const CUtensorMap &, unsigned, unsigned, cudaStream_t);
-#define PI_KV_ROWS(WORD, D, S) PI_KV_ROWS1(WORD, D, 1, S) PI_KV_ROWS1(WORD, D, 2, S)
+#define PI_KV_ROWS1(WORD, D, QT, S, F)                  \
+    WORD template cudaError_t rows_setup<D, QT, S, F>(); \
+    WORD template cudaError_t rows_launch<D, QT, S, F>(const KvAttendArgs &, const CUtensorMap &, const CUtensorMap &, unsigned, unsigned, cudaStream_t);
+#define PI_KV_ROWS(WORD, D, S) PI_KV_ROWS1(WORD, D, 1, S, false) PI_KV_ROWS1(WORD, D, 2, S, false)
+#define PI_KV_ROWS_FEW(WORD, D) PI_KV_ROWS1(WORD, D, 1, true, true) PI_KV_ROWS1(WORD, D, 2, true, true)
+PI_KV_ROWS_FEW(extern, 64) PI_KV_ROWS_FEW(extern, 128)
 PI_KV_ROWS(extern, 64, false) PI_KV_ROWS(extern, 128, false) PI_KV_ROWS(extern, 256, false)
 PI_KV_ROWS(extern, 64, true) PI_KV_ROWS(extern, 128, true) PI_KV_ROWS(extern, 256, true)
 

@@ -29,9 +29,10 @@
 
 namespace pi {
 
-template <int D, int QT>
+// FEW: items of up to 128 rows (head dims 64 and 128), without a second group's warps, whose registers the others have
+template <int D, int QT, bool FEW>
 struct RowsCfg {
-    static constexpr int NG = D == 256 ? 1 : 2;                 // groups of 128 rows
+    static constexpr int NG = D == 256 || FEW ? 1 : 2;          // groups of 128 rows
     static constexpr int ROWS = 128 * NG, RT = 2 * ROWS;        // rows, and their threads
     static constexpr int LOADERS = 128, NT = RT + LOADERS;
     static constexpr int TOK = D == 256 || QT == 2 ? 64 : 128;  // positions per tile
@@ -152,22 +153,22 @@ struct RowsShared {
     uint32_t taddr;
 };
 
-template <int D, int QT>
+template <int D, int QT, bool FEW>
 constexpr int rows_smem()
 {
-    using C = RowsCfg<D, QT>;
+    using C = RowsCfg<D, QT, FEW>;
     constexpr int n = C::DATA + (int)sizeof(RowsShared<C::ROWS, C::NT / 32>);
     static_assert(n <= 227 * 1024, "shared memory");
     return n;
 }
 
 // SHARED: a pass of pi_kv_attend_shared (a.pass), else one pass alone
-template <int D, int QT, bool SHARED>
-__global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_constant__ KvAttendArgs a,
+template <int D, int QT, bool SHARED, bool FEW>
+__global__ void __launch_bounds__(RowsCfg<D, QT, FEW>::NT, 1) k_kv_rows(const __grid_constant__ KvAttendArgs a,
                                                                     const __grid_constant__ CUtensorMap mk,
                                                                     const __grid_constant__ CUtensorMap mv)
 {
-    using C = RowsCfg<D, QT>;
+    using C = RowsCfg<D, QT, FEW>;
     constexpr int TOK = C::TOK, NB = C::NB, NW = C::NT / 32;
     constexpr int NBLK = D / 64, NV = TOK * D / 16 / C::LOADERS;   // 64-column blocks; 16-byte vectors per loader thread
     constexpr int RPY = C::LOADERS / 4;   // rows of a tile that the loaders take at a time
@@ -779,24 +780,24 @@ __global__ void __launch_bounds__(RowsCfg<D, QT>::NT, 1) k_kv_rows(const __grid_
     }
 }
 
-template <int D, int QT, bool SHARED>
+template <int D, int QT, bool SHARED, bool FEW>
 cudaError_t rows_setup()
 {
-    return cudaFuncSetAttribute(k_kv_rows<D, QT, SHARED>, cudaFuncAttributeMaxDynamicSharedMemorySize, rows_smem<D, QT>());
+    return cudaFuncSetAttribute(k_kv_rows<D, QT, SHARED, FEW>, cudaFuncAttributeMaxDynamicSharedMemorySize, rows_smem<D, QT, FEW>());
 }
 
-template <int D, int QT, bool SHARED>
+template <int D, int QT, bool SHARED, bool FEW>
 cudaError_t rows_launch(const KvAttendArgs &a, const CUtensorMap &mk, const CUtensorMap &mv, unsigned items,
                         unsigned splits, cudaStream_t s)
 {
     Launch L;
     L.grid = dim3(items, splits);
-    L.block = dim3(RowsCfg<D, QT>::NT);
-    L.smem = rows_smem<D, QT>();
+    L.block = dim3(RowsCfg<D, QT, FEW>::NT);
+    L.smem = rows_smem<D, QT, FEW>();
     L.stream = s;
     L.pdl = true;
     L.nsm = 0;
-    return launch_ex(L, k_kv_rows<D, QT, SHARED>, a, mk, mv);
+    return launch_ex(L, k_kv_rows<D, QT, SHARED, FEW>, a, mk, mv);
 }
 
 }  // namespace pi

@@ -4,4 +4,5 @@
 
 namespace pi {
 PI_KV_ROWS(, 128, true)
+PI_KV_ROWS_FEW(, 128)
 }  // namespace pi

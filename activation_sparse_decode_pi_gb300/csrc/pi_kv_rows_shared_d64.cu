@@ -4,4 +4,5 @@
 
 namespace pi {
 PI_KV_ROWS(, 64, true)
+PI_KV_ROWS_FEW(, 64)
 }  // namespace pi
