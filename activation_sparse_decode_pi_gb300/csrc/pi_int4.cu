@@ -24,7 +24,7 @@ namespace cg = cooperative_groups;
 constexpr int I4_NT = 512, I4_NW = I4_NT / 32;
 constexpr int I4_GROUP = 128;
 constexpr int I4_SMEM = 227 * 1024;    // of a CTA, one to an SM
-constexpr double I4_TILE_US = 0.5, I4_CLUSTER_US = 1.0, I4_X_US = 0.01;
+constexpr double I4_TILE_US = 0.5, I4_CLUSTER_US = 1.0, I4_X_US = 0.01;   // of the estimate below (measured)
 constexpr int I4_BOX = 32 * 128;       // bytes of a box: 32 rows of W, two groups
 constexpr int I4_SLOTS = 3;            // places for boxes of a warp, at most
 
@@ -336,9 +336,9 @@ __global__ void __launch_bounds__(I4_NT, 1) k_int4_linear(const __grid_constant_
                         if (b < nb) red[(wk * (8 * NT) + b) * (R + 1) + r] = tot[m][n][e];
                     }
             meet();
-            const int per = R / cs;   // rows that this CTA adds up
+            const int r_lo = R * rank / cs, per = R * (rank + 1) / cs - r_lo;   // rows that this CTA adds up
             for (int x = tid; x < per * nb; x += I4_NT) {
-                const int b = x / per, r = rank * per + x - b * per, i = tile * R + r;
+                const int b = x / per, r = r_lo + x - b * per, i = tile * R + r;
                 if (i >= a.n) continue;
                 float v = 0.f;
                 for (int c = 0; c < cs; ++c) {
@@ -356,6 +356,14 @@ __global__ void __launch_bounds__(I4_NT, 1) k_int4_linear(const __grid_constant_
 }
 
 namespace {
+
+// Clusters of cs CTAs, one to an SM, that run at a time. A cluster's SMs lie in one group of the GPU's SMs, so 152 SMs hold
+// (by the runtime's count) 15 of 8 and not 19.
+int clusters_at_once(int nsm, int cs)
+{
+    constexpr int of_152[8] = {152, 76, 46, 36, 28, 23, 15, 15};
+    return std::max(1, of_152[cs - 1] * nsm / 152);
+}
 
 struct Int4Plan {
     int kw, cluster, rows_per, slots;
@@ -379,7 +387,7 @@ cudaError_t launch_of(const Int4Args &in, const Int4Plan &p, const CUtensorMap &
     // CTAs stay and go through tiles: as many as the GPU holds at a time
     const int slices = (a.rows + p.rows_per - 1) / p.rows_per, tiles = (a.n + R - 1) / R;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(std::min(tiles, std::max(1, nsm / (p.cluster * slices))) * p.cluster), (unsigned)slices);
+    cfg.gridDim = dim3((unsigned)(std::min(tiles, std::max(1, clusters_at_once(nsm, p.cluster) / slices)) * p.cluster), (unsigned)slices);
     cfg.blockDim = dim3(I4_NT);
     cfg.dynamicSmemBytes = p.smem;
     cfg.stream = s;
@@ -404,19 +412,23 @@ cudaError_t launch_dt(const Int4Args &a, const CUtensorMap &map, int nsm, cudaSt
     p.rows_per = std::min(a.rows, std::max(1, fit));
     const int nt = p.rows_per <= 8 ? 1 : p.rows_per <= 16 ? 2 : 4;
     const int slices = (a.rows + p.rows_per - 1) / p.rows_per;
+    // The fastest by an estimate: rounds of tiles, each as long as its bytes of W take (45 bytes a nanosecond to an SM), or
+    // its products (16 NT T of 8 cycles to a warp's group, four warps to a scheduler), or a box's latency; and what a
+    // tile's sums, a cluster's barriers and bringing in x cost.
     double best = 0;
-    for (int cs = 1; cs <= 8; cs *= 2)
+    for (int cs = 1; cs <= 8; ++cs)
         for (int kw = 1; kw <= I4_NW; kw *= 2) {
             const int R = 32 * (I4_NW / kw), groups = (G + cs - 1) / cs;
-            if (R < cs) continue;
             const size_t sums = kw == 1 && cs == 1 ? 0 : (size_t)kw * 8 * nt * (R + 1) * 4;
             const size_t rest = ((size_t)groups * (256 * T * p.rows_per + 64 * nt) + sums + 7) / 8 * 8 + 8 * I4_NW * I4_SLOTS;
             if (rest + I4_NW * I4_BOX > I4_SMEM) continue;
             const int n_slots = std::min<int>(I4_SLOTS, (int)((I4_SMEM - rest) / (I4_NW * I4_BOX)));
-            const int64_t tiles = (int64_t)((a.n + R - 1) / R) * slices, room = std::max(1, nsm / cs);
-            const int64_t rounds = (tiles + room - 1) / room;
+            const int64_t tiles = (int64_t)((a.n + R - 1) / R) * slices;
+            const int64_t rounds = (tiles + clusters_at_once(nsm, cs) - 1) / clusters_at_once(nsm, cs);
             const int boxes = ((groups + 1) / 2 + kw - 1) / kw;
-            const double us = (double)rounds * (std::max(boxes * kw * (R / 32) * I4_BOX / 45e3, boxes * 0.15) + I4_TILE_US * (sums > 0) + (cs > 1 ? I4_CLUSTER_US : 0.0)) + (double)groups * p.rows_per * I4_X_US;
+            const double tile_us = std::max({boxes * kw * (R / 32) * I4_BOX / 45e3, boxes * 2 * 0.27 * nt * T, boxes * 0.15});
+            const double us = (double)rounds * (tile_us + I4_TILE_US * (sums > 0) + (cs > 1 ? I4_CLUSTER_US : 0.0)) +
+                              (double)groups * p.rows_per * I4_X_US;
             if (p.cluster == 0 || us < best) {
                 best = us;
                 p.cluster = cs;
