@@ -1,15 +1,22 @@
 // pi_int4.cu -- projections of a few rows with int4 group-128 weights (sm_103a).
 //
-// y[b, i] = sum_g s[i, g] sum_{k in g} q[i, k] x[b, k]. Up to a dozen rows the bytes of W bound it (half a byte a weight;
-// d 4096: 13 MB in 1.9 us), so the rest has to hide under its loads:
+// y[b, i] = sum_g s[i, g] sum_{k in g} q[i, k] x[b, k]. Up to about eight rows the bytes of W bound it (half a byte a weight;
+// d 12288: 226 MB in 34 us), so the rest has to hide under its loads:
+//  - weights come by TMA, a box of 32 rows and two groups at a time, into places of each warp's own, so that no warp waits
+//    for another's and a load costs no address arithmetic (loads to registers, 16 bytes a lane: 87 us where this takes 44);
 //  - products on mma.sync m16n8k16, 16 rows of W against up to 8 rows of x: 16 bytes of a row of W to a lane are 32
 //    nibbles, four lanes' a group. The contraction may run in any order that both operands share, so nibbles are used
-//    as they lie: a word's nibbles (i, i + 4) become an f16 pair by masking them into the mantissa of 1024, and x is
-//    laid into shared memory in that order;
+//    as they lie: a word's nibbles (i, i + 4) become an f16 pair by one mask, as subnormals, and x is laid into shared
+//    memory in that order. (tcgen05 products want 128 rows and both operands in shared memory: the f16 weights would be
+//    written there and read again, four bytes for every half that comes in.)
 //  - x is cut to f16 in units of a power of two for each row and group (fp32: two terms), undone in fp32 with the
-//    weights' scale, so a group's sum is of exact integers times f16 and nothing else is rounded before fp32;
-//  - a CTA's warps split its rows of W (MW ways) and the contraction (KW ways); CTAs of a cluster split the
-//    contraction further and add their sums through distributed shared memory, in the order of their ranks.
+//    weights' scale, so a group's sum is of whole numbers times f16 and nothing else is rounded before fp32;
+//  - one CTA to an SM stays and goes through tiles of W, x resident. Its 16 warps split a tile's rows and the
+//    contraction (kw ways); CTAs of a cluster split the contraction further, where x is too large for one or the tiles are
+//    few, and add their sums through distributed shared memory in the order of their ranks.
+// Measured, one row (graph of calls back to back): 12288 -> 36864 bf16 44 us = 5.3 TB/s, fp32 52 us (second terms: twice the
+// products), 4096 -> 6144 bf16 7.0 us (launch, x, one tile and its sums in turn). 5120 -> 15360: 8 rows fp32 19 us, 16 rows
+// 29 us, 64 rows 153 us: from 9 rows on the products (mma.sync gives 1024 a cycle and SM) and the cluster's sums bound it.
 #include <cooperative_groups.h>
 
 #include <algorithm>

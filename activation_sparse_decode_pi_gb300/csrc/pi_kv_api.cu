@@ -365,7 +365,7 @@ pi_status_t pi_kv_get_status(pi_kv_t *h)
     if ((s = cuda_status(cudaMemcpy(&v, h->status, 4, cudaMemcpyDeviceToHost)))) return s;
     if (v && (s = cuda_status(cudaMemset(h->status, 0, 4)))) return s;
     // a kernel that gave up between its tickets leaves them: start the next call clean
-    if (v == PI_ERR_TIMEOUT && (s = cuda_status(cudaMemset(h->tickets, 0, 3 * up((size_t)h->nsm * 4))))) return s;
+    if (v == PI_ERR_TIMEOUT && (s = cuda_status(cudaMemset(h->tickets, 0, (3 + SHORT_CTAS) * up((size_t)h->nsm * 4))))) return s;
     return (pi_status_t)v;
 }
 
@@ -475,6 +475,12 @@ pi_status_t pi_kv_attend_shared(pi_kv_t *h, int32_t layer, const int32_t *seqs, 
     const bool few = h->desc.head_dim <= 128 && group_rows <= (int64_t)128 * n_groups;
     const int64_t run = rows_per_item(h->desc.head_dim, few), most = ((group_rows + run - 1) / run + n_groups - 1) * h->desc.n_kv_heads;
     a.parts = n_groups > 0 && group_rows >= ROWS_FROM ? (int)std::max<int64_t>(1, std::min<int64_t>(16, h->nsm / most)) : 1;
+    const int64_t wide = (int64_t)h->desc.n_heads * h->desc.head_dim;
+    const Strided sw{work, 1, rows * (h->desc.head_dim + 2), rows * (h->desc.head_dim + 2), 4};
+    const int es = elt_size(dtype);
+    if (may_overlap(sw, {q, n_tokens, wide, ld_q, es}) || may_overlap(sw, {out, n_tokens, wide, ld_out, es}) ||
+        may_overlap(sw, {lse, 1, rows, rows, 4}))
+        return PI_ERR_INVALID_ARG;
     a.prior = a.parts > 1 ? h->prior : (float *)work;
     a.prior_ml = a.prior + a.parts * rows * h->desc.head_dim;
     const int32_t *lead = plan, *start = lead + n_groups, *len = start + n_groups + 1, *skip = len + n_groups, *was = skip + n;

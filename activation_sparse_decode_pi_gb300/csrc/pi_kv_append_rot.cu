@@ -7,6 +7,8 @@
 // token and a part of its heads to a warp, as in pi_rotate.cu. Keys and values: one to eight warps to one (page, head), as in
 // pi_kv_append.cu (largest value, block scale, codes), keys with cosines and sines that the CTA works out once for all its
 // heads.
+// Measured: 7 prompts of 1015..3351 tokens, 32 heads on 8 of 128, bf16 97 us = 3.5 TB/s; queries alone (the other CTAs out)
+// took 62 us, keys and values 60 us, and both want issue slots. 64 tokens of 40 + 80 heads, fp32 6.5 us; one token 3.3 us.
 #include <algorithm>
 
 #include "pi_rotary.cuh"

@@ -6,7 +6,7 @@
 
 namespace pi {
 
-constexpr int SH_NT = 256, SH_NW = SH_NT / 32;
+constexpr int SH_NT = 1024, SH_NW = SH_NT / 32;
 
 __global__ void __launch_bounds__(SH_NT) k_kv_share(const KvView c, const KvBatch b, const int32_t *groups, int ng, int32_t *plan)
 {

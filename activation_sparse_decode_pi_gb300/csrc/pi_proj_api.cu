@@ -131,9 +131,14 @@ pi_status_t pi_rotate(const pi_rotary_t *rotary, const int32_t *pos, int32_t n_t
         if (bytes < 0 || (x.ld * es) % 16) return PI_ERR_INVALID_ARG;
         if ((st = check_ptr(x.p, (size_t)bytes, 16, dev))) return st;
     }
-    for (int i = 1; i < 4; i += 2)
+    const Strided read[4] = {{pos, 1, n_tokens, n_tokens, 4}, {a.r.turns, 1, a.r.rot / 2, a.r.rot / 2, 8},
+                             {a.r.norm ? a.r.qn : nullptr, 1, head_dim, head_dim, 4}, {a.r.norm ? a.r.kn : nullptr, 1, head_dim, head_dim, 4}};
+    for (int i = 1; i < 4; i += 2) {
         for (int j = 0; j < 4; ++j)
             if (j != i && !(j == i - 1 && same_place(all[i], all[j])) && may_overlap(all[i], all[j])) return PI_ERR_INVALID_ARG;
+        for (const Strided &x : read)
+            if (may_overlap(all[i], x)) return PI_ERR_INVALID_ARG;
+    }
     a.pos = pos;
     a.q = q;
     a.qo = q_out;

@@ -178,34 +178,6 @@ __device__ __forceinline__ float head_inv(const RotaryDev &r, const float2 (&x)[
     return rsqrtf(s * (1.f / D) + r.eps);
 }
 
-// The lane's eight elements of one head, from its weights and the cosines and sines of its pairs (first two, last two): for
-// tokens that differ from lane to lane, where there are no coefficients to keep. The whole warp takes part.
-template <int D>
-__device__ __forceinline__ void rotate_once(const RotaryDev &r, const RotaryLane &l, const float (&w)[8], const float2 (&c)[2],
-                                            const float2 (&s)[2], float2 (&x)[4])
-{
-    if (r.norm) {
-        const float inv = head_inv<D>(r, x);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = fmul2(x[i], make_float2(w[2 * i] * inv, w[2 * i + 1] * inv));
-    }
-    if (!l.turned) return;
-    if (r.interleaved) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float cc = i & 1 ? c[i >> 1].y : c[i >> 1].x, ss = i & 1 ? s[i >> 1].y : s[i >> 1].x;
-            x[i] = ffma2(make_float2(x[i].y, x[i].x), make_float2(-ss, ss), fmul2(x[i], make_float2(cc, cc)));
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const float2 a = x[i], b = x[2 + i];
-            x[i] = ffma2(b, make_float2(-s[i].x, -s[i].y), fmul2(a, c[i]));
-            x[2 + i] = ffma2(a, s[i], fmul2(b, c[i]));
-        }
-    }
-}
-
 // The lane's eight outputs. The whole warp takes part.
 template <int DT, int D>
 __device__ __forceinline__ void rotate_eight(const RotaryDev &r, const RotaryLane &l, const Eight<DT> &raw, const RotaryCoef &k,
@@ -229,6 +201,40 @@ __device__ __forceinline__ void rotate_eight(const RotaryDev &r, const RotaryLan
     if (r.norm) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) out[i] = fmul2(out[i], make_float2(inv, inv));
+    }
+}
+
+// The same, to the bit, from a norm's weights and the cosines and sines of the lane's pairs (first two, last two): for tokens
+// that differ from lane to lane, where sixteen coefficients a token would only fill registers (7 prompts of ~2000 tokens, 8
+// heads of 128, 125 us so).
+template <int D>
+__device__ __forceinline__ void rotate_once(const RotaryDev &r, const RotaryLane &l, const float (&w)[8], const float2 (&c)[2],
+                                            const float2 (&s)[2], float2 (&x)[4])
+{
+    float inv = 1.f;
+    if (r.norm) inv = head_inv<D>(r, x);
+    if (!l.turned) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = fmul2(x[i], make_float2(w[2 * i], w[2 * i + 1]));
+    } else if (r.interleaved) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float cc = i & 1 ? c[i >> 1].y : c[i >> 1].x, ss = i & 1 ? s[i >> 1].y : s[i >> 1].x;
+            const float2 ww = make_float2(w[2 * i], w[2 * i + 1]), sw = make_float2(-w[2 * i + 1], w[2 * i]);
+            x[i] = ffma2(make_float2(x[i].y, x[i].x), fmul2(sw, make_float2(ss, ss)), fmul2(x[i], fmul2(ww, make_float2(cc, cc))));
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float2 a = x[i], b = x[2 + i];
+            const float2 wa = make_float2(w[2 * i], w[2 * i + 1]), wb = make_float2(w[4 + 2 * i], w[5 + 2 * i]);
+            x[i] = ffma2(b, fmul2(wb, make_float2(-s[i].x, -s[i].y)), fmul2(a, fmul2(wa, c[i])));
+            x[2 + i] = ffma2(a, fmul2(wa, s[i]), fmul2(b, fmul2(wb, c[i])));
+        }
+    }
+    if (r.norm) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = fmul2(x[i], make_float2(inv, inv));
     }
 }
 

@@ -24,8 +24,8 @@
  *    device, ascending from 0: sequence i's new tokens are rows tok_start[i] .. tok_start[i + 1] of
  *    the call's token arrays (n_tokens <= 2^30 rows; what lies past them is not touched, and flagged).
  *    Except for pi_kv_attend, a sequence appears at most once in a call.
- *  - A step: pi_kv_reserve once (lengths grow, pages are found), then per layer pi_kv_append and
- *    pi_kv_attend. No call allocates, synchronises or reads back: a step can be captured in a graph.
+ *  - A step: pi_kv_reserve once (lengths grow, pages are found), then per layer pi_kv_append (or
+ *    pi_kv_append_rotated) and pi_kv_attend (or pi_kv_attend_shared). No call allocates, synchronises or reads back: a step can be captured in a graph.
  */
 #ifndef PI_KV_H
 #define PI_KV_H
@@ -106,10 +106,12 @@ pi_status_t pi_kv_append(pi_kv_t *h, int32_t layer, const int32_t *seqs, const i
 
 /*
  * pi_kv_append with the norms and the rotation of pi_rotate in the same pass: the keys' heads are normed and turned by
- * their tokens' positions in the sequences (the last n_i) and then coded, from fp32; values are coded as they are; q_out
+ * their tokens' positions in the sequences (the last n_i) and then coded, from fp32 (with PI_F32 the codes are those of
+ * pi_rotate and pi_kv_append in turn); values are coded as they are; q_out
  * = the queries' heads, normed and turned. q, q_out: [n_tokens x n_heads x head_dim] of `dtype`, row t at element t *
  * ld_q (ld_q_out), bases and row strides multiples of 16 bytes; q_out is q (same address and stride) or touches no other
- * array of the call. A sequence that pi_kv_append would skip keeps its rows of q_out as they were.
+ * array of the call. A sequence that pi_kv_append would skip keeps its rows of q_out as they were (a page that is absent loses its keys and
+ * values alone).
  */
 pi_status_t pi_kv_append_rotated(pi_kv_t *h, int32_t layer, const int32_t *seqs, const int32_t *tok_start, int32_t n,
                                  int32_t n_tokens, const pi_rotary_t *rotary, const void *q, int64_t ld_q, void *q_out,
@@ -160,8 +162,8 @@ pi_status_t pi_kv_share(pi_kv_t *h, const int32_t *seqs, const int32_t *tok_star
  * through the table row of its first sequence with new tokens, what lies behind it for each sequence, and the two are joined
  * by their maxima and sums in fp32 (the output is rounded once). Same results as pi_kv_attend up to fp32 rounding and the
  * terms that many and few rows keep. plan: from pi_kv_share for the same seqs, tok_start and n_groups (a sequence
- * whose entry differs is skipped and flagged). work: fp32 device [n_tokens * n_heads * (head_dim + 2)], 16-byte
- * aligned, overwritten.
+ * whose entry differs is skipped and flagged). out may be q (same address and stride). work: fp32 device [n_tokens * n_heads * (head_dim + 2)], 16-byte
+ * aligned, overwritten; it touches no other array of the call.
  */
 pi_status_t pi_kv_attend_shared(pi_kv_t *h, int32_t layer, const int32_t *seqs, const int32_t *tok_start, int32_t n,
                                 int32_t n_tokens, const int32_t *plan, int32_t n_groups, const void *q, int64_t ld_q,

@@ -201,3 +201,45 @@ def test_refusals(P):
         b.cache.append_rotated(0, *args, r, h[:, :4], h[:, 4:6], h[:, 6:], q_out=h[:, 2:6])
     b.cache.append_rotated(0, *args, r, h[:, :4], h[:, 4:6], h[:, 6:], q_out=h[:, :4])
     assert b.cache.status() == 0 and block_scale(0.0) == float(b.ks[0, int(b.cache.table[0, 0]), 0])
+
+
+@pytest.mark.parametrize("per", [1, 6])
+def test_1024_sequences(P, per):
+    """As many sequences as a call takes, some without a new token: as rotation and append one after the other."""
+    a, b = (Both(P, hq=4, hkv=2, dim=64, page=16, n_pages=2100, max_seqs=1024, max_pages=6, seed=3) for _ in range(2))
+    r, _, _ = rotary(P, a.rng, 64, 64, norm=True, interleaved=False)
+    for turn in range(3):
+        new = [(per + i + turn) % (per + 2) for i in range(1024)]
+        seqs = [(7 * i + turn) % 1024 for i in range(1024)]
+        args = a.args(seqs, new)
+        for x in (a, b):
+            x.cache.reserve(*args)
+        pos = torch.cat([torch.arange(n - m, n) for n, m in zip(a.cache.length.cpu()[torch.tensor(seqs)].tolist(), new)])
+        q, k, v = (torch.randn((sum(new), n, 64), device="cuda") for n in (4, 2, 2))
+        qo, ko = r.rotate(pos.to(torch.int32).cuda(), q, k)
+        a.cache.append(0, *args, ko, v)
+        assert torch.equal(b.cache.append_rotated(0, *args, r, q, k, v), qo)
+        assert torch.equal(a.k.view(torch.uint8), b.k.view(torch.uint8)) and torch.equal(a.v.view(torch.uint8), b.v.view(torch.uint8))
+        assert a.cache.status() == 0 and b.cache.status() == 0
+
+
+def test_pools_past_32_bits(P):
+    """A pool of more than 2^32 bytes, the sequence's pages at its end: as in a small one."""
+    dim, page, hkv, n_pages = 256, 64, 2, 140000
+    b = Both(P, hq=4, hkv=hkv, dim=dim, page=page, n_pages=20, max_seqs=1, max_pages=14)
+    r, _, _ = rotary(P, b.rng, dim, 128, norm=True, interleaved=True)
+    b.cache.reserve(*b.args([0], [700]))
+    k, v = (torch.zeros((n_pages, hkv, page, dim), dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn) for _ in range(2))
+    ks, vs = (torch.ones((n_pages, hkv), device="cuda") for _ in range(2))
+    table = torch.arange(n_pages - 1, n_pages - 15, -1, dtype=torch.int32, device="cuda")[None].contiguous()
+    ref = torch.zeros(n_pages, dtype=torch.int32, device="cuda")
+    ref[table[0].long()] = 1
+    big = P.KVCache([dict(k=k, v=v, k_scale=ks, v_scale=vs)], table, torch.tensor([700], dtype=torch.int32, device="cuda"), ref, n_heads=4)
+    q, kn, vn = (torch.randn((700, n, dim), device="cuda") for n in (4, hkv, hkv))
+    outs = [c.append_rotated(0, *b.args([0], [700]), r, q, kn, vn) for c in (b.cache, big)]
+    assert torch.equal(*outs)
+    small = b.cache.table[0, :11].long()
+    for x, y in ((k, b.k[0]), (v, b.v[0])):
+        at, to = (z.view(torch.uint8)[p].transpose(1, 2).reshape(-1, hkv, dim)[:700] for z, p in ((x, table[0, :11].long()), (y, small)))
+        assert torch.equal(at, to)
+    assert big.status() == 0 and b.cache.status() == 0

@@ -262,6 +262,65 @@ def test_one_long_sequence_among_short_ones(P):
         b.check([0, 1, 2, 3, 4, 5, 7], [1, 1, 1, 1, 3, 1, 2], [0, 6], kind, [256])
 
 
+def test_1024_sequences_in_256_groups(P):
+    b = Shared(P, hq=2, hkv=1, dim=64, page=16, n_pages=4200, max_seqs=1024, max_pages=20)
+    lead = list(range(0, 1024, 4))
+    b.cache.reserve(*b.args(lead, [150] * 256))
+    k, v = (torch.randn((150 * 256, 1, 64), device="cuda") for _ in range(2))
+    b.cache.append(0, *b.args(lead, [150] * 256), k, v)
+    b.cache.fork(dev(np.repeat(lead, 3)), dev([s + i for s in lead for i in (1, 2, 3)]))
+    seqs, new = list(range(1024)), [1 + i % 3 for i in range(1024)]
+    args = b.args(seqs, new)
+    b.cache.reserve(*args)
+    k, v = (torch.randn((sum(new), 1, 64), device="cuda") for _ in range(2))
+    b.cache.append(0, *args, k, v)
+    plan = b.cache.share(*args, dev(range(0, 1025, 4)))
+    assert (plan[2 * 256 + 1:3 * 256 + 1] == 128).all()
+    for kind in ("f32", "bf16"):
+        q, _ = b.tokens(new, kind, 2, spread=0)
+        got, want = b.cache.attend_shared(0, *args, plan, q), b.cache.attend(0, *args, q)
+        # (values are below 6: A <= 6; one rounding and one-term weights each for 16-bit types)
+        tol = 6 * 2.2e-5 if kind == "f32" else 6 * (2 * HALF[kind] + 2 * 2.0 ** -11 + 2.2e-5)
+        assert torch.allclose(got.float(), want.float(), rtol=0, atol=tol) and b.cache.status() == 0
+
+
+def test_output_in_the_queries_place(P):
+    b = Shared(P, hq=16, hkv=2, dim=128, page=64, n_pages=120, max_seqs=8, max_pages=60)
+    b.grow([0], [2500])
+    b.fork([0] * 5, [1, 2, 3, 4, 5])
+    b.grow([0, 1, 2, 3, 4, 5], [1, 30, 900, 2, 1, 64])
+    args = b.args(range(6), [1, 1, 2, 1, 1, 40])
+    plan = b.cache.share(*args, dev([0, 6]))
+    q, _ = b.tokens([46], "bf16", 16)
+    want = b.cache.attend_shared(0, *args, plan, q)
+    assert torch.equal(b.cache.attend_shared(0, *args, plan, q, out=q), want) and b.cache.status() == 0
+
+
+def test_pools_past_32_bits(P):
+    """Prefix and what lies behind it at the end of pools of more than 2^32 bytes."""
+    dim, page, hkv, n_pages = 128, 64, 2, 270000
+    k, v = (torch.zeros((n_pages, hkv, page, dim), dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn) for _ in range(2))
+    ks, vs = (torch.ones((n_pages, hkv), device="cuda") for _ in range(2))
+    ids = torch.arange(n_pages - 1, n_pages - 31, -1, dtype=torch.int32, device="cuda")
+    table = torch.stack([torch.cat([ids[:10], ids[10 + 4 * i:14 + 4 * i]]) for i in range(5)])
+    ref = torch.bincount(table.flatten().long(), minlength=n_pages).to(torch.int32)
+    length = dev([890, 650, 700, 641, 895])
+    for pool in (k, v):
+        pool.view(torch.uint8)[ids.long()] = torch.randint(0, 0x60, (30, hkv, page, dim), device="cuda", dtype=torch.uint8)
+    ks[ids.long()] = vs[ids.long()] = 1 / 16
+    big = P.KVCache([dict(k=k, v=v, k_scale=ks, v_scale=vs)], table, length, ref, n_heads=8)
+    take = lambda x: x[ids.long()].contiguous()  # noqa: E731
+    small = P.KVCache([dict(k=take(k.view(torch.uint8)).view(torch.float8_e4m3fn), v=take(v.view(torch.uint8)).view(torch.float8_e4m3fn),
+                            k_scale=take(ks), v_scale=take(vs))], (n_pages - 1 - table).to(torch.int32).contiguous(), length.clone(),
+                      ref[ids.long()].contiguous(), n_heads=8)
+    seqs, start, groups = dev(range(5)), dev(range(6)), dev([0, 5])
+    for kind in ("bf16", "f32"):
+        q = torch.randn((5, 8, dim), device="cuda").to(TYPES[kind])
+        outs = [c.attend_shared(0, seqs, start, c.share(seqs, start, groups), q) for c in (big, small)]
+        assert torch.equal(*outs) and torch.isfinite(outs[0]).all()
+    assert big.status() == 0 and small.status() == 0
+
+
 @pytest.mark.parametrize("rows", [1, 40])
 def test_nan_in_the_prefix_reaches_all_and_behind_it_one(P, rows):
     b = Shared(P, hq=2, hkv=1, dim=64, page=16, n_pages=80, max_pages=40)
@@ -343,9 +402,11 @@ def test_refusals(P):
                dict(out=torch.empty(3, 4, 64, device="cuda")), dict(lse=torch.empty(2, 3, device="cuda"))):
         with pytest.raises(ValueError):
             b.cache.attend_shared(0, *args, plan, q, **kw)
+    room = torch.zeros(2 * 4 * 66, device="cuda")                               # work over the queries
     for call in (lambda: b.cache.attend_shared(1, *args, plan, q), lambda: b.cache.attend_shared(0, *args, plan, q.double()),
                  lambda: b.cache.attend_shared(0, *args, plan, q, scale=float("nan")),
-                 lambda: b.cache.attend_shared(0, *args, plan, q, work=torch.empty(2 * 4 * 66 + 1, device="cuda")[1:])):
+                 lambda: b.cache.attend_shared(0, *args, plan, q, work=torch.empty(2 * 4 * 66 + 1, device="cuda")[1:]),
+                 lambda: b.cache.attend_shared(0, *args, plan, room[:512].view(2, 4, 64), work=room)):
         with pytest.raises(P.PiError):
             call()
     none = dev([])

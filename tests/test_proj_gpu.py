@@ -159,6 +159,38 @@ def test_int4_linear_on_another_stream(P):
         assert torch.equal(z, y)
 
 
+def test_int4_linear_two_streams_at_once(P):
+    """Nothing is shared between calls: many under way on two streams."""
+    rng = np.random.default_rng(7)
+    calls = [check_linear(P, rng, rows, n, k, kind, add=None) for rows, n, k, kind in
+             [(1, 3000, 4096, "bf16"), (16, 2000, 5120, "f32"), (3, 500, 12288, "f32"), (40, 700, 1024, "f16")]]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    outs = []
+    for i in range(40):
+        for j, s in enumerate(streams):
+            lin, x, want = calls[(i + j) % 4]
+            outs.append((lin(x, stream=s), want))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in outs)
+
+
+def test_int4_linear_offsets_past_32_bits(P):
+    """More than 2^32 bytes of weights: the last outputs against fp64."""
+    n, k = 300001, 32768
+    w = torch.randint(0, 256, (n, k // 2), device="cuda", dtype=torch.uint8)
+    s = torch.rand((n, k // 128), device="cuda").half()
+    assert w.numel() > 2 ** 32
+    for rows, kind in ((1, "f32"), (9, "bf16")):
+        x = torch.randn((rows, k), device="cuda").to(TYPES[kind])
+        y = P.Int4Linear(w, s)(x)
+        for at in (0, 131071, n - 40):
+            v = plain.int4_values(w[at:at + 40].cpu().numpy(), s[at:at + 40].cpu().numpy())
+            want, size = num(x) @ v.T, np.abs(num(x)) @ np.abs(v).T
+            tol = size * (2.0 ** -19 + 2.0 ** -21 + (k // 128 + 3) * 2.0 ** -24) + HALF[kind] * np.abs(want)
+            assert (np.abs(num(y[:, at:at + 40]) - want) <= tol).all()
+
+
 def test_int4_linear_refusals(P):
     rng = np.random.default_rng(6)
     w, s = (torch.tensor(a, device="cuda") for a in weights(rng, 8, 256))
@@ -347,6 +379,9 @@ def test_rotate_refusals(P):
         P.Rotary(P.rotary_frequencies(64), 64, q_norm=torch.ones(64, device="cuda"))
     with pytest.raises(ValueError):
         P.Rotary(P.rotary_frequencies(64), 64, norm=True, k_norm=torch.ones(32, device="cuda"))
+    flat = torch.zeros(4 * 256, device="cuda")
+    with pytest.raises(P.PiError):                                   # the positions lie in the output
+        r.rotate(flat[8:12].view(torch.int32), q, q_out=flat.view(4, 4, 64))
     odd = torch.zeros(4 * 256 + 8, device="cuda")
     with pytest.raises(P.PiError):
         r.rotate(pos, odd[1:1025].view(4, 4, 64))
