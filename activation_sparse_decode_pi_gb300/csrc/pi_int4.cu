@@ -7,68 +7,30 @@
 //  - products on mma.sync m16n8k16, 16 rows of W against up to 8 rows of x: 16 bytes of a row of W to a lane are 32
 //    nibbles, four lanes' a group. The contraction may run in any order that both operands share, so nibbles are used
 //    as they lie: a word's nibbles (i, i + 4) become an f16 pair by one mask, as subnormals, and x is laid into shared
-//    memory in that order. (tcgen05 products want 128 rows and both operands in shared memory: the f16 weights would be
-//    written there and read again, four bytes for every half that comes in.)
+//    memory in that order. (pi_int4_rows.cu has tcgen05 products, whose hand-offs cost more than these up to 8 rows of fp32 or
+//    16 of 16 bits.)
 //  - x is cut to f16 in units of a power of two for each row and group (fp32: two terms), undone in fp32 with the
 //    weights' scale, so a group's sum is of whole numbers times f16 and nothing else is rounded before fp32;
 //  - one CTA to an SM stays and goes through tiles of W, x resident. Its 16 warps split a tile's rows and the
 //    contraction (kw ways); CTAs of a cluster split the contraction further, where x is too large for one or the tiles are
 //    few, and add their sums through distributed shared memory in the order of their ranks.
 // Measured, one row (graph of calls back to back): 12288 -> 36864 bf16 44 us = 5.3 TB/s, fp32 52 us (second terms: twice the
-// products), 4096 -> 6144 bf16 7.0 us (launch, x, one tile and its sums in turn). 5120 -> 15360: 8 rows fp32 19 us, 16 rows
-// 29 us, 64 rows 153 us: from 9 rows on the products (mma.sync gives 1024 a cycle and SM) and the cluster's sums bound it.
+// products), 4096 -> 6144 bf16 7.0 us (launch, x, one tile and its sums in turn). 5120 -> 15360: 8 rows fp32 19 us, 16
+// rows bf16 24 us: there the products (mma.sync gives 1024 a cycle and SM) and the cluster's sums bound it.
 #include <cooperative_groups.h>
 
 #include <algorithm>
 
-#include "pi_proj_internal.h"
-#include "pi_kv_device.cuh"
+#include "pi_int4.cuh"
 
 namespace pi {
 
 namespace cg = cooperative_groups;
 
 constexpr int I4_NT = 512, I4_NW = I4_NT / 32;
-constexpr int I4_GROUP = 128;
-constexpr int I4_SMEM = 227 * 1024;    // of a CTA, one to an SM
 constexpr double I4_TILE_US = 0.5, I4_CLUSTER_US = 1.0, I4_X_US = 0.01;   // of the estimate below (measured)
 constexpr int I4_BOX = 32 * 128;       // bytes of a box: 32 rows of W, two groups
 constexpr int I4_SLOTS = 3;            // places for boxes of a warp, at most
-
-// The eight nibbles of a word as f16 pairs (i, i + 4): a nibble in the low bits of a half is the subnormal (q + 8) 2^-24
-// (flipping its top bit turns two's complement into offset binary), one in bits 4..7 the subnormal (q + 8) 2^-20. So pairs
-// 1 and 3 are 16 times as large as 0 and 2, which their x makes up for, and the offset is taken off each group's sum.
-__device__ __forceinline__ void i4_word_h2(uint32_t w, uint32_t (&p)[4])
-{
-    const uint32_t w8 = w >> 8;
-    p[0] = lop3_and_xor(w, 0x000F000Fu, 0x00080008u);
-    p[1] = lop3_and_xor(w, 0x00F000F0u, 0x00800080u);
-    p[2] = lop3_and_xor(w8, 0x000F000Fu, 0x00080008u);
-    p[3] = lop3_and_xor(w8, 0x00F000F0u, 0x00800080u);
-}
-
-// Element k of row i by the plain definition: for rows of x with an infinity or NaN, where an offset's product is none.
-template <int DT>
-__device__ __noinline__ float plain_dot(const Int4Args &a, int64_t x_at, int i)
-{
-    const int G = a.k / I4_GROUP;
-    float v = 0.f;
-    for (int gr = 0; gr < G; ++gr) {
-        float d = 0.f;
-        for (int e = 0; e < I4_GROUP; ++e) {
-            const int k = gr * I4_GROUP + e;
-            const uint32_t byte = a.w[(size_t)i * (a.k / 2) + k / 2];
-            const float q = (float)((int)((k & 1 ? byte >> 4 : byte & 15u) ^ 8u) - 8);
-            float x;
-            if constexpr (DT == DT_F32) x = ((const float *)a.x)[x_at + k];
-            else if constexpr (DT == DT_BF16) x = __bfloat162float(((const __nv_bfloat16 *)a.x)[x_at + k]);
-            else x = __half2float(((const __half *)a.x)[x_at + k]);
-            d = fmaf(q, x, d);
-        }
-        v = fmaf(d, __half2float(a.s[(size_t)i * G + gr]), v);
-    }
-    return v;
-}
 
 // NT: runs of 8 rows of x.
 template <int DT, int NT>
@@ -141,68 +103,12 @@ __global__ void __launch_bounds__(I4_NT, 1) k_int4_linear(const __grid_constant_
     };
     uint32_t s0 = scale(), s1 = scale();
 
-    // x: a warp to a row's group, four elements to a lane, four groups' loads under way at a time
-    constexpr int S = 4;
-    for (int it0 = warp; it0 < gn * nb; it0 += S * I4_NW) {
-        float f[S][4];
-#pragma unroll
-        for (int y = 0; y < S; ++y) {
-            const int it = it0 + y * I4_NW, gl = it / nb, b = it - gl * nb;
-            if (it >= gn * nb) break;
-            const int64_t at = (int64_t)(b0 + b) * a.ldx + (int64_t)(g_lo + gl) * I4_GROUP + lane * 4;
-            if constexpr (DT == DT_F32) {
-                const float4 v = *(const float4 *)((const float *)a.x + at);
-                f[y][0] = v.x, f[y][1] = v.y, f[y][2] = v.z, f[y][3] = v.w;
-            } else {
-                const uint2 v = *(const uint2 *)((const uint16_t *)a.x + at);
-                if constexpr (DT == DT_BF16) {
-                    f[y][0] = __uint_as_float(v.x << 16), f[y][1] = __uint_as_float(v.x & 0xffff0000u);
-                    f[y][2] = __uint_as_float(v.y << 16), f[y][3] = __uint_as_float(v.y & 0xffff0000u);
-                } else {
-                    const float2 lo = __half22float2(u32_h2(v.x)), hi = __half22float2(u32_h2(v.y));
-                    f[y][0] = lo.x, f[y][1] = lo.y, f[y][2] = hi.x, f[y][3] = hi.y;
-                }
-            }
-        }
-        float top[S];
-#pragma unroll
-        for (int y = 0; y < S; ++y)
-            top[y] = fmaxf(fmaxf(finite_abs(f[y][0]), finite_abs(f[y][1])), fmaxf(finite_abs(f[y][2]), finite_abs(f[y][3])));
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-            for (int y = 0; y < S; ++y) top[y] = fmaxf(top[y], __shfl_xor_sync(0xffffffffu, top[y], o));
-#pragma unroll
-        for (int y = 0; y < S; ++y) {
-            const int it = it0 + y * I4_NW, gl = it / nb, b = it - gl * nb;
-            if (it >= gn * nb) break;
-            // 2^ex <= top < 2^(ex + 1): the largest lies in [2^11, 2^12) (zeros and the smallest numbers below)
-            const int ex = max((int)(__float_as_uint(top[y]) >> 23) - 127, -116);
-            const float mul = exp2i(11 - ex);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) f[y][e] *= e & 1 ? mul * 0.0625f : mul;   // (pairs 1 and 3: nibbles 16 times as large)
-            // a word's elements 0..3 lie in an even lane, 4..7 in the next: the even lane takes pairs (0, 4) and (1, 5)
-            const bool odd = lane & 1;
-            const float p0 = __shfl_xor_sync(0xffffffffu, odd ? f[y][0] : f[y][2], 1);
-            const float p1 = __shfl_xor_sync(0xffffffffu, odd ? f[y][1] : f[y][3], 1);
-            const float x0 = odd ? p0 : f[y][0], y0 = odd ? f[y][2] : p0, x1 = odd ? p1 : f[y][1], y1 = odd ? f[y][3] : p1;
-            const int word = (lane >> 1) & 3, qq = lane >> 3;
-            uint8_t *const to = frag + ((gl * 4 + word) * T * nb + b) * 64 + qq * 16 + odd * 8;
-            const uint32_t h0 = pack_f16(x0, y0), h1 = pack_f16(x1, y1);
-            const float2 c0 = __half22float2(u32_h2(h0)), c1 = __half22float2(u32_h2(h1));
-            float sum = (c0.x + c0.y) + 16.f * (c1.x + c1.y);   // of the terms that the products take
-            *(uint2 *)to = make_uint2(h0, h1);
-            if constexpr (T == 2) {
-                const uint32_t l0 = pack_f16(x0 - c0.x, y0 - c0.y), l1 = pack_f16(x1 - c1.x, y1 - c1.y);
-                const float2 r0 = __half22float2(u32_h2(l0)), r1 = __half22float2(u32_h2(l1));
-                sum += (r0.x + r0.y) + 16.f * (r1.x + r1.y);
-                *(uint2 *)(to + 64 * nb) = make_uint2(l0, l1);
-            }
-            sum = warp_sum(sum);
-            const float unit = exp2i(ex);
-            if (lane == 0) xf[gl * (8 * NT) + b] = make_float2(unit, -8.f * 0x1p-24f * sum * unit);
-        }
-    }
+    i4_take_x<DT, 4>(a, b0, nb, g_lo, gn, warp, I4_NW, lane,
+                  [&](int gl, int b, int term, uint2 v) {
+                      const int word = (lane >> 1) & 3, qq = lane >> 3;
+                      *(uint2 *)(frag + ((gl * 4 + word) * T * nb + b) * 64 + qq * 16 + (lane & 1) * 8 + term * 64 * nb) = v;
+                  },
+                  [&](int gl, int b, float unit, float off) { xf[gl * (8 * NT) + b] = make_float2(unit, off); });
     __syncthreads();
 
     // Row g of a product is row ((g & 1) << 2 | g >> 1) of a box (and 8 + that): so eight lanes' reads, two rows' halves, lie
@@ -282,21 +188,6 @@ __global__ void __launch_bounds__(I4_NT, 1) k_int4_linear(const __grid_constant_
         if (cs > 1) cl.sync();
         else __syncthreads();
     };
-    auto store = [&](float v, int b, int i) {   // row b of x, row i of W
-        if (v != v) v = plain_dot<DT>(a, (int64_t)(b0 + b) * a.ldx, i);
-        if (a.bias) v += a.bias[i];
-        const int64_t at = (int64_t)(b0 + b) * a.ldy + i, at_add = (int64_t)(b0 + b) * a.ldadd + i;
-        if constexpr (DT == DT_F32) {
-            if (a.add) v += ((const float *)a.add)[at_add];
-            ((float *)a.y)[at] = v;
-        } else if constexpr (DT == DT_BF16) {
-            if (a.add) v += __bfloat162float(((const __nv_bfloat16 *)a.add)[at_add]);
-            ((__nv_bfloat16 *)a.y)[at] = __float2bfloat16_rn(v);
-        } else {
-            if (a.add) v += __half2float(((const __half *)a.add)[at_add]);
-            ((__half *)a.y)[at] = __float2half_rn(v);
-        }
-    };
     int slot = 0;
     uint32_t parity = 0;
     bool dead = false;
@@ -329,7 +220,7 @@ __global__ void __launch_bounds__(I4_NT, 1) k_int4_linear(const __grid_constant_
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const int i = tile * R + wm * 32 + m * 16 + (e >> 1) * 8 + rg, b = 8 * n + 2 * q + (e & 1);
-                        if (b < nb && i < a.n) store(tot[m][n][e], b, i);
+                        if (b < nb && i < a.n) i4_store<DT>(a, tot[m][n][e], b0 + b, i);
                     }
         } else {
             if (tile != tile0) meet();   // the last tile's sums have been read
@@ -352,7 +243,7 @@ __global__ void __launch_bounds__(I4_NT, 1) k_int4_linear(const __grid_constant_
                     const float *from = cs > 1 ? cl.map_shared_rank(red, c) : red;
                     for (int y = 0; y < kw; ++y) v += from[(y * (8 * NT) + b) * (R + 1) + r];
                 }
-                store(v, b, i);
+                i4_store<DT>(a, v, b0 + b, i);
             }
         }
         clear();
@@ -363,14 +254,6 @@ __global__ void __launch_bounds__(I4_NT, 1) k_int4_linear(const __grid_constant_
 }
 
 namespace {
-
-// Clusters of cs CTAs, one to an SM, that run at a time. A cluster's SMs lie in one group of the GPU's SMs, so 152 SMs hold
-// (by the runtime's count) 15 of 8 and not 19.
-int clusters_at_once(int nsm, int cs)
-{
-    constexpr int of_152[8] = {152, 76, 46, 36, 28, 23, 15, 15};
-    return std::max(1, of_152[cs - 1] * nsm / 152);
-}
 
 struct Int4Plan {
     int kw, cluster, rows_per, slots;
@@ -415,9 +298,9 @@ cudaError_t launch_dt(const Int4Args &a, const CUtensorMap &map, int nsm, cudaSt
     const int G = a.k / I4_GROUP, T = DT == DT_F32 ? 2 : 1;
     Int4Plan p = {};
     // rows of x that a CTA keeps: what 8 CTAs' shared memory holds of their whole length
-    const int fit = (int)std::min<int64_t>(32, (int64_t)(I4_SMEM - I4_NW * I4_BOX - 72 * 1024) / ((int64_t)(G + 7) / 8 * 256 * T));
+    const int fit = (int)std::min<int64_t>(T == 2 ? 8 : 16, (int64_t)(I4_SMEM - I4_NW * I4_BOX - 72 * 1024) / ((int64_t)(G + 7) / 8 * 256 * T));
     p.rows_per = std::min(a.rows, std::max(1, fit));
-    const int nt = p.rows_per <= 8 ? 1 : p.rows_per <= 16 ? 2 : 4;
+    const int nt = p.rows_per <= 8 ? 1 : 2;
     const int slices = (a.rows + p.rows_per - 1) / p.rows_per;
     // The fastest by an estimate: rounds of tiles, each as long as its bytes of W take (45 bytes a nanosecond to an SM), or
     // its products (16 NT T of 8 cycles to a warp's group, four warps to a scheduler), or a box's latency; and what a
@@ -446,15 +329,19 @@ cudaError_t launch_dt(const Int4Args &a, const CUtensorMap &map, int nsm, cudaSt
             }
         }
     if (p.cluster == 0) return cudaErrorInvalidConfiguration;
-    return nt == 1   ? launch_of<DT, 1>(a, p, map, nsm, s)
-           : nt == 2 ? launch_of<DT, 2>(a, p, map, nsm, s)
-                     : launch_of<DT, 4>(a, p, map, nsm, s);
+    if constexpr (DT != DT_F32)
+        if (nt == 2) return launch_of<DT, 2>(a, p, map, nsm, s);
+    return launch_of<DT, 1>(a, p, map, nsm, s);
 }
 
 }  // namespace
 
 cudaError_t launch_int4_linear(const Int4Args &a, int dtype, int nsm, cudaStream_t s)
 {
+    // From 9 rows of fp32 (two terms) or 17 of 16 bits on the other kernel is faster, measured here against there: 16 rows of
+    // fp32 5120 -> 15360 28.3 against 28.6 us, 12288 -> 36864 223 against 98; 16 of bf16 23.7 against 30.9, 24 36.0 against 30.8.
+    cudaError_t e;
+    if (a.rows > (dtype == DT_F32 ? 8 : 16) && launch_int4_rows(a, dtype, nsm, s, &e)) return e;
     // W as rows of k / 2 bytes; boxes of 32 rows and 128 bytes, swizzled. What lies past its edges reads as zeros.
     CUtensorMap map;
     const cuuint64_t dims[2] = {(cuuint64_t)a.k / 2, (cuuint64_t)a.n}, strides[1] = {(cuuint64_t)a.k / 2};

@@ -248,8 +248,10 @@ cudaError_t launch_of(const KvAppendRotArgs &in, int nsm, cudaStream_t s)
 template <int DT, int D>
 cudaError_t launch_w(const KvAppendRotArgs &a, int nsm, cudaStream_t s)
 {
-    // four loads at a time where sequences bring 4 tokens or more on average: fewer have no more than one to a thread
-    return a.b.n_tokens >= 4 * (int64_t)a.b.n ? launch_of<DT, D, 4>(a, nsm, s) : launch_of<DT, D, 1>(a, nsm, s);
+    // Several loads at a time where sequences bring 4 tokens or more on average: fewer have no more than one to a thread.
+    // Four of 16 bits; two of fp32, of which four spill (7 prompts of ~2000 tokens 161 us with four, 132 with two).
+    constexpr int U = DT == DT_F32 ? 2 : 4;
+    return a.b.n_tokens >= 4 * (int64_t)a.b.n ? launch_of<DT, D, U>(a, nsm, s) : launch_of<DT, D, 1>(a, nsm, s);
 }
 
 template <int DT>

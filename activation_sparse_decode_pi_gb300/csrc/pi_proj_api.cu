@@ -69,7 +69,7 @@ pi_status_t pi_int4_linear(const void *w, const void *s, const float *bias, int3
 {
     const int es = elt_size(dtype);
     if (n < 1 || k < 1 || rows < 0 || rows > PI_INT4_MAX_ROWS || !es) return PI_ERR_INVALID_ARG;
-    if (k % 128 || k > INT4_MAX_K) return PI_ERR_UNSUPPORTED;
+    if (k % 128 || k > INT4_MAX_K || n > INT4_MAX_N) return PI_ERR_UNSUPPORTED;
     if (rows == 0) return PI_OK;
     const int64_t nw = (int64_t)n * (k / 2), ns = (int64_t)n * (k / 128) * 2;
     const int64_t nx = extent(rows, k, ld_x, es), ny = extent(rows, n, ld_y, es), na = add ? extent(rows, n, ld_add, es) : 0;

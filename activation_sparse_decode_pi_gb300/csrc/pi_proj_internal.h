@@ -47,6 +47,7 @@ struct Int4Args {
 };
 cudaError_t launch_int4_linear(const Int4Args &a, int dtype, int nsm, cudaStream_t s);   // k <= INT4_MAX_K
 constexpr int INT4_MAX_K = 1 << 18;   // a row of x in the shared memory of a cluster
+constexpr int INT4_MAX_N = 1 << 30;   // rows of tiles are counted in 32 bits
 
 struct RotaryDev {
     const uint64_t *turns;

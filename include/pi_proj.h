@@ -21,7 +21,7 @@ extern "C" {
 
 /*
  * y = x W^T (+ bias) (+ add):  y[b, i] = sum_k x[b, k] W[i, k] + bias[i] + add[b, i].
- * W: PI_INT4_G128 as in pi_ffn.h, n rows of k elements, k a multiple of 128 up to 2^18: w [n x k/2] bytes (16-byte aligned), s
+ * W: PI_INT4_G128 as in pi_ffn.h, n rows (up to 2^30) of k elements, k a multiple of 128 up to 2^18: w [n x k/2] bytes (16-byte aligned), s
  * fp16 [n x k/128], the value q * s of its group. bias: fp32 [n] or NULL. x [rows x k], add and y [rows x n] of `dtype`
  * (PI_F32, PI_BF16 or PI_F16), row b at element b * ld of its array; x's base and row stride are multiples of 16 bytes,
  * those of add and y multiples of the element. 0 <= rows <= PI_INT4_MAX_ROWS. add: NULL, or y itself (same address

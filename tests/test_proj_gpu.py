@@ -191,6 +191,47 @@ def test_int4_linear_offsets_past_32_bits(P):
             assert (np.abs(num(y[:, at:at + 40]) - want) <= tol).all()
 
 
+@pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("rows,n,k", [(17, 40000, 640), (40, 20000, 1280), (64, 30000, 384), (100, 5000, 2048), (200, 300, 5120),
+                                      (33, 129, 12288), (48, 700, 128 * 257), (18, 40, 1 << 18)])
+def test_int4_linear_many_rows(P, rows, n, k, kind):
+    """Many tiles to a CTA, shares of the contraction of every parity, several slices of the rows, the longest contraction."""
+    lin, x, y = check_linear(P, np.random.default_rng(rows), rows, n, k, kind, add=None)
+    assert torch.equal(lin(x), y)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_int4_linear_infinite_and_nan_inputs_among_many_rows(P, kind):
+    rng = np.random.default_rng(8)
+    w, s = weights(rng, 300, 1024)
+    w[w == 0] = 0x11
+    w[:, 50] = 0x23
+    lin = P.Int4Linear(torch.tensor(w, device="cuda"), torch.tensor(s, device="cuda"))
+    x = wide(rng, 40, 1024, kind)
+    clean = lin(x)
+    x[4, 100], x[37, 300], x[39, 101] = float("inf"), float("nan"), -float("inf")
+    y = lin(x)
+    keep = [i for i in range(40) if i not in (4, 37, 39)]
+    assert torch.equal(y[keep], clean[keep])
+    assert (y[4] == float("inf")).all() and torch.isnan(y[37]).all() and (y[39] == -float("inf")).all()
+
+
+def test_int4_linear_many_rows_two_streams_at_once(P):
+    """CTAs of two calls with clusters, side by side: each SM has one call's tensor memory at a time."""
+    rng = np.random.default_rng(9)
+    calls = [check_linear(P, rng, rows, n, k, kind, add=None) for rows, n, k, kind in
+             [(20, 3000, 1024, "bf16"), (30, 20000, 512, "f32"), (64, 2000, 5120, "f16")]]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    outs = []
+    for i in range(30):
+        for j, st in enumerate(streams):
+            lin, x, want = calls[(i + j) % 3]
+            outs.append((lin(x, stream=st), want))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in outs)
+
+
 def test_int4_linear_refusals(P):
     rng = np.random.default_rng(6)
     w, s = (torch.tensor(a, device="cuda") for a in weights(rng, 8, 256))
