@@ -8,9 +8,13 @@
 //    four to each group of a box;
 //  - one thread issues a group's products, 128 x NP x 128, into an accumulator of the group's own;
 //  - 8 warps, a thread to a row and half of the rows of x, read it and add it times the group's scale to the row's fp32 sums.
-// Four to six groups are under way between these. CTAs of a cluster share the contraction, and send each other the sums of
+// Five or six groups are under way between these. CTAs of a cluster share the contraction, and send each other the sums of
 // a tile: each adds up its part of the tile's rows in the order of
 // the ranks, a tile later, when they have long come.
+// Measured (5120 -> 15360): 16 rows fp32 25 us, 32 bf16 36, 64 fp32 48, 64 bf16 50; 12288 -> 36864: 32 bf16 122, 32 fp32 194.
+// Neither the tensor pipe nor issue slots bound it but the hand-offs: with one product of eight it takes as long, and of a
+// group's 750 cycles the warps of the sums work 380, on a wait, a load, 8 to 16 sums and an arrival in turn, and a tile's
+// exchange costs 2600. Bringing in x is 3 to 5 us.
 #include <cooperative_groups.h>
 
 #include "pi_int4.cuh"
@@ -24,13 +28,14 @@ constexpr int IR_ACC = 8, IR_COPY = IR_ACC + 8, IR_MMA = IR_COPY + 1, IR_NT = 32
 constexpr int IR_BOX = 128 * 128;   // bytes of a box: 128 rows of W, two groups
 constexpr int IR_SLOTS = 4;         // places for boxes, at most
 constexpr int IR_COLS = 512;
+constexpr double IR_GROUP_US = 0.2, IR_TILE_US = 0.7, IR_X_US = 0.02;   // of the estimate below (measured)
 // Of a CTA, at least: one to an SM. Two would wait for each other's tensor memory, and with their clusters' barriers for ever.
 constexpr size_t IR_SMEM_MIN = 120 * 1024;
 
 // NP: columns of the products, at least the rows of x that a CTA has.
 template <int NP>
 struct IrCfg {
-    static constexpr int STAGES = NP == 64 ? 4 : NP == 32 ? 5 : 6;    // groups under way: 64 columns of weights each, NP of sums
+    static constexpr int STAGES = NP == 32 ? 5 : 6;    // groups under way: 64 columns of weights each, NP of sums
     static_assert(STAGES * (64 + NP) <= IR_COLS);
 };
 
@@ -186,8 +191,7 @@ __global__ void __launch_bounds__(IR_NT, 1) k_int4_rows(const __grid_constant__ 
                     tc_fence_after();
                     uint32_t d[H];
                     if constexpr (H == 8) tmem_ld8u(from + st * NP, d);
-                    else if constexpr (H == 16) tmem_ld16u(from + st * NP, d);
-                    else tmem_ld32(from + st * NP, d);
+                    else tmem_ld16u(from + st * NP, d);
                     tmem_wait_ld(d);
                     tc_fence_before();
                     __syncwarp();
@@ -346,13 +350,14 @@ template <int DT>
 bool launch_dt(const Int4Args &a, int nsm, cudaStream_t s, cudaError_t *e)
 {
     const int G = a.k / I4_GROUP, T = DT == DT_F32 ? 2 : 1, tiles = (a.n + 127) / 128;
-    // The fastest by an estimate: rounds of tiles, each of its groups and its sums, behind bringing in x.
+    // The fastest by an estimate: rounds of tiles, each of its groups and its sums, behind bringing in x. (Up to 32 rows: with 64
+    // columns the sums' registers spill, 64 rows of bf16 5120 -> 15360 59.8 us where two slices of 32 take 49.8.)
     RowsPlan p = {};
     double best = 0;
     int np = 0;
-    for (int slices = (a.rows + 63) / 64; slices <= (a.rows + 7) / 8; ++slices)
+    for (int slices = (a.rows + 31) / 32; slices <= (a.rows + 7) / 8; ++slices)
         for (int cs = 1; cs <= 8; cs *= 2) {
-            const int per = (a.rows + slices - 1) / slices, r8 = (per + 7) / 8 * 8, cols = per <= 16 ? 16 : per <= 32 ? 32 : 64;
+            const int per = (a.rows + slices - 1) / slices, r8 = (per + 7) / 8 * 8, cols = per <= 16 ? 16 : 32;
             const int groups = (G + cs - 1) / cs;
             if (cs > G) continue;
             const size_t rest = (size_t)groups * (T * 256 * r8 + 8 * cols) + (cols - r8) * 128 + (cs > 1 ? 2 * 128 * 4 * r8 : 0);
@@ -360,8 +365,7 @@ bool launch_dt(const Int4Args &a, int nsm, cudaStream_t s, cudaError_t *e)
             const int slots = std::min<int>(IR_SLOTS, (int)((I4_SMEM - sizeof(RowsBars) - rest) / IR_BOX));
             const int at_once = std::max(1, clusters_at_once(nsm, cs) / slices);
             const int64_t rounds = (tiles + at_once - 1) / at_once;
-            const double group_us = cols == 64 ? 0.28 : 0.2;
-            const double us = rounds * (groups * group_us + (cs > 1 ? 1.0 : 0.3)) + groups * per * 0.012;
+            const double us = rounds * (groups * IR_GROUP_US + (cs > 1 ? IR_TILE_US : 0.0)) + groups * per * IR_X_US;
             if (p.cluster == 0 || us < best) {
                 best = us;
                 p = RowsPlan{cs, per, slots, (slots * (size_t)IR_BOX + rest + 7) / 8 * 8};
@@ -378,9 +382,7 @@ bool launch_dt(const Int4Args &a, int nsm, cudaStream_t s, cudaError_t *e)
                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         *e = cudaErrorUnknown;
     else
-        *e = np == 16   ? launch_of<DT, 16>(a, p, map, nsm, s)
-             : np == 32 ? launch_of<DT, 32>(a, p, map, nsm, s)
-                        : launch_of<DT, 64>(a, p, map, nsm, s);
+        *e = np == 16 ? launch_of<DT, 16>(a, p, map, nsm, s) : launch_of<DT, 32>(a, p, map, nsm, s);
     return true;
 }
 
