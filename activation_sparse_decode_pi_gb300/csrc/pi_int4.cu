@@ -339,7 +339,8 @@ cudaError_t launch_dt(const Int4Args &a, const CUtensorMap &map, int nsm, cudaSt
 cudaError_t launch_int4_linear(const Int4Args &a, int dtype, int nsm, cudaStream_t s)
 {
     // From 9 rows of fp32 (two terms) or 17 of 16 bits on the other kernel is faster, measured here against there: 16 rows of
-    // fp32 5120 -> 15360 28.3 against 25.0 us, 12288 -> 36864 223 against 98; 16 of bf16 23.7 against 30.9, 24 36.0 against 30.8.
+    // fp32 5120 -> 15360 28.3 against 25.0 us, 12288 -> 36864 223 against 98; 16 of bf16
+    // 23.5 against 25.9 and 75 against 85, 24 36.0 against 30.8 us.
     cudaError_t e;
     if (a.rows > (dtype == DT_F32 ? 8 : 16) && launch_int4_rows(a, dtype, nsm, s, &e)) return e;
     // W as rows of k / 2 bytes; boxes of 32 rows and 128 bytes, swizzled. What lies past its edges reads as zeros.
