@@ -127,14 +127,14 @@ cudaError_t attend_of(const pi_kv *h, int layer, KvAttendArgs a, cudaStream_t s)
             b.part_ml = h->short_ml;
             b.tickets = h->short_tickets;
             const CUtensorMap &bk = h->box_k[layer], &bv = h->box_v[layer];
-            e = a.dtype == PI_BF16 ? short_launch<D, 1>(b, bk, bv, h->nsm, s) : short_launch<D, 2>(b, bk, bv, h->nsm, s);
+            e = a.dtype == PI_F32 ? short_launch<D, 2>(b, bk, bv, h->nsm, s) : short_launch<D, 1>(b, bk, bv, h->nsm, s);
             done = true;
         }
     if (few && !done) {
         // 16 rows to a tile where the rows of a sequence (on average: all that the host knows) fill more than 8: the cache
         // is then read once instead of twice (64 sequences, 16 heads to a group: 229 / 323 us with 16 / 8; 8 heads, 128
         // sequences: 381 / 330 us, since 16 leave room for fewer warps)
-        const bool wide = (many && !SHARED) || rows > 8 * n, one = a.dtype == PI_BF16;
+        const bool wide = (many && !SHARED) || rows > 8 * n, one = a.dtype == PI_BF16 && !SHARED;
         const auto run = wide ? (one ? split_launch<D, 2, 1, SHARED> : split_launch<D, 2, 2, SHARED>)
                               : (one ? split_launch<D, 1, 1, SHARED> : split_launch<D, 1, 2, SHARED>);
         e = run(a, h->map_k[layer], h->map_v[layer], h->nsm, s);

@@ -78,7 +78,7 @@ cudaError_t split_launch(const KvAttendArgs &a, const CUtensorMap &mk, const CUt
 PI_KV_SPLIT(extern, 64, false) PI_KV_SPLIT(extern, 128, false) PI_KV_SPLIT(extern, 256, false)
 PI_KV_SPLIT(extern, 64, true) PI_KV_SPLIT(extern, 128, true) PI_KV_SPLIT(extern, 256, true)
 
-// The rows kernel (pi_kv_rows.cuh): QT 16-bit terms of queries and weights. items: an upper bound of the
+// The rows kernel (pi_kv_rows.cuh): QT 16-bit terms of queries, and of weights (SHARED: two of these). items: an upper bound of the
 // call's (sequence, kv head, run of rows_per_item rows); splits: parts of each item's cache.
 constexpr int rows_per_item(int dim, bool few = false) { return dim == 256 || few ? 128 : 256; }
 template <int D, int QT, bool SHARED, bool FEW>
@@ -95,7 +95,7 @@ PI_KV_ROWS_FEW(extern, 64) PI_KV_ROWS_FEW(extern, 128)
 PI_KV_ROWS(extern, 64, false) PI_KV_ROWS(extern, 128, false) PI_KV_ROWS(extern, 256, false)
 PI_KV_ROWS(extern, 64, true) PI_KV_ROWS(extern, 128, true) PI_KV_ROWS(extern, 256, true)
 
-// The kernel of few rows behind a shared prefix (pi_kv_short.cuh): head dims 64 and 128, T 16-bit terms, maps of 16-row
+// The kernel of few rows behind a shared prefix (pi_kv_short.cuh): head dims 64 and 128, T 16-bit terms of queries, maps of 16-row
 // boxes. part, part_ml and
 // tickets: [2 * grid][8][dim], [2 * grid][8][2] and [grid] for a grid of SHORT_CTAS * nsm at most.
 constexpr int SHORT_CTAS = 4;

@@ -18,13 +18,14 @@
 // 918 TFLOP/s of the visible pairs (tensor pipe 41% active: the hand-offs between conversion, products and
 // softmax bound it); one prompt of 8191 in a window of 1000 + 70, 32 heads, fp16 282 us.
 // A shared prefix's rows (SHARED, first pass) are all of its sequences' and all see all of it; its parts are left for the second
-// pass (512 rows over 16384 positions, 8 heads of 128, bf16 50 us; 36 rows over 300..6000, 8 x 40 heads, fp16 144 us: a
-// tile takes about 2.7 us however few its rows are).
+// pass.
 // Rounding: as in pi_kv_split.cuh: q as f16 scaled per row by a power of two, weights as f16 in
 // units of 2^-7 of a reference that trails the running maximum by at most 2^8 (floor 2^-31 of the
 // row's largest weight). QT = 2 (fp32 output): a second f16 term of both. QT = 1: 11 bits of the weight, for fp16
 // outputs as for bf16: on the windowed prompt the error against 64 bits is 2.7e-4, 2.1e-4 of it the output's rounding;
-// a second term would double the second product and halve the tile.
+// a second term would double the second product and halve the tile. Passes over and behind shared prefixes keep two terms
+// of a weight (WT) in every type: with one the fp16 output's error was 2.8e-4 on 8 groups of 9 samples. Two cost 229 -> 248 us
+// there, and 80 -> 97 us on 512 bf16 rows behind 16400 positions (tiles of 64; tiles of 128 spill and take 98).
 #pragma once
 
 #include "pi_kv_device.cuh"
@@ -33,12 +34,13 @@
 namespace pi {
 
 // FEW: items of up to 128 rows (head dims 64 and 128), without a second group's warps, whose registers the others have
-template <int D, int QT, bool FEW>
+template <int D, int QT, bool SHARED, bool FEW>
 struct RowsCfg {
+    static constexpr int WT = SHARED ? 2 : QT;                  // terms of a weight
     static constexpr int NG = D == 256 || FEW ? 1 : 2;          // groups of 128 rows
     static constexpr int ROWS = 128 * NG, RT = 2 * ROWS;        // rows, and their threads
     static constexpr int LOADERS = 128, NT = RT + LOADERS;
-    static constexpr int TOK = D == 256 || QT == 2 ? 64 : 128;  // positions per tile
+    static constexpr int TOK = D == 256 || QT == 2 || (WT == 2 && NG == 2) ? 64 : 128;  // positions per tile
     static constexpr int NB = D == 256 && QT == 2 ? 1 : 2;      // tiles of K and of V in shared memory
     static constexpr int Q_BYTES = 128 * D * 2, KV_BYTES = TOK * D * 2;
     static constexpr int STAGE = TOK * D;                       // bytes of the codes of one tile
@@ -47,7 +49,7 @@ struct RowsCfg {
     // The tensor cores keep products in their order only where these go to one accumulator in one shape. So the next
     // tile's S is not written over weights that P V may still read: P has columns of its own (APART), or S waits until
     // P V is done (head dim 128, 16-bit types).
-    static constexpr int TCOLS = 512, PCOLS = QT * TOK / 2;
+    static constexpr int TCOLS = 512, PCOLS = WT * TOK / 2;
     static constexpr bool APART = NG * (TOK + D + PCOLS) <= TCOLS;
     static constexpr int GCOLS = TOK + D + (APART ? PCOLS : 0);
 };
@@ -89,10 +91,10 @@ struct RowsShared {
     uint32_t taddr;
 };
 
-template <int D, int QT, bool FEW>
+template <int D, int QT, bool SHARED, bool FEW>
 constexpr int rows_smem()
 {
-    using C = RowsCfg<D, QT, FEW>;
+    using C = RowsCfg<D, QT, SHARED, FEW>;
     constexpr int n = C::DATA + (int)sizeof(RowsShared<C::ROWS, C::NT / 32>);
     static_assert(n <= 227 * 1024, "shared memory");
     return n;
@@ -100,12 +102,12 @@ constexpr int rows_smem()
 
 // SHARED: a pass of pi_kv_attend_shared (a.pass), else one pass alone
 template <int D, int QT, bool SHARED, bool FEW>
-__global__ void __launch_bounds__(RowsCfg<D, QT, FEW>::NT, 1) k_kv_rows(const __grid_constant__ KvAttendArgs a,
+__global__ void __launch_bounds__(RowsCfg<D, QT, SHARED, FEW>::NT, 1) k_kv_rows(const __grid_constant__ KvAttendArgs a,
                                                                     const __grid_constant__ CUtensorMap mk,
                                                                     const __grid_constant__ CUtensorMap mv)
 {
-    using C = RowsCfg<D, QT, FEW>;
-    constexpr int TOK = C::TOK, NB = C::NB, NW = C::NT / 32;
+    using C = RowsCfg<D, QT, SHARED, FEW>;
+    constexpr int TOK = C::TOK, NB = C::NB, NW = C::NT / 32, WT = C::WT;
     constexpr int NBLK = D / 64, NV = TOK * D / 16 / C::LOADERS;   // 64-column blocks; 16-byte vectors per loader thread
     constexpr int RPY = C::LOADERS / 4;   // rows of a tile that the loaders take at a time
     extern __shared__ __align__(1024) uint8_t dsm[];   // no static shared memory beside it: it starts on its alignment
@@ -502,7 +504,7 @@ __global__ void __launch_bounds__(RowsCfg<D, QT, FEW>::NT, 1) k_kv_rows(const __
             if (dead) return;
             const uint64_t v1 = dv + (uint32_t)(b * C::KV_BYTES / 16);
 #pragma unroll
-            for (int term = 0; term < QT; ++term)
+            for (int term = 0; term < WT; ++term)
 #pragma unroll
                 for (int j = 0; j < TOK / 16; ++j)
                     umma_f16_ts(to, tp + term * (TOK / 2) + j * 8, v1 + (uint32_t)(j * 2048 / 16), ID_O,
@@ -573,7 +575,7 @@ __global__ void __launch_bounds__(RowsCfg<D, QT, FEW>::NT, 1) k_kv_rows(const __
                 }
             }
             const float ref = m == -INFINITY ? 0.f : m;
-            uint32_t plo[QT == 2 ? HC / 2 : 1];
+            uint32_t plo[WT == 2 ? HC / 2 : 1];
 #pragma unroll
             for (int x = 0; x < HC / 16; ++x) {
                 const float f = factor[x], off = mt.vexp[half * (HC / 16) + x] - ref;
@@ -585,14 +587,14 @@ __global__ void __launch_bounds__(RowsCfg<D, QT, FEW>::NT, 1) k_kv_rows(const __
                     w.x = ex2(w.x);
                     w.y = ex2(w.y);
                     sum = fadd2(sum, w);
-                    if constexpr (QT == 2) split_pair(w.x, w.y, r[e / 2], plo[e / 2]);
+                    if constexpr (WT == 2) split_pair(w.x, w.y, r[e / 2], plo[e / 2]);
                     else r[e / 2] = pack_f16(w.x, w.y);
                 }
                 l = fmaf(sum.x + sum.y, mt.vback[half * (HC / 16) + x], l);
                 // Weights: first terms in columns [0, TOK / 2) of P, second ones behind.
                 if (x & 1) {
                     tmem_st16(my_p + (x / 2) * 16, r + (x / 2) * 16);
-                    if constexpr (QT == 2) tmem_st16(my_p + TOK / 2 + (x / 2) * 16, plo + (x / 2) * 16);
+                    if constexpr (WT == 2) tmem_st16(my_p + TOK / 2 + (x / 2) * 16, plo + (x / 2) * 16);
                 }
             }
             tmem_wait_st();
@@ -719,7 +721,7 @@ __global__ void __launch_bounds__(RowsCfg<D, QT, FEW>::NT, 1) k_kv_rows(const __
 template <int D, int QT, bool SHARED, bool FEW>
 cudaError_t rows_setup()
 {
-    return cudaFuncSetAttribute(k_kv_rows<D, QT, SHARED, FEW>, cudaFuncAttributeMaxDynamicSharedMemorySize, rows_smem<D, QT, FEW>());
+    return cudaFuncSetAttribute(k_kv_rows<D, QT, SHARED, FEW>, cudaFuncAttributeMaxDynamicSharedMemorySize, rows_smem<D, QT, SHARED, FEW>());
 }
 
 template <int D, int QT, bool SHARED, bool FEW>
@@ -728,8 +730,8 @@ cudaError_t rows_launch(const KvAttendArgs &a, const CUtensorMap &mk, const CUte
 {
     Launch L;
     L.grid = dim3(items, splits);
-    L.block = dim3(RowsCfg<D, QT, FEW>::NT);
-    L.smem = rows_smem<D, QT, FEW>();
+    L.block = dim3(RowsCfg<D, QT, SHARED, FEW>::NT);
+    L.smem = rows_smem<D, QT, SHARED, FEW>();
     L.stream = s;
     L.pdl = true;
     L.nsm = 0;

@@ -7,7 +7,7 @@
 // end: a CTA has four warps that share nothing until an item's end, four CTAs to an SM. A warp takes 16 of a tile's 64
 // positions: it asks for their codes by TMA, three tiles ahead, into boxes of its own, and keeps its own maximum, sum and
 // numerators; the products are pi_kv_split.cuh's (the cache as the 16-row operand on mma.sync m16n8k16, codes to f16 two
-// at a time, queries in terms), and so are their units and rounding. The items are laid end to end and cut into equal
+// at a time, queries in T terms), and so are their units and rounding; weights have two terms in every type. The items are laid end to end and cut into equal
 // shares. An item of up to two shares belongs to the CTA with its first step; a longer one is cut over CTAs and joined by
 // the last of them, in the order of its parts.
 // Measured: 64 sequences of 1..716 positions behind a prefix, 64 heads on 8 of 128, bf16, with the join of the prefix's 9
@@ -399,20 +399,16 @@ __global__ void __launch_bounds__(ShortCfg<D, T>::NT, ShortCfg<D, T>::CTAS)
             }
             // ---- weights, and their products with the values
             const float scale = sv * inv * 16384.f;
-            uint32_t pb[T][2];
+            uint32_t pb[2][2];   // two terms of a weight in every type
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 const float e0 = ex2(s[2 * x] - (m[0] == -INFINITY ? 0.f : m[0])), e1 = ex2(s[2 * x + 1] - (m[1] == -INFINITY ? 0.f : m[1]));
                 l[0] += e0;
                 l[1] += e1;
-                if constexpr (T == 2) {
-                    uint32_t hi, lo;
-                    split_pair(e0 * scale, e1 * scale, hi, lo);
-                    pb[0][x] = transpose8(hi);
-                    pb[T - 1][x] = transpose8(lo);
-                } else {
-                    pb[0][x] = transpose8(pack_f16(e0 * scale, e1 * scale));
-                }
+                uint32_t hi, lo;
+                split_pair(e0 * scale, e1 * scale, hi, lo);
+                pb[0][x] = transpose8(hi);
+                pb[1][x] = transpose8(lo);
             }
 #pragma unroll
             for (int w = 0; w < D / 32; ++w)
@@ -422,15 +418,11 @@ __global__ void __launch_bounds__(ShortCfg<D, T>::NT, ShortCfg<D, T>::CTAS)
                     e4m3x4_f16x4(__byte_perm(word4(vc[0][0], w), word4(vc[0][1], w), b2 ? 0x7362 : 0x5140), va[0], va[1]);
                     e4m3x4_f16x4(__byte_perm(word4(vc[1][0], w), word4(vc[1][1], w), b2 ? 0x7362 : 0x5140), va[2], va[3]);
                     const int j = w * 2 + b2;
-                    if constexpr (T == 2) {   // in a sum of their own, added with rounding
-                        float sum[4] = {0.f, 0.f, 0.f, 0.f};
-                        mma_f16(sum, va, pb[T - 1][0], pb[T - 1][1]);
-                        mma_f16(sum, va, pb[0][0], pb[0][1]);
+                    float sum[4] = {0.f, 0.f, 0.f, 0.f};   // added with rounding
+                    mma_f16(sum, va, pb[1][0], pb[1][1]);
+                    mma_f16(sum, va, pb[0][0], pb[0][1]);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) acc[j][e] += sum[e];
-                    } else {
-                        mma_f16(acc[j], va, pb[0][0], pb[0][1]);
-                    }
+                    for (int e = 0; e < 4; ++e) acc[j][e] += sum[e];
                 }
         }
         // ---------------------------------------------------------------- the warps' results, joined

@@ -160,8 +160,9 @@ pi_status_t pi_kv_share(pi_kv_t *h, const int32_t *seqs, const int32_t *tok_star
 /*
  * pi_kv_attend without a window, for sequences that share prefixes: a group's prefix is read once for all its rows,
  * through the table row of its first sequence with new tokens, what lies behind it for each sequence, and the two are joined
- * by their maxima and sums in fp32 (the output is rounded once). Same results as pi_kv_attend up to fp32 rounding and the
- * terms that many and few rows keep. plan: from pi_kv_share for the same seqs, tok_start and n_groups (a sequence
+ * by their maxima and sums in fp32 (the output is rounded once). Weights have two f16 terms (22 bits) and queries of PI_BF16
+ * and PI_F16 are exact, whatever the rows' number: for every type the result is that of pi_kv_attend in fp32, up to fp32
+ * rounding, rounded once (pi_kv_attend itself keeps 11 bits of a weight in some calls of 16-bit types). plan: from pi_kv_share for the same seqs, tok_start and n_groups (a sequence
  * whose entry differs is skipped and flagged). out may be q (same address and stride). work: fp32 device [n_tokens * n_heads * (head_dim + 2)], 16-byte
  * aligned, overwritten; it touches no other array of the call.
  */

@@ -413,3 +413,41 @@ def test_refusals(P):
     empty = b.cache.share(none, dev([0]), dev([0]))
     assert b.cache.attend_shared(0, none, dev([0]), empty, q[:0]).shape == (0, 4, 64)
     assert b.cache.status() == 0
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("dim,page", [(64, 16), (128, 64), (256, 32)])
+def test_weights_of_16_bit_types_keep_two_terms(P, dim, page, kind):
+    """Outputs are the rounding of what fp32 would give: they lie between the roundings of both ends of its bound (the head
+    of this file, with two terms). One value of each sequence's own and one of the prefix make a column, so that the
+    roundings of weights do not average out."""
+    b = Shared(P, hq=8, hkv=2, dim=dim, page=page, n_pages=-(-6000 // page), max_seqs=44, max_pages=-(-800 // page))
+    p = b.plain
+    b.grow([0], [700])
+    b.fork([0] * 40, range(1, 41))
+    b.grow(range(41), [40 if i == 3 else 1 + i % 3 for i in range(41)])
+    p.v[:] = 0
+    for seq in range(41):
+        for at, columns in ((77, slice(0, None, 2)), (700, slice(1, None, 2))):
+            codes = p.v[0, p.table[seq, at // page], :, at % page]
+            if not codes[:, columns].any():
+                codes[:, columns] = b.rng.integers(0x20, 0x7e, codes[:, columns].shape)
+    b.v.view(torch.uint8).copy_(torch.tensor(p.v, device="cuda"))
+    # rows to a group and behind it: few; 36; 128; 160; many new tokens of one sequence
+    for seqs, new in ((range(3), [1] * 3), (range(9), [1] * 9), (range(32), [1] * 32), (range(40), [1] * 40),
+                      ([0, 40, 3], [1, 1, 40])):
+        args = b.args(seqs, new)
+        plan = b.cache.share(*args, dev([0, len(new)]))
+        assert (plan[3:4 + len(new)] == 640).all()
+        q, qn = b.tokens(new, kind, p.hq, spread=0)
+        scale = 1 / 64
+        out = b.cache.attend_shared(0, *args, plan, q, scale=scale)
+        want, _ = p.attend(0, seqs, new, qn, scale)
+        signed, p.v = p.v, p.v & 0x7f
+        size, _ = p.attend(0, seqs, new, qn, scale)
+        p.v = signed
+        largest = scale * np.linalg.norm(qn, axis=-1, keepdims=True) * b.key_norms(seqs, new)
+        off = size * (1e-5 + 2 * 12 * 2.0 ** -23 * largest + 2.0 ** -22)
+        lo, hi = (torch.tensor(want + x, device="cuda").to(TYPES[kind]) for x in (-off, off))
+        beyond = (out < lo) | (out > hi)
+        assert not beyond.any() and b.cache.status() == 0, (len(new), int(beyond.sum()), beyond.numel())
