@@ -32,13 +32,13 @@ __global__ void __launch_bounds__(AR_NT, 3) k_kv_append_rot(const KvAppendRotArg
     // the blockIdx.x-th page that new tokens of the call fall into
     const int ps = __ffs(P) - 1;
     if (tid == 0) s_item = -1;
+    const bool flag = blockIdx.x == 0 && blockIdx.y == 0;   // the CTA that looks at every sequence, for what is out of range
     int before = 0;
-    for (int b0 = 0; b0 < a.b.n && before <= (int)blockIdx.x; b0 += AR_NT) {
+    for (int b0 = 0; b0 < a.b.n && (flag || before <= (int)blockIdx.x); b0 += AR_NT) {
         const int i = b0 + tid;
         KvSeq s = {};
         int cnt = 0;
         if (i < a.b.n) {
-            const bool flag = blockIdx.x == 0 && blockIdx.y == 0;
             s = kv_sequence(c, a.b, i, flag);
             if (s.n > 0 && s.n <= s.len) cnt = ((s.len - 1) >> ps) - ((s.len - s.n) >> ps) + 1;
             else if (s.n > 0 && flag) set_status(c.status, ST_DEVICE_CHECK);   // no room was reserved

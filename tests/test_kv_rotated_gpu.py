@@ -243,3 +243,24 @@ def test_pools_past_32_bits(P):
         at, to = (z.view(torch.uint8)[p].transpose(1, 2).reshape(-1, hkv, dim)[:700] for z, p in ((x, table[0, :11].long()), (y, small)))
         assert torch.equal(at, to)
     assert big.status() == 0 and b.cache.status() == 0
+
+
+@pytest.mark.parametrize("n,at", [(257, 256), (700, 300), (1024, 1023)])
+def test_flags_sequences_far_down_the_call(P, n, at):
+    """One entry out of range, then one without room, behind more sequences than a CTA looks at in one go."""
+    b = Both(P, hq=2, hkv=1, dim=64, page=16, n_pages=1100, max_seqs=1024, max_pages=2)
+    r, _, _ = rotary(P, b.rng, 64, 64, norm=False, interleaved=False)
+    seqs, start = (torch.arange(n + i, device="cuda", dtype=torch.int32) for i in (0, 1))
+    room = torch.cat([seqs[:at], seqs[at + 1:]])
+    b.cache.reserve(room, torch.arange(n, device="cuda", dtype=torch.int32))
+    q, k, v = (torch.randn((n, h, 64), device="cuda") for h in (2, 1, 1))
+    far = seqs.clone()
+    far[at] = 5000
+    for call in (far, seqs):
+        out = torch.full_like(q, 5.0)
+        b.cache.append_rotated(0, call, start, r, q, k, v, q_out=out)
+        assert b.cache.status() == P.PI_ERR_DEVICE_CHECK and b.cache.status() == 0
+        left = (out == 5.0).flatten(1).all(1)
+        assert left[at] and left.sum() == 1
+    b.cache.append_rotated(0, room, start[:n], r, q[:n - 1], k[:n - 1], v[:n - 1])
+    assert b.cache.status() == 0
