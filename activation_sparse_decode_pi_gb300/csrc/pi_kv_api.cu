@@ -96,12 +96,15 @@ cudaError_t setup_of()
 {
     for (cudaError_t e : {split_setup<D, 1, 1, false>(), split_setup<D, 1, 2, false>(), split_setup<D, 2, 1, false>(),
                           split_setup<D, 2, 2, false>(), rows_setup<D, 1, false, false>(), rows_setup<D, 2, false, false>(),
-                          split_setup<D, 1, 1, true>(), split_setup<D, 1, 2, true>(), split_setup<D, 2, 1, true>(),
-                          split_setup<D, 2, 2, true>(), rows_setup<D, 1, true, false>(), rows_setup<D, 2, true, false>()})
+                          rows_setup<D, 1, true, false>(), rows_setup<D, 2, true, false>()})
         if (e != cudaSuccess) return e;
-    if constexpr (D <= 128)
+    if constexpr (D <= 128) {
         for (cudaError_t e : {short_setup<D, 1>(), short_setup<D, 2>(), rows_setup<D, 1, true, true>(), rows_setup<D, 2, true, true>()})
             if (e != cudaSuccess) return e;
+    } else {
+        for (cudaError_t e : {split_setup<D, 1, 2, true>(), split_setup<D, 2, 2, true>()})
+            if (e != cudaSuccess) return e;
+    }
     return cudaSuccess;
 }
 
@@ -119,8 +122,7 @@ cudaError_t attend_of(const pi_kv *h, int layer, KvAttendArgs a, cudaStream_t s)
     const bool many = rows >= ROWS_FROM && (n == 1 || a.b.n_tokens > n), few = n > 1 || !many;
     a.rows_from = many ? (few ? ROWS_FROM : 0) : INT32_MAX;
     cudaError_t e = cudaSuccess;
-    bool done = false;   // the few rows
-    if constexpr (SHARED && D <= 128)
+    if constexpr (SHARED && D <= 128) {
         if (few) {
             KvAttendArgs b = a;
             b.part = h->short_part;
@@ -128,15 +130,15 @@ cudaError_t attend_of(const pi_kv *h, int layer, KvAttendArgs a, cudaStream_t s)
             b.tickets = h->short_tickets;
             const CUtensorMap &bk = h->box_k[layer], &bv = h->box_v[layer];
             e = a.dtype == PI_F32 ? short_launch<D, 2>(b, bk, bv, h->nsm, s) : short_launch<D, 1>(b, bk, bv, h->nsm, s);
-            done = true;
         }
-    if (few && !done) {
+    } else if (few) {
         // 16 rows to a tile where the rows of a sequence (on average: all that the host knows) fill more than 8: the cache
         // is then read once instead of twice (64 sequences, 16 heads to a group: 229 / 323 us with 16 / 8; 8 heads, 128
         // sequences: 381 / 330 us, since 16 leave room for fewer warps)
-        const bool wide = (many && !SHARED) || rows > 8 * n, one = a.dtype == PI_BF16 && !SHARED;
-        const auto run = wide ? (one ? split_launch<D, 2, 1, SHARED> : split_launch<D, 2, 2, SHARED>)
-                              : (one ? split_launch<D, 1, 1, SHARED> : split_launch<D, 1, 2, SHARED>);
+        const bool wide = (many && !SHARED) || rows > 8 * n;
+        auto run = wide ? split_launch<D, 2, 2, SHARED> : split_launch<D, 1, 2, SHARED>;
+        if constexpr (!SHARED)
+            if (a.dtype == PI_BF16) run = wide ? split_launch<D, 2, 1, false> : split_launch<D, 1, 1, false>;
         e = run(a, h->map_k[layer], h->map_v[layer], h->nsm, s);
     }
     if (many && e == cudaSuccess) {

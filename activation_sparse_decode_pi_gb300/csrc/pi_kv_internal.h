@@ -65,7 +65,7 @@ struct KvAttendArgs {
 constexpr int KV_SHARE = 128;   // a shared prefix is a multiple of this: whole tiles of both kernels, whole pages
 
 // The split kernel (pi_kv_split.cuh) of one head dim; QN: runs of 8 rows per tile, T: 16-bit terms, SHARED: for a pass of
-// pi_kv_attend_shared.
+// pi_kv_attend_shared (head dim 256, two terms; the others have pi_kv_short.cuh).
 template <int D, int QN, int T, bool SHARED>
 cudaError_t split_setup();   // shared-memory opt-in
 template <int D, int QN, int T, bool SHARED>
@@ -73,10 +73,10 @@ cudaError_t split_launch(const KvAttendArgs &a, const CUtensorMap &mk, const CUt
 #define PI_KV_SPLIT1(WORD, D, QN, T, S)                  \
     WORD template cudaError_t split_setup<D, QN, T, S>(); \
     WORD template cudaError_t split_launch<D, QN, T, S>(const KvAttendArgs &, const CUtensorMap &, const CUtensorMap &, int, cudaStream_t);
-#define PI_KV_SPLIT(WORD, D, S) \
-    PI_KV_SPLIT1(WORD, D, 1, 1, S) PI_KV_SPLIT1(WORD, D, 1, 2, S) PI_KV_SPLIT1(WORD, D, 2, 1, S) PI_KV_SPLIT1(WORD, D, 2, 2, S)
-PI_KV_SPLIT(extern, 64, false) PI_KV_SPLIT(extern, 128, false) PI_KV_SPLIT(extern, 256, false)
-PI_KV_SPLIT(extern, 64, true) PI_KV_SPLIT(extern, 128, true) PI_KV_SPLIT(extern, 256, true)
+#define PI_KV_SPLIT(WORD, D) \
+    PI_KV_SPLIT1(WORD, D, 1, 1, false) PI_KV_SPLIT1(WORD, D, 1, 2, false) PI_KV_SPLIT1(WORD, D, 2, 1, false) PI_KV_SPLIT1(WORD, D, 2, 2, false)
+#define PI_KV_SPLIT_SHARED(WORD) PI_KV_SPLIT1(WORD, 256, 1, 2, true) PI_KV_SPLIT1(WORD, 256, 2, 2, true)
+PI_KV_SPLIT(extern, 64) PI_KV_SPLIT(extern, 128) PI_KV_SPLIT(extern, 256) PI_KV_SPLIT_SHARED(extern)
 
 // The rows kernel (pi_kv_rows.cuh): QT 16-bit terms of queries, and of weights (SHARED: two of these). items: an upper bound of the
 // call's (sequence, kv head, run of rows_per_item rows); splits: parts of each item's cache.

@@ -2,5 +2,5 @@
 #include "pi_kv_split.cuh"
 
 namespace pi {
-PI_KV_SPLIT(, 128, false)
+PI_KV_SPLIT(, 128)
 }  // namespace pi

@@ -2,5 +2,5 @@
 #include "pi_kv_split.cuh"
 
 namespace pi {
-PI_KV_SPLIT(, 64, false)
+PI_KV_SPLIT(, 64)
 }  // namespace pi

@@ -3,5 +3,5 @@
 #include "pi_kv_split.cuh"
 
 namespace pi {
-PI_KV_SPLIT(, 256, true)
+PI_KV_SPLIT_SHARED()
 }  // namespace pi
