@@ -217,7 +217,8 @@ pi_status_t kv_create(pi_kv_t **out, const pi_kv_desc_t *desc, const pi_kv_layer
     const size_t rpart = up((size_t)2 * nsm * rows_per_item(d.head_dim) * d.head_dim * 4),
                  rml = up((size_t)2 * nsm * rows_per_item(d.head_dim) * 2 * 4);
     const size_t prior = up((size_t)nsm * rows_per_item(d.head_dim) * (d.head_dim + 2) * 4);
-    const size_t spart = up((size_t)2 * SHORT_CTAS * nsm * 8 * d.head_dim * 4), sml = up((size_t)2 * SHORT_CTAS * nsm * 8 * 2 * 4);
+    // (head dim 256 has no such kernel)
+    const size_t shorts = d.head_dim <= 128 ? (size_t)SHORT_CTAS * nsm : 0, spart = up(2 * shorts * 8 * d.head_dim * 4), sml = up(2 * shorts * 8 * 2 * 4);
     const size_t total = 3 * list + part + ml + rpart + rml + prior + spart + sml + (3 + SHORT_CTAS) * tick + lay + 2 * 256;
     if (injected_fault() == FAULT_ALLOC) return PI_ERR_OOM;
     if ((s = cuda_status(cudaMalloc(&h->ws, total)))) return s;
