@@ -56,18 +56,13 @@ pi_status_t check_ptr(const void *p, size_t bytes, size_t align, int dev)
                                    CU_POINTER_ATTRIBUTE_DEVICE_ORDINAL, CU_POINTER_ATTRIBUTE_RANGE_START_ADDR,
                                    CU_POINTER_ATTRIBUTE_RANGE_SIZE};
     void *to[5] = {&type, &managed, &device, &base, &size};
-    if (fn && fn(5, what, to, (CUdeviceptr)(uintptr_t)p) == CUDA_SUCCESS) {
-        if (!managed && (type != CU_MEMORYTYPE_DEVICE || device != dev)) return PI_ERR_INVALID_ARG;
-        if (size && (uintptr_t)p + bytes > (uintptr_t)base + size) return PI_ERR_INVALID_ARG;
-        return PI_OK;
+    const auto ask = [&]() { return fn && fn(5, what, to, (CUdeviceptr)(uintptr_t)p) == CUDA_SUCCESS; };
+    if (!ask()) {   // a thread that has no context yet: the runtime gives it the device's
+        if (cudaSetDevice(dev) != cudaSuccess) cudaGetLastError();
+        if (!ask()) return PI_ERR_INVALID_ARG;
     }
-    cudaPointerAttributes a;
-    if (cudaPointerGetAttributes(&a, p) != cudaSuccess) {
-        cudaGetLastError();
-        return PI_ERR_INVALID_ARG;
-    }
-    if (a.type != cudaMemoryTypeDevice && a.type != cudaMemoryTypeManaged) return PI_ERR_INVALID_ARG;
-    if (a.type == cudaMemoryTypeDevice && a.device != dev) return PI_ERR_INVALID_ARG;
+    if (!managed && (type != CU_MEMORYTYPE_DEVICE || device != dev)) return PI_ERR_INVALID_ARG;
+    if (size && (uintptr_t)p + bytes > (uintptr_t)base + size) return PI_ERR_INVALID_ARG;
     return PI_OK;
 }
 

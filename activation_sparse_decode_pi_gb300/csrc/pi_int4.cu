@@ -345,11 +345,7 @@ cudaError_t launch_int4_linear(const Int4Args &a, int dtype, int nsm, cudaStream
     if (a.rows > (dtype == DT_F32 ? 8 : 16) && launch_int4_rows(a, dtype, nsm, s, &e)) return e;
     // W as rows of k / 2 bytes; boxes of 32 rows and 128 bytes, swizzled. What lies past its edges reads as zeros.
     CUtensorMap map;
-    const cuuint64_t dims[2] = {(cuuint64_t)a.k / 2, (cuuint64_t)a.n}, strides[1] = {(cuuint64_t)a.k / 2};
-    const cuuint32_t box[2] = {128, 32}, one[2] = {1, 1};
-    const EncodeFn encode = tensor_map_encoder();
-    if (!encode || encode(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, (void *)a.w, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    if (!encode_bytes(&map, a.w, a.n, a.k / 2, 32, 128, CU_TENSOR_MAP_SWIZZLE_128B))
         return cudaErrorUnknown;
     switch (dtype) {
     case DT_F32: return launch_dt<DT_F32>(a, map, nsm, s);

@@ -376,11 +376,7 @@ bool launch_dt(const Int4Args &a, int nsm, cudaStream_t s, cudaError_t *e)
     if (p.cluster == 0) return false;
     // W as rows of k / 2 bytes; boxes of 128 rows and 128 bytes, swizzled. What lies past its edges reads as zeros.
     CUtensorMap map;
-    const cuuint64_t dims[2] = {(cuuint64_t)a.k / 2, (cuuint64_t)a.n}, strides[1] = {(cuuint64_t)a.k / 2};
-    const cuuint32_t box[2] = {128, 128}, one[2] = {1, 1};
-    const EncodeFn encode = tensor_map_encoder();
-    if (!encode || encode(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, (void *)a.w, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    if (!encode_bytes(&map, a.w, a.n, a.k / 2, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B))
         *e = cudaErrorUnknown;
     else
         *e = np == 16 ? launch_of<DT, 16>(a, p, map, nsm, s) : launch_of<DT, 32>(a, p, map, nsm, s);

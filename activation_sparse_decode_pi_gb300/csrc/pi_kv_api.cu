@@ -34,7 +34,12 @@ struct pi_kv {
 
 namespace pi {
 
-EncodeFn tensor_map_encoder()
+typedef CUresult (*EncodeFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                             const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                             CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// cuTensorMapEncodeTiled, or NULL
+static EncodeFn tensor_map_encoder()
 {
     static std::atomic<EncodeFn> found{nullptr};   // (looked up until it is there)
     if (EncodeFn fn = found.load(std::memory_order_relaxed)) return fn;
@@ -47,6 +52,25 @@ EncodeFn tensor_map_encoder()
     }
     cudaGetLastError();
     return nullptr;
+}
+
+bool encode_bytes(CUtensorMap *m, const void *base, int64_t rows, int64_t width, int box_rows, int box_width, CUtensorMapSwizzle swizzle)
+{
+    const EncodeFn fn = tensor_map_encoder();
+    const cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)width};
+    const cuuint32_t box[2] = {(cuuint32_t)box_width, (cuuint32_t)box_rows}, one[2] = {1, 1};
+    const auto encode = [&]() {
+        return fn && fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, (void *)base, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    };
+    if (encode()) return true;
+    // a thread that has no context yet: the runtime gives it the device's
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess) {
+        cudaGetLastError();
+        return false;
+    }
+    return encode();
 }
 
 }  // namespace pi
@@ -79,16 +103,10 @@ pi_status_t validate(const pi_kv_desc_t *d)
 
 // Pool of one layer as rows of head_dim bytes; boxes of one 64-position tile's share of a page (or of `rows` of it) and
 // 128 bytes (64 for head_dim 64), swizzled so that the kernels' reads spread over the banks.
-bool encode_pool(EncodeFn fn, CUtensorMap *m, const pi_kv_desc_t &d, void *base, int rows = KV_TILE)
+bool encode_pool(CUtensorMap *m, const pi_kv_desc_t &d, const void *base, int rows = KV_TILE)
 {
-    const cuuint64_t dims[2] = {(cuuint64_t)d.head_dim, (cuuint64_t)d.n_pages * d.n_kv_heads * d.page_tokens};
-    const cuuint64_t strides[1] = {(cuuint64_t)d.head_dim};
-    const cuuint32_t box[2] = {(cuuint32_t)(d.head_dim < 128 ? d.head_dim : 128),
-                               (cuuint32_t)std::min(d.page_tokens, rows)};
-    const cuuint32_t one[2] = {1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              d.head_dim < 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return encode_bytes(m, base, (int64_t)d.n_pages * d.n_kv_heads * d.page_tokens, d.head_dim, std::min(d.page_tokens, rows),
+                        std::min(d.head_dim, 128), d.head_dim < 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 template <int D>
@@ -181,8 +199,6 @@ pi_status_t kv_create(pi_kv_t **out, const pi_kv_desc_t *desc, const pi_kv_layer
     if ((s = check_ptr(state->table, (size_t)d.max_seqs * d.max_pages * 4, 4, dev))) return s;
     if ((s = check_ptr(state->length, (size_t)d.max_seqs * 4, 4, dev))) return s;
     if ((s = check_ptr(state->ref, (size_t)d.n_pages * 4, 4, dev))) return s;
-    EncodeFn enc = tensor_map_encoder();
-    if (!enc) return PI_ERR_CUDA;
 
     struct Holder {   // frees what exists when a later step fails
         pi_kv_t *h;
@@ -203,8 +219,8 @@ pi_status_t kv_create(pi_kv_t **out, const pi_kv_desc_t *desc, const pi_kv_layer
     h->box_v.resize(d.n_layers);
     for (int l = 0; l < d.n_layers; ++l) {
         h->layers.push_back({(uint8_t *)layers[l].k, (uint8_t *)layers[l].v, layers[l].k_scale, layers[l].v_scale});
-        if (!encode_pool(enc, &h->map_k[l], d, layers[l].k) || !encode_pool(enc, &h->map_v[l], d, layers[l].v) ||
-            !encode_pool(enc, &h->box_k[l], d, layers[l].k, 16) || !encode_pool(enc, &h->box_v[l], d, layers[l].v, 16))
+        if (!encode_pool(&h->map_k[l], d, layers[l].k) || !encode_pool(&h->map_v[l], d, layers[l].v) ||
+            !encode_pool(&h->box_k[l], d, layers[l].k, 16) || !encode_pool(&h->box_v[l], d, layers[l].v, 16))
             return PI_ERR_CUDA;
     }
     if ((s = cuda_status(d.head_dim == 64    ? setup_of<64>()

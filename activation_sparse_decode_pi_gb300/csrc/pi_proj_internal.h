@@ -13,11 +13,8 @@
 
 namespace pi {
 
-// cuTensorMapEncodeTiled, or NULL (pi_kv_api.cu)
-typedef CUresult (*EncodeFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                             const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                             CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-EncodeFn tensor_map_encoder();
+// A map for TMA copies of boxes out of `rows` rows of `width` bytes, dense; false: the driver has none (pi_kv_api.cu).
+bool encode_bytes(CUtensorMap *m, const void *base, int64_t rows, int64_t width, int box_rows, int box_width, CUtensorMapSwizzle swizzle);
 
 // Lets a kernel have `bytes` of dynamic shared memory on the current device, once for each device (safe from any thread).
 template <auto kernel>

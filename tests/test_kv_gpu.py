@@ -508,3 +508,28 @@ def test_other_stream_and_graph(P):
         want, _ = b.plain.attend(layer, [0, 1], [1, 1], q.double().cpu().numpy(), 128 ** -0.5)
         got = out[layer].double().cpu().numpy()
         assert np.linalg.norm(got - want) <= TOL["f32"] * np.linalg.norm(want)
+
+
+def test_a_cache_made_by_a_thread_without_a_context(P):
+    """A handle is made and used by host threads whose first CUDA call that is."""
+    import threading
+
+    b = Both(P)
+    b.grow([0], [20])
+    torch.cuda.synchronize()
+    made = []
+    layers = [dict(k=b.k[0], v=b.v[0], k_scale=b.ks[0], v_scale=b.vs[0])]
+    seqs, start = b.args([0], [1])
+
+    def make():
+        made.append(P.KVCache(layers, b.cache.table, b.cache.length, b.cache.ref, n_heads=4))
+
+    def reserve():
+        P.pi_kv_reserve(made[0].h, seqs, start, 1, 0)
+
+    for work in (make, reserve):
+        t = threading.Thread(target=work)
+        t.start()
+        t.join()
+    torch.cuda.synchronize()
+    assert made[0].length[0] == 21 and made[0].status() == 0

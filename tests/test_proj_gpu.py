@@ -269,6 +269,28 @@ def test_int4_linear_refusals(P):
     assert (lin(x1) == 0).all()
 
 
+def test_ranges_are_checked_for_a_thread_without_a_context(P):
+    """The first call of a new host thread works as every other does, and refuses arrays past their allocation."""
+    import threading
+
+    rng = np.random.default_rng(6)
+    w, s = (torch.tensor(a, device="cuda") for a in weights(rng, 8, 256))
+    x, y = torch.zeros((4, 256), device="cuda"), torch.zeros((4, 8), device="cuda")
+    torch.cuda.synchronize()
+    codes = []
+
+    def call(n):
+        codes.append(P._lib.pi_int4_linear(w.data_ptr(), s.data_ptr(), None, n, 256, x.data_ptr(), 256, 4, None, 0, y.data_ptr(),
+                                           n, 0, None))
+
+    for n in (1 << 24, 8):                                           # 2 GB of weights in another allocation; as they are
+        t = threading.Thread(target=call, args=(n,))
+        t.start()
+        t.join()
+    torch.cuda.synchronize()
+    assert codes == [1, 0] and (y == 0).all()
+
+
 # ------------------------------------------------------------------------------------------------ rotation
 
 POS = [0, 1, 2, 77, 4095, 131071, 1000003, 2 ** 30 + 1, 2 ** 31 - 1, -1, -100, -2 ** 31]
