@@ -10,6 +10,7 @@
 #include <cfloat>
 #include <cmath>
 #include <cstdint>
+#include <initializer_list>
 #include <new>
 #include <vector>
 
@@ -299,6 +300,28 @@ pi_status_t check_rows(const pi_kv_t *h, const void *p, int64_t n_tokens, int64_
     return check_ptr(p, (size_t)(((n_tokens - 1) * ld + width) * es), 16, h->dev);
 }
 
+// `bytes` of memory as an array
+Strided flat(const void *p, int64_t bytes) { return {p, 1, bytes, bytes, 1}; }
+
+// Whether an element of x may be one of the others', or of what the call reads besides: its batch, the handle's state and, of a
+// layer, the pools.
+bool touches(const pi_kv_t *h, const Strided &x, int layer, const int32_t *seqs, const int32_t *tok_start, int32_t n,
+             std::initializer_list<Strided> others)
+{
+    const pi_kv_desc_t &d = h->desc;
+    const int64_t blocks = (int64_t)d.n_pages * d.n_kv_heads, pool = blocks * d.page_tokens * d.head_dim;
+    for (const Strided &o : others)
+        if (may_overlap(x, o)) return true;
+    for (const Strided &o : {flat(seqs, n * 4ll), flat(tok_start, n * 4ll + 4), flat(h->view.table, (int64_t)d.max_seqs * d.max_pages * 4),
+                             flat(h->view.length, d.max_seqs * 4ll), flat(h->view.ref, d.n_pages * 4ll)})
+        if (may_overlap(x, o)) return true;
+    if (layer < 0) return false;
+    const KvLayerDev &l = h->layers[layer];
+    for (const Strided &o : {flat(l.k, pool), flat(l.v, pool), flat(l.ks, blocks * 4), flat(l.vs, blocks * 4)})
+        if (may_overlap(x, o)) return true;
+    return false;
+}
+
 // The arguments of an attention, checked; a is filled where there is something to do.
 pi_status_t attend_args(const pi_kv_t *h, int32_t layer, const int32_t *seqs, const int32_t *tok_start, int32_t n,
                         int32_t n_tokens, const void *q, int64_t ld_q, void *out, int64_t ld_out, float *lse, int32_t dtype,
@@ -434,7 +457,11 @@ pi_status_t pi_kv_append_rotated(pi_kv_t *h, int32_t layer, const int32_t *seqs,
     if ((s = check_rows(h, q_out, n_tokens, wide, ld_q_out, es))) return s;
     const Strided sq{q, n_tokens, wide, ld_q, es}, so{q_out, n_tokens, wide, ld_q_out, es};
     const Strided sk{k_new, n_tokens, width, ld, es}, sv{v_new, n_tokens, width, ld, es};
-    if ((!same_place(sq, so) && may_overlap(sq, so)) || may_overlap(so, sk) || may_overlap(so, sv)) return PI_ERR_INVALID_ARG;
+    if ((!same_place(sq, so) && may_overlap(sq, so)) ||
+        touches(h, so, layer, seqs, tok_start, n,
+                {sk, sv, flat(a.r.turns, a.r.rot * 4ll), flat(a.r.norm ? a.r.qn : nullptr, h->desc.head_dim * 4ll),
+                 flat(a.r.norm ? a.r.kn : nullptr, h->desc.head_dim * 4ll)}))
+        return PI_ERR_INVALID_ARG;
     a.c = h->view;
     a.b = {seqs, tok_start, n, n_tokens, nullptr, nullptr, nullptr};
     a.l = h->layers[layer];
@@ -470,6 +497,8 @@ pi_status_t pi_kv_share(pi_kv_t *h, const int32_t *seqs, const int32_t *tok_star
     if ((s = check_batch(h, seqs, tok_start, n))) return s;
     if ((s = check_ptr(group_start, ((size_t)n_groups + 1) * 4, 4, h->dev))) return s;
     if ((s = check_ptr(plan, (size_t)PI_KV_SHARE_INTS(n, n_groups) * 4, 4, h->dev))) return s;
+    if (touches(h, flat(plan, PI_KV_SHARE_INTS(n, n_groups) * 4ll), -1, seqs, tok_start, n, {flat(group_start, n_groups * 4ll + 4)}))
+        return PI_ERR_INVALID_ARG;
     return cuda_status(launch_kv_share(h->view, {seqs, tok_start, n, KV_MAX_LEN, nullptr, nullptr, nullptr}, group_start,
                                        n_groups, plan, (cudaStream_t)stream));
 }
@@ -495,10 +524,12 @@ pi_status_t pi_kv_attend_shared(pi_kv_t *h, int32_t layer, const int32_t *seqs, 
     const int64_t run = rows_per_item(h->desc.head_dim, few), most = ((group_rows + run - 1) / run + n_groups - 1) * h->desc.n_kv_heads;
     a.parts = n_groups > 0 && group_rows >= ROWS_FROM ? (int)std::max<int64_t>(1, std::min<int64_t>(16, h->nsm / most)) : 1;
     const int64_t wide = (int64_t)h->desc.n_heads * h->desc.head_dim;
-    const Strided sw{work, 1, rows * (h->desc.head_dim + 2), rows * (h->desc.head_dim + 2), 4};
     const int es = elt_size(dtype);
-    if (may_overlap(sw, {q, n_tokens, wide, ld_q, es}) || may_overlap(sw, {out, n_tokens, wide, ld_out, es}) ||
-        may_overlap(sw, {lse, 1, rows, rows, 4}))
+    const Strided sq{q, n_tokens, wide, ld_q, es}, so{out, n_tokens, wide, ld_out, es}, sl = flat(lse, rows * 4),
+        sp = flat(plan, PI_KV_SHARE_INTS(n, n_groups) * 4ll);
+    if ((!same_place(sq, so) && may_overlap(sq, so)) || touches(h, so, layer, seqs, tok_start, n, {sl, sp}) ||
+        touches(h, sl, layer, seqs, tok_start, n, {sq, sp}) ||
+        touches(h, flat(work, rows * (h->desc.head_dim + 2) * 4), layer, seqs, tok_start, n, {sq, so, sl, sp}))
         return PI_ERR_INVALID_ARG;
     a.prior = a.parts > 1 ? h->prior : (float *)work;
     a.prior_ml = a.prior + a.parts * rows * h->desc.head_dim;

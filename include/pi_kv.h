@@ -110,7 +110,7 @@ pi_status_t pi_kv_append(pi_kv_t *h, int32_t layer, const int32_t *seqs, const i
  * pi_rotate and pi_kv_append in turn); values are coded as they are; q_out
  * = the queries' heads, normed and turned. q, q_out: [n_tokens x n_heads x head_dim] of `dtype`, row t at element t *
  * ld_q (ld_q_out), bases and row strides multiples of 16 bytes; q_out is q (same address and stride) or touches no other
- * array of the call. A sequence that pi_kv_append would skip keeps its rows of q_out as they were (a page that is absent loses its keys and
+ * array of the call, the rotation's, the handle's state and the layer's pools among them (PI_ERR_INVALID_ARG). A sequence that pi_kv_append would skip keeps its rows of q_out as they were (a page that is absent loses its keys and
  * values alone).
  */
 pi_status_t pi_kv_append_rotated(pi_kv_t *h, int32_t layer, const int32_t *seqs, const int32_t *tok_start, int32_t n,
@@ -151,7 +151,8 @@ pi_status_t pi_kv_attend(pi_kv_t *h, int32_t layer, const int32_t *seqs, const i
  * multiple of 128 positions; it is 0 for a group with one such sequence. plan: int32 [PI_KV_SHARE_INTS(n, n_groups)]
  * device, written. It serves all layers and later steps as long as the sequences only grow (pi_kv_reserve,
  * pi_kv_append) or their pages move with their table rows (pi_kv_compact), and the calls name the same seqs,
- * tok_start and n_groups. groups out of order are flagged and share nothing.
+ * tok_start and n_groups. groups out of order are flagged and share nothing. plan touches no other array of the call
+ * (PI_ERR_INVALID_ARG).
  */
 #define PI_KV_SHARE_INTS(n, n_groups) (3 * ((n) + (n_groups)) + 2)
 pi_status_t pi_kv_share(pi_kv_t *h, const int32_t *seqs, const int32_t *tok_start, int32_t n, const int32_t *group_start,
@@ -163,8 +164,9 @@ pi_status_t pi_kv_share(pi_kv_t *h, const int32_t *seqs, const int32_t *tok_star
  * by their maxima and sums in fp32 (the output is rounded once). Weights have two f16 terms (22 bits) and queries of PI_BF16
  * and PI_F16 are exact, whatever the rows' number: for every type the result is that of pi_kv_attend in fp32, up to fp32
  * rounding, rounded once (pi_kv_attend itself keeps 11 bits of a weight in some calls of 16-bit types). plan: from pi_kv_share for the same seqs, tok_start and n_groups (a sequence
- * whose entry differs is skipped and flagged). out may be q (same address and stride). work: fp32 device [n_tokens * n_heads * (head_dim + 2)], 16-byte
- * aligned, overwritten; it touches no other array of the call.
+ * whose entry differs is skipped and flagged). out may be q (same address and stride). work: fp32 device
+ * [n_tokens * n_heads * (head_dim + 2)], 16-byte aligned, overwritten. out, lse and work touch nothing else of the call, the
+ * handle's state and the layer's pools among it (PI_ERR_INVALID_ARG).
  */
 pi_status_t pi_kv_attend_shared(pi_kv_t *h, int32_t layer, const int32_t *seqs, const int32_t *tok_start, int32_t n,
                                 int32_t n_tokens, const int32_t *plan, int32_t n_groups, const void *q, int64_t ld_q,

@@ -264,3 +264,39 @@ def test_flags_sequences_far_down_the_call(P, n, at):
         assert left[at] and left.sum() == 1
     b.cache.append_rotated(0, room, start[:n], r, q[:n - 1], k[:n - 1], v[:n - 1])
     assert b.cache.status() == 0
+
+
+def test_refuses_outputs_over_what_the_call_reads(P):
+    """q_out over the batch, the rotation's tables, the handle's state or its pools; beside them it is taken."""
+    b = Both(P, hq=2, hkv=1, dim=64, page=16)
+    b.reserve([0, 1], [1, 2])
+    room = torch.zeros(3 * 128 + 512, device="cuda")
+    out, rest = room[:384].view(3, 2, 64), room[384:]
+    q, k, v = (torch.randn((3, n, 64), device="cuda") for n in (2, 1, 1))
+    seqs, start = b.args([0, 1], [1, 2])
+
+    def at(place, x):                                                # a copy of x in the room
+        y = place[:x.numel() * x.element_size() // 4].view(x.dtype)
+        return y.copy_(x)
+
+    def made(place):
+        r = P.Rotary(P.rotary_frequencies(64), 64, norm=True, q_norm=torch.ones(64, device="cuda"), k_norm=torch.ones(64, device="cuda"))
+        for name, x in (("turns", r.turns), ("q_norm", r.q_norm), ("k_norm", r.k_norm)):
+            if name in place:
+                setattr(r, name, at(place[name], x))
+                setattr(r.desc, name, getattr(r, name).data_ptr())
+        return r
+
+    plain = made({})
+    for place, fine in ((room[128:], False), (rest, True)):
+        for r, s, t in ((made(dict(turns=place)), seqs, start), (made(dict(q_norm=place)), seqs, start),
+                        (made(dict(k_norm=place)), seqs, start), (plain, at(place, seqs), start), (plain, seqs, at(place, start))):
+            if fine:
+                b.cache.append_rotated(0, s, t, r, q, k, v, q_out=out)
+            else:
+                with pytest.raises(P.PiError):
+                    b.cache.append_rotated(0, s, t, r, q, k, v, q_out=out)
+    for x in (b.k, b.v):
+        with pytest.raises(P.PiError):                               # over the layer's pool
+            b.cache.append_rotated(0, seqs, start, plain, q, k, v, q_out=x.view(torch.float32).flatten()[:384].view(3, 2, 64))
+    assert b.cache.status() == 0

@@ -451,3 +451,62 @@ def test_weights_of_16_bit_types_keep_two_terms(P, dim, page, kind):
         lo, hi = (torch.tensor(want + x, device="cuda").to(TYPES[kind]) for x in (-off, off))
         beyond = (out < lo) | (out > hi)
         assert not beyond.any() and b.cache.status() == 0, (len(new), int(beyond.sum()), beyond.numel())
+
+
+def test_refuses_outputs_over_what_the_call_reads(P):
+    """work, out, lse and plan over other arrays of their call; beside them they are taken."""
+    b = Shared(P, hq=4, hkv=2, dim=64, page=16, n_pages=60, max_pages=30)
+    b.grow([0], [300])
+    b.fork([0], [1])
+    b.grow([0, 1], [1, 1])
+    seqs, start = b.args([0, 1], [1, 1])
+    groups = dev([0, 2])
+    plan = b.cache.share(seqs, start, groups)
+    room = torch.zeros(4096, device="cuda")
+    q, need = torch.randn(2, 4, 64, device="cuda"), 2 * 4 * 66
+
+    def at(x, first):                                                # a copy of x in the room
+        y = room[first:first + x.numel()].view(x.dtype)
+        return y.copy_(x.flatten()).view(x.shape)
+
+    def attend(first, *, seqs=seqs, start=start, plan=plan, q=q, out=None, lse=None):
+        room[:need].zero_()
+        return b.cache.attend_shared(0, seqs, start, plan, q, out=out, lse=lse, work=room[:need])
+
+    lse = torch.zeros(2, 4, device="cuda")
+    for first, fine in ((need - 4, False), (need, True)):
+        for name, x in (("plan", plan), ("seqs", seqs), ("start", start), ("q", q), ("out", q), ("lse", lse)):
+            if fine:
+                assert torch.isfinite(attend(first, **{name: at(x, first)})).all()
+            else:
+                with pytest.raises(P.PiError):
+                    attend(first, **{name: at(x, first)})
+    out = room[:512].view(2, 4, 64)
+    for first, fine in ((508, False), (512, True)):
+        for name, x in (("plan", plan), ("seqs", seqs), ("tok_start", start), ("lse", lse), ("q", q)):
+            args = dict(seqs=seqs, tok_start=start, plan=plan, q=q, lse=None)
+            args[name] = at(x, first)
+            if fine:
+                b.cache.attend_shared(0, out=out, **args)
+            else:
+                with pytest.raises(P.PiError):
+                    b.cache.attend_shared(0, out=out, **args)
+    for name, x in (("plan", plan), ("seqs", seqs), ("tok_start", start), ("q", q)):      # the sums' logarithms likewise
+        args = dict(seqs=seqs, tok_start=start, plan=plan, q=q)
+        args[name] = at(x, 4)
+        with pytest.raises(P.PiError):
+            b.cache.attend_shared(0, lse=room[:8].view(2, 4), **args)
+    pool = b.v.view(torch.float32).flatten()
+    with pytest.raises(P.PiError):
+        b.cache.attend_shared(0, seqs, start, plan, q, out=pool[:512].view(2, 4, 64))
+    with pytest.raises(P.PiError):
+        b.cache.attend_shared(0, seqs, start, plan, q, work=pool[:need])
+    words = torch.zeros(40, dtype=torch.int32, device="cuda")
+    size = plan.numel()
+    for i, x in enumerate((seqs, start, groups)):                    # the plan over what it is made from
+        for first, code in ((size - 1, 1), (size, 0)):
+            args = [seqs, start, groups]
+            args[i] = words[first:first + x.numel()].copy_(x)
+            assert P._lib.pi_kv_share(b.cache.h, args[0].data_ptr(), args[1].data_ptr(), 2, args[2].data_ptr(), 1, words.data_ptr(),
+                                      torch.cuda.current_stream().cuda_stream) == code
+    assert torch.equal(words[:size], plan) and b.cache.status() == 0
