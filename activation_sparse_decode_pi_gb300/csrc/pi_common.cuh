@@ -138,6 +138,16 @@ __device__ __forceinline__ void i4_word_f32x2(uint32_t w, float2 (&p)[4])
     p[3] = __half22float2(__hfma2(u32_h2(lop3_and_xor(w8, 0x00F000F0u, 0x64806480u)), k16th, km72));
 }
 
+// (a.x b.x, a.y b.y) in one instruction
+__device__ __forceinline__ float2 fmul2(float2 a, float2 b)
+{
+    unsigned long long r;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(r)
+        : "l"(*reinterpret_cast<unsigned long long *>(&a)), "l"(*reinterpret_cast<unsigned long long *>(&b)));
+    return *reinterpret_cast<float2 *>(&r);
+}
+
 // (a.x b.x + c.x, a.y b.y + c.y): two fp32 FMAs in one instruction, each rounded as fmaf.
 __device__ __forceinline__ float2 ffma2(float2 a, float2 b, float2 c)
 {

@@ -6,17 +6,17 @@
 //    for another's and a load costs no address arithmetic (loads to registers, 16 bytes a lane: 87 us where this takes 44);
 //  - products on mma.sync m16n8k16, 16 rows of W against up to 8 rows of x: 16 bytes of a row of W to a lane are 32
 //    nibbles, four lanes' a group. The contraction may run in any order that both operands share, so nibbles are used
-//    as they lie: a word's nibbles (i, i + 4) become an f16 pair by one mask, as subnormals, and x is laid into shared
-//    memory in that order. (pi_int4_rows.cu has tcgen05 products, whose hand-offs cost more than these up to 8 rows of fp32 or
+//    as they lie: a word's nibbles (i, i + 4) become an f16 pair by a mask and one operation, as subnormals, and x is laid into
+//    shared memory in that order. (pi_int4_rows.cu has tcgen05 products, whose hand-offs cost more than these up to 8 rows of fp32 or
 //    16 of 16 bits.)
 //  - x is cut to f16 in units of a power of two for each row and group (fp32: two terms), undone in fp32 with the
 //    weights' scale, so a group's sum is of whole numbers times f16 and nothing else is rounded before fp32;
 //  - one CTA to an SM stays and goes through tiles of W, x resident. Its 16 warps split a tile's rows and the
 //    contraction (kw ways); CTAs of a cluster split the contraction further, where x is too large for one or the tiles are
 //    few, and add their sums through distributed shared memory in the order of their ranks.
-// Measured, one row (graph of calls back to back): 12288 -> 36864 bf16 44 us = 5.3 TB/s, fp32 52 us (second terms: twice the
-// products), 4096 -> 6144 bf16 7.0 us (launch, x, one tile and its sums in turn). 5120 -> 15360: 8 rows fp32 19 us, 16
-// rows bf16 24 us: there the products (mma.sync gives 1024 a cycle and SM) and the cluster's sums bound it.
+// Measured, one row (graph of calls back to back): 12288 -> 36864 bf16 45 us = 5.2 TB/s, fp32 54 us (second terms: twice the
+// products; with weights left in offset binary, at twice the error, 42 and 52), 4096 -> 6144 bf16 6.7 us (launch, x, one
+// tile and its sums in turn). 5120 -> 15360: 8 rows fp32 17 us, 16 rows bf16 21 us: there the products (mma.sync gives 1024 a cycle and SM) and the cluster's sums bound it.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -48,9 +48,8 @@ __global__ void __launch_bounds__(I4_NT, 1) k_int4_linear(const __grid_constant_
 
     uint8_t *const ring = smem + warp * slots * I4_BOX;                    // the warp's boxes
     uint8_t *const frag = smem + I4_NW * slots * I4_BOX;                   // [group][word][term][row][64 bytes]
-    // [group][8 NT]: the unit of x, and what the offset 8 adds to a sum in that unit, negative
-    float2 *const xf = (float2 *)(frag + (size_t)a.groups * 256 * T * nb);
-    float *const red = (float *)(xf + a.groups * 8 * NT);                  // [KW][8 NT][R + 1] sums
+    float *const xf = (float *)(frag + (size_t)a.groups * 256 * T * nb);   // [group][8 NT]: 2^11 times the unit of x
+    float *const red = xf + a.groups * 8 * NT;                             // [KW][8 NT][R + 1] sums
     uint64_t *const full = (uint64_t *)(smem + a.bar_at) + warp * slots;
     if (lane == 0) {
         for (int x = 0; x < slots; ++x) mbar_init(&full[x], 1);
@@ -108,7 +107,7 @@ __global__ void __launch_bounds__(I4_NT, 1) k_int4_linear(const __grid_constant_
                       const int word = (lane >> 1) & 3, qq = lane >> 3;
                       *(uint2 *)(frag + ((gl * 4 + word) * T * nb + b) * 64 + qq * 16 + (lane & 1) * 8 + term * 64 * nb) = v;
                   },
-                  [&](int gl, int b, float unit, float off) { xf[gl * (8 * NT) + b] = make_float2(unit, off); });
+                  [&](int gl, int b, float unit) { xf[gl * (8 * NT) + b] = unit; });
     __syncthreads();
 
     // Row g of a product is row ((g & 1) << 2 | g >> 1) of a box (and 8 + that): so eight lanes' reads, two rows' halves, lie
@@ -172,14 +171,14 @@ __global__ void __launch_bounds__(I4_NT, 1) k_int4_linear(const __grid_constant_
             for (int h = 0; h < 2; ++h) se[m][h] = __shfl_sync(0xffffffffu, sv, m * 16 + h * 8 + rg);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const float4 u = *(const float4 *)&xf[gl * (8 * NT) + 8 * n + 2 * q];
+            const float2 u = *(const float2 *)&xf[gl * (8 * NT) + 8 * n + 2 * q];
 #pragma unroll
             for (int m = 0; m < 2; ++m)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     float v = d[0][m][n][e];
                     if constexpr (T == 2) v += d[T - 1][m][n][e];
-                    tot[m][n][e] = fmaf(fmaf(v, e & 1 ? u.z : u.x, e & 1 ? u.w : u.y), se[m][e >> 1], tot[m][n][e]);
+                    tot[m][n][e] = fmaf(v * (e & 1 ? u.y : u.x), se[m][e >> 1], tot[m][n][e]);
                 }
         }
     };
@@ -197,7 +196,7 @@ __global__ void __launch_bounds__(I4_NT, 1) k_int4_linear(const __grid_constant_
             s0 = s1, s1 = scale();
             if (!dead && !warp_wait(&full[slot], parity)) dead = true;
             const uint8_t *const box = ring + slot * I4_BOX;
-            // (x's unit is 2^-11 of xf's, the nibbles' 2^-24)
+            // (x's unit is 2^-11 of xf's, the weights' 2^-24)
             step(box, 0, sv.x * 0x1p13f, 2 * pair);
             if (2 * pair + 1 < gn) step(box, 1, sv.y * 0x1p13f, 2 * pair + 1);
             fence_proxy_async_smem();   // the next copy into the place comes after the loads
@@ -310,7 +309,7 @@ cudaError_t launch_dt(const Int4Args &a, const CUtensorMap &map, int nsm, cudaSt
         for (int kw = 1; kw <= I4_NW; kw *= 2) {
             const int R = 32 * (I4_NW / kw), groups = (G + cs - 1) / cs;
             const size_t sums = kw == 1 && cs == 1 ? 0 : (size_t)kw * 8 * nt * (R + 1) * 4;
-            const size_t rest = ((size_t)groups * (256 * T * p.rows_per + 64 * nt) + sums + 7) / 8 * 8 + 8 * I4_NW * I4_SLOTS;
+            const size_t rest = ((size_t)groups * (256 * T * p.rows_per + 32 * nt) + sums + 7) / 8 * 8 + 8 * I4_NW * I4_SLOTS;
             if (rest + I4_NW * I4_BOX > I4_SMEM) continue;
             const int n_slots = std::min<int>(I4_SLOTS, (int)((I4_SMEM - rest) / (I4_NW * I4_BOX)));
             const int64_t tiles = (int64_t)((a.n + R - 1) / R) * slices;

@@ -11,44 +11,26 @@ namespace pi {
 constexpr int I4_GROUP = 128;
 constexpr int I4_SMEM = 227 * 1024;    // of a CTA, one to an SM
 
-// The eight nibbles of a word as f16 pairs (i, i + 4): a nibble in the low bits of a half is the subnormal (q + 8) 2^-24
-// (flipping its top bit turns two's complement into offset binary), one in bits 4..7 the subnormal (q + 8) 2^-20. So pairs
-// 1 and 3 are 16 times as large as 0 and 2, which their x makes up for, and the offset is taken off each group's sum.
+// The eight nibbles of a word as f16 pairs (i, i + 4), each the subnormal q 2^-24: a nibble in the low bits of a half reads
+// (q + 8) 2^-24 (flipping its top bit turns two's complement into offset binary), one in bits 4..7 16 times that; one exact
+// half-precision operation takes both to q 2^-24. (With the offset left on and taken off each group's sum instead, sums were
+// twice as large as need be, groups of zeros did not give 0, and an infinity gave NaN everywhere.)
 __device__ __forceinline__ void i4_word_h2(uint32_t w, uint32_t (&p)[4])
 {
     const uint32_t w8 = w >> 8;
-    p[0] = lop3_and_xor(w, 0x000F000Fu, 0x00080008u);
-    p[1] = lop3_and_xor(w, 0x00F000F0u, 0x00800080u);
-    p[2] = lop3_and_xor(w8, 0x000F000Fu, 0x00080008u);
-    p[3] = lop3_and_xor(w8, 0x00F000F0u, 0x00800080u);
-}
-
-// Element k of row i by the plain definition: for rows of x with an infinity or NaN, where an offset's product is none.
-template <int DT>
-__device__ __noinline__ float plain_dot(const Int4Args &a, int64_t x_at, int i)
-{
-    const int G = a.k / I4_GROUP;
-    float v = 0.f;
-    for (int gr = 0; gr < G; ++gr) {
-        float d = 0.f;
-        for (int e = 0; e < I4_GROUP; ++e) {
-            const int k = gr * I4_GROUP + e;
-            const uint32_t byte = a.w[(size_t)i * (a.k / 2) + k / 2];
-            const float q = (float)((int)((k & 1 ? byte >> 4 : byte & 15u) ^ 8u) - 8);
-            float x;
-            if constexpr (DT == DT_F32) x = ((const float *)a.x)[x_at + k];
-            else if constexpr (DT == DT_BF16) x = __bfloat162float(((const __nv_bfloat16 *)a.x)[x_at + k]);
-            else x = __half2float(((const __half *)a.x)[x_at + k]);
-            d = fmaf(q, x, d);
-        }
-        v = fmaf(d, __half2float(a.s[(size_t)i * G + gr]), v);
-    }
-    return v;
+    const __half2 off = u32_h2(0x80088008u), sixteenth = __half2half2(__ushort_as_half(0x2c00));   // -8 2^-24; 2^-4
+    const __half2 h[4] = {__hadd2(u32_h2(lop3_and_xor(w, 0x000F000Fu, 0x00080008u)), off),
+                          __hfma2(u32_h2(lop3_and_xor(w, 0x00F000F0u, 0x00800080u)), sixteenth, off),
+                          __hadd2(u32_h2(lop3_and_xor(w8, 0x000F000Fu, 0x00080008u)), off),
+                          __hfma2(u32_h2(lop3_and_xor(w8, 0x00F000F0u, 0x00800080u)), sixteenth, off)};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p[i] = *reinterpret_cast<const uint32_t *>(&h[i]);
 }
 
 // Groups [g_lo, g_lo + gn) of rows [b0, b0 + nb) of x as f16 terms by `warps` warps: put(group, row, term, halves) gets the
 // lane's four of a word's eight (word lane / 2; its pairs 0 and 1 in an even lane, 2 and 3 in an odd one), units(group, row,
-// unit, offset) the unit of x and what the offset 8 adds to a sum in that unit, negative.
+// unit) 2^11 times the unit of x. The largest element of a row's group lies in [2^14, 2^15) of its unit, so a term's
+// smallest step (2^-25 at most away) is 2^-39 of it.
 template <int DT, int S, class Put, class Units>
 __device__ __forceinline__ void i4_take_x(const Int4Args &a, int b0, int nb, int g_lo, int gn, int warp, int warps, int lane, Put put,
                                           Units units)
@@ -77,7 +59,6 @@ __device__ __forceinline__ void i4_take_x(const Int4Args &a, int b0, int nb, int
                 }
             }
         }
-        float sum[S];   // of the terms that the products take
         int ex[S];
 #pragma unroll
         for (int y = 0; y < S; ++y) {
@@ -87,48 +68,31 @@ __device__ __forceinline__ void i4_take_x(const Int4Args &a, int b0, int nb, int
                 const uint32_t u = __float_as_uint(f[y][e]) & 0x7fffffffu;
                 top = max(top, u < 0x7f800000u ? u : 0u);
             }
-            // 2^ex <= top < 2^(ex + 1): the largest will lie in [2^11, 2^12) (zeros and the smallest numbers below)
-            ex[y] = max((int)(__reduce_max_sync(0xffffffffu, top) >> 23) - 127, -116);
-            sum[y] = 0.f;
+            // 2^ex <= top < 2^(ex + 1) (zeros and the smallest numbers below)
+            ex[y] = max((int)(__reduce_max_sync(0xffffffffu, top) >> 23) - 127, -113);
         }
 #pragma unroll
         for (int y = 0; y < S; ++y) {
             const int it = it0 + y * warps, gl = (int)(it * magic >> 32), b = it - gl * nb;
             if (it >= all) break;
-            const float mul = exp2i(11 - ex[y]);
+            const float mul = exp2i(14 - ex[y]);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) f[y][e] *= e & 1 ? mul * 0.0625f : mul;   // (pairs 1 and 3: nibbles 16 times as large)
+            for (int e = 0; e < 4; ++e) f[y][e] *= mul;
             // a word's elements 0..3 lie in an even lane, 4..7 in the next: the even lane takes pairs (0, 4) and (1, 5)
             const bool odd = lane & 1;
             const float p0 = __shfl_xor_sync(0xffffffffu, odd ? f[y][0] : f[y][2], 1);
             const float p1 = __shfl_xor_sync(0xffffffffu, odd ? f[y][1] : f[y][3], 1);
             const float x0 = odd ? p0 : f[y][0], y0 = odd ? f[y][2] : p0, x1 = odd ? p1 : f[y][1], y1 = odd ? f[y][3] : p1;
             const uint32_t h0 = pack_f16(x0, y0), h1 = pack_f16(x1, y1);
-            const float2 c0 = __half22float2(u32_h2(h0)), c1 = __half22float2(u32_h2(h1));
-            sum[y] = (c0.x + c0.y) + 16.f * (c1.x + c1.y);
             put(gl, b, 0, make_uint2(h0, h1));
             if constexpr (DT == DT_F32) {
-                const uint32_t l0 = pack_f16(x0 - c0.x, y0 - c0.y), l1 = pack_f16(x1 - c1.x, y1 - c1.y);
-                const float2 r0 = __half22float2(u32_h2(l0)), r1 = __half22float2(u32_h2(l1));
-                sum[y] += (r0.x + r0.y) + 16.f * (r1.x + r1.y);
-                put(gl, b, 1, make_uint2(l0, l1));
+                const float2 c0 = __half22float2(u32_h2(h0)), c1 = __half22float2(u32_h2(h1));
+                // (an infinity or NaN is in the first term)
+                const auto rest = [](float x, float c) { return fabsf(x) < INFINITY ? x - c : 0.f; };
+                put(gl, b, 1, make_uint2(pack_f16(rest(x0, c0.x), rest(y0, c0.y)), pack_f16(rest(x1, c1.x), rest(y1, c1.y))));
             }
+            if (lane == 0) units(gl, b, exp2i(ex[y] - 3));
         }
-        // S sums over the warp: at each exchange a lane keeps half of them, then one, which 32 / S lanes share
-#pragma unroll
-        for (int w = S / 2, o = 16; w > 0; w /= 2, o /= 2)
-#pragma unroll
-            for (int y = 0; y < w; ++y) {
-                const bool up = lane & o;
-                const float keep = up ? sum[y + w] : sum[y], give = up ? sum[y] : sum[y + w];
-                sum[y] = keep + __shfl_xor_sync(0xffffffffu, give, o);
-                ex[y] = up ? ex[y + w] : ex[y];
-            }
-#pragma unroll
-        for (int o = 16 / S; o > 0; o /= 2) sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], o);
-        const int it = it0 + lane / (32 / S) * warps, gl = (int)(it * magic >> 32);
-        const float unit = exp2i(ex[0]);
-        if (lane % (32 / S) == 0 && it < all) units(gl, it - gl * nb, unit, -8.f * 0x1p-24f * sum[0] * unit);
     }
 }
 
@@ -136,7 +100,6 @@ __device__ __forceinline__ void i4_take_x(const Int4Args &a, int b0, int nb, int
 template <int DT>
 __device__ __forceinline__ void i4_store(const Int4Args &a, float v, int b, int i)
 {
-    if (v != v) v = plain_dot<DT>(a, (int64_t)b * a.ldx, i);
     if (a.bias) v += a.bias[i];
     const int64_t at = (int64_t)b * a.ldy + i, at_add = (int64_t)b * a.ldadd + i;
     if constexpr (DT == DT_F32) {

@@ -3,7 +3,7 @@
 // As pi_int4.cu (the same cut of x to f16 terms, the same use of a nibble as an f16 subnormal), for batches whose products
 // would bound mma.sync. A CTA has tiles of 128 rows of W and a share of the contraction, whose x stays in shared memory:
 //  - weights come by TMA, boxes of 128 rows and two groups;
-//  - a thread to a row turns a group's 64 bytes into 64 f16 pairs (five operations for eight weights) and writes them to
+//  - a thread to a row turns a group's 64 bytes into 64 f16 pairs (nine operations for eight weights) and writes them to
 //    tensor memory, where they are the product's A operand: nothing of the f16 weights passes through shared memory. 8 warps,
 //    four to each group of a box;
 //  - one thread issues a group's products, 128 x NP x 128, into an accumulator of the group's own;
@@ -93,9 +93,8 @@ __global__ void __launch_bounds__(IR_NT, 1) k_int4_rows(const __grid_constant__ 
     uint8_t *const ring = smem;
     uint8_t *const frag = smem + slots * IR_BOX;   // [group][term][64 columns of K][R8 rows][128 bytes], swizzled
     // (a product's columns from R8 on read on into what follows; nobody looks at them)
-    float *const xu = (float *)(frag + (size_t)a.groups * T * 256 * R8 + (NP - R8) * 128);   // [group][NP]: unit of x
-    float *const xo = xu + a.groups * NP;                                  // what the offset 8 adds to a sum, negative
-    float *const recv = xo + a.groups * NP;                                // [2][rank][row of x][row of W]: sums sent here
+    float *const xu = (float *)(frag + (size_t)a.groups * T * 256 * R8 + (NP - R8) * 128);   // [group][NP]: 2^11 times x's unit
+    float *const recv = xu + a.groups * NP;                                // [2][rank][row of x][row of W]: sums sent here
     RowsBars &bars = *(RowsBars *)(smem + a.bar_at);
     if (warp == IR_COPY && lane == 0) {
         for (int x = 0; x < slots; ++x) mbar_init(&bars.wfull[x], 1), mbar_init(&bars.wfree[x], 8);
@@ -138,7 +137,7 @@ __global__ void __launch_bounds__(IR_NT, 1) k_int4_rows(const __grid_constant__ 
                       uint8_t *const to = frag + ((size_t)gl * T + term) * 256 * R8 + (word >> 3) * (128 * R8);
                       *(uint2 *)(to + sw128_off(b, word & 7) + (lane & 1) * 8) = v;
                   },
-                  [&](int gl, int b, float unit, float off) { xu[gl * NP + b] = unit, xo[gl * NP + b] = off; });
+                  [&](int gl, int b, float unit) { xu[gl * NP + b] = unit; });
     fence_proxy_async_smem();   // the products read it
     tc_fence_before();
     cg::cluster_group cl = cg::this_cluster();
@@ -182,7 +181,7 @@ __global__ void __launch_bounds__(IR_NT, 1) k_int4_rows(const __grid_constant__ 
             for (int x = 0; x < H / 2; ++x) tot[x] = make_float2(0.f, 0.f);
             for (int g0 = 0; g0 < gn; g0 += 4) {
 #pragma unroll
-                for (int y = 0; y < 4; ++y) sc[y] = sn[y] * 0x1p13f;   // (x's unit is 2^-11 of xu's, the nibbles' 2^-24)
+                for (int y = 0; y < 4; ++y) sc[y] = sn[y] * 0x1p13f;   // (x's unit is 2^-11 of xu's, the weights' 2^-24)
                 scales(tile, g0 + 4, sn);
 #pragma unroll
                 for (int y = 0; y < 4; ++y) {
@@ -199,12 +198,12 @@ __global__ void __launch_bounds__(IR_NT, 1) k_int4_rows(const __grid_constant__ 
                     if (!dead && lane == 0) mbar_arrive(&bars.dfree[st]);
 #pragma unroll
                     for (int x = 0; x < H; x += 4) {
-                        const float4 u = *(const float4 *)&xu[g * NP + c0 + x], o = *(const float4 *)&xo[g * NP + c0 + x];
+                        const float4 u = *(const float4 *)&xu[g * NP + c0 + x];
                         const float2 s2 = make_float2(sc[y], sc[y]);
                         float2 v0 = make_float2(__uint_as_float(d[x]), __uint_as_float(d[x + 1]));
                         float2 v1 = make_float2(__uint_as_float(d[x + 2]), __uint_as_float(d[x + 3]));
-                        v0 = ffma2(v0, make_float2(u.x, u.y), make_float2(o.x, o.y));
-                        v1 = ffma2(v1, make_float2(u.z, u.w), make_float2(o.z, o.w));
+                        v0 = fmul2(v0, make_float2(u.x, u.y));
+                        v1 = fmul2(v1, make_float2(u.z, u.w));
                         tot[x / 2] = ffma2(v0, s2, tot[x / 2]);
                         tot[x / 2 + 1] = ffma2(v1, s2, tot[x / 2 + 1]);
                     }
@@ -361,7 +360,7 @@ bool launch_dt(const Int4Args &a, int nsm, cudaStream_t s, cudaError_t *e)
             const int per = (a.rows + slices - 1) / slices, r8 = (per + 7) / 8 * 8, cols = per <= 16 ? 16 : 32;
             const int groups = (G + cs - 1) / cs;
             if (cs > G) continue;
-            const size_t rest = (size_t)groups * (T * 256 * r8 + 8 * cols) + (cols - r8) * 128 + (cs > 1 ? 2 * 128 * 4 * r8 : 0);
+            const size_t rest = (size_t)groups * (T * 256 * r8 + 4 * cols) + (cols - r8) * 128 + (cs > 1 ? 2 * 128 * 4 * r8 : 0);
             if (rest + 2 * IR_BOX + sizeof(RowsBars) > I4_SMEM) continue;
             const int slots = std::min<int>(IR_SLOTS, (int)((I4_SMEM - sizeof(RowsBars) - rest) / IR_BOX));
             const int at_once = std::max(1, clusters_at_once(nsm, cs) / slices);

@@ -88,16 +88,6 @@ __device__ __forceinline__ float2 turn_cos_sin(uint64_t turns, int p, float amp)
     return quarter & 2 ? make_float2(-a, -b) : make_float2(a, b);
 }
 
-// (a.x b.x, a.y b.y) in one instruction
-__device__ __forceinline__ float2 fmul2(float2 a, float2 b)
-{
-    unsigned long long r;
-    asm("mul.rn.f32x2 %0, %1, %2;"
-        : "=l"(r)
-        : "l"(*reinterpret_cast<unsigned long long *>(&a)), "l"(*reinterpret_cast<unsigned long long *>(&b)));
-    return *reinterpret_cast<float2 *>(&r);
-}
-
 // Which elements of a head a lane has.
 struct RotaryLane {
     int off_a, off_b;   // first elements of its runs

@@ -27,8 +27,10 @@ extern "C" {
  * those of add and y multiples of the element. 0 <= rows <= PI_INT4_MAX_ROWS. add: NULL, or y itself (same address
  * and stride), or an array that y does not touch; y overlaps neither x nor the weights.
  * Products are of the exact integers and x as f16 terms in units of a power of two for each row and group: one term for
- * PI_BF16 and PI_F16 (exact where an element is at least 2^-22 of its group's largest), two for PI_F32 (22 bits).
- * Group sums, their scaling, bias and add are fp32; y is rounded to `dtype` once. The same call gives the same bits.
+ * PI_BF16 and PI_F16 (exact where an element is at least 2^-28 of its group's largest), two for PI_F32 (22 bits of an element,
+ * or 2^-39 of its group's largest). Group sums, their scaling, bias and add are fp32; y is rounded to `dtype` once. Infinities
+ * and NaN go where the formula takes them, 0 times an infinity too. The same call gives the same bits. (A kernel whose
+ * bounded waits run out, which nothing but a fault makes them do, leaves NaN.)
  */
 pi_status_t pi_int4_linear(const void *w, const void *s, const float *bias, int32_t n, int32_t k, const void *x,
                            int64_t ld_x, int32_t rows, const void *add, int64_t ld_add, void *y, int64_t ld_y,

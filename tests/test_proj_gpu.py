@@ -291,6 +291,71 @@ def test_ranges_are_checked_for_a_thread_without_a_context(P):
     assert codes == [1, 0] and (y == 0).all()
 
 
+@pytest.mark.parametrize("rows", [1, 20])
+@pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
+def test_int4_linear_zero_weights_give_zero(P, kind, rows):
+    """Groups of zeros with scales that are not add nothing, whatever x is."""
+    rng = np.random.default_rng(10)
+    w, s = weights(rng, 200, 1024)
+    w[:] = 0
+    y = P.Int4Linear(torch.tensor(w, device="cuda"), torch.tensor(s, device="cuda"))(wide(rng, rows, 1024, kind))
+    assert (y == 0).all()
+
+
+@pytest.mark.parametrize("rows", [1, 20])
+@pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
+def test_int4_linear_large_elements_of_zero_weight(P, kind, rows):
+    """One element of each group thousands of times the others, its weight 0: the others keep their bits (f16 terms hold them
+    to 2^-39 of the large one, 2^-25 of themselves)."""
+    rng = np.random.default_rng(11)
+    n, k = 150, 1280
+    w, s = weights(rng, n, k)
+    w[:, 2::64] &= 0x0f                                              # element 5 of every group
+    w[:, 40::64] &= 0xf0                                             # element 80
+    x = rng.standard_normal((rows, k)) * 2.0 ** -10
+    x[:, 5::128], x[:, 80::128] = rng.uniform(8, 16, (rows, k // 128)), -rng.uniform(4, 8, (rows, k // 128))
+    x = torch.tensor(x, device="cuda").to(TYPES[kind])
+    y = P.Int4Linear(torch.tensor(w, device="cuda"), torch.tensor(s, device="cuda"))(x)
+    v, xs = plain.int4_values(w, s), num(x)
+    want, size = xs @ v.T, np.abs(xs) @ np.abs(v).T
+    tol = size * (2.0 ** -19 + 2.0 ** -21 + (k // 128 + 3) * 2.0 ** -24) + HALF[kind] * np.abs(want) + TINY[kind]
+    assert (np.abs(num(y) - want) <= tol).all()
+
+
+@pytest.mark.parametrize("rows,n,k", [(1, 300, 512), (1, 300, 5120), (8, 300, 12288), (1, 200, 128 * 257), (16, 300, 5120),
+                                      (20, 300, 12288), (16, 200, 128 * 257)])
+def test_int4_linear_error_of_long_contractions(P, rows, n, k):
+    """fp32 rows in the L2 norm, whose bound does not grow with k: errors of groups are independent, so that their sum is to
+    the result as one group's error is to one group's sum. That is 8 cut-offs of 2^-23 of a running sum, all of one sign,
+    whose mean over the 8 steps is 2/3 of the final one in the norm, 2^-20.6 in all; x's terms are off by 2^-23 of an element
+    at most: below 2^-20, and twice that for chance. (x's second term left out of one group of 257 costs 1.2e-5.)"""
+    rng = np.random.default_rng(k + rows)
+    w, s = weights(rng, n, k)
+    x = wide(rng, rows, k, "f32")
+    y = P.Int4Linear(torch.tensor(w, device="cuda"), torch.tensor(s, device="cuda"))(x)
+    want = num(x) @ plain.int4_values(w, s).T
+    err = np.linalg.norm(num(y) - want, axis=1) / np.linalg.norm(want, axis=1)
+    assert err.max() <= 2.0 ** -19, err.max()
+
+
+@pytest.mark.parametrize("rows", [6, 20])
+@pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
+def test_int4_linear_infinities_meet_every_weight(P, kind, rows):
+    """An infinity times 0 is NaN, and two of different sign are; else it gives its own."""
+    rng = np.random.default_rng(12)
+    w, s = weights(rng, 300, 512)
+    s[7] = 0
+    x = wide(rng, rows, 512, kind)
+    inf = float("inf")
+    x[0, 3], x[1, 200], x[3, 1], x[3, 257], x[4, 128], x[4, 129] = inf, -inf, inf, inf, -inf, float("nan")
+    y = P.Int4Linear(torch.tensor(w, device="cuda"), torch.tensor(s, device="cuda"))(x)
+    with np.errstate(invalid="ignore"):
+        want = (num(x)[:, None, :] * plain.int4_values(w, s)[None]).sum(-1)
+    assert np.array_equal(np.isnan(num(y)), np.isnan(want)) and np.isnan(want[4]).all() and not np.isnan(want[2]).any()
+    bad = np.isinf(want)
+    assert bad.any() and np.array_equal(num(y)[bad], want[bad]) and np.isfinite(num(y)[~bad & ~np.isnan(want)]).all()
+
+
 # ------------------------------------------------------------------------------------------------ rotation
 
 POS = [0, 1, 2, 77, 4095, 131071, 1000003, 2 ** 30 + 1, 2 ** 31 - 1, -1, -100, -2 ** 31]
