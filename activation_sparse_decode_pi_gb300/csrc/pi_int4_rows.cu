@@ -363,8 +363,9 @@ bool launch_dt(const Int4Args &a, int nsm, cudaStream_t s, cudaError_t *e)
             const size_t rest = (size_t)groups * (T * 256 * r8 + 4 * cols) + (cols - r8) * 128 + (cs > 1 ? 2 * 128 * 4 * r8 : 0);
             if (rest + 2 * IR_BOX + sizeof(RowsBars) > I4_SMEM) continue;
             const int slots = std::min<int>(IR_SLOTS, (int)((I4_SMEM - sizeof(RowsBars) - rest) / IR_BOX));
-            const int at_once = std::max(1, clusters_at_once(nsm, cs) / slices);
-            const int64_t rounds = (tiles + at_once - 1) / at_once;
+            // (clusters of a slice; more slices than clusters at a time go one after the other)
+            const int all = clusters_at_once(nsm, cs), at_once = std::max(1, all / slices);
+            const int64_t rounds = (int64_t)((tiles + at_once - 1) / at_once) * ((slices + all - 1) / all);
             const double us = rounds * (groups * IR_GROUP_US + (cs > 1 ? IR_TILE_US : 0.0)) + groups * per * IR_X_US;
             if (p.cluster == 0 || us < best) {
                 best = us;
