@@ -7,8 +7,8 @@
 //  - products on mma.sync m16n8k16, 16 rows of W against up to 8 rows of x: 16 bytes of a row of W to a lane are 32
 //    nibbles, four lanes' a group. The contraction may run in any order that both operands share, so nibbles are used
 //    as they lie: a word's nibbles (i, i + 4) become an f16 pair by a mask and one operation, as subnormals, and x is laid into
-//    shared memory in that order. (pi_int4_rows.cu has tcgen05 products, whose hand-offs cost more than these up to 8 rows of fp32 or
-//    16 of 16 bits.)
+//    shared memory in that order. (pi_int4_rows.cu has tcgen05 products, whose hand-offs cost more than these up to 8 rows, or
+//    16 of 16 bits where W has many rows.)
 //  - x is cut to f16 in units of a power of two for each row and group (fp32: two terms), undone in fp32 with the
 //    weights' scale, so a group's sum is of whole numbers times f16 and nothing else is rounded before fp32;
 //  - one CTA to an SM stays and goes through tiles of W, x resident. Its 16 warps split a tile's rows and the
@@ -16,7 +16,8 @@
 //    few, and add their sums through distributed shared memory in the order of their ranks.
 // Measured, one row (graph of calls back to back): 12288 -> 36864 bf16 45 us = 5.2 TB/s, fp32 54 us (second terms: twice the
 // products; with weights left in offset binary, at twice the error, 42 and 52), 4096 -> 6144 bf16 6.7 us (launch, x, one
-// tile and its sums in turn). 5120 -> 15360: 8 rows fp32 17 us, 16 rows bf16 21 us: there the products (mma.sync gives 1024 a cycle and SM) and the cluster's sums bound it.
+// tile and its sums in turn). 5120 -> 15360: 8 rows fp32 17 us, 16 rows bf16 21 us: there the products (mma.sync gives 1024 a
+// cycle and SM) and the cluster's sums bound it.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -337,11 +338,15 @@ cudaError_t launch_dt(const Int4Args &a, const CUtensorMap &map, int nsm, cudaSt
 
 cudaError_t launch_int4_linear(const Int4Args &a, int dtype, int nsm, cudaStream_t s)
 {
-    // From 9 rows of fp32 (two terms) or 17 of 16 bits on the other kernel is faster, measured here against there: 16 rows of
-    // fp32 5120 -> 15360 28.3 against 25.0 us, 12288 -> 36864 223 against 98; 16 of bf16
-    // 23.5 against 25.9 and 75 against 85, 24 36.0 against 30.8 us.
+    // The other kernel is faster for more than 8 rows of fp32 (two terms). Measured in us, this against that, 8 and 9 rows:
+    // 5120 -> 15360 16.9 / 21.0 and 27.8 / 21.6, 12288 -> 36864 65 / 83 and 115 / 99, 5120 -> 5120 10.8 / 11.4 and 14.1 / 11.6,
+    // 640 -> 40000 8.6 / 10.2 and 13.5 / 10.3 (1024 -> 2560 has it at 7 rows: 5.8 / 5.1). For more than 16 of 16 bits, 16 and 20 rows:
+    // 20.8 / 22.8 and 36.4 / 25.6, 76 / 87 and 131 / 95, 640 -> 40000 10.0 / 10.8 and 15.5 / 13.1. But for more than 8 of 16 bits too
+    // where W has few tiles, which this kernel spreads over clusters: 9 and 16 rows 5120 -> 5120 11.1 / 11.3 and 14.2 / 12.1,
+    // 1024 -> 2560 6.7 / 5.3 and 8.5 / 5.6, 4096 -> 6144 (48 tiles of 128 rows) 12.0 / 11.8 and 12.7 / 12.9.
+    const bool small = (a.n + 127) / 128 * 3 <= nsm;
     cudaError_t e;
-    if (a.rows > (dtype == DT_F32 ? 8 : 16) && launch_int4_rows(a, dtype, nsm, s, &e)) return e;
+    if (a.rows > (dtype == DT_F32 || small ? 8 : 16) && launch_int4_rows(a, dtype, nsm, s, &e)) return e;
     // W as rows of k / 2 bytes; boxes of 32 rows and 128 bytes, swizzled. What lies past its edges reads as zeros.
     CUtensorMap map;
     if (!encode_bytes(&map, a.w, a.n, a.k / 2, 32, 128, CU_TENSOR_MAP_SWIZZLE_128B))

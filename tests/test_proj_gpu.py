@@ -356,6 +356,13 @@ def test_int4_linear_infinities_meet_every_weight(P, kind, rows):
     assert bad.any() and np.array_equal(num(y)[bad], want[bad]) and np.isfinite(num(y)[~bad & ~np.isnan(want)]).all()
 
 
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("rows,n,k", [(9, 6600, 1280), (13, 20001, 256), (16, 9000, 5120), (16, 15360, 128), (10, 7000, 128 * 97)])
+def test_int4_linear_some_rows_of_many_outputs(P, rows, n, k, kind):
+    lin, x, y = check_linear(P, np.random.default_rng(rows + n), rows, n, k, kind)
+    assert torch.equal(lin(x), lin(x))
+
+
 # ------------------------------------------------------------------------------------------------ rotation
 
 POS = [0, 1, 2, 77, 4095, 131071, 1000003, 2 ** 30 + 1, 2 ** 31 - 1, -1, -100, -2 ** 31]
