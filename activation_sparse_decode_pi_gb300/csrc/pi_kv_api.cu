@@ -519,7 +519,7 @@ pi_status_t pi_kv_attend_shared(pi_kv_t *h, int32_t layer, const int32_t *seqs, 
     // to each group but one); their parts lie in the workspace then, which has room for them: parts * most * run <= nsm * 256.
     const int64_t group_rows = (int64_t)n_tokens * (h->desc.n_heads / h->desc.n_kv_heads);
     // Up to 128 rows to a group on average take items of 128 rows (measured, 8 prefixes of 36 rows, 40 heads of 128, fp16, the
-    // whole call: 229 us, with items of 256 rows 245 us).
+    // whole call: 247 us, with items of 256 rows 315 us; fp32 330 and 326).
     const bool few = h->desc.head_dim <= 128 && group_rows <= (int64_t)128 * n_groups;
     const int64_t run = rows_per_item(h->desc.head_dim, few), most = ((group_rows + run - 1) / run + n_groups - 1) * h->desc.n_kv_heads;
     a.parts = n_groups > 0 && group_rows >= ROWS_FROM ? (int)std::max<int64_t>(1, std::min<int64_t>(16, h->nsm / most)) : 1;

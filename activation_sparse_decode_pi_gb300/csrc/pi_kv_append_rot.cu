@@ -7,8 +7,8 @@
 // token and a part of its heads to a warp, as in pi_rotate.cu. Keys and values: one to eight warps to one (page, head), as in
 // pi_kv_append.cu (largest value, block scale, codes), keys with cosines and sines that the CTA works out once for all its
 // heads.
-// Measured: 7 prompts of 1015..3351 tokens, 32 heads on 8 of 128, bf16 97 us = 3.5 TB/s; queries alone (the other CTAs out)
-// took 62 us, keys and values 60 us, and both want issue slots. 64 tokens of 40 + 80 heads, fp32 6.5 us; one token 3.3 us.
+// Measured: 7 prompts of 1015..3351 tokens, 32 heads on 8 of 128, bf16 96 us = 3.5 TB/s; queries alone (the other CTAs out)
+// took 62 us, keys and values 60 us, and both want issue slots. 64 tokens of 40 + 80 heads, fp32 6.3 us; one token 3.1 us.
 #include <algorithm>
 
 #include "pi_rotary.cuh"
@@ -220,7 +220,8 @@ cudaError_t launch_of(const KvAppendRotArgs &in, int nsm, cudaStream_t s)
     // Pages that T tokens of n sequences touch, at most.
     const int64_t pages = std::min(T, T / a.c.page + 2 * n);
     // Warps to a page's head: one where that makes enough of them (48 to an SM), and no more than its rows fill (measured,
-    // 7 prompts of ~2000 tokens, 8 heads of 128, bf16: 98, 94 and 89 us with eight, four and two).
+    // 7 prompts of ~2000 tokens, 8 heads of 128, bf16, where the rule takes two: 110, 102, 96 and 95 us with eight, four, two
+    // and one; 64 single tokens, which fill one: 6.3 us, 10.4 with two).
     a.warps = 1;
     while (a.warps < AR_NW && pages * 2 * a.c.hkv * a.warps < 48 * (int64_t)nsm && std::min<int64_t>(a.c.page, T / n) * D > a.warps * 256 * U)
         a.warps *= 2;
