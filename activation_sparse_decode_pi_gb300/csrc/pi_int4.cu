@@ -6,16 +6,16 @@
 //    for another's and a load costs no address arithmetic (loads to registers, 16 bytes a lane: 87 us where this takes 44);
 //  - products on mma.sync m16n8k16, 16 rows of W against up to 8 rows of x: 16 bytes of a row of W to a lane are 32
 //    nibbles, four lanes' a group. The contraction may run in any order that both operands share, so nibbles are used
-//    as they lie: a word's nibbles (i, i + 4) become an f16 pair by a mask and one operation, as subnormals, and x is laid into
-//    shared memory in that order. (pi_int4_rows.cu has tcgen05 products, whose hand-offs cost more than these up to 8 rows, or
+//    as they lie: a word's nibbles (i, i + 4) become an f16 pair by a mask and one operation, and x is laid into shared
+//    memory in that order. (pi_int4_rows.cu has tcgen05 products, whose hand-offs cost more than these up to 8 rows, or
 //    16 of 16 bits where W has many rows.)
 //  - x is cut to f16 in units of a power of two for each row and group (fp32: two terms), undone in fp32 with the
 //    weights' scale, so a group's sum is of whole numbers times f16 and nothing else is rounded before fp32;
 //  - one CTA to an SM stays and goes through tiles of W, x resident. Its 16 warps split a tile's rows and the
 //    contraction (kw ways); CTAs of a cluster split the contraction further, where x is too large for one or the tiles are
 //    few, and add their sums through distributed shared memory in the order of their ranks.
-// Measured, one row (graph of calls back to back): 12288 -> 36864 bf16 45 us = 5.2 TB/s, fp32 54 us (second terms: twice the
-// products; with weights left in offset binary, at twice the error, 42 and 52), 4096 -> 6144 bf16 6.7 us (launch, x, one
+// Measured, one row (graph of calls back to back): 12288 -> 36864 bf16 45 us = 5.2 TB/s, fp32 55 us (second terms: twice the
+// products; with weights left in offset binary, at five times the error, 42 and 52), 4096 -> 6144 bf16 6.7 us (launch, x, one
 // tile and its sums in turn). 5120 -> 15360: 8 rows fp32 17 us, 16 rows bf16 21 us: there the products (mma.sync gives 1024 a
 // cycle and SM) and the cluster's sums bound it.
 #include <cooperative_groups.h>
@@ -49,7 +49,7 @@ __global__ void __launch_bounds__(I4_NT, 1) k_int4_linear(const __grid_constant_
 
     uint8_t *const ring = smem + warp * slots * I4_BOX;                    // the warp's boxes
     uint8_t *const frag = smem + I4_NW * slots * I4_BOX;                   // [group][word][term][row][64 bytes]
-    float *const xf = (float *)(frag + (size_t)a.groups * 256 * T * nb);   // [group][8 NT]: 2^11 times the unit of x
+    float *const xf = (float *)(frag + (size_t)a.groups * 256 * T * nb);   // [group][8 NT]: 2 times the unit of x
     float *const red = xf + a.groups * 8 * NT;                             // [KW][8 NT][R + 1] sums
     uint64_t *const full = (uint64_t *)(smem + a.bar_at) + warp * slots;
     if (lane == 0) {
@@ -197,9 +197,9 @@ __global__ void __launch_bounds__(I4_NT, 1) k_int4_linear(const __grid_constant_
             s0 = s1, s1 = scale();
             if (!dead && !warp_wait(&full[slot], parity)) dead = true;
             const uint8_t *const box = ring + slot * I4_BOX;
-            // (x's unit is 2^-11 of xf's, the weights' 2^-24)
-            step(box, 0, sv.x * 0x1p13f, 2 * pair);
-            if (2 * pair + 1 < gn) step(box, 1, sv.y * 0x1p13f, 2 * pair + 1);
+            // (x's unit is half of xf's, the weights' 2^-10)
+            step(box, 0, sv.x * 512.f, 2 * pair);
+            if (2 * pair + 1 < gn) step(box, 1, sv.y * 512.f, 2 * pair + 1);
             fence_proxy_async_smem();   // the next copy into the place comes after the loads
             __syncwarp();
             if (!dead) request(slot);

@@ -11,25 +11,27 @@ namespace pi {
 constexpr int I4_GROUP = 128;
 constexpr int I4_SMEM = 227 * 1024;    // of a CTA, one to an SM
 
-// The eight nibbles of a word as f16 pairs (i, i + 4), each the subnormal q 2^-24: a nibble in the low bits of a half reads
-// (q + 8) 2^-24 (flipping its top bit turns two's complement into offset binary), one in bits 4..7 16 times that; one exact
-// half-precision operation takes both to q 2^-24. (With the offset left on and taken off each group's sum instead, sums were
-// twice as large as need be, groups of zeros did not give 0, and an infinity gave NaN everywhere.)
+// The eight nibbles of a word as f16 pairs (i, i + 4), each q 2^-10: a nibble in the low bits of a half reads as the subnormal
+// (q + 8) 2^-24 (flipping its top bit turns two's complement into offset binary), one in bits 4..7 as 16 times that; one exact
+// half-precision operation takes both to q 2^-10, a normal number: the tensor cores line products up by their operands'
+// exponents, and a subnormal's says 2^-14 however small it is, so sums of subnormals lose low bits (1 x 12288 -> 36864, fp32,
+// error against 64 bits: 7.3e-7 with q 2^-24). (With the offset left on and taken off each group's sum, groups of zeros did
+// not give 0, and an infinity gave NaN everywhere.)
 __device__ __forceinline__ void i4_word_h2(uint32_t w, uint32_t (&p)[4])
 {
     const uint32_t w8 = w >> 8;
-    const __half2 off = u32_h2(0x80088008u), sixteenth = __half2half2(__ushort_as_half(0x2c00));   // -8 2^-24; 2^-4
-    const __half2 h[4] = {__hadd2(u32_h2(lop3_and_xor(w, 0x000F000Fu, 0x00080008u)), off),
-                          __hfma2(u32_h2(lop3_and_xor(w, 0x00F000F0u, 0x00800080u)), sixteenth, off),
-                          __hadd2(u32_h2(lop3_and_xor(w8, 0x000F000Fu, 0x00080008u)), off),
-                          __hfma2(u32_h2(lop3_and_xor(w8, 0x00F000F0u, 0x00800080u)), sixteenth, off)};
+    const __half2 low = u32_h2(0x74007400u), high = u32_h2(0x64006400u), off = u32_h2(0xa000a000u);   // 2^14, 2^10; -8 2^-10
+    const __half2 h[4] = {__hfma2(u32_h2(lop3_and_xor(w, 0x000F000Fu, 0x00080008u)), low, off),
+                          __hfma2(u32_h2(lop3_and_xor(w, 0x00F000F0u, 0x00800080u)), high, off),
+                          __hfma2(u32_h2(lop3_and_xor(w8, 0x000F000Fu, 0x00080008u)), low, off),
+                          __hfma2(u32_h2(lop3_and_xor(w8, 0x00F000F0u, 0x00800080u)), high, off)};
 #pragma unroll
     for (int i = 0; i < 4; ++i) p[i] = *reinterpret_cast<const uint32_t *>(&h[i]);
 }
 
 // Groups [g_lo, g_lo + gn) of rows [b0, b0 + nb) of x as f16 terms by `warps` warps: put(group, row, term, halves) gets the
 // lane's four of a word's eight (word lane / 2; its pairs 0 and 1 in an even lane, 2 and 3 in an odd one), units(group, row,
-// unit) 2^11 times the unit of x. The largest element of a row's group lies in [2^14, 2^15) of its unit, so a term's
+// unit) 2 times the unit of x. The largest element of a row's group lies in [2^14, 2^15) of its unit, so a term's
 // smallest step (2^-25 at most away) is 2^-39 of it.
 template <int DT, int S, class Put, class Units>
 __device__ __forceinline__ void i4_take_x(const Int4Args &a, int b0, int nb, int g_lo, int gn, int warp, int warps, int lane, Put put,
@@ -91,7 +93,7 @@ __device__ __forceinline__ void i4_take_x(const Int4Args &a, int b0, int nb, int
                 const auto rest = [](float x, float c) { return fabsf(x) < INFINITY ? x - c : 0.f; };
                 put(gl, b, 1, make_uint2(pack_f16(rest(x0, c0.x), rest(y0, c0.y)), pack_f16(rest(x1, c1.x), rest(y1, c1.y))));
             }
-            if (lane == 0) units(gl, b, exp2i(ex[y] - 3));
+            if (lane == 0) units(gl, b, exp2i(ex[y] - 13));
         }
     }
 }

@@ -1,6 +1,6 @@
 // pi_int4_rows.cu -- projections of many rows with int4 group-128 weights, on tcgen05 (sm_103a).
 //
-// As pi_int4.cu (the same cut of x to f16 terms, the same use of a nibble as an f16 subnormal), for batches whose products
+// As pi_int4.cu (the same cut of x to f16 terms, the same f16 weights from nibbles), for batches whose products
 // would bound mma.sync. A CTA has tiles of 128 rows of W and a share of the contraction, whose x stays in shared memory:
 //  - weights come by TMA, boxes of 128 rows and two groups;
 //  - a thread to a row turns a group's 64 bytes into 64 f16 pairs (nine operations for eight weights) and writes them to
@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(IR_NT, 1) k_int4_rows(const __grid_constant__ 
     uint8_t *const ring = smem;
     uint8_t *const frag = smem + slots * IR_BOX;   // [group][term][64 columns of K][R8 rows][128 bytes], swizzled
     // (a product's columns from R8 on read on into what follows; nobody looks at them)
-    float *const xu = (float *)(frag + (size_t)a.groups * T * 256 * R8 + (NP - R8) * 128);   // [group][NP]: 2^11 times x's unit
+    float *const xu = (float *)(frag + (size_t)a.groups * T * 256 * R8 + (NP - R8) * 128);   // [group][NP]: 2 times x's unit
     float *const recv = xu + a.groups * NP;                                // [2][rank][row of x][row of W]: sums sent here
     RowsBars &bars = *(RowsBars *)(smem + a.bar_at);
     if (warp == IR_COPY && lane == 0) {
@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(IR_NT, 1) k_int4_rows(const __grid_constant__ 
             for (int x = 0; x < H / 2; ++x) tot[x] = make_float2(0.f, 0.f);
             for (int g0 = 0; g0 < gn; g0 += 4) {
 #pragma unroll
-                for (int y = 0; y < 4; ++y) sc[y] = sn[y] * 0x1p13f;   // (x's unit is 2^-11 of xu's, the weights' 2^-24)
+                for (int y = 0; y < 4; ++y) sc[y] = sn[y] * 512.f;   // (x's unit is half of xu's, the weights' 2^-10)
                 scales(tile, g0 + 4, sn);
 #pragma unroll
                 for (int y = 0; y < 4; ++y) {
