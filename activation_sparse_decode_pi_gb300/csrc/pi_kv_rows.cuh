@@ -51,7 +51,13 @@ struct RowsCfg {
     // P V is done (head dim 128, 16-bit types).
     static constexpr int TCOLS = 512, PCOLS = WT * TOK / 2;
     static constexpr bool APART = NG * (TOK + D + PCOLS) <= TCOLS;
-    static constexpr int GCOLS = TOK + D + (APART ? PCOLS : 0);
+    // The tensor cores cut a running sum off towards 0 with every product, so that one over a long prefix, whose positions
+    // may all add up, would lose more the longer it is. So a first pass takes O from the accumulator every FOLD tiles, to a sum
+    // of its own, and starts anew: in tensor memory where there is room for a second O (SUMS), every 512 positions; else in
+    // what the pass leaves, every 2048.
+    static constexpr bool SUMS = SHARED && APART && NG * (TOK + 2 * D + PCOLS) <= TCOLS;
+    static constexpr int FOLD = (SUMS ? 512 : 2048) / TOK;
+    static constexpr int GCOLS = TOK + D + (APART ? PCOLS : 0) + (SUMS ? D : 0);
 };
 
 constexpr float ROWS_TRAIL = 8.f;   // base-2 growth of the maximum that is taken up without rescaling
@@ -414,10 +420,12 @@ __global__ void __launch_bounds__(RowsCfg<D, QT, SHARED, FEW>::NT, 1) k_kv_rows(
     }
 
     // ---------------------------------------------------------------- softmax
-    float m = -INFINITY, l = 0.f, unit = 0.f;
+    float m = -INFINITY, l = 0.f, unit = 0.f, m_kept = -INFINITY;   // m_kept: the reference of the numerators in memory
+    bool kept = false;
     const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
-    const uint32_t ts = tmem + grp * C::GCOLS, to = ts + TOK, tp = C::APART ? to + D : ts;
+    const uint32_t ts = tmem + grp * C::GCOLS, to = ts + TOK, tp = C::APART ? to + D : ts, tk = tp + C::PCOLS;
     if (mine && grp < groups) {
+        const auto row_of_call = [&]() { return ((int64_t)sq.start + (row0 + row) / G) * c.hq + h * G + (row0 + row) % G; };
         // ------------------------------------------------------------ queries: half a row to a thread
         float qf;
         {
@@ -503,12 +511,13 @@ __global__ void __launch_bounds__(RowsCfg<D, QT, SHARED, FEW>::NT, 1) k_kv_rows(
             wait_alone(&vfull[b], (i / NB) & 1);
             if (dead) return;
             const uint64_t v1 = dv + (uint32_t)(b * C::KV_BYTES / 16);
+            const bool more = flat ? i % C::FOLD > 0 : i > 0;
 #pragma unroll
             for (int term = 0; term < WT; ++term)
 #pragma unroll
                 for (int j = 0; j < TOK / 16; ++j)
                     umma_f16_ts(to, tp + term * (TOK / 2) + j * 8, v1 + (uint32_t)(j * 2048 / 16), ID_O,
-                                i > 0 || term + j > 0);
+                                more || term + j > 0);
             if constexpr (!C::APART) umma_commit(&bar_p[grp]);
             umma_commit(&vempty[b]);
             if (i + 1 == nt) umma_commit(&bar_o[grp]);
@@ -516,11 +525,57 @@ __global__ void __launch_bounds__(RowsCfg<D, QT, SHARED, FEW>::NT, 1) k_kv_rows(
         const bool issues = (warp & 7) == 0;
         if (nt > 0 && issues && elect_one()) issue_s(0);
         dead = __any_sync(0xffffffffu, dead);
+        // First pass: this thread's columns (half of the row's) of the sum over earlier tiles, in numbers of their own against
+        // the reference m_kept.
+        const auto kept_at = [&]() { return (float4 *)(a.prior + (row_of_call() + blockIdx.y * all_rows) * D + half * (D / 2)); };
+        const auto kept_weight = [&]() { return m_kept == -INFINITY ? 0.f : ex2(m_kept - m); };
+        auto fold = [&]() {   // by the whole warp; the products so far are done
+            const float old = kept_weight(), scale = exp2i(-(int)ROWS_UNIT) * unit;
+#pragma unroll 1
+            for (int x = 0; x < D / 2; x += 32) {
+                uint32_t o[32];
+                if constexpr (C::SUMS) {
+                    uint32_t s[32];
+                    tmem_ld32(to + lane_base + half * (D / 2) + x, o);
+                    if (kept) tmem_ld32(tk + lane_base + half * (D / 2) + x, s);
+                    tmem_wait_ld(o);
+                    tmem_wait_ld(s);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        const float v = __uint_as_float(o[e]) * scale;
+                        o[e] = __float_as_uint(kept ? fmaf(__uint_as_float(s[e]), old, v) : v);
+                    }
+                    tmem_st16(tk + lane_base + half * (D / 2) + x, o);
+                    tmem_st16(tk + lane_base + half * (D / 2) + x + 16, o + 16);
+                } else {
+                    float4 *const at = kept_at() + x / 4;
+                    float4 v[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[e] = on && kept ? at[e] : make_float4(0.f, 0.f, 0.f, 0.f);
+                    tmem_ld32(to + lane_base + half * (D / 2) + x, o);
+                    tmem_wait_ld(o);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        v[e].x = fmaf(v[e].x, old, __uint_as_float(o[4 * e]) * scale);
+                        v[e].y = fmaf(v[e].y, old, __uint_as_float(o[4 * e + 1]) * scale);
+                        v[e].z = fmaf(v[e].z, old, __uint_as_float(o[4 * e + 2]) * scale);
+                        v[e].w = fmaf(v[e].w, old, __uint_as_float(o[4 * e + 3]) * scale);
+                        if (on) at[e] = v[e];
+                    }
+                    __syncwarp();   // the next load of tensor memory takes the whole warp
+                }
+            }
+            if constexpr (C::SUMS) tmem_wait_st();
+            m_kept = m;
+            kept = true;
+        };
         constexpr int HC = TOK / 2;   // positions of the tile that this thread takes
         const uint32_t my_s = ts + lane_base + half * HC, my_p = tp + lane_base + half * (HC / 2);
         for (int i = 0; i < nt; ++i) {
             wait(&bar_s[grp], i & 1);
             tc_fence_after();
+            const bool fresh = flat && i > 0 && i % C::FOLD == 0;
+            if (fresh) fold();   // (the last tile's product is done: the scores were committed behind it)
             const RowsMeta &mt = meta[i & 3];
             uint32_t r[HC];
 #pragma unroll
@@ -563,7 +618,7 @@ __global__ void __launch_bounds__(RowsCfg<D, QT, SHARED, FEW>::NT, 1) k_kv_rows(
                 m = top;
             }
             unit = mt.unit;
-            if (i > 0 && __any_sync(0xffffffffu, shrink != 1.f)) {
+            if (i > 0 && !fresh && __any_sync(0xffffffffu, shrink != 1.f)) {
 #pragma unroll 1
                 for (int x = half * (D / 2); x < (half + 1) * (D / 2); x += 16) {
                     uint32_t o[16];
@@ -623,7 +678,7 @@ __global__ void __launch_bounds__(RowsCfg<D, QT, SHARED, FEW>::NT, 1) k_kv_rows(
         l += s_half[half ^ 1][row];
         // (the unit, which may be as small as an append's 2^-120, is multiplied in by itself: its quotient would lose bits)
         const float back = exp2i(-(int)ROWS_UNIT), norm = splits > 1 || flat || join ? back : l == 0.f ? 0.f : back / l;
-        const int64_t prow = ((int64_t)sq.start + (row0 + row) / G) * c.hq + h * G + (row0 + row) % G;
+        const int64_t prow = row_of_call();
         float M = m, S = l;
         const int64_t at = ((int64_t)blockIdx.x * splits + blockIdx.y) * C::ROWS + row;
         const int64_t at_out = ((int64_t)sq.start + (row0 + row) / G) * a.ldo + (int64_t)(h * G + (row0 + row) % G) * D;
@@ -634,10 +689,24 @@ __global__ void __launch_bounds__(RowsCfg<D, QT, SHARED, FEW>::NT, 1) k_kv_rows(
                 tmem_ld32(to + lane_base + x, o);
                 tmem_wait_ld(o);
             }
+            uint32_t s[C::SUMS ? 32 : 1];
+            if constexpr (C::SUMS)
+                if (kept) {
+                    tmem_ld32(tk + lane_base + x, s);
+                    tmem_wait_ld(s);
+                }
             if (on) {
                 float f[32];   // l = 0: nothing seen (a NaN sum stays: it is not equal to 0)
 #pragma unroll
                 for (int e = 0; e < 32; ++e) f[e] = nt == 0 || l == 0.f ? 0.f : __uint_as_float(o[e]) * norm * unit;
+                if (flat && kept && l != 0.f) {
+                    const float old = kept_weight();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        if constexpr (C::SUMS) f[e] = fmaf(__uint_as_float(s[e]), old, f[e]);
+                        else f[e] = fmaf(((const float *)kept_at())[x - half * (D / 2) + e], old, f[e]);
+                    }
+                }
                 if (join && splits == 1) {   // (a split item's where its parts are added)
 #pragma unroll
                     for (int e = 0; e < 32; e += 4) {

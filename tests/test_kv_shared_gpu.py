@@ -510,3 +510,46 @@ def test_refuses_outputs_over_what_the_call_reads(P):
             assert P._lib.pi_kv_share(b.cache.h, args[0].data_ptr(), args[1].data_ptr(), 2, args[2].data_ptr(), 1, words.data_ptr(),
                                       torch.cuda.current_stream().cuda_stream) == code
     assert torch.equal(words[:size], plan) and b.cache.status() == 0
+
+
+@pytest.mark.parametrize("dim,page,hq,hkv,samples,length,run", [
+    (128, 32, 8, 2, 12, 5000, 512), (128, 64, 8, 1, 17, 9000, 2048), (64, 16, 4, 2, 17, 3000, 512), (256, 64, 4, 1, 17, 7000, 2048),
+    (64, 64, 16, 1, 17, 4000, 512)])
+def test_long_prefixes_of_values_of_one_sign(P, dim, page, hq, hkv, samples, length, run):
+    """Sums over thousands of positions that all add up stay within fp32, however many: groups enough that no prefix is split
+    over CTAs. Bound: the head of this file, where its 1e-5 of A is: `run` positions to a running sum are run / 16 products,
+    each of which cuts off 2^-23 of it at most, which is half of the final one on the way: run / 16 2^-24; and 1e-6 for sums
+    of these (some ten, 2^-24 each) and exponentials (2^-22)."""
+    groups = 60
+    pages = -(-(length + 40) // page)
+    b = Shared(P, hq=hq, hkv=hkv, dim=dim, page=page, n_pages=groups * (pages + samples * 2), max_seqs=groups * samples, max_pages=pages + 1)
+    lead = list(range(0, groups * samples, samples))
+    b.cache.reserve(*b.args(lead, [length - 38 * g for g in range(groups)]))
+    b.k.view(torch.uint8).copy_(torch.randint(0, 0x3c, b.k.shape, device="cuda", dtype=torch.uint8) +
+                                128 * torch.randint(0, 2, b.k.shape, device="cuda", dtype=torch.uint8))
+    b.v.view(torch.uint8).copy_(torch.randint(0x30, 0x40, b.v.shape, device="cuda", dtype=torch.uint8))
+    b.ks.fill_(0.25)
+    b.vs.copy_(2.0 ** torch.randint(-2, 3, b.vs.shape, device="cuda").float())
+    b.cache.fork(dev(np.repeat(lead, samples - 1)), dev([s + i for s in lead for i in range(1, samples)]))
+    seqs = list(range(groups * samples))
+    args = b.args(seqs, [1] * len(seqs))
+    b.cache.reserve(*args)
+    plan = b.cache.share(*args, dev([samples * g for g in range(groups + 1)]))
+    assert (plan[2 * groups + 1:3 * groups + 1] > 512).all()
+    q = torch.randn(len(seqs), hq, dim, device="cuda")
+    got = b.cache.attend_shared(0, *args, plan, q)
+    assert b.cache.status() == 0
+    scale, G = dim ** -0.5, hq // hkv
+    table, lengths = b.cache.table.long(), b.cache.length.tolist()
+    for s in (0, 1, samples - 1, 7 * samples + 2, len(seqs) - 1):
+        j = torch.arange(lengths[s], device="cuda")
+        at = table[s, j // page]
+        k, v = (x.view(torch.uint8)[0, at, :, j % page].view(torch.float8_e4m3fn).double() * y[0, at].double()[..., None]
+                for x, y in ((b.k, b.ks), (b.v, b.vs)))
+        x = torch.einsum("hgd,khd->hgk", q[s].double().view(hkv, G, dim), k) * scale
+        want = torch.einsum("hgk,khd->hgd", torch.softmax(x, -1), v).view(hq, dim)
+        largest = scale * q[s].double().norm(dim=-1, keepdim=True) * k.norm(dim=-1).max()
+        sums = run / 16 * 2.0 ** -24 + 1e-6
+        off = (got[s].double() - want) / want
+        assert (off.abs() <= sums + 2.0 ** -24 + 2 * 12 * 2.0 ** -23 * largest).all(), off.abs().max()
+        assert off.mean().abs() <= sums, off.mean()                 # (a logit's errors have either sign)
