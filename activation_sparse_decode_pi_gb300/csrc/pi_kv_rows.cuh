@@ -24,7 +24,7 @@
 // row's largest weight). QT = 2 (fp32 output): a second f16 term of both. QT = 1: 11 bits of the weight, for fp16
 // outputs as for bf16: on the windowed prompt the error against 64 bits is 2.7e-4, 2.1e-4 of it the output's rounding;
 // a second term would double the second product and halve the tile. Passes over and behind shared prefixes keep two terms
-// of a weight (WT) in every type: with one the fp16 output's error was 2.8e-4 on 8 groups of 9 samples. Two cost 229 -> 248 us
+// of a weight (WT) in every type: with one the fp16 output's error was 2.8e-4 on 8 groups of 9 samples. Two cost 229 -> 247 us
 // there, and 80 -> 97 us on 512 bf16 rows behind 16400 positions (tiles of 64; tiles of 128 spill and take 98).
 #pragma once
 
@@ -54,7 +54,9 @@ struct RowsCfg {
     // The tensor cores cut a running sum off towards 0 with every product, so that one over a long prefix, whose positions
     // may all add up, would lose more the longer it is. So a first pass takes O from the accumulator every FOLD tiles, to a sum
     // of its own, and starts anew: in tensor memory where there is room for a second O (SUMS), every 512 positions; else in
-    // what the pass leaves, every 2048.
+    // what the pass leaves, every 2048. Measured, fp32, values of one sign: error 1.5e-6 and 7.5e-6 where it was 1.8e-5 after
+    // 6000 positions and 4e-5 after 9000; 8 groups of 36 rows 247 -> 261 us, 24 of 136 over 9000 positions, 4 heads of 128, 308 -> 325
+    // (each row's sums beside each other in memory: 350; every 512 positions there: 124 us for 512 rows behind 16400, 101 so).
     static constexpr bool SUMS = SHARED && APART && NG * (TOK + 2 * D + PCOLS) <= TCOLS;
     static constexpr int FOLD = (SUMS ? 512 : 2048) / TOK;
     static constexpr int GCOLS = TOK + D + (APART ? PCOLS : 0) + (SUMS ? D : 0);
@@ -528,16 +530,22 @@ __global__ void __launch_bounds__(RowsCfg<D, QT, SHARED, FEW>::NT, 1) k_kv_rows(
         // First pass: this thread's columns (half of the row's) of the sum over earlier tiles, in numbers of their own against
         // the reference m_kept.
         const auto kept_at = [&]() { return (float4 *)(a.prior + (row_of_call() + blockIdx.y * all_rows) * D + half * (D / 2)); };
+        // In memory a warp's 32 rows exchange places within each 32 columns, so that its accesses are whole lines: where four of
+        // this thread's lie (float4 x of the 32 columns from c on); by the whole warp.
+        const bool whole_warp = __all_sync(0xffffffffu, on);
+        const auto kept_place = [&](int c, int x) {
+            const int at = whole_warp ? x * 32 + lane : lane * 8 + x;
+            return (float4 *)__shfl_sync(0xffffffffu, (unsigned long long)kept_at(), at / 8) + c / 4 + at % 8;
+        };
         const auto kept_weight = [&]() { return m_kept == -INFINITY ? 0.f : ex2(m_kept - m); };
         auto fold = [&]() {   // by the whole warp; the products so far are done
             const float old = kept_weight(), scale = exp2i(-(int)ROWS_UNIT) * unit;
+            if constexpr (C::SUMS) {
 #pragma unroll 1
-            for (int x = 0; x < D / 2; x += 32) {
-                uint32_t o[32];
-                if constexpr (C::SUMS) {
-                    uint32_t s[32];
-                    tmem_ld32(to + lane_base + half * (D / 2) + x, o);
-                    if (kept) tmem_ld32(tk + lane_base + half * (D / 2) + x, s);
+                for (int x = half * (D / 2); x < (half + 1) * (D / 2); x += 32) {
+                    uint32_t o[32], s[32];
+                    tmem_ld32(to + lane_base + x, o);
+                    if (kept) tmem_ld32(tk + lane_base + x, s);
                     tmem_wait_ld(o);
                     tmem_wait_ld(s);
 #pragma unroll
@@ -545,27 +553,34 @@ __global__ void __launch_bounds__(RowsCfg<D, QT, SHARED, FEW>::NT, 1) k_kv_rows(
                         const float v = __uint_as_float(o[e]) * scale;
                         o[e] = __float_as_uint(kept ? fmaf(__uint_as_float(s[e]), old, v) : v);
                     }
-                    tmem_st16(tk + lane_base + half * (D / 2) + x, o);
-                    tmem_st16(tk + lane_base + half * (D / 2) + x + 16, o + 16);
-                } else {
-                    float4 *const at = kept_at() + x / 4;
-                    float4 v[8];
+                    tmem_st16(tk + lane_base + x, o);
+                    tmem_st16(tk + lane_base + x + 16, o + 16);
+                }
+                tmem_wait_st();
+            } else {
+#pragma unroll 1
+                for (int x = 0; x < D / 2; x += 16) {
+                    uint32_t o[16];
+                    float4 v[4];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) v[e] = on && kept ? at[e] : make_float4(0.f, 0.f, 0.f, 0.f);
-                    tmem_ld32(to + lane_base + half * (D / 2) + x, o);
+                    for (int e = 0; e < 4; ++e) {
+                        const float4 *const at = kept_place(x & ~31, (x & 16) / 4 + e);
+                        v[e] = on && kept ? *at : make_float4(0.f, 0.f, 0.f, 0.f);
+                    }
+                    tmem_ld16u(to + lane_base + half * (D / 2) + x, o);
                     tmem_wait_ld(o);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
+                    for (int e = 0; e < 4; ++e) {
                         v[e].x = fmaf(v[e].x, old, __uint_as_float(o[4 * e]) * scale);
                         v[e].y = fmaf(v[e].y, old, __uint_as_float(o[4 * e + 1]) * scale);
                         v[e].z = fmaf(v[e].z, old, __uint_as_float(o[4 * e + 2]) * scale);
                         v[e].w = fmaf(v[e].w, old, __uint_as_float(o[4 * e + 3]) * scale);
-                        if (on) at[e] = v[e];
+                        float4 *const at = kept_place(x & ~31, (x & 16) / 4 + e);
+                        if (on) *at = v[e];
                     }
                     __syncwarp();   // the next load of tensor memory takes the whole warp
                 }
             }
-            if constexpr (C::SUMS) tmem_wait_st();
             m_kept = m;
             kept = true;
         };
@@ -690,23 +705,39 @@ __global__ void __launch_bounds__(RowsCfg<D, QT, SHARED, FEW>::NT, 1) k_kv_rows(
                 tmem_wait_ld(o);
             }
             uint32_t s[C::SUMS ? 32 : 1];
-            if constexpr (C::SUMS)
+            if constexpr (C::SUMS) {
                 if (kept) {
                     tmem_ld32(tk + lane_base + x, s);
                     tmem_wait_ld(s);
                 }
+            } else if constexpr (SHARED) {
+                if (kept) {
+                    const float old = kept_weight();
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float4 *const at = kept_place(x - half * (D / 2), e);
+                        const float4 v = on ? *at : make_float4(0.f, 0.f, 0.f, 0.f);
+                        o[4 * e] = __float_as_uint(fmaf(v.x, old, __uint_as_float(o[4 * e]) * norm * unit));
+                        o[4 * e + 1] = __float_as_uint(fmaf(v.y, old, __uint_as_float(o[4 * e + 1]) * norm * unit));
+                        o[4 * e + 2] = __float_as_uint(fmaf(v.z, old, __uint_as_float(o[4 * e + 2]) * norm * unit));
+                        o[4 * e + 3] = __float_as_uint(fmaf(v.w, old, __uint_as_float(o[4 * e + 3]) * norm * unit));
+                    }
+                    __syncwarp();   // all have theirs before the places become the rows' own
+                }
+            }
             if (on) {
                 float f[32];   // l = 0: nothing seen (a NaN sum stays: it is not equal to 0)
 #pragma unroll
-                for (int e = 0; e < 32; ++e) f[e] = nt == 0 || l == 0.f ? 0.f : __uint_as_float(o[e]) * norm * unit;
-                if (flat && kept && l != 0.f) {
-                    const float old = kept_weight();
+                for (int e = 0; e < 32; ++e)
+                    f[e] = nt == 0 || l == 0.f           ? 0.f
+                           : SHARED && !C::SUMS && kept ? __uint_as_float(o[e])
+                                                        : __uint_as_float(o[e]) * norm * unit;
+                if constexpr (C::SUMS)
+                    if (kept && l != 0.f) {
+                        const float old = kept_weight();
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        if constexpr (C::SUMS) f[e] = fmaf(__uint_as_float(s[e]), old, f[e]);
-                        else f[e] = fmaf(((const float *)kept_at())[x - half * (D / 2) + e], old, f[e]);
+                        for (int e = 0; e < 32; ++e) f[e] = fmaf(__uint_as_float(s[e]), old, f[e]);
                     }
-                }
                 if (join && splits == 1) {   // (a split item's where its parts are added)
 #pragma unroll
                     for (int e = 0; e < 32; e += 4) {
