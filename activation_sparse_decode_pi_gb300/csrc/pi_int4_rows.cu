@@ -11,10 +11,10 @@
 // Five or six groups are under way between these. CTAs of a cluster share the contraction, and send each other the sums of
 // a tile: each adds up its part of the tile's rows in the order of
 // the ranks, a tile later, when they have long come.
-// Measured (5120 -> 15360): 16 rows fp32 25 us, 32 bf16 36, 64 fp32 48, 64 bf16 50; 12288 -> 36864: 32 bf16 122, 32 fp32 194.
-// Neither the tensor pipe nor issue slots bound it but the hand-offs: with one product of eight it takes as long, and of a
-// group's 750 cycles the warps of the sums work 380, on a wait, a load, 8 to 16 sums and an arrival in turn, and a tile's
-// exchange costs 2600. Bringing in x is 3 us (5120 in eight shares, 16 rows) to 12 us (12288,
+// Measured (5120 -> 15360): 16 rows fp32 23 us, 32 bf16 31, 64 fp32 45, 64 bf16 44; 12288 -> 36864: 32 bf16 120, 32 fp32 204.
+// Neither the tensor pipe (13% active) nor issue slots (43%) bound it but the hand-offs: with one product of eight it took as
+// long, and of a group's 750 cycles the warps of the sums worked 380, on a wait, a load, 8 to 16 sums and an arrival in turn, and
+// a tile's exchange cost 2600 (stamped when the weights' offset was still in the sums). Bringing in x is 3 us (5120 in eight shares, 16 rows) to 12 us (12288,
 // 32 rows), whether the first boxes are asked for before it or after.
 #include <cooperative_groups.h>
 

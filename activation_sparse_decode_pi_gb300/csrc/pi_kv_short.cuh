@@ -11,10 +11,10 @@
 // shares. An item of up to two shares belongs to the CTA with its first step; a longer one is cut over CTAs and joined by
 // the last of them, in the order of its parts.
 // Measured: 64 sequences of 1..716 positions behind a prefix, 64 heads on 8 of 128, bf16, with the join of the prefix's 9
-// parts 33 us; 72 of 4..331, 40 heads, fp16 74 us = 2.1 TB/s. An item takes about 15 us from end to end (search 1.5,
+// parts 29 us; 72 of 4..331, 40 heads, fp16 68 us = 2.3 TB/s. An item takes about 15 us from end to end (search 1.5,
 // queries and page lookups 2, first codes and the prefix's parts 3..5, 0.8 a tile, join 2), bound by latency and, with many
-// items, by issue slots; one or two warps to an item took as long or longer (251 and 247 us for the whole call of the
-// latter, 242 with four).
+// items, by issue slots; one or two warps to an item took as long or longer (the latter's whole call, with an earlier first
+// pass: 251 and 247 us, 242 with four).
 #pragma once
 
 #include "pi_kv_device.cuh"

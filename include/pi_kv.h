@@ -23,7 +23,7 @@
  *  - seqs: int32 [n] device, table rows, 0 <= n <= PI_KV_MAX_CALL_SEQS; tok_start: int32 [n + 1]
  *    device, ascending from 0: sequence i's new tokens are rows tok_start[i] .. tok_start[i + 1] of
  *    the call's token arrays (n_tokens <= 2^30 rows; what lies past them is not touched, and flagged).
- *    Except for pi_kv_attend, a sequence appears at most once in a call.
+ *    Except for the attentions and pi_kv_share, a sequence appears at most once in a call.
  *  - A step: pi_kv_reserve once (lengths grow, pages are found), then per layer pi_kv_append (or
  *    pi_kv_append_rotated) and pi_kv_attend (or pi_kv_attend_shared). No call allocates, synchronises or reads back: a step can be captured in a graph.
  */
