@@ -57,8 +57,9 @@ pi_status_t check_ptr(const void *p, size_t bytes, size_t align, int dev)
                                    CU_POINTER_ATTRIBUTE_RANGE_SIZE};
     void *to[5] = {&type, &managed, &device, &base, &size};
     const auto ask = [&]() { return fn && fn(5, what, to, (CUdeviceptr)(uintptr_t)p) == CUDA_SUCCESS; };
-    if (!ask()) {   // a thread that has no context yet: the runtime gives it the device's
-        if (cudaSetDevice(dev) != cudaSuccess) cudaGetLastError();
+    if (!ask()) {   // a thread that has no context yet: the runtime gives it its device's
+        int now = 0;
+        if (cudaGetDevice(&now) != cudaSuccess || cudaSetDevice(now) != cudaSuccess) cudaGetLastError();
         if (!ask()) return PI_ERR_INVALID_ARG;
     }
     if (!managed && (type != CU_MEMORYTYPE_DEVICE || device != dev)) return PI_ERR_INVALID_ARG;
